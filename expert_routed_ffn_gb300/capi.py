@@ -106,8 +106,13 @@ def load():
     L.moe_get_stage_name.argtypes = [P, I]
     L.moe_get_stage_name.restype = ctypes.c_char_p
     L.moe_dispatch_noalloc.argtypes = [P, I, I, I, P, P, P, P, P]
+    L.moe_operators_status.argtypes = []
+    L.moe_grouped_forward.argtypes = [P, P, P, I, I, I, I, I, P, P]
+    L.moe_grouped_dgrad.argtypes = [P, P, P, I, I, I, I, I, P, P]
+    L.moe_grouped_wgrad.argtypes = [P, P, P, I, I, I, I, I, I, P, P]
     for name in ("moe_create", "moe_route", "moe_forward", "moe_forward_host", "moe_sync_status", "moe_dispatch_noalloc",
-                 "moe_set_option", "moe_get_stats", "moe_inspect", "moe_get_stage_times", "moe_get_trace"):
+                 "moe_set_option", "moe_get_stats", "moe_inspect", "moe_get_stage_times", "moe_get_trace",
+                 "moe_operators_status", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad"):
         getattr(L, name).restype = I
     _lib = L
     return L
@@ -255,3 +260,111 @@ def block_from_inputs(shape, inputs: dict, max_tokens: int = None) -> MoeBlock:
              **{k: inputs.get(k) for k in SCALE_KEYS})
     blk = MoeBlock(config_from_shape(shape, max_tokens), w)
     return blk
+
+
+# ------------------------------------------------------------------ operators
+# The products of the block one at a time and what surrounds them (include/moe.h,
+# "Operators around the stacked expert weights").  Each runs on the device of its
+# tensors, on `stream` or that device's current stream, and allocates only outputs it
+# was not given.
+
+def _need(cond, message):
+    if not cond:
+        raise ValueError(message)
+
+
+def _dtype_code(dtype):
+    import torch
+    _need(dtype in (torch.bfloat16, torch.float32), f"dtype must be bfloat16 or float32, not {dtype}")
+    return MOE_DTYPE_F32 if dtype == torch.float32 else MOE_DTYPE_BF16
+
+
+def _tensor(t, name, shape, dtype, device):
+    """t is a contiguous tensor of this shape and type on this device (None in shape: any size)."""
+    _need(t.device == device and device.type == "cuda", f"{name} must be on the CUDA device of the other tensors")
+    _need(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
+    _need(t.dim() == len(shape) and all(s is None or s == n for s, n in zip(shape, t.shape)),
+          f"{name} must have shape {list(shape)}, not {list(t.shape)}")
+    _need(t.is_contiguous(), f"{name} must be contiguous")
+    return t
+
+
+class _on:
+    """The device of a call's tensors as the current one, and `stream` as its current stream."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.device = torch.cuda.device(device)
+        self.stream = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        import torch
+        self.device.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        self.device.__exit__(*exc)
+
+
+def operators_status(device=None) -> int:
+    """moe_operators_status on `device` (default: the current one): synchronises, returns
+    and clears what the operators recorded there."""
+    import torch
+    with torch.cuda.device(device):
+        return load().moe_operators_status()
+
+
+def _grouped(name, A, W, offs, out, out_dtype, stream, forward):
+    import torch
+    _need(W.dim() == 3, "W must be [E, N, K]")
+    E, N, K = W.shape
+    cols, red = (N, K) if forward else (K, N)
+    _tensor(W, "W", (E, N, K), torch.bfloat16, A.device)
+    _tensor(A, "X" if forward else "dY", (None, red), torch.bfloat16, A.device)
+    _tensor(offs, "offs", (E + 1,), torch.int32, A.device)
+    rows = A.shape[0]
+    with _on(A.device, stream) as st:
+        if out is None:
+            out = torch.empty((rows, cols), dtype=out_dtype or torch.bfloat16, device=A.device)
+        _tensor(out, "out", (rows, cols), out_dtype or out.dtype, A.device)
+        check(getattr(load(), name)(_ptr(A), _ptr(W), _ptr(offs), rows, E, N, K, _dtype_code(out.dtype), _ptr(out), st),
+              name)
+    return out
+
+
+def grouped_forward(X, W, offs, out=None, out_dtype=None, stream=None):
+    """Y[r] = W[e] X[r] for the rows offs[e] <= r < offs[e + 1] of X [rows, K] bf16; W [E, N, K]
+    bf16, offs [E + 1] int32.  Returns out (default: a new [rows, N] tensor of out_dtype, bf16
+    by default), whose rows outside [offs[0], offs[E]) are left as they were."""
+    return _grouped("moe_grouped_forward", X, W, offs, out, out_dtype, stream, True)
+
+
+def grouped_dgrad(dY, W, offs, out=None, out_dtype=None, stream=None):
+    """The gradient of grouped_forward by its X: dX[r] = W[e]^T dY[r], dY [rows, N] bf16."""
+    return _grouped("moe_grouped_dgrad", dY, W, offs, out, out_dtype, stream, False)
+
+
+def grouped_wgrad(dY, X, offs, out=None, out_dtype=None, accumulate=False, stream=None):
+    """The gradient of grouped_forward by its W: dW[e] = sum over e's rows of dY[r] X[r]^T, in
+    out (default: a new [E, N, K] tensor, fp32 unless out_dtype says otherwise).  accumulate:
+    add to what out holds."""
+    import torch
+    _tensor(X, "X", (None, None), torch.bfloat16, X.device)
+    rows, K = X.shape
+    _tensor(dY, "dY", (rows, None), torch.bfloat16, X.device)
+    N = dY.shape[1]
+    _need(offs.dim() == 1 and offs.numel() >= 2, "offs must be [E + 1]")
+    _tensor(offs, "offs", (None,), torch.int32, X.device)
+    E = offs.numel() - 1
+    _need(out is not None or not accumulate, "accumulate needs out")
+    with _on(X.device, stream) as st:
+        if out is None:
+            out = torch.empty((E, N, K), dtype=out_dtype or torch.float32, device=X.device)
+        _tensor(out, "out", (E, N, K), out_dtype or out.dtype, X.device)
+        check(load().moe_grouped_wgrad(_ptr(dY), _ptr(X), _ptr(offs), rows, E, N, K, _dtype_code(out.dtype),
+                                       int(accumulate), _ptr(out), st), "moe_grouped_wgrad")
+    return out

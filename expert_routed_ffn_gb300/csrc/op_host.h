@@ -1,0 +1,47 @@
+// Host helpers shared by the stateless operators (grouped products, MX
+// quantisation, gradient clipping): error reporting, argument checks, the
+// driver's tensor-map encoder and per-device facts.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moe.h"
+
+void moe_set_last_error_internal(const char *msg);
+
+namespace moe {
+
+// Set the thread's error message (printf style) and return `st`.
+moe_status op_fail(moe_status st, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+
+// MOE_OK, or the failure of a CUDA call made by operator `op`.
+moe_status op_cuda(cudaError_t e, const char *op);
+
+inline bool op_aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// SM count of the current device (looked up once per device), or 0 after an error.
+int op_num_sms();
+
+// Allow `kernel` `bytes` of dynamic shared memory on the current device.  `done` is a
+// bit per device (index < 64), so the attribute is set once on each.
+cudaError_t op_allow_smem(const void *kernel, int bytes, unsigned long long *done);
+
+// A tiled tensor map of up to 4 dimensions (innermost first; strides in bytes, of
+// dimensions 1 ..), zero fill out of bounds.
+struct OpMap {
+    CUtensorMapDataType type;
+    int rank;
+    const void *base;
+    uint64_t dims[4];
+    uint64_t strides[3];
+    uint32_t box[4];
+    CUtensorMapSwizzle swizzle;
+};
+CUresult op_encode(CUtensorMap *m, const OpMap &d);
+
+// Device address of the operators' error word (op_capi.cu) on the current device.
+int *op_error_word();
+
+}  // namespace moe

@@ -355,6 +355,48 @@ moe_status moe_inspect(const moe_handle *h, int buffer, void *dst, size_t bytes,
 moe_status moe_dispatch_noalloc(const int32_t *topk_idx, int T, int k, int E, int32_t *expert_offs,
                                 int32_t *sorted_token, int32_t *slot, int *bad_index, moe_stream_t stream);
 
+/* ----------------------------------------------------------------------------
+ * Operators around the stacked expert weights: the products of the block one at a
+ * time, their gradients, block-scaled (MX) quantisation and products, and the clipping
+ * of gradients.  They take no handle and keep nothing between calls; the conventions
+ * above hold (borrowed pointers, row-major contiguous tensors, 16-byte alignment,
+ * asynchronous on `stream`, argument errors before anything is launched), the current
+ * device's context is used, and calls may overlap on different streams and threads and
+ * may be captured into CUDA graphs.
+ *
+ * Rows grouped by expert: the rows of expert e are [offs[e], offs[e + 1]), offs[E + 1]
+ * int32 on the device, as moe_dispatch_noalloc and MOE_BUF_EXPERT_OFFS give them, with
+ * 0 <= offs[0] <= ... <= offs[E] <= rows.  Experts may be empty; rows before offs[0]
+ * and from offs[E] on are neither read into any result nor written.  Offsets that
+ * break the rule are found on the device: the call writes nothing and
+ * moe_operators_status reports MOE_ERR_DEVICE_CHECK.
+ */
+
+/* Wait for the current device and report (then clear) what the operators below
+ * recorded on it since the last call: MOE_OK, MOE_ERR_DEVICE_CHECK (offsets) or
+ * MOE_ERR_TIMEOUT (a bounded device wait ran out), or MOE_ERR_CUDA.  Not during a
+ * stream capture. */
+moe_status moe_operators_status(void);
+
+/* Grouped products.  X [rows, K], dY [rows, N] and W [E, N, K] are bf16; out_dtype
+ * (moe_dtype) is the type of the result, bf16 or fp32.  Sums are fp32, rounded once.
+ * Limits: 1 <= E <= 256; N and K multiples of 8, up to 2^20; rows up to 2^30, else
+ * MOE_ERR_UNSUPPORTED.  The output must not overlap an input.
+ *   forward: Y [rows, N],  Y[r, :]  = W[e] X[r, :]
+ *   dgrad:   dX [rows, K], dX[r, :] = W[e]^T dY[r, :]
+ *   wgrad:   dW [E, N, K], dW[e]    = sum over e's rows of dY[r, :] X[r, :]^T, added to
+ *            what dW holds when accumulate is 1 (in fp32, one rounding); an expert
+ *            without rows gets zeros (unchanged when accumulating).
+ * rows == 0: forward and dgrad do nothing, wgrad as if every expert were empty; the
+ * pointers of empty tensors may then be NULL.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+moe_status moe_grouped_forward(const void *X, const void *W, const int32_t *offs, int rows, int E, int N, int K,
+                               int out_dtype, void *Y, moe_stream_t stream);
+moe_status moe_grouped_dgrad(const void *dY, const void *W, const int32_t *offs, int rows, int E, int N, int K,
+                             int out_dtype, void *dX, moe_stream_t stream);
+moe_status moe_grouped_wgrad(const void *dY, const void *X, const int32_t *offs, int rows, int E, int N, int K,
+                             int out_dtype, int accumulate, void *dW, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
