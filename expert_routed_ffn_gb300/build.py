@@ -22,7 +22,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libmoe.so")
 
 SOURCES = ["router.cu", "router_tc.cu", "stream.cu", "gemm_tc.cu", "gemm_sab.cu", "gemm_mxt.cu", "moe_capi.cu",
-           "dispatch_static.cu", "op_capi.cu", "grouped.cu"]
+           "dispatch_static.cu", "op_capi.cu", "grouped.cu", "mx_quant.cu", "grad_clip.cu"]
 HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "kernels.h"), os.path.join(CSRC, "routing.cuh"),
            os.path.join(CSRC, "op_host.h"), os.path.join(INCLUDE, "moe.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

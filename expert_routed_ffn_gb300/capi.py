@@ -110,9 +110,15 @@ def load():
     L.moe_grouped_forward.argtypes = [P, P, P, I, I, I, I, I, P, P]
     L.moe_grouped_dgrad.argtypes = [P, P, P, I, I, I, I, I, P, P]
     L.moe_grouped_wgrad.argtypes = [P, P, P, I, I, I, I, I, I, P, P]
+    SZ = ctypes.c_size_t
+    L.moe_mx_quantize.argtypes = [P, I, I, I, I, I, P, P, P]
+    L.moe_mx_dequantize.argtypes = [P, P, I, I, I, I, I, P, P]
+    L.moe_clip_workspace.argtypes = [I, ctypes.POINTER(SZ)]
+    L.moe_clip_grad_norm.argtypes = [P, I, ctypes.c_float, P, P, SZ, P]
     for name in ("moe_create", "moe_route", "moe_forward", "moe_forward_host", "moe_sync_status", "moe_dispatch_noalloc",
                  "moe_set_option", "moe_get_stats", "moe_inspect", "moe_get_stage_times", "moe_get_trace",
-                 "moe_operators_status", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad"):
+                 "moe_operators_status", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad", "moe_mx_quantize",
+                 "moe_mx_dequantize", "moe_clip_workspace", "moe_clip_grad_norm"):
         getattr(L, name).restype = I
     _lib = L
     return L
@@ -368,3 +374,87 @@ def grouped_wgrad(dY, X, offs, out=None, out_dtype=None, accumulate=False, strea
         check(load().moe_grouped_wgrad(_ptr(dY), _ptr(X), _ptr(offs), rows, E, N, K, _dtype_code(out.dtype),
                                        int(accumulate), _ptr(out), st), "moe_grouped_wgrad")
     return out
+
+
+def _mx_format(fmt):
+    _need(fmt in ("mxfp8", "mxfp4"), f"fmt must be 'mxfp8' or 'mxfp4', not {fmt!r}")
+    return WEIGHT_FORMATS[fmt]
+
+
+def _mx_shapes(shape, fmt):
+    """(slices, rows, K), codes shape and scales shape of a [.., rows, K] tensor."""
+    _need(len(shape) in (2, 3), "the tensor must be [rows, K] or [slices, rows, K]")
+    lead, (rows, K) = tuple(shape[:-2]), tuple(shape[-2:])
+    return (lead[0] if lead else 1, rows, K), lead + (rows, K if fmt == "mxfp8" else K // 2), lead + (K // 32, rows)
+
+
+def mx_quantize(X, fmt, codes=None, scales=None, stream=None):
+    """[rows, K] or [slices, rows, K] bf16 or fp32 -> element codes and block scales (uint8) in
+    the layout of the block's MX weights: codes [.., rows, K] (mxfp8) or [.., rows, K / 2]
+    (mxfp4), scales [.., K / 32, rows]."""
+    import torch
+    code = _mx_format(fmt)
+    (slices, rows, K), cshape, sshape = _mx_shapes(X.shape, fmt)
+    _tensor(X, "X", X.shape, X.dtype, X.device)
+    with _on(X.device, stream) as st:
+        codes = torch.empty(cshape, dtype=torch.uint8, device=X.device) if codes is None else codes
+        scales = torch.empty(sshape, dtype=torch.uint8, device=X.device) if scales is None else scales
+        _tensor(codes, "codes", cshape, torch.uint8, X.device)
+        _tensor(scales, "scales", sshape, torch.uint8, X.device)
+        check(load().moe_mx_quantize(_ptr(X), _dtype_code(X.dtype), slices, rows, K, code, _ptr(codes), _ptr(scales), st),
+              "moe_mx_quantize")
+    return codes, scales
+
+
+def mx_dequantize(codes, scales, fmt, dtype=None, out=None, stream=None):
+    """The values of mx_quantize's codes and scales as dtype (bf16 by default)."""
+    import torch
+    code = _mx_format(fmt)
+    shape = tuple(codes.shape[:-1]) + (codes.shape[-1] * (1 if fmt == "mxfp8" else 2),)
+    (slices, rows, K), cshape, sshape = _mx_shapes(shape, fmt)
+    _tensor(codes, "codes", cshape, torch.uint8, codes.device)
+    _tensor(scales, "scales", sshape, torch.uint8, codes.device)
+    with _on(codes.device, stream) as st:
+        if out is None:
+            out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=codes.device)
+        _tensor(out, "out", shape, dtype or out.dtype, codes.device)
+        check(load().moe_mx_dequantize(_ptr(codes), _ptr(scales), code, slices, rows, K, _dtype_code(out.dtype), _ptr(out),
+                                       st), "moe_mx_dequantize")
+    return out
+
+
+class MoeGrad(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("count", ctypes.c_longlong), ("dtype", ctypes.c_int)]
+
+
+def clip_grad_norm(grads, max_norm, out=None, stream=None):
+    """The norm of all `grads` (bf16 or fp32 CUDA tensors of one device) together, as a 0-dim
+    fp32 tensor, and the gradients times min(1, max_norm / norm): in place, or into the
+    tensors `out`.  If a gradient holds an infinity or a NaN the norm says so and the
+    gradients are passed on as they are."""
+    import torch
+    grads = list(grads)
+    out = grads if out is None else list(out)
+    _need(len(grads) > 0, "clip_grad_norm needs at least one gradient")
+    _need(len(out) == len(grads), "out must have a tensor for each gradient")
+    device = grads[0].device
+    both = grads if out is grads else grads + out
+    _need(device.type == "cuda" and set(map(torch.Tensor.get_device, both)) == {device.index},
+          "the gradients must be on one CUDA device")
+    _need(all(map(torch.Tensor.is_contiguous, both)), "the gradients must be contiguous")
+    types = [g.dtype for g in grads]
+    counts = list(map(torch.Tensor.numel, grads))
+    _need(set(types) <= {torch.bfloat16, torch.float32}, "the gradients must be bfloat16 or float32")
+    _need(out is grads or (types == [o.dtype for o in out] and counts == list(map(torch.Tensor.numel, out))),
+          "out must have the gradients' types and sizes")
+    src = list(map(torch.Tensor.data_ptr, grads))
+    dst = src if out is grads else list(map(torch.Tensor.data_ptr, out))
+    table = (MoeGrad * len(grads))(*zip(src, dst, counts, [int(t == torch.float32) for t in types]))
+    need = ctypes.c_size_t()
+    check(load().moe_clip_workspace(len(grads), ctypes.byref(need)), "moe_clip_workspace")
+    with _on(device, stream) as st:
+        norm = torch.empty((), dtype=torch.float32, device=device)
+        work = torch.empty(need.value, dtype=torch.uint8, device=device)
+        check(load().moe_clip_grad_norm(table, len(grads), max_norm, _ptr(norm), _ptr(work), need.value, st),
+              "moe_clip_grad_norm")
+    return norm

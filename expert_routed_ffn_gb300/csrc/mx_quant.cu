@@ -1,0 +1,271 @@
+// Block-scaled (OCP microscaling) quantisation and its inverse.
+//
+// Per block of 32 consecutive values along a row, with a = max |x|:
+//   scale byte  c = max(floor(log2 a) - emax + 127, 0)      (emax: 2 for E2M1, 8 for E4M3)
+//   codes       rne_saturate(x * 2^(127 - c))               (multiplying by a power of two is exact)
+// floor(log2 a) is the exponent field of a; a zero or subnormal a gives c = 0.  A block
+// that holds an infinity or a NaN gets c = 255 (NaN) and zero codes: all of it decodes to
+// NaN, as a sum over it would be.
+//
+// Bound by HBM: one read of the tensor, one write of codes and scales.  A CTA takes 64 rows
+// x 256 columns; a lane loads 8 consecutive values (four lanes hold a block, so a warp's
+// loads are contiguous) of eight rows at once, which keeps 128 to 256 bytes per thread in
+// flight.  The scales' layout is block-major ([K / 32, rows]), across the rows' direction:
+// they are collected in shared memory and leave as 64-byte runs.
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "moe.h"
+#include "op_host.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRows = 64;    // rows per CTA, eight per warp
+constexpr int kCols = 256;   // columns per CTA: eight values per lane
+constexpr int kPerWarp = kRows / (kThreads / 32);
+
+struct MxArgs {
+    const void *x;        // quantise: [slices, rows, K]; dequantise: unused
+    void *out;            // dequantise: [slices, rows, K]
+    uint8_t *codes, *scales;
+    int rows, K;
+    int row_tiles, col_tiles;
+};
+
+struct Place {
+    int slice, row0, col0;
+};
+__device__ __forceinline__ Place place(const MxArgs &p) {
+    const unsigned b = blockIdx.x, r = b / p.col_tiles;
+    return {(int)(r / p.row_tiles), (int)(r % p.row_tiles) * kRows, (int)(b % p.col_tiles) * kCols};
+}
+
+// 8 values of a row as fp32, and the bits of the largest magnitude (>= 0x7f800000: not finite)
+template <bool F32>
+struct Eight {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const void *x, size_t at) {
+        if (F32) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const float *>(x) + at);
+            a = __ldcs(src);
+            b = __ldcs(src + 1);
+        } else {
+            a = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(x) + at));
+        }
+    }
+    __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void floats(float (&v)[8]) const {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = F32 ? __uint_as_float(w[i]) : (i & 1) ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+    }
+};
+
+template <bool F32, bool FP4>
+__global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const MxArgs p) {
+    __shared__ uint8_t s_scale[kCols / 32][kRows];
+    pdl_wait();
+    pdl_trigger();
+    const Place t = place(p);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int col = t.col0 + 8 * lane;
+    const bool in_cols = col < p.K;  // K is a multiple of 32: a block's four lanes agree
+    Eight<F32> in[kPerWarp];
+#pragma unroll
+    for (int i = 0; i < kPerWarp; ++i) {
+        const int row = t.row0 + warp * kPerWarp + i;
+        in[i].zero();
+        if (in_cols && row < p.rows) in[i].load(p.x, ((size_t)t.slice * p.rows + row) * p.K + col);
+    }
+#pragma unroll
+    for (int i = 0; i < kPerWarp; ++i) {
+        const int row = t.row0 + warp * kPerWarp + i;
+        float v[8];
+        in[i].floats(v);
+        uint32_t big = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) big = max(big, __float_as_uint(v[j]) & 0x7fffffffu);
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        const int ex = (int)(big >> 23);
+        const bool finite = ex < 255;
+        const int c = finite ? max(ex - (FP4 ? 2 : 8), 0) : 255;
+        const float mul = __uint_as_float((uint32_t)(254 - (finite ? c : 127)) << 23);  // 2^(127 - c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = finite ? v[j] * mul : 0.0f;
+        if ((lane & 3) == 0) s_scale[lane >> 2][warp * kPerWarp + i] = (uint8_t)c;
+        if (in_cols && row < p.rows) {
+            const size_t at = ((size_t)t.slice * p.rows + row) * p.K + col;
+            if (FP4) {
+                uint32_t o;
+                asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+                    "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+                    "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+                    "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+                    "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+                    "mov.b32 %0, {a, b, c, d};\n\t}"
+                    : "=r"(o)
+                    : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+                *reinterpret_cast<uint32_t *>(p.codes + at / 2) = o;
+            } else {
+                uint16_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(o[j]) : "f"(v[2 * j]), "f"(v[2 * j + 1]));
+                *reinterpret_cast<uint2 *>(p.codes + at) =
+                    make_uint2(o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16);
+            }
+        }
+    }
+    __syncthreads();
+    // scales: 8 blocks x 64 rows, two bytes per thread (K / 32 blocks and rows may end inside)
+    const int kb = threadIdx.x >> 5, r = 2 * lane, row = t.row0 + r;
+    if (t.col0 + 32 * kb < p.K && row < p.rows) {
+        uint8_t *dst = p.scales + ((size_t)t.slice * (p.K / 32) + t.col0 / 32 + kb) * p.rows + row;
+        const uint8_t c0 = s_scale[kb][r], c1 = s_scale[kb][r + 1];
+        if ((reinterpret_cast<uintptr_t>(dst) & 1u) == 0 && row + 1 < p.rows) {
+            *reinterpret_cast<uint16_t *>(dst) = (uint16_t)(c0 | (uint16_t)c1 << 8);
+        } else {
+            dst[0] = c0;
+            if (row + 1 < p.rows) dst[1] = c1;
+        }
+    }
+}
+
+template <bool F32, bool FP4>
+__global__ void __launch_bounds__(kThreads) mx_dequantize_kernel(const MxArgs p) {
+    __shared__ uint8_t s_scale[kCols / 32][kRows];
+    pdl_wait();
+    pdl_trigger();
+    const Place t = place(p);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int col = t.col0 + 8 * lane;
+    const bool in_cols = col < p.K;
+    uint2 code[kPerWarp];
+#pragma unroll
+    for (int i = 0; i < kPerWarp; ++i) {
+        const int row = t.row0 + warp * kPerWarp + i;
+        code[i] = make_uint2(0, 0);
+        if (in_cols && row < p.rows) {
+            const size_t at = ((size_t)t.slice * p.rows + row) * p.K + col;
+            if (FP4)
+                code[i].x = __ldcs(reinterpret_cast<const uint32_t *>(p.codes + at / 2));
+            else
+                code[i] = __ldcs(reinterpret_cast<const uint2 *>(p.codes + at));
+        }
+    }
+    {
+        const int kb = threadIdx.x >> 5;
+        for (int r = lane; r < kRows; r += 32)
+            if (t.col0 + 32 * kb < p.K && t.row0 + r < p.rows)
+                s_scale[kb][r] = p.scales[((size_t)t.slice * (p.K / 32) + t.col0 / 32 + kb) * p.rows + t.row0 + r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPerWarp; ++i) {
+        const int row = t.row0 + warp * kPerWarp + i;
+        if (!in_cols || row >= p.rows) continue;
+        const uint32_t c = s_scale[lane >> 2][warp * kPerWarp + i];
+        // 2^(c - 127): c = 0 is the subnormal 2^-127, c = 255 NaN
+        const float mul = __uint_as_float(c == 255u ? 0x7fc00000u : c == 0u ? 0x00400000u : c << 23);
+        uint32_t h[4];  // pairs of f16, which holds every element value exactly
+        if (FP4) {
+            asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+                "mov.b32 {a, b, c, d}, %4;\n\t"
+                "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+                "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+                "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+                "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+                : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+                : "r"(code[i].x));
+        } else {
+            const uint16_t w[4] = {(uint16_t)code[i].x, (uint16_t)(code[i].x >> 16), (uint16_t)code[i].y,
+                                   (uint16_t)(code[i].y >> 16)};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[j]) : "h"(w[j]));
+        }
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
+            v[2 * j] = f.x * mul;
+            v[2 * j + 1] = f.y * mul;
+        }
+        const size_t at = ((size_t)t.slice * p.rows + row) * p.K + col;
+        if (F32) {
+            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at);
+            o[0] = make_float4(v[0], v[1], v[2], v[3]);
+            o[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint4 *>(static_cast<bf16 *>(p.out) + at) =
+                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                           pack_bf16x2(v[6], v[7]));
+        }
+    }
+}
+
+moe_status check(const char *op, const void *x, int dtype, int slices, int rows, int K, int format, const void *codes,
+                 const void *scales, MxArgs *a, unsigned *grid) {
+    if (slices < 0 || rows < 0 || K < 1) return op_fail(MOE_ERR_INVALID_ARG, "%s: need slices >= 0, rows >= 0, K >= 1", op);
+    if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F32)
+        return op_fail(MOE_ERR_INVALID_ARG, "%s: unknown dtype %d", op, dtype);
+    if (format != MOE_WEIGHTS_MXFP8 && format != MOE_WEIGHTS_MXFP4)
+        return op_fail(MOE_ERR_INVALID_ARG, "%s: format must be MXFP8 or MXFP4", op);
+    if (K % 32) return op_fail(MOE_ERR_UNSUPPORTED, "%s: K must be a multiple of 32 (K %d)", op, K);
+    a->rows = rows;
+    a->K = K;
+    a->row_tiles = (rows + kRows - 1) / kRows;
+    a->col_tiles = (K + kCols - 1) / kCols;
+    const long long tiles = (long long)slices * a->row_tiles;
+    if (tiles > 0 && tiles > ((1ll << 31) - 1) / a->col_tiles)
+        return op_fail(MOE_ERR_UNSUPPORTED, "%s: the tensor is too large for one call", op);
+    *grid = (unsigned)(tiles * a->col_tiles);
+    if (*grid == 0) return MOE_OK;
+    if (!x || !codes || !scales) return op_fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", op);
+    if (!op_aligned16(x) || !op_aligned16(codes) || !op_aligned16(scales))
+        return op_fail(MOE_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", op);
+    return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" moe_status moe_mx_quantize(const void *X, int dtype, int slices, int rows, int K, int format, void *codes,
+                                      uint8_t *scales, moe_stream_t stream) {
+    using namespace moe;
+    MxArgs a = {};
+    unsigned grid = 0;
+    const moe_status st = check("moe_mx_quantize", X, dtype, slices, rows, K, format, codes, scales, &a, &grid);
+    if (st != MOE_OK || grid == 0) return st;
+    a.x = X;
+    a.codes = static_cast<uint8_t *>(codes);
+    a.scales = scales;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(grid), dim3(kThreads), 0, s, a); };
+    const bool f32 = dtype == MOE_DTYPE_F32, fp4 = format == MOE_WEIGHTS_MXFP4;
+    return op_cuda(f32 ? (fp4 ? go(mx_quantize_kernel<true, true>) : go(mx_quantize_kernel<true, false>))
+                       : (fp4 ? go(mx_quantize_kernel<false, true>) : go(mx_quantize_kernel<false, false>)),
+                   "moe_mx_quantize");
+}
+
+extern "C" moe_status moe_mx_dequantize(const void *codes, const uint8_t *scales, int format, int slices, int rows, int K,
+                                        int dtype, void *X, moe_stream_t stream) {
+    using namespace moe;
+    MxArgs a = {};
+    unsigned grid = 0;
+    const moe_status st = check("moe_mx_dequantize", X, dtype, slices, rows, K, format, codes, scales, &a, &grid);
+    if (st != MOE_OK || grid == 0) return st;
+    a.out = X;
+    a.codes = static_cast<uint8_t *>(const_cast<void *>(codes));
+    a.scales = const_cast<uint8_t *>(scales);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(grid), dim3(kThreads), 0, s, a); };
+    const bool f32 = dtype == MOE_DTYPE_F32, fp4 = format == MOE_WEIGHTS_MXFP4;
+    return op_cuda(f32 ? (fp4 ? go(mx_dequantize_kernel<true, true>) : go(mx_dequantize_kernel<true, false>))
+                       : (fp4 ? go(mx_dequantize_kernel<false, true>) : go(mx_dequantize_kernel<false, false>)),
+                   "moe_mx_dequantize");
+}

@@ -397,6 +397,44 @@ moe_status moe_grouped_dgrad(const void *dY, const void *W, const int32_t *offs,
 moe_status moe_grouped_wgrad(const void *dY, const void *X, const int32_t *offs, int rows, int E, int N, int K,
                              int out_dtype, int accumulate, void *dW, moe_stream_t stream);
 
+/* Block-scaled quantisation of X [slices, rows, K] (dtype: moe_dtype) to MXFP8 or MXFP4
+ * (moe_weight_format) in the layout of the block's weights: codes [slices, rows, K] or
+ * [slices, rows, K / 2], scales [slices, K / 32, rows].  Per block of 32 values along K
+ * the scale byte is max(floor(log2 max|x|) - emax + 127, 0) (emax 8 for E4M3, 2 for
+ * E2M1) and the elements are rounded to nearest, ties to even, and saturated; a block
+ * that holds an infinity or a NaN gets scale 255 (NaN) and zero codes.  K must be a
+ * multiple of 32.  slices == 0 or rows == 0 is a no-op.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+moe_status moe_mx_quantize(const void *X, int dtype, int slices, int rows, int K, int format, void *codes,
+                           uint8_t *scales, moe_stream_t stream);
+
+/* The values of codes and scales, rounded once to dtype (exact in fp32 and, for values in
+ * its range, in bf16); scale 255 gives NaN.  Errors: as moe_mx_quantize. */
+moe_status moe_mx_dequantize(const void *codes, const uint8_t *scales, int format, int slices, int rows, int K,
+                             int dtype, void *X, moe_stream_t stream);
+
+/* One gradient of moe_clip_grad_norm (device pointers, aligned to their type; 16-byte
+ * alignment of both is faster). */
+typedef struct {
+    const void *grad;
+    void *out;        /* the clipped gradient: grad itself, or a tensor that overlaps none of the list */
+    long long count;  /* values */
+    int dtype;        /* moe_dtype of both */
+} moe_grad;
+
+/* Bytes of workspace moe_clip_grad_norm needs for a list of `count` tensors. */
+moe_status moe_clip_workspace(int count, size_t *bytes);
+
+/* The norm of all gradients of the list together, sqrt(sum g^2), to norm[0] (device, fp32)
+ * and out = g * min(1, max_norm / norm).  Squares are summed in fp32 over 32 values and in
+ * fp64 from there, in a fixed order.  If a gradient holds an infinity or a NaN, the norm
+ * says so and out = g.  max_norm > 0 (infinity: the norm alone is wanted).  The list is
+ * read before the call returns; tensors must not overlap each other.  count == 0: norm 0.
+ * `workspace` (device) is used until the call's kernels end: calls that may overlap, and
+ * graphs that may, need one each.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+moe_status moe_clip_grad_norm(const moe_grad *grads, int count, float max_norm, float *norm, void *workspace,
+                              size_t workspace_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

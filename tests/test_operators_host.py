@@ -43,3 +43,38 @@ def test_grouped_special_arguments(lib):
     assert lib.moe_grouped_wgrad(FAKE, FAKE, FAKE, 16, 4, 64, 64, 0, 2, FAKE, None) == capi.MOE_ERR_INVALID_ARG
     assert lib.moe_grouped_wgrad(None, None, None, 0, 4, 64, 64, 0, 0, None, None) == capi.MOE_ERR_INVALID_ARG
     assert lib.moe_grouped_wgrad(None, None, None, 0, 4, 64, 64, 0, 1, FAKE, None) == capi.MOE_OK
+
+
+QUANT = {"X": FAKE, "dtype": 0, "slices": 2, "rows": 16, "K": 64, "format": 2, "codes": FAKE, "scales": FAKE}
+
+
+@pytest.mark.parametrize("change,status", [
+    ({"X": None}, capi.MOE_ERR_INVALID_ARG), ({"codes": None}, capi.MOE_ERR_INVALID_ARG), ({"scales": None}, capi.MOE_ERR_INVALID_ARG),
+    ({"X": ODD}, capi.MOE_ERR_INVALID_ARG), ({"codes": ODD}, capi.MOE_ERR_INVALID_ARG), ({"scales": ODD}, capi.MOE_ERR_INVALID_ARG),
+    ({"dtype": 2}, capi.MOE_ERR_INVALID_ARG), ({"slices": -1}, capi.MOE_ERR_INVALID_ARG), ({"rows": -1}, capi.MOE_ERR_INVALID_ARG),
+    ({"K": 0}, capi.MOE_ERR_INVALID_ARG), ({"K": 48}, capi.MOE_ERR_UNSUPPORTED), ({"format": 0}, capi.MOE_ERR_INVALID_ARG),
+    ({"format": 3}, capi.MOE_ERR_INVALID_ARG), ({"slices": 1 << 30, "rows": 1 << 30}, capi.MOE_ERR_UNSUPPORTED),
+    ({"rows": 0, "X": None}, capi.MOE_OK), ({"slices": 0, "codes": None}, capi.MOE_OK),
+])
+def test_mx_refusals(lib, change, status):
+    a = {**QUANT, **change}
+    assert lib.moe_mx_quantize(*[a[k] for k in ("X", "dtype", "slices", "rows", "K", "format", "codes", "scales")], None) == status
+    assert lib.moe_mx_dequantize(*[a[k] for k in ("codes", "scales", "format", "slices", "rows", "K", "dtype", "X")], None) == status
+
+
+def test_clip_refusals(lib):
+    need = ctypes.c_size_t()
+    assert lib.moe_clip_workspace(-1, ctypes.byref(need)) == capi.MOE_ERR_INVALID_ARG
+    assert lib.moe_clip_workspace(3, None) == capi.MOE_ERR_INVALID_ARG
+    assert lib.moe_clip_workspace(3, ctypes.byref(need)) == capi.MOE_OK and need.value > 0
+
+    def call(grad=FAKE, out=FAKE, count=8, dtype=1, n=1, max_norm=1.0, norm=FAKE, work=FAKE, size=need.value, table=True):
+        t = (capi.MoeGrad * 1)(capi.MoeGrad(grad, out, count, dtype))
+        return lib.moe_clip_grad_norm(t if table else None, n, max_norm, norm, work, size, None)
+
+    for bad in (dict(grad=None), dict(out=None), dict(count=-1), dict(dtype=2), dict(n=-1), dict(max_norm=0.0),
+                dict(max_norm=float("nan")), dict(norm=None), dict(work=None), dict(size=need.value - 1), dict(table=False),
+                dict(work=ODD), dict(grad=ctypes.c_void_p((1 << 20) + 2)), dict(out=ctypes.c_void_p((1 << 20) + 1), dtype=0),
+                dict(norm=ctypes.c_void_p((1 << 20) + 2))):
+        assert call(**bad) == capi.MOE_ERR_INVALID_ARG, bad
+        assert "moe_clip_grad_norm" in lib.moe_last_error().decode()
