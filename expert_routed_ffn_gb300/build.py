@@ -22,9 +22,10 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libmoe.so")
 
 SOURCES = ["router.cu", "router_tc.cu", "stream.cu", "gemm_tc.cu", "gemm_sab.cu", "gemm_mxt.cu", "moe_capi.cu",
-           "dispatch_static.cu", "op_capi.cu", "grouped.cu", "mx_quant.cu", "grad_clip.cu"]
+           "dispatch_static.cu", "op_capi.cu", "grouped.cu", "mx_quant.cu", "mx_grouped.cu",
+           "grad_clip.cu"]
 HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "kernels.h"), os.path.join(CSRC, "routing.cuh"),
-           os.path.join(CSRC, "op_host.h"), os.path.join(INCLUDE, "moe.h")]
+           os.path.join(CSRC, "op_host.h"), os.path.join(CSRC, "grouped.cuh"), os.path.join(INCLUDE, "moe.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

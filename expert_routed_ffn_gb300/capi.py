@@ -113,12 +113,13 @@ def load():
     SZ = ctypes.c_size_t
     L.moe_mx_quantize.argtypes = [P, I, I, I, I, I, P, P, P]
     L.moe_mx_dequantize.argtypes = [P, P, I, I, I, I, I, P, P]
+    L.moe_mx_grouped_forward.argtypes = [P, P, P, P, P, I, I, I, I, I, P, P]
     L.moe_clip_workspace.argtypes = [I, ctypes.POINTER(SZ)]
     L.moe_clip_grad_norm.argtypes = [P, I, ctypes.c_float, P, P, SZ, P]
     for name in ("moe_create", "moe_route", "moe_forward", "moe_forward_host", "moe_sync_status", "moe_dispatch_noalloc",
                  "moe_set_option", "moe_get_stats", "moe_inspect", "moe_get_stage_times", "moe_get_trace",
                  "moe_operators_status", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad", "moe_mx_quantize",
-                 "moe_mx_dequantize", "moe_clip_workspace", "moe_clip_grad_norm"):
+                 "moe_mx_dequantize", "moe_mx_grouped_forward", "moe_clip_workspace", "moe_clip_grad_norm"):
         getattr(L, name).restype = I
     _lib = L
     return L
@@ -420,6 +421,30 @@ def mx_dequantize(codes, scales, fmt, dtype=None, out=None, stream=None):
         _tensor(out, "out", shape, dtype or out.dtype, codes.device)
         check(load().moe_mx_dequantize(_ptr(codes), _ptr(scales), code, slices, rows, K, _dtype_code(out.dtype), _ptr(out),
                                        st), "moe_mx_dequantize")
+    return out
+
+
+def mx_grouped_forward(Xc, Xs, Wc, Ws, offs, out=None, out_dtype=None, stream=None):
+    """grouped_forward on MXFP4 operands: Xc [rows, K / 2], Xs [K / 32, rows], Wc [E, N, K / 2],
+    Ws [E, K / 32, N] uint8 as mx_quantize gives them, offs [E + 1] int32.  Returns out (default:
+    a new [rows, N] tensor of out_dtype, bf16 by default), whose rows outside
+    [offs[0], offs[E]) are left as they were."""
+    import torch
+    _need(Wc.dim() == 3, "Wc must be [E, N, K / 2]")
+    E, N, half = Wc.shape
+    K = 2 * half
+    _tensor(Wc, "Wc", (E, N, half), torch.uint8, Xc.device)
+    _tensor(Ws, "Ws", (E, K // 32, N), torch.uint8, Xc.device)
+    _tensor(Xc, "Xc", (None, half), torch.uint8, Xc.device)
+    rows = Xc.shape[0]
+    _tensor(Xs, "Xs", (K // 32, rows), torch.uint8, Xc.device)
+    _tensor(offs, "offs", (E + 1,), torch.int32, Xc.device)
+    with _on(Xc.device, stream) as st:
+        if out is None:
+            out = torch.empty((rows, N), dtype=out_dtype or torch.bfloat16, device=Xc.device)
+        _tensor(out, "out", (rows, N), out_dtype or out.dtype, Xc.device)
+        check(load().moe_mx_grouped_forward(_ptr(Xc), _ptr(Xs), _ptr(Wc), _ptr(Ws), _ptr(offs), rows, E, N, K,
+                                            _dtype_code(out.dtype), _ptr(out), st), "moe_mx_grouped_forward")
     return out
 
 

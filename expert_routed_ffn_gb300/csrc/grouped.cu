@@ -35,6 +35,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "grouped.cuh"
 #include "kernels.h"
 #include "moe.h"
 #include "op_host.h"
@@ -46,37 +47,17 @@ enum : int { kForward = 0, kDgrad = 1, kWgrad = 2 };
 
 constexpr int kBK = 64;           // reduction steps per stage: 128 bytes of bf16
 constexpr int kMaxStages = 12;
-constexpr int kEpiWarps = 4;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kAccCols = 256;     // columns of one accumulator
 constexpr uint32_t kTmemCols = 2 * kAccCols;
 constexpr int kChunk = 64 * kBK * 2;  // an MN-major tile of 64 columns x 64 reduction rows
-constexpr int kMaxExperts = 256;
-constexpr unsigned long long kWaitNs = 2000000000ull;   // bound of every wait
-constexpr unsigned long long kDrainNs = 1000000000ull;  // bound of the drain after an abort
-constexpr int kEpiBytes = kEpiWarps * 4096;
 constexpr int kStageSpace = 196608;  // 192 KB of stages
 constexpr int kSmemBytes = kStageSpace + kEpiBytes + 1024 /* alignment */;
 
 struct GroupedArgs {
-    CUtensorMap map_a, map_b, map_out;
-    const int32_t *offs;
-    void *out;
-    int *err;
-    int E, rows;
-    int n_out;       // columns of the output
-    int m_dense;     // wgrad: rows of one expert's output (N)
-    int red;         // forward, dgrad: length of the reduction
-    int bm, bn;      // tile: rows of A per box (32, 64 or 128), output columns
-    int n_tiles;     // tiles along the output columns
-    int m_tiles;     // wgrad: tiles along N
+    CUtensorMap map_a, map_b;
+    GroupedOut o;
     int stages;
-    int out_f32, accumulate;
-};
-
-struct Tile {
-    int e, row0, m_valid, col0;  // expert, first output row, valid rows, first output column
-    int r0, r1;                  // reduction range
 };
 
 // Tensor-core descriptor of an MN-major tile: 64 contiguous elements (128 bytes) per
@@ -92,145 +73,6 @@ __device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr) {
     return d;
 }
 
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ void fence_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t src, int x, int y, int z) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(src), "r"(x), "r"(y), "r"(z)
-                 : "memory");
-}
-
-// Expert offsets into s_offs, their tile prefix into s_tiles; false (in every CTA alike)
-// if they decrease or leave [0, rows].
-template <int OP>
-__device__ __forceinline__ bool load_offsets(const GroupedArgs &p, int *s_offs, int *s_tiles) {
-    const int E = p.E;
-    for (int i = threadIdx.x; i <= E; i += kThreads) s_offs[i] = p.offs[i];
-    __syncthreads();
-    int bad = 0;
-    for (int i = threadIdx.x; i < E; i += kThreads) bad |= s_offs[i] > s_offs[i + 1];
-    bad |= s_offs[0] < 0 || s_offs[E] > p.rows;
-    if (__syncthreads_or(bad)) return false;
-    if (OP != kWgrad && threadIdx.x < 32) {
-        constexpr int kPer = kMaxExperts / 32;
-        const int lane = threadIdx.x;
-        int cnt[kPer], sum = 0;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int e = lane * kPer + j;
-            cnt[j] = e < E ? (s_offs[e + 1] - s_offs[e] + p.bm - 1) / p.bm : 0;
-            sum += cnt[j];
-        }
-        int incl = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += o;
-        }
-        int run = incl - sum;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int e = lane * kPer + j;
-            if (e <= E) s_tiles[e] = run;
-            run += cnt[j];
-        }
-        if (lane == 31 && E == kMaxExperts) s_tiles[E] = run;
-    }
-    __syncthreads();
-    return true;
-}
-
-// Tile number -> tile.  Inside an expert the row tiles of one column tile are adjacent, so
-// that concurrent CTAs share its weights in L2.
-template <int OP>
-__device__ __forceinline__ Tile decode(const GroupedArgs &p, int tile, const int *s_offs, const int *s_tiles) {
-    Tile t;
-    if (OP == kWgrad) {
-        const int per = p.m_tiles * p.n_tiles;
-        t.e = tile / per;
-        const int local = tile - t.e * per;
-        t.col0 = (local / p.m_tiles) * p.bn;
-        t.row0 = (local % p.m_tiles) * 128;
-        t.m_valid = min(128, p.m_dense - t.row0);
-        t.r0 = s_offs[t.e];
-        t.r1 = s_offs[t.e + 1];
-    } else {
-        int lo = 0, hi = p.E - 1;  // the last expert whose first tile is <= tile
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_tiles[mid] * p.n_tiles <= tile)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        const int mt = s_tiles[lo + 1] - s_tiles[lo];
-        const int local = tile - s_tiles[lo] * p.n_tiles;
-        t.e = lo;
-        t.col0 = (local / mt) * p.bn;
-        t.row0 = s_offs[lo] + (local % mt) * p.bm;
-        t.m_valid = min(p.bm, s_offs[lo + 1] - t.row0);
-        t.r0 = 0;
-        t.r1 = p.red;
-    }
-    return t;
-}
-
-// One warp's slice of the output, [32 rows][128 bytes of fp32 or bf16 columns] in its
-// swizzled staging buffer `sb` (lane i wrote row i; 16-byte unit j at j ^ (i % 8)).
-template <int OP>
-__device__ __forceinline__ void flush(const GroupedArgs &p, const Tile &t, uint32_t sb, int row, int rows, int col,
-                                      int lane) {
-    const int u = lane & 7;
-    if (OP == kWgrad && p.accumulate) {  // staged as 32 fp32 columns: dW + the product, in fp32
-        __syncwarp();
-        const int c = col + 4 * u;
-        for (int i = lane >> 3; i < rows; i += 4) {
-            const uint4 v = ld_shared_v4(sb + (uint32_t)i * 128u + ((uint32_t)(u ^ (i & 7)) << 4));
-            if (c >= p.n_out) continue;
-            const size_t at = ((size_t)t.e * p.m_dense + row + i) * p.n_out + c;
-            if (p.out_f32) {
-                float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at);
-                float4 old = *o;
-                old.x += __uint_as_float(v.x);
-                old.y += __uint_as_float(v.y);
-                old.z += __uint_as_float(v.z);
-                old.w += __uint_as_float(v.w);
-                *o = old;
-            } else {
-                uint2 *o = reinterpret_cast<uint2 *>(static_cast<bf16 *>(p.out) + at);
-                const uint2 old = *o;
-                *o = make_uint2(pack_bf16x2(bf16_lo(old.x) + __uint_as_float(v.x), bf16_hi(old.x) + __uint_as_float(v.y)),
-                                pack_bf16x2(bf16_lo(old.y) + __uint_as_float(v.z), bf16_hi(old.y) + __uint_as_float(v.w)));
-            }
-        }
-        __syncwarp();
-    } else if (OP == kWgrad || rows == 32) {  // past N or n_out the copy engine writes nothing
-        fence_smem();
-        __syncwarp();
-        if (lane == 0) {
-            tma_store_3d(&p.map_out, sb, col, row, OP == kWgrad ? t.e : 0);
-            bulk_commit();
-        }
-    } else {
-        __syncwarp();
-        const int es = p.out_f32 ? 4 : 2, c = col + (16 / es) * u;
-        for (int i = lane >> 3; i < rows; i += 4) {
-            const uint4 v = ld_shared_v4(sb + (uint32_t)i * 128u + ((uint32_t)(u ^ (i & 7)) << 4));
-            if (c < p.n_out)
-                *reinterpret_cast<uint4 *>(static_cast<char *>(p.out) + ((size_t)(row + i) * p.n_out + c) * es) = v;
-        }
-        __syncwarp();
-    }
-}
-
 template <int OP>
 __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_constant__ GroupedArgs p) {
     extern __shared__ uint8_t smem_raw[];
@@ -239,7 +81,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const int a_stage = (OP == kWgrad ? 128 : p.bm) * kBK * 2, b_stage = p.bn * kBK * 2;
+    const int a_stage = (OP == kWgrad ? 128 : p.o.bm) * kBK * 2, b_stage = p.o.bn * kBK * 2;
     // all A stages first: the MMA reads 128 rows of A where the box brought 32 or 64; the
     // rest is whatever follows, and its results are not stored
     const uint32_t sA = base, sB = base + (uint32_t)(p.stages * a_stage), sE = base + kStageSpace;
@@ -252,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int *abort_flag = &s_abort;
     auto raise = [&]() {
-        atomicOr(p.err, ERR_TIMEOUT);
+        atomicOr(p.o.err, ERR_TIMEOUT);
         *abort_flag = 1;
     };
 
@@ -270,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
         s_abort = 0;
         tma_prefetch_desc(&p.map_a);
         tma_prefetch_desc(&p.map_b);
-        tma_prefetch_desc(&p.map_out);
+        tma_prefetch_desc(&p.o.map);
     }
     if (warp == 1) {
         tmem_alloc(smem_u32(&s_tmem), kTmemCols);
@@ -282,9 +124,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
     const uint32_t tmem_base = s_tmem;
     pdl_wait();  // the offsets and operands of earlier kernels on the stream
     pdl_trigger();
-    const bool good = load_offsets<OP>(p, s_offs, s_tiles);
-    if (!good && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, ERR_BOUNDS);
-    const int total = !good ? 0 : OP == kWgrad ? p.E * p.m_tiles * p.n_tiles : s_tiles[p.E] * p.n_tiles;
+    const bool good = load_offsets<OP == kWgrad>(p.o, s_offs, s_tiles);
+    if (!good && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.o.err, ERR_BOUNDS);
+    const int total = !good ? 0 : OP == kWgrad ? p.o.E * p.o.m_tiles * p.o.n_tiles : s_tiles[p.o.E] * p.o.n_tiles;
     const int stride = (int)gridDim.x;
 
     if (warp == 0) {
@@ -294,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
             uint32_t ph = 1;
             bool ok = true;
             for (int tile = blockIdx.x; ok && tile < total; tile += stride) {
-                const Tile t = decode<OP>(p, tile, s_offs, s_tiles);
+                const Tile t = decode<OP == kWgrad>(p.o, tile, s_offs, s_tiles);
                 for (int r = t.r0; r < t.r1; r += kBK) {
                     if (!mbar_wait(empty_bar(s), ph, kWaitNs, abort_flag)) {
                         ok = false;
@@ -305,13 +147,13 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                     if (OP == kWgrad) {
                         tma_load_2d(da, &p.map_a, bar, t.row0, r);
                         tma_load_2d(da + kChunk, &p.map_a, bar, t.row0 + 64, r);
-                        for (int c = 0; c < p.bn; c += 64) tma_load_2d(db + c * (kBK * 2), &p.map_b, bar, t.col0 + c, r);
+                        for (int c = 0; c < p.o.bn; c += 64) tma_load_2d(db + c * (kBK * 2), &p.map_b, bar, t.col0 + c, r);
                     } else {
                         tma_load_2d(da, &p.map_a, bar, r, t.row0);
                         if (OP == kForward)
                             tma_load_3d(db, &p.map_b, bar, r, t.col0, t.e);
                         else
-                            for (int c = 0; c < p.bn; c += 64)
+                            for (int c = 0; c < p.o.bn; c += 64)
                                 tma_load_3d(db + c * (kBK * 2), &p.map_b, bar, t.col0 + c, r, t.e);
                     }
                     ++L;
@@ -333,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
         // The wgrad's last k-block is zeroed by the whole warp, so there all lanes follow the
         // loop; otherwise lane 0 alone.
         if (OP == kWgrad || lane == 0) {
-            const uint32_t idesc = idesc_bf16_f32(128, p.bn) | (OP == kWgrad ? 1u << 15 : 0u) | (OP != kForward ? 1u << 16 : 0u);
+            const uint32_t idesc = idesc_bf16_f32(128, p.o.bn) | (OP == kWgrad ? 1u << 15 : 0u) | (OP != kForward ? 1u << 16 : 0u);
             constexpr uint32_t kStepA = OP == kWgrad ? (16 * 128) >> 4 : 2;   // 16 reduction steps on,
             constexpr uint32_t kStepB = OP == kForward ? 2 : (16 * 128) >> 4;  // in units of 16 bytes
             uint32_t n_acc = 0, ph = 0;
@@ -344,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                 return OP == kWgrad ? __all_sync(0xffffffffu, got) != 0 : got;
             };
             for (int tile = blockIdx.x; ok && tile < total; tile += stride) {
-                const Tile t = decode<OP>(p, tile, s_offs, s_tiles);
+                const Tile t = decode<OP == kWgrad>(p.o, tile, s_offs, s_tiles);
                 if (t.r0 >= t.r1) continue;  // an expert without rows: the epilogue writes its zeros
                 const uint32_t a = n_acc & 1u;
                 if (!wait(tempty_bar(a), ((n_acc >> 1) & 1u) ^ 1u)) {
@@ -365,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                         const int valid = t.r1 - r;
                         steps = (valid + 15) / 16;
                         const int words = (steps * 16 - valid) * 8;  // 16-byte units per 64-column chunk
-                        for (int c = 0; c < 2 + p.bn / 64; ++c) {
+                        for (int c = 0; c < 2 + p.o.bn / 64; ++c) {
                             const uint32_t chunk = (c < 2 ? da + c * kChunk : db + (c - 2) * kChunk) + valid * 128;
                             for (int w = lane; w < words; w += 32) st_shared_v4(chunk + 16 * w, 0, 0, 0, 0);
                         }
@@ -399,12 +241,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
         }
     } else {
         const int q = warp & 3;  // the TMEM lane quadrant this warp may read
-        const uint32_t sb = sE + (uint32_t)q * 4096u, srow = sb + (uint32_t)lane * 128u;
-        const int sw = lane & 7;
+        const uint32_t sb = sE + (uint32_t)q * 4096u;
         uint32_t n_acc = 0;
-        const bool wide = p.out_f32 || (OP == kWgrad && p.accumulate);  // staged as fp32
         for (int tile = blockIdx.x; tile < total; tile += stride) {
-            const Tile t = decode<OP>(p, tile, s_offs, s_tiles);
+            const Tile t = decode<OP == kWgrad>(p.o, tile, s_offs, s_tiles);
             const bool empty = t.r0 >= t.r1;
             const uint32_t a = n_acc & 1u;
             if (!empty) {
@@ -414,43 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                 }
                 tc_fence_after();
             }
-            const int rows = min(32, t.m_valid - 32 * q);
-            if (rows > 0 && !(empty && p.accumulate)) {  // warp-uniform
-                const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + a * kAccCols;
-                const int end = min(p.bn, p.n_out - t.col0), step = wide ? 32 : 64;
-#pragma unroll 1
-                for (int c0 = 0; c0 < end; c0 += step) {
-                    if (lane == 0) bulk_wait_read_all();  // the previous slice's store has read the buffer
-                    __syncwarp();
-#pragma unroll 1
-                    for (int h = 0; h < step; h += 32) {
-                        uint32_t v[32];
-                        if (empty) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = 0u;
-                        } else {
-                            tmem_ld32(tb + c0 + h, v);
-                            tmem_ld_wait();
-                        }
-                        if (wide) {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                st_shared_v4(srow + ((uint32_t)(j ^ sw) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2],
-                                             v[4 * j + 3]);
-                        } else {
-                            uint32_t o[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                o[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                st_shared_v4(srow + ((uint32_t)((h / 8 + j) ^ sw) << 4), o[4 * j], o[4 * j + 1],
-                                             o[4 * j + 2], o[4 * j + 3]);
-                        }
-                    }
-                    flush<OP>(p, t, sb, t.row0 + 32 * q, rows, t.col0 + c0, lane);
-                }
-            }
+            store_tile<OP == kWgrad>(p.o, t, tmem_base + a * kAccCols, empty, sb, q, lane);
             if (!empty) {
                 tc_fence_before();
                 __syncwarp();
@@ -474,7 +278,8 @@ unsigned long long g_attr[3];
 
 // Tile sizes.  Rows: 32-row boxes while the experts average at most 16 rows, as the fused
 // block's decode tiles.  Columns: the widest tile that still gives every SM one.
-void choose_tiles(GroupedArgs &a, int op, int sms) {
+void choose_tiles(GroupedArgs &g, int op, int sms) {
+    GroupedOut &a = g.o;
     const long long active = std::min<long long>(a.E, a.rows);
     if (op == kWgrad) {
         a.bm = 128;
@@ -490,7 +295,7 @@ void choose_tiles(GroupedArgs &a, int op, int sms) {
         a.bn /= 2;
     }
     a.n_tiles = (a.n_out + a.bn - 1) / a.bn;
-    a.stages = std::min(kMaxStages, kStageSpace / ((a.bm + a.bn) * kBK * 2));
+    g.stages = std::min(kMaxStages, kStageSpace / ((a.bm + a.bn) * kBK * 2));
 }
 
 moe_status check(const char *op, const void *a, const void *b, const int32_t *offs, const void *out, int rows, int E,
@@ -516,19 +321,19 @@ moe_status launch(const char *name, int op, const void *a, const void *b, const 
     int *err = op_error_word();
     if (sms < 1 || err == nullptr) return op_fail(MOE_ERR_CUDA, "%s: no usable current device", name);
     GroupedArgs g = {};
-    g.offs = offs;
-    g.out = out;
-    g.err = err;
-    g.E = E;
-    g.rows = rows;
-    g.n_out = op == kForward ? N : K;
-    g.m_dense = N;
-    g.red = op == kForward ? K : N;
-    g.out_f32 = dtype == MOE_DTYPE_F32;
-    g.accumulate = accumulate;
+    g.o.offs = offs;
+    g.o.out = out;
+    g.o.err = err;
+    g.o.E = E;
+    g.o.rows = rows;
+    g.o.n_out = op == kForward ? N : K;
+    g.o.m_dense = N;
+    g.o.red = op == kForward ? K : N;
+    g.o.f32 = dtype == MOE_DTYPE_F32;
+    g.o.accumulate = accumulate;
     choose_tiles(g, op, sms);
-    const long long tiles = op == kWgrad ? (long long)E * g.m_tiles * g.n_tiles
-                                         : ((long long)rows / g.bm + std::min(E, rows)) * g.n_tiles;
+    const long long tiles = op == kWgrad ? (long long)E * g.o.m_tiles * g.o.n_tiles
+                                         : ((long long)rows / g.o.bm + std::min(E, rows)) * g.o.n_tiles;
     if (tiles > (1ll << 30)) return op_fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^30 output tiles", name);
 
     const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -539,12 +344,12 @@ moe_status launch(const char *name, int op, const void *a, const void *b, const 
         ma = {bf, 2, a, {n, r}, {n * 2}, {64, kBK}, sw};
         mb = {bf, 2, b, {k, r}, {k * 2}, {64, kBK}, sw};
     } else {
-        const uint64_t c = g.red;
-        ma = {bf, 2, a, {c, r}, {c * 2}, {kBK, (uint32_t)g.bm}, sw};
-        mb = {bf, 3, b, {k, n, e}, {k * 2, n * k * 2}, {64, op == kForward ? (uint32_t)g.bn : (uint32_t)kBK, 1}, sw};
+        const uint64_t c = g.o.red;
+        ma = {bf, 2, a, {c, r}, {c * 2}, {kBK, (uint32_t)g.o.bm}, sw};
+        mb = {bf, 3, b, {k, n, e}, {k * 2, n * k * 2}, {64, op == kForward ? (uint32_t)g.o.bn : (uint32_t)kBK, 1}, sw};
     }
-    const uint64_t es = g.out_f32 ? 4 : 2, cols = g.n_out;
-    const OpMap mo = {g.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : bf,
+    const uint64_t es = g.o.f32 ? 4 : 2, cols = g.o.n_out;
+    const OpMap mo = {g.o.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : bf,
                       3,
                       out,
                       {cols, op == kWgrad ? n : r, op == kWgrad ? e : 1},
@@ -552,7 +357,7 @@ moe_status launch(const char *name, int op, const void *a, const void *b, const 
                       {(uint32_t)(128 / es), 32, 1},
                       sw};
     if (op_encode(&g.map_a, ma) != CUDA_SUCCESS || op_encode(&g.map_b, mb) != CUDA_SUCCESS ||
-        op_encode(&g.map_out, mo) != CUDA_SUCCESS)
+        op_encode(&g.o.map, mo) != CUDA_SUCCESS)
         return op_fail(MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", name);
     const dim3 grid((unsigned)std::min<long long>(sms, tiles));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -413,6 +413,16 @@ moe_status moe_mx_quantize(const void *X, int dtype, int slices, int rows, int K
 moe_status moe_mx_dequantize(const void *codes, const uint8_t *scales, int format, int slices, int rows, int K,
                              int dtype, void *X, moe_stream_t stream);
 
+/* Grouped product with both operands in MXFP4 (codes and scales as moe_mx_quantize
+ * writes them): Xc [rows, K / 2], Xs [K / 32, rows], Wc [E, N, K / 2], Ws [E, K / 32, N];
+ * Y [rows, N], Y[r, :] = W[e] X[r, :] over the decoded values, summed in fp32 and rounded
+ * once to out_dtype.  A scale of 255 makes the results that use it NaN.  Rows, offsets
+ * and limits as moe_grouped_forward, with N a multiple of 8 and K a multiple of 32.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+moe_status moe_mx_grouped_forward(const void *Xc, const uint8_t *Xs, const void *Wc, const uint8_t *Ws,
+                                  const int32_t *offs, int rows, int E, int N, int K, int out_dtype, void *Y,
+                                  moe_stream_t stream);
+
 /* One gradient of moe_clip_grad_norm (device pointers, aligned to their type; 16-byte
  * alignment of both is faster). */
 typedef struct {

@@ -78,3 +78,19 @@ def test_clip_refusals(lib):
                 dict(norm=ctypes.c_void_p((1 << 20) + 2))):
         assert call(**bad) == capi.MOE_ERR_INVALID_ARG, bad
         assert "moe_clip_grad_norm" in lib.moe_last_error().decode()
+
+
+MX_GROUPED = {"Xc": FAKE, "Xs": FAKE, "Wc": FAKE, "Ws": FAKE, "offs": FAKE, "rows": 16, "E": 4, "N": 64, "K": 64, "out_dtype": 0,
+              "Y": FAKE}
+
+
+@pytest.mark.parametrize("change,status", [
+    *[({k: None}, capi.MOE_ERR_INVALID_ARG) for k in ("Xc", "Xs", "Wc", "Ws", "offs", "Y")],
+    *[({k: ODD}, capi.MOE_ERR_INVALID_ARG) for k in ("Xc", "Xs", "Wc", "Ws", "Y")],
+    ({"rows": -1}, capi.MOE_ERR_INVALID_ARG), ({"E": 0}, capi.MOE_ERR_INVALID_ARG), ({"out_dtype": -1}, capi.MOE_ERR_INVALID_ARG),
+    ({"E": 257}, capi.MOE_ERR_UNSUPPORTED), ({"N": 60}, capi.MOE_ERR_UNSUPPORTED), ({"K": 48}, capi.MOE_ERR_UNSUPPORTED),
+    ({"rows": 0, "Xc": None, "Y": None}, capi.MOE_OK),
+])
+def test_mx_grouped_refusals(lib, change, status):
+    a = {**MX_GROUPED, **change}
+    assert lib.moe_mx_grouped_forward(*a.values(), None) == status
