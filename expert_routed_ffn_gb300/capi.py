@@ -8,9 +8,11 @@ fallback: if libmoe.so has not been built (``expert_routed_ffn_gb300.build``),
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -282,39 +284,41 @@ def _need(cond, message):
 
 def _dtype_code(dtype):
     import torch
-    _need(dtype in (torch.bfloat16, torch.float32), f"dtype must be bfloat16 or float32, not {dtype}")
-    return MOE_DTYPE_F32 if dtype == torch.float32 else MOE_DTYPE_BF16
+    if dtype is torch.bfloat16:
+        return MOE_DTYPE_BF16
+    if dtype is torch.float32:
+        return MOE_DTYPE_F32
+    _need(False, f"dtype must be bfloat16 or float32, not {dtype}")
 
 
 def _tensor(t, name, shape, dtype, device):
-    """t is a contiguous tensor of this shape and type on this device (None in shape: any size)."""
+    """t is a contiguous CUDA tensor of this shape and type on this device (None in shape: any size)."""
+    if t.is_cuda and t.dtype is dtype and t.device == device and t.is_contiguous() and t.shape == shape:
+        return
     _need(t.device == device and device.type == "cuda", f"{name} must be on the CUDA device of the other tensors")
     _need(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
     _need(t.dim() == len(shape) and all(s is None or s == n for s, n in zip(shape, t.shape)),
           f"{name} must have shape {list(shape)}, not {list(t.shape)}")
     _need(t.is_contiguous(), f"{name} must be contiguous")
-    return t
 
 
-class _on:
-    """The device of a call's tensors as the current one, and `stream` as its current stream."""
+def _enter(device, stream):
+    """(raw stream, undo): makes the tensors' device the current one and `stream` its current
+    stream (so that outputs are allocated for it).  undo is None where nothing had to change."""
+    import torch
+    index = device.index
+    if stream is None and torch._C._cuda_getDevice() == index:
+        return torch._C._cuda_getCurrentRawStream(index), None
+    undo = contextlib.ExitStack()
+    undo.enter_context(torch.cuda.device(index))
+    if stream is not None:
+        undo.enter_context(torch.cuda.stream(stream))
+    return torch.cuda.current_stream().cuda_stream, undo
 
-    def __init__(self, device, stream):
-        import torch
-        self.device = torch.cuda.device(device)
-        self.stream = None if stream is None else torch.cuda.stream(stream)
 
-    def __enter__(self):
-        import torch
-        self.device.__enter__()
-        if self.stream is not None:
-            self.stream.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-
-    def __exit__(self, *exc):
-        if self.stream is not None:
-            self.stream.__exit__(*exc)
-        self.device.__exit__(*exc)
+def _leave(undo):
+    if undo is not None:
+        undo.close()
 
 
 def operators_status(device=None) -> int:
@@ -327,19 +331,30 @@ def operators_status(device=None) -> int:
 
 def _grouped(name, A, W, offs, out, out_dtype, stream, forward):
     import torch
-    _need(W.dim() == 3, "W must be [E, N, K]")
+    _need(W.dim() == 3 and A.dim() == 2, "W must be [E, N, K] and X or dY [rows, ..]")
     E, N, K = W.shape
     cols, red = (N, K) if forward else (K, N)
-    _tensor(W, "W", (E, N, K), torch.bfloat16, A.device)
-    _tensor(A, "X" if forward else "dY", (None, red), torch.bfloat16, A.device)
-    _tensor(offs, "offs", (E + 1,), torch.int32, A.device)
-    rows = A.shape[0]
-    with _on(A.device, stream) as st:
+    rows, width = A.shape
+    device = A.device
+    bf16 = torch.bfloat16
+    # the usual case in one expression; what it does not cover is named by the checks below
+    if not (A.is_cuda and A.dtype is bf16 and W.dtype is bf16 and offs.dtype is torch.int32 and width == red
+            and offs.dim() == 1 and offs.numel() == E + 1 and W.device == device and offs.device == device
+            and A.is_contiguous() and W.is_contiguous() and offs.is_contiguous()):
+        _tensor(W, "W", (E, N, K), bf16, device)
+        _tensor(A, "X" if forward else "dY", (None, red), bf16, device)
+        _tensor(offs, "offs", (E + 1,), torch.int32, device)
+    raw, undo = _enter(device, stream)
+    try:
         if out is None:
-            out = torch.empty((rows, cols), dtype=out_dtype or torch.bfloat16, device=A.device)
-        _tensor(out, "out", (rows, cols), out_dtype or out.dtype, A.device)
-        check(getattr(load(), name)(_ptr(A), _ptr(W), _ptr(offs), rows, E, N, K, _dtype_code(out.dtype), _ptr(out), st),
-              name)
+            out = torch.empty((rows, cols), dtype=out_dtype or bf16, device=device)
+        else:
+            _tensor(out, "out", (rows, cols), out_dtype or out.dtype, device)
+        status = getattr(_lib or load(), name)(A.data_ptr(), W.data_ptr(), offs.data_ptr(), rows, E, N, K,
+                                               _dtype_code(out.dtype), out.data_ptr(), raw)
+    finally:
+        _leave(undo)
+    check(status, name)
     return out
 
 
@@ -360,20 +375,25 @@ def grouped_wgrad(dY, X, offs, out=None, out_dtype=None, accumulate=False, strea
     out (default: a new [E, N, K] tensor, fp32 unless out_dtype says otherwise).  accumulate:
     add to what out holds."""
     import torch
-    _tensor(X, "X", (None, None), torch.bfloat16, X.device)
-    rows, K = X.shape
-    _tensor(dY, "dY", (rows, None), torch.bfloat16, X.device)
-    N = dY.shape[1]
+    _need(X.dim() == 2 and dY.dim() == 2, "X must be [rows, K] and dY [rows, N]")
     _need(offs.dim() == 1 and offs.numel() >= 2, "offs must be [E + 1]")
-    _tensor(offs, "offs", (None,), torch.int32, X.device)
+    (rows, K), N = X.shape, dY.shape[1]
+    _tensor(X, "X", (rows, K), torch.bfloat16, X.device)
+    _tensor(dY, "dY", (rows, N), torch.bfloat16, X.device)
+    _tensor(offs, "offs", (offs.numel(),), torch.int32, X.device)
     E = offs.numel() - 1
     _need(out is not None or not accumulate, "accumulate needs out")
-    with _on(X.device, stream) as st:
+    raw, undo = _enter(X.device, stream)
+    try:
         if out is None:
             out = torch.empty((E, N, K), dtype=out_dtype or torch.float32, device=X.device)
-        _tensor(out, "out", (E, N, K), out_dtype or out.dtype, X.device)
-        check(load().moe_grouped_wgrad(_ptr(dY), _ptr(X), _ptr(offs), rows, E, N, K, _dtype_code(out.dtype),
-                                       int(accumulate), _ptr(out), st), "moe_grouped_wgrad")
+        else:
+            _tensor(out, "out", (E, N, K), out_dtype or out.dtype, X.device)
+        status = load().moe_grouped_wgrad(dY.data_ptr(), X.data_ptr(), offs.data_ptr(), rows, E, N, K,
+                                          _dtype_code(out.dtype), int(accumulate), out.data_ptr(), raw)
+    finally:
+        _leave(undo)
+    check(status, "moe_grouped_wgrad")
     return out
 
 
@@ -396,14 +416,22 @@ def mx_quantize(X, fmt, codes=None, scales=None, stream=None):
     import torch
     code = _mx_format(fmt)
     (slices, rows, K), cshape, sshape = _mx_shapes(X.shape, fmt)
-    _tensor(X, "X", X.shape, X.dtype, X.device)
-    with _on(X.device, stream) as st:
-        codes = torch.empty(cshape, dtype=torch.uint8, device=X.device) if codes is None else codes
-        scales = torch.empty(sshape, dtype=torch.uint8, device=X.device) if scales is None else scales
-        _tensor(codes, "codes", cshape, torch.uint8, X.device)
-        _tensor(scales, "scales", sshape, torch.uint8, X.device)
-        check(load().moe_mx_quantize(_ptr(X), _dtype_code(X.dtype), slices, rows, K, code, _ptr(codes), _ptr(scales), st),
-              "moe_mx_quantize")
+    device, dtype = X.device, _dtype_code(X.dtype)
+    _tensor(X, "X", X.shape, X.dtype, device)
+    raw, undo = _enter(device, stream)
+    try:
+        if codes is None:
+            codes = torch.empty(cshape, dtype=torch.uint8, device=device)
+        else:
+            _tensor(codes, "codes", cshape, torch.uint8, device)
+        if scales is None:
+            scales = torch.empty(sshape, dtype=torch.uint8, device=device)
+        else:
+            _tensor(scales, "scales", sshape, torch.uint8, device)
+        status = load().moe_mx_quantize(X.data_ptr(), dtype, slices, rows, K, code, codes.data_ptr(), scales.data_ptr(), raw)
+    finally:
+        _leave(undo)
+    check(status, "moe_mx_quantize")
     return codes, scales
 
 
@@ -415,12 +443,17 @@ def mx_dequantize(codes, scales, fmt, dtype=None, out=None, stream=None):
     (slices, rows, K), cshape, sshape = _mx_shapes(shape, fmt)
     _tensor(codes, "codes", cshape, torch.uint8, codes.device)
     _tensor(scales, "scales", sshape, torch.uint8, codes.device)
-    with _on(codes.device, stream) as st:
+    raw, undo = _enter(codes.device, stream)
+    try:
         if out is None:
             out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=codes.device)
-        _tensor(out, "out", shape, dtype or out.dtype, codes.device)
-        check(load().moe_mx_dequantize(_ptr(codes), _ptr(scales), code, slices, rows, K, _dtype_code(out.dtype), _ptr(out),
-                                       st), "moe_mx_dequantize")
+        else:
+            _tensor(out, "out", shape, dtype or out.dtype, codes.device)
+        status = load().moe_mx_dequantize(codes.data_ptr(), scales.data_ptr(), code, slices, rows, K,
+                                          _dtype_code(out.dtype), out.data_ptr(), raw)
+    finally:
+        _leave(undo)
+    check(status, "moe_mx_dequantize")
     return out
 
 
@@ -435,16 +468,22 @@ def mx_grouped_forward(Xc, Xs, Wc, Ws, offs, out=None, out_dtype=None, stream=No
     K = 2 * half
     _tensor(Wc, "Wc", (E, N, half), torch.uint8, Xc.device)
     _tensor(Ws, "Ws", (E, K // 32, N), torch.uint8, Xc.device)
-    _tensor(Xc, "Xc", (None, half), torch.uint8, Xc.device)
+    _need(Xc.dim() == 2, "Xc must be [rows, K / 2]")
     rows = Xc.shape[0]
+    _tensor(Xc, "Xc", (rows, half), torch.uint8, Xc.device)
     _tensor(Xs, "Xs", (K // 32, rows), torch.uint8, Xc.device)
     _tensor(offs, "offs", (E + 1,), torch.int32, Xc.device)
-    with _on(Xc.device, stream) as st:
+    raw, undo = _enter(Xc.device, stream)
+    try:
         if out is None:
             out = torch.empty((rows, N), dtype=out_dtype or torch.bfloat16, device=Xc.device)
-        _tensor(out, "out", (rows, N), out_dtype or out.dtype, Xc.device)
-        check(load().moe_mx_grouped_forward(_ptr(Xc), _ptr(Xs), _ptr(Wc), _ptr(Ws), _ptr(offs), rows, E, N, K,
-                                            _dtype_code(out.dtype), _ptr(out), st), "moe_mx_grouped_forward")
+        else:
+            _tensor(out, "out", (rows, N), out_dtype or out.dtype, Xc.device)
+        status = load().moe_mx_grouped_forward(Xc.data_ptr(), Xs.data_ptr(), Wc.data_ptr(), Ws.data_ptr(), offs.data_ptr(),
+                                               rows, E, N, K, _dtype_code(out.dtype), out.data_ptr(), raw)
+    finally:
+        _leave(undo)
+    check(status, "moe_mx_grouped_forward")
     return out
 
 
@@ -472,14 +511,21 @@ def clip_grad_norm(grads, max_norm, out=None, stream=None):
     _need(set(types) <= {torch.bfloat16, torch.float32}, "the gradients must be bfloat16 or float32")
     _need(out is grads or (types == [o.dtype for o in out] and counts == list(map(torch.Tensor.numel, out))),
           "out must have the gradients' types and sizes")
-    src = list(map(torch.Tensor.data_ptr, grads))
-    dst = src if out is grads else list(map(torch.Tensor.data_ptr, out))
-    table = (MoeGrad * len(grads))(*zip(src, dst, counts, [int(t == torch.float32) for t in types]))
+    n = len(grads)
+    flat = [0] * (5 * n)  # an array of moe_grad: grad, out, count, dtype and its padding
+    flat[0::5] = src = list(map(torch.Tensor.data_ptr, grads))
+    flat[1::5] = src if out is grads else map(torch.Tensor.data_ptr, out)
+    flat[2::5] = counts
+    flat[3::5] = [int(t is torch.float32) for t in types]
+    table = struct.pack("@" + "PPqii" * n, *flat)
     need = ctypes.c_size_t()
-    check(load().moe_clip_workspace(len(grads), ctypes.byref(need)), "moe_clip_workspace")
-    with _on(device, stream) as st:
+    check(load().moe_clip_workspace(n, ctypes.byref(need)), "moe_clip_workspace")
+    raw, undo = _enter(device, stream)
+    try:
         norm = torch.empty((), dtype=torch.float32, device=device)
         work = torch.empty(need.value, dtype=torch.uint8, device=device)
-        check(load().moe_clip_grad_norm(table, len(grads), max_norm, _ptr(norm), _ptr(work), need.value, st),
-              "moe_clip_grad_norm")
+        status = load().moe_clip_grad_norm(table, n, max_norm, norm.data_ptr(), work.data_ptr(), need.value, raw)
+    finally:
+        _leave(undo)
+    check(status, "moe_clip_grad_norm")
     return norm

@@ -9,29 +9,34 @@
 // bf16 operands, products and sums in fp32 on the tensor cores (tcgen05, accumulators in
 // tensor memory), one rounding to the output type.  No operand is transposed in memory:
 // the tensor core reads a shared-memory tile with its reduction index innermost
-// ("K-major": X, dY and W of the forward) or outermost ("MN-major": W of the dgrad, both
-// operands of the wgrad), so all three read the tensors as they are stored.
+// ("K-major": both operands of the forward, dY of the dgrad) or outermost ("MN-major": W of
+// the dgrad, both operands of the wgrad), so all three read the tensors as they are stored.
 //
-// Persistent kernel, 6 warps:
-//   warp 0     TMA producer: per stage one k-block of 64 reduction steps, A tile
-//              [bm rows] and B tile [bn columns], 128-byte swizzle
-//   warp 1     allocates tensor memory; issues tcgen05.mma (M 128, N bn, K 16) into one of
-//              two accumulators, so a tile's epilogue overlaps the next tile's main loop
-//   warps 2-5  epilogue: tcgen05.ld, conversion, a swizzled 4 KB slice per warp in shared
-//              memory, one TMA store (or coalesced stores of the valid rows where the next
-//              expert's rows follow; or load-add-store when accumulating)
+// Persistent kernel on CTA pairs (tcgen05 cta_group::2): a tile is up to 256 output columns
+// (M; 128 in each CTA) x up to 256 output rows (N; each CTA stages half of them), so a CTA
+// brings 32 KB per 64 reduction steps instead of the 48 KB of a 128 x 256 tile of its own,
+// and L2 keeps up with the tensor cores.  Six warps per CTA:
+//   warp 0     TMA producer: per stage 64 reduction steps of this CTA's A (columns) and B
+//              (rows) operand, 128-byte swizzle; both CTAs' copies complete on the barrier
+//              of the even CTA
+//   warp 1     allocates tensor memory; in the even CTA issues tcgen05.mma (K 16) into one
+//              of two accumulators, so a tile's epilogue overlaps the next one's main loop
+//   warps 2-5  epilogue (grouped.cuh)
+//   warp 6     (wgrad) zeroes the rest of tails, see below
 // Every CTA reads the offsets, checks them and derives the tile list itself, so there is
 // no workspace, no launch before the product and no atomic; a tile's sum has a fixed order
 // and results are the same from call to call.
 //
-// The wgrad reduces over an expert's rows, whose number is arbitrary: the last k-block
-// also brings rows of the next expert (or past the buffer).  Whole 16-row steps past the
-// end are not issued, and the MMA warp zeroes the rest of the last step in both operand
-// tiles (a zero in one would not do: the other may hold an infinity or a NaN).
+// The wgrad reduces over an expert's rows, whose number is arbitrary: the last stage also
+// brings rows of the next expert (or past the buffer).  Whole 16-row steps past the end are
+// not issued, and the rest of the last step is zeroed in both operand tiles by warp 6 of
+// each CTA (a zero in one would not do: the other may hold an infinity or a NaN).  Such a
+// stage's copies complete on a barrier of their own CTA, and the stage is handed to the MMA
+// when both CTAs have zeroed.
 //
 // Decreasing or out-of-range offsets: every CTA sees the same, records ERR_BOUNDS and
-// writes nothing.  Every wait is bounded; on a timeout the kernel records ERR_TIMEOUT,
-// drains its copies and MMAs, frees tensor memory and returns.
+// writes nothing.  Every wait is bounded; on a timeout the kernel records ERR_TIMEOUT in
+// both CTAs, lets its copies and MMAs end, frees tensor memory and returns.
 #include <algorithm>
 
 #include "common.cuh"
@@ -45,18 +50,31 @@ namespace {
 
 enum : int { kForward = 0, kDgrad = 1, kWgrad = 2 };
 
-constexpr int kBK = 64;           // reduction steps per stage: 128 bytes of bf16
+constexpr int kBK = 64;                // reduction steps per stage: 128 bytes of bf16
 constexpr int kMaxStages = 12;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kAccCols = 256;     // columns of one accumulator
+constexpr int kThreads = 64 + 32 * kEpiWarps;  // the wgrad has one warp more
+constexpr int kAccCols = 256;          // TMEM columns of one accumulator
 constexpr uint32_t kTmemCols = 2 * kAccCols;
-constexpr int kChunk = 64 * kBK * 2;  // an MN-major tile of 64 columns x 64 reduction rows
-constexpr int kStageSpace = 196608;  // 192 KB of stages
-constexpr int kSmemBytes = kStageSpace + kEpiBytes + 1024 /* alignment */;
+constexpr int kRow = kBK * 2;          // bytes of a K-major row, or of 64 columns in MN-major
+constexpr int kChunk = 64 * kRow;      // an MN-major tile of 64 columns x 64 reduction rows
+constexpr int kBoxes = 8;              // B boxes of 16, 32, .. 128 rows (K-major)
+constexpr int kStageSpace = 229376;    // 224 KB of stages
+
+// Shared memory: the header, then the stages.
+struct Header {
+    uint64_t bars[4 * kMaxStages + 5];
+    TileTable table;
+    uint32_t tmem;
+    volatile int abort;
+};
+constexpr int kHeaderBytes = 3072;
+constexpr int kSmemBytes = kHeaderBytes + kStageSpace;
+static_assert(sizeof(Header) <= kHeaderBytes && kSmemBytes <= 232448, "shared memory of one CTA");
 
 struct GroupedArgs {
-    CUtensorMap map_a, map_b;
+    CUtensorMap map_a, map_b[kBoxes];
     GroupedOut o;
+    int a_stage, b_stage;  // bytes per stage and CTA
     int stages;
 };
 
@@ -72,230 +90,279 @@ __device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr) {
     d |= (uint64_t)2 << 61;
     return d;
 }
-
+__device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
+}
 template <int OP>
-__global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_constant__ GroupedArgs p) {
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t s_bars[2 * kMaxStages + 5];
-    __shared__ int s_offs[kMaxExperts + 1], s_tiles[kMaxExperts + 1];
-    __shared__ uint32_t s_tmem;
-    __shared__ volatile int s_abort;
-    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const int a_stage = (OP == kWgrad ? 128 : p.o.bm) * kBK * 2, b_stage = p.o.bn * kBK * 2;
-    // all A stages first: the MMA reads 128 rows of A where the box brought 32 or 64; the
-    // rest is whatever follows, and its results are not stored
-    const uint32_t sA = base, sB = base + (uint32_t)(p.stages * a_stage), sE = base + kStageSpace;
-    const uint32_t bar0 = smem_u32(s_bars);
+__global__ void __launch_bounds__(kThreads + (OP == kWgrad ? 32 : 0), 1) grouped_kernel(const __grid_constant__ GroupedArgs p) {
+    constexpr bool kDense = OP == kWgrad;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Header &h = *reinterpret_cast<Header *>(smem);
+    const TileTable &tab = h.table;
+    const uint32_t base = smem_u32(smem) + kHeaderBytes;
+    const int a_stage = p.a_stage, b_stage = p.b_stage, stages = p.stages;
+    // all A stages first: the MMA reads 128 columns of A where the box brought 64; the rest is
+    // whatever follows, and its results are not stored
+    const uint32_t sA = base, sB = base + (uint32_t)(stages * a_stage);
+    const uint32_t bar0 = smem_u32(h.bars);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
-    auto tfull_bar = [&](uint32_t a) { return bar0 + 8u * (2 * kMaxStages + a); };
-    auto tempty_bar = [&](uint32_t a) { return bar0 + 8u * (2 * kMaxStages + 2 + a); };
-    const uint32_t drain_bar = bar0 + 8u * (2 * kMaxStages + 4);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    volatile int *abort_flag = &s_abort;
-    auto raise = [&]() {
+    auto tail_bar = [&](int s) { return bar0 + 8u * (2 * kMaxStages + s); };
+    auto zeroed_bar = [&](int s) { return bar0 + 8u * (3 * kMaxStages + s); };
+    auto tfull_bar = [&](uint32_t a) { return bar0 + 8u * (4 * kMaxStages + a); };
+    auto tempty_bar = [&](uint32_t a) { return bar0 + 8u * (4 * kMaxStages + 2 + a); };
+    const uint32_t drain_bar = bar0 + 8u * (4 * kMaxStages + 4);
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank();
+    const bool leader = rank == 0;
+    volatile int *abort_flag = &h.abort;
+    auto raise = [&]() {  // stops both CTAs' roles
         atomicOr(p.o.err, ERR_TIMEOUT);
         *abort_flag = 1;
+        st_cluster_s32(mapa_shared(smem_u32(const_cast<int *>(&h.abort)), (uint32_t)rank ^ 1u), 1);
     };
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kMaxStages; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
+            mbar_init(tail_bar(s), 1);
+            mbar_init(zeroed_bar(s), 2);  // both CTAs'
         }
         for (uint32_t a = 0; a < 2; ++a) {
             mbar_init(tfull_bar(a), 1);
-            mbar_init(tempty_bar(a), kEpiWarps);
+            mbar_init(tempty_bar(a), 2 * kEpiWarps);  // both CTAs'
         }
         mbar_init(drain_bar, 1);
         fence_mbar_init();
-        s_abort = 0;
+        h.abort = 0;
         tma_prefetch_desc(&p.map_a);
-        tma_prefetch_desc(&p.map_b);
-        tma_prefetch_desc(&p.o.map);
+        tma_prefetch_desc(&p.map_b[0]);
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(&s_tmem), kTmemCols);
-        tmem_relinquish();
+        tmem_alloc_pair(smem_u32(&h.tmem), kTmemCols);
+        tmem_relinquish_pair();
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before any copy or arrival crosses over
     tc_fence_after();
-    const uint32_t tmem_base = s_tmem;
+    const uint32_t tmem_base = h.tmem;
     pdl_wait();  // the offsets and operands of earlier kernels on the stream
     pdl_trigger();
-    const bool good = load_offsets<OP == kWgrad>(p.o, s_offs, s_tiles);
-    if (!good && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.o.err, ERR_BOUNDS);
-    const int total = !good ? 0 : OP == kWgrad ? p.o.E * p.o.m_tiles * p.o.n_tiles : s_tiles[p.o.E] * p.o.n_tiles;
-    const int stride = (int)gridDim.x;
+    if (!load_table<kDense>(p.o, h.table) && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.o.err, ERR_BOUNDS);
+    const int total = tab.total;
+    const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
+    const int half_cols = tab.o.cols / 2;
+    // wgrad: the stage at reduction row r ends inside a 16-row step
+    auto is_tail = [&](const Tile &t, int r) { return kDense && t.r1 - r < kBK && (t.r1 - r) % 16 != 0; };
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t L = 0;
-            int s = 0;
-            uint32_t ph = 1;
-            bool ok = true;
-            for (int tile = blockIdx.x; ok && tile < total; tile += stride) {
-                const Tile t = decode<OP == kWgrad>(p.o, tile, s_offs, s_tiles);
-                for (int r = t.r0; r < t.r1; r += kBK) {
-                    if (!mbar_wait(empty_bar(s), ph, kWaitNs, abort_flag)) {
-                        ok = false;
-                        break;
+        uint32_t ph = 1;
+        int s = 0;
+        bool ok = true;
+        for (int tile = first; ok && tile < total; tile += stride) {
+            const Tile t = decode<kDense>(tab, tile);
+            const int col = t.col0 + rank * half_cols, row = t.row0 + rank * (t.n / 2);
+            const bool two_b = t.n / 2 > 64;  // MN-major B: two chunks of 64 columns
+            const CUtensorMap *map_b = kDense ? &p.map_b[0] : &p.map_b[t.n / 32 - 1];  // K-major B: n / 2 rows
+            const uint32_t bytes = a_stage + (kDense ? (two_b ? 2 : 1) * kChunk : (t.n / 2) * kRow);
+            for (int r = t.r0; r < t.r1; r += kBK) {
+                if (!__all_sync(0xffffffffu, wait_bar(empty_bar(s), ph, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t da = sA + s * a_stage, db = sB + s * b_stage;
+                const uint32_t bar = mapa_shared(full_bar(s), 0);
+                if (is_tail(t, r)) {  // complete on this CTA's own barrier, for warp 6 to zero the rest
+                    if (elect_one()) {
+                        if (leader) mbar_arrive(full_bar(s));
+                        mbar_arrive_expect_tx(tail_bar(s), bytes);
+                        tma_load_2d(da, &p.map_a, tail_bar(s), col, r);
+                        if (half_cols > 64) tma_load_2d(da + kChunk, &p.map_a, tail_bar(s), col + 64, r);
+                        tma_load_2d(db, map_b, tail_bar(s), row, r);
+                        if (two_b) tma_load_2d(db + kChunk, map_b, tail_bar(s), row + 64, r);
                     }
-                    const uint32_t bar = full_bar(s), da = sA + s * a_stage, db = sB + s * b_stage;
-                    mbar_arrive_expect_tx(bar, a_stage + b_stage);
-                    if (OP == kWgrad) {
-                        tma_load_2d(da, &p.map_a, bar, t.row0, r);
-                        tma_load_2d(da + kChunk, &p.map_a, bar, t.row0 + 64, r);
-                        for (int c = 0; c < p.o.bn; c += 64) tma_load_2d(db + c * (kBK * 2), &p.map_b, bar, t.col0 + c, r);
+                } else if (elect_one()) {
+                    if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * bytes);
+                    if (OP == kForward) {
+                        tma_load_3d_pair(da, &p.map_a, bar, r, col, t.e);
+                    } else if (OP == kDgrad) {
+                        tma_load_3d_pair(da, &p.map_a, bar, col, r, t.e);
+                        if (half_cols > 64) tma_load_3d_pair(da + kChunk, &p.map_a, bar, col + 64, r, t.e);
                     } else {
-                        tma_load_2d(da, &p.map_a, bar, r, t.row0);
-                        if (OP == kForward)
-                            tma_load_3d(db, &p.map_b, bar, r, t.col0, t.e);
-                        else
-                            for (int c = 0; c < p.o.bn; c += 64)
-                                tma_load_3d(db + c * (kBK * 2), &p.map_b, bar, t.col0 + c, r, t.e);
+                        tma_load_2d_pair(da, &p.map_a, bar, col, r);
+                        if (half_cols > 64) tma_load_2d_pair(da + kChunk, &p.map_a, bar, col + 64, r);
                     }
-                    ++L;
-                    if (++s == p.stages) {
-                        s = 0;
-                        ph ^= 1u;
+                    if (OP != kWgrad) {
+                        tma_load_2d_pair(db, map_b, bar, r, row);
+                    } else {
+                        tma_load_2d_pair(db, map_b, bar, row, r);
+                        if (two_b) tma_load_2d_pair(db + kChunk, map_b, bar, row + 64, r);
                     }
                 }
-            }
-            if (!ok) {
-                raise();
-                for (uint32_t i = 0; i < (uint32_t)p.stages && i < L; ++i) {  // the copies still in flight
-                    const uint32_t l = L - 1 - i;
-                    mbar_wait(full_bar(l % p.stages), (l / p.stages) & 1u, kDrainNs, nullptr);
+                __syncwarp();
+                if (++s == stages) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
         }
+        if (!ok && lane == 0) {
+            raise();
+            // a stage's copies complete together with the other CTA's, which an abort may have
+            // kept from being issued: wait a fixed time for the copies in flight instead
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < kPairDrainNs) __nanosleep(1000);
+        }
     } else if (warp == 1) {
-        // The wgrad's last k-block is zeroed by the whole warp, so there all lanes follow the
-        // loop; otherwise lane 0 alone.
-        if (OP == kWgrad || lane == 0) {
-            const uint32_t idesc = idesc_bf16_f32(128, p.o.bn) | (OP == kWgrad ? 1u << 15 : 0u) | (OP != kForward ? 1u << 16 : 0u);
-            constexpr uint32_t kStepA = OP == kWgrad ? (16 * 128) >> 4 : 2;   // 16 reduction steps on,
-            constexpr uint32_t kStepB = OP == kForward ? 2 : (16 * 128) >> 4;  // in units of 16 bytes
-            uint32_t n_acc = 0, ph = 0;
+        if (leader) {
+            constexpr uint32_t kStepA = OP == kForward ? 2 : (16 * kRow) >> 4;  // 16 reduction steps on,
+            constexpr uint32_t kStepB = OP == kWgrad ? (16 * kRow) >> 4 : 2;    // in units of 16 bytes
+            const uint64_t desc_a = OP == kForward ? smem_desc_k128(sA) : smem_desc_mn128(sA);
+            const uint64_t desc_b = kDense ? smem_desc_mn128(sB) : smem_desc_k128(sB);
+            uint32_t n_acc = 0, ph = 0, zeroed_ph = 0;
             int s = 0;
             bool ok = true, issued = false;
-            auto wait = [&](uint32_t bar, uint32_t parity) {
-                const bool got = mbar_wait(bar, parity, kWaitNs, abort_flag);
-                return OP == kWgrad ? __all_sync(0xffffffffu, got) != 0 : got;
-            };
-            for (int tile = blockIdx.x; ok && tile < total; tile += stride) {
-                const Tile t = decode<OP == kWgrad>(p.o, tile, s_offs, s_tiles);
-                if (t.r0 >= t.r1) continue;  // an expert without rows: the epilogue writes its zeros
-                const uint32_t a = n_acc & 1u;
-                if (!wait(tempty_bar(a), ((n_acc >> 1) & 1u) ^ 1u)) {
+            Tile next;
+            if (first < total) next = decode<kDense>(tab, first);
+            for (int tile = first; ok && tile < total; tile += stride) {
+                const Tile t = next;
+                if (t.r0 >= t.r1) {  // an expert without rows: the epilogue writes its zeros
+                    if (tile + stride < total) next = decode<kDense>(tab, tile + stride);
+                    continue;
+                }
+                const uint32_t idesc = idesc_bf16_f32(256, t.n) | (OP != kForward ? 1u << 15 : 0u) | (kDense ? 1u << 16 : 0u);
+                const uint32_t a = n_acc & 1u, d = tmem_base + a * kAccCols;
+                if (!__all_sync(0xffffffffu, wait_bar<true>(tempty_bar(a), ((n_acc >> 1) & 1u) ^ 1u, abort_flag))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d = tmem_base + a * kAccCols;
                 for (int r = t.r0; r < t.r1; r += kBK) {
-                    if (!wait(full_bar(s), ph)) {
+                    bool got = wait_bar(full_bar(s), ph, abort_flag);
+                    if (is_tail(t, r)) {
+                        got = got && wait_bar<true>(zeroed_bar(s), zeroed_ph >> s & 1u, abort_flag);
+                        zeroed_ph ^= 1u << s;
+                    }
+                    if (!__all_sync(0xffffffffu, got)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t da = sA + s * a_stage, db = sB + s * b_stage;
-                    int steps = kBK / 16;
-                    if (OP == kWgrad && t.r1 - r < kBK) {
-                        const int valid = t.r1 - r;
-                        steps = (valid + 15) / 16;
-                        const int words = (steps * 16 - valid) * 8;  // 16-byte units per 64-column chunk
-                        for (int c = 0; c < 2 + p.o.bn / 64; ++c) {
-                            const uint32_t chunk = (c < 2 ? da + c * kChunk : db + (c - 2) * kChunk) + valid * 128;
-                            for (int w = lane; w < words; w += 32) st_shared_v4(chunk + 16 * w, 0, 0, 0, 0);
-                        }
-                        fence_smem();
-                        __syncwarp();
+                    const uint64_t ad = desc_a + (uint32_t)(s * a_stage >> 4), bd = desc_b + (uint32_t)(s * b_stage >> 4);
+                    const int left = t.r1 - r;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < kBK / 16; ++k)
+                            if (!kDense || 16 * k < left)
+                                tc_mma_bf16_pair(d, ad + k * kStepA, bd + k * kStepB, idesc, (r != t.r0) | (k != 0));
+                        tc_commit_pair(empty_bar(s), 3);  // frees the stage in both CTAs
+                        if (left <= kBK) tc_commit_pair(tfull_bar(a), 3);
                     }
-                    if (lane == 0) {
-                        const uint64_t ad = OP == kWgrad ? smem_desc_mn128(da) : smem_desc_k128(da);
-                        const uint64_t bd = OP == kForward ? smem_desc_k128(db) : smem_desc_mn128(db);
-                        for (int k = 0; k < steps; ++k)
-                            tc_mma_bf16(d, ad + k * kStepA, bd + k * kStepB, idesc, (r != t.r0) | (k != 0));
-                        tc_commit(empty_bar(s));
-                        issued = true;
-                    }
-                    if (++s == p.stages) {
+                    __syncwarp();
+                    issued = true;
+                    // the next tile's place, while this one's products run
+                    if (r == t.r0 && tile + stride < total) next = decode<kDense>(tab, tile + stride);
+                    if (++s == stages) {
                         s = 0;
                         ph ^= 1u;
                     }
                 }
-                if (!ok) break;
-                if (lane == 0) tc_commit(tfull_bar(a));
                 ++n_acc;
             }
             if (!ok && lane == 0) {
                 raise();
                 if (issued) {
-                    tc_commit(drain_bar);
-                    mbar_wait(drain_bar, 0, kDrainNs, nullptr);
+                    tc_commit_pair(drain_bar, 1);
+                    wait_bar(drain_bar, 0, nullptr);
                 }
             }
         }
+    } else if (warp == 2 + kEpiWarps) {
+        // wgrad: zero the rows past each tail's end, then hand the stage to the MMA
+        uint32_t tail_ph = 0;
+        int s = 0;
+        const int chunks_a = half_cols / 64;
+        for (int tile = first; tile < total; tile += stride) {
+            const Tile t = decode<kDense>(tab, tile);
+            const int k_blocks = (t.r1 - t.r0 + kBK - 1) / kBK;
+            const int last = t.r0 + (k_blocks - 1) * kBK;
+            if (k_blocks > 0 && is_tail(t, last)) {
+                const int st = (s + k_blocks - 1) % stages;
+                if (!__all_sync(0xffffffffu, wait_bar(tail_bar(st), tail_ph >> st & 1u, abort_flag))) {
+                    if (lane == 0) raise();
+                    break;
+                }
+                tail_ph ^= 1u << st;
+                const uint32_t da = sA + st * a_stage, db = sB + st * b_stage;
+                const int valid = t.r1 - last, words = ((valid + 15) / 16 * 16 - valid) * (kRow / 16);
+                const int chunks = chunks_a + (t.n / 2 > 64 ? 2 : 1);
+                for (int c = 0; c < chunks; ++c) {
+                    const uint32_t at = (c < chunks_a ? da + c * kChunk : db + (c - chunks_a) * kChunk) + valid * kRow;
+                    for (int w = lane; w < words; w += 32) st_shared_zero16(at + 16 * w);
+                }
+                fence_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(zeroed_bar(st), 0));
+            }
+            s = (s + k_blocks) % stages;
+        }
     } else {
         const int q = warp & 3;  // the TMEM lane quadrant this warp may read
-        const uint32_t sb = sE + (uint32_t)q * 4096u;
+        const int in_half = 32 * q + lane;  // column within this CTA's half
         uint32_t n_acc = 0;
-        for (int tile = blockIdx.x; tile < total; tile += stride) {
-            const Tile t = decode<OP == kWgrad>(p.o, tile, s_offs, s_tiles);
+        for (int tile = first; tile < total; tile += stride) {
+            const Tile t = decode<kDense>(tab, tile);
             const bool empty = t.r0 >= t.r1;
             const uint32_t a = n_acc & 1u;
             if (!empty) {
-                if (!__all_sync(0xffffffffu, mbar_wait(tfull_bar(a), (n_acc >> 1) & 1u, kWaitNs, abort_flag))) {
+                if (!__all_sync(0xffffffffu, wait_bar<true>(tfull_bar(a), (n_acc >> 1) & 1u, abort_flag))) {
                     if (lane == 0) raise();
                     break;
                 }
                 tc_fence_after();
             }
-            store_tile<OP == kWgrad>(p.o, t, tmem_base + a * kAccCols, empty, sb, q, lane);
+            if (32 * q < half_cols)
+                store_tile<kDense>(tab.o, t, tmem_base + ((uint32_t)(q * 32) << 16) + a * kAccCols, empty,
+                                   t.col0 + rank * half_cols + in_half, lane);
             if (!empty) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(tempty_bar(a));
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(a), 0));
                 ++n_acc;
             }
         }
-        if (lane == 0) bulk_wait_all();  // the stores are performed before the CTA ends
     }
 
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // no arrival or MMA of the pair outlives either CTA
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem_base, kTmemCols);
+        tmem_dealloc_pair(tmem_base, kTmemCols);
     }
 }
 
 unsigned long long g_attr[3];
 
-// Tile sizes.  Rows: 32-row boxes while the experts average at most 16 rows, as the fused
-// block's decode tiles.  Columns: the widest tile that still gives every SM one.
+// Tile sizes.  Rows: up to 256, fewer where the experts average fewer.  Columns: 256, or 128
+// (64 per CTA) where 256 would leave SMs without a tile.
 void choose_tiles(GroupedArgs &g, int op, int sms) {
-    GroupedOut &a = g.o;
-    const long long active = std::min<long long>(a.E, a.rows);
-    if (op == kWgrad) {
-        a.bm = 128;
-        a.m_tiles = (a.m_dense + 127) / 128;
-    } else {
-        a.bm = a.rows <= 16ll * a.E ? 32 : 128;
-    }
-    a.bn = 256;
-    while (a.bn > 64) {
-        const long long n = (a.n_out + a.bn - 1) / a.bn;
-        const long long tiles = op == kWgrad ? n * a.m_tiles * a.E : n * std::max<long long>(active, a.rows / a.bm);
-        if (tiles >= sms && a.bn - 64 < a.n_out) break;
-        a.bn /= 2;
-    }
-    a.n_tiles = (a.n_out + a.bn - 1) / a.bn;
-    g.stages = std::min(kMaxStages, kStageSpace / ((a.bm + a.bn) * kBK * 2));
+    GroupedOut &o = g.o;
+    const long long pairs = sms / 2, active = std::max<long long>(1, std::min(o.E, o.rows));
+    const int most = op == kWgrad ? o.m_dense : (int)std::min<long long>(256, 2 * (o.rows / active) + 1);
+    o.tile_rows = 256;
+    while (o.tile_rows > 32 && o.tile_rows / 2 >= most) o.tile_rows /= 2;
+    const long long row_tiles = op == kWgrad ? (long long)o.E * ((o.m_dense + o.tile_rows - 1) / o.tile_rows)
+                                             : std::max<long long>(active, o.rows / o.tile_rows);
+    o.cols = (o.n_out + 255) / 256 * row_tiles >= pairs && o.n_out > 128 ? 256 : 128;
+    o.col_tiles = (o.n_out + o.cols - 1) / o.cols;
+    o.row_tiles = (o.m_dense + o.tile_rows - 1) / o.tile_rows;
+    g.a_stage = o.cols / 2 * kRow;
+    g.b_stage = op == kWgrad ? (o.tile_rows / 2 + 63) / 64 * kChunk : o.tile_rows / 2 * kRow;
+    g.stages = std::min(kMaxStages, kStageSpace / (g.a_stage + g.b_stage));
 }
 
 moe_status check(const char *op, const void *a, const void *b, const int32_t *offs, const void *out, int rows, int E,
@@ -314,56 +381,52 @@ moe_status check(const char *op, const void *a, const void *b, const int32_t *of
     return MOE_OK;
 }
 
-// a: X or dY [rows, ..]; b: W [E, N, K], or X for the wgrad
-moe_status launch(const char *name, int op, const void *a, const void *b, const int32_t *offs, void *out, int rows, int E,
+// x: X or dY [rows, ..]; w: W [E, N, K], or X for the wgrad
+moe_status launch(const char *name, int op, const void *x, const void *w, const int32_t *offs, void *out, int rows, int E,
                   int N, int K, int dtype, int accumulate, moe_stream_t stream) {
     const int sms = op_num_sms();
     int *err = op_error_word();
-    if (sms < 1 || err == nullptr) return op_fail(MOE_ERR_CUDA, "%s: no usable current device", name);
+    if (sms < 2 || err == nullptr) return op_fail(MOE_ERR_CUDA, "%s: no usable current device", name);
     GroupedArgs g = {};
-    g.o.offs = offs;
-    g.o.out = out;
-    g.o.err = err;
-    g.o.E = E;
-    g.o.rows = rows;
-    g.o.n_out = op == kForward ? N : K;
-    g.o.m_dense = N;
-    g.o.red = op == kForward ? K : N;
-    g.o.f32 = dtype == MOE_DTYPE_F32;
-    g.o.accumulate = accumulate;
+    GroupedOut &o = g.o;
+    o.offs = offs;
+    o.out = out;
+    o.err = err;
+    o.E = E;
+    o.rows = rows;
+    o.n_out = op == kForward ? N : K;
+    o.m_dense = N;
+    o.red = op == kForward ? K : N;
+    o.f32 = dtype == MOE_DTYPE_F32;
+    o.accumulate = accumulate;
     choose_tiles(g, op, sms);
-    const long long tiles = op == kWgrad ? (long long)E * g.o.m_tiles * g.o.n_tiles
-                                         : ((long long)rows / g.o.bm + std::min(E, rows)) * g.o.n_tiles;
+    const long long tiles = op == kWgrad ? (long long)E * o.row_tiles * o.col_tiles
+                                         : ((long long)rows / o.tile_rows + std::min(E, rows)) * o.col_tiles;
     if (tiles > (1ll << 30)) return op_fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^30 output tiles", name);
 
     const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
     const uint64_t n = N, k = K, r = rows, e = E;
-    OpMap ma, mb;
+    CUresult cr;
     if (op == kWgrad) {
-        ma = {bf, 2, a, {n, r}, {n * 2}, {64, kBK}, sw};
-        mb = {bf, 2, b, {k, r}, {k * 2}, {64, kBK}, sw};
+        cr = op_encode(&g.map_a, {bf, 2, w, {k, r}, {k * 2}, {64, kBK}, sw});
+        if (cr == CUDA_SUCCESS) cr = op_encode(&g.map_b[0], {bf, 2, x, {n, r}, {n * 2}, {64, kBK}, sw});
     } else {
-        const uint64_t c = g.o.red;
-        ma = {bf, 2, a, {c, r}, {c * 2}, {kBK, (uint32_t)g.o.bm}, sw};
-        mb = {bf, 3, b, {k, n, e}, {k * 2, n * k * 2}, {64, op == kForward ? (uint32_t)g.o.bn : (uint32_t)kBK, 1}, sw};
+        cr = op_encode(&g.map_a, {bf, 3, w, {k, n, e}, {k * 2, n * k * 2},
+                                  {64, op == kForward ? (uint32_t)o.cols / 2 : (uint32_t)kBK, 1}, sw});
+        const uint64_t c = o.red;
+        for (int i = 0; i < o.tile_rows / 32 && cr == CUDA_SUCCESS; ++i)
+            cr = op_encode(&g.map_b[i], {bf, 2, x, {c, r}, {c * 2}, {kBK, 16u * (i + 1)}, sw});
     }
-    const uint64_t es = g.o.f32 ? 4 : 2, cols = g.o.n_out;
-    const OpMap mo = {g.o.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : bf,
-                      3,
-                      out,
-                      {cols, op == kWgrad ? n : r, op == kWgrad ? e : 1},
-                      {cols * es, cols * es * (op == kWgrad ? n : r)},
-                      {(uint32_t)(128 / es), 32, 1},
-                      sw};
-    if (op_encode(&g.map_a, ma) != CUDA_SUCCESS || op_encode(&g.map_b, mb) != CUDA_SUCCESS ||
-        op_encode(&g.o.map, mo) != CUDA_SUCCESS)
-        return op_fail(MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", name);
-    const dim3 grid((unsigned)std::min<long long>(sms, tiles));
+    if (cr != CUDA_SUCCESS) return op_fail(MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", name, (int)cr);
+    const dim3 grid(2u * (unsigned)std::min<long long>(sms / 2, tiles));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     auto go = [&](auto kernel) -> cudaError_t {
-        const cudaError_t err2 = op_allow_smem(reinterpret_cast<const void *>(kernel), kSmemBytes, &g_attr[op]);
-        return err2 != cudaSuccess ? err2 : launch_pdl(kernel, grid, dim3(kThreads), (size_t)kSmemBytes, s, g);
+        const cudaError_t ce = op_allow_smem(reinterpret_cast<const void *>(kernel), kSmemBytes, &g_attr[op]);
+        return ce != cudaSuccess
+                   ? ce
+                   : launch_pdl_cluster(kernel, grid, dim3(kThreads + (op == kWgrad ? 32 : 0)), (size_t)kSmemBytes, s,
+                                        dim3(2, 1, 1), g);
     };
     return op_cuda(op == kForward ? go(grouped_kernel<kForward>)
                                   : op == kDgrad ? go(grouped_kernel<kDgrad>) : go(grouped_kernel<kWgrad>),

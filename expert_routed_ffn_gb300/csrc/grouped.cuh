@@ -1,5 +1,11 @@
 // What the products over expert-grouped rows share: the tile list derived from the row
 // offsets, and the epilogue that moves a tile from tensor memory to its output rows.
+//
+// A tile is computed with the output's columns as the MMA's M and the output's rows (the
+// tokens) as its N.  N goes in steps of 32, so an expert with 300 rows costs two tiles of
+// 160 rather than three of 128, and one token costs 32; and since a TMEM lane is an output
+// column, a warp's store of one row is 32 consecutive columns: results go from registers
+// straight to memory, whatever the number of valid rows.
 #pragma once
 
 #include <algorithm>
@@ -12,15 +18,13 @@ namespace moe {
 
 constexpr int kMaxExperts = 256;
 constexpr int kEpiWarps = 4;          // epilogue warps, one per TMEM lane quadrant
-constexpr int kEpiBytes = kEpiWarps * 4096;
-constexpr unsigned long long kWaitNs = 2000000000ull;   // bound of every wait
-constexpr unsigned long long kDrainNs = 1000000000ull;  // bound of the drain after an abort
+constexpr long long kWaitCycles = 4000000000ll;         // bound of every wait (about 2 s)
+constexpr unsigned long long kPairDrainNs = 1000000ull; // grace for the copies in flight after an abort
 
 // The output and its tiles.  Row-grouped (forward, dgrad): out [rows, n_out], the rows of
 // expert e are [offs[e], offs[e + 1]).  Dense (wgrad): out [E, m_dense, n_out], and the
 // offsets bound the reduction.
 struct GroupedOut {
-    CUtensorMap map;  // boxes of [32 rows][128 bytes], 128-byte swizzle
     const int32_t *offs;
     void *out;
     int *err;
@@ -28,53 +32,87 @@ struct GroupedOut {
     int n_out;       // columns of the output
     int m_dense;     // dense: rows of one expert's output
     int red;         // row-grouped: length of the reduction
-    int bm, bn;      // tile: rows (32 or 128) and columns
-    int n_tiles;     // tiles along the output columns
-    int m_tiles;     // dense: tiles along m_dense
+    int cols;        // a tile's output columns, half of them in each CTA of a pair
+    int tile_rows;   // most output rows of a tile, a multiple of 32
+    int col_tiles;   // tiles along the output columns
+    int row_tiles;   // dense: tiles along m_dense
     int f32;         // output type: fp32, else bf16
     int accumulate;  // dense: add to the output
 };
 
 struct Tile {
-    int e, row0, m_valid, col0;  // expert, first output row, valid rows, first output column
+    int e, row0, rows, n, col0;  // expert, first output row, valid rows, MMA N, first output column
     int r0, r1;                  // reduction range
 };
 
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
-}
 __device__ __forceinline__ void fence_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t src, int x, int y, int z) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(src), "r"(x), "r"(y), "r"(z)
-                 : "memory");
+// 2D load into this CTA's shared memory, completing on a barrier of either CTA of the pair
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
 }
 
-// Expert offsets into s_offs, their tile prefix into s_tiles; false (in every CTA alike)
-// if they decrease or leave [0, rows].
+// Wait until the phase of parity `parity` of a barrier has completed; CLUSTER: a barrier that
+// threads of the other CTA arrive on.  Bounded by the SM's clock (the global timer is slow to
+// read beside waits this short).  False after the bound, or once *abort is set.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort) {
+    auto done = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+    if (done()) return true;
+    const long long t0 = clock64();
+    for (;;) {
+        if (done()) return true;
+        if (abort != nullptr && *abort) return false;
+        if (clock64() - t0 > kWaitCycles) return false;
+    }
+}
+
+// One lane of a converged warp.  The roles that issue copies and MMAs run their loops on the
+// whole warp and only the instructions themselves on one lane: the addresses and descriptors
+// stay warp-uniform, which is what those instructions take (with the loop itself on one lane,
+// issuing a stage's four MMAs measured 350 cycles of the 416 that they run).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
+// What every role reads per tile, in shared memory.
+struct TileTable {
+    GroupedOut o;                      // a parameter read that misses the constant cache costs more
+    int offs[kMaxExperts + 1];         // first row of each expert
+    int tiles[kMaxExperts];            // row-grouped: its first row tile; INT_MAX behind the last
+    uint16_t share[kMaxExperts];       // row-grouped: rows of its tiles but the last, a multiple of 32
+    int total;                         // tiles, 0 where the offsets decrease or leave [0, rows]
+};
+
+// Fill the table (all threads of the CTA); false, in every CTA alike, for bad offsets.
 template <bool DENSE>
-__device__ __forceinline__ bool load_offsets(const GroupedOut &p, int *s_offs, int *s_tiles) {
+__device__ __forceinline__ bool load_table(const GroupedOut &p, TileTable &tab) {
     const int E = p.E;
-    for (int i = threadIdx.x; i <= E; i += blockDim.x) s_offs[i] = p.offs[i];
+    if (threadIdx.x == 0) tab.o = p;
+    for (int i = threadIdx.x; i <= E; i += blockDim.x) tab.offs[i] = p.offs[i];
     __syncthreads();
     int bad = 0;
-    for (int i = threadIdx.x; i < E; i += blockDim.x) bad |= s_offs[i] > s_offs[i + 1];
-    bad |= s_offs[0] < 0 || s_offs[E] > p.rows;
-    if (__syncthreads_or(bad)) return false;
-    if (!DENSE && threadIdx.x < 32) {
+    for (int i = threadIdx.x; i < E; i += blockDim.x) bad |= tab.offs[i] > tab.offs[i + 1];
+    bad |= tab.offs[0] < 0 || tab.offs[E] > p.rows;
+    const bool ok = !__syncthreads_or(bad);
+    if (threadIdx.x < 32) {
         constexpr int kPer = kMaxExperts / 32;
         const int lane = threadIdx.x;
         int cnt[kPer], sum = 0;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            const int e = lane * kPer + j;
-            cnt[j] = e < E ? (s_offs[e + 1] - s_offs[e] + p.bm - 1) / p.bm : 0;
+            const int e = lane * kPer + j, rows = !DENSE && ok && e < E ? tab.offs[e + 1] - tab.offs[e] : 0;
+            cnt[j] = (rows + p.tile_rows - 1) / p.tile_rows;
+            if (!DENSE && cnt[j] > 0) tab.share[e] = (uint16_t)(((rows + cnt[j] - 1) / cnt[j] + 31) & ~31);
             sum += cnt[j];
         }
         int incl = sum;
@@ -87,139 +125,127 @@ __device__ __forceinline__ bool load_offsets(const GroupedOut &p, int *s_offs, i
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             const int e = lane * kPer + j;
-            if (e <= E) s_tiles[e] = run;
+            tab.tiles[e] = e < E ? run : 0x7fffffff;
             run += cnt[j];
         }
-        if (lane == 31 && E == kMaxExperts) s_tiles[E] = run;
+        if (lane == 31) tab.total = !ok ? 0 : DENSE ? E * p.row_tiles * p.col_tiles : run * p.col_tiles;
     }
     __syncthreads();
-    return true;
+    return ok;
 }
 
-// Tile number -> tile.  Inside an expert the row tiles of one column tile are adjacent, so
-// that concurrent CTAs share its weights in L2.
+// Tile number -> tile, by a converged warp.  Inside an expert the row tiles of one column tile
+// are adjacent, so that concurrent CTAs share its weights in L2; its rows are dealt evenly to
+// its row tiles, in multiples of 32 (no tile is left empty: with `parts` tiles of at most T
+// rows either parts <= T / 32, and rounding shares up takes fewer than `parts` * 32 of the more
+// than T * (parts - 1) rows, or the shares are T).
 template <bool DENSE>
-__device__ __forceinline__ Tile decode(const GroupedOut &p, int tile, const int *s_offs, const int *s_tiles) {
+__device__ __forceinline__ Tile decode(const TileTable &tab, int tile) {
+    const GroupedOut &p = tab.o;
     Tile t;
     if (DENSE) {
-        const int per = p.m_tiles * p.n_tiles;
-        t.e = tile / per;
-        const int local = tile - t.e * per;
-        t.col0 = (local / p.m_tiles) * p.bn;
-        t.row0 = (local % p.m_tiles) * 128;
-        t.m_valid = min(128, p.m_dense - t.row0);
-        t.r0 = s_offs[t.e];
-        t.r1 = s_offs[t.e + 1];
+        const int parts = p.row_tiles, strip = tile / parts;  // (expert, column tile)
+        t.e = strip / p.col_tiles;
+        t.col0 = (strip - t.e * p.col_tiles) * p.cols;
+        t.row0 = (tile - strip * parts) * p.tile_rows;
+        t.rows = min(p.tile_rows, p.m_dense - t.row0);
+        t.r0 = tab.offs[t.e];
+        t.r1 = tab.offs[t.e + 1];
     } else {
-        int lo = 0, hi = p.E - 1;  // the last expert whose first tile is <= tile
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_tiles[mid] * p.n_tiles <= tile)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        const int mt = s_tiles[lo + 1] - s_tiles[lo];
-        const int local = tile - s_tiles[lo] * p.n_tiles;
-        t.e = lo;
-        t.col0 = (local / mt) * p.bn;
-        t.row0 = s_offs[lo] + (local % mt) * p.bm;
-        t.m_valid = min(p.bm, s_offs[lo + 1] - t.row0);
+        // the last expert whose first tile is <= tile (one with rows: the next ones start later)
+        const int lane = threadIdx.x & 31;
+        const int row_tile = tile / p.col_tiles;  // experts are whole multiples of col_tiles
+        const int group = __popc(__ballot_sync(0xffffffffu, tab.tiles[lane * (kMaxExperts / 32)] <= row_tile)) - 1;
+        const int in = __popc(__ballot_sync(0xffffffffu, lane < kMaxExperts / 32 &&
+                                                              tab.tiles[group * (kMaxExperts / 32) + lane] <= row_tile));
+        t.e = group * (kMaxExperts / 32) + in - 1;
+        const int first = tab.offs[t.e], end = tab.offs[t.e + 1];
+        const int share = tab.share[t.e], parts = (end - first + p.tile_rows - 1) / p.tile_rows;
+        const int local = tile - tab.tiles[t.e] * p.col_tiles, strip = local / parts;
+        t.col0 = strip * p.cols;
+        t.row0 = first + (local - strip * parts) * share;
+        t.rows = min(share, end - t.row0);
         t.r0 = 0;
         t.r1 = p.red;
     }
+    t.n = (t.rows + 31) & ~31;
     return t;
 }
 
-// One warp's slice of the output, [32 rows][128 bytes of fp32 or bf16 columns] in its
-// swizzled staging buffer `sb` (lane i wrote row i; 16-byte unit j at j ^ (i % 8)).
-template <bool DENSE>
-__device__ __forceinline__ void flush(const GroupedOut &p, const Tile &t, uint32_t sb, int row, int rows, int col,
-                                      int lane) {
-    const int u = lane & 7;
-    if (DENSE && p.accumulate) {  // staged as 32 fp32 columns: dW + the product, in fp32
-        __syncwarp();
-        const int c = col + 4 * u;
-        for (int i = lane >> 3; i < rows; i += 4) {
-            const uint4 v = ld_shared_v4(sb + (uint32_t)i * 128u + ((uint32_t)(u ^ (i & 7)) << 4));
-            if (c >= p.n_out) continue;
-            const size_t at = ((size_t)t.e * p.m_dense + row + i) * p.n_out + c;
-            if (p.f32) {
-                float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at);
-                float4 old = *o;
-                old.x += __uint_as_float(v.x);
-                old.y += __uint_as_float(v.y);
-                old.z += __uint_as_float(v.z);
-                old.w += __uint_as_float(v.w);
-                *o = old;
+// A tile's epilogue by one warp: TMEM lane = output column `col` (its own lane's; `col_ok`:
+// inside the output), column = row.  `tcol`: the accumulator, at the warp's lane quadrant;
+// `empty`: there is no sum, zeros are stored.  ADD: to what the output holds, in fp32.
+template <bool DENSE, bool ADD>
+__device__ __forceinline__ void store_rows(const GroupedOut &p, const Tile &t, uint32_t tcol, bool empty, int col,
+                                           int lane) {
+    const bool ok = col < p.n_out;
+    const size_t row0 = (DENSE ? (size_t)t.e * p.m_dense : 0) + t.row0;
+    const size_t ld = p.n_out;
+    for (int c = 0; c < t.rows; c += 32) {
+        uint32_t v[32];
+        if (DENSE && empty) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0u;
+        } else {
+            tmem_ld32(tcol + c, v);
+            tmem_ld_wait();
+        }
+        const int rows = ok ? min(32, t.rows - c) : 0;
+        if (p.f32) {
+            float *o = static_cast<float *>(p.out) + (row0 + c) * ld + col;
+            if (ADD) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (j < rows) v[j] = __float_as_uint(__uint_as_float(v[j]) + o[j * ld]);
+            }
+            if (rows == 32) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j * ld] = __uint_as_float(v[j]);
             } else {
-                uint2 *o = reinterpret_cast<uint2 *>(static_cast<bf16 *>(p.out) + at);
-                const uint2 old = *o;
-                *o = make_uint2(pack_bf16x2(bf16_lo(old.x) + __uint_as_float(v.x), bf16_hi(old.x) + __uint_as_float(v.y)),
-                                pack_bf16x2(bf16_lo(old.y) + __uint_as_float(v.z), bf16_hi(old.y) + __uint_as_float(v.w)));
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (j < rows) o[j * ld] = __uint_as_float(v[j]);
+            }
+        } else {
+            // n_out is even, so lanes 2i and 2i + 1 are in or out together: the even lane takes
+            // both columns of row j, the odd one of row j + 1, in one 4-byte access
+            const int odd = lane & 1;
+            uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<bf16 *>(p.out) + (row0 + c + odd) * ld + (col & ~1));
+            const int left = rows - odd;
+            uint32_t w[16], old[16];
+            if (ADD) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) old[j] = 2 * j < left ? o[j * ld] : 0u;  // two rows on: n_out words
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const uint32_t mine = odd ? v[2 * j + 1] : v[2 * j], give = odd ? v[2 * j] : v[2 * j + 1];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
+                float lo = __uint_as_float(odd ? got : mine), hi = __uint_as_float(odd ? mine : got);
+                if (ADD) {
+                    lo += bf16_lo(old[j]);
+                    hi += bf16_hi(old[j]);
+                }
+                w[j] = pack_bf16x2(lo, hi);
+            }
+            if (rows == 32) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j * ld] = w[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (2 * j < left) o[j * ld] = w[j];
             }
         }
-        __syncwarp();
-    } else if (DENSE || rows == 32) {  // past N or n_out the copy engine writes nothing
-        fence_smem();
-        __syncwarp();
-        if (lane == 0) {
-            tma_store_3d(&p.map, sb, col, row, DENSE ? t.e : 0);
-            bulk_commit();
-        }
-    } else {
-        __syncwarp();
-        const int es = p.f32 ? 4 : 2, c = col + (16 / es) * u;
-        for (int i = lane >> 3; i < rows; i += 4) {
-            const uint4 v = ld_shared_v4(sb + (uint32_t)i * 128u + ((uint32_t)(u ^ (i & 7)) << 4));
-            if (c < p.n_out)
-                *reinterpret_cast<uint4 *>(static_cast<char *>(p.out) + ((size_t)(row + i) * p.n_out + c) * es) = v;
-        }
-        __syncwarp();
     }
 }
-
-// The epilogue of one tile by one warp (TMEM lane quadrant q): its accumulator's columns at
-// `tcol`, `empty` where there is no sum and zeros are stored.  `sb`: the warp's 4 KB staging
-// buffer in shared memory.
 template <bool DENSE>
-__device__ __forceinline__ void store_tile(const GroupedOut &p, const Tile &t, uint32_t tcol, bool empty, uint32_t sb,
-                                           int q, int lane) {
-    const int rows = min(32, t.m_valid - 32 * q);
-    if (rows <= 0 || (DENSE && empty && p.accumulate)) return;  // warp-uniform
-    const bool wide = p.f32 || (DENSE && p.accumulate);         // staged as fp32
-    const uint32_t tb = tcol + ((uint32_t)(q * 32) << 16), srow = sb + (uint32_t)lane * 128u;
-    const int sw = lane & 7, end = min(p.bn, p.n_out - t.col0), step = wide ? 32 : 64;
-#pragma unroll 1
-    for (int c0 = 0; c0 < end; c0 += step) {
-        if (lane == 0) bulk_wait_read_all();  // the previous slice's store has read the buffer
-        __syncwarp();
-#pragma unroll 1
-        for (int h = 0; h < step; h += 32) {
-            uint32_t v[32];
-            if (DENSE && empty) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = 0u;
-            } else {
-                tmem_ld32(tb + c0 + h, v);
-                tmem_ld_wait();
-            }
-            if (wide) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    st_shared_v4(srow + ((uint32_t)(j ^ sw) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-            } else {
-                uint32_t o[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    o[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    st_shared_v4(srow + ((uint32_t)((h / 8 + j) ^ sw) << 4), o[4 * j], o[4 * j + 1], o[4 * j + 2],
-                                 o[4 * j + 3]);
-            }
-        }
-        flush<DENSE>(p, t, sb, t.row0 + 32 * q, rows, t.col0 + c0, lane);
+__device__ __forceinline__ void store_tile(const GroupedOut &p, const Tile &t, uint32_t tcol, bool empty, int col,
+                                           int lane) {
+    if (DENSE && p.accumulate) {
+        if (!empty) store_rows<DENSE, true>(p, t, tcol, false, col, lane);
+    } else {
+        store_rows<DENSE, false>(p, t, tcol, empty, col, lane);
     }
 }
 

@@ -5,19 +5,22 @@
 // scales as it accumulates in fp32: nothing is decoded, so a k-step of 256 values is 128
 // bytes of codes per row, a quarter of bf16's.
 //
-// Persistent kernel, 14 warps:
-//   warp 0      TMA producer: codes of bm token rows and bn weight rows, 256 values
-//               (128 bytes, 128-byte swizzle) per stage
-//   warp 1      allocates tensor memory; copies a stage's scales from shared to tensor
-//               memory (tcgen05.cp, in order with the MMAs that follow) and issues the MMAs
+// Persistent kernel on CTA pairs with the tiles of the bf16 products (grouped.cu): 256
+// weight rows as the MMA's M, up to 192 token rows as its N.  14 warps per CTA:
+//   warp 0      TMA producer: codes of this CTA's weight rows and half of the token rows,
+//               256 values (128 bytes, 128-byte swizzle) per stage
+//   warp 1      allocates tensor memory; in the even CTA copies a stage's scales from shared
+//               to tensor memory of both CTAs (tcgen05.cp, in order with the MMAs that
+//               follow) and issues the MMAs
 //   warps 2-5   epilogue (grouped.cuh), overlapping the next tile's main loop
 //   warps 6-13  scales, two sets of four warps taking alternate stages.  The tensor core
 //               wants four consecutive blocks' scales of a row in one word, the tensors hold a
 //               block's scales for consecutive rows: the warps read runs along the rows,
-//               transpose in registers and write the words where tcgen05.cp reads them.  A
-//               set's loads for its next stage are in flight while it waits to store this one.
-// Tensor memory (512 columns): two accumulators of bn columns, then per stage the scales of
-// the tokens (8 columns) and of the weights (8 per 128 of them).
+//               transpose in registers and write the words where tcgen05.cp reads them; each
+//               CTA those of its own weight rows and of all the tile's tokens.  A set's loads
+//               for its next stage are in flight while it waits to store this one.
+// Tensor memory (512 columns): two accumulators of up to 192 columns, then per stage the
+// scales of the weights (8 columns) and of the tokens (8 per 128 of them).
 #include <algorithm>
 
 #include "common.cuh"
@@ -29,21 +32,33 @@
 namespace moe {
 namespace {
 
-constexpr int kBK = 256;           // values per stage: 128 bytes of codes
+constexpr int kBK = 256;           // values per stage
+constexpr int kRow = kBK / 2;      // their bytes: one row of codes
 constexpr int kBlocks = kBK / 32;  // scale blocks per stage
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 16;
 constexpr int kScaleSets = 2;
 constexpr int kThreads = 64 + 32 * kEpiWarps + 128 * kScaleSets;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMaxBn = 192;
-constexpr int kScaleStage = 1024 + 2048;  // tokens' and weights' scale words of a stage
-constexpr int kStageSpace = 196608;
-constexpr int kSmemBytes = kStageSpace + kEpiBytes + 1024 /* alignment */;
+constexpr int kMaxRows = 192;      // token rows of a tile
+constexpr int kBoxes = kMaxRows / 32;
+constexpr int kStageSpace = 225280;
+
+struct Header {
+    uint64_t bars[3 * kMaxStages + 5];
+    TileTable table;
+    uint32_t tmem;
+    volatile int abort;
+};
+constexpr int kHeaderBytes = 4096;
+constexpr int kSmemBytes = kHeaderBytes + kStageSpace;
+static_assert(sizeof(Header) <= kHeaderBytes && kSmemBytes <= 232448, "shared memory of one CTA");
 
 struct MxGroupedArgs {
-    CUtensorMap map_a, map_b;
+    CUtensorMap map_a, map_b[kBoxes];  // weight codes; token codes in boxes of 16, 32, .. rows
     GroupedOut o;
-    const uint8_t *xs, *ws;  // [K / 32, rows], [E, K / 32, N]
+    const uint8_t *xs, *ws;            // [K / 32, rows], [E, K / 32, N]
+    int a_stage, b_stage;              // bytes of codes per stage and CTA
+    int atoms;                         // 128-row groups of token scales
     int stages;
 };
 
@@ -53,304 +68,338 @@ struct MxGroupedArgs {
 __device__ __forceinline__ uint32_t idesc_mxf4(int M, int N) {
     return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void tc_mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                            uint32_t accumulate) {
+__device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                                 uint32_t sfb, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
+// 512 bytes of scales in shared memory: no swizzle; 8-lane groups of 16-byte rows 128 bytes apart
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+}
 // 512 bytes of shared memory (32 lanes x 16 bytes) to four columns of tensor memory, the same
-// in each of its four lane quadrants
-__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint32_t saddr) {
-    // no swizzle; 8-lane groups of 16-byte rows 128 bytes apart
-    const uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+// in each of its four lane quadrants; in both CTAs, each from its own shared memory
+__device__ __forceinline__ void tc_copy_scales_pair(uint32_t taddr, uint64_t d) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
 __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+constexpr int kTokenTasks = kMaxRows * 2 / 128;  // (row, four blocks) pairs per scale thread
+
 // One scale thread's share of a stage, between its loads and its stores.
 struct Scales {
-    uint32_t a[2];  // its token row's words (blocks 0-3, 4-7)
-    uint32_t b[4];  // four weight rows' bytes of four blocks
+    uint32_t w[4];            // four weight rows' bytes of four blocks
+    uint32_t x[kTokenTasks];  // token rows' words
 };
 
 __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_constant__ MxGroupedArgs p) {
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t s_bars[3 * kMaxStages + 5];
-    __shared__ int s_offs[kMaxExperts + 1], s_tiles[kMaxExperts + 1];
-    __shared__ uint32_t s_tmem;
-    __shared__ volatile int s_abort;
-    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const int bn = p.o.bn, atoms = (bn + 127) / 128;  // 128-row groups of weight scales
-    const int a_stage = p.o.bm * 128, b_stage = bn * 128;
-    const uint32_t sA = base, sB = base + (uint32_t)(p.stages * a_stage), sS = sB + (uint32_t)(p.stages * b_stage),
-                   sE = base + kStageSpace;
-    const uint32_t bar0 = smem_u32(s_bars);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Header &h = *reinterpret_cast<Header *>(smem);
+    const TileTable &tab = h.table;
+    const uint32_t base = smem_u32(smem) + kHeaderBytes;
+    const int a_stage = p.a_stage, b_stage = p.b_stage, stages = p.stages;
+    const int scale_stage = 1024 + 1024 * p.atoms;
+    // A first: the MMA reads 128 rows of A where the box brought 64; the rest is whatever
+    // follows, and its results are not stored
+    const uint32_t sA = base, sB = sA + (uint32_t)(p.stages * p.a_stage), sS = sB + (uint32_t)(p.stages * p.b_stage);
+    const uint32_t bar0 = smem_u32(h.bars);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto scale_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
     auto empty_bar = [&](int s) { return bar0 + 8u * (2 * kMaxStages + s); };
     auto tfull_bar = [&](uint32_t a) { return bar0 + 8u * (3 * kMaxStages + a); };
     auto tempty_bar = [&](uint32_t a) { return bar0 + 8u * (3 * kMaxStages + 2 + a); };
     const uint32_t drain_bar = bar0 + 8u * (3 * kMaxStages + 4);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    volatile int *abort_flag = &s_abort;
-    auto raise = [&]() {
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank();
+    const bool leader = rank == 0;
+    volatile int *abort_flag = &h.abort;
+    auto raise = [&]() {  // stops both CTAs' roles
         atomicOr(p.o.err, ERR_TIMEOUT);
         *abort_flag = 1;
+        st_cluster_s32(mapa_shared(smem_u32(const_cast<int *>(&h.abort)), (uint32_t)rank ^ 1u), 1);
     };
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kMaxStages; ++s) {
+        for (int s = 0; s < p.stages; ++s) {
             mbar_init(full_bar(s), 1);
-            mbar_init(scale_bar(s), 4);
+            mbar_init(scale_bar(s), 8);  // four warps of each CTA
             mbar_init(empty_bar(s), 1);
         }
         for (uint32_t a = 0; a < 2; ++a) {
             mbar_init(tfull_bar(a), 1);
-            mbar_init(tempty_bar(a), kEpiWarps);
+            mbar_init(tempty_bar(a), 2 * kEpiWarps);
         }
         mbar_init(drain_bar, 1);
         fence_mbar_init();
-        s_abort = 0;
+        h.abort = 0;
         tma_prefetch_desc(&p.map_a);
-        tma_prefetch_desc(&p.map_b);
-        tma_prefetch_desc(&p.o.map);
+        tma_prefetch_desc(&p.map_b[0]);
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(&s_tmem), kTmemCols);
-        tmem_relinquish();
+        tmem_alloc_pair(smem_u32(&h.tmem), kTmemCols);
+        tmem_relinquish_pair();
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before any copy or arrival crosses over
     tc_fence_after();
-    const uint32_t tmem_base = s_tmem;
+    const uint32_t tmem_base = h.tmem;
     pdl_wait();
     pdl_trigger();
-    const bool good = load_offsets<false>(p.o, s_offs, s_tiles);
-    if (!good && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.o.err, ERR_BOUNDS);
-    const int total = good ? s_tiles[p.o.E] * p.o.n_tiles : 0;
-    const int stride = (int)gridDim.x;
-    const int K = p.o.red, k_stages = (K + kBK - 1) / kBK;
+    if (!load_table<false>(p.o, h.table) && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.o.err, ERR_BOUNDS);
+    const int total = tab.total;
+    const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
+    const int half_cols = tab.o.cols / 2, atoms = p.atoms;
+    const int K = tab.o.red, k_stages = (K + kBK - 1) / kBK;
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t L = 0, ph = 1;
-            int s = 0;
-            bool ok = true;
-            for (int tile = blockIdx.x; ok && tile < total; tile += stride) {
-                const Tile t = decode<false>(p.o, tile, s_offs, s_tiles);
-                for (int k = 0; k < k_stages; ++k) {
-                    if (!mbar_wait(empty_bar(s), ph, kWaitNs, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_arrive_expect_tx(full_bar(s), a_stage + b_stage);
-                    tma_load_2d(sA + s * a_stage, &p.map_a, full_bar(s), k * 128, t.row0);
-                    tma_load_3d(sB + s * b_stage, &p.map_b, full_bar(s), k * 128, t.col0, t.e);
-                    ++L;
-                    if (++s == p.stages) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+        uint32_t ph = 1;
+        int s = 0;
+        bool ok = true;
+        for (int tile = first; ok && tile < total; tile += stride) {
+            const Tile t = decode<false>(tab, tile);
+            const int col = t.col0 + rank * half_cols, row = t.row0 + rank * (t.n / 2);
+            const CUtensorMap *map_b = &p.map_b[t.n / 32 - 1];
+            const uint32_t bytes = a_stage + (t.n / 2) * kRow;
+            for (int k = 0; k < k_stages; ++k) {
+                if (!__all_sync(0xffffffffu, wait_bar(empty_bar(s), ph, abort_flag))) {
+                    ok = false;
+                    break;
                 }
-            }
-            if (!ok) {
-                raise();
-                for (uint32_t i = 0; i < (uint32_t)p.stages && i < L; ++i) {  // the copies still in flight
-                    const uint32_t l = L - 1 - i;
-                    mbar_wait(full_bar(l % p.stages), (l / p.stages) & 1u, kDrainNs, nullptr);
+                const uint32_t bar = mapa_shared(full_bar(s), 0);
+                if (elect_one()) {
+                    if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * bytes);
+                    tma_load_3d_pair(sA + s * a_stage, &p.map_a, bar, k * kRow, col, t.e);
+                    tma_load_2d_pair(sB + s * b_stage, map_b, bar, k * kRow, row);
+                }
+                __syncwarp();
+                if (++s == stages) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
         }
+        if (!ok && lane == 0) {
+            raise();
+            // a stage's copies complete together with the other CTA's, which an abort may have
+            // kept from being issued: wait a fixed time for the copies in flight instead
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < kPairDrainNs) __nanosleep(1000);
+        }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = idesc_mxf4(128, bn);
-            const uint32_t cols_a = 8, cols_s = cols_a + 8 * atoms;  // scale columns of a stage
-            const uint32_t scale0 = tmem_base + 2 * bn;
+        if (leader) {
+            const uint32_t acc_cols = tab.o.tile_rows;
+            const uint32_t cols_s = 8 + 8 * atoms;  // scale columns of a stage
+            const uint32_t scale0 = tmem_base + 2 * acc_cols;
+            const uint64_t desc_a = smem_desc_k128(sA), desc_b = smem_desc_k128(sB), desc_s = scale_desc(sS);
             uint32_t n_acc = 0, ph = 0;
             int s = 0;
             bool ok = true, issued = false;
-            for (int tile = blockIdx.x; ok && tile < total; tile += stride) {
-                const uint32_t a = n_acc & 1u;
-                if (!mbar_wait(tempty_bar(a), ((n_acc >> 1) & 1u) ^ 1u, kWaitNs, abort_flag)) {
+            Tile next;
+            if (first < total) next = decode<false>(tab, first);
+            for (int tile = first; ok && tile < total; tile += stride) {
+                const Tile t = next;
+                const uint32_t idesc = idesc_mxf4(256, t.n);
+                const uint32_t a = n_acc & 1u, d = tmem_base + a * acc_cols;
+                if (!__all_sync(0xffffffffu, wait_bar<true>(tempty_bar(a), ((n_acc >> 1) & 1u) ^ 1u, abort_flag))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d = tmem_base + a * bn;
                 for (int k = 0; k < k_stages; ++k) {
-                    if (!mbar_wait(full_bar(s), ph, kWaitNs, abort_flag) ||
-                        !mbar_wait(scale_bar(s), ph, kWaitNs, abort_flag)) {
+                    if (!__all_sync(0xffffffffu, wait_bar(full_bar(s), ph, abort_flag) &&
+                                                     wait_bar<true>(scale_bar(s), ph, abort_flag))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t ta = scale0 + s * cols_s, tb = ta + cols_a;
-                    const uint32_t sc = sS + s * kScaleStage;
-                    for (int g = 0; g < 2; ++g) {  // four blocks (128 values) each
-                        tc_copy_scales(ta + 4 * g, sc + 512 * g);
-                        for (int j = 0; j < atoms; ++j)
-                            tc_copy_scales(tb + 4 * (g * atoms + j), sc + 1024 + 512 * (g * atoms + j));
+                    const uint32_t ta = scale0 + s * cols_s, tb = ta + 8;
+                    const uint64_t ad = desc_a + (uint32_t)(s * a_stage >> 4), bd = desc_b + (uint32_t)(s * b_stage >> 4);
+                    const uint64_t sd = desc_s + (uint32_t)(s * scale_stage >> 4);
+                    const int left = K - k * kBK;  // values
+                    if (elect_one()) {
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {  // four blocks (128 values) each
+                            if (128 * g >= left) break;
+                            tc_copy_scales_pair(ta + 4 * g, sd + 32 * g);
+                            tc_copy_scales_pair(tb + 4 * g * atoms, sd + 64 + 32 * (g * atoms));
+                            if (atoms > 1) tc_copy_scales_pair(tb + 4 * (g * atoms + 1), sd + 64 + 32 * (g * atoms + 1));
+                        }
+#pragma unroll
+                        for (int i = 0; i < kBK / 64; ++i) {
+                            if (64 * i >= left) break;
+                            const uint32_t half = (uint32_t)(i & 1) * 2u;  // the step's two blocks within the word
+                            tc_mma_mxf4_pair(d, ad + 2 * i, bd + 2 * i, idesc | half << 29 | half << 4, ta + 4 * (i >> 1),
+                                             tb + 4 * atoms * (i >> 1), (k | i) != 0);
+                        }
+                        tc_commit_pair(empty_bar(s), 3);
+                        if (k + 1 == k_stages) tc_commit_pair(tfull_bar(a), 3);
                     }
-                    const uint64_t ad = smem_desc_k128(sA + s * a_stage), bd = smem_desc_k128(sB + s * b_stage);
-                    const int steps = (min(K - k * kBK, kBK) + 63) / 64;
-                    for (int i = 0; i < steps; ++i) {
-                        const uint32_t half = (uint32_t)(i & 1) * 2u;  // the step's two blocks within the word
-                        tc_mma_mxf4(d, ad + 2 * i, bd + 2 * i, idesc | half << 29 | half << 4, ta + 4 * (i >> 1),
-                                    tb + 4 * atoms * (i >> 1), (k | i) != 0);
-                    }
-                    tc_commit(empty_bar(s));
+                    __syncwarp();
                     issued = true;
-                    if (++s == p.stages) {
+                    if (k == 0 && tile + stride < total) next = decode<false>(tab, tile + stride);
+                    if (++s == stages) {
                         s = 0;
                         ph ^= 1u;
                     }
                 }
-                if (!ok) break;
-                tc_commit(tfull_bar(a));
                 ++n_acc;
             }
-            if (!ok) {
+            if (!ok && lane == 0) {
                 raise();
                 if (issued) {
-                    tc_commit(drain_bar);
-                    mbar_wait(drain_bar, 0, kDrainNs, nullptr);
+                    tc_commit_pair(drain_bar, 1);
+                    wait_bar(drain_bar, 0, nullptr);
                 }
             }
         }
     } else if (warp < 2 + kEpiWarps) {
         const int q = warp & 3;  // the TMEM lane quadrant this warp may read
-        const uint32_t sb = sE + (uint32_t)q * 4096u;
         uint32_t n_acc = 0;
-        for (int tile = blockIdx.x; tile < total; tile += stride, ++n_acc) {
-            const Tile t = decode<false>(p.o, tile, s_offs, s_tiles);
+        for (int tile = first; tile < total; tile += stride, ++n_acc) {
+            const Tile t = decode<false>(tab, tile);
             const uint32_t a = n_acc & 1u;
-            if (!__all_sync(0xffffffffu, mbar_wait(tfull_bar(a), (n_acc >> 1) & 1u, kWaitNs, abort_flag))) {
+            if (!__all_sync(0xffffffffu, wait_bar<true>(tfull_bar(a), (n_acc >> 1) & 1u, abort_flag))) {
                 if (lane == 0) raise();
                 break;
             }
             tc_fence_after();
-            store_tile<false>(p.o, t, tmem_base + a * bn, false, sb, q, lane);
+            if (32 * q < half_cols)
+                store_tile<false>(tab.o, t, tmem_base + ((uint32_t)(q * 32) << 16) + a * tab.o.tile_rows, false,
+                                  t.col0 + rank * half_cols + 32 * q + lane, lane);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(tempty_bar(a));
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(a), 0));
         }
-        if (lane == 0) bulk_wait_all();  // the stores are performed before the CTA ends
     } else {
         const int set = (warp - 2 - kEpiWarps) >> 2;
         const int i = (int)threadIdx.x - 64 - 32 * kEpiWarps - 128 * set;  // 0..127 within the set
-        const int quads = bn / 4;                                          // groups of four weight rows
-        const int bg = i / quads, bj = i % quads;                          // this thread's four blocks and four rows
+        const int wg = i >> 5, wq = i & 31;  // weights (i < 64): its four blocks, its four rows
         const int n_blocks = K / 32;
-        const size_t ws_e = (size_t)n_blocks * p.o.n_out;
+        const size_t ws_e = (size_t)n_blocks * tab.o.n_out;
         auto load = [&](const Tile &t, int k) {
             Scales v;
-            v.a[0] = v.a[1] = 0;
-            v.b[0] = v.b[1] = v.b[2] = v.b[3] = 0;
+            v.w[0] = v.w[1] = v.w[2] = v.w[3] = 0;
             const int b0 = k * kBlocks;
-            if (i < t.m_valid) {
-                const uint8_t *src = p.xs + (size_t)b0 * p.o.rows + t.row0 + i;
-#pragma unroll
-                for (int j = 0; j < kBlocks; ++j)
-                    if (b0 + j < n_blocks) v.a[j >> 2] |= (uint32_t)__ldg(src + (size_t)j * p.o.rows) << (8 * (j & 3));
-            }
-            const int n = t.col0 + 4 * bj;
-            if (bg < 2 && n < p.o.n_out) {  // n_out is a multiple of 8
-                const uint8_t *src = p.ws + t.e * ws_e + (size_t)(b0 + 4 * bg) * p.o.n_out + n;
+            const int n = t.col0 + rank * half_cols + 4 * wq;
+            if (wg < 2 && 4 * wq < half_cols && n < tab.o.n_out) {  // n_out is a multiple of 8
+                const uint8_t *src = p.ws + t.e * ws_e + (size_t)(b0 + 4 * wg) * tab.o.n_out + n;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (b0 + 4 * bg + j < n_blocks)
-                        v.b[j] = __ldg(reinterpret_cast<const uint32_t *>(src + (size_t)j * p.o.n_out));
+                    if (b0 + 4 * wg + j < n_blocks)
+                        v.w[j] = __ldg(reinterpret_cast<const uint32_t *>(src + (size_t)j * tab.o.n_out));
+            }
+#pragma unroll
+            for (int m = 0; m < kTokenTasks; ++m) {
+                const int task = i + 128 * m, g = task >= t.n ? 1 : 0, r = task - (g ? t.n : 0);
+                v.x[m] = 0;
+                if (r < t.rows) {
+                    const uint8_t *src = p.xs + (size_t)(b0 + 4 * g) * tab.o.rows + t.row0 + r;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (b0 + 4 * g + j < n_blocks) v.x[m] |= (uint32_t)__ldg(src + (size_t)j * tab.o.rows) << (8 * j);
+                }
             }
             return v;
         };
-        auto store = [&](const Scales &v, int s) {
-            const uint32_t sc = sS + s * kScaleStage;
-            const uint32_t at = sc + (uint32_t)(i & 31) * 16u + (uint32_t)(i >> 5) * 4u;
-            st_shared_u32(at, v.a[0]);
-            st_shared_u32(at + 512, v.a[1]);
-            if (bg < 2) {
-                const uint32_t p01 = __byte_perm(v.b[0], v.b[1], 0x5140), p23 = __byte_perm(v.b[2], v.b[3], 0x5140);
-                const uint32_t q01 = __byte_perm(v.b[0], v.b[1], 0x7362), q23 = __byte_perm(v.b[2], v.b[3], 0x7362);
+        auto store = [&](const Scales &v, int n, int s) {
+            const uint32_t sc = sS + s * scale_stage;
+            if (wg < 2) {  // row 4 wq + j of the word's four blocks: byte j of each loaded word
+                const uint32_t p01 = __byte_perm(v.w[0], v.w[1], 0x5140), p23 = __byte_perm(v.w[2], v.w[3], 0x5140);
+                const uint32_t q01 = __byte_perm(v.w[0], v.w[1], 0x7362), q23 = __byte_perm(v.w[2], v.w[3], 0x7362);
                 const uint32_t w[4] = {__byte_perm(p01, p23, 0x5410), __byte_perm(p01, p23, 0x7632),
                                        __byte_perm(q01, q23, 0x5410), __byte_perm(q01, q23, 0x7632)};
-                const int r0 = 4 * bj, rr = r0 & 127;
-                const uint32_t bt = sc + 1024u + 512u * (uint32_t)(bg * atoms + (r0 >> 7)) + (uint32_t)(rr >> 5) * 4u +
-                                    (uint32_t)(rr & 31) * 16u;
+                const int r0 = 4 * wq;
+                const uint32_t at = sc + 512u * wg + (uint32_t)(r0 >> 5) * 4u + (uint32_t)(r0 & 31) * 16u;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) st_shared_u32(bt + 16 * j, w[j]);
+                for (int j = 0; j < 4; ++j) st_shared_u32(at + 16 * j, w[j]);
+            }
+#pragma unroll
+            for (int m = 0; m < kTokenTasks; ++m) {
+                const int task = i + 128 * m, g = task >= n ? 1 : 0, r = task - (g ? n : 0);
+                if (r < n)
+                    st_shared_u32(sc + 1024u + 512u * (uint32_t)(g * atoms + (r >> 7)) + (uint32_t)(r & 31) * 16u +
+                                      (uint32_t)((r & 127) >> 5) * 4u,
+                                  v.x[m]);
             }
         };
         // this set's stages: number n = set, set + kScaleSets, .. of the CTA's sequence
-        int tile = blockIdx.x, k = set;
+        int tile = first, k = set;
         auto settle = [&]() {
             while (tile < total && k >= k_stages) {
                 k -= k_stages;
                 tile += stride;
             }
         };
-        settle();
         Scales next;
         Tile t;
         int t_of = -1;
         auto fetch = [&]() {
             if (tile >= total) return;
             if (t_of != tile) {
-                t = decode<false>(p.o, tile, s_offs, s_tiles);
+                t = decode<false>(tab, tile);
                 t_of = tile;
             }
             next = load(t, k);
         };
+        settle();
         fetch();
-        for (uint32_t n = set; tile < total; n += kScaleSets) {
+        int s = set % stages;
+        uint32_t ph = 1;
+        while (tile < total) {
             const Scales now = next;
+            const int n = t.n;
             k += kScaleSets;
             settle();
             fetch();
-            const int s = n % p.stages;
-            if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(s), ((n / p.stages) & 1u) ^ 1u, kWaitNs, abort_flag))) {
+            if (!__all_sync(0xffffffffu, wait_bar(empty_bar(s), ph, abort_flag))) {
                 if (lane == 0) raise();
                 break;
             }
-            store(now, s);
+            store(now, n, s);
             fence_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(scale_bar(s));
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(scale_bar(s), 0));
+            s += kScaleSets;
+            if (s >= stages) {
+                s -= stages;
+                ph ^= 1u;
+            }
         }
     }
 
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // no arrival or MMA of the pair outlives either CTA
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem_base, kTmemCols);
+        tmem_dealloc_pair(tmem_base, kTmemCols);
     }
 }
 
 unsigned long long g_attr;
 
-// Tile sizes.  Rows: 32-row boxes while the experts average at most 16 rows.  Columns: the
-// widest tile that still gives every SM one.
+// Tile sizes, as the bf16 products': rows up to 192, fewer where the experts average fewer;
+// 256 columns, or 128 where 256 would leave SMs without a tile.
 void choose_tiles(MxGroupedArgs &g, int sms) {
-    GroupedOut &a = g.o;
-    const long long active = std::min<long long>(a.E, a.rows);
-    a.bm = a.rows <= 16ll * a.E ? 32 : 128;
-    a.bn = kMaxBn;
-    while (a.bn > 64) {
-        const long long n = (a.n_out + a.bn - 1) / a.bn;
-        if (n * std::max<long long>(active, a.rows / a.bm) >= sms && a.bn - 64 < a.n_out) break;
-        a.bn -= 64;
-    }
-    a.n_tiles = (a.n_out + a.bn - 1) / a.bn;
-    const int atoms = (a.bn + 127) / 128;
-    g.stages = std::min({kMaxStages, kStageSpace / ((a.bm + a.bn) * 128 + kScaleStage),
-                         ((int)kTmemCols - 2 * a.bn) / (8 + 8 * atoms)});
+    GroupedOut &o = g.o;
+    const long long active = std::max<long long>(1, std::min(o.E, o.rows)), most = 2 * (o.rows / active) + 1;
+    o.tile_rows = most <= 32 ? 32 : most <= 64 ? 64 : most <= 128 ? 128 : kMaxRows;
+    const long long row_tiles = std::max<long long>(active, o.rows / o.tile_rows);
+    o.cols = (o.n_out + 255) / 256 * row_tiles >= sms / 2 && o.n_out > 128 ? 256 : 128;
+    o.col_tiles = (o.n_out + o.cols - 1) / o.cols;
+    g.a_stage = o.cols / 2 * kRow;
+    g.b_stage = o.tile_rows / 2 * kRow;
+    g.atoms = (o.tile_rows + 127) / 128;
+    g.stages = std::min({kMaxStages, kStageSpace / (g.a_stage + g.b_stage + 1024 + 1024 * g.atoms),
+                         ((int)kTmemCols - 2 * o.tile_rows) / (8 + 8 * g.atoms)});
 }
 
 }  // namespace
@@ -376,34 +425,32 @@ extern "C" moe_status moe_mx_grouped_forward(const void *Xc, const uint8_t *Xs, 
     if (rows == 0) return MOE_OK;
     const int sms = op_num_sms();
     int *err = op_error_word();
-    if (sms < 1 || err == nullptr) return op_fail(MOE_ERR_CUDA, "%s: no usable current device", op);
+    if (sms < 2 || err == nullptr) return op_fail(MOE_ERR_CUDA, "%s: no usable current device", op);
     MxGroupedArgs g = {};
-    g.o.offs = offs;
-    g.o.out = Y;
-    g.o.err = err;
-    g.o.E = E;
-    g.o.rows = rows;
-    g.o.n_out = N;
-    g.o.red = K;
-    g.o.f32 = out_dtype == MOE_DTYPE_F32;
+    GroupedOut &o = g.o;
+    o.offs = offs;
+    o.out = Y;
+    o.err = err;
+    o.E = E;
+    o.rows = rows;
+    o.n_out = N;
+    o.red = K;
+    o.f32 = out_dtype == MOE_DTYPE_F32;
     g.xs = Xs;
     g.ws = Ws;
     choose_tiles(g, sms);
-    const long long tiles = ((long long)rows / g.o.bm + std::min(E, rows)) * g.o.n_tiles;
+    const long long tiles = ((long long)rows / o.tile_rows + std::min(E, rows)) * o.col_tiles;
     if (tiles > (1ll << 30)) return op_fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^30 output tiles", op);
     const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
-    const uint64_t n = N, c = K / 2, r = rows, e = E, es = g.o.f32 ? 4 : 2;
-    const OpMap ma = {u8, 2, Xc, {c, r}, {c}, {128, (uint32_t)g.o.bm}, sw};
-    const OpMap mb = {u8, 3, Wc, {c, n, e}, {c, n * c}, {128, (uint32_t)g.o.bn, 1}, sw};
-    const OpMap mo = {g.o.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                      3, Y, {n, r, 1}, {n * es, n * es * r}, {(uint32_t)(128 / es), 32, 1}, sw};
-    if (op_encode(&g.map_a, ma) != CUDA_SUCCESS || op_encode(&g.map_b, mb) != CUDA_SUCCESS ||
-        op_encode(&g.o.map, mo) != CUDA_SUCCESS)
-        return op_fail(MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", op);
+    const uint64_t n = N, c = K / 2, r = rows, e = E;
+    CUresult cr = op_encode(&g.map_a, {u8, 3, Wc, {c, n, e}, {c, n * c}, {kRow, (uint32_t)o.cols / 2, 1}, sw});
+    for (int i = 0; i < o.tile_rows / 32 && cr == CUDA_SUCCESS; ++i)
+        cr = op_encode(&g.map_b[i], {u8, 2, Xc, {c, r}, {c}, {kRow, 16u * (i + 1)}, sw});
+    if (cr != CUDA_SUCCESS) return op_fail(MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", op, (int)cr);
     cudaError_t ce = op_allow_smem(reinterpret_cast<const void *>(mx_grouped_kernel), kSmemBytes, &g_attr);
     if (ce == cudaSuccess)
-        ce = launch_pdl(mx_grouped_kernel, dim3((unsigned)std::min<long long>(sms, tiles)), dim3(kThreads),
-                        (size_t)kSmemBytes, reinterpret_cast<cudaStream_t>(stream), g);
+        ce = launch_pdl_cluster(mx_grouped_kernel, dim3(2u * (unsigned)std::min<long long>(sms / 2, tiles)),
+                                dim3(kThreads), (size_t)kSmemBytes, reinterpret_cast<cudaStream_t>(stream), dim3(2, 1, 1), g);
     return op_cuda(ce, op);
 }
