@@ -15,21 +15,21 @@
 // Persistent kernel on CTA pairs (tcgen05 cta_group::2): a tile is up to 256 output columns
 // (M; 128 in each CTA) x up to 256 output rows (N; each CTA stages half of them), so a CTA
 // brings 32 KB per 64 reduction steps instead of the 48 KB of a 128 x 256 tile of its own,
-// and L2 keeps up with the tensor cores.  Six warps per CTA:
+// and L2 keeps up with the tensor cores.  Warps of a CTA:
 //   warp 0     TMA producer: per stage 64 reduction steps of this CTA's A (columns) and B
 //              (rows) operand, 128-byte swizzle; both CTAs' copies complete on the barrier
 //              of the even CTA
 //   warp 1     allocates tensor memory; in the even CTA issues tcgen05.mma (K 16) into one
 //              of two accumulators, so a tile's epilogue overlaps the next one's main loop
-//   warps 2-5  epilogue (grouped.cuh)
-//   warp 6     (wgrad) zeroes the rest of tails, see below
+//   warps 2-9  epilogue (grouped.cuh)
+//   warp 10    (wgrad) zeroes the rest of tails, see below
 // Every CTA reads the offsets, checks them and derives the tile list itself, so there is
 // no workspace, no launch before the product and no atomic; a tile's sum has a fixed order
 // and results are the same from call to call.
 //
 // The wgrad reduces over an expert's rows, whose number is arbitrary: the last stage also
 // brings rows of the next expert (or past the buffer).  Whole 16-row steps past the end are
-// not issued, and the rest of the last step is zeroed in both operand tiles by warp 6 of
+// not issued, and the rest of the last step is zeroed in both operand tiles by warp 10 of
 // each CTA (a zero in one would not do: the other may hold an infinity or a NaN).  Such a
 // stage's copies complete on a barrier of their own CTA, and the stage is handed to the MMA
 // when both CTAs have zeroed.
@@ -52,7 +52,12 @@ enum : int { kForward = 0, kDgrad = 1, kWgrad = 2 };
 
 constexpr int kBK = 64;                // reduction steps per stage: 128 bytes of bf16
 constexpr int kMaxStages = 12;
-constexpr int kThreads = 64 + 32 * kEpiWarps;  // the wgrad has one warp more
+// Epilogue warps per TMEM lane quadrant.  One against two: a small product 11.7 / 11.0 us, a
+// small bf16 weight gradient 26.6 / 24.6 us, prefill the same.
+constexpr int kParts = 2;
+constexpr int kEpiWarps = kQuads * kParts;
+template <int OP>
+constexpr int kThreads = 64 + 32 * kEpiWarps + (OP == kWgrad ? 32 : 0);  // the wgrad's last warp zeroes tails
 constexpr int kAccCols = 256;          // TMEM columns of one accumulator
 constexpr uint32_t kTmemCols = 2 * kAccCols;
 constexpr int kRow = kBK * 2;          // bytes of a K-major row, or of 64 columns in MN-major
@@ -93,8 +98,8 @@ __device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr) {
 __device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
 }
-template <int OP>
-__global__ void __launch_bounds__(kThreads + (OP == kWgrad ? 32 : 0), 1) grouped_kernel(const __grid_constant__ GroupedArgs p) {
+template <int OP, bool ADD>
+__global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_constant__ GroupedArgs p) {
     constexpr bool kDense = OP == kWgrad;
     extern __shared__ __align__(1024) uint8_t smem[];
     Header &h = *reinterpret_cast<Header *>(smem);
@@ -151,7 +156,6 @@ __global__ void __launch_bounds__(kThreads + (OP == kWgrad ? 32 : 0), 1) grouped
     pdl_wait();  // the offsets and operands of earlier kernels on the stream
     pdl_trigger();
     if (!load_table<kDense>(p.o, h.table) && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.o.err, ERR_BOUNDS);
-    const int total = tab.total;
     const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
     const int half_cols = tab.o.cols / 2;
     // wgrad: the stage at reduction row r ends inside a 16-row step
@@ -161,8 +165,8 @@ __global__ void __launch_bounds__(kThreads + (OP == kWgrad ? 32 : 0), 1) grouped
         uint32_t ph = 1;
         int s = 0;
         bool ok = true;
-        for (int tile = first; ok && tile < total; tile += stride) {
-            const Tile t = decode<kDense>(tab, tile);
+        for (TileWalk<kDense> walk(tab, first, stride); ok && walk.more(); walk.next()) {
+            const Tile t = walk.get();
             const int col = t.col0 + rank * half_cols, row = t.row0 + rank * (t.n / 2);
             const bool two_b = t.n / 2 > 64;  // MN-major B: two chunks of 64 columns
             const CUtensorMap *map_b = kDense ? &p.map_b[0] : &p.map_b[t.n / 32 - 1];  // K-major B: n / 2 rows
@@ -174,7 +178,7 @@ __global__ void __launch_bounds__(kThreads + (OP == kWgrad ? 32 : 0), 1) grouped
                 }
                 const uint32_t da = sA + s * a_stage, db = sB + s * b_stage;
                 const uint32_t bar = mapa_shared(full_bar(s), 0);
-                if (is_tail(t, r)) {  // complete on this CTA's own barrier, for warp 6 to zero the rest
+                if (is_tail(t, r)) {  // complete on this CTA's own barrier, for warp 10 to zero the rest
                     if (elect_one()) {
                         if (leader) mbar_arrive(full_bar(s));
                         mbar_arrive_expect_tx(tail_bar(s), bytes);
@@ -224,12 +228,17 @@ __global__ void __launch_bounds__(kThreads + (OP == kWgrad ? 32 : 0), 1) grouped
             uint32_t n_acc = 0, ph = 0, zeroed_ph = 0;
             int s = 0;
             bool ok = true, issued = false;
+            TileWalk<kDense> walk(tab, first, stride);
             Tile next;
-            if (first < total) next = decode<kDense>(tab, first);
-            for (int tile = first; ok && tile < total; tile += stride) {
+            auto advance = [&]() {
+                walk.next();
+                if (walk.more()) next = walk.get();
+            };
+            if (walk.more()) next = walk.get();
+            while (ok && walk.more()) {
                 const Tile t = next;
                 if (t.r0 >= t.r1) {  // an expert without rows: the epilogue writes its zeros
-                    if (tile + stride < total) next = decode<kDense>(tab, tile + stride);
+                    advance();
                     continue;
                 }
                 const uint32_t idesc = idesc_bf16_f32(256, t.n) | (OP != kForward ? 1u << 15 : 0u) | (kDense ? 1u << 16 : 0u);
@@ -263,7 +272,7 @@ __global__ void __launch_bounds__(kThreads + (OP == kWgrad ? 32 : 0), 1) grouped
                     __syncwarp();
                     issued = true;
                     // the next tile's place, while this one's products run
-                    if (r == t.r0 && tile + stride < total) next = decode<kDense>(tab, tile + stride);
+                    if (r == t.r0) advance();
                     if (++s == stages) {
                         s = 0;
                         ph ^= 1u;
@@ -279,13 +288,13 @@ __global__ void __launch_bounds__(kThreads + (OP == kWgrad ? 32 : 0), 1) grouped
                 }
             }
         }
-    } else if (warp == 2 + kEpiWarps) {
+    } else if (kDense && warp == 2 + kEpiWarps) {
         // wgrad: zero the rows past each tail's end, then hand the stage to the MMA
         uint32_t tail_ph = 0;
         int s = 0;
         const int chunks_a = half_cols / 64;
-        for (int tile = first; tile < total; tile += stride) {
-            const Tile t = decode<kDense>(tab, tile);
+        for (TileWalk<kDense> walk(tab, first, stride); walk.more(); walk.next()) {
+            const Tile t = walk.get();
             const int k_blocks = (t.r1 - t.r0 + kBK - 1) / kBK;
             const int last = t.r0 + (k_blocks - 1) * kBK;
             if (k_blocks > 0 && is_tail(t, last)) {
@@ -312,8 +321,8 @@ __global__ void __launch_bounds__(kThreads + (OP == kWgrad ? 32 : 0), 1) grouped
         const int q = warp & 3;  // the TMEM lane quadrant this warp may read
         const int in_half = 32 * q + lane;  // column within this CTA's half
         uint32_t n_acc = 0;
-        for (int tile = first; tile < total; tile += stride) {
-            const Tile t = decode<kDense>(tab, tile);
+        for (TileWalk<kDense> walk(tab, first, stride); walk.more(); walk.next()) {
+            const Tile t = walk.get();
             const bool empty = t.r0 >= t.r1;
             const uint32_t a = n_acc & 1u;
             if (!empty) {
@@ -324,12 +333,12 @@ __global__ void __launch_bounds__(kThreads + (OP == kWgrad ? 32 : 0), 1) grouped
                 tc_fence_after();
             }
             if (32 * q < half_cols)
-                store_tile<kDense>(tab.o, t, tmem_base + ((uint32_t)(q * 32) << 16) + a * kAccCols, empty,
-                                   t.col0 + rank * half_cols + in_half, lane);
+                store_tile<kDense, ADD, kParts>(tab.o, t, tmem_base + ((uint32_t)(q * 32) << 16) + a * kAccCols, empty,
+                                   t.col0 + rank * half_cols + in_half, (warp - 2) >> 2, lane);
             if (!empty) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(a), 0));
+                if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(a), 0));
                 ++n_acc;
             }
         }
@@ -345,7 +354,7 @@ __global__ void __launch_bounds__(kThreads + (OP == kWgrad ? 32 : 0), 1) grouped
     }
 }
 
-unsigned long long g_attr[3];
+unsigned long long g_attr[4];
 
 // Tile sizes.  Rows: up to 256, fewer where the experts average fewer.  Columns: 256, or 128
 // (64 per CTA) where 256 would leave SMs without a tile.
@@ -398,7 +407,6 @@ moe_status launch(const char *name, int op, const void *x, const void *w, const 
     o.m_dense = N;
     o.red = op == kForward ? K : N;
     o.f32 = dtype == MOE_DTYPE_F32;
-    o.accumulate = accumulate;
     choose_tiles(g, op, sms);
     const long long tiles = op == kWgrad ? (long long)E * o.row_tiles * o.col_tiles
                                          : ((long long)rows / o.tile_rows + std::min(E, rows)) * o.col_tiles;
@@ -421,16 +429,18 @@ moe_status launch(const char *name, int op, const void *x, const void *w, const 
     if (cr != CUDA_SUCCESS) return op_fail(MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", name, (int)cr);
     const dim3 grid(2u * (unsigned)std::min<long long>(sms / 2, tiles));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    auto go = [&](auto kernel) -> cudaError_t {
-        const cudaError_t ce = op_allow_smem(reinterpret_cast<const void *>(kernel), kSmemBytes, &g_attr[op]);
+    auto go = [&](auto kernel, int threads, int which) -> cudaError_t {
+        const cudaError_t ce = op_allow_smem(reinterpret_cast<const void *>(kernel), kSmemBytes, &g_attr[which]);
         return ce != cudaSuccess
                    ? ce
-                   : launch_pdl_cluster(kernel, grid, dim3(kThreads + (op == kWgrad ? 32 : 0)), (size_t)kSmemBytes, s,
+                   : launch_pdl_cluster(kernel, grid, dim3((unsigned)threads), (size_t)kSmemBytes, s,
                                         dim3(2, 1, 1), g);
     };
-    return op_cuda(op == kForward ? go(grouped_kernel<kForward>)
-                                  : op == kDgrad ? go(grouped_kernel<kDgrad>) : go(grouped_kernel<kWgrad>),
-                   name);
+    const cudaError_t ce = op == kForward ? go(grouped_kernel<kForward, false>, kThreads<kForward>, 0)
+                           : op == kDgrad ? go(grouped_kernel<kDgrad, false>, kThreads<kDgrad>, 1)
+                           : accumulate   ? go(grouped_kernel<kWgrad, true>, kThreads<kWgrad>, 2)
+                                          : go(grouped_kernel<kWgrad, false>, kThreads<kWgrad>, 3);
+    return op_cuda(ce, name);
 }
 
 }  // namespace

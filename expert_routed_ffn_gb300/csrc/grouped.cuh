@@ -17,7 +17,7 @@
 namespace moe {
 
 constexpr int kMaxExperts = 256;
-constexpr int kEpiWarps = 4;          // epilogue warps, one per TMEM lane quadrant
+constexpr int kQuads = 4;              // TMEM lane quadrants, of 32 lanes
 constexpr long long kWaitCycles = 4000000000ll;         // bound of every wait (about 2 s)
 constexpr unsigned long long kPairDrainNs = 1000000ull; // grace for the copies in flight after an abort
 
@@ -37,7 +37,6 @@ struct GroupedOut {
     int col_tiles;   // tiles along the output columns
     int row_tiles;   // dense: tiles along m_dense
     int f32;         // output type: fp32, else bf16
-    int accumulate;  // dense: add to the output
 };
 
 struct Tile {
@@ -70,6 +69,14 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     }
 }
 
+// Arrive on a barrier of either CTA (address from mapa_shared) without waiting for this
+// thread's stores: for handing back an accumulator, whose reads tcgen05.wait::ld has completed.
+// The releasing form waits until the tile's output stores have been performed (measured: about
+// 2000 cycles per tile in which the next products wait).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // One lane of a converged warp.  The roles that issue copies and MMAs run their loops on the
 // whole warp and only the instructions themselves on one lane: the addresses and descriptors
 // stay warp-uniform, which is what those instructions take (with the loop itself on one lane,
@@ -90,6 +97,7 @@ struct TileTable {
     int offs[kMaxExperts + 1];         // first row of each expert
     int tiles[kMaxExperts];            // row-grouped: its first row tile; INT_MAX behind the last
     uint16_t share[kMaxExperts];       // row-grouped: rows of its tiles but the last, a multiple of 32
+    int row_tiles;                     // row-grouped: of all experts
     int total;                         // tiles, 0 where the offsets decrease or leave [0, rows]
 };
 
@@ -128,60 +136,103 @@ __device__ __forceinline__ bool load_table(const GroupedOut &p, TileTable &tab) 
             tab.tiles[e] = e < E ? run : 0x7fffffff;
             run += cnt[j];
         }
+        if (lane == 31) tab.row_tiles = run;
         if (lane == 31) tab.total = !ok ? 0 : DENSE ? E * p.row_tiles * p.col_tiles : run * p.col_tiles;
     }
     __syncthreads();
     return ok;
 }
 
-// Tile number -> tile, by a converged warp.  Inside an expert the row tiles of one column tile
-// are adjacent, so that concurrent CTAs share its weights in L2; its rows are dealt evenly to
-// its row tiles, in multiples of 32 (no tile is left empty: with `parts` tiles of at most T
-// rows either parts <= T / 32, and rounding shares up takes fewer than `parts` * 32 of the more
-// than T * (parts - 1) rows, or the shares are T).
+// Walks a CTA pair's tiles first, first + stride, .. (a converged warp).  Inside an expert the
+// row tiles of one column tile are adjacent, so that concurrent CTAs share its weights in L2;
+// its rows are dealt evenly to its row tiles, in multiples of 32 (no tile is left empty: with
+// `parts` tiles of at most T rows either parts <= T / 32, and rounding shares up takes fewer
+// than `parts` * 32 of the more than T * (parts - 1) rows, or the shares are T).
 template <bool DENSE>
-__device__ __forceinline__ Tile decode(const TileTable &tab, int tile) {
-    const GroupedOut &p = tab.o;
-    Tile t;
-    if (DENSE) {
-        const int parts = p.row_tiles, strip = tile / parts;  // (expert, column tile)
-        t.e = strip / p.col_tiles;
-        t.col0 = (strip - t.e * p.col_tiles) * p.cols;
-        t.row0 = (tile - strip * parts) * p.tile_rows;
-        t.rows = min(p.tile_rows, p.m_dense - t.row0);
-        t.r0 = tab.offs[t.e];
-        t.r1 = tab.offs[t.e + 1];
-    } else {
-        // the last expert whose first tile is <= tile (one with rows: the next ones start later)
-        const int lane = threadIdx.x & 31;
-        const int row_tile = tile / p.col_tiles;  // experts are whole multiples of col_tiles
-        const int group = __popc(__ballot_sync(0xffffffffu, tab.tiles[lane * (kMaxExperts / 32)] <= row_tile)) - 1;
-        const int in = __popc(__ballot_sync(0xffffffffu, lane < kMaxExperts / 32 &&
-                                                              tab.tiles[group * (kMaxExperts / 32) + lane] <= row_tile));
-        t.e = group * (kMaxExperts / 32) + in - 1;
-        const int first = tab.offs[t.e], end = tab.offs[t.e + 1];
-        const int share = tab.share[t.e], parts = (end - first + p.tile_rows - 1) / p.tile_rows;
-        const int local = tile - tab.tiles[t.e] * p.col_tiles, strip = local / parts;
-        t.col0 = strip * p.cols;
-        t.row0 = first + (local - strip * parts) * share;
-        t.rows = min(share, end - t.row0);
-        t.r0 = 0;
-        t.r1 = p.red;
-    }
-    t.n = (t.rows + 31) & ~31;
-    return t;
-}
+struct TileWalk {
+    const TileTable &tab;
+    int tile, stride;
+    // dense: the tile as (expert, column tile, row tile), and the stride in the same digits
+    int e = 0, c = 0, r = 0, de = 0, dc = 0, dr = 0;
 
-// A tile's epilogue by one warp: TMEM lane = output column `col` (its own lane's; `col_ok`:
-// inside the output), column = row.  `tcol`: the accumulator, at the warp's lane quadrant;
-// `empty`: there is no sum, zeros are stored.  ADD: to what the output holds, in fp32.
-template <bool DENSE, bool ADD>
-__device__ __forceinline__ void store_rows(const GroupedOut &p, const Tile &t, uint32_t tcol, bool empty, int col,
-                                           int lane) {
+    __device__ __forceinline__ TileWalk(const TileTable &table, int first, int step)
+        : tab(table), tile(first), stride(step) {
+        if (DENSE) {
+            split(first, e, c, r);
+            split(step, de, dc, dr);
+        }
+    }
+    __device__ __forceinline__ void split(int n, int &x, int &y, int &z) const {
+        const int strip = n / tab.o.row_tiles;
+        z = n - strip * tab.o.row_tiles;
+        x = strip / tab.o.col_tiles;
+        y = strip - x * tab.o.col_tiles;
+    }
+    __device__ __forceinline__ bool more() const { return tile < tab.total; }
+    __device__ __forceinline__ void next() {
+        tile += stride;
+        if (DENSE) {
+            r += dr;
+            c += dc;
+            e += de;
+            if (r >= tab.o.row_tiles) {
+                r -= tab.o.row_tiles;
+                ++c;
+            }
+            if (c >= tab.o.col_tiles) {
+                c -= tab.o.col_tiles;
+                ++e;
+            }
+        }
+    }
+    // the current tile (more() holds)
+    __device__ __forceinline__ Tile get() const {
+        const GroupedOut &p = tab.o;
+        Tile t;
+        if (DENSE) {
+            t.e = e;
+            t.col0 = c * p.cols;
+            t.row0 = r * p.tile_rows;
+            t.rows = min(p.tile_rows, p.m_dense - t.row0);
+            t.r0 = tab.offs[e];
+            t.r1 = tab.offs[e + 1];
+        } else {
+            // the last expert whose first tile is <= tile (one with rows: the next ones start later)
+            constexpr int kPer = kMaxExperts / 32;
+            const int lane = threadIdx.x & 31;
+            const int row_tile = tile / p.col_tiles;  // an expert's tiles: a multiple of col_tiles
+            const int group = __popc(__ballot_sync(0xffffffffu, tab.tiles[lane * kPer] <= row_tile)) - 1;
+            const int in = __popc(__ballot_sync(0xffffffffu, lane < kPer && tab.tiles[group * kPer + lane] <= row_tile));
+            t.e = group * kPer + in - 1;
+            const int first = tab.offs[t.e], end = tab.offs[t.e + 1], share = tab.share[t.e];
+            const int parts = (t.e + 1 < p.E ? tab.tiles[t.e + 1] : tab.row_tiles) - tab.tiles[t.e];
+            const int local = tile - tab.tiles[t.e] * p.col_tiles, strip = local / parts;
+            t.col0 = strip * p.cols;
+            t.row0 = first + (local - strip * parts) * share;
+            t.rows = min(share, end - t.row0);
+            t.r0 = 0;
+            t.r1 = p.red;
+        }
+        t.n = (t.rows + 31) & ~31;
+        return t;
+    }
+};
+
+// A tile's epilogue by one warp: TMEM lane = output column `col` (its own lane's), column = row.
+// `tcol`: the accumulator, at the warp's lane quadrant; `empty`: there is no sum, zeros are
+// stored; PARTS warps share a quadrant, this one takes the 32-row chunks `part`, part + PARTS, ..
+// ADD: to what the output holds, in fp32.
+template <bool DENSE, bool ADD, int PARTS>
+__device__ __forceinline__ void store_tile(const GroupedOut &p, const Tile &t, uint32_t tcol, bool empty, int col,
+                                           int part, int lane) {
+    // fp32 weight gradients are bound by their own stores: with both warps storing, their bursts
+    // delay the operand loads (160 against 166 us; bf16 ones 26.6 against 24.6 us the other way)
+    const int parts = DENSE && p.f32 ? 1 : PARTS;
+    if ((ADD && empty) || part >= parts) return;
     const bool ok = col < p.n_out;
     const size_t row0 = (DENSE ? (size_t)t.e * p.m_dense : 0) + t.row0;
     const size_t ld = p.n_out;
-    for (int c = 0; c < t.rows; c += 32) {
+    for (int c = 32 * part; c < t.rows; c += 32 * parts) {
         uint32_t v[32];
         if (DENSE && empty) {
 #pragma unroll
@@ -189,16 +240,23 @@ __device__ __forceinline__ void store_rows(const GroupedOut &p, const Tile &t, u
         } else {
             tmem_ld32(tcol + c, v);
             tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));  // not read before the wait
         }
         const int rows = ok ? min(32, t.rows - c) : 0;
         if (p.f32) {
             float *o = static_cast<float *>(p.out) + (row0 + c) * ld + col;
             if (ADD) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (j < rows) v[j] = __float_as_uint(__uint_as_float(v[j]) + o[j * ld]);
-            }
-            if (rows == 32) {
+                for (int g = 0; g < 32; g += 8) {  // eight loads in flight
+                    float old[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) old[j] = g + j < rows ? o[(g + j) * ld] : 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (g + j < rows) o[(g + j) * ld] = old[j] + __uint_as_float(v[g + j]);
+                }
+            } else if (rows == 32) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) o[j * ld] = __uint_as_float(v[j]);
             } else {
@@ -219,14 +277,16 @@ __device__ __forceinline__ void store_rows(const GroupedOut &p, const Tile &t, u
             }
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                const uint32_t mine = odd ? v[2 * j + 1] : v[2 * j], give = odd ? v[2 * j] : v[2 * j + 1];
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
-                float lo = __uint_as_float(odd ? got : mine), hi = __uint_as_float(odd ? mine : got);
                 if (ADD) {
-                    lo += bf16_lo(old[j]);
-                    hi += bf16_hi(old[j]);
+                    const uint32_t mine = odd ? v[2 * j + 1] : v[2 * j], give = odd ? v[2 * j] : v[2 * j + 1];
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
+                    w[j] = pack_bf16x2(__uint_as_float(odd ? got : mine) + bf16_lo(old[j]),
+                                       __uint_as_float(odd ? mine : got) + bf16_hi(old[j]));
+                } else {
+                    const uint32_t mine = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, mine, 1);
+                    w[j] = __byte_perm(mine, got, odd ? 0x3276 : 0x5410);
                 }
-                w[j] = pack_bf16x2(lo, hi);
             }
             if (rows == 32) {
 #pragma unroll
@@ -237,15 +297,6 @@ __device__ __forceinline__ void store_rows(const GroupedOut &p, const Tile &t, u
                     if (2 * j < left) o[j * ld] = w[j];
             }
         }
-    }
-}
-template <bool DENSE>
-__device__ __forceinline__ void store_tile(const GroupedOut &p, const Tile &t, uint32_t tcol, bool empty, int col,
-                                           int lane) {
-    if (DENSE && p.accumulate) {
-        if (!empty) store_rows<DENSE, true>(p, t, tcol, false, col, lane);
-    } else {
-        store_rows<DENSE, false>(p, t, tcol, empty, col, lane);
     }
 }
 

@@ -6,19 +6,21 @@
 // bytes of codes per row, a quarter of bf16's.
 //
 // Persistent kernel on CTA pairs with the tiles of the bf16 products (grouped.cu): 256
-// weight rows as the MMA's M, up to 192 token rows as its N.  14 warps per CTA:
-//   warp 0      TMA producer: codes of this CTA's weight rows and half of the token rows,
-//               256 values (128 bytes, 128-byte swizzle) per stage
-//   warp 1      allocates tensor memory; in the even CTA copies a stage's scales from shared
-//               to tensor memory of both CTAs (tcgen05.cp, in order with the MMAs that
-//               follow) and issues the MMAs
-//   warps 2-5   epilogue (grouped.cuh), overlapping the next tile's main loop
-//   warps 6-13  scales, two sets of four warps taking alternate stages.  The tensor core
-//               wants four consecutive blocks' scales of a row in one word, the tensors hold a
-//               block's scales for consecutive rows: the warps read runs along the rows,
-//               transpose in registers and write the words where tcgen05.cp reads them; each
-//               CTA those of its own weight rows and of all the tile's tokens.  A set's loads
-//               for its next stage are in flight while it waits to store this one.
+// weight rows as the MMA's M, up to 192 token rows as its N.  18 warps per CTA:
+//   warp 0       TMA producer: codes of this CTA's weight rows and half of the token rows,
+//                256 values (128 bytes, 128-byte swizzle) per stage
+//   warp 1       allocates tensor memory; in the even CTA copies a stage's scales from shared
+//                to tensor memory of both CTAs (tcgen05.cp, in order with the MMAs that
+//                follow) and issues the MMAs
+//   warps 2-5    epilogue (grouped.cuh), overlapping the next tile's main loop
+//   warps 6-9    fetch scales, up to kRaw stages ahead: those of this CTA's weight rows and of
+//                all the tile's tokens, as they lie (a block's scales for consecutive rows),
+//                with 4-byte asynchronous copies: an expert's first row has any alignment
+//   warps 10-17  two sets of four, on alternate stages: the tensor core wants four consecutive
+//                blocks' scales of a row in one word, so they transpose from the fetched runs
+//                into the words that tcgen05.cp reads.  They are warps of their own because
+//                handing a stage to the other CTA waits for the warp's outstanding loads
+//                (fetching in the same warps: 146 us against the figure below at prefill).
 // Tensor memory (512 columns): two accumulators of up to 192 columns, then per stage the
 // scales of the weights (8 columns) and of the tokens (8 per 128 of them).
 #include <algorithm>
@@ -36,21 +38,28 @@ constexpr int kBK = 256;           // values per stage
 constexpr int kRow = kBK / 2;      // their bytes: one row of codes
 constexpr int kBlocks = kBK / 32;  // scale blocks per stage
 constexpr int kMaxStages = 16;
-constexpr int kScaleSets = 2;
-constexpr int kThreads = 64 + 32 * kEpiWarps + 128 * kScaleSets;
+constexpr int kEpiWarps = kQuads;
+constexpr int kSets = 2;           // sets of transposing warps
+constexpr int kFetch = 2 + kEpiWarps, kTranspose = kFetch + 4;  // first warp of the role
+constexpr int kThreads = 32 * (kTranspose + 4 * kSets);
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxRows = 192;      // token rows of a tile
 constexpr int kBoxes = kMaxRows / 32;
-constexpr int kStageSpace = 225280;
+// fetched scales of a stage: 8 blocks of tokens (192 and an alignment of up to 3) and of weights
+constexpr int kRaw = 8;
+constexpr int kRawToken = 208, kRawWeight = 128;
+constexpr int kRawStage = kBlocks * (kRawToken + kRawWeight);
+constexpr int kTokenWords = (kMaxRows + 3) / 4 + 1;
+constexpr int kStageSpace = 203776;
 
 struct Header {
-    uint64_t bars[3 * kMaxStages + 5];
+    uint64_t bars[3 * kMaxStages + 2 * kRaw + 5];
     TileTable table;
     uint32_t tmem;
     volatile int abort;
 };
 constexpr int kHeaderBytes = 4096;
-constexpr int kSmemBytes = kHeaderBytes + kStageSpace;
+constexpr int kSmemBytes = kHeaderBytes + kStageSpace + kRaw * kRawStage;
 static_assert(sizeof(Header) <= kHeaderBytes && kSmemBytes <= 232448, "shared memory of one CTA");
 
 struct MxGroupedArgs {
@@ -90,13 +99,24 @@ __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-constexpr int kTokenTasks = kMaxRows * 2 / 128;  // (row, four blocks) pairs per scale thread
-
-// One scale thread's share of a stage, between its loads and its stores.
-struct Scales {
-    uint32_t w[4];            // four weight rows' bytes of four blocks
-    uint32_t x[kTokenTasks];  // token rows' words
-};
+// 4 bytes to shared memory; only `bytes` of them are read, the rest is zero
+__device__ __forceinline__ void copy_word(uint32_t dst, const uint8_t *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// arrive on `bar` when this thread's copies so far have landed
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
 
 __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_constant__ MxGroupedArgs p) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -107,7 +127,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
     const int scale_stage = 1024 + 1024 * p.atoms;
     // A first: the MMA reads 128 rows of A where the box brought 64; the rest is whatever
     // follows, and its results are not stored
-    const uint32_t sA = base, sB = sA + (uint32_t)(p.stages * p.a_stage), sS = sB + (uint32_t)(p.stages * p.b_stage);
+    const uint32_t sA = base, sB = sA + (uint32_t)(stages * a_stage), sS = sB + (uint32_t)(stages * b_stage);
+    const uint32_t sR = base + kStageSpace;  // the fetched scales
     const uint32_t bar0 = smem_u32(h.bars);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto scale_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
@@ -115,6 +136,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
     auto tfull_bar = [&](uint32_t a) { return bar0 + 8u * (3 * kMaxStages + a); };
     auto tempty_bar = [&](uint32_t a) { return bar0 + 8u * (3 * kMaxStages + 2 + a); };
     const uint32_t drain_bar = bar0 + 8u * (3 * kMaxStages + 4);
+    auto raw_full_bar = [&](int i) { return bar0 + 8u * (3 * kMaxStages + 5 + i); };
+    auto raw_empty_bar = [&](int i) { return bar0 + 8u * (3 * kMaxStages + 5 + kRaw + i); };
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank();
     const bool leader = rank == 0;
@@ -135,6 +158,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
             mbar_init(tfull_bar(a), 1);
             mbar_init(tempty_bar(a), 2 * kEpiWarps);
         }
+        for (int i = 0; i < kRaw; ++i) {
+            mbar_init(raw_full_bar(i), 128);
+            mbar_init(raw_empty_bar(i), 4);
+        }
         mbar_init(drain_bar, 1);
         fence_mbar_init();
         h.abort = 0;
@@ -153,7 +180,6 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
     pdl_wait();
     pdl_trigger();
     if (!load_table<false>(p.o, h.table) && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.o.err, ERR_BOUNDS);
-    const int total = tab.total;
     const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
     const int half_cols = tab.o.cols / 2, atoms = p.atoms;
     const int K = tab.o.red, k_stages = (K + kBK - 1) / kBK;
@@ -162,8 +188,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
         uint32_t ph = 1;
         int s = 0;
         bool ok = true;
-        for (int tile = first; ok && tile < total; tile += stride) {
-            const Tile t = decode<false>(tab, tile);
+        for (TileWalk<false> walk(tab, first, stride); ok && walk.more(); walk.next()) {
+            const Tile t = walk.get();
             const int col = t.col0 + rank * half_cols, row = t.row0 + rank * (t.n / 2);
             const CUtensorMap *map_b = &p.map_b[t.n / 32 - 1];
             const uint32_t bytes = a_stage + (t.n / 2) * kRow;
@@ -201,9 +227,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
             uint32_t n_acc = 0, ph = 0;
             int s = 0;
             bool ok = true, issued = false;
+            TileWalk<false> walk(tab, first, stride);
             Tile next;
-            if (first < total) next = decode<false>(tab, first);
-            for (int tile = first; ok && tile < total; tile += stride) {
+            if (walk.more()) next = walk.get();
+            while (ok && walk.more()) {
                 const Tile t = next;
                 const uint32_t idesc = idesc_mxf4(256, t.n);
                 const uint32_t a = n_acc & 1u, d = tmem_base + a * acc_cols;
@@ -243,7 +270,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
                     }
                     __syncwarp();
                     issued = true;
-                    if (k == 0 && tile + stride < total) next = decode<false>(tab, tile + stride);
+                    if (k == 0) {  // the next tile's place, while this one's products run
+                        walk.next();
+                        if (walk.more()) next = walk.get();
+                    }
                     if (++s == stages) {
                         s = 0;
                         ph ^= 1u;
@@ -262,8 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
     } else if (warp < 2 + kEpiWarps) {
         const int q = warp & 3;  // the TMEM lane quadrant this warp may read
         uint32_t n_acc = 0;
-        for (int tile = first; tile < total; tile += stride, ++n_acc) {
-            const Tile t = decode<false>(tab, tile);
+        for (TileWalk<false> walk(tab, first, stride); walk.more(); walk.next(), ++n_acc) {
+            const Tile t = walk.get();
             const uint32_t a = n_acc & 1u;
             if (!__all_sync(0xffffffffu, wait_bar<true>(tfull_bar(a), (n_acc >> 1) & 1u, abort_flag))) {
                 if (lane == 0) raise();
@@ -271,107 +301,131 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
             }
             tc_fence_after();
             if (32 * q < half_cols)
-                store_tile<false>(tab.o, t, tmem_base + ((uint32_t)(q * 32) << 16) + a * tab.o.tile_rows, false,
-                                  t.col0 + rank * half_cols + 32 * q + lane, lane);
+                store_tile<false, false, 1>(tab.o, t, tmem_base + ((uint32_t)(q * 32) << 16) + a * tab.o.tile_rows, false,
+                                  t.col0 + rank * half_cols + 32 * q + lane, 0, lane);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(a), 0));
+            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(a), 0));
         }
-    } else {
-        const int set = (warp - 2 - kEpiWarps) >> 2;
-        const int i = (int)threadIdx.x - 64 - 32 * kEpiWarps - 128 * set;  // 0..127 within the set
-        const int wg = i >> 5, wq = i & 31;  // weights (i < 64): its four blocks, its four rows
-        const int n_blocks = K / 32;
-        const size_t ws_e = (size_t)n_blocks * tab.o.n_out;
-        auto load = [&](const Tile &t, int k) {
-            Scales v;
-            v.w[0] = v.w[1] = v.w[2] = v.w[3] = 0;
-            const int b0 = k * kBlocks;
-            const int n = t.col0 + rank * half_cols + 4 * wq;
-            if (wg < 2 && 4 * wq < half_cols && n < tab.o.n_out) {  // n_out is a multiple of 8
-                const uint8_t *src = p.ws + t.e * ws_e + (size_t)(b0 + 4 * wg) * tab.o.n_out + n;
+    } else if (warp < kTranspose) {
+        const int i = (int)threadIdx.x - 32 * kFetch;
+        const int n_blocks = K / 32, rows = tab.o.rows, n_out = tab.o.n_out;
+        const uint8_t *const xs = p.xs, *const xs_end = xs + (size_t)n_blocks * rows;
+        int raw = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        for (TileWalk<false> walk(tab, first, stride); ok && walk.more(); walk.next()) {
+            const Tile t = walk.get();
+            const int col = t.col0 + rank * half_cols;
+            const uint8_t *const ws = p.ws + (size_t)t.e * n_blocks * n_out;
+            for (int b0 = 0; b0 < n_blocks; b0 += kBlocks) {
+                if (!__all_sync(0xffffffffu, wait_bar(raw_empty_bar(raw), ph, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t rt = sR + raw * kRawStage, rw = rt + kBlocks * kRawToken;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (b0 + 4 * wg + j < n_blocks)
-                        v.w[j] = __ldg(reinterpret_cast<const uint32_t *>(src + (size_t)j * tab.o.n_out));
-            }
-#pragma unroll
-            for (int m = 0; m < kTokenTasks; ++m) {
-                const int task = i + 128 * m, g = task >= t.n ? 1 : 0, r = task - (g ? t.n : 0);
-                v.x[m] = 0;
-                if (r < t.rows) {
-                    const uint8_t *src = p.xs + (size_t)(b0 + 4 * g) * tab.o.rows + t.row0 + r;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (b0 + 4 * g + j < n_blocks) v.x[m] |= (uint32_t)__ldg(src + (size_t)j * tab.o.rows) << (8 * j);
+                for (int id = i; id < kBlocks * 32; id += 128) {
+                    const int b = id >> 5, w = 4 * (id & 31);
+                    // n_out is a multiple of 8: a word is inside or outside
+                    const bool in = b0 + b < n_blocks && w < half_cols && col + w < n_out;
+                    copy_word(rw + b * kRawWeight + w, in ? ws + (size_t)(b0 + b) * n_out + col + w : ws, in ? 4 : 0);
+                }
+                for (int id = i; id < kBlocks * kTokenWords; id += 128) {
+                    const int b = id / kTokenWords, w = id - b * kTokenWords;
+                    const uint8_t *src = xs;
+                    int bytes = 0;
+                    if (b0 + b < n_blocks) {
+                        const size_t at = (size_t)(b0 + b) * rows + t.row0;
+                        src = xs + (at & ~(size_t)3) + 4 * w;
+                        if (src < xs + at + t.rows) bytes = (int)min((ptrdiff_t)4, xs_end - src);
+                    }
+                    copy_word(rt + b * kRawToken + 4 * w, bytes ? src : xs, bytes);
+                }
+                copies_arrive(raw_full_bar(raw));
+                if (++raw == kRaw) {
+                    raw = 0;
+                    ph ^= 1u;
                 }
             }
-            return v;
-        };
-        auto store = [&](const Scales &v, int n, int s) {
-            const uint32_t sc = sS + s * scale_stage;
-            if (wg < 2) {  // row 4 wq + j of the word's four blocks: byte j of each loaded word
-                const uint32_t p01 = __byte_perm(v.w[0], v.w[1], 0x5140), p23 = __byte_perm(v.w[2], v.w[3], 0x5140);
-                const uint32_t q01 = __byte_perm(v.w[0], v.w[1], 0x7362), q23 = __byte_perm(v.w[2], v.w[3], 0x7362);
-                const uint32_t w[4] = {__byte_perm(p01, p23, 0x5410), __byte_perm(p01, p23, 0x7632),
-                                       __byte_perm(q01, q23, 0x5410), __byte_perm(q01, q23, 0x7632)};
-                const int r0 = 4 * wq;
-                const uint32_t at = sc + 512u * wg + (uint32_t)(r0 >> 5) * 4u + (uint32_t)(r0 & 31) * 16u;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) st_shared_u32(at + 16 * j, w[j]);
+        }
+        if (!ok && lane == 0) raise();
+        asm volatile("cp.async.wait_all;" ::: "memory");  // none outlives the CTA
+    } else {
+        const int set = (warp - kTranspose) >> 2;
+        const int i = (int)threadIdx.x - 32 * kTranspose - 128 * set;  // 0..127 within the set
+        const int rows = tab.o.rows;
+        const uint32_t to_weights = 512u * (uint32_t)(i >> 5) + (uint32_t)(i & 7) * 64u + (uint32_t)((i & 31) >> 3) * 4u;
+        // this set's stages: number n = set, set + kSets, .. of the CTA's sequence
+        int s = set, raw = set;
+        uint32_t ph = 1, raw_ph = 0;
+        int skip = set;  // stages until its next one
+        bool ok = true;
+        for (TileWalk<false> walk(tab, first, stride); ok && walk.more(); walk.next()) {
+            if (skip >= k_stages) {
+                skip -= k_stages;
+                continue;
             }
+            const Tile t = walk.get();
+            int k = skip;
+            for (; k < k_stages; k += kSets) {
+                if (!__all_sync(0xffffffffu, wait_bar(raw_full_bar(raw), raw_ph, abort_flag) &&
+                                                 wait_bar(empty_bar(s), ph, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t rt = sR + raw * kRawStage, rw = rt + kBlocks * kRawToken;
+                const uint32_t sc = sS + s * scale_stage;
+                if (i < 64) {  // weight rows 4 (i % 32) ..: byte j of each block's word is row j's
+                    const uint32_t at = rw + (uint32_t)(i >> 5) * (4 * kRawWeight) + (uint32_t)(i & 31) * 4u;
+                    const uint32_t w0 = ld_shared_u32(at), w1 = ld_shared_u32(at + kRawWeight),
+                                   w2 = ld_shared_u32(at + 2 * kRawWeight), w3 = ld_shared_u32(at + 3 * kRawWeight);
+                    const uint32_t p01 = __byte_perm(w0, w1, 0x5140), p23 = __byte_perm(w2, w3, 0x5140);
+                    const uint32_t q01 = __byte_perm(w0, w1, 0x7362), q23 = __byte_perm(w2, w3, 0x7362);
+                    const uint32_t to = sc + to_weights;
+                    st_shared_u32(to, __byte_perm(p01, p23, 0x5410));
+                    st_shared_u32(to + 16, __byte_perm(p01, p23, 0x7632));
+                    st_shared_u32(to + 32, __byte_perm(q01, q23, 0x5410));
+                    st_shared_u32(to + 48, __byte_perm(q01, q23, 0x7632));
+                }
+                // tokens: (four blocks, row); a block's run starts at its first byte's place in a word
+                const uint32_t first_at = (uint32_t)(k * kBlocks) * (uint32_t)rows + (uint32_t)t.row0;
+                for (int task = i; task < 2 * t.n; task += 128) {
+                    const int g = task >= t.n ? 1 : 0, r = task - (g ? t.n : 0);
+                    uint32_t v = 0;
 #pragma unroll
-            for (int m = 0; m < kTokenTasks; ++m) {
-                const int task = i + 128 * m, g = task >= n ? 1 : 0, r = task - (g ? n : 0);
-                if (r < n)
+                    for (int j = 0; j < 4; ++j) {
+                        const int b = 4 * g + j;
+                        const uint32_t shift = (first_at + (uint32_t)b * (uint32_t)rows) & 3u;
+                        v |= ld_shared_u8(rt + (uint32_t)b * kRawToken + shift + (uint32_t)r) << (8 * j);
+                    }
                     st_shared_u32(sc + 1024u + 512u * (uint32_t)(g * atoms + (r >> 7)) + (uint32_t)(r & 31) * 16u +
                                       (uint32_t)((r & 127) >> 5) * 4u,
-                                  v.x[m]);
+                                  v);
+                }
+                fence_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(raw_empty_bar(raw));
+                    if (leader)
+                        mbar_arrive(scale_bar(s));
+                    else
+                        mbar_arrive_cluster(mapa_shared(scale_bar(s), 0));
+                }
+                s += kSets;
+                if (s >= stages) {
+                    s -= stages;
+                    ph ^= 1u;
+                }
+                raw += kSets;
+                if (raw >= kRaw) {
+                    raw -= kRaw;
+                    raw_ph ^= 1u;
+                }
             }
-        };
-        // this set's stages: number n = set, set + kScaleSets, .. of the CTA's sequence
-        int tile = first, k = set;
-        auto settle = [&]() {
-            while (tile < total && k >= k_stages) {
-                k -= k_stages;
-                tile += stride;
-            }
-        };
-        Scales next;
-        Tile t;
-        int t_of = -1;
-        auto fetch = [&]() {
-            if (tile >= total) return;
-            if (t_of != tile) {
-                t = decode<false>(tab, tile);
-                t_of = tile;
-            }
-            next = load(t, k);
-        };
-        settle();
-        fetch();
-        int s = set % stages;
-        uint32_t ph = 1;
-        while (tile < total) {
-            const Scales now = next;
-            const int n = t.n;
-            k += kScaleSets;
-            settle();
-            fetch();
-            if (!__all_sync(0xffffffffu, wait_bar(empty_bar(s), ph, abort_flag))) {
-                if (lane == 0) raise();
-                break;
-            }
-            store(now, n, s);
-            fence_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(scale_bar(s), 0));
-            s += kScaleSets;
-            if (s >= stages) {
-                s -= stages;
-                ph ^= 1u;
-            }
+            skip = k - k_stages;
         }
+        if (!ok && lane == 0) raise();
     }
 
     tc_fence_before();
