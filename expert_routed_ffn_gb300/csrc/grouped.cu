@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
                 }
                 fence_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(mapa_shared(zeroed_bar(st), 0));
+                if (lane == 0) mbar_arrive_pair(mapa_shared(zeroed_bar(st), 0));
             }
             s = (s + k_blocks) % stages;
         }
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
             if (!empty) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(a), 0));
+                if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_bar(a), 0));
                 ++n_acc;
             }
         }

@@ -69,12 +69,13 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     }
 }
 
-// Arrive on a barrier of either CTA (address from mapa_shared) without waiting for this
-// thread's stores: for handing back an accumulator, whose reads tcgen05.wait::ld has completed.
-// The releasing form waits until the tile's output stores have been performed (measured: about
-// 2000 cycles per tile in which the next products wait).
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// Arrive on a barrier of either CTA (address from mapa_shared), with the default semantics: what
+// it hands over stays within each CTA (an accumulator whose reads tcgen05.wait::ld has completed;
+// shared memory that the CTA's own tensor core reads next, after fence.proxy.async), so nothing
+// has to be made visible to the other one.  The form that releases at cluster scope waits for the
+// warp's outstanding stores and loads: about 2000 cycles per tile, or per stage of scales.
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // One lane of a converged warp.  The roles that issue copies and MMAs run their loops on the

@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
                                   t.col0 + rank * half_cols + 32 * q + lane, 0, lane);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(a), 0));
+            if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_bar(a), 0));
         }
     } else if (warp < kTranspose) {
         const int i = (int)threadIdx.x - 32 * kFetch;
@@ -407,10 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(raw_empty_bar(raw));
-                    if (leader)
-                        mbar_arrive(scale_bar(s));
-                    else
-                        mbar_arrive_cluster(mapa_shared(scale_bar(s), 0));
+                    mbar_arrive_pair(mapa_shared(scale_bar(s), 0));
                 }
                 s += kSets;
                 if (s >= stages) {
