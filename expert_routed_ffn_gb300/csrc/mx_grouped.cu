@@ -49,7 +49,6 @@ constexpr int kBoxes = kMaxRows / 32;
 constexpr int kRaw = 8;
 constexpr int kRawToken = 208, kRawWeight = 128;
 constexpr int kRawStage = kBlocks * (kRawToken + kRawWeight);
-constexpr int kTokenWords = (kMaxRows + 3) / 4 + 1;
 constexpr int kStageSpace = 203776;
 
 struct Header {
@@ -308,41 +307,44 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
             if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_bar(a), 0));
         }
     } else if (warp < kTranspose) {
-        const int i = (int)threadIdx.x - 32 * kFetch;
+        // 16 threads per block: of its weights 4-byte words 16 m + i % 16 (m < 2), of its tokens
+        // those with m < 4.  A stage is 8 blocks on, which moves a token run by a multiple of 8
+        // bytes, so its alignment holds for the tile.
+        const int i = (int)threadIdx.x - 32 * kFetch, b = i >> 4, w0 = 4 * (i & 15);
         const int n_blocks = K / 32, rows = tab.o.rows, n_out = tab.o.n_out;
-        const uint8_t *const xs = p.xs, *const xs_end = xs + (size_t)n_blocks * rows;
+        const uint8_t *const xs_end = p.xs + (size_t)n_blocks * rows;
+        const uint32_t rt0 = sR + (uint32_t)(b * kRawToken + w0), rw0 = sR + (uint32_t)(kBlocks * kRawToken + b * kRawWeight + w0);
         int raw = 0;
         uint32_t ph = 1;
         bool ok = true;
         for (TileWalk<false> walk(tab, first, stride); ok && walk.more(); walk.next()) {
             const Tile t = walk.get();
-            const int col = t.col0 + rank * half_cols;
-            const uint8_t *const ws = p.ws + (size_t)t.e * n_blocks * n_out;
-            for (int b0 = 0; b0 < n_blocks; b0 += kBlocks) {
+            const int col = t.col0 + rank * half_cols + w0;
+            const uint8_t *ws = p.ws + ((size_t)t.e * n_blocks + b) * n_out + col;
+            // n_out and half_cols are multiples of 8 and 64: a word is inside or outside
+            const bool w_in[2] = {w0 < half_cols && col < n_out, w0 + 64 < half_cols && col + 64 < n_out};
+            const size_t at = (size_t)b * rows + t.row0;
+            const uint8_t *xs = p.xs + (at & ~(size_t)3) + w0;
+            const int x_bytes = (int)(at & 3) + t.rows - w0;  // of the run from this thread's first word on
+            for (int left = n_blocks - b; left > -b; left -= kBlocks) {  // left <= 0: a block past K
                 if (!__all_sync(0xffffffffu, wait_bar(raw_empty_bar(raw), ph, abort_flag))) {
                     ok = false;
                     break;
                 }
-                const uint32_t rt = sR + raw * kRawStage, rw = rt + kBlocks * kRawToken;
+                const uint32_t off = (uint32_t)(raw * kRawStage);
+                const bool in = left > 0;
 #pragma unroll
-                for (int id = i; id < kBlocks * 32; id += 128) {
-                    const int b = id >> 5, w = 4 * (id & 31);
-                    // n_out is a multiple of 8: a word is inside or outside
-                    const bool in = b0 + b < n_blocks && w < half_cols && col + w < n_out;
-                    copy_word(rw + b * kRawWeight + w, in ? ws + (size_t)(b0 + b) * n_out + col + w : ws, in ? 4 : 0);
-                }
-                for (int id = i; id < kBlocks * kTokenWords; id += 128) {
-                    const int b = id / kTokenWords, w = id - b * kTokenWords;
-                    const uint8_t *src = xs;
-                    int bytes = 0;
-                    if (b0 + b < n_blocks) {
-                        const size_t at = (size_t)(b0 + b) * rows + t.row0;
-                        src = xs + (at & ~(size_t)3) + 4 * w;
-                        if (src < xs + at + t.rows) bytes = (int)min((ptrdiff_t)4, xs_end - src);
+                for (int m = 0; m < 2; ++m)
+                    if (!in || w_in[m]) copy_word(rw0 + off + 64 * m, in ? ws + 64 * m : p.ws, in ? 4 : 0);
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    if (x_bytes > 64 * m) {  // at the tensor's end a word may hold fewer bytes
+                        const uint8_t *src = in ? xs + 64 * m : p.xs;
+                        copy_word(rt0 + off + 64 * m, src, in ? (int)min((ptrdiff_t)4, xs_end - src) : 0);
                     }
-                    copy_word(rt + b * kRawToken + 4 * w, bytes ? src : xs, bytes);
-                }
                 copies_arrive(raw_full_bar(raw));
+                ws += (size_t)kBlocks * n_out;
+                xs += (size_t)kBlocks * rows;
                 if (++raw == kRaw) {
                     raw = 0;
                     ph ^= 1u;
