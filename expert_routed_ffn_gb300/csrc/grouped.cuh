@@ -98,7 +98,6 @@ struct TileTable {
     int offs[kMaxExperts + 1];         // first row of each expert
     int tiles[kMaxExperts];            // row-grouped: its first row tile; INT_MAX behind the last
     uint16_t share[kMaxExperts];       // row-grouped: rows of its tiles but the last, a multiple of 32
-    int row_tiles;                     // row-grouped: of all experts
     int total;                         // tiles, 0 where the offsets decrease or leave [0, rows]
 };
 
@@ -137,80 +136,74 @@ __device__ __forceinline__ bool load_table(const GroupedOut &p, TileTable &tab) 
             tab.tiles[e] = e < E ? run : 0x7fffffff;
             run += cnt[j];
         }
-        if (lane == 31) tab.row_tiles = run;
         if (lane == 31) tab.total = !ok ? 0 : DENSE ? E * p.row_tiles * p.col_tiles : run * p.col_tiles;
     }
     __syncthreads();
     return ok;
 }
 
-// Walks a CTA pair's tiles first, first + stride, .. (a converged warp).  Inside an expert the
-// row tiles of one column tile are adjacent, so that concurrent CTAs share its weights in L2;
-// its rows are dealt evenly to its row tiles, in multiples of 32 (no tile is left empty: with
-// `parts` tiles of at most T rows either parts <= T / 32, and rounding shares up takes fewer
-// than `parts` * 32 of the more than T * (parts - 1) rows, or the shares are T).
+// Walks a CTA pair's tiles first, first + stride, .. (a converged warp), numbered with the column
+// tile innermost: the position is kept in digits, so that a step takes no division (one took a
+// thousand cycles of the thread that feeds the tensor core).  An expert's rows are dealt evenly
+// to its row tiles, in multiples of 32 (no tile is left empty: with `parts` tiles of at most T
+// rows either parts <= T / 32, and rounding shares up takes fewer than `parts` * 32 of the more
+// than T * (parts - 1) rows, or the shares are T).
 template <bool DENSE>
 struct TileWalk {
     const TileTable &tab;
     int tile, stride;
-    // dense: the tile as (expert, column tile, row tile), and the stride in the same digits
-    int e = 0, c = 0, r = 0, de = 0, dc = 0, dr = 0;
+    int c, r, e = 0;             // column tile; row tile (dense: within the expert); dense: expert
+    int dc, dr, de = 0;          // the stride in the same digits
 
     __device__ __forceinline__ TileWalk(const TileTable &table, int first, int step)
         : tab(table), tile(first), stride(step) {
+        r = first / tab.o.col_tiles;
+        c = first - r * tab.o.col_tiles;
+        dr = step / tab.o.col_tiles;
+        dc = step - dr * tab.o.col_tiles;
         if (DENSE) {
-            split(first, e, c, r);
-            split(step, de, dc, dr);
+            e = r / tab.o.row_tiles;
+            r -= e * tab.o.row_tiles;
+            de = dr / tab.o.row_tiles;
+            dr -= de * tab.o.row_tiles;
         }
-    }
-    __device__ __forceinline__ void split(int n, int &x, int &y, int &z) const {
-        const int strip = n / tab.o.row_tiles;
-        z = n - strip * tab.o.row_tiles;
-        x = strip / tab.o.col_tiles;
-        y = strip - x * tab.o.col_tiles;
     }
     __device__ __forceinline__ bool more() const { return tile < tab.total; }
     __device__ __forceinline__ void next() {
         tile += stride;
-        if (DENSE) {
-            r += dr;
-            c += dc;
-            e += de;
-            if (r >= tab.o.row_tiles) {
-                r -= tab.o.row_tiles;
-                ++c;
-            }
-            if (c >= tab.o.col_tiles) {
-                c -= tab.o.col_tiles;
-                ++e;
-            }
+        c += dc;
+        r += dr;
+        e += de;
+        if (c >= tab.o.col_tiles) {
+            c -= tab.o.col_tiles;
+            ++r;
+        }
+        if (DENSE && r >= tab.o.row_tiles) {
+            r -= tab.o.row_tiles;
+            ++e;
         }
     }
     // the current tile (more() holds)
     __device__ __forceinline__ Tile get() const {
         const GroupedOut &p = tab.o;
         Tile t;
+        t.col0 = c * p.cols;
         if (DENSE) {
             t.e = e;
-            t.col0 = c * p.cols;
             t.row0 = r * p.tile_rows;
             t.rows = min(p.tile_rows, p.m_dense - t.row0);
             t.r0 = tab.offs[e];
             t.r1 = tab.offs[e + 1];
         } else {
-            // the last expert whose first tile is <= tile (one with rows: the next ones start later)
+            // the last expert whose first row tile is <= r (one with rows: the next ones start later)
             constexpr int kPer = kMaxExperts / 32;
             const int lane = threadIdx.x & 31;
-            const int row_tile = tile / p.col_tiles;  // an expert's tiles: a multiple of col_tiles
-            const int group = __popc(__ballot_sync(0xffffffffu, tab.tiles[lane * kPer] <= row_tile)) - 1;
-            const int in = __popc(__ballot_sync(0xffffffffu, lane < kPer && tab.tiles[group * kPer + lane] <= row_tile));
+            const int group = __popc(__ballot_sync(0xffffffffu, tab.tiles[lane * kPer] <= r)) - 1;
+            const int in = __popc(__ballot_sync(0xffffffffu, lane < kPer && tab.tiles[group * kPer + lane] <= r));
             t.e = group * kPer + in - 1;
-            const int first = tab.offs[t.e], end = tab.offs[t.e + 1], share = tab.share[t.e];
-            const int parts = (t.e + 1 < p.E ? tab.tiles[t.e + 1] : tab.row_tiles) - tab.tiles[t.e];
-            const int local = tile - tab.tiles[t.e] * p.col_tiles, strip = local / parts;
-            t.col0 = strip * p.cols;
-            t.row0 = first + (local - strip * parts) * share;
-            t.rows = min(share, end - t.row0);
+            const int share = tab.share[t.e];
+            t.row0 = tab.offs[t.e] + (r - tab.tiles[t.e]) * share;
+            t.rows = min(share, tab.offs[t.e + 1] - t.row0);
             t.r0 = 0;
             t.r1 = p.red;
         }

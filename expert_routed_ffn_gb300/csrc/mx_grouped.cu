@@ -52,7 +52,7 @@ constexpr int kRawStage = kBlocks * (kRawToken + kRawWeight);
 constexpr int kStageSpace = 203776;
 
 struct Header {
-    uint64_t bars[3 * kMaxStages + 2 * kRaw + 5];
+    uint64_t bars[2 * kMaxStages + 2 * kRaw + 5];
     TileTable table;
     uint32_t tmem;
     volatile int abort;
@@ -130,13 +130,12 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
     const uint32_t sR = base + kStageSpace;  // the fetched scales
     const uint32_t bar0 = smem_u32(h.bars);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
-    auto scale_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
-    auto empty_bar = [&](int s) { return bar0 + 8u * (2 * kMaxStages + s); };
-    auto tfull_bar = [&](uint32_t a) { return bar0 + 8u * (3 * kMaxStages + a); };
-    auto tempty_bar = [&](uint32_t a) { return bar0 + 8u * (3 * kMaxStages + 2 + a); };
-    const uint32_t drain_bar = bar0 + 8u * (3 * kMaxStages + 4);
-    auto raw_full_bar = [&](int i) { return bar0 + 8u * (3 * kMaxStages + 5 + i); };
-    auto raw_empty_bar = [&](int i) { return bar0 + 8u * (3 * kMaxStages + 5 + kRaw + i); };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
+    auto tfull_bar = [&](uint32_t a) { return bar0 + 8u * (2 * kMaxStages + a); };
+    auto tempty_bar = [&](uint32_t a) { return bar0 + 8u * (2 * kMaxStages + 2 + a); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * kMaxStages + 4);
+    auto raw_full_bar = [&](int i) { return bar0 + 8u * (2 * kMaxStages + 5 + i); };
+    auto raw_empty_bar = [&](int i) { return bar0 + 8u * (2 * kMaxStages + 5 + kRaw + i); };
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank();
     const bool leader = rank == 0;
@@ -149,8 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
-            mbar_init(full_bar(s), 1);
-            mbar_init(scale_bar(s), 8);  // four warps of each CTA
+            mbar_init(full_bar(s), 9);  // the copies of codes, four scale warps of each CTA
             mbar_init(empty_bar(s), 1);
         }
         for (uint32_t a = 0; a < 2; ++a) {
@@ -239,8 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
                 }
                 tc_fence_after();
                 for (int k = 0; k < k_stages; ++k) {
-                    if (!__all_sync(0xffffffffu, wait_bar(full_bar(s), ph, abort_flag) &&
-                                                     wait_bar<true>(scale_bar(s), ph, abort_flag))) {
+                    if (!__all_sync(0xffffffffu, wait_bar<true>(full_bar(s), ph, abort_flag))) {
                         ok = false;
                         break;
                     }
@@ -409,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(raw_empty_bar(raw));
-                    mbar_arrive_pair(mapa_shared(scale_bar(s), 0));
+                    mbar_arrive_pair(mapa_shared(full_bar(s), 0));
                 }
                 s += kSets;
                 if (s >= stages) {
