@@ -13,14 +13,14 @@
 //                to tensor memory of both CTAs (tcgen05.cp, in order with the MMAs that
 //                follow) and issues the MMAs
 //   warps 2-5    epilogue (grouped.cuh), overlapping the next tile's main loop
-//   warps 6-9    fetch scales, up to kRaw stages ahead: those of this CTA's weight rows and of
-//                all the tile's tokens, as they lie (a block's scales for consecutive rows),
-//                with 4-byte asynchronous copies: an expert's first row has any alignment
+//   warps 6-9    fetch scales, four stages' at a time: those of this CTA's weight rows and of all
+//                the tile's tokens, as they lie (a block's scales for consecutive rows), with
+//                4-byte asynchronous copies, for an expert's first row has any alignment
+//                (one stage at a time, the waits between the copies bounded the kernel: prefill
+//                61 us, a decode batch 27 us)
 //   warps 10-17  two sets of four, on alternate stages: the tensor core wants four consecutive
 //                blocks' scales of a row in one word, so they transpose from the fetched runs
-//                into the words that tcgen05.cp reads.  They are warps of their own because
-//                handing a stage to the other CTA waits for the warp's outstanding loads
-//                (fetching in the same warps: 146 us against the figure below at prefill).
+//                into the words that tcgen05.cp reads
 // Tensor memory (512 columns): two accumulators of up to 192 columns, then per stage the
 // scales of the weights (8 columns) and of the tokens (8 per 128 of them).
 #include <algorithm>
@@ -45,11 +45,12 @@ constexpr int kThreads = 32 * (kTranspose + 4 * kSets);
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxRows = 192;      // token rows of a tile
 constexpr int kBoxes = kMaxRows / 32;
-// fetched scales of a stage: 8 blocks of tokens (192 and an alignment of up to 3) and of weights
-constexpr int kRaw = 8;
+// fetched scales of four stages: per block of tokens (192 and an alignment of up to 3) and weights
+constexpr int kFetchStages = 4, kFetchBlocks = kFetchStages * kBlocks;
+constexpr int kRaw = 3;
 constexpr int kRawToken = 208, kRawWeight = 128;
-constexpr int kRawStage = kBlocks * (kRawToken + kRawWeight);
-constexpr int kStageSpace = 203776;
+constexpr int kRawBytes = kFetchBlocks * (kRawToken + kRawWeight);
+constexpr int kStageSpace = 195584;
 
 struct Header {
     uint64_t bars[2 * kMaxStages + 2 * kRaw + 5];
@@ -58,7 +59,7 @@ struct Header {
     volatile int abort;
 };
 constexpr int kHeaderBytes = 4096;
-constexpr int kSmemBytes = kHeaderBytes + kStageSpace + kRaw * kRawStage;
+constexpr int kSmemBytes = kHeaderBytes + kStageSpace + kRaw * kRawBytes;
 static_assert(sizeof(Header) <= kHeaderBytes && kSmemBytes <= 232448, "shared memory of one CTA");
 
 struct MxGroupedArgs {
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
         }
         for (int i = 0; i < kRaw; ++i) {
             mbar_init(raw_full_bar(i), 128);
-            mbar_init(raw_empty_bar(i), 4);
+            mbar_init(raw_empty_bar(i), 4 * kSets);
         }
         mbar_init(drain_bar, 1);
         fence_mbar_init();
@@ -305,12 +306,14 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
         }
     } else if (warp < kTranspose) {
         // 16 threads per block: of its weights 4-byte words 16 m + i % 16 (m < 2), of its tokens
-        // those with m < 4.  A stage is 8 blocks on, which moves a token run by a multiple of 8
-        // bytes, so its alignment holds for the tile.
+        // those with m < 4; a thread's blocks are 8 apart, which moves a token run by a multiple
+        // of 8 bytes, so its alignment holds for the tile.
         const int i = (int)threadIdx.x - 32 * kFetch, b = i >> 4, w0 = 4 * (i & 15);
         const int n_blocks = K / 32, rows = tab.o.rows, n_out = tab.o.n_out;
         const uint8_t *const xs_end = p.xs + (size_t)n_blocks * rows;
-        const uint32_t rt0 = sR + (uint32_t)(b * kRawToken + w0), rw0 = sR + (uint32_t)(kBlocks * kRawToken + b * kRawWeight + w0);
+        const size_t x_step = (size_t)kBlocks * rows, w_step = (size_t)kBlocks * n_out;
+        const uint32_t rt0 = sR + (uint32_t)(b * kRawToken + w0);
+        const uint32_t rw0 = sR + (uint32_t)(kFetchBlocks * kRawToken + b * kRawWeight + w0);
         int raw = 0;
         uint32_t ph = 1;
         bool ok = true;
@@ -323,25 +326,32 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
             const size_t at = (size_t)b * rows + t.row0;
             const uint8_t *xs = p.xs + (at & ~(size_t)3) + w0;
             const int x_bytes = (int)(at & 3) + t.rows - w0;  // of the run from this thread's first word on
-            for (int left = n_blocks - b; left > -b; left -= kBlocks) {  // left <= 0: a block past K
+            for (int b0 = 0; b0 < n_blocks; b0 += kFetchBlocks) {
                 if (!__all_sync(0xffffffffu, wait_bar(raw_empty_bar(raw), ph, abort_flag))) {
                     ok = false;
                     break;
                 }
-                const uint32_t off = (uint32_t)(raw * kRawStage);
-                const bool in = left > 0;
+                const uint32_t off = (uint32_t)(raw * kRawBytes);
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
-                    if (!in || w_in[m]) copy_word(rw0 + off + 64 * m, in ? ws + 64 * m : p.ws, in ? 4 : 0);
+                for (int f = 0; f < kFetchStages; ++f) {
+                    const int stage_b = b0 + f * kBlocks;
+                    if (stage_b >= n_blocks) break;
+                    const bool in = stage_b + b < n_blocks;  // else a block past K: zeros
+                    const uint32_t rw = rw0 + off + (uint32_t)(f * kBlocks * kRawWeight);
+                    const uint32_t rt = rt0 + off + (uint32_t)(f * kBlocks * kRawToken);
 #pragma unroll
-                for (int m = 0; m < 4; ++m)
-                    if (x_bytes > 64 * m) {  // at the tensor's end a word may hold fewer bytes
-                        const uint8_t *src = in ? xs + 64 * m : p.xs;
-                        copy_word(rt0 + off + 64 * m, src, in ? (int)min((ptrdiff_t)4, xs_end - src) : 0);
-                    }
+                    for (int m = 0; m < 2; ++m)
+                        if (!in || w_in[m]) copy_word(rw + 64 * m, in ? ws + 64 * m : p.ws, in ? 4 : 0);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+                        if (x_bytes > 64 * m) {  // at the tensor's end a word may hold fewer bytes
+                            const uint8_t *src = in ? xs + 64 * m : p.xs;
+                            copy_word(rt + 64 * m, src, in ? (int)min((ptrdiff_t)4, xs_end - src) : 0);
+                        }
+                    ws += w_step;
+                    xs += x_step;
+                }
                 copies_arrive(raw_full_bar(raw));
-                ws += (size_t)kBlocks * n_out;
-                xs += (size_t)kBlocks * rows;
                 if (++raw == kRaw) {
                     raw = 0;
                     ph ^= 1u;
@@ -355,71 +365,68 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
         const int i = (int)threadIdx.x - 32 * kTranspose - 128 * set;  // 0..127 within the set
         const int rows = tab.o.rows;
         const uint32_t to_weights = 512u * (uint32_t)(i >> 5) + (uint32_t)(i & 7) * 64u + (uint32_t)((i & 31) >> 3) * 4u;
-        // this set's stages: number n = set, set + kSets, .. of the CTA's sequence
-        int s = set, raw = set;
+        int s = 0, raw = 0;
         uint32_t ph = 1, raw_ph = 0;
-        int skip = set;  // stages until its next one
         bool ok = true;
         for (TileWalk<false> walk(tab, first, stride); ok && walk.more(); walk.next()) {
-            if (skip >= k_stages) {
-                skip -= k_stages;
-                continue;
-            }
             const Tile t = walk.get();
-            int k = skip;
-            for (; k < k_stages; k += kSets) {
-                if (!__all_sync(0xffffffffu, wait_bar(raw_full_bar(raw), raw_ph, abort_flag) &&
-                                                 wait_bar(empty_bar(s), ph, abort_flag))) {
+            for (int k = 0; k < k_stages; ++k) {
+                const int f = k % kFetchStages;
+                if (f == 0 && !__all_sync(0xffffffffu, wait_bar(raw_full_bar(raw), raw_ph, abort_flag))) {
                     ok = false;
                     break;
                 }
-                const uint32_t rt = sR + raw * kRawStage, rw = rt + kBlocks * kRawToken;
-                const uint32_t sc = sS + s * scale_stage;
-                if (i < 64) {  // weight rows 4 (i % 32) ..: byte j of each block's word is row j's
-                    const uint32_t at = rw + (uint32_t)(i >> 5) * (4 * kRawWeight) + (uint32_t)(i & 31) * 4u;
-                    const uint32_t w0 = ld_shared_u32(at), w1 = ld_shared_u32(at + kRawWeight),
-                                   w2 = ld_shared_u32(at + 2 * kRawWeight), w3 = ld_shared_u32(at + 3 * kRawWeight);
-                    const uint32_t p01 = __byte_perm(w0, w1, 0x5140), p23 = __byte_perm(w2, w3, 0x5140);
-                    const uint32_t q01 = __byte_perm(w0, w1, 0x7362), q23 = __byte_perm(w2, w3, 0x7362);
-                    const uint32_t to = sc + to_weights;
-                    st_shared_u32(to, __byte_perm(p01, p23, 0x5410));
-                    st_shared_u32(to + 16, __byte_perm(p01, p23, 0x7632));
-                    st_shared_u32(to + 32, __byte_perm(q01, q23, 0x5410));
-                    st_shared_u32(to + 48, __byte_perm(q01, q23, 0x7632));
-                }
-                // tokens: (four blocks, row); a block's run starts at its first byte's place in a word
-                const uint32_t first_at = (uint32_t)(k * kBlocks) * (uint32_t)rows + (uint32_t)t.row0;
-                for (int task = i; task < 2 * t.n; task += 128) {
-                    const int g = task >= t.n ? 1 : 0, r = task - (g ? t.n : 0);
-                    uint32_t v = 0;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int b = 4 * g + j;
-                        const uint32_t shift = (first_at + (uint32_t)b * (uint32_t)rows) & 3u;
-                        v |= ld_shared_u8(rt + (uint32_t)b * kRawToken + shift + (uint32_t)r) << (8 * j);
+                if (k % kSets == set) {
+                    if (!__all_sync(0xffffffffu, wait_bar(empty_bar(s), ph, abort_flag))) {
+                        ok = false;
+                        break;
                     }
-                    st_shared_u32(sc + 1024u + 512u * (uint32_t)(g * atoms + (r >> 7)) + (uint32_t)(r & 31) * 16u +
-                                      (uint32_t)((r & 127) >> 5) * 4u,
-                                  v);
+                    const uint32_t rt = sR + (uint32_t)(raw * kRawBytes + f * kBlocks * kRawToken);
+                    const uint32_t rw = sR + (uint32_t)(raw * kRawBytes + kFetchBlocks * kRawToken + f * kBlocks * kRawWeight);
+                    const uint32_t sc = sS + s * scale_stage;
+                    if (i < 64) {  // weight rows 4 (i % 32) ..: byte j of each block's word is row j's
+                        const uint32_t at = rw + (uint32_t)(i >> 5) * (4 * kRawWeight) + (uint32_t)(i & 31) * 4u;
+                        const uint32_t w0 = ld_shared_u32(at), w1 = ld_shared_u32(at + kRawWeight),
+                                       w2 = ld_shared_u32(at + 2 * kRawWeight), w3 = ld_shared_u32(at + 3 * kRawWeight);
+                        const uint32_t p01 = __byte_perm(w0, w1, 0x5140), p23 = __byte_perm(w2, w3, 0x5140);
+                        const uint32_t q01 = __byte_perm(w0, w1, 0x7362), q23 = __byte_perm(w2, w3, 0x7362);
+                        const uint32_t to = sc + to_weights;
+                        st_shared_u32(to, __byte_perm(p01, p23, 0x5410));
+                        st_shared_u32(to + 16, __byte_perm(p01, p23, 0x7632));
+                        st_shared_u32(to + 32, __byte_perm(q01, q23, 0x5410));
+                        st_shared_u32(to + 48, __byte_perm(q01, q23, 0x7632));
+                    }
+                    // tokens: (four blocks, row); a block's run starts at its first byte's place in a word
+                    for (int task = i; task < 2 * t.n; task += 128) {
+                        const int g = task >= t.n ? 1 : 0, r = task - (g ? t.n : 0);
+                        uint32_t v = 0;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int b = 4 * g + j;
+                            const uint32_t shift = ((uint32_t)t.row0 + (uint32_t)b * (uint32_t)rows) & 3u;
+                            v |= ld_shared_u8(rt + (uint32_t)b * kRawToken + shift + (uint32_t)r) << (8 * j);
+                        }
+                        st_shared_u32(sc + 1024u + 512u * (uint32_t)(g * atoms + (r >> 7)) + (uint32_t)(r & 31) * 16u +
+                                          (uint32_t)((r & 127) >> 5) * 4u,
+                                      v);
+                    }
+                    fence_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_pair(mapa_shared(full_bar(s), 0));
                 }
-                fence_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(raw_empty_bar(raw));
-                    mbar_arrive_pair(mapa_shared(full_bar(s), 0));
+                if (f + 1 == kFetchStages || k + 1 == k_stages) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(raw_empty_bar(raw));
+                    if (++raw == kRaw) {
+                        raw = 0;
+                        raw_ph ^= 1u;
+                    }
                 }
-                s += kSets;
-                if (s >= stages) {
-                    s -= stages;
+                if (++s == stages) {
+                    s = 0;
                     ph ^= 1u;
                 }
-                raw += kSets;
-                if (raw >= kRaw) {
-                    raw -= kRaw;
-                    raw_ph ^= 1u;
-                }
             }
-            skip = k - k_stages;
         }
         if (!ok && lane == 0) raise();
     }
