@@ -2,20 +2,26 @@
 //   c = min(1, max_norm / norm),   norm = sqrt(sum of all g^2)
 // (c = 1 where the norm is not finite: the caller sees it and skips the step).
 //
-// Two kernels.  The first sums squares: 32 values per thread and chunk in fp32, those sums
-// in fp64 (per thread, CTA, and over the CTAs in a fixed order, so the result is the same
-// from call to call).  A thread whose fp32 sum overflowed, or is so small that squares may
-// have been flushed, squares its values again in fp64.  In the second kernel every CTA adds
-// up the first one's partial sums, then scales chunks; it goes through them from the last to
-// the first, so that what the first kernel read last is still in L2.  Where the result goes
-// to the gradients themselves and c is 1, nothing is written.
+// Two kernels, whose CTAs walk blocks of the list's values.  The first sums squares: per thread
+// and step (up to 64 values) in fp32; over steps, threads and warps as unevaluated sums of two
+// fp32 numbers; over CTAs in fp64, always in the same order.  (fp64 everywhere past the steps
+// cost more than the memory: its units are few, 33 us for the second kernel of a list of 5
+// million values.)  A step whose fp32 sum may have overflowed, or is so small that squares may
+// have been flushed, is squared again in fp64.  In the second kernel every CTA adds up the
+// first one's partial sums, then scales its blocks from the last to the first, so that what was
+// read last is still in L2.  Where the result goes to the gradients themselves and c is 1,
+// nothing is written.
 //
 // Bound by HBM: one read to sum, one read (from L2 up to its size) and one write to scale.
+// Concurrent CTAs read neighbouring blocks; with one long run per CTA instead, 2.2 GB took 1022
+// against 989 us.
 //
 // The tensors' addresses travel as kernel parameters (up to kMaxTensors per launch, more in
-// further launches): no table is copied to the device and a captured call owns its list.
+// further launches), with the tensor each CTA's first block is in: no table is copied to the
+// device, a captured call owns its list, and a short list needs no search of the table, each
+// step of which can be a miss of the constant cache.
 #include <algorithm>
-#include <cmath>
+#include <iterator>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -26,10 +32,10 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPerThread = 32;                       // values per thread and chunk
-constexpr int kChunkElems = kThreads * kPerThread;   // 8192
+constexpr int kChunk = 2048;      // values: what blocks are made of
+constexpr int kVecs = 8;          // 16-byte accesses per thread and step
 constexpr int kCtasPerSm = 8;
-constexpr int kMaxGrid = 2048;                       // partial sums per launch
+constexpr int kMaxGrid = 1280;    // CTAs, and partial sums, per launch
 constexpr int kMaxTensors = 960;
 
 struct Entry {
@@ -40,9 +46,10 @@ struct Entry {
 template <int N>
 struct ClipArgs {
     Entry t[N];
-    int first[N];       // number of the tensor's first chunk
+    int first[N + 1];             // number of the tensor's first chunk; the total
     uint32_t f32[(N + 31) / 32];  // bit set: fp32, else bf16
-    int tensors, chunks;
+    uint16_t start[kMaxGrid];     // the tensor a CTA's first chunk is in
+    int tensors, chunks, block;   // block: chunks of a block
     double *partial;    // norm kernel: this launch's sums; scale kernel: all of them
     int num_partial;
     float max_norm;
@@ -50,52 +57,71 @@ struct ClipArgs {
 };
 static_assert(sizeof(ClipArgs<kMaxTensors>) <= 32764, "kernel parameter space");
 
-struct Chunk {
-    const void *src;
-    void *dst;
-    int n;       // values in the chunk
-    bool f32, vec;
-};
-
+// The tensor that chunk `c`, the first of a CTA's block number `blk`, lies in
 template <int N>
-__device__ __forceinline__ Chunk find(const ClipArgs<N> &p, int chunk) {
+__device__ __forceinline__ int tensor_of(const ClipArgs<N> &p, int blk, int c) {
+    if (blk < (int)gridDim.x) return p.start[blk];
     int lo = 0, hi = p.tensors - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (p.first[mid] <= chunk)
+        if (p.first[mid] <= c)
             lo = mid;
         else
             hi = mid - 1;
     }
-    const long long at = (long long)(chunk - p.first[lo]) * kChunkElems;
-    Chunk c;
-    c.f32 = p.f32[lo >> 5] >> (lo & 31) & 1u;
-    const long long bytes = at * (c.f32 ? 4 : 2);
-    c.src = static_cast<const char *>(p.t[lo].grad) + bytes;
-    c.dst = static_cast<char *>(p.t[lo].out) + bytes;
-    c.n = (int)min((long long)kChunkElems, p.t[lo].count - at);
-    // full chunks of aligned tensors go in 16-byte accesses
-    c.vec = c.n == kChunkElems && ((reinterpret_cast<uintptr_t>(c.src) | reinterpret_cast<uintptr_t>(c.dst)) & 15u) == 0;
-    return c;
+    return lo;
 }
 
-__device__ __forceinline__ float load1(const Chunk &c, int i) {
-    return c.f32 ? static_cast<const float *>(c.src)[i]
-                 : __bfloat162float(static_cast<const bf16 *>(c.src)[i]);
+// The part of the chunks [c0, c1) that lies in tensor k
+struct Segment {
+    const char *src;
+    char *dst;
+    int n;          // values
+    bool f32, vec;  // vec: 16-byte accesses
+};
+template <int N>
+__device__ __forceinline__ Segment segment(const ClipArgs<N> &p, int k, int c0, int c1) {
+    const Entry &e = p.t[k];
+    const int first = p.first[k], a = max(c0, first) - first, b = min(c1, p.first[k + 1]) - first;
+    const long long at = (long long)a * kChunk;
+    Segment s;
+    s.f32 = p.f32[k >> 5] >> (k & 31) & 1u;
+    s.n = (int)(min(e.count, (long long)b * kChunk) - at);
+    s.src = static_cast<const char *>(e.grad) + at * (s.f32 ? 4 : 2);
+    s.dst = static_cast<char *>(e.out) + at * (s.f32 ? 4 : 2);
+    s.vec = ((reinterpret_cast<uintptr_t>(s.src) | reinterpret_cast<uintptr_t>(s.dst)) & 15u) == 0;
+    return s;
+}
+__device__ __forceinline__ float load1(const Segment &s, int i) {
+    return s.f32 ? reinterpret_cast<const float *>(s.src)[i] : __bfloat162float(reinterpret_cast<const bf16 *>(s.src)[i]);
 }
 
-// Sum of squares of one thread's values, as a double.
+// A running sum hi + lo, and what does not fit its range
+struct Sum {
+    float hi = 0.f, lo = 0.f;
+    double far = 0.0;
+    __device__ __forceinline__ void add(float t) {  // exact: hi + t = s + the rounding error
+        const float s = hi + t, b = s - hi;
+        lo += (hi - (s - b)) + (t - b);
+        hi = s;
+    }
+};
+
+// Add the squares of a step's values.
 template <int W>
-__device__ __forceinline__ double squares(const uint32_t (&w)[W], bool f32) {
+__device__ __forceinline__ void squares(const uint32_t (&w)[W], bool f32, Sum &sum) {
     float s[4] = {0.f, 0.f, 0.f, 0.f};
     uint32_t any = 0;
+    if (f32) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-        if (f32) {
+        for (int i = 0; i < W; ++i) {
             const float v = __uint_as_float(w[i]);
             s[i & 3] = fmaf(v, v, s[i & 3]);
             any |= w[i] << 1;
-        } else {
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
             const float a = bf16_lo(w[i]), b = bf16_hi(w[i]);
             s[i & 1] = fmaf(a, a, s[i & 1]);
             s[2 + (i & 1)] = fmaf(b, b, s[2 + (i & 1)]);
@@ -103,125 +129,177 @@ __device__ __forceinline__ double squares(const uint32_t (&w)[W], bool f32) {
         }
     }
     const float t = (s[0] + s[1]) + (s[2] + s[3]);
-    // 2^-80: what a flushed or subnormal square (< 2^-126 each) could add is far below 2^-24 of it
-    if ((t >= 8.271806e-25f && t <= 3.0e38f) || any == 0) return (double)t;
-    double d = 0.0;
+    // from 2^-80 (what flushed or subnormal squares, < 2^-126 each, could add is far below 2^-24
+    // of it) to 2^90 (2^37 of them do not overflow)
+    if ((t >= 8.271806e-25f && t <= 1.2379400e27f) || any == 0) {
+        sum.add(t);
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-        if (f32) {
-            const double v = __uint_as_float(w[i]);
-            d += v * v;
-        } else {
-            const double a = bf16_lo(w[i]), b = bf16_hi(w[i]);
-            d += a * a + b * b;
-        }
+        const double a = f32 ? __uint_as_float(w[i]) : bf16_lo(w[i]), b = f32 ? 0.f : bf16_hi(w[i]);
+        sum.far += a * a + b * b;
     }
-    return d;
 }
 
-__device__ __forceinline__ double block_sum(double v) {
-    __shared__ double s[kThreads / 32];
+// The CTA's sum, in thread 0
+__device__ __forceinline__ double block_sum(Sum v) {
+    __shared__ Sum s[kThreads / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    for (int d = 16; d > 0; d >>= 1) {
+        const float hi = __shfl_xor_sync(0xffffffffu, v.hi, d), lo = __shfl_xor_sync(0xffffffffu, v.lo, d);
+        v.add(hi);
+        v.lo += lo;
+    }
+    if (__any_sync(0xffffffffu, !(v.far == 0.0))) {  // (a NaN too)
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) v.far += __shfl_xor_sync(0xffffffffu, v.far, d);
+    }
+    if (lane == 0) s[warp] = v;
     __syncthreads();
-    double r = 0.0;
+    if (threadIdx.x != 0) return 0.0;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) r += s[i];
-    return r;
+    for (int i = 1; i < kThreads / 32; ++i) {
+        v.add(s[i].hi);
+        v.lo += s[i].lo;
+        if (!(s[i].far == 0.0)) v.far += s[i].far;
+    }
+    return (double)v.hi + (double)v.lo + v.far;
 }
 
 template <int N>
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ ClipArgs<N> p) {
     pdl_wait();
     pdl_trigger();
-    double sum = 0.0;
-    for (int chunk = blockIdx.x; chunk < p.chunks; chunk += gridDim.x) {
-        const Chunk c = find(p, chunk);
-        if (c.vec) {
-            const uint4 *src = static_cast<const uint4 *>(c.src) + threadIdx.x;
-            if (c.f32) {
-                uint32_t w[32];
+    const int tid = threadIdx.x;
+    Sum sum;
+    for (int blk = blockIdx.x; (long long)blk * p.block < p.chunks; blk += gridDim.x) {
+        const int c0 = blk * p.block, c1 = min(c0 + p.block, p.chunks);
+        for (int k = tensor_of(p, blk, c0); k < p.tensors && p.first[k] < c1; ++k) {
+            const Segment s = segment(p, k, c0, c1);
+            int done = 0;  // values covered by whole vectors
+            if (s.vec) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(s.src);
+                const int per = s.f32 ? 4 : 8, nv = s.n / per;
+                for (int base = 0; base < nv; base += kVecs * kThreads) {
+                    uint32_t w[4 * kVecs];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) reinterpret_cast<uint4 *>(w)[j] = src[j * kThreads];
-                sum += squares(w, true);
-            } else {
-                uint32_t w[16];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) reinterpret_cast<uint4 *>(w)[j] = src[j * kThreads];
-                sum += squares(w, false);
+                    for (int j = 0; j < kVecs; ++j) {
+                        const int i = base + j * kThreads + tid;
+                        reinterpret_cast<uint4 *>(w)[j] = i < nv ? src[i] : make_uint4(0, 0, 0, 0);
+                    }
+                    squares(w, s.f32, sum);
+                }
+                done = nv * per;
             }
-        } else {
-            uint32_t w[kPerThread];
+            for (int base = done; base < s.n; base += 8 * kThreads) {
+                uint32_t w[8];
 #pragma unroll
-            for (int j = 0; j < kPerThread; ++j) {
-                const int i = threadIdx.x + j * kThreads;
-                w[j] = i < c.n ? __float_as_uint(load1(c, i)) : 0u;
+                for (int j = 0; j < 8; ++j) {
+                    const int i = base + j * kThreads + tid;
+                    w[j] = i < s.n ? __float_as_uint(load1(s, i)) : 0u;
+                }
+                squares(w, true, sum);
             }
-            sum += squares(w, true);
         }
     }
     const double total = block_sum(sum);
-    if (threadIdx.x == 0) p.partial[blockIdx.x] = total;
+    if (tid == 0) p.partial[blockIdx.x] = total;
+}
+
+// The norm and the factor from the sum of squares, with the exponent apart: the square of a
+// value may be out of fp32's range, and fp64 square roots and quotients are slow here.
+__device__ __forceinline__ void norm_of(double sum, float max_norm, float &norm, float &scale, bool &clip) {
+    const long long bits = __double_as_longlong(sum);
+    const int ex = (int)(bits >> 52 & 0x7ff);
+    clip = false;
+    scale = 1.0f;
+    norm = 0.0f;
+    if (sum == 0.0) return;
+    if (ex == 0x7ff) {  // a NaN or an infinity among the gradients: they pass through
+        norm = (float)sum;
+        return;
+    }
+    const int e = ex - 1023, h = e >> 1;  // sum = m 2^(2 h), 1 <= m < 4
+    const float root = sqrtf((float)__longlong_as_double((bits & 0xfffffffffffffll) | (long long)(1023 + e - 2 * h) << 52));
+    norm = scalbnf(root, h);
+    clip = norm > max_norm;
+    if (clip) scale = scalbnf(max_norm / root, -h);
 }
 
 template <int N>
 __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ ClipArgs<N> p) {
+    __shared__ float s_scale;
+    __shared__ bool s_clip;
+    const int tid = threadIdx.x;
+    const int blocks = (p.chunks + p.block - 1) / p.block;
     pdl_wait();
     pdl_trigger();
-    double sum = 0.0;
-    for (int i = threadIdx.x; i < p.num_partial; i += kThreads) sum += p.partial[i];
-    const double norm = sqrt(block_sum(sum));
-    if (p.norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = (float)norm;
-    // a NaN or an infinity among the gradients: they pass through
-    const bool clip = norm > (double)p.max_norm && norm <= 1.7e308;
-    const float scale = clip ? (float)((double)p.max_norm / norm) : 1.0f;
-    for (int chunk = p.chunks - 1 - (int)blockIdx.x; chunk >= 0; chunk -= gridDim.x) {
-        const Chunk c = find(p, chunk);
-        if (!clip && c.src == c.dst) continue;
-        if (c.vec) {
-            const uint4 *src = static_cast<const uint4 *>(c.src) + threadIdx.x;
-            uint4 *dst = static_cast<uint4 *>(c.dst) + threadIdx.x;
-            if (c.f32) {
-                uint4 w[8];
+    if (tid < 32) {
+        double sum = 0.0;
+        for (int i = tid; i < p.num_partial; i += 32) sum += p.partial[i];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = src[j * kThreads];
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        float norm, scale;
+        bool clip;
+        norm_of(sum, p.max_norm, norm, scale, clip);
+        if (tid == 0) {
+            s_scale = scale;
+            s_clip = clip;
+            if (p.norm != nullptr && blockIdx.x == 0) *p.norm = norm;
+        }
+    }
+    __syncthreads();
+    const float scale = s_scale;
+    const bool clip = s_clip;
+    if ((int)blockIdx.x >= blocks) return;
+    for (int blk = ((blocks - 1 - (int)blockIdx.x) / (int)gridDim.x) * (int)gridDim.x + (int)blockIdx.x; blk >= 0; blk -= gridDim.x) {
+        const int c0 = blk * p.block, c1 = min(c0 + p.block, p.chunks);
+        for (int k = tensor_of(p, blk, c0); k < p.tensors && p.first[k] < c1; ++k) {
+            const Segment s = segment(p, k, c0, c1);
+            if (!clip && s.src == s.dst) continue;
+            int done = 0;
+            if (s.vec) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(s.src);
+                uint4 *dst = reinterpret_cast<uint4 *>(s.dst);
+                const int per = s.f32 ? 4 : 8, nv = s.n / per;
+                done = nv * per;
+                for (int base = 0; base < nv; base += kVecs * kThreads) {
+                    uint4 w[kVecs];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float4 f = *reinterpret_cast<float4 *>(&w[j]);
-                    f.x *= scale;
-                    f.y *= scale;
-                    f.z *= scale;
-                    f.w *= scale;
-                    __stcs(reinterpret_cast<float4 *>(dst + j * kThreads), f);
-                }
-            } else {
-                uint4 w[4];
+                    for (int j = 0; j < kVecs; ++j) {
+                        const int i = base + j * kThreads + tid;
+                        if (i < nv) w[j] = src[i];
+                    }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = src[j * kThreads];
+                    for (int j = 0; j < kVecs; ++j) {
+                        const int i = base + j * kThreads + tid;
+                        uint32_t *x = reinterpret_cast<uint32_t *>(&w[j]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t *x = reinterpret_cast<uint32_t *>(&w[j]);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) x[k] = pack_bf16x2(bf16_lo(x[k]) * scale, bf16_hi(x[k]) * scale);
-                    __stcs(dst + j * kThreads, w[j]);
+                        for (int q = 0; q < 4; ++q)
+                            x[q] = s.f32 ? __float_as_uint(__uint_as_float(x[q]) * scale)
+                                         : pack_bf16x2(bf16_lo(x[q]) * scale, bf16_hi(x[q]) * scale);
+                        if (i < nv) __stcs(dst + i, w[j]);
+                    }
                 }
             }
-        } else {
-            for (int i = threadIdx.x; i < c.n; i += kThreads) {
-                const float v = load1(c, i) * scale;
-                if (c.f32)
-                    static_cast<float *>(c.dst)[i] = v;
+            for (int i = done + tid; i < s.n; i += kThreads) {
+                const float v = load1(s, i) * scale;
+                if (s.f32)
+                    reinterpret_cast<float *>(s.dst)[i] = v;
                 else
-                    static_cast<bf16 *>(c.dst)[i] = __float2bfloat16_rn(v);
+                    reinterpret_cast<bf16 *>(s.dst)[i] = __float2bfloat16_rn(v);
             }
         }
     }
 }
 
-// One launch's share of the list; -1: a count whose chunks do not fit an int.
+// One launch's share of the list; the grid, or -1 if it is too long.  Short lists: blocks of up
+// to 8 chunks, as many CTAs as blocks; long ones: blocks of 4 (a thread's step of fp32 values),
+// kCtasPerSm CTAs per SM.
 template <int N>
-int fill(ClipArgs<N> &a, const moe_grad *g, int n) {
+int fill(ClipArgs<N> &a, const moe_grad *g, int n, int sms) {
     long long chunks = 0;
     a.tensors = 0;
     for (int i = 0; i < n; ++i) {
@@ -230,11 +308,21 @@ int fill(ClipArgs<N> &a, const moe_grad *g, int n) {
         a.t[k] = {g[i].grad, g[i].out, g[i].count};
         a.first[k] = (int)chunks;
         if (g[i].dtype == MOE_DTYPE_F32) a.f32[k >> 5] |= 1u << (k & 31);
-        chunks += (g[i].count + kChunkElems - 1) / kChunkElems;
-        if (chunks > (1ll << 30)) return -1;
+        // a CTA's part of a tensor is counted in an int
+        const long long add = (g[i].count - 1) / kChunk + 1;
+        if (add > (1ll << 26) || (chunks += add) > (1ll << 26)) return -1;
     }
     a.chunks = (int)chunks;
-    return a.chunks;
+    a.first[a.tensors] = a.chunks;
+    const int most = std::min(kMaxGrid, kCtasPerSm * sms);
+    a.block = a.chunks > 8 * most ? 4 : std::max(1, std::min(8, a.chunks / (2 * sms)));
+    const int grid = std::max(1, std::min((a.chunks + a.block - 1) / a.block, most));
+    for (int b = 0, k = 0; b < grid; ++b) {
+        const int c = b * a.block;
+        while (k + 1 < a.tensors && a.first[k + 1] <= c) ++k;
+        a.start[b] = (uint16_t)k;
+    }
+    return grid;
 }
 
 int launches_of(int count) { return std::max(1, (count + kMaxTensors - 1) / kMaxTensors); }
@@ -242,27 +330,22 @@ int launches_of(int count) { return std::max(1, (count + kMaxTensors - 1) / kMax
 template <int N>
 moe_status run(const moe_grad *grads, int count, float max_norm, float *norm, double *partial, int sms, cudaStream_t s) {
     const char *op = "moe_clip_grad_norm";
-    const int launches = launches_of(count), most = std::min(kMaxGrid, kCtasPerSm * sms);
+    const int launches = launches_of(count);
     int used = 0;
     for (int pass = 0; pass < 2; ++pass)
         for (int l = 0; l < launches; ++l) {
-            ClipArgs<N> a = {};
+            ClipArgs<N> a;
+            std::fill(std::begin(a.f32), std::end(a.f32), 0u);
             const int at = l * kMaxTensors;
-            if (fill(a, grads + at, std::min(kMaxTensors, count - at)) < 0)
-                return op_fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^43 values in one launch", op);
-            const int grid = std::max(1, std::min(a.chunks, most));
+            const int grid = fill(a, grads + at, std::min(kMaxTensors, count - at), sms);
+            if (grid < 0) return op_fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^37 values in one launch's tensors", op);
             a.max_norm = max_norm;
-            cudaError_t e;
-            if (pass == 0) {
-                a.partial = partial + used;
-                used += grid;
-                e = launch_pdl(grad_norm_kernel<N>, dim3(grid), dim3(kThreads), 0, s, a);
-            } else {
-                a.partial = partial;
-                a.num_partial = used;
-                a.norm = l == 0 ? norm : nullptr;
-                e = launch_pdl(grad_scale_kernel<N>, dim3(grid), dim3(kThreads), 0, s, a);
-            }
+            a.partial = pass == 0 ? partial + used : partial;
+            a.num_partial = used;
+            a.norm = pass == 1 && l == 0 ? norm : nullptr;
+            if (pass == 0) used += grid;
+            const cudaError_t e = pass == 0 ? launch_pdl(grad_norm_kernel<N>, dim3(grid), dim3(kThreads), 0, s, a)
+                                            : launch_pdl(grad_scale_kernel<N>, dim3(grid), dim3(kThreads), 0, s, a);
             if (e != cudaSuccess) return op_cuda(e, op);
         }
     return MOE_OK;

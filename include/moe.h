@@ -436,8 +436,8 @@ typedef struct {
 moe_status moe_clip_workspace(int count, size_t *bytes);
 
 /* The norm of all gradients of the list together, sqrt(sum g^2), to norm[0] (device, fp32)
- * and out = g * min(1, max_norm / norm).  Squares are summed in fp32 over 32 values and in
- * fp64 from there, in a fixed order.  If a gradient holds an infinity or a NaN, the norm
+ * and out = g * min(1, max_norm / norm).  Squares are summed in fp32 over at most 64 values and
+ * in fp64 from there, in a fixed order.  If a gradient holds an infinity or a NaN, the norm
  * says so and out = g.  max_norm > 0 (infinity: the norm alone is wanted).  The list is
  * read before the call returns; tensors must not overlap each other.  count == 0: norm 0.
  * `workspace` (device) is used until the call's kernels end: calls that may overlap, and
