@@ -277,36 +277,46 @@ def block_from_inputs(shape, inputs: dict, max_tokens: int = None) -> MoeBlock:
 # tensors, on `stream` or that device's current stream, and allocates only outputs it
 # was not given.
 
+_torch = None
+
+
+def _t():
+    """torch, imported with the first operator."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+        load()
+    return _torch
+
+
 def _need(cond, message):
     if not cond:
         raise ValueError(message)
 
 
 def _dtype_code(dtype):
-    import torch
-    if dtype is torch.bfloat16:
+    if dtype is _torch.bfloat16:
         return MOE_DTYPE_BF16
-    if dtype is torch.float32:
+    if dtype is _torch.float32:
         return MOE_DTYPE_F32
-    _need(False, f"dtype must be bfloat16 or float32, not {dtype}")
+    raise ValueError(f"dtype must be bfloat16 or float32, not {dtype}")
 
 
-def _tensor(t, name, shape, dtype, device):
-    """t is a contiguous CUDA tensor of this shape and type on this device (None in shape: any size)."""
-    if t.is_cuda and t.dtype is dtype and t.device == device and t.is_contiguous() and t.shape == shape:
+def _tensor(t, name, shape, dtype, index):
+    """t is a contiguous CUDA tensor of this shape and type on device `index`."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous() and index >= 0:
         return
-    _need(t.device == device and device.type == "cuda", f"{name} must be on the CUDA device of the other tensors")
-    _need(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
-    _need(t.dim() == len(shape) and all(s is None or s == n for s, n in zip(shape, t.shape)),
-          f"{name} must have shape {list(shape)}, not {list(t.shape)}")
+    _need(index >= 0 and t.get_device() == index, f"{name} must be on the CUDA device of the other tensors")
+    _need(t.dtype is dtype, f"{name} must be {dtype}, not {t.dtype}")
+    _need(t.shape == shape, f"{name} must have shape {list(shape)}, not {list(t.shape)}")
     _need(t.is_contiguous(), f"{name} must be contiguous")
 
 
-def _enter(device, stream):
+def _enter(index, stream):
     """(raw stream, undo): makes the tensors' device the current one and `stream` its current
     stream (so that outputs are allocated for it).  undo is None where nothing had to change."""
-    import torch
-    index = device.index
+    torch = _torch
     if stream is None and torch._C._cuda_getDevice() == index:
         return torch._C._cuda_getCurrentRawStream(index), None
     undo = contextlib.ExitStack()
@@ -324,34 +334,28 @@ def _leave(undo):
 def operators_status(device=None) -> int:
     """moe_operators_status on `device` (default: the current one): synchronises, returns
     and clears what the operators recorded there."""
-    import torch
-    with torch.cuda.device(device):
+    with _t().cuda.device(device):
         return load().moe_operators_status()
 
 
 def _grouped(name, A, W, offs, out, out_dtype, stream, forward):
-    import torch
+    torch = _t()
     _need(W.dim() == 3 and A.dim() == 2, "W must be [E, N, K] and X or dY [rows, ..]")
     E, N, K = W.shape
     cols, red = (N, K) if forward else (K, N)
-    rows, width = A.shape
-    device = A.device
-    bf16 = torch.bfloat16
-    # the usual case in one expression; what it does not cover is named by the checks below
-    if not (A.is_cuda and A.dtype is bf16 and W.dtype is bf16 and offs.dtype is torch.int32 and width == red
-            and offs.dim() == 1 and offs.numel() == E + 1 and W.device == device and offs.device == device
-            and A.is_contiguous() and W.is_contiguous() and offs.is_contiguous()):
-        _tensor(W, "W", (E, N, K), bf16, device)
-        _tensor(A, "X" if forward else "dY", (None, red), bf16, device)
-        _tensor(offs, "offs", (E + 1,), torch.int32, device)
-    raw, undo = _enter(device, stream)
+    rows = A.shape[0]
+    index = A.get_device()
+    _tensor(A, "X" if forward else "dY", (rows, red), torch.bfloat16, index)
+    _tensor(W, "W", (E, N, K), torch.bfloat16, index)
+    _tensor(offs, "offs", (E + 1,), torch.int32, index)
+    raw, undo = _enter(index, stream)
     try:
         if out is None:
-            out = torch.empty((rows, cols), dtype=out_dtype or bf16, device=device)
+            out = torch.empty((rows, cols), dtype=out_dtype or torch.bfloat16, device=A.device)
         else:
-            _tensor(out, "out", (rows, cols), out_dtype or out.dtype, device)
-        status = getattr(_lib or load(), name)(A.data_ptr(), W.data_ptr(), offs.data_ptr(), rows, E, N, K,
-                                               _dtype_code(out.dtype), out.data_ptr(), raw)
+            _tensor(out, "out", (rows, cols), out_dtype or out.dtype, index)
+        status = getattr(_lib, name)(A.data_ptr(), W.data_ptr(), offs.data_ptr(), rows, E, N, K, _dtype_code(out.dtype),
+                                     out.data_ptr(), raw)
     finally:
         _leave(undo)
     check(status, name)
@@ -374,23 +378,23 @@ def grouped_wgrad(dY, X, offs, out=None, out_dtype=None, accumulate=False, strea
     """The gradient of grouped_forward by its W: dW[e] = sum over e's rows of dY[r] X[r]^T, in
     out (default: a new [E, N, K] tensor, fp32 unless out_dtype says otherwise).  accumulate:
     add to what out holds."""
-    import torch
+    torch = _t()
     _need(X.dim() == 2 and dY.dim() == 2, "X must be [rows, K] and dY [rows, N]")
     _need(offs.dim() == 1 and offs.numel() >= 2, "offs must be [E + 1]")
-    (rows, K), N = X.shape, dY.shape[1]
-    _tensor(X, "X", (rows, K), torch.bfloat16, X.device)
-    _tensor(dY, "dY", (rows, N), torch.bfloat16, X.device)
-    _tensor(offs, "offs", (offs.numel(),), torch.int32, X.device)
-    E = offs.numel() - 1
     _need(out is not None or not accumulate, "accumulate needs out")
-    raw, undo = _enter(X.device, stream)
+    (rows, K), N, E = X.shape, dY.shape[1], offs.numel() - 1
+    index = X.get_device()
+    _tensor(X, "X", (rows, K), torch.bfloat16, index)
+    _tensor(dY, "dY", (rows, N), torch.bfloat16, index)
+    _tensor(offs, "offs", (E + 1,), torch.int32, index)
+    raw, undo = _enter(index, stream)
     try:
         if out is None:
             out = torch.empty((E, N, K), dtype=out_dtype or torch.float32, device=X.device)
         else:
-            _tensor(out, "out", (E, N, K), out_dtype or out.dtype, X.device)
-        status = load().moe_grouped_wgrad(dY.data_ptr(), X.data_ptr(), offs.data_ptr(), rows, E, N, K,
-                                          _dtype_code(out.dtype), int(accumulate), out.data_ptr(), raw)
+            _tensor(out, "out", (E, N, K), out_dtype or out.dtype, index)
+        status = _lib.moe_grouped_wgrad(dY.data_ptr(), X.data_ptr(), offs.data_ptr(), rows, E, N, K,
+                                        _dtype_code(out.dtype), int(accumulate), out.data_ptr(), raw)
     finally:
         _leave(undo)
     check(status, "moe_grouped_wgrad")
@@ -398,37 +402,36 @@ def grouped_wgrad(dY, X, offs, out=None, out_dtype=None, accumulate=False, strea
 
 
 def _mx_format(fmt):
-    _need(fmt in ("mxfp8", "mxfp4"), f"fmt must be 'mxfp8' or 'mxfp4', not {fmt!r}")
-    return WEIGHT_FORMATS[fmt]
-
-
-def _mx_shapes(shape, fmt):
-    """(slices, rows, K), codes shape and scales shape of a [.., rows, K] tensor."""
-    _need(len(shape) in (2, 3), "the tensor must be [rows, K] or [slices, rows, K]")
-    lead, (rows, K) = tuple(shape[:-2]), tuple(shape[-2:])
-    return (lead[0] if lead else 1, rows, K), lead + (rows, K if fmt == "mxfp8" else K // 2), lead + (K // 32, rows)
+    if fmt == "mxfp4":
+        return MOE_WEIGHTS_MXFP4
+    _need(fmt == "mxfp8", f"fmt must be 'mxfp8' or 'mxfp4', not {fmt!r}")
+    return MOE_WEIGHTS_MXFP8
 
 
 def mx_quantize(X, fmt, codes=None, scales=None, stream=None):
     """[rows, K] or [slices, rows, K] bf16 or fp32 -> element codes and block scales (uint8) in
     the layout of the block's MX weights: codes [.., rows, K] (mxfp8) or [.., rows, K / 2]
     (mxfp4), scales [.., K / 32, rows]."""
-    import torch
+    torch = _t()
     code = _mx_format(fmt)
-    (slices, rows, K), cshape, sshape = _mx_shapes(X.shape, fmt)
-    device, dtype = X.device, _dtype_code(X.dtype)
-    _tensor(X, "X", X.shape, X.dtype, device)
-    raw, undo = _enter(device, stream)
+    shape = X.shape
+    _need(len(shape) in (2, 3), "the tensor must be [rows, K] or [slices, rows, K]")
+    *lead, rows, K = shape
+    per = K if code == MOE_WEIGHTS_MXFP8 else K // 2
+    index, dtype = X.get_device(), _dtype_code(X.dtype)
+    _tensor(X, "X", shape, X.dtype, index)
+    raw, undo = _enter(index, stream)
     try:
         if codes is None:
-            codes = torch.empty(cshape, dtype=torch.uint8, device=device)
+            codes = torch.empty((*lead, rows, per), dtype=torch.uint8, device=X.device)
         else:
-            _tensor(codes, "codes", cshape, torch.uint8, device)
+            _tensor(codes, "codes", (*lead, rows, per), torch.uint8, index)
         if scales is None:
-            scales = torch.empty(sshape, dtype=torch.uint8, device=device)
+            scales = torch.empty((*lead, K // 32, rows), dtype=torch.uint8, device=X.device)
         else:
-            _tensor(scales, "scales", sshape, torch.uint8, device)
-        status = load().moe_mx_quantize(X.data_ptr(), dtype, slices, rows, K, code, codes.data_ptr(), scales.data_ptr(), raw)
+            _tensor(scales, "scales", (*lead, K // 32, rows), torch.uint8, index)
+        status = _lib.moe_mx_quantize(X.data_ptr(), dtype, lead[0] if lead else 1, rows, K, code, codes.data_ptr(),
+                                      scales.data_ptr(), raw)
     finally:
         _leave(undo)
     check(status, "moe_mx_quantize")
@@ -437,20 +440,24 @@ def mx_quantize(X, fmt, codes=None, scales=None, stream=None):
 
 def mx_dequantize(codes, scales, fmt, dtype=None, out=None, stream=None):
     """The values of mx_quantize's codes and scales as dtype (bf16 by default)."""
-    import torch
+    torch = _t()
     code = _mx_format(fmt)
-    shape = tuple(codes.shape[:-1]) + (codes.shape[-1] * (1 if fmt == "mxfp8" else 2),)
-    (slices, rows, K), cshape, sshape = _mx_shapes(shape, fmt)
-    _tensor(codes, "codes", cshape, torch.uint8, codes.device)
-    _tensor(scales, "scales", sshape, torch.uint8, codes.device)
-    raw, undo = _enter(codes.device, stream)
+    shape = codes.shape
+    _need(len(shape) in (2, 3), "the tensor must be [rows, K] or [slices, rows, K]")
+    *lead, rows, K = shape
+    if code == MOE_WEIGHTS_MXFP4:
+        K *= 2
+    index = codes.get_device()
+    _tensor(codes, "codes", shape, torch.uint8, index)
+    _tensor(scales, "scales", (*lead, K // 32, rows), torch.uint8, index)
+    raw, undo = _enter(index, stream)
     try:
         if out is None:
-            out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=codes.device)
+            out = torch.empty((*lead, rows, K), dtype=dtype or torch.bfloat16, device=codes.device)
         else:
-            _tensor(out, "out", shape, dtype or out.dtype, codes.device)
-        status = load().moe_mx_dequantize(codes.data_ptr(), scales.data_ptr(), code, slices, rows, K,
-                                          _dtype_code(out.dtype), out.data_ptr(), raw)
+            _tensor(out, "out", (*lead, rows, K), dtype or out.dtype, index)
+        status = _lib.moe_mx_dequantize(codes.data_ptr(), scales.data_ptr(), code, lead[0] if lead else 1, rows, K,
+                                        _dtype_code(out.dtype), out.data_ptr(), raw)
     finally:
         _leave(undo)
     check(status, "moe_mx_dequantize")
@@ -462,25 +469,24 @@ def mx_grouped_forward(Xc, Xs, Wc, Ws, offs, out=None, out_dtype=None, stream=No
     Ws [E, K / 32, N] uint8 as mx_quantize gives them, offs [E + 1] int32.  Returns out (default:
     a new [rows, N] tensor of out_dtype, bf16 by default), whose rows outside
     [offs[0], offs[E]) are left as they were."""
-    import torch
-    _need(Wc.dim() == 3, "Wc must be [E, N, K / 2]")
+    torch = _t()
+    _need(Wc.dim() == 3 and Xc.dim() == 2, "Wc must be [E, N, K / 2] and Xc [rows, K / 2]")
     E, N, half = Wc.shape
-    K = 2 * half
-    _tensor(Wc, "Wc", (E, N, half), torch.uint8, Xc.device)
-    _tensor(Ws, "Ws", (E, K // 32, N), torch.uint8, Xc.device)
-    _need(Xc.dim() == 2, "Xc must be [rows, K / 2]")
-    rows = Xc.shape[0]
-    _tensor(Xc, "Xc", (rows, half), torch.uint8, Xc.device)
-    _tensor(Xs, "Xs", (K // 32, rows), torch.uint8, Xc.device)
-    _tensor(offs, "offs", (E + 1,), torch.int32, Xc.device)
-    raw, undo = _enter(Xc.device, stream)
+    rows, K = Xc.shape[0], 2 * half
+    index, u8 = Xc.get_device(), torch.uint8
+    _tensor(Xc, "Xc", (rows, half), u8, index)
+    _tensor(Xs, "Xs", (K // 32, rows), u8, index)
+    _tensor(Wc, "Wc", (E, N, half), u8, index)
+    _tensor(Ws, "Ws", (E, K // 32, N), u8, index)
+    _tensor(offs, "offs", (E + 1,), torch.int32, index)
+    raw, undo = _enter(index, stream)
     try:
         if out is None:
             out = torch.empty((rows, N), dtype=out_dtype or torch.bfloat16, device=Xc.device)
         else:
-            _tensor(out, "out", (rows, N), out_dtype or out.dtype, Xc.device)
-        status = load().moe_mx_grouped_forward(Xc.data_ptr(), Xs.data_ptr(), Wc.data_ptr(), Ws.data_ptr(), offs.data_ptr(),
-                                               rows, E, N, K, _dtype_code(out.dtype), out.data_ptr(), raw)
+            _tensor(out, "out", (rows, N), out_dtype or out.dtype, index)
+        status = _lib.moe_mx_grouped_forward(Xc.data_ptr(), Xs.data_ptr(), Wc.data_ptr(), Ws.data_ptr(), offs.data_ptr(),
+                                             rows, E, N, K, _dtype_code(out.dtype), out.data_ptr(), raw)
     finally:
         _leave(undo)
     check(status, "moe_mx_grouped_forward")
@@ -496,35 +502,38 @@ def clip_grad_norm(grads, max_norm, out=None, stream=None):
     fp32 tensor, and the gradients times min(1, max_norm / norm): in place, or into the
     tensors `out`.  If a gradient holds an infinity or a NaN the norm says so and the
     gradients are passed on as they are."""
-    import torch
+    torch = _t()
+    T = torch.Tensor
     grads = list(grads)
-    out = grads if out is None else list(out)
-    _need(len(grads) > 0, "clip_grad_norm needs at least one gradient")
-    _need(len(out) == len(grads), "out must have a tensor for each gradient")
-    device = grads[0].device
-    both = grads if out is grads else grads + out
-    _need(device.type == "cuda" and set(map(torch.Tensor.get_device, both)) == {device.index},
-          "the gradients must be on one CUDA device")
-    _need(all(map(torch.Tensor.is_contiguous, both)), "the gradients must be contiguous")
-    types = [g.dtype for g in grads]
-    counts = list(map(torch.Tensor.numel, grads))
-    _need(set(types) <= {torch.bfloat16, torch.float32}, "the gradients must be bfloat16 or float32")
-    _need(out is grads or (types == [o.dtype for o in out] and counts == list(map(torch.Tensor.numel, out))),
-          "out must have the gradients' types and sizes")
     n = len(grads)
+    _need(n > 0, "clip_grad_norm needs at least one gradient")
+    index = grads[0].get_device()
+    types, counts = [g.dtype for g in grads], list(map(T.numel, grads))
+    both, src = grads, list(map(T.data_ptr, grads))
+    dst = src
+    if out is not None:
+        out = list(out)
+        _need(len(out) == n, "out must have a tensor for each gradient")
+        _need([o.dtype for o in out] == types and list(map(T.numel, out)) == counts,
+              "out must have the gradients' types and sizes")
+        both, dst = grads + out, list(map(T.data_ptr, out))
+    _need(index >= 0 and set(map(T.get_device, both)) == {index}, "the gradients must be on one CUDA device")
+    _need(all(map(T.is_contiguous, both)), "the gradients must be contiguous")
+    code = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
+    kinds = set(types)
+    _need(kinds <= code.keys(), "the gradients must be bfloat16 or float32")
     flat = [0] * (5 * n)  # an array of moe_grad: grad, out, count, dtype and its padding
-    flat[0::5] = src = list(map(torch.Tensor.data_ptr, grads))
-    flat[1::5] = src if out is grads else map(torch.Tensor.data_ptr, out)
-    flat[2::5] = counts
-    flat[3::5] = [int(t is torch.float32) for t in types]
+    flat[0::5], flat[1::5], flat[2::5] = src, dst, counts
+    flat[3::5] = [code[types[0]]] * n if len(kinds) == 1 else map(code.__getitem__, types)
     table = struct.pack("@" + "PPqii" * n, *flat)
     need = ctypes.c_size_t()
-    check(load().moe_clip_workspace(n, ctypes.byref(need)), "moe_clip_workspace")
-    raw, undo = _enter(device, stream)
+    check(_lib.moe_clip_workspace(n, ctypes.byref(need)), "moe_clip_workspace")
+    raw, undo = _enter(index, stream)
     try:
+        device = grads[0].device
         norm = torch.empty((), dtype=torch.float32, device=device)
         work = torch.empty(need.value, dtype=torch.uint8, device=device)
-        status = load().moe_clip_grad_norm(table, n, max_norm, norm.data_ptr(), work.data_ptr(), need.value, raw)
+        status = _lib.moe_clip_grad_norm(table, n, max_norm, norm.data_ptr(), work.data_ptr(), need.value, raw)
     finally:
         _leave(undo)
     check(status, "moe_clip_grad_norm")
