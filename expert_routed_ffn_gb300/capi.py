@@ -109,6 +109,7 @@ def load():
     L.moe_get_stage_name.restype = ctypes.c_char_p
     L.moe_dispatch_noalloc.argtypes = [P, I, I, I, P, P, P, P, P]
     L.moe_operators_status.argtypes = []
+    L.moe_operators_wait_limit.argtypes = [LL]
     L.moe_grouped_forward.argtypes = [P, P, P, I, I, I, I, I, P, P]
     L.moe_grouped_dgrad.argtypes = [P, P, P, I, I, I, I, I, P, P]
     L.moe_grouped_wgrad.argtypes = [P, P, P, I, I, I, I, I, I, P, P]
@@ -120,7 +121,7 @@ def load():
     L.moe_clip_grad_norm.argtypes = [P, I, ctypes.c_float, P, P, SZ, P]
     for name in ("moe_create", "moe_route", "moe_forward", "moe_forward_host", "moe_sync_status", "moe_dispatch_noalloc",
                  "moe_set_option", "moe_get_stats", "moe_inspect", "moe_get_stage_times", "moe_get_trace",
-                 "moe_operators_status", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad", "moe_mx_quantize",
+                 "moe_operators_status", "moe_operators_wait_limit", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad", "moe_mx_quantize",
                  "moe_mx_dequantize", "moe_mx_grouped_forward", "moe_clip_workspace", "moe_clip_grad_norm"):
         getattr(L, name).restype = I
     _lib = L

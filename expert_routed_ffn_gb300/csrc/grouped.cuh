@@ -18,8 +18,8 @@ namespace moe {
 
 constexpr int kMaxExperts = 256;
 constexpr int kQuads = 4;              // TMEM lane quadrants, of 32 lanes
-constexpr long long kWaitCycles = 4000000000ll;         // bound of every wait (about 2 s)
-constexpr unsigned long long kPairDrainNs = 1000000ull; // grace for the copies in flight after an abort
+constexpr long long kDrainCycles = 2000000000ll;  // after an abort: bound of the wait for the MMAs issued
+constexpr unsigned long long kGraceNs = 1000000ull;  // and the time given to the copies in flight
 
 // The output and its tiles.  Row-grouped (forward, dgrad): out [rows, n_out], the rows of
 // expert e are [offs[e], offs[e + 1]).  Dense (wgrad): out [E, m_dense, n_out], and the
@@ -37,6 +37,7 @@ struct GroupedOut {
     int col_tiles;   // tiles along the output columns
     int row_tiles;   // dense: tiles along m_dense
     int f32;         // output type: fp32, else bf16
+    long long wait;  // bound of every wait in SM cycles, see wait_cycles
 };
 
 struct Tile {
@@ -54,18 +55,25 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// About 2 s, and what the longest sum may take: the epilogue waits for all of a tile's stages.
+// moe_operators_wait_limit replaces it.
+inline long long wait_cycles(long long stages_per_tile) {
+    const long long limit = op_wait_limit();
+    return limit >= 0 ? limit : 4000000000ll + 4096 * stages_per_tile;
+}
+
 // Wait until the phase of parity `parity` of a barrier has completed; CLUSTER: a barrier that
 // threads of the other CTA arrive on.  Bounded by the SM's clock (the global timer is slow to
 // read beside waits this short).  False after the bound, or once *abort is set.
 template <bool CLUSTER = false>
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort) {
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, long long limit, volatile int *abort) {
     auto done = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
     if (done()) return true;
     const long long t0 = clock64();
     for (;;) {
         if (done()) return true;
         if (abort != nullptr && *abort) return false;
-        if (clock64() - t0 > kWaitCycles) return false;
+        if (clock64() - t0 > limit) return false;
     }
 }
 
@@ -76,6 +84,20 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
 // warp's outstanding stores and loads: about 2000 cycles per tile, or per stage of scales.
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// The end of both kernels, by all threads: no arrival, MMA or copy of the pair outlives either
+// CTA.  After an abort a stage's copies may never complete their barrier together, so those in
+// flight are given a fixed time.
+__device__ __forceinline__ void leave_pair(volatile int *abort) {
+    tc_fence_before();
+    __syncthreads();
+    if (*abort) {
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < kGraceNs) __nanosleep(1000);
+    }
+    __syncthreads();
+    cluster_sync();
 }
 
 // One lane of a converged warp.  The roles that issue copies and MMAs run their loops on the

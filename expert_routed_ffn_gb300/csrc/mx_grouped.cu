@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
             const CUtensorMap *map_b = &p.map_b[t.n / 32 - 1];
             const uint32_t bytes = a_stage + (t.n / 2) * kRow;
             for (int k = 0; k < k_stages; ++k) {
-                if (!__all_sync(0xffffffffu, wait_bar(empty_bar(s), ph, abort_flag))) {
+                if (!__all_sync(0xffffffffu, wait_bar(empty_bar(s), ph, p.o.wait, abort_flag))) {
                     ok = false;
                     break;
                 }
@@ -209,13 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
                 }
             }
         }
-        if (!ok && lane == 0) {
-            raise();
-            // a stage's copies complete together with the other CTA's, which an abort may have
-            // kept from being issued: wait a fixed time for the copies in flight instead
-            const uint64_t t0 = global_timer_ns();
-            while (global_timer_ns() - t0 < kPairDrainNs) __nanosleep(1000);
-        }
+        if (!ok && lane == 0) raise();
     } else if (warp == 1) {
         if (leader) {
             const uint32_t acc_cols = tab.o.tile_rows;
@@ -232,13 +226,13 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
                 const Tile t = next;
                 const uint32_t idesc = idesc_mxf4(256, t.n);
                 const uint32_t a = n_acc & 1u, d = tmem_base + a * acc_cols;
-                if (!__all_sync(0xffffffffu, wait_bar<true>(tempty_bar(a), ((n_acc >> 1) & 1u) ^ 1u, abort_flag))) {
+                if (!__all_sync(0xffffffffu, wait_bar<true>(tempty_bar(a), ((n_acc >> 1) & 1u) ^ 1u, p.o.wait, abort_flag))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 for (int k = 0; k < k_stages; ++k) {
-                    if (!__all_sync(0xffffffffu, wait_bar<true>(full_bar(s), ph, abort_flag))) {
+                    if (!__all_sync(0xffffffffu, wait_bar<true>(full_bar(s), ph, p.o.wait, abort_flag))) {
                         ok = false;
                         break;
                     }
@@ -282,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
                 raise();
                 if (issued) {
                     tc_commit_pair(drain_bar, 1);
-                    wait_bar(drain_bar, 0, nullptr);
+                    wait_bar(drain_bar, 0, kDrainCycles, nullptr);
                 }
             }
         }
@@ -292,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
         for (TileWalk<false> walk(tab, first, stride); walk.more(); walk.next(), ++n_acc) {
             const Tile t = walk.get();
             const uint32_t a = n_acc & 1u;
-            if (!__all_sync(0xffffffffu, wait_bar<true>(tfull_bar(a), (n_acc >> 1) & 1u, abort_flag))) {
+            if (!__all_sync(0xffffffffu, wait_bar<true>(tfull_bar(a), (n_acc >> 1) & 1u, p.o.wait, abort_flag))) {
                 if (lane == 0) raise();
                 break;
             }
@@ -327,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
             const uint8_t *xs = p.xs + (at & ~(size_t)3) + w0;
             const int x_bytes = (int)(at & 3) + t.rows - w0;  // of the run from this thread's first word on
             for (int b0 = 0; b0 < n_blocks; b0 += kFetchBlocks) {
-                if (!__all_sync(0xffffffffu, wait_bar(raw_empty_bar(raw), ph, abort_flag))) {
+                if (!__all_sync(0xffffffffu, wait_bar(raw_empty_bar(raw), ph, p.o.wait, abort_flag))) {
                     ok = false;
                     break;
                 }
@@ -372,12 +366,12 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
             const Tile t = walk.get();
             for (int k = 0; k < k_stages; ++k) {
                 const int f = k % kFetchStages;
-                if (f == 0 && !__all_sync(0xffffffffu, wait_bar(raw_full_bar(raw), raw_ph, abort_flag))) {
+                if (f == 0 && !__all_sync(0xffffffffu, wait_bar(raw_full_bar(raw), raw_ph, p.o.wait, abort_flag))) {
                     ok = false;
                     break;
                 }
                 if (k % kSets == set) {
-                    if (!__all_sync(0xffffffffu, wait_bar(empty_bar(s), ph, abort_flag))) {
+                    if (!__all_sync(0xffffffffu, wait_bar(empty_bar(s), ph, p.o.wait, abort_flag))) {
                         ok = false;
                         break;
                     }
@@ -431,9 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
         if (!ok && lane == 0) raise();
     }
 
-    tc_fence_before();
-    __syncthreads();
-    cluster_sync();  // no arrival or MMA of the pair outlives either CTA
+    leave_pair(abort_flag);
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
@@ -493,6 +485,7 @@ extern "C" moe_status moe_mx_grouped_forward(const void *Xc, const uint8_t *Xs, 
     o.n_out = N;
     o.red = K;
     o.f32 = out_dtype == MOE_DTYPE_F32;
+    o.wait = wait_cycles(K / kBK + 1);
     g.xs = Xs;
     g.ws = Ws;
     choose_tiles(g, sms);

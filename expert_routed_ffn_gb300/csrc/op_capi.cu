@@ -1,6 +1,7 @@
 // Host helpers of the stateless operators, and their device error word: the
 // bounded waits and offset checks of the grouped products record failures in one
 // word per device, which moe_operators_status() reads and clears.
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -21,6 +22,7 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
 constexpr int kMaxDevices = 64;
 std::mutex g_mutex;
 int g_sms[kMaxDevices];
+std::atomic<long long> g_wait_limit{-1};
 
 }  // namespace
 
@@ -84,12 +86,20 @@ CUresult op_encode(CUtensorMap *m, const OpMap &d) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+long long op_wait_limit() { return g_wait_limit.load(std::memory_order_relaxed); }
+
 int *op_error_word() {
     void *p = nullptr;
     return cudaGetSymbolAddress(&p, g_op_error) == cudaSuccess ? static_cast<int *>(p) : nullptr;
 }
 
 }  // namespace moe
+
+extern "C" moe_status moe_operators_wait_limit(long long cycles) {
+    if (cycles < -1) return moe::op_fail(MOE_ERR_INVALID_ARG, "moe_operators_wait_limit: need cycles >= -1");
+    moe::g_wait_limit.store(cycles, std::memory_order_relaxed);
+    return MOE_OK;
+}
 
 extern "C" moe_status moe_operators_status(void) {
     using namespace moe;

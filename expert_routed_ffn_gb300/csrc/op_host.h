@@ -41,6 +41,9 @@ struct OpMap {
 };
 CUresult op_encode(CUtensorMap *m, const OpMap &d);
 
+// The bound set with moe_operators_wait_limit, -1: none.
+long long op_wait_limit();
+
 // Device address of the operators' error word (op_capi.cu) on the current device.
 int *op_error_word();
 

@@ -378,6 +378,12 @@ moe_status moe_dispatch_noalloc(const int32_t *topk_idx, int T, int k, int E, in
  * stream capture. */
 moe_status moe_operators_status(void);
 
+/* Bound of the device-side waits of the grouped products launched from now on, in SM clock
+ * cycles, for the whole process: -1 (the start) is about 2 s and more for very long sums; 0
+ * makes the first wait that finds its data not ready give up, which exercises the timeout
+ * path.  Errors: INVALID_ARG. */
+moe_status moe_operators_wait_limit(long long cycles);
+
 /* Grouped products.  X [rows, K], dY [rows, N] and W [E, N, K] are bf16; out_dtype
  * (moe_dtype) is the type of the result, bf16 or fp32.  Sums are fp32, rounded once.
  * Limits: 1 <= E <= 256; N and K multiples of 8, up to 2^20; rows up to 2^30, else

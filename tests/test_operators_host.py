@@ -94,3 +94,8 @@ MX_GROUPED = {"Xc": FAKE, "Xs": FAKE, "Wc": FAKE, "Ws": FAKE, "offs": FAKE, "row
 def test_mx_grouped_refusals(lib, change, status):
     a = {**MX_GROUPED, **change}
     assert lib.moe_mx_grouped_forward(*a.values(), None) == status
+
+
+def test_wait_limit_refuses_what_is_no_bound(lib):
+    assert lib.moe_operators_wait_limit(-2) == capi.MOE_ERR_INVALID_ARG
+    assert lib.moe_operators_wait_limit(-1) == capi.MOE_OK
