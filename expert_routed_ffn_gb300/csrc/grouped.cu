@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
             const uint64_t desc_b = kDense ? smem_desc_mn128(sB) : smem_desc_k128(sB);
             uint32_t n_acc = 0, ph = 0, zeroed_ph = 0;
             int s = 0;
-            bool ok = true, issued = false;
+            bool ok = p.o.wait != 0, issued = false;  // a bound of 0: give up at once
             TileWalk<kDense> walk(tab, first, stride);
             Tile next;
             auto advance = [&]() {

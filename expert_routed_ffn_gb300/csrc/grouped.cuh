@@ -62,25 +62,14 @@ inline long long wait_cycles(long long stages_per_tile) {
     return limit >= 0 ? limit : 4000000000ll + 4096 * stages_per_tile;
 }
 
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 // Wait until the phase of parity `parity` of a barrier has completed; CLUSTER: a barrier that
 // threads of the other CTA arrive on.  Bounded by the SM's clock (the global timer is slow to
-// read beside waits this short).  False after the bound, or once *abort is set.
+// read beside waits this short).  False after the bound, or once *abort is set.  (A try may
+// suspend the thread for a while, so a bound of 0 is not seen here: the MMA's role gives up at
+// its first wait then.  Checked in every wait it cost up to 70 cycles a stage.)
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, long long limit, volatile int *abort) {
     auto done = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
-    if (limit == 0) return mbar_test(bar, parity);  // one look: a try may suspend the thread for long
     if (done()) return true;
     const long long t0 = clock64();
     for (;;) {

@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
             const uint64_t desc_a = smem_desc_k128(sA), desc_b = smem_desc_k128(sB), desc_s = scale_desc(sS);
             uint32_t n_acc = 0, ph = 0;
             int s = 0;
-            bool ok = true, issued = false;
+            bool ok = p.o.wait != 0, issued = false;  // a bound of 0: give up at once
             TileWalk<false> walk(tab, first, stride);
             Tile next;
             if (walk.more()) next = walk.get();
@@ -435,15 +435,19 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
 
 unsigned long long g_attr;
 
-// Tile sizes, as the bf16 products': rows up to 192, fewer where the experts average fewer;
-// 256 columns, or 128 where 256 would leave SMs without a tile.
+// Tile sizes, by the bf16 products' rule: rows up to 192, fewer where the experts average fewer;
+// 256 columns, or 128 where 256 would leave CTA pairs without a tile; where there still are not
+// half as many tiles as pairs and the experts' rows fill them, tiles of fewer rows, down to 64.
 void choose_tiles(MxGroupedArgs &g, int sms) {
     GroupedOut &o = g.o;
-    const long long active = std::max<long long>(1, std::min(o.E, o.rows)), most = 2 * (o.rows / active) + 1;
+    const long long pairs = sms / 2, active = std::max<long long>(1, std::min(o.E, o.rows)), fill = o.rows / active;
+    const long long most = 2 * fill + 1;
     o.tile_rows = most <= 32 ? 32 : most <= 64 ? 64 : most <= 128 ? 128 : kMaxRows;
-    const long long row_tiles = std::max<long long>(active, o.rows / o.tile_rows);
-    o.cols = (o.n_out + 255) / 256 * row_tiles >= sms / 2 && o.n_out > 128 ? 256 : 128;
+    auto row_tiles = [&] { return std::max<long long>(active, o.rows / o.tile_rows); };
+    o.cols = (o.n_out + 255) / 256 * row_tiles() >= pairs && o.n_out > 128 ? 256 : 128;
     o.col_tiles = (o.n_out + o.cols - 1) / o.cols;
+    while (o.tile_rows > 64 && 2 * fill >= o.tile_rows && 2 * row_tiles() * o.col_tiles <= pairs)
+        o.tile_rows = (o.tile_rows / 2 + 31) / 32 * 32;
     g.a_stage = o.cols / 2 * kRow;
     g.b_stage = o.tile_rows / 2 * kRow;
     g.atoms = (o.tile_rows + 127) / 128;

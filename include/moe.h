@@ -380,8 +380,8 @@ moe_status moe_operators_status(void);
 
 /* Bound of the device-side waits of the grouped products launched from now on, in SM clock
  * cycles, for the whole process: -1 (the start) is about 2 s and more for very long sums; 0
- * makes the first wait that finds its data not ready give up, which exercises the timeout
- * path.  Errors: INVALID_ARG. */
+ * makes the products give up at their first wait for data, which exercises the timeout path.
+ * Errors: INVALID_ARG. */
 moe_status moe_operators_wait_limit(long long cycles);
 
 /* Grouped products.  X [rows, K], dY [rows, N] and W [E, N, K] are bf16; out_dtype

@@ -1,5 +1,5 @@
-"""The grouped products' bounded waits, without a GPU fault: with the bound set to 0 the first
-wait that finds its data not ready gives up; the kernel records the timeout, lets its copies and
+"""The grouped products' bounded waits, without a GPU fault: with the bound set to 0 the
+products give up at their first wait, with copies in flight; the kernel records the timeout, lets its copies and
 products end, frees its tensor memory and returns, and the next call is right again."""
 
 import pytest
