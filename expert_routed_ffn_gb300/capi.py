@@ -320,6 +320,7 @@ def _enter(index, stream):
     torch = _torch
     if stream is None and torch._C._cuda_getDevice() == index:
         return torch._C._cuda_getCurrentRawStream(index), None
+    _need(index >= 0 and (stream is None or stream.device_index == index), "the stream must be of the tensors' device")
     undo = contextlib.ExitStack()
     undo.enter_context(torch.cuda.device(index))
     if stream is not None:

@@ -392,14 +392,10 @@ moe_status check(const char *op, const void *a, const void *b, const int32_t *of
 // x: X or dY [rows, ..]; w: W [E, N, K], or X for the wgrad
 moe_status launch(const char *name, int op, const void *x, const void *w, const int32_t *offs, void *out, int rows, int E,
                   int N, int K, int dtype, int accumulate, moe_stream_t stream) {
-    const int sms = op_num_sms();
-    int *err = op_error_word();
-    if (sms < 2 || err == nullptr) return op_fail(MOE_ERR_CUDA, "%s: no usable current device", name);
     GroupedArgs g = {};
     GroupedOut &o = g.o;
     o.offs = offs;
     o.out = out;
-    o.err = err;
     o.E = E;
     o.rows = rows;
     o.n_out = op == kForward ? N : K;
@@ -407,14 +403,22 @@ moe_status launch(const char *name, int op, const void *x, const void *w, const 
     o.red = op == kForward ? K : N;
     o.f32 = dtype == MOE_DTYPE_F32;
     o.wait = wait_cycles((op == kWgrad ? rows : o.red) / kBK + 1);
+    const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    const uint64_t n = N, k = K, r = rows, e = E;
+    const uint64_t x_bytes = 2 * r * (op == kForward ? k : n), w_bytes = 2 * (op == kWgrad ? r * k : e * n * k);
+    const uint64_t out_bytes = (o.f32 ? 4 : 2) * (op == kWgrad ? e * n * k : r * (uint64_t)o.n_out);
+    if (op_overlap(out, out_bytes, x, x_bytes) || op_overlap(out, out_bytes, w, w_bytes) ||
+        op_overlap(out, out_bytes, offs, 4 * (e + 1)))
+        return op_fail(MOE_ERR_INVALID_ARG, "%s: the output overlaps an input", name);
+    const int sms = op_num_sms();
+    o.err = op_error_word();
+    if (sms < 2 || o.err == nullptr) return op_fail(MOE_ERR_CUDA, "%s: no usable current device", name);
     choose_tiles(g, op, sms);
     const long long tiles = op == kWgrad ? (long long)E * o.row_tiles * o.col_tiles
                                          : ((long long)rows / o.tile_rows + std::min(E, rows)) * o.col_tiles;
     if (tiles > (1ll << 30)) return op_fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^30 output tiles", name);
 
-    const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
-    const uint64_t n = N, k = K, r = rows, e = E;
     CUresult cr;
     if (op == kWgrad) {
         cr = op_encode(&g.map_a, {bf, 2, w, {k, r}, {k * 2}, {64, kBK}, sw});

@@ -476,6 +476,10 @@ extern "C" moe_status moe_mx_grouped_forward(const void *Xc, const uint8_t *Xs, 
         (reinterpret_cast<uintptr_t>(offs) & 3u))
         return op_fail(MOE_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned, the offsets 4-byte aligned", op);
     if (rows == 0) return MOE_OK;
+    const uint64_t n = N, c = K / 2, b = K / 32, r = rows, e = E, y_bytes = (out_dtype == MOE_DTYPE_F32 ? 4 : 2) * r * n;
+    if (op_overlap(Y, y_bytes, Xc, r * c) || op_overlap(Y, y_bytes, Xs, r * b) || op_overlap(Y, y_bytes, Wc, e * n * c) ||
+        op_overlap(Y, y_bytes, Ws, e * n * b) || op_overlap(Y, y_bytes, offs, 4 * (e + 1)))
+        return op_fail(MOE_ERR_INVALID_ARG, "%s: the output overlaps an input", op);
     const int sms = op_num_sms();
     int *err = op_error_word();
     if (sms < 2 || err == nullptr) return op_fail(MOE_ERR_CUDA, "%s: no usable current device", op);
@@ -497,7 +501,6 @@ extern "C" moe_status moe_mx_grouped_forward(const void *Xc, const uint8_t *Xs, 
     if (tiles > (1ll << 30)) return op_fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^30 output tiles", op);
     const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
-    const uint64_t n = N, c = K / 2, r = rows, e = E;
     CUresult cr = op_encode(&g.map_a, {u8, 3, Wc, {c, n, e}, {c, n * c}, {kRow, (uint32_t)o.cols / 2, 1}, sw});
     for (int i = 0; i < o.tile_rows / 32 && cr == CUDA_SUCCESS; ++i)
         cr = op_encode(&g.map_b[i], {u8, 2, Xc, {c, r}, {c}, {kRow, 16u * (i + 1)}, sw});

@@ -245,6 +245,11 @@ moe_status check(const char *op, const void *x, int dtype, int slices, int rows,
     if (!x || !codes || !scales) return op_fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", op);
     if (!op_aligned16(x) || !op_aligned16(codes) || !op_aligned16(scales))
         return op_fail(MOE_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", op);
+    const uint64_t n = (uint64_t)slices * rows * K, x_bytes = n * (dtype == MOE_DTYPE_F32 ? 4 : 2);
+    const uint64_t c_bytes = format == MOE_WEIGHTS_MXFP8 ? n : n / 2;
+    if (op_overlap(x, x_bytes, codes, c_bytes) || op_overlap(x, x_bytes, scales, n / 32) ||
+        op_overlap(codes, c_bytes, scales, n / 32))
+        return op_fail(MOE_ERR_INVALID_ARG, "%s: tensors overlap", op);
     return MOE_OK;
 }
 

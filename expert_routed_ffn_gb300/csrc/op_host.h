@@ -21,6 +21,12 @@ moe_status op_cuda(cudaError_t e, const char *op);
 
 inline bool op_aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Whether two buffers share bytes.
+inline bool op_overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
+    const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return na && nb && x < y + nb && y < x + na;
+}
+
 // SM count of the current device (looked up once per device), or 0 after an error.
 int op_num_sms();
 

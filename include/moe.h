@@ -387,7 +387,7 @@ moe_status moe_operators_wait_limit(long long cycles);
 /* Grouped products.  X [rows, K], dY [rows, N] and W [E, N, K] are bf16; out_dtype
  * (moe_dtype) is the type of the result, bf16 or fp32.  Sums are fp32, rounded once.
  * Limits: 1 <= E <= 256; N and K multiples of 8, up to 2^20; rows up to 2^30, else
- * MOE_ERR_UNSUPPORTED.  The output must not overlap an input.
+ * MOE_ERR_UNSUPPORTED.  An output that overlaps an input is refused.
  *   forward: Y [rows, N],  Y[r, :]  = W[e] X[r, :]
  *   dgrad:   dX [rows, K], dX[r, :] = W[e]^T dY[r, :]
  *   wgrad:   dW [E, N, K], dW[e]    = sum over e's rows of dY[r, :] X[r, :]^T, added to
@@ -409,7 +409,7 @@ moe_status moe_grouped_wgrad(const void *dY, const void *X, const int32_t *offs,
  * the scale byte is max(floor(log2 max|x|) - emax + 127, 0) (emax 8 for E4M3, 2 for
  * E2M1) and the elements are rounded to nearest, ties to even, and saturated; a block
  * that holds an infinity or a NaN gets scale 255 (NaN) and zero codes.  K must be a
- * multiple of 32.  slices == 0 or rows == 0 is a no-op.
+ * multiple of 32; tensors that overlap are refused.  slices == 0 or rows == 0 is a no-op.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 moe_status moe_mx_quantize(const void *X, int dtype, int slices, int rows, int K, int format, void *codes,
                            uint8_t *scales, moe_stream_t stream);

@@ -99,3 +99,30 @@ def test_mx_grouped_refusals(lib, change, status):
 def test_wait_limit_refuses_what_is_no_bound(lib):
     assert lib.moe_operators_wait_limit(-2) == capi.MOE_ERR_INVALID_ARG
     assert lib.moe_operators_wait_limit(-1) == capi.MOE_OK
+
+
+def _at(byte):
+    return ctypes.c_void_p((1 << 30) + byte)
+
+
+def test_outputs_that_overlap_inputs_are_refused(lib):
+    """16 rows, E 4, N = K = 64, bf16: rows are 2 KB, the weights 32 KB; the offsets 20 bytes."""
+    far, offs = _at(1 << 20), _at(1 << 21)
+    for op, sizes in (("forward", (2048, 32768, 2048)), ("dgrad", (2048, 32768, 2048)), ("wgrad", (2048, 2048, 32768))):
+        tail = [0] if op == "wgrad" else []
+        for a, b, o, out in ((_at(0), far, offs, _at(sizes[0] - 16)), (far, _at(0), offs, _at(sizes[1] - 16)),
+                             (_at(sizes[2] - 16), far, offs, _at(0)), (far, _at(1 << 22), _at(16), _at(0))):
+            args = [a, b, o, 16, 4, 64, 64, 0, *tail, out, None]
+            assert getattr(lib, f"moe_grouped_{op}")(*args) == capi.MOE_ERR_INVALID_ARG
+            assert "overlaps" in lib.moe_last_error().decode()
+    # Xc 512 bytes, Xs 32, Wc 8 KB, Ws 512, Y 2 KB
+    good = [far, _at(2 << 20), _at(3 << 20), _at(4 << 20), offs]
+    for i, size in enumerate((512, 32, 8192, 512, 20)):
+        args = list(good)
+        args[i] = _at(0)
+        assert lib.moe_mx_grouped_forward(*args, 16, 4, 64, 64, 0, _at(size - size % 16 - 16 if size > 16 else 0), None) == capi.MOE_ERR_INVALID_ARG
+        assert "overlaps" in lib.moe_last_error().decode()
+    # 2 x 16 x 64 bf16 values: X 4 KB, codes 1 KB, scales 64 bytes
+    for X, codes, scales in ((_at(0), _at(4080), far), (_at(0), far, _at(4080)), (far, _at(0), _at(1008))):
+        assert lib.moe_mx_quantize(X, 0, 2, 16, 64, 2, codes, scales, None) == capi.MOE_ERR_INVALID_ARG
+        assert "overlap" in lib.moe_last_error().decode()
