@@ -278,16 +278,17 @@ def block_from_inputs(shape, inputs: dict, max_tokens: int = None) -> MoeBlock:
 # tensors, on `stream` or that device's current stream, and allocates only outputs it
 # was not given.
 
-_torch = None
+_torch = _device = _raw_stream = None
 
 
 def _t():
     """torch, imported with the first operator."""
-    global _torch
+    global _torch, _device, _raw_stream
     if _torch is None:
         import torch
-        _torch = torch
         load()
+        _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        _torch = torch
     return _torch
 
 
@@ -317,15 +318,14 @@ def _tensor(t, name, shape, dtype, index):
 def _enter(index, stream):
     """(raw stream, undo): makes the tensors' device the current one and `stream` its current
     stream (so that outputs are allocated for it).  undo is None where nothing had to change."""
-    torch = _torch
-    if stream is None and torch._C._cuda_getDevice() == index:
-        return torch._C._cuda_getCurrentRawStream(index), None
+    if stream is None and _device() == index:
+        return _raw_stream(index), None
     _need(index >= 0 and (stream is None or stream.device_index == index), "the stream must be of the tensors' device")
     undo = contextlib.ExitStack()
-    undo.enter_context(torch.cuda.device(index))
+    undo.enter_context(_torch.cuda.device(index))
     if stream is not None:
-        undo.enter_context(torch.cuda.stream(stream))
-    return torch.cuda.current_stream().cuda_stream, undo
+        undo.enter_context(_torch.cuda.stream(stream))
+    return _torch.cuda.current_stream().cuda_stream, undo
 
 
 def _leave(undo):
@@ -410,30 +410,43 @@ def _mx_format(fmt):
     return MOE_WEIGHTS_MXFP8
 
 
+def _mx_shapes(shape, code, of):
+    """(slices, rows, K, the shape of codes (of 1) or values (of 2), that of scales) of a tensor of
+    values (of 1) or codes (of 2)."""
+    two = code == MOE_WEIGHTS_MXFP4
+    if len(shape) == 2:
+        rows, K = shape
+        last = (K // 2 if two else K) if of == 1 else (2 * K if two else K)
+        K = K if of == 1 else last
+        return 1, rows, K, (rows, last), (K // 32, rows)
+    _need(len(shape) == 3, "the tensor must be [rows, K] or [slices, rows, K]")
+    slices, rows, K = shape
+    last = (K // 2 if two else K) if of == 1 else (2 * K if two else K)
+    K = K if of == 1 else last
+    return slices, rows, K, (slices, rows, last), (slices, K // 32, rows)
+
+
 def mx_quantize(X, fmt, codes=None, scales=None, stream=None):
     """[rows, K] or [slices, rows, K] bf16 or fp32 -> element codes and block scales (uint8) in
     the layout of the block's MX weights: codes [.., rows, K] (mxfp8) or [.., rows, K / 2]
     (mxfp4), scales [.., K / 32, rows]."""
     torch = _t()
     code = _mx_format(fmt)
-    shape = X.shape
-    _need(len(shape) in (2, 3), "the tensor must be [rows, K] or [slices, rows, K]")
-    *lead, rows, K = shape
-    per = K if code == MOE_WEIGHTS_MXFP8 else K // 2
-    index, dtype = X.get_device(), _dtype_code(X.dtype)
-    _tensor(X, "X", shape, X.dtype, index)
+    slices, rows, K, of_codes, of_scales = _mx_shapes(X.shape, code, 1)
+    index, kind, u8 = X.get_device(), X.dtype, torch.uint8
+    dtype = _dtype_code(kind)
+    _need(index >= 0 and X.is_contiguous(), "X must be a contiguous CUDA tensor")
     raw, undo = _enter(index, stream)
     try:
         if codes is None:
-            codes = torch.empty((*lead, rows, per), dtype=torch.uint8, device=X.device)
+            codes = torch.empty(of_codes, dtype=u8, device=X.device)
         else:
-            _tensor(codes, "codes", (*lead, rows, per), torch.uint8, index)
+            _tensor(codes, "codes", of_codes, u8, index)
         if scales is None:
-            scales = torch.empty((*lead, K // 32, rows), dtype=torch.uint8, device=X.device)
+            scales = torch.empty(of_scales, dtype=u8, device=X.device)
         else:
-            _tensor(scales, "scales", (*lead, K // 32, rows), torch.uint8, index)
-        status = _lib.moe_mx_quantize(X.data_ptr(), dtype, lead[0] if lead else 1, rows, K, code, codes.data_ptr(),
-                                      scales.data_ptr(), raw)
+            _tensor(scales, "scales", of_scales, u8, index)
+        status = _lib.moe_mx_quantize(X.data_ptr(), dtype, slices, rows, K, code, codes.data_ptr(), scales.data_ptr(), raw)
     finally:
         _leave(undo)
     check(status, "moe_mx_quantize")
@@ -444,22 +457,18 @@ def mx_dequantize(codes, scales, fmt, dtype=None, out=None, stream=None):
     """The values of mx_quantize's codes and scales as dtype (bf16 by default)."""
     torch = _t()
     code = _mx_format(fmt)
-    shape = codes.shape
-    _need(len(shape) in (2, 3), "the tensor must be [rows, K] or [slices, rows, K]")
-    *lead, rows, K = shape
-    if code == MOE_WEIGHTS_MXFP4:
-        K *= 2
+    slices, rows, K, of_values, of_scales = _mx_shapes(codes.shape, code, 2)
     index = codes.get_device()
-    _tensor(codes, "codes", shape, torch.uint8, index)
-    _tensor(scales, "scales", (*lead, K // 32, rows), torch.uint8, index)
+    _need(index >= 0 and codes.is_contiguous() and codes.dtype is torch.uint8, "codes must be a contiguous uint8 CUDA tensor")
+    _tensor(scales, "scales", of_scales, torch.uint8, index)
     raw, undo = _enter(index, stream)
     try:
         if out is None:
-            out = torch.empty((*lead, rows, K), dtype=dtype or torch.bfloat16, device=codes.device)
+            out = torch.empty(of_values, dtype=dtype or torch.bfloat16, device=codes.device)
         else:
-            _tensor(out, "out", (*lead, rows, K), dtype or out.dtype, index)
-        status = _lib.moe_mx_dequantize(codes.data_ptr(), scales.data_ptr(), code, lead[0] if lead else 1, rows, K,
-                                        _dtype_code(out.dtype), out.data_ptr(), raw)
+            _tensor(out, "out", of_values, dtype or out.dtype, index)
+        status = _lib.moe_mx_dequantize(codes.data_ptr(), scales.data_ptr(), code, slices, rows, K, _dtype_code(out.dtype),
+                                        out.data_ptr(), raw)
     finally:
         _leave(undo)
     check(status, "moe_mx_dequantize")
