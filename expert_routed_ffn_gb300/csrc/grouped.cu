@@ -34,6 +34,18 @@
 // stage's copies complete on a barrier of their own CTA, and the stage is handed to the MMA
 // when both CTAs have zeroed.
 //
+// What bounds it, measured on GB300 (bf16; 64 experts, N 1408, K 2048):
+//   forward, 24576 rows    108 us, 1.31 PFLOP/s, 5.0 TB/s: the tensor pipe is 76% busy at the 1.6
+//                          GHz the SM clock settles to, and HBM 63%; the first two waves of tiles
+//                          wait for weights
+//   dgrad, 24576 rows on a few experts   112 us; of 1408 columns the sixth tile is half empty
+//   wgrad, 24576 rows, fp32 out   147 us, 6.2 TB/s: the 738 MB it writes
+//   forward, 384 rows      60 us, 6.2 TB/s: the weights, streamed once
+//   forward, one expert, 16384 rows, K 1408, N 2048   54 us, 1.75 PFLOP/s
+//   forward, one token's six experts   14 us alone, 11 us in a row of calls: start and end of the
+//                          launch, then 35 MB
+// One CTA per 128 x 256 tile with the rows as M took 128 (forward), 145 and 181 us.
+//
 // Decreasing or out-of-range offsets: every CTA sees the same, records ERR_BOUNDS and
 // writes nothing.  Every wait is bounded; on a timeout the kernel records ERR_TIMEOUT in
 // both CTAs, lets its copies and MMAs end, frees tensor memory and returns.

@@ -23,6 +23,11 @@
 //                into the words that tcgen05.cp reads
 // Tensor memory (512 columns): two accumulators of up to 192 columns, then per stage the
 // scales of the weights (8 columns) and of the tokens (8 per 128 of them).
+//
+// Measured on GB300 (64 experts, N 1408, K 2048): 24576 rows 55 us, 2.6 PFLOP/s, 3.5 TB/s; 384
+// rows 22 us, 4.5 TB/s; one expert, 8192 rows, N and K 2048: 24 us, 2.8 PFLOP/s.  No unit is
+// near its rate: without the copies of codes it takes 33 us, without the scales' way to tensor
+// memory and the products 44; the stages' hand-overs between five roles are what is left.
 #include <algorithm>
 
 #include "common.cuh"
