@@ -20,6 +20,8 @@
 // further launches), with the tensor each CTA's first block is in: no table is copied to the
 // device, a captured call owns its list, and a short list needs no search of the table, each
 // step of which can be a miss of the constant cache.
+#include <stdlib.h>
+
 #include <algorithm>
 #include <iterator>
 
@@ -351,6 +353,41 @@ moe_status run(const moe_grad *grads, int count, float max_norm, float *norm, do
     return MOE_OK;
 }
 
+// The bytes of a buffer
+struct Range {
+    uintptr_t begin, end;
+};
+bool operator<(const Range &a, const Range &b) { return a.begin < b.begin; }
+
+// Whether a result shares bytes with another result, with a gradient that is not its own, or
+// only in part with its own; or the norm or the workspace with any of them.  Blocks run in any
+// order, so such a value might be scaled twice, or be summed after it was scaled.  `r`: room
+// for `count` ranges.
+bool lists_overlap(const moe_grad *grads, int count, Range norm, Range work, Range *r) {
+    auto bytes = [](const void *p, const moe_grad &g) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        return Range{at, at + (uintptr_t)g.count * (g.dtype == MOE_DTYPE_F32 ? 4 : 2)};
+    };
+    auto meet = [](const Range &a, const Range &b) { return a.begin < b.end && b.begin < a.end; };
+    int n = 0;
+    for (int i = 0; i < count; ++i)
+        if (grads[i].count > 0) r[n++] = bytes(grads[i].out, grads[i]);
+    if (!std::is_sorted(r, r + n)) std::sort(r, r + n);
+    for (int i = 1; i < n; ++i)
+        if (r[i].begin < r[i - 1].end) return true;
+    auto meets_result = [&](const Range &x) {  // the results are disjoint: only the last that begins before x ends
+        const Range *after = std::lower_bound(r, r + n, Range{x.end, 0});
+        return after != r && after[-1].end > x.begin;
+    };
+    if (meet(norm, work) || meets_result(norm) || meets_result(work)) return true;
+    for (int i = 0; i < count; ++i) {
+        if (grads[i].count == 0 || grads[i].grad == grads[i].out) continue;
+        const Range x = bytes(grads[i].grad, grads[i]);
+        if (meet(x, norm) || meet(x, work) || meets_result(x)) return true;
+    }
+    return false;
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -380,6 +417,15 @@ extern "C" moe_status moe_clip_grad_norm(const moe_grad *grads, int count, float
         if (g.count < 0 || (g.count > 0 && (!g.grad || !g.out)) ||
             ((reinterpret_cast<uintptr_t>(g.grad) | reinterpret_cast<uintptr_t>(g.out)) & mask))
             return op_fail(MOE_ERR_INVALID_ARG, "%s: tensor %d: a NULL or misaligned pointer, or a negative count", op, i);
+    }
+    if (count > 0) {
+        Range *room = static_cast<Range *>(malloc(sizeof(Range) * (size_t)count));
+        if (room == nullptr) return op_fail(MOE_ERR_OOM, "%s: no host memory for a list of %d", op, count);
+        const uintptr_t at = reinterpret_cast<uintptr_t>(norm), w = reinterpret_cast<uintptr_t>(workspace);
+        const bool overlap = lists_overlap(grads, count, {at, at + sizeof(float)}, {w, w + need}, room);
+        free(room);
+        if (overlap)
+            return op_fail(MOE_ERR_INVALID_ARG, "%s: tensors overlap (a result may only be its own gradient)", op);
     }
     const int sms = op_num_sms();
     if (sms < 1) return op_fail(MOE_ERR_CUDA, "%s: no usable current device", op);

@@ -173,3 +173,21 @@ def test_refusals():
     for bad in (0.0, -1.0, float("nan")):
         with pytest.raises(capi.MoeError, match="max_norm"):
             capi.clip_grad_norm([g], bad)
+
+
+def test_gradients_that_touch_or_repeat():
+    """Neighbours in one buffer, in any order, are no overlap; nor are inputs that repeat."""
+    flat = _tensors([50_000], (torch.float32,))[0]
+    ref, cuts = flat.clone(), [0, 1, 9000, 20_003, 50_000]
+    parts = [flat[a:b] for a, b in zip(cuts, cuts[1:])]
+    norm = _norm([flat])
+    assert abs(float(capi.clip_grad_norm([parts[i] for i in (2, 0, 3, 1)], norm / 2)) - norm) <= REL * norm
+    _close(flat, ref, 0.5)
+    out = [torch.empty_like(ref), torch.empty_like(ref)]
+    got = capi.clip_grad_norm([ref, ref], norm / 2, out=out)
+    assert abs(float(got) - 2 ** 0.5 * norm) <= REL * 2 ** 0.5 * norm
+    assert torch.equal(out[0], out[1])
+    _close(out[0], ref, 0.5 ** 1.5)
+    for grads, into in (([ref, ref], None), ([ref], [ref[1:]]), ([ref[1:], flat], [flat[1:], out[0]])):
+        with pytest.raises((capi.MoeError, ValueError), match="overlap|sizes"):
+            capi.clip_grad_norm(grads, 1.0, out=into)

@@ -126,3 +126,26 @@ def test_outputs_that_overlap_inputs_are_refused(lib):
     for X, codes, scales in ((_at(0), _at(4080), far), (_at(0), far, _at(4080)), (far, _at(0), _at(1008))):
         assert lib.moe_mx_quantize(X, 0, 2, 16, 64, 2, codes, scales, None) == capi.MOE_ERR_INVALID_ARG
         assert "overlap" in lib.moe_last_error().decode()
+
+
+# (gradient, result, values) of fp32 tensors; one with no values overlaps nothing
+@pytest.mark.parametrize("tensors", [
+    [(0, 0, 64), (0, 0, 64)],                             # the same gradient twice, in place
+    [(4096, 4096, 64), (0, 0, 64), (252, 252, 64)],       # the last value of one is the first of another
+    [(0, 4096, 64), (1024, 4348, 64)],                    # results
+    [(0, 4096, 64), (4348, 8192, 64)],                    # a result and another gradient
+    [(0, 4, 64)],                                         # a result and part of its own gradient
+    [(4, 0, 64)],
+    [(8192, 8192, 16), (0, 4096, 2000), (16384, 16384, 1)],  # a long result over a short one
+    [(1 << 20, 4096, 64)],                                # the norm is a value of a gradient
+    [(4096, 1 << 20, 64)],
+    [(2 << 20, 4096, 64)],                                # the workspace
+    [(4096, (2 << 20) + 8, 64)],
+])
+def test_clip_lists_that_overlap_are_refused(lib, tensors):
+    need = ctypes.c_size_t()
+    assert lib.moe_clip_workspace(len(tensors) + 1, ctypes.byref(need)) == capi.MOE_OK
+    table = (capi.MoeGrad * (len(tensors) + 1))(capi.MoeGrad(_at(0), _at(0), 0, 1),
+                                                *[capi.MoeGrad(_at(g), _at(o), n, 1) for g, o, n in tensors])
+    status = lib.moe_clip_grad_norm(table, len(tensors) + 1, 1.0, _at(1 << 20), _at(2 << 20), need, None)
+    assert status == capi.MOE_ERR_INVALID_ARG and "overlap" in lib.moe_last_error().decode()
