@@ -13,12 +13,14 @@
 //                to tensor memory of both CTAs (tcgen05.cp, in order with the MMAs that
 //                follow) and issues the MMAs
 //   warps 2-5    epilogue (grouped.cuh), overlapping the next tile's main loop
-//   warps 6-9    fetch scales, four stages' at a time: those of this CTA's weight rows and of all
-//                the tile's tokens, as they lie (a block's scales for consecutive rows), with
-//                4-byte asynchronous copies, for an expert's first row has any alignment
-//                (one stage at a time, the waits between the copies bounded the kernel: prefill
-//                61 us, a decode batch 27 us)
-//   warps 10-17  two sets of four, on alternate stages: the tensor core wants four consecutive
+//   fetch        scales, four stages' at a time: those of this CTA's weight rows and of all the
+//                tile's tokens, as they lie (a block's scales for consecutive rows).  Where rows
+//                and N are multiples of 16, which TMA wants of a tensor's strides: one warp, two
+//                copies, the token run starting at the 16 bytes that hold the tile's first row.
+//                Else four warps with 4-byte asynchronous copies, for an expert's first row has
+//                any alignment (24576 rows 47 against 51 us; one stage at a time, the waits
+//                between the copies bounded the kernel: 61 us)
+//   8 warps      two sets of four, on alternate stages: the tensor core wants four consecutive
 //                blocks' scales of a row in one word, so they transpose from the fetched runs
 //                into the words that tcgen05.cp reads
 // Tensor memory (512 columns): two accumulators of up to 192 columns, then per stage the
@@ -45,8 +47,7 @@ constexpr int kBlocks = kBK / 32;  // scale blocks per stage
 constexpr int kMaxStages = 16;
 constexpr int kEpiWarps = kQuads;
 constexpr int kSets = 2;           // sets of transposing warps
-constexpr int kFetch = 2 + kEpiWarps, kTranspose = kFetch + 4;  // first warp of the role
-constexpr int kThreads = 32 * (kTranspose + 4 * kSets);
+constexpr int kFetch = 2 + kEpiWarps;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxRows = 192;      // token rows of a tile
 constexpr int kBoxes = kMaxRows / 32;
@@ -64,14 +65,16 @@ struct Header {
     volatile int abort;
 };
 constexpr int kHeaderBytes = 4096;
-constexpr int kSmemBytes = kHeaderBytes + kStageSpace + kRaw * kRawBytes;
+constexpr int kSmemBytes = kHeaderBytes + kStageSpace + kRaw * kRawBytes + 16;  // (a word behind the last run is read)
 static_assert(sizeof(Header) <= kHeaderBytes && kSmemBytes <= 232448, "shared memory of one CTA");
 
 struct MxGroupedArgs {
+    CUtensorMap map_xs, map_ws;        // scales: four stages' blocks of a tile
     CUtensorMap map_a, map_b[kBoxes];  // weight codes; token codes in boxes of 16, 32, .. rows
     GroupedOut o;
     const uint8_t *xs, *ws;            // [K / 32, rows], [E, K / 32, N]
     int a_stage, b_stage;              // bytes of codes per stage and CTA
+    uint32_t x_run;                    // bytes fetched of a block's token scales
     int atoms;                         // 128-row groups of token scales
     int stages;
 };
@@ -112,18 +115,39 @@ __device__ __forceinline__ void copy_word(uint32_t dst, const uint8_t *src, int 
 __device__ __forceinline__ void copies_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
-}
 __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
     return v;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_constant__ MxGroupedArgs p) {
+// Scales of four rows of four blocks, whose runs (of bytes, one per row) lie `run` bytes apart
+// at `from`, the first row `shift` bytes further, in each next block `move` more (modulo 4): to
+// one word per row, 16 bytes apart at `to`, byte j for block j.
+__device__ __forceinline__ void transpose(uint32_t from, uint32_t run, uint32_t shift, uint32_t move, uint32_t to) {
+    uint32_t w[4];
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j) {
+        const uint32_t bytes = move ? (shift + j * move) & 3u : shift;
+        const uint32_t at = from + j * run + (bytes & ~3u);
+        w[j] = __funnelshift_r(ld_shared_u32(at), ld_shared_u32(at + 4), 8 * (bytes & 3u));
+    }
+    const uint32_t p01 = __byte_perm(w[0], w[1], 0x5140), p23 = __byte_perm(w[2], w[3], 0x5140);
+    const uint32_t q01 = __byte_perm(w[0], w[1], 0x7362), q23 = __byte_perm(w[2], w[3], 0x7362);
+    st_shared_u32(to, __byte_perm(p01, p23, 0x5410));
+    st_shared_u32(to + 16, __byte_perm(p01, p23, 0x7632));
+    st_shared_u32(to + 32, __byte_perm(q01, q23, 0x5410));
+    st_shared_u32(to + 48, __byte_perm(q01, q23, 0x7632));
+}
+
+// First warp of the transposing role
+__host__ __device__ constexpr int transpose_warp(bool tma) { return kFetch + (tma ? 1 : 4); }
+__host__ __device__ constexpr int num_threads(bool tma) { return 32 * (transpose_warp(tma) + 4 * kSets); }
+
+// TMA: scales are fetched by TMA
+template <bool TMA>
+__global__ void __launch_bounds__(num_threads(TMA), 1) mx_grouped_kernel(const __grid_constant__ MxGroupedArgs p) {
+    constexpr int kTranspose = transpose_warp(TMA);
     extern __shared__ __align__(1024) uint8_t smem[];
     Header &h = *reinterpret_cast<Header *>(smem);
     const TileTable &tab = h.table;
@@ -162,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
             mbar_init(tempty_bar(a), 2 * kEpiWarps);
         }
         for (int i = 0; i < kRaw; ++i) {
-            mbar_init(raw_full_bar(i), 128);
+            mbar_init(raw_full_bar(i), TMA ? 1 : 128);
             mbar_init(raw_empty_bar(i), 4 * kSets);
         }
         mbar_init(drain_bar, 1);
@@ -170,6 +194,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
         h.abort = 0;
         tma_prefetch_desc(&p.map_a);
         tma_prefetch_desc(&p.map_b[0]);
+        if (TMA) {
+            tma_prefetch_desc(&p.map_ws);
+            tma_prefetch_desc(&p.map_xs);
+        }
     }
     if (warp == 1) {
         tmem_alloc_pair(smem_u32(&h.tmem), kTmemCols);
@@ -185,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
     if (!load_table<false>(p.o, h.table) && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.o.err, ERR_BOUNDS);
     const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
     const int half_cols = tab.o.cols / 2, atoms = p.atoms;
+    const uint32_t w_run = half_cols, x_run = p.x_run;  // fetched bytes of a block's scales
     const int K = tab.o.red, k_stages = (K + kBK - 1) / kBK;
 
     if (warp == 0) {
@@ -303,7 +332,32 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
             __syncwarp();
             if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_bar(a), 0));
         }
-    } else if (warp < kTranspose) {
+    } else if (TMA && warp == kFetch) {
+        int raw = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        for (TileWalk<false> walk(tab, first, stride); ok && walk.more(); walk.next()) {
+            const Tile t = walk.get();
+            for (int b0 = 0; b0 < K / 32; b0 += kFetchBlocks) {
+                if (!__all_sync(0xffffffffu, wait_bar(raw_empty_bar(raw), ph, p.o.wait, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    const uint32_t to = sR + raw * kRawBytes, bar = raw_full_bar(raw);
+                    mbar_arrive_expect_tx(bar, kFetchBlocks * (w_run + x_run));
+                    tma_load_3d(to + kFetchBlocks * kRawToken, &p.map_ws, bar, t.col0 + rank * half_cols, b0, t.e);
+                    tma_load_2d(to, &p.map_xs, bar, t.row0 & ~15, b0);
+                }
+                __syncwarp();
+                if (++raw == kRaw) {
+                    raw = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        if (!ok && lane == 0) raise();
+    } else if (!TMA && warp < kTranspose) {
         // 16 threads per block: of its weights 4-byte words 16 m + i % 16 (m < 2), of its tokens
         // those with m < 4; a thread's blocks are 8 apart, which moves a token run by a multiple
         // of 8 bytes, so its alignment holds for the tile.
@@ -311,8 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
         const int n_blocks = K / 32, rows = tab.o.rows, n_out = tab.o.n_out;
         const uint8_t *const xs_end = p.xs + (size_t)n_blocks * rows;
         const size_t x_step = (size_t)kBlocks * rows, w_step = (size_t)kBlocks * n_out;
-        const uint32_t rt0 = sR + (uint32_t)(b * kRawToken + w0);
-        const uint32_t rw0 = sR + (uint32_t)(kFetchBlocks * kRawToken + b * kRawWeight + w0);
+        const uint32_t rt0 = sR + b * x_run + w0, rw0 = sR + kFetchBlocks * kRawToken + b * w_run + w0;
         int raw = 0;
         uint32_t ph = 1;
         bool ok = true;
@@ -336,8 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
                     const int stage_b = b0 + f * kBlocks;
                     if (stage_b >= n_blocks) break;
                     const bool in = stage_b + b < n_blocks;  // else a block past K: zeros
-                    const uint32_t rw = rw0 + off + (uint32_t)(f * kBlocks * kRawWeight);
-                    const uint32_t rt = rt0 + off + (uint32_t)(f * kBlocks * kRawToken);
+                    const uint32_t rw = rw0 + off + f * kBlocks * w_run, rt = rt0 + off + f * kBlocks * x_run;
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
                         if (!in || w_in[m]) copy_word(rw + 64 * m, in ? ws + 64 * m : p.ws, in ? 4 : 0);
@@ -362,13 +414,14 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
     } else {
         const int set = (warp - kTranspose) >> 2;
         const int i = (int)threadIdx.x - 32 * kTranspose - 128 * set;  // 0..127 within the set
-        const int rows = tab.o.rows;
-        const uint32_t to_weights = 512u * (uint32_t)(i >> 5) + (uint32_t)(i & 7) * 64u + (uint32_t)((i & 31) >> 3) * 4u;
+        // a block's run begins with the 16 (or 4) aligned bytes that hold its first scale
+        const uint32_t x_move = TMA ? 0 : (uint32_t)tab.o.rows & 3u;
         int s = 0, raw = 0;
         uint32_t ph = 1, raw_ph = 0;
         bool ok = true;
         for (TileWalk<false> walk(tab, first, stride); ok && walk.more(); walk.next()) {
             const Tile t = walk.get();
+            const uint32_t x_at = (uint32_t)t.row0 & (TMA ? 15u : 3u);
             for (int k = 0; k < k_stages; ++k) {
                 const int f = k % kFetchStages;
                 if (f == 0 && !__all_sync(0xffffffffu, wait_bar(raw_full_bar(raw), raw_ph, p.o.wait, abort_flag))) {
@@ -380,34 +433,20 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
                         ok = false;
                         break;
                     }
-                    const uint32_t rt = sR + (uint32_t)(raw * kRawBytes + f * kBlocks * kRawToken);
-                    const uint32_t rw = sR + (uint32_t)(raw * kRawBytes + kFetchBlocks * kRawToken + f * kBlocks * kRawWeight);
+                    const uint32_t rt = sR + raw * kRawBytes + f * kBlocks * x_run;
+                    const uint32_t rw = sR + raw * kRawBytes + kFetchBlocks * kRawToken + f * kBlocks * w_run;
                     const uint32_t sc = sS + s * scale_stage;
-                    if (i < 64) {  // weight rows 4 (i % 32) ..: byte j of each block's word is row j's
-                        const uint32_t at = rw + (uint32_t)(i >> 5) * (4 * kRawWeight) + (uint32_t)(i & 31) * 4u;
-                        const uint32_t w0 = ld_shared_u32(at), w1 = ld_shared_u32(at + kRawWeight),
-                                       w2 = ld_shared_u32(at + 2 * kRawWeight), w3 = ld_shared_u32(at + 3 * kRawWeight);
-                        const uint32_t p01 = __byte_perm(w0, w1, 0x5140), p23 = __byte_perm(w2, w3, 0x5140);
-                        const uint32_t q01 = __byte_perm(w0, w1, 0x7362), q23 = __byte_perm(w2, w3, 0x7362);
-                        const uint32_t to = sc + to_weights;
-                        st_shared_u32(to, __byte_perm(p01, p23, 0x5410));
-                        st_shared_u32(to + 16, __byte_perm(p01, p23, 0x7632));
-                        st_shared_u32(to + 32, __byte_perm(q01, q23, 0x5410));
-                        st_shared_u32(to + 48, __byte_perm(q01, q23, 0x7632));
-                    }
-                    // tokens: (four blocks, row); a block's run starts at its first byte's place in a word
-                    for (int task = i; task < 2 * t.n; task += 128) {
-                        const int g = task >= t.n ? 1 : 0, r = task - (g ? t.n : 0);
-                        uint32_t v = 0;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int b = 4 * g + j;
-                            const uint32_t shift = ((uint32_t)t.row0 + (uint32_t)b * (uint32_t)rows) & 3u;
-                            v |= ld_shared_u8(rt + (uint32_t)b * kRawToken + shift + (uint32_t)r) << (8 * j);
+                    // a task: four blocks' scales of four rows, first the weights', then the tokens'
+                    for (int task = i; task < 64 + t.n / 2; task += 128) {
+                        if (task < 64) {
+                            const uint32_t m = (uint32_t)task & 31u, g = (uint32_t)task >> 5;
+                            transpose(rw + g * (4 * w_run) + 4 * m, w_run, 0, 0, sc + 512 * g + (m & 7) * 64 + (m >> 3) * 4);
+                        } else {
+                            const uint32_t at = (uint32_t)task - 64, g = at >= (uint32_t)t.n / 4 ? 1 : 0;
+                            const uint32_t m = at - g * (uint32_t)t.n / 4, r = 4 * m;
+                            transpose(rt + g * (4 * x_run) + r, x_run, x_at + 4 * g * x_move, x_move,
+                                      sc + 1024 + 512 * (g * atoms + (r >> 7)) + (r & 31) * 16 + ((r & 127) >> 5) * 4);
                         }
-                        st_shared_u32(sc + 1024u + 512u * (uint32_t)(g * atoms + (r >> 7)) + (uint32_t)(r & 31) * 16u +
-                                          (uint32_t)((r & 127) >> 5) * 4u,
-                                      v);
                     }
                     fence_smem();
                     __syncwarp();
@@ -438,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_grouped_kernel(const __grid_co
     }
 }
 
-unsigned long long g_attr;
+unsigned long long g_attr[2];
 
 // Tile sizes, by the bf16 products' rule: rows up to 192, fewer where the experts average fewer;
 // 256 columns, or 128 where 256 would leave CTA pairs without a tile; where there still are not
@@ -455,6 +494,7 @@ void choose_tiles(MxGroupedArgs &g, int sms) {
         o.tile_rows = (o.tile_rows / 2 + 31) / 32 * 32;
     g.a_stage = o.cols / 2 * kRow;
     g.b_stage = o.tile_rows / 2 * kRow;
+    g.x_run = o.tile_rows + 16;
     g.atoms = (o.tile_rows + 127) / 128;
     g.stages = std::min({kMaxStages, kStageSpace / (g.a_stage + g.b_stage + 1024 + 1024 * g.atoms),
                          ((int)kTmemCols - 2 * o.tile_rows) / (8 + 8 * g.atoms)});
@@ -502,6 +542,7 @@ extern "C" moe_status moe_mx_grouped_forward(const void *Xc, const uint8_t *Xs, 
     g.xs = Xs;
     g.ws = Ws;
     choose_tiles(g, sms);
+    const bool tma = rows % 16 == 0 && N % 16 == 0;
     const long long tiles = ((long long)rows / o.tile_rows + std::min(E, rows)) * o.col_tiles;
     if (tiles > (1ll << 30)) return op_fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^30 output tiles", op);
     const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -509,10 +550,15 @@ extern "C" moe_status moe_mx_grouped_forward(const void *Xc, const uint8_t *Xs, 
     CUresult cr = op_encode(&g.map_a, {u8, 3, Wc, {c, n, e}, {c, n * c}, {kRow, (uint32_t)o.cols / 2, 1}, sw});
     for (int i = 0; i < o.tile_rows / 32 && cr == CUDA_SUCCESS; ++i)
         cr = op_encode(&g.map_b[i], {u8, 2, Xc, {c, r}, {c}, {kRow, 16u * (i + 1)}, sw});
+    const auto flat = CU_TENSOR_MAP_SWIZZLE_NONE;
+    if (tma && cr == CUDA_SUCCESS)
+        cr = op_encode(&g.map_ws, {u8, 3, Ws, {n, b, e}, {n, n * b}, {(uint32_t)o.cols / 2, kFetchBlocks, 1}, flat});
+    if (tma && cr == CUDA_SUCCESS) cr = op_encode(&g.map_xs, {u8, 2, Xs, {r, b}, {r}, {g.x_run, kFetchBlocks}, flat});
     if (cr != CUDA_SUCCESS) return op_fail(MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", op, (int)cr);
-    cudaError_t ce = op_allow_smem(reinterpret_cast<const void *>(mx_grouped_kernel), kSmemBytes, &g_attr);
+    auto kernel = tma ? mx_grouped_kernel<true> : mx_grouped_kernel<false>;
+    cudaError_t ce = op_allow_smem(reinterpret_cast<const void *>(kernel), kSmemBytes, &g_attr[tma]);
     if (ce == cudaSuccess)
-        ce = launch_pdl_cluster(mx_grouped_kernel, dim3(2u * (unsigned)std::min<long long>(sms / 2, tiles)),
-                                dim3(kThreads), (size_t)kSmemBytes, reinterpret_cast<cudaStream_t>(stream), dim3(2, 1, 1), g);
+        ce = launch_pdl_cluster(kernel, dim3(2u * (unsigned)std::min<long long>(sms / 2, tiles)), dim3(num_threads(tma)),
+                                (size_t)kSmemBytes, reinterpret_cast<cudaStream_t>(stream), dim3(2, 1, 1), g);
     return op_cuda(ce, op);
 }
