@@ -6,7 +6,7 @@
 // bytes of codes per row, a quarter of bf16's.
 //
 // Persistent kernel on CTA pairs with the tiles of the bf16 products (grouped.cu): 256
-// weight rows as the MMA's M, up to 192 token rows as its N.  18 warps per CTA:
+// weight rows as the MMA's M, up to 192 token rows as its N.  Warps of a CTA:
 //   warp 0       TMA producer: codes of this CTA's weight rows and half of the token rows,
 //                256 values (128 bytes, 128-byte swizzle) per stage
 //   warp 1       allocates tensor memory; in the even CTA copies a stage's scales from shared
@@ -26,10 +26,11 @@
 // Tensor memory (512 columns): two accumulators of up to 192 columns, then per stage the
 // scales of the weights (8 columns) and of the tokens (8 per 128 of them).
 //
-// Measured on GB300 (64 experts, N 1408, K 2048): 24576 rows 55 us, 2.6 PFLOP/s, 3.5 TB/s; 384
-// rows 22 us, 4.5 TB/s; one expert, 8192 rows, N and K 2048: 24 us, 2.8 PFLOP/s.  No unit is
-// near its rate: without the copies of codes it takes 33 us, without the scales' way to tensor
-// memory and the products 44; the stages' hand-overs between five roles are what is left.
+// Measured on GB300 (64 experts, N 1408, K 2048): 24576 rows 46 us, 3.1 PFLOP/s, 4.2 TB/s; 384
+// rows 21 us, 4.8 TB/s; one expert, 8192 rows, N and K 2048: 20 us, 3.4 PFLOP/s.  The copies of
+// codes and the stores bound it: without products it takes 42 of the 46 us (L2 delivers 9.3 TB/s;
+// the tensor pipe is 40% busy).  Tiles of 224 rows, for which tensor memory has room for two
+// stages' scales beside the accumulators, took the same time.
 #include <algorithm>
 
 #include "common.cuh"
