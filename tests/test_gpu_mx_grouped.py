@@ -167,3 +167,46 @@ def test_refusals():
         capi.mx_grouped_forward(*X, *W, offs[:2])
     with pytest.raises(capi.MoeError, match="UNSUPPORTED"):
         capi.mx_grouped_forward(X[0][:, :24].contiguous(), X[1][:1], W[0][:, :, :24].contiguous(), W[1][:, :1].contiguous(), offs)
+
+
+# rows and N multiples of 16, so that scales come by TMA: behind fills the rows up
+ALIGNED = {
+    "one_block": ([16], 16, 32, 0),
+    "two_rows": ([1, 0, 1], 32, 64, 0),
+    "ragged_starts": ([5, 0, 130, 17, 0, 64, 33], 208, 352, 3),
+    "many_experts": ([(7 * i) % 41 for i in range(256)], 144, 192, 5),
+    "more_than_a_chunk": ([1, 7, 200, 15, 193], 272, 2752, 0),
+    "one_expert_large": ([1504], 1040, 1568, 0),
+    "tokens": ([1, 0, 0, 1, 0, 1, 1] + [0] * 50 + [2], 1408, 2048, 0),
+    "exact_tiles": ([192, 384, 192], 256, 512, 0),
+}
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("name", list(ALIGNED))
+def test_aligned_sizes(name, dtype):
+    """Against fp64, and bit for bit what the same rows give with one more behind them."""
+    counts, N, K, before = ALIGNED[name]
+    X, W, offs = _operands(counts, N, K, before, -(before + sum(counts)) % 16, seed=43)
+    rows = X[0].shape[0]
+    out = torch.full((rows, N), -3.0, dtype=dtype, device="cuda")
+    capi.mx_grouped_forward(*X, *W, offs, out=out)
+    _check(out, X, W, offs)
+    own = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    own[before:before + sum(counts)] = True
+    assert bool((out[~own] == -3.0).all())
+    more = torch.cat([X[0], X[0][:1]]), torch.cat([X[1], X[1][:, :1]], 1)
+    assert torch.equal(capi.mx_grouped_forward(*more, *W, offs, out_dtype=dtype)[:rows][own], out[own])
+
+
+def test_aligned_non_finite_blocks_stay_in_their_rows():
+    X, W, offs = _operands([40, 100, 3], 144, 1056, 1, 16)
+    clean = capi.mx_grouped_forward(*X, *W, offs)
+    X[1][3, 18] = X[1][32, 142] = 255  # row 17 of expert 0; the last block of a row of expert 2
+    X[1][:, 0] = X[1][:, 144:] = 255   # no expert's rows
+    W[1][1, 4, 100] = 255
+    got = capi.mx_grouped_forward(*X, *W, offs)
+    nan = torch.zeros_like(got, dtype=torch.bool)
+    nan[18], nan[142], nan[41:141, 100] = True, True, True
+    assert torch.equal(got[1:144].isnan(), nan[1:144])
+    assert torch.equal(got[1:144][~nan[1:144]], clean[1:144][~nan[1:144]])
