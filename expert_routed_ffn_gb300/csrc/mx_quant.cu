@@ -236,8 +236,8 @@ moe_status check(const char *op, const void *x, int dtype, int slices, int rows,
     if (K % 32) return op_fail(MOE_ERR_UNSUPPORTED, "%s: K must be a multiple of 32 (K %d)", op, K);
     a->rows = rows;
     a->K = K;
-    a->row_tiles = (rows + kRows - 1) / kRows;
-    a->col_tiles = (K + kCols - 1) / kCols;
+    a->row_tiles = (int)((rows + (kRows - 1ll)) / kRows);
+    a->col_tiles = (int)((K + (kCols - 1ll)) / kCols);
     const long long tiles = (long long)slices * a->row_tiles;
     if (tiles > 0 && tiles > ((1ll << 31) - 1) / a->col_tiles)
         return op_fail(MOE_ERR_UNSUPPORTED, "%s: the tensor is too large for one call", op);

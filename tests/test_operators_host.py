@@ -149,3 +149,15 @@ def test_clip_lists_that_overlap_are_refused(lib, tensors):
                                                 *[capi.MoeGrad(_at(g), _at(o), n, 1) for g, o, n in tensors])
     status = lib.moe_clip_grad_norm(table, len(tensors) + 1, 1.0, _at(1 << 20), _at(2 << 20), need, None)
     assert status == capi.MOE_ERR_INVALID_ARG and "overlap" in lib.moe_last_error().decode()
+
+
+@pytest.mark.parametrize("slices,rows,K,status", [
+    (32, 2 ** 31 - 1, 32, capi.MOE_ERR_UNSUPPORTED),    # 2^31 blocks of rows
+    (1, 2 ** 31 - 1, 32, capi.MOE_ERR_INVALID_ARG),     # a valid size: the missing pointer is refused
+    (1, 1, 2 ** 31 - 32, capi.MOE_ERR_INVALID_ARG),
+    (1, 2 ** 31 - 1, 2 ** 31 - 32, capi.MOE_ERR_UNSUPPORTED),
+])
+def test_mx_sizes_at_the_end_of_an_int(lib, slices, rows, K, status):
+    assert lib.moe_mx_quantize(None, 0, slices, rows, K, 2, FAKE, FAKE, None) == status
+    assert lib.moe_mx_dequantize(None, FAKE, 1, slices, rows, K, 0, FAKE, None) == status
+    assert ("too large" in lib.moe_last_error().decode()) == (status == capi.MOE_ERR_UNSUPPORTED)
