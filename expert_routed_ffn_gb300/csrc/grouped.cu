@@ -42,8 +42,8 @@
 //   wgrad, 24576 rows, fp32 out   147 us, 6.2 TB/s: the 738 MB it writes
 //   forward, 384 rows      60 us, 6.2 TB/s: the weights, streamed once
 //   forward, one expert, 16384 rows, K 1408, N 2048   54 us, 1.75 PFLOP/s
-//   forward, one token's six experts   14 us alone, 11 us in a row of calls: start and end of the
-//                          launch, then 35 MB
+//   forward, one token's six experts   9 us in a row of calls: start and end of the launch around
+//                          35 MB
 // One CTA per 128 x 256 tile with the rows as M took 128 (forward), 145 and 181 us.
 //
 // Decreasing or out-of-range offsets: every CTA sees the same, records ERR_BOUNDS and
@@ -361,10 +361,14 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
 unsigned long long g_attr[4];
 
 // Tile sizes.  Rows: up to 256, fewer where the experts average fewer.  Columns: 256, or 128 (64
-// per CTA) where 256 would leave CTA pairs without a tile.  Where there still are not half as
-// many tiles as pairs and the experts' rows fill them, tiles of fewer rows, down to 64 (one
-// expert, 256 rows, N 6144, K 2048: dgrad 33 -> 22 us; 4096 rows, N 256, K 1024: wgrad 23 -> 17;
-// 16 experts of 48 rows keep theirs: 6.9 against 7.8 us).
+// per CTA) where there are no more (with 256, 0.1 us slower).  128 where 256 leave CTA pairs
+// without a tile are slower: a tile's MMAs take the same time (one token's six experts, N 2048, K
+// 1408: 11.6 against 8.7 us; one expert, 256 rows, N 6144, K 2048: 16.0 against 11.7; the other
+// way round 16 experts of 48 rows, dgrad to 200 columns, 7.0 against 7.4).  Where there are not
+// half as many tiles as pairs and the experts' rows fill 64, tiles of fewer rows, down to 64
+// (dgrad of one expert, 256 rows, N 6144, K 2048: 33 -> 20 us; of four experts of 108 rows, N
+// 2040, K 224: 12.5 -> 10.6; wgrad of 4096 rows, N 256, K 1024: 23 -> 17; 16 experts of 48 rows
+// would lose 0.9 of 6.9 us).
 void choose_tiles(GroupedArgs &g, int op, int sms) {
     GroupedOut &o = g.o;
     const long long pairs = sms / 2, active = std::max<long long>(1, std::min(o.E, o.rows));
@@ -375,10 +379,10 @@ void choose_tiles(GroupedArgs &g, int op, int sms) {
         return op == kWgrad ? (long long)o.E * ((o.m_dense + o.tile_rows - 1) / o.tile_rows)
                             : std::max<long long>(active, o.rows / o.tile_rows);
     };
-    o.cols = (o.n_out + 255) / 256 * row_tiles() >= pairs && o.n_out > 128 ? 256 : 128;
+    o.cols = o.n_out > 128 ? 256 : 128;
     o.col_tiles = (o.n_out + o.cols - 1) / o.cols;
     const long long fill = op == kWgrad ? o.m_dense : o.rows / active;  // rows that an expert's tiles share
-    while (o.tile_rows > 64 && 2 * fill >= o.tile_rows && 2 * row_tiles() * o.col_tiles <= pairs) o.tile_rows /= 2;
+    while (o.tile_rows > 64 && fill >= 64 && 2 * row_tiles() * o.col_tiles <= pairs) o.tile_rows /= 2;
     o.row_tiles = (o.m_dense + o.tile_rows - 1) / o.tile_rows;
     g.a_stage = o.cols / 2 * kRow;
     g.b_stage = op == kWgrad ? (o.tile_rows / 2 + 63) / 64 * kChunk : o.tile_rows / 2 * kRow;
