@@ -84,7 +84,7 @@ struct Header {
     uint32_t tmem;
     volatile int abort;
 };
-constexpr int kHeaderBytes = 3072;
+constexpr int kHeaderBytes = 3 << 10;
 constexpr int kSmemBytes = kHeaderBytes + kStageSpace;
 static_assert(sizeof(Header) <= kHeaderBytes && kSmemBytes <= 232448, "shared memory of one CTA");
 
