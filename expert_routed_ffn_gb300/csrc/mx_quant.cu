@@ -10,11 +10,17 @@
 // Bound by HBM: one read of the tensor, one write of codes and scales.  A CTA takes 32 rows
 // x 256 columns; a lane loads 8 consecutive values (four lanes hold a block, so a warp's
 // loads are contiguous) of four rows at once (64 rows per CTA: 28.2 against 26.7 us for 24576 x
-// 2048 bf16; CTAs that walk the tiles with the next one in flight: 30.4).  The scales lie
-// block-major ([K / 32, rows]), across the rows' direction:
-// they are collected in shared memory and leave as 32-byte runs.
-// Measured on GB300: 64 x 1408 x 2048 bf16 values to MXFP4 and back 153 us, 6.1 TB/s.
+// 2048 bf16; 16: slower everywhere; CTAs that walk the tiles with the next one in flight: 30.4).
+// The instructions count as well, at a CTA per 700 cycles of an SM: without divisions, with one
+// address for four rows, and bf16 values scaled in pairs, 64 x 1408 x 2048 values take 68.5
+// instead of 79.9 us (of that 13 us because loads are not marked as streaming).  The scales lie
+// block-major ([K / 32, rows]), across the rows' direction: they are collected in shared memory
+// and leave as 32-byte runs.
+// Measured on GB300, 64 x 1408 x 2048 values: bf16 to MXFP4 68.5 us, 6.8 TB/s, and back 68.7;
+// fp32 115 us, 7.2 TB/s (part of the tensor is still in L2), and back 137, 6.1 TB/s.
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -28,6 +34,21 @@ constexpr int kThreads = 256;
 constexpr int kRows = 32;    // rows per CTA
 constexpr int kCols = 256;   // columns per CTA: eight values per lane
 constexpr int kPerWarp = kRows / (kThreads / 32);
+static_assert(kRows == 32 && kCols == kThreads, "scales: a warp per block, a lane per row");
+
+// Division of n < 2^31 by d <= 2^l, l >= 1 (and d > 2^(l - 1)): mul = floor(2^(31 + l) / d) + 1
+// exceeds 2^(31 + l) / d by at most 1, that is n mul / 2^(31 + l) exceeds n / d by less than
+// 2^-l <= 1 / d.  (A division by instructions costs each warp as much as a row's conversion.)
+struct Divisor {
+    uint32_t mul;
+    int shift;  // l - 1; -1: d = 1
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return shift < 0 ? n : __umulhi(n, mul) >> shift; }
+};
+Divisor divisor(int d) {
+    int l = 0;
+    while ((1ll << l) < d) ++l;
+    return {l == 0 ? 0u : (uint32_t)((1ull << (31 + l)) / (uint32_t)d + 1), l - 1};
+}
 
 struct MxArgs {
     const void *x;        // quantise: [slices, rows, K]; dequantise: unused
@@ -35,14 +56,15 @@ struct MxArgs {
     uint8_t *codes, *scales;
     int rows, K;
     int row_tiles, col_tiles;
+    Divisor by_rows, by_cols;  // by row_tiles, by col_tiles
 };
 
 struct Place {
     int slice, row0, col0;
 };
 __device__ __forceinline__ Place place(const MxArgs &p) {
-    const unsigned b = blockIdx.x, r = b / p.col_tiles;
-    return {(int)(r / p.row_tiles), (int)(r % p.row_tiles) * kRows, (int)(b % p.col_tiles) * kCols};
+    const uint32_t b = blockIdx.x, r = p.by_cols(b), slice = p.by_rows(r);
+    return {(int)slice, (int)(r - slice * p.row_tiles) * kRows, (int)(b - r * p.col_tiles) * kCols};
 }
 
 // 8 values of a row
@@ -52,10 +74,10 @@ struct Eight {
     __device__ __forceinline__ void load(const void *x, size_t at) {
         if (F32) {
             const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const float *>(x) + at);
-            a = __ldcs(src);
-            b = __ldcs(src + 1);
+            a = __ldg(src);
+            b = __ldg(src + 1);
         } else {
-            a = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(x) + at));
+            a = __ldg(reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(x) + at));
         }
     }
     __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
@@ -82,12 +104,22 @@ struct Eight {
         m = most(m, __byte_perm(m, m, 0x1032));
         return (int)(m >> 23);
     }
-    // the values times a power of two
-    __device__ __forceinline__ void scaled(float mul, float (&v)[8]) const {
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    // the values times 2^(127 - c), c <= 253.  Products of bf16 values stay bf16: exact but for
+    // those below its normal range, which are zero as codes.
+    __device__ __forceinline__ void scaled(int c, float (&v)[8]) const {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}, e = (uint32_t)(254 - c);
+        if (F32) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = mul * (F32 ? __uint_as_float(w[i]) : (i & 1) ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]));
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]) * __uint_as_float(e << 23);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t x;
+                asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(w[i]), "r"((e << 7) * 0x10001u));
+                v[2 * i] = bf16_lo(x);
+                v[2 * i + 1] = bf16_hi(x);
+            }
+        }
     }
 };
 
@@ -100,24 +132,24 @@ __global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const MxArgs p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = t.col0 + 8 * lane;
     const bool in_cols = col < p.K;  // K is a multiple of 32: a block's four lanes agree
+    const int first = t.row0 + warp * kPerWarp;  // the warp's rows
+    const size_t at0 = ((size_t)t.slice * p.rows + first) * p.K + col;
     Eight<F32> in[kPerWarp];
 #pragma unroll
     for (int i = 0; i < kPerWarp; ++i) {
-        const int row = t.row0 + warp * kPerWarp + i;
         in[i].zero();
-        if (in_cols && row < p.rows) in[i].load(p.x, ((size_t)t.slice * p.rows + row) * p.K + col);
+        if (in_cols && first + i < p.rows) in[i].load(p.x, at0 + (size_t)i * p.K);
     }
 #pragma unroll
     for (int i = 0; i < kPerWarp; ++i) {
-        const int row = t.row0 + warp * kPerWarp + i;
         const int ex = in[i].exponent();
         const bool finite = ex < 255;
         const int c = finite ? max(ex - (FP4 ? 2 : 8), 0) : 255;
         float v[8];
-        in[i].scaled(__uint_as_float((uint32_t)(254 - min(c, 253)) << 23), v);  // 2^(127 - c)
+        in[i].scaled(min(c, 253), v);
         if ((lane & 3) == 0) s_scale[lane >> 2][warp * kPerWarp + i] = (uint8_t)c;
-        if (in_cols && row < p.rows) {
-            const size_t at = ((size_t)t.slice * p.rows + row) * p.K + col;
+        if (in_cols && first + i < p.rows) {
+            const size_t at = at0 + (size_t)i * p.K;
             if (FP4) {
                 uint32_t o;
                 asm("{\n\t.reg .b8 a, b, c, d;\n\t"
@@ -154,6 +186,8 @@ __global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const MxArgs p) {
     }
 }
 
+// A lane's values: 8 in a row (16 bytes of bf16), or of fp32 twice 4, 128 columns apart (16 bytes
+// each, so that a warp stores 512 in a row: 141 against 155 us; with streaming stores 137).
 template <bool F32, bool FP4>
 __global__ void __launch_bounds__(kThreads) mx_dequantize_kernel(const MxArgs p) {
     __shared__ uint8_t s_scale[kCols / 32][kRows];
@@ -161,35 +195,42 @@ __global__ void __launch_bounds__(kThreads) mx_dequantize_kernel(const MxArgs p)
     pdl_trigger();
     const Place t = place(p);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int col = t.col0 + 8 * lane;
-    const bool in_cols = col < p.K;
+    const int col = t.col0 + (F32 ? 4 : 8) * lane;
+    const bool in_cols = col < p.K, in_next = F32 && col + 128 < p.K;
+    const int first = t.row0 + warp * kPerWarp;  // the warp's rows
+    const size_t at0 = ((size_t)t.slice * p.rows + first) * p.K + col;
     uint2 code[kPerWarp];
 #pragma unroll
     for (int i = 0; i < kPerWarp; ++i) {
-        const int row = t.row0 + warp * kPerWarp + i;
         code[i] = make_uint2(0, 0);
-        if (in_cols && row < p.rows) {
-            const size_t at = ((size_t)t.slice * p.rows + row) * p.K + col;
-            if (FP4)
-                code[i].x = __ldcs(reinterpret_cast<const uint32_t *>(p.codes + at / 2));
-            else
-                code[i] = __ldcs(reinterpret_cast<const uint2 *>(p.codes + at));
+        if (!in_cols || first + i >= p.rows) continue;
+        const size_t at = at0 + (size_t)i * p.K;
+        if (F32 && FP4) {
+            const uint16_t *src = reinterpret_cast<const uint16_t *>(p.codes + at / 2);
+            code[i].x = __ldcs(src) | (in_next ? (uint32_t)__ldcs(src + 32) << 16 : 0u);
+        } else if (F32) {
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(p.codes + at);
+            code[i] = make_uint2(__ldcs(src), in_next ? __ldcs(src + 32) : 0u);
+        } else if (FP4) {
+            code[i].x = __ldcs(reinterpret_cast<const uint32_t *>(p.codes + at / 2));
+        } else {
+            code[i] = __ldcs(reinterpret_cast<const uint2 *>(p.codes + at));
         }
     }
     {
         const int kb = threadIdx.x >> 5;
-        for (int r = lane; r < kRows; r += 32)
-            if (t.col0 + 32 * kb < p.K && t.row0 + r < p.rows)
-                s_scale[kb][r] = p.scales[((size_t)t.slice * (p.K / 32) + t.col0 / 32 + kb) * p.rows + t.row0 + r];
+        if (t.col0 + 32 * kb < p.K && t.row0 + lane < p.rows)
+            s_scale[kb][lane] = p.scales[((size_t)t.slice * (p.K / 32) + t.col0 / 32 + kb) * p.rows + t.row0 + lane];
     }
     __syncthreads();
+    // 2^(c - 127): c = 0 is the subnormal 2^-127, c = 255 NaN
+    auto factor = [&](int block, int i) {
+        const uint32_t c = s_scale[block][warp * kPerWarp + i];
+        return __uint_as_float(c == 255u ? 0x7fc00000u : c == 0u ? 0x00400000u : c << 23);
+    };
 #pragma unroll
     for (int i = 0; i < kPerWarp; ++i) {
-        const int row = t.row0 + warp * kPerWarp + i;
-        if (!in_cols || row >= p.rows) continue;
-        const uint32_t c = s_scale[lane >> 2][warp * kPerWarp + i];
-        // 2^(c - 127): c = 0 is the subnormal 2^-127, c = 255 NaN
-        const float mul = __uint_as_float(c == 255u ? 0x7fc00000u : c == 0u ? 0x00400000u : c << 23);
+        if (!in_cols || first + i >= p.rows) continue;
         uint32_t h[4];  // pairs of f16, which holds every element value exactly
         if (FP4) {
             asm("{\n\t.reg .b8 a, b, c, d;\n\t"
@@ -206,22 +247,23 @@ __global__ void __launch_bounds__(kThreads) mx_dequantize_kernel(const MxArgs p)
 #pragma unroll
             for (int j = 0; j < 4; ++j) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[j]) : "h"(w[j]));
         }
+        const float mul[2] = {factor(F32 ? lane >> 3 : lane >> 2, i), F32 ? factor(4 + (lane >> 3), i) : 0.f};
         float v[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
-            v[2 * j] = f.x * mul;
-            v[2 * j + 1] = f.y * mul;
+            v[2 * j] = f.x * mul[F32 ? j / 2 : 0];
+            v[2 * j + 1] = f.y * mul[F32 ? j / 2 : 0];
         }
-        const size_t at = ((size_t)t.slice * p.rows + row) * p.K + col;
+        const size_t at = at0 + (size_t)i * p.K;
         if (F32) {
             float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at);
-            o[0] = make_float4(v[0], v[1], v[2], v[3]);
-            o[1] = make_float4(v[4], v[5], v[6], v[7]);
+            __stcs(o, make_float4(v[0], v[1], v[2], v[3]));
+            if (in_next) __stcs(o + 32, make_float4(v[4], v[5], v[6], v[7]));
         } else {
-            *reinterpret_cast<uint4 *>(static_cast<bf16 *>(p.out) + at) =
-                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                           pack_bf16x2(v[6], v[7]));
+            __stcs(reinterpret_cast<uint4 *>(static_cast<bf16 *>(p.out) + at),
+                   make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                              pack_bf16x2(v[6], v[7])));
         }
     }
 }
@@ -238,6 +280,8 @@ moe_status check(const char *op, const void *x, int dtype, int slices, int rows,
     a->K = K;
     a->row_tiles = (int)((rows + (kRows - 1ll)) / kRows);
     a->col_tiles = (int)((K + (kCols - 1ll)) / kCols);
+    a->by_rows = divisor(std::max(1, a->row_tiles));
+    a->by_cols = divisor(a->col_tiles);
     const long long tiles = (long long)slices * a->row_tiles;
     if (tiles > 0 && tiles > ((1ll << 31) - 1) / a->col_tiles)
         return op_fail(MOE_ERR_UNSUPPORTED, "%s: the tensor is too large for one call", op);
