@@ -338,9 +338,14 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
                 }
                 tc_fence_after();
             }
-            if (32 * q < half_cols)
-                store_tile<kDense, ADD, kParts>(tab.o, t, tmem_base + ((uint32_t)(q * 32) << 16) + a * kAccCols, empty,
-                                   t.col0 + rank * half_cols + in_half, (warp - 2) >> 2, lane);
+            if (32 * q < half_cols) {
+                const uint32_t acc = tmem_base + ((uint32_t)(q * 32) << 16) + a * kAccCols;
+                const int col = t.col0 + rank * half_cols + in_half, part = (warp - 2) >> 2;
+                if (!ADD && t.add)
+                    store_tile<kDense, true, kParts>(tab.o, t, acc, empty, col, part, lane);
+                else
+                    store_tile<kDense, ADD, kParts>(tab.o, t, acc, empty, col, part, lane);
+            }
             if (!empty) {
                 tc_fence_before();
                 __syncwarp();
@@ -418,6 +423,7 @@ moe_status launch(const char *name, int op, const void *x, const void *w, const 
     o.m_dense = N;
     o.red = op == kForward ? K : N;
     o.f32 = dtype == MOE_DTYPE_F32;
+    o.segment = o.f32 ? kSegment : 1 << 30;
     o.wait = wait_cycles((op == kWgrad ? rows : o.red) / kBK + 1);
     const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;

@@ -37,12 +37,14 @@ struct GroupedOut {
     int col_tiles;   // tiles along the output columns
     int row_tiles;   // dense: tiles along m_dense
     int f32;         // output type: fp32, else bf16
+    int segment;     // reduction steps summed in tensor memory before they go to the output
     long long wait;  // bound of every wait in SM cycles, see wait_cycles
 };
 
 struct Tile {
     int e, row0, rows, n, col0;  // expert, first output row, valid rows, MMA N, first output column
     int r0, r1;                  // reduction range
+    bool add;                    // not the output's first segment
 };
 
 __device__ __forceinline__ void fence_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -121,7 +123,7 @@ struct TileTable {
     GroupedOut o;                      // a parameter read that misses the constant cache costs more
     int offs[kMaxExperts + 1];         // first row of each expert
     int tiles[kMaxExperts];            // row-grouped: its first row tile; INT_MAX behind the last
-    uint16_t share[kMaxExperts];       // row-grouped: rows of its tiles but the last, a multiple of 32
+    uint8_t share[kMaxExperts];        // row-grouped: rows of its tiles but the last, in units of 32
     int total;                         // tiles, 0 where the offsets decrease or leave [0, rows]
 };
 
@@ -144,7 +146,7 @@ __device__ __forceinline__ bool load_table(const GroupedOut &p, TileTable &tab) 
         for (int j = 0; j < kPer; ++j) {
             const int e = lane * kPer + j, rows = !DENSE && ok && e < E ? tab.offs[e + 1] - tab.offs[e] : 0;
             cnt[j] = (rows + p.tile_rows - 1) / p.tile_rows;
-            if (!DENSE && cnt[j] > 0) tab.share[e] = (uint16_t)(((rows + cnt[j] - 1) / cnt[j] + 31) & ~31);
+            if (!DENSE && cnt[j] > 0) tab.share[e] = (uint8_t)(((rows + cnt[j] - 1) / cnt[j] + 31) / 32);
             sum += cnt[j];
         }
         int incl = sum;
@@ -166,18 +168,25 @@ __device__ __forceinline__ bool load_table(const GroupedOut &p, TileTable &tab) 
     return ok;
 }
 
+// Longer sums reach an fp32 output in segments of so many reduction steps, added there in fp32 by
+// the thread that stored the one before.  The tensor core's additions truncate: 4096 steps are
+// 4.4e-6 (2-norm) from the exact sum, 8192 in one segment 9.1e-6 and 65536 7.6e-5; in segments
+// both stay at 4.4e-6 (8192 steps of 128 x 128 sums 29.6 against 27.7 us).
+constexpr int kSegment = 4096;
+
 // Walks a CTA pair's tiles first, first + stride, .. (a converged warp), numbered with the column
 // tile innermost: the position is kept in digits, so that a step takes no division (one took a
 // thousand cycles of the thread that feeds the tensor core).  An expert's rows are dealt evenly
 // to its row tiles, in multiples of 32 (no tile is left empty: with `parts` tiles of at most T
 // rows either parts <= T / 32, and rounding shares up takes fewer than `parts` * 32 of the more
 // than T * (parts - 1) rows, or the shares are T).
-template <bool DENSE>
+template <bool DENSE, bool SEGMENTS = true>
 struct TileWalk {
     const TileTable &tab;
     int tile, stride;
     int c, r, e = 0;             // column tile; row tile (dense: within the expert); dense: expert
     int dc, dr, de = 0;          // the stride in the same digits
+    int at = 0;                  // the first of the current segment's reduction steps
 
     __device__ __forceinline__ TileWalk(const TileTable &table, int first, int step)
         : tab(table), tile(first), stride(step) {
@@ -194,6 +203,11 @@ struct TileWalk {
     }
     __device__ __forceinline__ bool more() const { return tile < tab.total; }
     __device__ __forceinline__ void next() {
+        if (SEGMENTS && at + tab.o.segment < (DENSE ? tab.offs[e + 1] - tab.offs[e] : tab.o.red)) {
+            at += tab.o.segment;
+            return;
+        }
+        at = 0;
         tile += stride;
         c += dc;
         r += dr;
@@ -216,8 +230,8 @@ struct TileWalk {
             t.e = e;
             t.row0 = r * p.tile_rows;
             t.rows = min(p.tile_rows, p.m_dense - t.row0);
-            t.r0 = tab.offs[e];
-            t.r1 = tab.offs[e + 1];
+            t.r0 = tab.offs[e] + at;
+            t.r1 = t.r0 + min(tab.offs[e + 1] - t.r0, p.segment);
         } else {
             // the last expert whose first row tile is <= r (one with rows: the next ones start later)
             constexpr int kPer = kMaxExperts / 32;
@@ -225,13 +239,14 @@ struct TileWalk {
             const int group = __popc(__ballot_sync(0xffffffffu, tab.tiles[lane * kPer] <= r)) - 1;
             const int in = __popc(__ballot_sync(0xffffffffu, lane < kPer && tab.tiles[group * kPer + lane] <= r));
             t.e = group * kPer + in - 1;
-            const int share = tab.share[t.e];
+            const int share = 32 * tab.share[t.e];
             t.row0 = tab.offs[t.e] + (r - tab.tiles[t.e]) * share;
             t.rows = min(share, tab.offs[t.e + 1] - t.row0);
-            t.r0 = 0;
-            t.r1 = p.red;
+            t.r0 = at;
+            t.r1 = SEGMENTS ? at + min(p.red - at, p.segment) : p.red;
         }
         t.n = (t.rows + 31) & ~31;
+        t.add = SEGMENTS && at > 0;
         return t;
     }
 };

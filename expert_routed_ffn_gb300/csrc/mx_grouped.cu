@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(num_threads(TMA), 1) mx_grouped_kernel(const _
         uint32_t ph = 1;
         int s = 0;
         bool ok = true;
-        for (TileWalk<false> walk(tab, first, stride); ok && walk.more(); walk.next()) {
+        for (TileWalk<false, false> walk(tab, first, stride); ok && walk.more(); walk.next()) {
             const Tile t = walk.get();
             const int col = t.col0 + rank * half_cols, row = t.row0 + rank * (t.n / 2);
             const CUtensorMap *map_b = &p.map_b[t.n / 32 - 1];
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(num_threads(TMA), 1) mx_grouped_kernel(const _
             uint32_t n_acc = 0, ph = 0;
             int s = 0;
             bool ok = p.o.wait != 0, issued = false;  // a bound of 0: give up at once
-            TileWalk<false> walk(tab, first, stride);
+            TileWalk<false, false> walk(tab, first, stride);
             Tile next;
             if (walk.more()) next = walk.get();
             while (ok && walk.more()) {
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(num_threads(TMA), 1) mx_grouped_kernel(const _
     } else if (warp < 2 + kEpiWarps) {
         const int q = warp & 3;  // the TMEM lane quadrant this warp may read
         uint32_t n_acc = 0;
-        for (TileWalk<false> walk(tab, first, stride); walk.more(); walk.next(), ++n_acc) {
+        for (TileWalk<false, false> walk(tab, first, stride); walk.more(); walk.next(), ++n_acc) {
             const Tile t = walk.get();
             const uint32_t a = n_acc & 1u;
             if (!__all_sync(0xffffffffu, wait_bar<true>(tfull_bar(a), (n_acc >> 1) & 1u, p.o.wait, abort_flag))) {
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(num_threads(TMA), 1) mx_grouped_kernel(const _
         int raw = 0;
         uint32_t ph = 1;
         bool ok = true;
-        for (TileWalk<false> walk(tab, first, stride); ok && walk.more(); walk.next()) {
+        for (TileWalk<false, false> walk(tab, first, stride); ok && walk.more(); walk.next()) {
             const Tile t = walk.get();
             for (int b0 = 0; b0 < K / 32; b0 += kFetchBlocks) {
                 if (!__all_sync(0xffffffffu, wait_bar(raw_empty_bar(raw), ph, p.o.wait, abort_flag))) {
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(num_threads(TMA), 1) mx_grouped_kernel(const _
         int raw = 0;
         uint32_t ph = 1;
         bool ok = true;
-        for (TileWalk<false> walk(tab, first, stride); ok && walk.more(); walk.next()) {
+        for (TileWalk<false, false> walk(tab, first, stride); ok && walk.more(); walk.next()) {
             const Tile t = walk.get();
             const int col = t.col0 + rank * half_cols + w0;
             const uint8_t *ws = p.ws + ((size_t)t.e * n_blocks + b) * n_out + col;
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(num_threads(TMA), 1) mx_grouped_kernel(const _
         int s = 0, raw = 0;
         uint32_t ph = 1, raw_ph = 0;
         bool ok = true;
-        for (TileWalk<false> walk(tab, first, stride); ok && walk.more(); walk.next()) {
+        for (TileWalk<false, false> walk(tab, first, stride); ok && walk.more(); walk.next()) {
             const Tile t = walk.get();
             const uint32_t x_at = (uint32_t)t.row0 & (TMA ? 15u : 3u);
             for (int k = 0; k < k_stages; ++k) {

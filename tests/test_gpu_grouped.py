@@ -306,3 +306,28 @@ def test_refuses_what_it_cannot_take():
     with pytest.raises(capi.MoeError, match="UNSUPPORTED"):
         capi.grouped_forward(X[:, :60].contiguous(), W[:, :, :60].contiguous(), offs)
     assert lib.moe_operators_status() == capi.MOE_OK
+
+
+@pytest.mark.parametrize("op", ["forward", "dgrad", "wgrad"])
+def test_long_sums_keep_their_precision(op):
+    """Sums of positive products, the worst case of additions that truncate.  fp32 outputs are
+    summed in segments of 4096: a segment's 256 additions of 16 products lose at most 2^-23 of the
+    running sum each, on average half of the last one's (256 / 2 * 2^-23 = 2^-16 at most), those
+    of the segments half a step each; 2^-15 leaves a factor of almost two for the order in the 16."""
+    gen = torch.Generator(device="cuda").manual_seed(51)
+    long, N, counts = 40_016, 136, [40_016, 0, 4096, 8200] if op == "wgrad" else [70, 0, 33, 1]
+    if op == "wgrad":
+        A, B = _bf16(gen, sum(counts), N).abs(), _bf16(gen, sum(counts), 264).abs()
+    else:
+        A = _bf16(gen, sum(counts), long).abs()
+        B = _bf16(gen, *((4, N, long) if op == "forward" else (4, long, N))).abs()
+    offs = _offs(counts)
+    got = _call(op, A, B, offs, out_dtype=torch.float32)
+    ref, mag, num = _reference(op, A, B, offs, tuple(got.shape))
+    assert bool(((got.double() - ref).abs() <= 2.0 ** -15 * ref).all())
+    again = torch.zeros_like(got)
+    _call(op, A, B, offs, out=again)
+    assert torch.equal(again, got)
+    if op == "wgrad":  # added to what is there: one more rounding of fp32 sums twice as large
+        _call(op, A, B, offs, out=again, accumulate=True)
+        assert bool(((again.double() - 2 * ref).abs() <= 2.0 ** -15 * 2 * ref).all())
