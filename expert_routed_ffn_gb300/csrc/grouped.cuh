@@ -231,7 +231,7 @@ struct TileWalk {
             t.row0 = r * p.tile_rows;
             t.rows = min(p.tile_rows, p.m_dense - t.row0);
             t.r0 = tab.offs[e] + at;
-            t.r1 = t.r0 + min(tab.offs[e + 1] - t.r0, p.segment);
+            t.r1 = SEGMENTS ? t.r0 + min(tab.offs[e + 1] - t.r0, p.segment) : tab.offs[e + 1];
         } else {
             // the last expert whose first row tile is <= r (one with rows: the next ones start later)
             constexpr int kPer = kMaxExperts / 32;
