@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
         tma_prefetch_desc(&p.map_a);
         tma_prefetch_desc(&p.map_b[0]);
     }
+    if (threadIdx.x == 64) start_table<kDense>(p.o, h.table);
     if (warp == 1) {
         tmem_alloc_pair(smem_u32(&h.tmem), kTmemCols);
         tmem_relinquish_pair();
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
     const uint32_t tmem_base = h.tmem;
     pdl_wait();  // the offsets and operands of earlier kernels on the stream
     pdl_trigger();
-    if (!load_table<kDense>(p.o, h.table) && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.o.err, ERR_BOUNDS);
+    if (!load_table<kDense>(h.table) && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.o.err, ERR_BOUNDS);
     const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
     const int half_cols = tab.o.cols / 2;
     // wgrad: the stage at reduction row r ends inside a 16-row step

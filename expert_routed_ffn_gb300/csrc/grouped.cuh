@@ -125,44 +125,62 @@ struct TileTable {
     int tiles[kMaxExperts];            // row-grouped: its first row tile; INT_MAX behind the last
     uint8_t share[kMaxExperts];        // row-grouped: rows of its tiles but the last, in units of 32
     int total;                         // tiles, 0 where the offsets decrease or leave [0, rows]
+    int sums[kMaxExperts / 32];        // row-grouped: row tiles of 32 experts
+    int c, r, e, dc, dr, de;           // this pair's first tile and the stride, see TileWalk
 };
 
-// Fill the table (all threads of the CTA); false, in every CTA alike, for bad offsets.
+// What of the table depends on the launch alone, by one thread, before earlier kernels have ended.
 template <bool DENSE>
-__device__ __forceinline__ bool load_table(const GroupedOut &p, TileTable &tab) {
-    const int E = p.E;
-    if (threadIdx.x == 0) tab.o = p;
-    for (int i = threadIdx.x; i <= E; i += blockDim.x) tab.offs[i] = p.offs[i];
-    __syncthreads();
-    int bad = 0;
-    for (int i = threadIdx.x; i < E; i += blockDim.x) bad |= tab.offs[i] > tab.offs[i + 1];
-    bad |= tab.offs[0] < 0 || tab.offs[E] > p.rows;
-    const bool ok = !__syncthreads_or(bad);
-    if (threadIdx.x < 32) {
-        constexpr int kPer = kMaxExperts / 32;
-        const int lane = threadIdx.x;
-        int cnt[kPer], sum = 0;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int e = lane * kPer + j, rows = !DENSE && ok && e < E ? tab.offs[e + 1] - tab.offs[e] : 0;
-            cnt[j] = (rows + p.tile_rows - 1) / p.tile_rows;
-            if (!DENSE && cnt[j] > 0) tab.share[e] = (uint8_t)(((rows + cnt[j] - 1) / cnt[j] + 31) / 32);
-            sum += cnt[j];
+__device__ __forceinline__ void start_table(const GroupedOut &p, TileTable &tab) {
+    const int first = (int)blockIdx.x / 2, step = (int)gridDim.x / 2;
+    int r = first / p.col_tiles, dr = step / p.col_tiles;
+    tab.o = p;
+    tab.c = first - r * p.col_tiles;
+    tab.dc = step - dr * p.col_tiles;
+    tab.e = DENSE ? r / p.row_tiles : 0;
+    tab.de = DENSE ? dr / p.row_tiles : 0;
+    tab.r = r - tab.e * p.row_tiles;
+    tab.dr = dr - tab.de * p.row_tiles;
+}
+
+// The rest, from the offsets, by all threads of the CTA (at least 256, one per expert, so that the
+// divisions take their time once: with 32 threads for them and more barriers this took 3800 cycles
+// of every call, one token's six experts 8.7 instead of 7.5 us); false, in every CTA alike, for
+// bad offsets.
+template <bool DENSE>
+__device__ __forceinline__ bool load_table(TileTable &tab) {
+    const GroupedOut &p = tab.o;
+    const int i = threadIdx.x, E = p.E, lane = i & 31, warp = i >> 5;
+    int bad = 0, cnt = 0;
+    if (i < E) {
+        const int a = p.offs[i], b = p.offs[i + 1];
+        tab.offs[i] = a;
+        if (i == E - 1) tab.offs[E] = b;
+        bad = a < 0 || a > b || b > p.rows;
+        if (!DENSE && !bad && a < b) {
+            cnt = (b - a + p.tile_rows - 1) / p.tile_rows;
+            tab.share[i] = (uint8_t)(((cnt == 1 ? b - a : (b - a + cnt - 1) / cnt) + 31) / 32);
         }
-        int incl = sum;
+    }
+    int incl = cnt;
+    if (!DENSE) {
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, incl, d);
             if (lane >= d) incl += o;
         }
-        int run = incl - sum;
+        if (lane == 31 && warp < kMaxExperts / 32) tab.sums[warp] = incl;
+    }
+    const bool ok = !__syncthreads_or(bad);
+    if (i < kMaxExperts) {
+        int before = 0, all = 0;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int e = lane * kPer + j;
-            tab.tiles[e] = e < E ? run : 0x7fffffff;
-            run += cnt[j];
+        for (int w = 0; !DENSE && w < kMaxExperts / 32; ++w) {
+            if (w < warp) before += tab.sums[w];
+            all += tab.sums[w];
         }
-        if (lane == 31) tab.total = !ok ? 0 : DENSE ? E * p.row_tiles * p.col_tiles : run * p.col_tiles;
+        if (!DENSE) tab.tiles[i] = i < E ? before + incl - cnt : 0x7fffffff;
+        if (i == 0) tab.total = !ok ? 0 : DENSE ? E * p.row_tiles * p.col_tiles : all * p.col_tiles;
     }
     __syncthreads();
     return ok;
@@ -184,23 +202,12 @@ template <bool DENSE, bool SEGMENTS = true>
 struct TileWalk {
     const TileTable &tab;
     int tile, stride;
-    int c, r, e = 0;             // column tile; row tile (dense: within the expert); dense: expert
-    int dc, dr, de = 0;          // the stride in the same digits
+    int c, r, e;                 // column tile; row tile (dense: within the expert); dense: expert
+    int dc, dr, de;              // the stride in the same digits
     int at = 0;                  // the first of the current segment's reduction steps
 
     __device__ __forceinline__ TileWalk(const TileTable &table, int first, int step)
-        : tab(table), tile(first), stride(step) {
-        r = first / tab.o.col_tiles;
-        c = first - r * tab.o.col_tiles;
-        dr = step / tab.o.col_tiles;
-        dc = step - dr * tab.o.col_tiles;
-        if (DENSE) {
-            e = r / tab.o.row_tiles;
-            r -= e * tab.o.row_tiles;
-            de = dr / tab.o.row_tiles;
-            dr -= de * tab.o.row_tiles;
-        }
-    }
+        : tab(table), tile(first), stride(step), c(table.c), r(table.r), e(table.e), dc(table.dc), dr(table.dr), de(table.de) {}
     __device__ __forceinline__ bool more() const { return tile < tab.total; }
     __device__ __forceinline__ void next() {
         if (SEGMENTS && at + tab.o.segment < (DENSE ? tab.offs[e + 1] - tab.offs[e] : tab.o.red)) {

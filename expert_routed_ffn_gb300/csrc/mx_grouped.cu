@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(num_threads(TMA), 1) mx_grouped_kernel(const _
             tma_prefetch_desc(&p.map_xs);
         }
     }
+    if (threadIdx.x == 64) start_table<false>(p.o, h.table);
     if (warp == 1) {
         tmem_alloc_pair(smem_u32(&h.tmem), kTmemCols);
         tmem_relinquish_pair();
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(num_threads(TMA), 1) mx_grouped_kernel(const _
     const uint32_t tmem_base = h.tmem;
     pdl_wait();
     pdl_trigger();
-    if (!load_table<false>(p.o, h.table) && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.o.err, ERR_BOUNDS);
+    if (!load_table<false>(h.table) && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.o.err, ERR_BOUNDS);
     const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
     const int half_cols = tab.o.cols / 2, atoms = p.atoms;
     const uint32_t w_run = half_cols, x_run = p.x_run;  // fetched bytes of a block's scales
