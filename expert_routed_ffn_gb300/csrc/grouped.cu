@@ -16,8 +16,8 @@
 // (M; 128 in each CTA) x up to 256 output rows (N; each CTA stages half of them), so a CTA
 // brings 32 KB per 64 reduction steps instead of the 48 KB of a 128 x 256 tile of its own,
 // and L2 keeps up with the tensor cores.  Warps of a CTA:
-//   warp 0     TMA producer: per stage 64 reduction steps of this CTA's A (columns) and B
-//              (rows) operand, 128-byte swizzle; both CTAs' copies complete on the barrier
+//   warp 0     TMA producer: per stage one or two blocks of 64 reduction steps of this CTA's A
+//              (columns) and B (rows) operand, 128-byte swizzle; both CTAs' copies complete on the barrier
 //              of the even CTA
 //   warp 1     allocates tensor memory; in the even CTA issues tcgen05.mma (K 16) into one
 //              of two accumulators, so a tile's epilogue overlaps the next one's main loop
@@ -42,7 +42,7 @@
 //   wgrad, 24576 rows, fp32 out   147 us, 6.2 TB/s: the 738 MB it writes
 //   forward, 384 rows      60 us, 6.2 TB/s: the weights, streamed once
 //   forward, one expert, 16384 rows, K 1408, N 2048   54 us, 1.75 PFLOP/s
-//   forward, one token's six experts   9 us in a row of calls: start and end of the launch around
+//   forward, one token's six experts   8 us in a row of calls: start and end of the launch around
 //                          35 MB
 // One CTA per 128 x 256 tile with the rows as M took 128 (forward), 145 and 181 us.
 //
@@ -91,7 +91,7 @@ static_assert(sizeof(Header) <= kHeaderBytes && kSmemBytes <= 232448, "shared me
 struct GroupedArgs {
     CUtensorMap map_a, map_b[kBoxes];
     GroupedOut o;
-    int a_stage, b_stage;  // bytes per stage and CTA
+    int a_block, b_block;  // bytes of 64 reduction steps per CTA
     int stages;
 };
 
@@ -110,18 +110,18 @@ __device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr) {
 __device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
 }
-// ADD: to what the output holds (wgrad); SEGMENTS: sums may come in several (grouped.cuh)
-template <int OP, bool ADD, bool SEGMENTS>
+// BLOCKS: most blocks of 64 reduction steps of a stage; ADD: to what the output holds (wgrad); SEGMENTS: sums may come in several (grouped.cuh)
+template <int OP, int BLOCKS, bool ADD, bool SEGMENTS>
 __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_constant__ GroupedArgs p) {
     constexpr bool kDense = OP == kWgrad;
     extern __shared__ __align__(1024) uint8_t smem[];
     Header &h = *reinterpret_cast<Header *>(smem);
     const TileTable &tab = h.table;
     const uint32_t base = smem_u32(smem) + kHeaderBytes;
-    const int a_stage = p.a_stage, b_stage = p.b_stage, stages = p.stages;
-    // all A stages first: the MMA reads 128 columns of A where the box brought 64; the rest is
+    const int a_block = p.a_block, b_block = p.b_block, stages = p.stages;
+    // all A blocks first: the MMA reads 128 columns of A where the box brought 64; the rest is
     // whatever follows, and its results are not stored
-    const uint32_t sA = base, sB = base + (uint32_t)(stages * a_stage);
+    const uint32_t sA = base, sB = base + (uint32_t)(stages * BLOCKS * a_block);
     const uint32_t bar0 = smem_u32(h.bars);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
@@ -173,6 +173,11 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
     const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
     const int half_cols = tab.o.cols / 2;
     // wgrad: the stage at reduction row r ends inside a 16-row step
+    // blocks of the stage at reduction step r: those left, of the wgrad two only if both are whole
+    auto blocks_at = [&](const Tile &t, int r) {
+        if (BLOCKS == 1) return 1;
+        return kDense ? (t.r1 - r >= BLOCKS * kBK ? BLOCKS : 1) : min(BLOCKS, (t.r1 - r + kBK - 1) / kBK);
+    };
     auto is_tail = [&](const Tile &t, int r) { return kDense && t.r1 - r < kBK && (t.r1 - r) % 16 != 0; };
 
     if (warp == 0) {
@@ -184,13 +189,14 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
             const int col = t.col0 + rank * half_cols, row = t.row0 + rank * (t.n / 2);
             const bool two_b = t.n / 2 > 64;  // MN-major B: two chunks of 64 columns
             const CUtensorMap *map_b = kDense ? &p.map_b[0] : &p.map_b[t.n / 32 - 1];  // K-major B: n / 2 rows
-            const uint32_t bytes = a_stage + (kDense ? (two_b ? 2 : 1) * kChunk : (t.n / 2) * kRow);
-            for (int r = t.r0; r < t.r1; r += kBK) {
+            const uint32_t bytes = a_block + (kDense ? (two_b ? 2 : 1) * kChunk : (t.n / 2) * kRow);
+            for (int r = t.r0, here; r < t.r1; r += here * kBK) {
+                here = blocks_at(t, r);
                 if (!__all_sync(0xffffffffu, wait_bar(empty_bar(s), ph, p.o.wait, abort_flag))) {
                     ok = false;
                     break;
                 }
-                const uint32_t da = sA + s * a_stage, db = sB + s * b_stage;
+                uint32_t da = sA + s * BLOCKS * a_block, db = sB + s * BLOCKS * b_block;
                 const uint32_t bar = mapa_shared(full_bar(s), 0);
                 if (is_tail(t, r)) {  // complete on this CTA's own barrier, for warp 10 to zero the rest
                     if (elect_one()) {
@@ -202,21 +208,26 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
                         if (two_b) tma_load_2d(db + kChunk, map_b, tail_bar(s), row + 64, r);
                     }
                 } else if (elect_one()) {
-                    if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * bytes);
-                    if (OP == kForward) {
-                        tma_load_3d_pair(da, &p.map_a, bar, r, col, t.e);
-                    } else if (OP == kDgrad) {
-                        tma_load_3d_pair(da, &p.map_a, bar, col, r, t.e);
-                        if (half_cols > 64) tma_load_3d_pair(da + kChunk, &p.map_a, bar, col + 64, r, t.e);
-                    } else {
-                        tma_load_2d_pair(da, &p.map_a, bar, col, r);
-                        if (half_cols > 64) tma_load_2d_pair(da + kChunk, &p.map_a, bar, col + 64, r);
-                    }
-                    if (OP != kWgrad) {
-                        tma_load_2d_pair(db, map_b, bar, r, row);
-                    } else {
-                        tma_load_2d_pair(db, map_b, bar, row, r);
-                        if (two_b) tma_load_2d_pair(db + kChunk, map_b, bar, row + 64, r);
+                    if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * bytes * here);
+#pragma unroll
+                    for (int b = 0; b < BLOCKS; ++b, da += a_block, db += b_block) {
+                        if (b >= here) break;
+                        const int rb = r + b * kBK;
+                        if (OP == kForward) {
+                            tma_load_3d_pair(da, &p.map_a, bar, rb, col, t.e);
+                        } else if (OP == kDgrad) {
+                            tma_load_3d_pair(da, &p.map_a, bar, col, rb, t.e);
+                            if (half_cols > 64) tma_load_3d_pair(da + kChunk, &p.map_a, bar, col + 64, rb, t.e);
+                        } else {
+                            tma_load_2d_pair(da, &p.map_a, bar, col, rb);
+                            if (half_cols > 64) tma_load_2d_pair(da + kChunk, &p.map_a, bar, col + 64, rb);
+                        }
+                        if (OP != kWgrad) {
+                            tma_load_2d_pair(db, map_b, bar, rb, row);
+                        } else {
+                            tma_load_2d_pair(db, map_b, bar, row, rb);
+                            if (two_b) tma_load_2d_pair(db + kChunk, map_b, bar, row + 64, rb);
+                        }
                     }
                 }
                 __syncwarp();
@@ -256,7 +267,8 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
                     break;
                 }
                 tc_fence_after();
-                for (int r = t.r0; r < t.r1; r += kBK) {
+                for (int r = t.r0, here; r < t.r1; r += here * kBK) {
+                    here = blocks_at(t, r);
                     bool got = wait_bar(full_bar(s), ph, p.o.wait, abort_flag);
                     if (is_tail(t, r)) {
                         got = got && wait_bar<true>(zeroed_bar(s), zeroed_ph >> s & 1u, p.o.wait, abort_flag);
@@ -267,15 +279,21 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t ad = desc_a + (uint32_t)(s * a_stage >> 4), bd = desc_b + (uint32_t)(s * b_stage >> 4);
+                    uint64_t ad = desc_a + (uint32_t)(s * BLOCKS * a_block >> 4), bd = desc_b + (uint32_t)(s * BLOCKS * b_block >> 4);
                     const int left = t.r1 - r;
                     if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < kBK / 16; ++k)
-                            if (!kDense || 16 * k < left)
-                                tc_mma_bf16_pair(d, ad + k * kStepA, bd + k * kStepB, idesc, (r != t.r0) | (k != 0));
+                        for (int b = 0; b < BLOCKS; ++b) {
+                            if (b >= here) break;
+#pragma unroll
+                            for (int k = 0; k < kBK / 16; ++k)
+                                if (!kDense || b * kBK + 16 * k < left)
+                                    tc_mma_bf16_pair(d, ad + k * kStepA, bd + k * kStepB, idesc, (r != t.r0) | (b + k != 0));
+                            ad += (uint32_t)a_block >> 4;
+                            bd += (uint32_t)b_block >> 4;
+                        }
                         tc_commit_pair(empty_bar(s), 3);  // frees the stage in both CTAs
-                        if (left <= kBK) tc_commit_pair(tfull_bar(a), 3);
+                        if (left <= here * kBK) tc_commit_pair(tfull_bar(a), 3);
                     }
                     __syncwarp();
                     issued = true;
@@ -303,16 +321,17 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
         const int chunks_a = half_cols / 64;
         for (TileWalk<kDense, SEGMENTS> walk(tab, first, stride); walk.more(); walk.next()) {
             const Tile t = walk.get();
-            const int k_blocks = (t.r1 - t.r0 + kBK - 1) / kBK;
-            const int last = t.r0 + (k_blocks - 1) * kBK;
-            if (k_blocks > 0 && is_tail(t, last)) {
-                const int st = (s + k_blocks - 1) % stages;
+            const int whole = (t.r1 - t.r0) / (BLOCKS * kBK), rest = t.r1 - t.r0 - whole * (BLOCKS * kBK);
+            const int tile_stages = whole + (rest + kBK - 1) / kBK;
+            const int last = t.r1 - ((t.r1 - t.r0 - 1) % kBK + 1);  // first row of the last block
+            if (tile_stages > 0 && is_tail(t, last)) {
+                const int st = (s + tile_stages - 1) % stages;
                 if (!__all_sync(0xffffffffu, wait_bar(tail_bar(st), tail_ph >> st & 1u, p.o.wait, abort_flag))) {
                     if (lane == 0) raise();
                     break;
                 }
                 tail_ph ^= 1u << st;
-                const uint32_t da = sA + st * a_stage, db = sB + st * b_stage;
+                const uint32_t da = sA + st * BLOCKS * a_block, db = sB + st * BLOCKS * b_block;
                 const int valid = t.r1 - last, words = ((valid + 15) / 16 * 16 - valid) * (kRow / 16);
                 const int chunks = chunks_a + (t.n / 2 > 64 ? 2 : 1);
                 for (int c = 0; c < chunks; ++c) {
@@ -323,7 +342,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
                 __syncwarp();
                 if (lane == 0) mbar_arrive_pair(mapa_shared(zeroed_bar(st), 0));
             }
-            s = (s + k_blocks) % stages;
+            s = (s + tile_stages) % stages;
         }
     } else {
         const int q = warp & 3;  // the TMEM lane quadrant this warp may read
@@ -365,7 +384,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
     }
 }
 
-unsigned long long g_attr[7];
+unsigned long long g_attr[11];
 
 // Tile sizes.  Rows: up to 256, fewer where the experts average fewer.  Columns: 256, or 128 (64
 // per CTA) where there are no more (with 256, 0.1 us slower).  128 where 256 leave CTA pairs
@@ -375,8 +394,11 @@ unsigned long long g_attr[7];
 // half as many tiles as pairs and the experts' rows fill 64, tiles of fewer rows, down to 64
 // (dgrad of one expert, 256 rows, N 6144, K 2048: 33 -> 20 us; of four experts of 108 rows, N
 // 2040, K 224: 12.5 -> 10.6; wgrad of 4096 rows, N 256, K 1024: 23 -> 17; 16 experts of 48 rows
-// would lose 0.9 of 6.9 us).
-void choose_tiles(GroupedArgs &g, int op, int sms) {
+// would lose 0.9 of 6.9 us).  Stages of two blocks where a tile has so few rows that its waits and
+// commits take longer than its MMAs (one expert, 2048 rows, N 256, K 2048: 9.4 -> 8.4 us; dgrad of
+// 256 rows, N 6144, K 2048: 18.2 -> 15.8; wgrad of 8192 rows, N = K = 128: 28.8 -> 19.7; up to 128
+// rows the dgrad gains, 61.5 -> 59.6 for 48 rows each of 64 experts, and the forward loses, 62.7 -> 63.7).
+int choose_tiles(GroupedArgs &g, int op, bool one_block, int sms) {
     GroupedOut &o = g.o;
     const long long pairs = sms / 2, active = std::max<long long>(1, std::min(o.E, o.rows));
     const long long most = op == kWgrad ? o.m_dense : std::min<long long>(256, 2 * (o.rows / active) + 1);
@@ -391,9 +413,12 @@ void choose_tiles(GroupedArgs &g, int op, int sms) {
     const long long fill = op == kWgrad ? o.m_dense : o.rows / active;  // rows that an expert's tiles share
     while (o.tile_rows > 64 && fill >= 64 && 2 * row_tiles() * o.col_tiles <= pairs) o.tile_rows /= 2;
     o.row_tiles = (o.m_dense + o.tile_rows - 1) / o.tile_rows;
-    g.a_stage = o.cols / 2 * kRow;
-    g.b_stage = op == kWgrad ? (o.tile_rows / 2 + 63) / 64 * kChunk : o.tile_rows / 2 * kRow;
-    g.stages = std::min(kMaxStages, kStageSpace / (g.a_stage + g.b_stage));
+    const bool two = o.tile_rows <= (op == kDgrad ? 128 : 64);
+    const int blocks = two && !one_block ? 2 : 1;
+    g.a_block = o.cols / 2 * kRow;
+    g.b_block = op == kWgrad ? (o.tile_rows / 2 + 63) / 64 * kChunk : o.tile_rows / 2 * kRow;
+    g.stages = std::min(kMaxStages, kStageSpace / (blocks * (g.a_block + g.b_block)));
+    return blocks;
 }
 
 moe_status check(const char *op, const void *a, const void *b, const int32_t *offs, const void *out, int rows, int E,
@@ -438,7 +463,8 @@ moe_status launch(const char *name, int op, const void *x, const void *w, const 
     const int sms = op_num_sms();
     o.err = op_error_word();
     if (sms < 2 || o.err == nullptr) return op_fail(MOE_ERR_CUDA, "%s: no usable current device", name);
-    choose_tiles(g, op, sms);
+    const bool segments = (op == kWgrad ? rows : o.red) > o.segment;
+    const int blocks = choose_tiles(g, op, op == kWgrad ? accumulate != 0 : segments, sms);
     const long long tiles = op == kWgrad ? (long long)E * o.row_tiles * o.col_tiles
                                          : ((long long)rows / o.tile_rows + std::min(E, rows)) * o.col_tiles;
     if (tiles > (1ll << 30)) return op_fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^30 output tiles", name);
@@ -466,19 +492,25 @@ moe_status launch(const char *name, int op, const void *x, const void *w, const 
     };
     // sums of one segment have kernels without the walk over segments (128 experts of 16 rows, wgrad:
     // 16.4 against 16.9 us; 16 of 48, dgrad: 7.4 against 7.8)
-    const bool longer = (op == kWgrad ? rows : o.red) > o.segment;
+    // sums of one segment have kernels without the walk over segments (128 experts of 16 rows, wgrad:
+    // 16.4 against 16.9 us; 16 of 48, dgrad: 7.4 against 7.8)
     cudaError_t ce;
     if (op == kForward)
-        ce = longer ? go(grouped_kernel<kForward, false, true>, kThreads<kForward>, 0)
-                    : go(grouped_kernel<kForward, false, false>, kThreads<kForward>, 1);
+        ce = segments      ? go(grouped_kernel<kForward, 1, false, true>, kThreads<kForward>, 0)
+             : blocks == 1 ? go(grouped_kernel<kForward, 1, false, false>, kThreads<kForward>, 1)
+                           : go(grouped_kernel<kForward, 2, false, false>, kThreads<kForward>, 2);
     else if (op == kDgrad)
-        ce = longer ? go(grouped_kernel<kDgrad, false, true>, kThreads<kDgrad>, 2)
-                    : go(grouped_kernel<kDgrad, false, false>, kThreads<kDgrad>, 3);
+        ce = segments      ? go(grouped_kernel<kDgrad, 1, false, true>, kThreads<kDgrad>, 3)
+             : blocks == 1 ? go(grouped_kernel<kDgrad, 1, false, false>, kThreads<kDgrad>, 4)
+                           : go(grouped_kernel<kDgrad, 2, false, false>, kThreads<kDgrad>, 5);
     else if (accumulate)
-        ce = go(grouped_kernel<kWgrad, true, true>, kThreads<kWgrad>, 4);
+        ce = go(grouped_kernel<kWgrad, 1, true, true>, kThreads<kWgrad>, 6);
+    else if (segments)
+        ce = blocks == 1 ? go(grouped_kernel<kWgrad, 1, false, true>, kThreads<kWgrad>, 7)
+                         : go(grouped_kernel<kWgrad, 2, false, true>, kThreads<kWgrad>, 8);
     else
-        ce = longer ? go(grouped_kernel<kWgrad, false, true>, kThreads<kWgrad>, 5)
-                    : go(grouped_kernel<kWgrad, false, false>, kThreads<kWgrad>, 6);
+        ce = blocks == 1 ? go(grouped_kernel<kWgrad, 1, false, false>, kThreads<kWgrad>, 9)
+                         : go(grouped_kernel<kWgrad, 2, false, false>, kThreads<kWgrad>, 10);
     return op_cuda(ce, name);
 }
 

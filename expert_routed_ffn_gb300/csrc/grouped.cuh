@@ -189,7 +189,7 @@ __device__ __forceinline__ bool load_table(TileTable &tab) {
 // Longer sums reach an fp32 output in segments of so many reduction steps, added there in fp32 by
 // the thread that stored the one before.  The tensor core's additions truncate: 4096 steps are
 // 4.4e-6 (2-norm) from the exact sum, 8192 in one segment 9.1e-6 and 65536 7.6e-5; in segments
-// both stay at 4.4e-6 (8192 steps of 128 x 128 sums 29.6 against 27.7 us).
+// both stay at 4.4e-6.
 constexpr int kSegment = 4096;
 
 // Walks a CTA pair's tiles first, first + stride, .. (a converged warp), numbered with the column

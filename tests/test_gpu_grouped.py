@@ -331,3 +331,33 @@ def test_long_sums_keep_their_precision(op):
     if op == "wgrad":  # added to what is there: one more rounding of fp32 sums twice as large
         _call(op, A, B, offs, out=again, accumulate=True)
         assert bool(((again.double() - 2 * ref).abs() <= 2.0 ** -15 * 2 * ref).all())
+
+
+LENGTHS = [1, 15, 16, 17, 63, 64, 65, 79, 127, 128, 129, 143, 191, 192, 193, 255, 256, 257, 999, 0]
+
+
+@pytest.mark.parametrize("rows", [64, 200])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_wgrad_sums_of_every_length(rows, dtype):
+    """Sums that end anywhere in a stage, for tiles of few rows and of many; the rows around an
+    expert's hold NaN in turn, which its own sum may not meet."""
+    gen = torch.Generator(device="cuda").manual_seed(52)
+    dY, X, offs = _bf16(gen, sum(LENGTHS), rows), _bf16(gen, sum(LENGTHS), 136), _offs(LENGTHS)
+    ref, mag, num = _reference("wgrad", dY, X, offs, (len(LENGTHS), rows, 136))
+    for odd in (0, 1):
+        a, b = dY.clone(), X.clone()
+        for e in range(odd, len(LENGTHS), 2):
+            a[offs[e]:offs[e + 1]] = b[offs[e]:offs[e + 1]] = float("nan")
+        mine = [e for e in range(1 - odd, len(LENGTHS), 2)]
+        _check(_call("wgrad", a, b, offs, out_dtype=dtype)[mine], ref[mine], mag[mine], num[mine])
+
+
+@pytest.mark.parametrize("counts", [[1, 0, 33, 2], [100, 0, 120, 3], [300, 500]])
+@pytest.mark.parametrize("length", [8, 56, 64, 72, 120, 128, 136, 192, 200, 1000])
+@pytest.mark.parametrize("op", ["forward", "dgrad"])
+def test_sums_of_every_length(op, length, counts):
+    gen = torch.Generator(device="cuda").manual_seed(53)
+    A = _bf16(gen, sum(counts), length)
+    B = _bf16(gen, *((len(counts), 264, length) if op == "forward" else (len(counts), length, 264)))
+    got = _call(op, A, B, _offs(counts), out_dtype=torch.float32)
+    _check(got, *_reference(op, A, B, _offs(counts), tuple(got.shape)))
