@@ -22,6 +22,7 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
 constexpr int kMaxDevices = 64;
 std::mutex g_mutex;
 int g_sms[kMaxDevices];
+std::atomic<int *> g_error_word[kMaxDevices];  // where g_op_error lies on each
 std::atomic<long long> g_wait_limit{-1};
 
 }  // namespace
@@ -89,8 +90,14 @@ CUresult op_encode(CUtensorMap *m, const OpMap &d) {
 long long op_wait_limit() { return g_wait_limit.load(std::memory_order_relaxed); }
 
 int *op_error_word() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+    int *word = g_error_word[dev].load(std::memory_order_relaxed);
+    if (word != nullptr) return word;
     void *p = nullptr;
-    return cudaGetSymbolAddress(&p, g_op_error) == cudaSuccess ? static_cast<int *>(p) : nullptr;
+    if (cudaGetSymbolAddress(&p, g_op_error) != cudaSuccess) return nullptr;
+    g_error_word[dev].store(static_cast<int *>(p), std::memory_order_relaxed);
+    return static_cast<int *>(p);
 }
 
 }  // namespace moe
