@@ -35,13 +35,13 @@
 // when both CTAs have zeroed.
 //
 // What bounds it, measured on GB300 (bf16; 64 experts, N 1408, K 2048):
-//   forward, 24576 rows    108 us, 1.31 PFLOP/s, 5.0 TB/s: the tensor pipe is 76% busy at the 1.6
+//   forward, 24576 rows    104 us, 1.36 PFLOP/s, 5.2 TB/s: the tensor pipe is 76% busy at the 1.6
 //                          GHz the SM clock settles to, and HBM 63%; the first two waves of tiles
 //                          wait for weights
-//   dgrad, 24576 rows on a few experts   112 us; of 1408 columns the sixth tile is half empty
+//   dgrad, 24576 rows      103 us; of 1408 columns the sixth tile is half empty
 //   wgrad, 24576 rows, fp32 out   147 us, 6.2 TB/s: the 738 MB it writes
-//   forward, 384 rows      60 us, 6.2 TB/s: the weights, streamed once
-//   forward, one expert, 16384 rows, K 1408, N 2048   54 us, 1.75 PFLOP/s
+//   forward, 384 rows      57 us, 6.5 TB/s: the weights, streamed once
+//   forward, one expert, 16384 rows, K 1408, N 2048   53 us, 1.78 PFLOP/s
 //   forward, one token's six experts   8 us in a row of calls: start and end of the launch around
 //                          35 MB
 // One CTA per 128 x 256 tile with the rows as M took 128 (forward), 145 and 181 us.

@@ -26,11 +26,11 @@
 // Tensor memory (512 columns): two accumulators of up to 192 columns, then per stage the
 // scales of the weights (8 columns) and of the tokens (8 per 128 of them).
 //
-// Measured on GB300 (64 experts, N 1408, K 2048): 24576 rows 46 us, 3.1 PFLOP/s, 4.2 TB/s; 384
-// rows 21 us, 4.8 TB/s; one expert, 8192 rows, N and K 2048: 20 us, 3.4 PFLOP/s.  The copies of
-// codes and the stores bound it: without products it takes 42 of the 46 us (L2 delivers 9.3 TB/s;
-// the tensor pipe is 40% busy).  Tiles of 224 rows, for which tensor memory has room for two
-// stages' scales beside the accumulators, took the same time.
+// Measured on GB300 (64 experts, N 1408, K 2048): 24576 rows 44 us, 3.2 PFLOP/s, 4.4 TB/s; 384
+// rows 18 us, 5.5 TB/s (part of it from L2; 23 us from HBM); one expert, 8192 rows, N and K 2048:
+// 19 us, 3.6 PFLOP/s.  The copies of codes and the stores bound it: without products it takes 4 us
+// less (L2 delivers 9.3 TB/s; the tensor pipe is 40% busy).  Tiles of 224 rows, for which tensor
+// memory has room for two stages' scales beside the accumulators, took the same time.
 #include <algorithm>
 
 #include "common.cuh"
