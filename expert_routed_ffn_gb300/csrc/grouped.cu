@@ -110,7 +110,8 @@ __device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr) {
 __device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
 }
-// BLOCKS: most blocks of 64 reduction steps of a stage; ADD: to what the output holds (wgrad); SEGMENTS: sums may come in several (grouped.cuh)
+// BLOCKS: most blocks of 64 reduction steps of a stage; ADD: to what the output holds (wgrad);
+// SEGMENTS: a sum may come in several (grouped.cuh)
 template <int OP, int BLOCKS, bool ADD, bool SEGMENTS>
 __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_constant__ GroupedArgs p) {
     constexpr bool kDense = OP == kWgrad;
