@@ -70,6 +70,7 @@ constexpr int kParts = 2;
 constexpr int kEpiWarps = kQuads * kParts;
 template <int OP>
 constexpr int kThreads = 64 + 32 * kEpiWarps + (OP == kWgrad ? 32 : 0);  // the wgrad's last warp zeroes tails
+static_assert(kThreads<kForward> >= kMaxExperts, "load_table: a thread per expert");
 constexpr int kAccCols = 256;          // TMEM columns of one accumulator
 constexpr uint32_t kTmemCols = 2 * kAccCols;
 constexpr int kRow = kBK * 2;          // bytes of a K-major row, or of 64 columns in MN-major

@@ -144,6 +144,7 @@ __device__ __forceinline__ void transpose(uint32_t from, uint32_t run, uint32_t 
 // First warp of the transposing role
 __host__ __device__ constexpr int transpose_warp(bool tma) { return kFetch + (tma ? 1 : 4); }
 __host__ __device__ constexpr int num_threads(bool tma) { return 32 * (transpose_warp(tma) + 4 * kSets); }
+static_assert(num_threads(true) >= kMaxExperts, "load_table: a thread per expert");
 
 // TMA: scales are fetched by TMA
 template <bool TMA>

@@ -385,7 +385,8 @@ moe_status moe_operators_status(void);
 moe_status moe_operators_wait_limit(long long cycles);
 
 /* Grouped products.  X [rows, K], dY [rows, N] and W [E, N, K] are bf16; out_dtype
- * (moe_dtype) is the type of the result, bf16 or fp32.  Sums are fp32, rounded once.
+ * (moe_dtype) is the type of the result, bf16 or fp32.  Sums are fp32, rounded once to bf16; to
+ * an fp32 result they are added every 4096 products.
  * Limits: 1 <= E <= 256; N and K multiples of 8, up to 2^20; rows up to 2^30, else
  * MOE_ERR_UNSUPPORTED.  An output that overlaps an input is refused.
  *   forward: Y [rows, N],  Y[r, :]  = W[e] X[r, :]

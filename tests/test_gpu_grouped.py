@@ -361,3 +361,17 @@ def test_sums_of_every_length(op, length, counts):
     B = _bf16(gen, *((len(counts), 264, length) if op == "forward" else (len(counts), length, 264)))
     got = _call(op, A, B, _offs(counts), out_dtype=torch.float32)
     _check(got, *_reference(op, A, B, _offs(counts), tuple(got.shape)))
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_long_sum_among_many_experts(accumulate):
+    """One expert's sum takes three segments, in tiles of full height; the others' take one.
+    Tolerance as in test_long_sums_keep_their_precision."""
+    gen = torch.Generator(device="cuda").manual_seed(54)
+    counts = [3] * 20 + [8209] + [0, 70] * 10
+    dY, X, offs = _bf16(gen, sum(counts), 256).abs(), _bf16(gen, sum(counts), 264).abs(), _offs(counts)
+    ref, _, _ = _reference("wgrad", dY, X, offs, (len(counts), 256, 264))
+    out = torch.ones_like(ref, dtype=torch.float32)
+    _call("wgrad", dY, X, offs, out=out, accumulate=accumulate)
+    ref = ref + (1.0 if accumulate else 0.0)
+    assert bool(((out.double() - ref).abs() <= 2.0 ** -15 * ref).all())
