@@ -246,7 +246,8 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
             constexpr uint32_t kStepB = OP == kWgrad ? (16 * kRow) >> 4 : 2;    // in units of 16 bytes
             const uint64_t desc_a = OP == kForward ? smem_desc_k128(sA) : smem_desc_mn128(sA);
             const uint64_t desc_b = kDense ? smem_desc_mn128(sB) : smem_desc_k128(sB);
-            uint32_t n_acc = 0, ph = 0, zeroed_ph = 0;
+            Accumulators accs;
+            uint32_t ph = 0, zeroed_ph = 0;
             int s = 0;
             bool ok = p.o.wait != 0, issued = false;  // a bound of 0: give up at once
             TileWalk<kDense, SEGMENTS> walk(tab, first, stride);
@@ -263,8 +264,8 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
                     continue;
                 }
                 const uint32_t idesc = idesc_bf16_f32(256, t.n) | (OP != kForward ? 1u << 15 : 0u) | (kDense ? 1u << 16 : 0u);
-                const uint32_t a = n_acc & 1u, d = tmem_base + a * kAccCols;
-                if (!__all_sync(0xffffffffu, wait_bar<true>(tempty_bar(a), ((n_acc >> 1) & 1u) ^ 1u, p.o.wait, abort_flag))) {
+                const uint32_t a = accs.next, d = tmem_base + a * kAccCols;
+                if (!__all_sync(0xffffffffu, wait_bar<true>(tempty_bar(a), accs.take(), p.o.wait, abort_flag))) {
                     ok = false;
                     break;
                 }
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
                         ph ^= 1u;
                     }
                 }
-                ++n_acc;
+                accs.done(t);
             }
             if (!ok && lane == 0) {
                 raise();
@@ -349,32 +350,37 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
     } else {
         const int q = warp & 3;  // the TMEM lane quadrant this warp may read
         const int in_half = 32 * q + lane;  // column within this CTA's half
-        uint32_t n_acc = 0;
+        const int part = (warp - 2) >> 2;
+        const bool mine = 32 * q < half_cols;
+        Accumulators accs;
+        auto release = [&](uint32_t a) {  // the MMA may write accumulator a
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_bar(a), 0));
+        };
         for (TileWalk<kDense, SEGMENTS> walk(tab, first, stride); walk.more(); walk.next()) {
             const Tile t = walk.get();
             const bool empty = t.r0 >= t.r1;
-            const uint32_t a = n_acc & 1u;
+            const uint32_t a = accs.next, tmem_q = tmem_base + ((uint32_t)(q * 32) << 16);
+            const int col = t.col0 + rank * half_cols + in_half;
             if (!empty) {
-                if (!__all_sync(0xffffffffu, wait_bar<true>(tfull_bar(a), (n_acc >> 1) & 1u, p.o.wait, abort_flag))) {
+                if (!__all_sync(0xffffffffu, wait_bar<true>(tfull_bar(a), accs.ready(), p.o.wait, abort_flag))) {
                     if (lane == 0) raise();
                     break;
                 }
                 tc_fence_after();
             }
-            if (32 * q < half_cols) {
-                const uint32_t acc = tmem_base + ((uint32_t)(q * 32) << 16) + a * kAccCols;
-                const int col = t.col0 + rank * half_cols + in_half, part = (warp - 2) >> 2;
-                if (SEGMENTS && !ADD && t.add)
-                    store_tile<kDense, true, kParts>(tab.o, t, acc, empty, col, part, lane);
-                else
-                    store_tile<kDense, ADD, kParts>(tab.o, t, acc, empty, col, part, lane);
+            uint32_t from = a;
+            if (SEGMENTS && !(t.first && t.last)) {
+                from = a ^ 1u;
+                if (mine) add_segment<kDense, kParts>(tab.o, t, tmem_q + a * kAccCols, tmem_q + from * kAccCols, part);
+                release(a);
             }
-            if (!empty) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_bar(a), 0));
-                ++n_acc;
+            if (!SEGMENTS || t.last) {
+                if (mine) store_tile<kDense, ADD, kParts>(tab.o, t, tmem_q + from * kAccCols, empty, col, part, lane);
+                if (!empty) release(from);
             }
+            if (!empty) accs.done(t);
         }
     }
 
@@ -386,7 +392,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
     }
 }
 
-unsigned long long g_attr[11];
+unsigned long long g_attr[12];
 
 // Tile sizes.  Rows: up to 256, fewer where the experts average fewer.  Columns: 256, or 128 (64
 // per CTA) where there are no more (with 256, 0.1 us slower).  128 where 256 leave CTA pairs
@@ -452,7 +458,7 @@ moe_status launch(const char *name, int op, const void *x, const void *w, const 
     o.m_dense = N;
     o.red = op == kForward ? K : N;
     o.f32 = dtype == MOE_DTYPE_F32;
-    o.segment = o.f32 ? kSegment : 1 << 30;
+    o.segment = segment_of(o.f32, 16);
     o.wait = wait_cycles((op == kWgrad ? rows : o.red) / kBK + 1);
     const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
@@ -494,8 +500,6 @@ moe_status launch(const char *name, int op, const void *x, const void *w, const 
     };
     // sums of one segment have kernels without the walk over segments (128 experts of 16 rows, wgrad:
     // 16.4 against 16.9 us; 16 of 48, dgrad: 7.4 against 7.8)
-    // sums of one segment have kernels without the walk over segments (128 experts of 16 rows, wgrad:
-    // 16.4 against 16.9 us; 16 of 48, dgrad: 7.4 against 7.8)
     cudaError_t ce;
     if (op == kForward)
         ce = segments      ? go(grouped_kernel<kForward, 1, false, true>, kThreads<kForward>, 0)
@@ -506,7 +510,8 @@ moe_status launch(const char *name, int op, const void *x, const void *w, const 
              : blocks == 1 ? go(grouped_kernel<kDgrad, 1, false, false>, kThreads<kDgrad>, 4)
                            : go(grouped_kernel<kDgrad, 2, false, false>, kThreads<kDgrad>, 5);
     else if (accumulate)
-        ce = go(grouped_kernel<kWgrad, 1, true, true>, kThreads<kWgrad>, 6);
+        ce = segments ? go(grouped_kernel<kWgrad, 1, true, true>, kThreads<kWgrad>, 6)
+                      : go(grouped_kernel<kWgrad, 1, true, false>, kThreads<kWgrad>, 11);
     else if (segments)
         ce = blocks == 1 ? go(grouped_kernel<kWgrad, 1, false, true>, kThreads<kWgrad>, 7)
                          : go(grouped_kernel<kWgrad, 2, false, true>, kThreads<kWgrad>, 8);

@@ -37,14 +37,14 @@ struct GroupedOut {
     int col_tiles;   // tiles along the output columns
     int row_tiles;   // dense: tiles along m_dense
     int f32;         // output type: fp32, else bf16
-    int segment;     // reduction steps summed in tensor memory before they go to the output
+    int segment;     // reduction steps that one accumulator sums, see segment_of
     long long wait;  // bound of every wait in SM cycles, see wait_cycles
 };
 
 struct Tile {
     int e, row0, rows, n, col0;  // expert, first output row, valid rows, MMA N, first output column
-    int r0, r1;                  // reduction range
-    bool add;                    // not the output's first segment
+    int r0, r1;                  // reduction range: the sum's, or one segment's
+    bool first, last;            // of its sum's segments
 };
 
 __device__ __forceinline__ void fence_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -186,11 +186,40 @@ __device__ __forceinline__ bool load_table(TileTable &tab) {
     return ok;
 }
 
-// Longer sums reach an fp32 output in segments of so many reduction steps, added there in fp32 by
-// the thread that stored the one before.  The tensor core's additions truncate: 4096 steps are
-// 4.4e-6 (2-norm) from the exact sum, 8192 in one segment 9.1e-6 and 65536 7.6e-5; in segments
-// both stay at 4.4e-6.
-constexpr int kSegment = 4096;
+// The tensor core's additions truncate, so a sum's error grows with the number of instructions that
+// add to one accumulator: 256 of them are up to 1.4e-5 off (products of one sign; 4.4e-6 of mixed
+// ones), 4096 3.6e-4, 65536 6e-3, more than bf16's own rounding.  Longer sums are taken in segments,
+// added to nearest in tensor memory, and the error stays that of one: of 256 instructions for fp32
+// results, and for bf16 ones of 1024, at most 2^-14, a 64th of half a bf16 step.  `step`: products
+// that an instruction adds.
+__host__ __device__ constexpr int segment_of(bool f32, int step) { return (f32 ? 256 : 1024) * step; }
+
+// What a role knows of the two accumulators: which one the next tile takes, and the parity of
+// each one's next phase as full and as empty.  A sum of several segments takes one for all its
+// segments and the other for their running sum, which frees that other when it has been stored;
+// the next tile takes the first again, since that is free sooner.
+struct Accumulators {
+    uint32_t next = 0, full = 0, empty = 0;
+    // MMA: the parity to wait for before a segment's products
+    __device__ __forceinline__ uint32_t take() {
+        const uint32_t parity = (empty >> next & 1u) ^ 1u;
+        empty ^= 1u << next;
+        return parity;
+    }
+    // epilogue: the parity to wait for before a segment's sums are read
+    __device__ __forceinline__ uint32_t ready() {
+        const uint32_t parity = full >> next & 1u;
+        full ^= 1u << next;
+        return parity;
+    }
+    // after a segment: the MMA counts the running sum's release, which it waits for in take()
+    __device__ __forceinline__ void done(const Tile &t) {
+        if (t.first && t.last)
+            next ^= 1u;
+        else if (t.last)
+            empty ^= 1u << (next ^ 1u);
+    }
+};
 
 // Walks a CTA pair's tiles first, first + stride, .. (a converged warp), numbered with the column
 // tile innermost: the position is kept in digits, so that a step takes no division (one took a
@@ -239,6 +268,7 @@ struct TileWalk {
             t.rows = min(p.tile_rows, p.m_dense - t.row0);
             t.r0 = tab.offs[e] + at;
             t.r1 = SEGMENTS ? t.r0 + min(tab.offs[e + 1] - t.r0, p.segment) : tab.offs[e + 1];
+            t.last = !SEGMENTS || t.r1 == tab.offs[e + 1];
         } else {
             // the last expert whose first row tile is <= r (one with rows: the next ones start later)
             constexpr int kPer = kMaxExperts / 32;
@@ -251,12 +281,57 @@ struct TileWalk {
             t.rows = min(share, tab.offs[t.e + 1] - t.row0);
             t.r0 = at;
             t.r1 = SEGMENTS ? at + min(p.red - at, p.segment) : p.red;
+            t.last = !SEGMENTS || t.r1 == p.red;
         }
         t.n = (t.rows + 31) & ~31;
-        t.add = SEGMENTS && at > 0;
+        t.first = !SEGMENTS || at == 0;
         return t;
     }
 };
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// fp32 weight gradients are bound by their own stores: with both warps storing, their bursts
+// delay the operand loads (160 against 166 us; bf16 ones 26.6 against 24.6 us the other way)
+template <bool DENSE, int PARTS>
+__device__ __forceinline__ int storing_parts(const GroupedOut &p) {
+    return DENSE && p.f32 ? 1 : PARTS;
+}
+
+// Add a segment's accumulator to the running sum of its tile (fp32, to nearest): by the warp, and
+// in the chunks, that store_tile then stores.
+template <bool DENSE, int PARTS>
+__device__ __forceinline__ void add_segment(const GroupedOut &p, const Tile &t, uint32_t acc, uint32_t run, int part) {
+    const int parts = storing_parts<DENSE, PARTS>(p);
+    if (part >= parts) return;
+    for (int c = 32 * part; c < t.rows; c += 32 * parts) {
+        uint32_t v[32], sum[32];
+        tmem_ld32(acc + c, v);
+        if (!t.first) tmem_ld32(run + c, sum);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));  // not read before the wait
+        if (!t.first) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                asm volatile("" : "+r"(sum[i]));
+                v[i] = __float_as_uint(__uint_as_float(sum[i]) + __uint_as_float(v[i]));
+            }
+        }
+        tmem_st32(run + c, v);
+    }
+    tmem_st_wait();
+}
 
 // A tile's epilogue by one warp: TMEM lane = output column `col` (its own lane's), column = row.
 // `tcol`: the accumulator, at the warp's lane quadrant; `empty`: there is no sum, zeros are
@@ -265,9 +340,7 @@ struct TileWalk {
 template <bool DENSE, bool ADD, int PARTS>
 __device__ __forceinline__ void store_tile(const GroupedOut &p, const Tile &t, uint32_t tcol, bool empty, int col,
                                            int part, int lane) {
-    // fp32 weight gradients are bound by their own stores: with both warps storing, their bursts
-    // delay the operand loads (160 against 166 us; bf16 ones 26.6 against 24.6 us the other way)
-    const int parts = DENSE && p.f32 ? 1 : PARTS;
+    const int parts = storing_parts<DENSE, PARTS>(p);
     if ((ADD && empty) || part >= parts) return;
     const bool ok = col < p.n_out;
     const size_t row0 = (DENSE ? (size_t)t.e * p.m_dense : 0) + t.row0;

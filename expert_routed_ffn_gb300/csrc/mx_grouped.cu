@@ -66,6 +66,8 @@ struct Header {
     volatile int abort;
 };
 constexpr int kHeaderBytes = 4096;
+static_assert(segment_of(true, 64) % (kFetchStages * kBK) == 0 && segment_of(false, 64) % (kFetchStages * kBK) == 0,
+              "a segment's scales are whole fetches");
 constexpr int kSmemBytes = kHeaderBytes + kStageSpace + kRaw * kRawBytes + 16;  // (a word behind the last run is read)
 static_assert(sizeof(Header) <= kHeaderBytes && kSmemBytes <= 232448, "shared memory of one CTA");
 
@@ -146,8 +148,8 @@ __host__ __device__ constexpr int transpose_warp(bool tma) { return kFetch + (tm
 __host__ __device__ constexpr int num_threads(bool tma) { return 32 * (transpose_warp(tma) + 4 * kSets); }
 static_assert(num_threads(true) >= kMaxExperts, "load_table: a thread per expert");
 
-// TMA: scales are fetched by TMA
-template <bool TMA>
+// TMA: scales are fetched by TMA; SEGMENTS: a sum comes in several (grouped.cuh)
+template <bool TMA, bool SEGMENTS>
 __global__ void __launch_bounds__(num_threads(TMA), 1) mx_grouped_kernel(const __grid_constant__ MxGroupedArgs p) {
     constexpr int kTranspose = transpose_warp(TMA);
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -217,18 +219,21 @@ __global__ void __launch_bounds__(num_threads(TMA), 1) mx_grouped_kernel(const _
     const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
     const int half_cols = tab.o.cols / 2, atoms = p.atoms;
     const uint32_t w_run = half_cols, x_run = p.x_run;  // fetched bytes of a block's scales
-    const int K = tab.o.red, k_stages = (K + kBK - 1) / kBK;
+    const int K = tab.o.red;
+    // stages of a sum, or of a segment of it, which begins and ends between two fetches of scales
+    auto first_stage = [](const Tile &t) { return t.r0 / kBK; };
+    auto end_stage = [](const Tile &t) { return (t.r1 + kBK - 1) / kBK; };
 
     if (warp == 0) {
         uint32_t ph = 1;
         int s = 0;
         bool ok = true;
-        for (TileWalk<false, false> walk(tab, first, stride); ok && walk.more(); walk.next()) {
+        for (TileWalk<false, SEGMENTS> walk(tab, first, stride); ok && walk.more(); walk.next()) {
             const Tile t = walk.get();
             const int col = t.col0 + rank * half_cols, row = t.row0 + rank * (t.n / 2);
             const CUtensorMap *map_b = &p.map_b[t.n / 32 - 1];
             const uint32_t bytes = a_stage + (t.n / 2) * kRow;
-            for (int k = 0; k < k_stages; ++k) {
+            for (int k = first_stage(t); k < end_stage(t); ++k) {
                 if (!__all_sync(0xffffffffu, wait_bar(empty_bar(s), ph, p.o.wait, abort_flag))) {
                     ok = false;
                     break;
@@ -253,22 +258,24 @@ __global__ void __launch_bounds__(num_threads(TMA), 1) mx_grouped_kernel(const _
             const uint32_t cols_s = 8 + 8 * atoms;  // scale columns of a stage
             const uint32_t scale0 = tmem_base + 2 * acc_cols;
             const uint64_t desc_a = smem_desc_k128(sA), desc_b = smem_desc_k128(sB), desc_s = scale_desc(sS);
-            uint32_t n_acc = 0, ph = 0;
+            Accumulators accs;
+            uint32_t ph = 0;
             int s = 0;
             bool ok = p.o.wait != 0, issued = false;  // a bound of 0: give up at once
-            TileWalk<false, false> walk(tab, first, stride);
+            TileWalk<false, SEGMENTS> walk(tab, first, stride);
             Tile next;
             if (walk.more()) next = walk.get();
             while (ok && walk.more()) {
                 const Tile t = next;
                 const uint32_t idesc = idesc_mxf4(256, t.n);
-                const uint32_t a = n_acc & 1u, d = tmem_base + a * acc_cols;
-                if (!__all_sync(0xffffffffu, wait_bar<true>(tempty_bar(a), ((n_acc >> 1) & 1u) ^ 1u, p.o.wait, abort_flag))) {
+                const uint32_t a = accs.next, d = tmem_base + a * acc_cols;
+                if (!__all_sync(0xffffffffu, wait_bar<true>(tempty_bar(a), accs.take(), p.o.wait, abort_flag))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                for (int k = 0; k < k_stages; ++k) {
+                const int k0 = first_stage(t), k1 = end_stage(t);
+                for (int k = k0; k < k1; ++k) {
                     if (!__all_sync(0xffffffffu, wait_bar<true>(full_bar(s), ph, p.o.wait, abort_flag))) {
                         ok = false;
                         break;
@@ -291,14 +298,14 @@ __global__ void __launch_bounds__(num_threads(TMA), 1) mx_grouped_kernel(const _
                             if (64 * i >= left) break;
                             const uint32_t half = (uint32_t)(i & 1) * 2u;  // the step's two blocks within the word
                             tc_mma_mxf4_pair(d, ad + 2 * i, bd + 2 * i, idesc | half << 29 | half << 4, ta + 4 * (i >> 1),
-                                             tb + 4 * atoms * (i >> 1), (k | i) != 0);
+                                             tb + 4 * atoms * (i >> 1), (k != k0) | (i != 0));
                         }
                         tc_commit_pair(empty_bar(s), 3);
-                        if (k + 1 == k_stages) tc_commit_pair(tfull_bar(a), 3);
+                        if (k + 1 == k1) tc_commit_pair(tfull_bar(a), 3);
                     }
                     __syncwarp();
                     issued = true;
-                    if (k == 0) {  // the next tile's place, while this one's products run
+                    if (k == k0) {  // the next tile's place, while this one's products run
                         walk.next();
                         if (walk.more()) next = walk.get();
                     }
@@ -307,7 +314,7 @@ __global__ void __launch_bounds__(num_threads(TMA), 1) mx_grouped_kernel(const _
                         ph ^= 1u;
                     }
                 }
-                ++n_acc;
+                accs.done(t);
             }
             if (!ok && lane == 0) {
                 raise();
@@ -319,29 +326,43 @@ __global__ void __launch_bounds__(num_threads(TMA), 1) mx_grouped_kernel(const _
         }
     } else if (warp < 2 + kEpiWarps) {
         const int q = warp & 3;  // the TMEM lane quadrant this warp may read
-        uint32_t n_acc = 0;
-        for (TileWalk<false, false> walk(tab, first, stride); walk.more(); walk.next(), ++n_acc) {
+        const uint32_t tmem_q = tmem_base + ((uint32_t)(q * 32) << 16), acc_cols = tab.o.tile_rows;
+        const bool mine = 32 * q < half_cols;
+        Accumulators accs;
+        auto release = [&](uint32_t a) {  // the MMA may write accumulator a
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_bar(a), 0));
+        };
+        for (TileWalk<false, SEGMENTS> walk(tab, first, stride); walk.more(); walk.next()) {
             const Tile t = walk.get();
-            const uint32_t a = n_acc & 1u;
-            if (!__all_sync(0xffffffffu, wait_bar<true>(tfull_bar(a), (n_acc >> 1) & 1u, p.o.wait, abort_flag))) {
+            const uint32_t a = accs.next;
+            if (!__all_sync(0xffffffffu, wait_bar<true>(tfull_bar(a), accs.ready(), p.o.wait, abort_flag))) {
                 if (lane == 0) raise();
                 break;
             }
             tc_fence_after();
-            if (32 * q < half_cols)
-                store_tile<false, false, 1>(tab.o, t, tmem_base + ((uint32_t)(q * 32) << 16) + a * tab.o.tile_rows, false,
-                                  t.col0 + rank * half_cols + 32 * q + lane, 0, lane);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_bar(a), 0));
+            uint32_t from = a;
+            if (SEGMENTS && !(t.first && t.last)) {
+                from = a ^ 1u;
+                if (mine) add_segment<false, 1>(tab.o, t, tmem_q + a * acc_cols, tmem_q + from * acc_cols, 0);
+                release(a);
+            }
+            if (!SEGMENTS || t.last) {
+                if (mine)
+                    store_tile<false, false, 1>(tab.o, t, tmem_q + from * acc_cols, false,
+                                                t.col0 + rank * half_cols + 32 * q + lane, 0, lane);
+                release(from);
+            }
+            accs.done(t);
         }
     } else if (TMA && warp == kFetch) {
         int raw = 0;
         uint32_t ph = 1;
         bool ok = true;
-        for (TileWalk<false, false> walk(tab, first, stride); ok && walk.more(); walk.next()) {
+        for (TileWalk<false, SEGMENTS> walk(tab, first, stride); ok && walk.more(); walk.next()) {
             const Tile t = walk.get();
-            for (int b0 = 0; b0 < K / 32; b0 += kFetchBlocks) {
+            for (int b0 = t.r0 / 32; b0 < t.r1 / 32; b0 += kFetchBlocks) {
                 if (!__all_sync(0xffffffffu, wait_bar(raw_empty_bar(raw), ph, p.o.wait, abort_flag))) {
                     ok = false;
                     break;
@@ -372,16 +393,16 @@ __global__ void __launch_bounds__(num_threads(TMA), 1) mx_grouped_kernel(const _
         int raw = 0;
         uint32_t ph = 1;
         bool ok = true;
-        for (TileWalk<false, false> walk(tab, first, stride); ok && walk.more(); walk.next()) {
+        for (TileWalk<false, SEGMENTS> walk(tab, first, stride); ok && walk.more(); walk.next()) {
             const Tile t = walk.get();
             const int col = t.col0 + rank * half_cols + w0;
-            const uint8_t *ws = p.ws + ((size_t)t.e * n_blocks + b) * n_out + col;
+            const uint8_t *ws = p.ws + ((size_t)t.e * n_blocks + t.r0 / 32 + b) * n_out + col;
             // n_out and half_cols are multiples of 8 and 64: a word is inside or outside
             const bool w_in[2] = {w0 < half_cols && col < n_out, w0 + 64 < half_cols && col + 64 < n_out};
-            const size_t at = (size_t)b * rows + t.row0;
+            const size_t at = (size_t)(t.r0 / 32 + b) * rows + t.row0;
             const uint8_t *xs = p.xs + (at & ~(size_t)3) + w0;
             const int x_bytes = (int)(at & 3) + t.rows - w0;  // of the run from this thread's first word on
-            for (int b0 = 0; b0 < n_blocks; b0 += kFetchBlocks) {
+            for (int b0 = t.r0 / 32; b0 < t.r1 / 32; b0 += kFetchBlocks) {
                 if (!__all_sync(0xffffffffu, wait_bar(raw_empty_bar(raw), ph, p.o.wait, abort_flag))) {
                     ok = false;
                     break;
@@ -422,10 +443,11 @@ __global__ void __launch_bounds__(num_threads(TMA), 1) mx_grouped_kernel(const _
         int s = 0, raw = 0;
         uint32_t ph = 1, raw_ph = 0;
         bool ok = true;
-        for (TileWalk<false, false> walk(tab, first, stride); ok && walk.more(); walk.next()) {
+        for (TileWalk<false, SEGMENTS> walk(tab, first, stride); ok && walk.more(); walk.next()) {
             const Tile t = walk.get();
             const uint32_t x_at = (uint32_t)t.row0 & (TMA ? 15u : 3u);
-            for (int k = 0; k < k_stages; ++k) {
+            const int k1 = end_stage(t);
+            for (int k = first_stage(t); k < k1; ++k) {
                 const int f = k % kFetchStages;
                 if (f == 0 && !__all_sync(0xffffffffu, wait_bar(raw_full_bar(raw), raw_ph, p.o.wait, abort_flag))) {
                     ok = false;
@@ -455,7 +477,7 @@ __global__ void __launch_bounds__(num_threads(TMA), 1) mx_grouped_kernel(const _
                     __syncwarp();
                     if (lane == 0) mbar_arrive_pair(mapa_shared(full_bar(s), 0));
                 }
-                if (f + 1 == kFetchStages || k + 1 == k_stages) {
+                if (f + 1 == kFetchStages || k + 1 == k1) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(raw_empty_bar(raw));
                     if (++raw == kRaw) {
@@ -480,7 +502,7 @@ __global__ void __launch_bounds__(num_threads(TMA), 1) mx_grouped_kernel(const _
     }
 }
 
-unsigned long long g_attr[2];
+unsigned long long g_attr[4];
 
 // Tile sizes, by the bf16 products' rule: rows up to 192, fewer where the experts average fewer;
 // 256 columns, or 128 where there are no more (128 where 256 leave CTA pairs without a tile: 11.4
@@ -542,6 +564,7 @@ extern "C" moe_status moe_mx_grouped_forward(const void *Xc, const uint8_t *Xs, 
     o.n_out = N;
     o.red = K;
     o.f32 = out_dtype == MOE_DTYPE_F32;
+    o.segment = segment_of(o.f32, 64);
     o.wait = wait_cycles(K / kBK + 1);
     g.xs = Xs;
     g.ws = Ws;
@@ -559,8 +582,10 @@ extern "C" moe_status moe_mx_grouped_forward(const void *Xc, const uint8_t *Xs, 
         cr = op_encode(&g.map_ws, {u8, 3, Ws, {n, b, e}, {n, n * b}, {(uint32_t)o.cols / 2, kFetchBlocks, 1}, flat});
     if (tma && cr == CUDA_SUCCESS) cr = op_encode(&g.map_xs, {u8, 2, Xs, {r, b}, {r}, {g.x_run, kFetchBlocks}, flat});
     if (cr != CUDA_SUCCESS) return op_fail(MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", op, (int)cr);
-    auto kernel = tma ? mx_grouped_kernel<true> : mx_grouped_kernel<false>;
-    cudaError_t ce = op_allow_smem(reinterpret_cast<const void *>(kernel), kSmemBytes, &g_attr[tma]);
+    const bool segments = K > o.segment;
+    auto kernel = segments ? (tma ? mx_grouped_kernel<true, true> : mx_grouped_kernel<false, true>)
+                           : (tma ? mx_grouped_kernel<true, false> : mx_grouped_kernel<false, false>);
+    cudaError_t ce = op_allow_smem(reinterpret_cast<const void *>(kernel), kSmemBytes, &g_attr[2 * segments + tma]);
     if (ce == cudaSuccess)
         ce = launch_pdl_cluster(kernel, dim3(2u * (unsigned)std::min<long long>(sms / 2, tiles)), dim3(num_threads(tma)),
                                 (size_t)kSmemBytes, reinterpret_cast<cudaStream_t>(stream), dim3(2, 1, 1), g);

@@ -385,8 +385,10 @@ moe_status moe_operators_status(void);
 moe_status moe_operators_wait_limit(long long cycles);
 
 /* Grouped products.  X [rows, K], dY [rows, N] and W [E, N, K] are bf16; out_dtype
- * (moe_dtype) is the type of the result, bf16 or fp32.  Sums are fp32, rounded once to bf16; to
- * an fp32 result they are added every 4096 products.
+ * (moe_dtype) is the type of the result, bf16 or fp32.  Sums are fp32: by the tensor core, whose
+ * additions truncate, over up to 4096 products (fp32 results) or 16384 (bf16), and to nearest from
+ * there, so that the error does not grow with the length (at most 2^-15 and 2^-13 of the sum of
+ * the products' magnitudes); a bf16 result is rounded once.
  * Limits: 1 <= E <= 256; N and K multiples of 8, up to 2^20; rows up to 2^30, else
  * MOE_ERR_UNSUPPORTED.  An output that overlaps an input is refused.
  *   forward: Y [rows, N],  Y[r, :]  = W[e] X[r, :]
@@ -422,8 +424,8 @@ moe_status moe_mx_dequantize(const void *codes, const uint8_t *scales, int forma
 
 /* Grouped product with both operands in MXFP4 (codes and scales as moe_mx_quantize
  * writes them): Xc [rows, K / 2], Xs [K / 32, rows], Wc [E, N, K / 2], Ws [E, K / 32, N];
- * Y [rows, N], Y[r, :] = W[e] X[r, :] over the decoded values, summed in fp32 and rounded
- * once to out_dtype.  A scale of 255 makes the results that use it NaN.  Rows, offsets
+ * Y [rows, N], Y[r, :] = W[e] X[r, :] over the decoded values, summed as in the products above
+ * (over up to 16384 products for fp32 results, 65536 for bf16) and rounded once to out_dtype.  A scale of 255 makes the results that use it NaN.  Rows, offsets
  * and limits as moe_grouped_forward, with N a multiple of 8 and K a multiple of 32.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 moe_status moe_mx_grouped_forward(const void *Xc, const uint8_t *Xs, const void *Wc, const uint8_t *Ws,
