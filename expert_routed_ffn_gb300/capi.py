@@ -512,7 +512,8 @@ def clip_grad_norm(grads, max_norm, out=None, stream=None):
     """The norm of all `grads` (bf16 or fp32 CUDA tensors of one device) together, as a 0-dim
     fp32 tensor, and the gradients times min(1, max_norm / norm): in place, or into the
     tensors `out`.  If a gradient holds an infinity or a NaN the norm says so and the
-    gradients are passed on as they are.  Results must not overlap other tensors of the lists:
+    gradients are passed on as they are; a finite norm beyond fp32 is reported as an infinity and
+    the gradients are clipped by its value.  Results must not overlap other tensors of the lists:
     a gradient that is there twice cannot be clipped in place."""
     torch = _t()
     T = torch.Tensor

@@ -1,6 +1,7 @@
 // The global norm of a list of gradients, and the gradients scaled by
 //   c = min(1, max_norm / norm),   norm = sqrt(sum of all g^2)
-// (c = 1 where the norm is not finite: the caller sees it and skips the step).
+// (c = 1 where a gradient is not finite: the caller sees it in the norm and skips the step; a norm
+// that is finite but beyond fp32 is reported as an infinity, and c comes from its value).
 //
 // Two kernels, whose CTAs walk blocks of the list's values.  The first sums squares: per thread
 // and step (up to 64 values) in fp32; over steps, threads and warps as unevaluated sums of two
@@ -210,30 +211,43 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
     if (tid == 0) p.partial[blockIdx.x] = total;
 }
 
+// What the gradients are multiplied by: near, or where that is no normal fp32 number (norms of
+// more than about 2^125 max_norm) far, which is 0 otherwise.
+struct Factor {
+    float near = 1.0f;
+    double far = 0.0;
+    bool clip = false;
+};
+
 // The norm and the factor from the sum of squares, with the exponent apart: the square of a
 // value may be out of fp32's range, and fp64 square roots and quotients are slow here.
-__device__ __forceinline__ void norm_of(double sum, float max_norm, float &norm, float &scale, bool &clip) {
+__device__ __forceinline__ Factor factor_of(double sum, float max_norm, float &norm) {
     const long long bits = __double_as_longlong(sum);
     const int ex = (int)(bits >> 52 & 0x7ff);
-    clip = false;
-    scale = 1.0f;
+    Factor f;
     norm = 0.0f;
-    if (sum == 0.0) return;
+    if (sum == 0.0) return f;
     if (ex == 0x7ff) {  // a NaN or an infinity among the gradients: they pass through
         norm = (float)sum;
-        return;
+        return f;
     }
     const int e = ex - 1023, h = e >> 1;  // sum = m 2^(2 h), 1 <= m < 4
     const float root = sqrtf((float)__longlong_as_double((bits & 0xfffffffffffffll) | (long long)(1023 + e - 2 * h) << 52));
     norm = scalbnf(root, h);
-    clip = norm > max_norm;
-    if (clip) scale = scalbnf(max_norm / root, -h);
+    f.clip = norm > max_norm;
+    if (!f.clip) return f;
+    const int em = ilogbf(max_norm), t = em - h;            // max_norm may be subnormal
+    const float q = scalbnf(max_norm, -em) / root;          // the factor is q 2^t, 1/2 < q < 2
+    if (t >= -125)
+        f.near = scalbnf(q, t);
+    else  // t >= -149 - 147
+        f.far = (double)q * __longlong_as_double((long long)(1023 + t) << 52);
+    return f;
 }
 
 template <int N>
 __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ ClipArgs<N> p) {
-    __shared__ float s_scale;
-    __shared__ bool s_clip;
+    __shared__ Factor s_factor;
     const int tid = threadIdx.x;
     const int blocks = (p.chunks + p.block - 1) / p.block;
     pdl_wait();
@@ -243,18 +257,16 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
         for (int i = tid; i < p.num_partial; i += 32) sum += p.partial[i];
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        float norm, scale;
-        bool clip;
-        norm_of(sum, p.max_norm, norm, scale, clip);
+        float norm;
+        const Factor f = factor_of(sum, p.max_norm, norm);
         if (tid == 0) {
-            s_scale = scale;
-            s_clip = clip;
+            s_factor = f;
             if (p.norm != nullptr && blockIdx.x == 0) *p.norm = norm;
         }
     }
     __syncthreads();
-    const float scale = s_scale;
-    const bool clip = s_clip;
+    const float scale = s_factor.near;
+    const bool clip = s_factor.clip, is_far = s_factor.far != 0.0;
     if ((int)blockIdx.x >= blocks) return;
     for (int blk = ((blocks - 1 - (int)blockIdx.x) / (int)gridDim.x) * (int)gridDim.x + (int)blockIdx.x; blk >= 0; blk -= gridDim.x) {
         const int c0 = blk * p.block, c1 = min(c0 + p.block, p.chunks);
@@ -262,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
             const Segment s = segment(p, k, c0, c1);
             if (!clip && s.src == s.dst) continue;
             int done = 0;
-            if (s.vec) {
+            if (s.vec && !is_far) {
                 const uint4 *src = reinterpret_cast<const uint4 *>(s.src);
                 uint4 *dst = reinterpret_cast<uint4 *>(s.dst);
                 const int per = s.f32 ? 4 : 8, nv = s.n / per;
@@ -287,7 +299,7 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
                 }
             }
             for (int i = done + tid; i < s.n; i += kThreads) {
-                const float v = load1(s, i) * scale;
+                const float g = load1(s, i), v = is_far ? (float)((double)g * s_factor.far) : g * scale;
                 if (s.f32)
                     reinterpret_cast<float *>(s.dst)[i] = v;
                 else

@@ -447,7 +447,8 @@ moe_status moe_clip_workspace(int count, size_t *bytes);
 /* The norm of all gradients of the list together, sqrt(sum g^2), to norm[0] (device, fp32)
  * and out = g * min(1, max_norm / norm).  Squares are summed in fp32 over at most 64 values and
  * as pairs of fp32 numbers or in fp64 from there, in a fixed order.  If a gradient holds an
- * infinity or a NaN, the norm says so and out = g.  max_norm > 0 (infinity: the norm alone is
+ * infinity or a NaN, the norm says so and out = g; a finite norm beyond fp32 is reported as an
+ * infinity, and the gradients are clipped by its value.  max_norm > 0 (infinity: the norm alone is
  * wanted).  The list is read before the call returns.  A result that shares bytes with another
  * gradient or result, or in part with its own gradient, is refused (so is the same gradient
  * twice, in place), and so are a norm or a workspace inside the tensors.  count == 0: norm 0.
