@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
             const uint32_t bytes = a_block + (kDense ? (two_b ? 2 : 1) * kChunk : (t.n / 2) * kRow);
             for (int r = t.r0, here; r < t.r1; r += here * kBK) {
                 here = blocks_at(t, r);
-                if (!__all_sync(0xffffffffu, wait_bar(empty_bar(s), ph, p.o.wait, abort_flag))) {
+                if (!__all_sync(0xffffffffu, wait_bar(empty_bar(s), ph, p.o.wait + walk.slack, abort_flag))) {
                     ok = false;
                     break;
                 }
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
                 }
                 const uint32_t idesc = idesc_bf16_f32(256, t.n) | (OP != kForward ? 1u << 15 : 0u) | (kDense ? 1u << 16 : 0u);
                 const uint32_t a = accs.next, d = tmem_base + a * kAccCols;
-                if (!__all_sync(0xffffffffu, wait_bar<true>(tempty_bar(a), accs.take(), p.o.wait, abort_flag))) {
+                if (!__all_sync(0xffffffffu, wait_bar<true>(tempty_bar(a), accs.take(), p.o.wait + walk.slack, abort_flag))) {
                     ok = false;
                     break;
                 }
@@ -321,6 +321,9 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
         // wgrad: zero the rows past each tail's end, then hand the stage to the MMA
         uint32_t tail_ph = 0;
         int s = 0;
+        // This warp does not wait in tiles without a tail, so that its next wait may last as long as
+        // all their stages do: the bound grows with them, by as much a stage as in wait_cycles.
+        long long passed = 0;
         const int chunks_a = half_cols / 64;
         for (TileWalk<kDense, SEGMENTS> walk(tab, first, stride); walk.more(); walk.next()) {
             const Tile t = walk.get();
@@ -329,7 +332,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
             const int last = t.r1 - ((t.r1 - t.r0 - 1) % kBK + 1);  // first row of the last block
             if (tile_stages > 0 && is_tail(t, last)) {
                 const int st = (s + tile_stages - 1) % stages;
-                if (!__all_sync(0xffffffffu, wait_bar(tail_bar(st), tail_ph >> st & 1u, p.o.wait, abort_flag))) {
+                if (!__all_sync(0xffffffffu, wait_bar(tail_bar(st), tail_ph >> st & 1u, p.o.wait + walk.slack + passed, abort_flag))) {
                     if (lane == 0) raise();
                     break;
                 }
@@ -345,6 +348,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
                 __syncwarp();
                 if (lane == 0) mbar_arrive_pair(mapa_shared(zeroed_bar(st), 0));
             }
+            passed += kStageCycles * tile_stages;
             s = (s + tile_stages) % stages;
         }
     } else {
@@ -364,7 +368,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
             const uint32_t a = accs.next, tmem_q = tmem_base + ((uint32_t)(q * 32) << 16);
             const int col = t.col0 + rank * half_cols + in_half;
             if (!empty) {
-                if (!__all_sync(0xffffffffu, wait_bar<true>(tfull_bar(a), accs.ready(), p.o.wait, abort_flag))) {
+                if (!__all_sync(0xffffffffu, wait_bar<true>(tfull_bar(a), accs.ready(), p.o.wait + walk.slack, abort_flag))) {
                     if (lane == 0) raise();
                     break;
                 }

@@ -57,11 +57,14 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// What a stage, and the epilogue of a tile, may take at most.
+constexpr long long kStageCycles = 4096, kTileCycles = 65536;
+
 // About 2 s, and what the longest sum may take: the epilogue waits for all of a tile's stages.
 // moe_operators_wait_limit replaces it.
 inline long long wait_cycles(long long stages_per_tile) {
     const long long limit = op_wait_limit();
-    return limit >= 0 ? limit : 4000000000ll + 4096 * stages_per_tile;
+    return limit >= 0 ? limit : 4000000000ll + kStageCycles * stages_per_tile;
 }
 
 // Wait until the phase of parity `parity` of a barrier has completed; CLUSTER: a barrier that
@@ -234,6 +237,9 @@ struct TileWalk {
     int c, r, e;                 // column tile; row tile (dense: within the expert); dense: expert
     int dc, dr, de;              // the stride in the same digits
     int at = 0;                  // the first of the current segment's reduction steps
+    // Dense: what the epilogue may take for the tiles passed.  Those of experts without rows are
+    // nothing to the other roles, whose next wait then lasts as long as the zeros are stored.
+    long long slack = 0;
 
     __device__ __forceinline__ TileWalk(const TileTable &table, int first, int step)
         : tab(table), tile(first), stride(step), c(table.c), r(table.r), e(table.e), dc(table.dc), dr(table.dr), de(table.de) {}
@@ -244,6 +250,7 @@ struct TileWalk {
             return;
         }
         at = 0;
+        if (DENSE) slack += kTileCycles;
         tile += stride;
         c += dc;
         r += dr;

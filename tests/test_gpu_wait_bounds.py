@@ -1,0 +1,43 @@
+"""The grouped products' bounded waits under work that is long but sound: with a bound far above
+every single wait and far below the kernel's run time, no wait may run out."""
+
+import pytest
+import torch
+
+from expert_routed_ffn_gb300 import capi
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("counts,N,K", [
+    ([64] * 254 + [33], 2048, 2048),            # one stage a tile, then a tail
+    ([64] * 100 + [0] * 100 + [33, 48, 17], 2048, 2048),
+    ([2048] * 60 + [1, 2048, 2047], 1024, 1024),  # many stages a tile
+])
+def test_wgrad_with_a_tail_behind_many_tiles_without(counts, N, K):
+    """Only the last experts' row counts leave a tail to zero: the warp that does so has nothing to
+    wait for until then."""
+    from expert_routed_ffn_gb300 import build
+    build.build()
+    lib = capi.load()
+    gen = torch.Generator(device="cuda").manual_seed(91)
+    rows = sum(counts)
+    dY, X = (torch.randn(rows, n, generator=gen, device="cuda").to(torch.bfloat16) for n in (N, K))
+    offs = torch.tensor([0] + [sum(counts[:i + 1]) for i in range(len(counts))], dtype=torch.int32, device="cuda")
+    out = torch.empty(len(counts), N, K, device="cuda")
+    capi.grouped_wgrad(dY, X, offs, out=out)  # the first call also loads the kernel
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    capi.grouped_wgrad(dY, X, offs, out=out)
+    end.record()
+    assert capi.operators_status() == capi.MOE_OK
+    want, us = out.clone(), start.elapsed_time(end) * 1e3
+    assert us > 133  # the bound below, at 1.5 GHz (97 us at 2.07)
+    capi.check(lib.moe_operators_wait_limit(200_000), "moe_operators_wait_limit")
+    try:
+        out.fill_(-1)
+        capi.grouped_wgrad(dY, X, offs, out=out)
+        assert capi.operators_status() == capi.MOE_OK
+    finally:
+        capi.check(lib.moe_operators_wait_limit(-1), "moe_operators_wait_limit")
+    assert torch.equal(out, want)
