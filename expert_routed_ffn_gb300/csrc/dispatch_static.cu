@@ -39,10 +39,11 @@ std::mutex g_setup_mutex;
 int32_t *g_scratch_addr[kMaxDevices] = {};
 unsigned long long g_scratch_ctx[kMaxDevices] = {};
 
+}  // namespace
+
 using CtxGetCurrentFn = CUresult (*)(CUcontext *);
 using CtxGetIdFn = CUresult (*)(CUcontext, unsigned long long *);
 
-// The current context's unique id (driver entry points fetched once), or 0.
 unsigned long long current_context_id() {
     static CtxGetCurrentFn get_current = nullptr;
     static CtxGetIdFn get_id = nullptr;
@@ -65,6 +66,8 @@ unsigned long long current_context_id() {
         return 0;
     return id;
 }
+
+namespace {
 
 __global__ void __launch_bounds__(kThreads) static_hist_kernel(const int32_t *topk_idx, int T, int k, int E,
                                                                 int32_t *blk_hist, int *bad) {

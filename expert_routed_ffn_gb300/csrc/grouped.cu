@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
     }
 }
 
-unsigned long long g_attr[12];
+OpDone g_attr[12];
 
 // Tile sizes.  Rows: up to 256, fewer where the experts average fewer.  Columns: 256, or 128 (64
 // per CTA) where there are no more (with 256, 0.1 us slower).  128 where 256 leave CTA pairs

@@ -52,6 +52,11 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
 
 using bf16 = __nv_bfloat16;
 
+// The current context's unique id (driver entry points fetched once), or 0.  What is kept per
+// device but belongs to a context (addresses of device variables, kernel attributes) is kept with
+// this id: after a device reset, or in a second context, it is looked up or set anew.
+unsigned long long current_context_id();
+
 // Bits of the device error word.
 enum : int { ERR_TIMEOUT = 1, ERR_BOUNDS = 2 };
 

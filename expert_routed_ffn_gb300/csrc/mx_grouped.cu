@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(num_threads(TMA), 1) mx_grouped_kernel(const _
     }
 }
 
-unsigned long long g_attr[4];
+OpDone g_attr[4];
 
 // Tile sizes, by the bf16 products' rule: rows up to 192, fewer where the experts average fewer;
 // 256 columns, or 128 where there are no more (128 where 256 leave CTA pairs without a tile: 11.4

@@ -19,10 +19,10 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-constexpr int kMaxDevices = 64;
 std::mutex g_mutex;
-int g_sms[kMaxDevices];
-std::atomic<int *> g_error_word[kMaxDevices];  // where g_op_error lies on each
+int g_sms[kOpMaxDevices];
+int *g_error_word[kOpMaxDevices];  // where g_op_error lies on each,
+OpDone g_error_word_of;            // and in which context
 std::atomic<long long> g_wait_limit{-1};
 
 }  // namespace
@@ -43,22 +43,23 @@ moe_status op_cuda(cudaError_t e, const char *op) {
 
 int op_num_sms() {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kOpMaxDevices) return 0;
     std::lock_guard<std::mutex> lock(g_mutex);
     if (g_sms[dev] == 0 && cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         g_sms[dev] = 0;
     return g_sms[dev];
 }
 
-cudaError_t op_allow_smem(const void *kernel, int bytes, unsigned long long *done) {
+cudaError_t op_allow_smem(const void *kernel, int bytes, OpDone *done) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (dev < 0 || dev >= kOpMaxDevices) return cudaErrorInvalidDevice;
+    const unsigned long long ctx = current_context_id();
     std::lock_guard<std::mutex> lock(g_mutex);
-    if (*done >> dev & 1ull) return cudaSuccess;
+    if (ctx != 0 && done->ctx[dev] == ctx) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) *done |= 1ull << dev;
+    if (e == cudaSuccess) done->ctx[dev] = ctx;
     return e;
 }
 
@@ -91,13 +92,15 @@ long long op_wait_limit() { return g_wait_limit.load(std::memory_order_relaxed);
 
 int *op_error_word() {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
-    int *word = g_error_word[dev].load(std::memory_order_relaxed);
-    if (word != nullptr) return word;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kOpMaxDevices) return nullptr;
+    const unsigned long long ctx = current_context_id();
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (ctx != 0 && g_error_word_of.ctx[dev] == ctx) return g_error_word[dev];
     void *p = nullptr;
     if (cudaGetSymbolAddress(&p, g_op_error) != cudaSuccess) return nullptr;
-    g_error_word[dev].store(static_cast<int *>(p), std::memory_order_relaxed);
-    return static_cast<int *>(p);
+    g_error_word[dev] = static_cast<int *>(p);
+    g_error_word_of.ctx[dev] = ctx;
+    return g_error_word[dev];
 }
 
 }  // namespace moe

@@ -30,9 +30,15 @@ inline bool op_overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
 // SM count of the current device (looked up once per device), or 0 after an error.
 int op_num_sms();
 
-// Allow `kernel` `bytes` of dynamic shared memory on the current device.  `done` is a
-// bit per device (index < 64), so the attribute is set once on each.
-cudaError_t op_allow_smem(const void *kernel, int bytes, unsigned long long *done);
+constexpr int kOpMaxDevices = 64;
+
+// The context (its id) of each device in which something has been set.
+struct OpDone {
+    unsigned long long ctx[kOpMaxDevices];
+};
+
+// Allow `kernel` `bytes` of dynamic shared memory in the current context, once in each.
+cudaError_t op_allow_smem(const void *kernel, int bytes, OpDone *done);
 
 // A tiled tensor map of up to 4 dimensions (innermost first; strides in bytes, of
 // dimensions 1 ..), zero fill out of bounds.
@@ -50,7 +56,7 @@ CUresult op_encode(CUtensorMap *m, const OpMap &d);
 // The bound set with moe_operators_wait_limit, -1: none.
 long long op_wait_limit();
 
-// Device address of the operators' error word (op_capi.cu) on the current device.
+// Device address of the operators' error word (op_capi.cu) in the current context.
 int *op_error_word();
 
 }  // namespace moe

@@ -379,10 +379,9 @@ moe_status moe_dispatch_noalloc(const int32_t *topk_idx, int T, int k, int E, in
 moe_status moe_operators_status(void);
 
 /* Bound of the device-side waits of the grouped products launched from now on, in SM clock
- * cycles, for the whole process: -1 (the start) is about 2 s and more for very long sums (weight
- * gradients add what the tiles passed so far may take); 0
+ * cycles, for the whole process: -1 (the start) is about 2 s and more for very long sums; 0
  * makes the products give up at their first wait for data, which exercises the timeout path.
- * Errors: INVALID_ARG. */
+ * Weight gradients add what the tiles passed so far may take.  Errors: INVALID_ARG. */
 moe_status moe_operators_wait_limit(long long cycles);
 
 /* Grouped products.  X [rows, K], dY [rows, N] and W [E, N, K] are bf16; out_dtype
