@@ -1,6 +1,7 @@
 // Host helpers of the stateless operators, and their device error word: the
 // bounded waits and offset checks of the grouped products record failures in one
-// word per device, which moe_operators_status() reads and clears.
+// word per context, which moe_operators_status() reads and clears in one exchange: other threads
+// and streams may record the next error at any time.
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
@@ -14,12 +15,16 @@ namespace moe {
 namespace {
 
 __device__ int g_op_error;
+__device__ int g_taken;  // what the last exchange took out of it
+
+__global__ void take_error_kernel() { g_taken = atomicExch(&g_op_error, 0); }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 std::mutex g_mutex;
+std::mutex g_take_mutex;  // from an exchange until its result has been read
 int g_sms[kOpMaxDevices];
 int *g_error_word[kOpMaxDevices];  // where g_op_error lies on each,
 OpDone g_error_word_of;            // and in which context
@@ -116,14 +121,15 @@ extern "C" moe_status moe_operators_status(void) {
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return op_cuda(e, "moe_operators_status");
     int word = 0;
-    e = cudaMemcpyFromSymbol(&word, g_op_error, sizeof word);
+    {
+        std::lock_guard<std::mutex> lock(g_take_mutex);
+        e = cudaLaunchKernel(reinterpret_cast<const void *>(take_error_kernel), dim3(1), dim3(1), nullptr, 0, nullptr);
+        if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&word, g_taken, sizeof word);  // waits for the kernel
+    }
     if (e != cudaSuccess) return op_cuda(e, "moe_operators_status");
     if (word == 0) return MOE_OK;
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_op_error, &zero, sizeof zero);
-    if (e != cudaSuccess) return op_cuda(e, "moe_operators_status");
     if (word & ERR_BOUNDS)
-        return op_fail(MOE_ERR_DEVICE_CHECK,
-                       "an operator met row offsets that decrease or leave [0, rows]; it wrote nothing");
+        return op_fail(MOE_ERR_DEVICE_CHECK, "an operator met row offsets that decrease or leave [0, rows]; it wrote nothing%s",
+                       word & ERR_TIMEOUT ? "; and a device-side wait of an operator ran past its bound" : "");
     return op_fail(MOE_ERR_TIMEOUT, "a device-side wait of an operator ran past its bound");
 }

@@ -373,9 +373,10 @@ moe_status moe_dispatch_noalloc(const int32_t *topk_idx, int T, int k, int E, in
  */
 
 /* Wait for the current device and report (then clear) what the operators below
- * recorded on it since the last call: MOE_OK, MOE_ERR_DEVICE_CHECK (offsets) or
- * MOE_ERR_TIMEOUT (a bounded device wait ran out), or MOE_ERR_CUDA.  Not during a
- * stream capture. */
+ * recorded on it since the last call: MOE_OK, MOE_ERR_DEVICE_CHECK (offsets; the message
+ * says so if a wait ran out as well) or MOE_ERR_TIMEOUT (a bounded device wait ran out), or
+ * MOE_ERR_CUDA.  What a call of another thread records meanwhile is reported now or by the
+ * next call.  Not during a stream capture. */
 moe_status moe_operators_status(void);
 
 /* Bound of the device-side waits of the grouped products launched from now on, in SM clock
