@@ -309,24 +309,26 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
     }
 }
 
-// One launch's share of the list; the grid, or -1 if it is too long.  Short lists: blocks of up
+// A CTA's part of a tensor, and the chunks of a launch's tensors, are counted in an int
+constexpr long long kMaxChunks = 1ll << 26;
+long long chunks_of(const moe_grad &g) { return g.count == 0 ? 0 : (g.count - 1) / kChunk + 1; }
+
+// One launch's share of the list (at most kMaxChunks); the grid.  Short lists: blocks of up
 // to 8 chunks, as many CTAs as blocks; long ones: blocks of 4 (a thread's step of fp32 values),
 // kCtasPerSm CTAs per SM.
 template <int N>
 int fill(ClipArgs<N> &a, const moe_grad *g, int n, int sms) {
-    long long chunks = 0;
+    int chunks = 0;
     a.tensors = 0;
     for (int i = 0; i < n; ++i) {
         if (g[i].count == 0) continue;
         const int k = a.tensors++;
         a.t[k] = {g[i].grad, g[i].out, g[i].count};
-        a.first[k] = (int)chunks;
+        a.first[k] = chunks;
         if (g[i].dtype == MOE_DTYPE_F32) a.f32[k >> 5] |= 1u << (k & 31);
-        // a CTA's part of a tensor is counted in an int
-        const long long add = (g[i].count - 1) / kChunk + 1;
-        if (add > (1ll << 26) || (chunks += add) > (1ll << 26)) return -1;
+        chunks += (int)chunks_of(g[i]);
     }
-    a.chunks = (int)chunks;
+    a.chunks = chunks;
     a.first[a.tensors] = a.chunks;
     const int most = std::min(kMaxGrid, kCtasPerSm * sms);
     a.block = a.chunks > 8 * most ? 4 : std::max(1, std::min(8, a.chunks / (2 * sms)));
@@ -343,7 +345,6 @@ int launches_of(int count) { return std::max(1, (count + kMaxTensors - 1) / kMax
 
 template <int N>
 moe_status run(const moe_grad *grads, int count, float max_norm, float *norm, double *partial, int sms, cudaStream_t s) {
-    const char *op = "moe_clip_grad_norm";
     const int launches = launches_of(count);
     int used = 0;
     for (int pass = 0; pass < 2; ++pass)
@@ -352,7 +353,6 @@ moe_status run(const moe_grad *grads, int count, float max_norm, float *norm, do
             std::fill(std::begin(a.f32), std::end(a.f32), 0u);
             const int at = l * kMaxTensors;
             const int grid = fill(a, grads + at, std::min(kMaxTensors, count - at), sms);
-            if (grid < 0) return op_fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^37 values in one launch's tensors", op);
             a.max_norm = max_norm;
             a.partial = pass == 0 ? partial + used : partial;
             a.num_partial = used;
@@ -360,7 +360,7 @@ moe_status run(const moe_grad *grads, int count, float max_norm, float *norm, do
             if (pass == 0) used += grid;
             const cudaError_t e = pass == 0 ? launch_pdl(grad_norm_kernel<N>, dim3(grid), dim3(kThreads), 0, s, a)
                                             : launch_pdl(grad_scale_kernel<N>, dim3(grid), dim3(kThreads), 0, s, a);
-            if (e != cudaSuccess) return op_cuda(e, op);
+            if (e != cudaSuccess) return op_cuda(e, "moe_clip_grad_norm");
         }
     return MOE_OK;
 }
@@ -429,6 +429,12 @@ extern "C" moe_status moe_clip_grad_norm(const moe_grad *grads, int count, float
         if (g.count < 0 || (g.count > 0 && (!g.grad || !g.out)) ||
             ((reinterpret_cast<uintptr_t>(g.grad) | reinterpret_cast<uintptr_t>(g.out)) & mask))
             return op_fail(MOE_ERR_INVALID_ARG, "%s: tensor %d: a NULL or misaligned pointer, or a negative count", op, i);
+    }
+    for (int at = 0; at < count; at += kMaxTensors) {  // before anything is launched
+        long long chunks = 0;
+        for (int i = at; i < std::min(count, at + kMaxTensors); ++i)
+            if (chunks_of(grads[i]) > kMaxChunks || (chunks += chunks_of(grads[i])) > kMaxChunks)
+                return op_fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^37 values in %d tensors", op, kMaxTensors);
     }
     if (count > 0) {
         Range *room = static_cast<Range *>(malloc(sizeof(Range) * (size_t)count));

@@ -454,7 +454,8 @@ moe_status moe_clip_workspace(int count, size_t *bytes);
  * gradient or result, or in part with its own gradient, is refused (so is the same gradient
  * twice, in place), and so are a norm or a workspace inside the tensors.  count == 0: norm 0.
  * `workspace` (device) is used until the call's kernels end: calls that may overlap, and
- * graphs that may, need one each.  Errors: INVALID_ARG, UNSUPPORTED, CUDA, OOM. */
+ * graphs that may, need one each.  More than 2^37 values among 960 tensors of the list are
+ * refused.  Errors: INVALID_ARG, UNSUPPORTED, CUDA, OOM. */
 moe_status moe_clip_grad_norm(const moe_grad *grads, int count, float max_norm, float *norm, void *workspace,
                               size_t workspace_bytes, moe_stream_t stream);
 

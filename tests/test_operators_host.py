@@ -161,3 +161,16 @@ def test_mx_sizes_at_the_end_of_an_int(lib, slices, rows, K, status):
     assert lib.moe_mx_quantize(None, 0, slices, rows, K, 2, FAKE, FAKE, None) == status
     assert lib.moe_mx_dequantize(None, FAKE, 1, slices, rows, K, 0, FAKE, None) == status
     assert ("too large" in lib.moe_last_error().decode()) == (status == capi.MOE_ERR_UNSUPPORTED)
+
+
+@pytest.mark.parametrize("at", [0, 959, 960, 961, 2000])
+def test_clip_refuses_too_long_a_list_before_it_launches(lib, at):
+    """More than 2^37 values among the tensors of one launch, wherever in the list they are."""
+    n = 2100
+    need = ctypes.c_size_t()
+    assert lib.moe_clip_workspace(n, ctypes.byref(need)) == capi.MOE_OK
+    for count in ((1 << 37) + 1, 1 << 62):
+        table = (capi.MoeGrad * n)(*[capi.MoeGrad(_at(64 * i), _at(64 * i), 16, 1) for i in range(n)])
+        table[at] = capi.MoeGrad(_at(1 << 40), _at(1 << 40), count, 0)
+        assert lib.moe_clip_grad_norm(table, n, 1.0, _at(1 << 28), _at(1 << 29), need, None) == capi.MOE_ERR_UNSUPPORTED
+        assert "2^37" in lib.moe_last_error().decode()
