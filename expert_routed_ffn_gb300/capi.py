@@ -297,6 +297,12 @@ def _need(cond, message):
         raise ValueError(message)
 
 
+def _fits(*sizes):
+    """The library takes sizes as int; ctypes would pass on their lower 32 bits."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"sizes must be below 2^31: {sizes}")
+
+
 def _dtype_code(dtype):
     if dtype is _torch.bfloat16:
         return MOE_DTYPE_BF16
@@ -346,6 +352,7 @@ def _grouped(name, A, W, offs, out, out_dtype, stream, forward):
     E, N, K = W.shape
     cols, red = (N, K) if forward else (K, N)
     rows = A.shape[0]
+    _fits(rows, E, N, K)
     index = A.get_device()
     _tensor(A, "X" if forward else "dY", (rows, red), torch.bfloat16, index)
     _tensor(W, "W", (E, N, K), torch.bfloat16, index)
@@ -385,6 +392,7 @@ def grouped_wgrad(dY, X, offs, out=None, out_dtype=None, accumulate=False, strea
     _need(offs.dim() == 1 and offs.numel() >= 2, "offs must be [E + 1]")
     _need(out is not None or not accumulate, "accumulate needs out")
     (rows, K), N, E = X.shape, dY.shape[1], offs.numel() - 1
+    _fits(rows, E, N, K)
     index = X.get_device()
     _tensor(X, "X", (rows, K), torch.bfloat16, index)
     _tensor(dY, "dY", (rows, N), torch.bfloat16, index)
@@ -418,11 +426,13 @@ def _mx_shapes(shape, code, of):
         rows, K = shape
         last = (K // 2 if two else K) if of == 1 else (2 * K if two else K)
         K = K if of == 1 else last
+        _fits(rows, K)
         return 1, rows, K, (rows, last), (K // 32, rows)
     _need(len(shape) == 3, "the tensor must be [rows, K] or [slices, rows, K]")
     slices, rows, K = shape
     last = (K // 2 if two else K) if of == 1 else (2 * K if two else K)
     K = K if of == 1 else last
+    _fits(slices, rows, K)
     return slices, rows, K, (slices, rows, last), (slices, K // 32, rows)
 
 
@@ -484,6 +494,7 @@ def mx_grouped_forward(Xc, Xs, Wc, Ws, offs, out=None, out_dtype=None, stream=No
     _need(Wc.dim() == 3 and Xc.dim() == 2, "Wc must be [E, N, K / 2] and Xc [rows, K / 2]")
     E, N, half = Wc.shape
     rows, K = Xc.shape[0], 2 * half
+    _fits(rows, E, N, K)
     index, u8 = Xc.get_device(), torch.uint8
     _tensor(Xc, "Xc", (rows, half), u8, index)
     _tensor(Xs, "Xs", (K // 32, rows), u8, index)
