@@ -466,8 +466,9 @@ __device__ __forceinline__ void store8(void *Y, int y_f32, size_t off, const flo
 
 // The 8 gains at column c: g = w (norm 1) or 1 + w (norm 2)
 __device__ __forceinline__ void gain8(const float *w, int norm, int c, float (&g)[8]) {
-    const float4 lo = __ldg(reinterpret_cast<const float4 *>(w + c));
-    const float4 hi = __ldg(reinterpret_cast<const float4 *>(w + c + 4));
+    // plain loads: the compiler may move those of __ldg ahead of a wait for earlier kernels
+    const float4 lo = *reinterpret_cast<const float4 *>(w + c);
+    const float4 hi = *reinterpret_cast<const float4 *>(w + c + 4);
     g[0] = lo.x; g[1] = lo.y; g[2] = lo.z; g[3] = lo.w; g[4] = hi.x; g[5] = hi.y; g[6] = hi.z; g[7] = hi.w;
     if (norm == 2) {
 #pragma unroll
@@ -507,7 +508,8 @@ __global__ void __launch_bounds__(kRowMaxThreads) combine_kernel(const CombineAr
         s_w[0][threadIdx.x] = __ldcg(a.topk_w + (size_t)t * k + threadIdx.x);
     }
     float g[8];
-    if (NORM && on) gain8(a.post_w, a.norm, c, g);  // weights: not written by any kernel
+    // weights: written, if at all, by kernels before the forward, which the GEMM has waited for
+    if (NORM && on) gain8(a.post_w, a.norm, c, g);
     pdl_wait();
     trace_mark(a.trace, 1);
     pdl_trigger();
@@ -819,8 +821,6 @@ __global__ void __launch_bounds__(kRowMaxThreads) rmsnorm_kernel(const NormArgs 
     const int t = blockIdx.x, H = a.H, c = threadIdx.x * 8;
     const bool on = c < H;
     trace_mark(a.trace, 0);
-    float g[8];
-    if (on) gain8(a.w, a.norm, c, g);
     pdl_wait();
     trace_mark(a.trace, 1);
     pdl_trigger();
@@ -829,9 +829,10 @@ __global__ void __launch_bounds__(kRowMaxThreads) rmsnorm_kernel(const NormArgs 
         for (int i = threadIdx.x; i < a.zero_b_n; i += blockDim.x) a.zero_b[i] = 0;
     }
     const size_t off = (size_t)t * H + c;
-    float v[8], ss = 0.f;
+    float v[8], g[8], ss = 0.f;
     if (on) {
         load8_as_f32(a.X, a.x_f32, off, v);
+        gain8(a.w, a.norm, c, g);  // the forward's first kernel: an operator just before may have written them
 #pragma unroll
         for (int q = 0; q < 8; ++q) ss = fmaf(v[q], v[q], ss);
     }
