@@ -44,3 +44,58 @@ def test_norm_weights_written_by_the_operator_before(T, norm):
     assert blk.sync_status() == capi.MOE_OK
     for i, y in enumerate(got):
         assert torch.equal(y, want[i % 4]), i
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows", [3, 500, 24576])
+def test_tensors_rewritten_between_the_operators(rows, dtype):
+    """One buffer that every operator's result goes to and the next one reads, many rounds without a
+    pause and as a captured graph."""
+    K, N = 512, 512
+    gen = torch.Generator(device="cuda").manual_seed(102)
+    W = torch.randn(2, N, K, generator=gen, device="cuda").mul_(0.06).to(torch.bfloat16)
+    Wq = capi.mx_quantize(W, "mxfp4")
+    offs = torch.tensor([0, rows // 3, rows], dtype=torch.int32, device="cuda")
+    start = torch.randn(rows, K, generator=gen, device="cuda").to(torch.bfloat16)
+    codes, scales = capi.mx_quantize(start, "mxfp4")
+    X, Y, dW = torch.empty_like(start), torch.empty(rows, N, dtype=dtype, device="cuda"), torch.empty(2, N, K, device="cuda")
+
+    def step(pause):
+        for call in (
+                lambda: capi.mx_quantize(Y, "mxfp4", codes=codes, scales=scales),
+                lambda: capi.mx_dequantize(codes, scales, "mxfp4", out=X),
+                lambda: capi.grouped_forward(X, W, offs, out=Y),
+                lambda: capi.clip_grad_norm([Y], 3.0 * rows ** 0.5),
+                lambda: capi.mx_quantize(Y, "mxfp4", codes=codes, scales=scales),
+                lambda: capi.mx_grouped_forward(codes, scales, *Wq, offs, out=Y),
+                lambda: capi.mx_quantize(Y, "mxfp8", codes=codes8, scales=scales),
+                lambda: capi.mx_dequantize(codes8, scales, "mxfp8", out=X),
+                lambda: capi.grouped_wgrad(X, X, offs, out=dW),
+                lambda: capi.grouped_dgrad(X, W, offs, out=Y)):
+            call()
+            if pause:
+                torch.cuda.synchronize()
+
+    codes8 = torch.empty(rows, K, dtype=torch.uint8, device="cuda")
+    want = []
+    Y.copy_(start)
+    for _ in range(6):
+        step(True)
+        want.append((Y.clone(), dW.clone()))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(False)
+    for run in (lambda: step(False), graph.replay):
+        for _ in range(3):
+            X.fill_(float("nan"))
+            dW.fill_(float("nan"))
+            Y.copy_(start)
+            got = []
+            for _ in range(6):
+                run()
+                got.append((Y.clone(), dW.clone()))
+            torch.cuda.synchronize()
+            for i, (g, w) in enumerate(zip(got, want)):
+                assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1]), i
+    assert capi.operators_status() == capi.MOE_OK
+    assert bool(want[-1][0].isfinite().all()) and float(want[-1][0].float().abs().max()) > 0
