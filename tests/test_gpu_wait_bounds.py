@@ -41,3 +41,44 @@ def test_wgrad_with_a_tail_behind_many_tiles_without(counts, N, K):
     finally:
         capi.check(lib.moe_operators_wait_limit(-1), "moe_operators_wait_limit")
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("op", ["forward", "dgrad", "wgrad", "accumulate", "mx_forward"])
+def test_timeout_in_a_sum_of_several_segments(op, dtype):
+    """The bound at 0: the products give up at their first wait, report it, and the next call is right."""
+    from expert_routed_ffn_gb300 import build
+    build.build()
+    lib = capi.load()
+    gen = torch.Generator(device="cuda").manual_seed(92)
+    long, counts = 70_016, [33, 0, 90, 5]
+    if op in ("wgrad", "accumulate"):
+        counts = [33, 70_017, 0, 5]
+    rows, N, K = sum(counts), 136, 264
+    if op in ("forward", "mx_forward"):
+        K = long
+    elif op == "dgrad":
+        N = long
+    offs = torch.tensor([0] + [sum(counts[:i + 1]) for i in range(4)], dtype=torch.int32, device="cuda")
+    X, dY, W = (torch.randn(*s, generator=gen, device="cuda").to(torch.bfloat16) for s in ((rows, K), (rows, N), (4, N, K)))
+    if op == "mx_forward":
+        Xq, Wq = capi.mx_quantize(X, "mxfp4"), capi.mx_quantize(W, "mxfp4")
+
+    def call():
+        if op == "accumulate":
+            return capi.grouped_wgrad(dY, X, offs, out=torch.ones(4, N, K, dtype=dtype, device="cuda"), accumulate=True)
+        if op == "mx_forward":
+            return capi.mx_grouped_forward(*Xq, *Wq, offs, out_dtype=dtype)
+        f, a, b = {"forward": (capi.grouped_forward, X, W), "dgrad": (capi.grouped_dgrad, dY, W), "wgrad": (capi.grouped_wgrad, dY, X)}[op]
+        return f(a, b, offs, out_dtype=dtype)
+
+    want = call()
+    assert capi.operators_status() == capi.MOE_OK
+    capi.check(lib.moe_operators_wait_limit(0), "moe_operators_wait_limit")
+    try:
+        call()
+        assert capi.operators_status() == capi.MOE_ERR_TIMEOUT
+    finally:
+        capi.check(lib.moe_operators_wait_limit(-1), "moe_operators_wait_limit")
+    assert torch.equal(call(), want)
+    assert capi.operators_status() == capi.MOE_OK
