@@ -276,7 +276,9 @@ def block_from_inputs(shape, inputs: dict, max_tokens: int = None) -> MoeBlock:
 # The products of the block one at a time and what surrounds them (include/moe.h,
 # "Operators around the stacked expert weights").  Each runs on the device of its
 # tensors, on `stream` or that device's current stream, and allocates only outputs it
-# was not given.
+# was not given.  None of them is recorded by autograd: results never require a gradient,
+# whatever the inputs do, and the gradients are operators of their own.  After offsets that
+# break the rule, a result allocated here is uninitialised: operators_status() tells.
 
 _torch = _device = _raw_stream = None
 
@@ -520,9 +522,9 @@ class MoeGrad(ctypes.Structure):
 
 
 def clip_grad_norm(grads, max_norm, out=None, stream=None):
-    """The norm of all `grads` (bf16 or fp32 CUDA tensors of one device) together, as a 0-dim
-    fp32 tensor, and the gradients times min(1, max_norm / norm): in place, or into the
-    tensors `out`.  If a gradient holds an infinity or a NaN the norm says so and the
+    """The norm of all `grads` (one or more contiguous bf16 or fp32 CUDA tensors of one device)
+    together, as a 0-dim fp32 tensor, and the gradients times min(1, max_norm / norm): in place,
+    or into the tensors `out`.  If a gradient holds an infinity or a NaN the norm says so and the
     gradients are passed on as they are; a finite norm beyond fp32 is reported as an infinity and
     the gradients are clipped by its value.  Results must not overlap other tensors of the lists:
     a gradient that is there twice cannot be clipped in place."""

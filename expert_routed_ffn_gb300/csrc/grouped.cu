@@ -34,16 +34,18 @@
 // stage's copies complete on a barrier of their own CTA, and the stage is handed to the MMA
 // when both CTAs have zeroed.
 //
-// What bounds it, measured on GB300 (bf16; 64 experts, N 1408, K 2048):
-//   forward, 24576 rows    104 us, 1.36 PFLOP/s, 5.2 TB/s: the tensor pipe is 76% busy at the 1.6
-//                          GHz the SM clock settles to, and HBM 63%; the first two waves of tiles
-//                          wait for weights
-//   dgrad, 24576 rows      103 us; of 1408 columns the sixth tile is half empty
-//   wgrad, 24576 rows, fp32 out   147 us, 6.2 TB/s: the 738 MB it writes
-//   forward, 384 rows      57 us, 6.5 TB/s: the weights, streamed once
-//   forward, one expert, 16384 rows, K 1408, N 2048   53 us, 1.78 PFLOP/s
-//   forward, one token's six experts   8 us in a row of calls: start and end of the launch around
-//                          35 MB
+// Measured on GB300, one call in a row of them on the same tensors, / alone with cold caches (bf16;
+// 64 experts, N 1408, K 2048):
+//   forward, 24576 rows    105 / 113 us, 1.35 PFLOP/s, 5.1 TB/s.  The tensor pipe is 77% busy and
+//                          HBM 65%: of 1408 columns the sixth tile is half empty (8% of the
+//                          products), and eight of 76 pairs take an eleventh tile
+//   dgrad, 24576 rows      98 / 105 us to 2048 columns
+//   wgrad, 24576 rows      fp32 146 / 148 us, 6.2 TB/s: the 738 MB it writes; bf16 105 / 105
+//   the same, accumulating fp32 888 / 895 us, bf16 219 / 222: store_tile has eight loads of the old
+//                          values in flight per lane, and waits for them between its stores
+//   forward, 384 rows      58 / 76 us, 6.5 TB/s: the weights, streamed once
+//   forward, one expert, 16384 rows, K 1408, N 2048   54 / 58 us, 1.76 PFLOP/s
+//   forward, one token's six experts   7.4 / 17 us: start and end of the launch around 35 MB
 // One CTA per 128 x 256 tile with the rows as M took 128 (forward), 145 and 181 us.
 //
 // Decreasing or out-of-range offsets: every CTA sees the same, records ERR_BOUNDS and
@@ -174,12 +176,12 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
     if (!load_table<kDense>(h.table) && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.o.err, ERR_BOUNDS);
     const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
     const int half_cols = tab.o.cols / 2;
-    // wgrad: the stage at reduction row r ends inside a 16-row step
     // blocks of the stage at reduction step r: those left, of the wgrad two only if both are whole
     auto blocks_at = [&](const Tile &t, int r) {
         if (BLOCKS == 1) return 1;
         return kDense ? (t.r1 - r >= BLOCKS * kBK ? BLOCKS : 1) : min(BLOCKS, (t.r1 - r + kBK - 1) / kBK);
     };
+    // wgrad: the stage at reduction row r ends inside a 16-row step
     auto is_tail = [&](const Tile &t, int r) { return kDense && t.r1 - r < kBK && (t.r1 - r) % 16 != 0; };
 
     if (warp == 0) {

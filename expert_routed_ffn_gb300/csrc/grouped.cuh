@@ -84,11 +84,14 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, long lon
     }
 }
 
-// Arrive on a barrier of either CTA (address from mapa_shared), with the default semantics: what
-// it hands over stays within each CTA (an accumulator whose reads tcgen05.wait::ld has completed;
-// shared memory that the CTA's own tensor core reads next, after fence.proxy.async), so nothing
-// has to be made visible to the other one.  The form that releases at cluster scope waits for the
-// warp's outstanding stores and loads: about 2000 cycles per tile, or per stage of scales.
+// Arrive on a barrier of either CTA (address from mapa_shared), with the default semantics, a
+// release at CTA scope: what it hands over stays within the arriving CTA (an accumulator whose
+// reads tcgen05.wait::ld has completed; shared memory that this CTA's own tensor core reads next,
+// and that fence.proxy.async has made visible to it before the arrival), so nothing has to become
+// visible to threads of the other one, which only issue the instruction.  The form that releases
+// at cluster scope waits for the warp's outstanding stores and loads: for the scales alone the
+// MXFP4 product takes 73 for 40 us (24576 rows; 34 for 18 with 384), for the zeroed tails alone
+// weight gradients 10 to 18% more (bf16, 24576 rows in ragged experts: 128 for 108 us).
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }

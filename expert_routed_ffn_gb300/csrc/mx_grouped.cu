@@ -26,11 +26,15 @@
 // Tensor memory (512 columns): two accumulators of up to 192 columns, then per stage the
 // scales of the weights (8 columns) and of the tokens (8 per 128 of them).
 //
-// Measured on GB300 (64 experts, N 1408, K 2048): 24576 rows 44 us, 3.2 PFLOP/s, 4.4 TB/s; 384
-// rows 18 us, 5.5 TB/s (part of it from L2; 23 us from HBM); one expert, 8192 rows, N and K 2048:
-// 19 us, 3.6 PFLOP/s.  The copies of codes and the stores bound it: without products it takes 4 us
-// less (L2 delivers 9.3 TB/s; the tensor pipe is 40% busy).  Tiles of 224 rows, for which tensor
-// memory has room for two stages' scales beside the accumulators, took the same time.
+// Measured on GB300, one call in a row of them on the same tensors (part of the weights stays in
+// L2) / alone with cold caches (64 experts, N 1408, K 2048): 24576 rows 41 / 50 us, 3.4 PFLOP/s,
+// 4.7 TB/s; 384 rows 19 / 32 us; one expert, 8192 rows, N and K 2048: 19 / 25 us, 3.7 PFLOP/s.
+// Neither memory nor the tensor pipe is at its limit (24576 rows): HBM is 44% busy, the tensor pipe
+// 42% of its active cycles (58% with the copies of scales), and L2 delivers 9.5 TB/s, less than it
+// gives the bf16 products.  Without products it took 4 of 46 us less, without scales 1.  Part of
+// it are tiles that are not full: experts of 385 rows take three where 384 take two, and
+// of 1408 columns the sixth tile is half empty.  Tiles of 224 rows, for which tensor memory has
+// room for two stages' scales beside the accumulators, took the same time.
 #include <algorithm>
 
 #include "common.cuh"

@@ -16,8 +16,9 @@
 // instead of 79.9 us (of that 13 us because loads are not marked as streaming).  The scales lie
 // block-major ([K / 32, rows]), across the rows' direction: they are collected in shared memory
 // and leave as 32-byte runs.
-// Measured on GB300, 64 x 1408 x 2048 values: bf16 to MXFP4 68.5 us, 6.8 TB/s, and back 68.7;
-// fp32 115 us, 7.2 TB/s (part of the tensor is still in L2), and back 137, 6.1 TB/s.
+// Measured on GB300, 64 x 1408 x 2048 values, one call in a row: bf16 to MXFP4 70.8 us, 6.6 TB/s,
+// and back 67.3; to MXFP8 81.6 us, 6.9 TB/s, and back 79.6; fp32 to MXFP4 117 us, 7.1 TB/s (part
+// of the tensor is still in L2), and back 136, 6.1 TB/s.
 #include <cuda_fp16.h>
 
 #include <algorithm>
