@@ -466,7 +466,8 @@ __device__ __forceinline__ void store8(void *Y, int y_f32, size_t off, const flo
 
 // The 8 gains at column c: g = w (norm 1) or 1 + w (norm 2)
 __device__ __forceinline__ void gain8(const float *w, int norm, int c, float (&g)[8]) {
-    // plain loads: the compiler may move those of __ldg ahead of a wait for earlier kernels
+    // plain loads: those of __ldg want memory that is constant from the kernel's start, which may be
+    // before the end of the kernel that wrote it
     const float4 lo = *reinterpret_cast<const float4 *>(w + c);
     const float4 hi = *reinterpret_cast<const float4 *>(w + c + 4);
     g[0] = lo.x; g[1] = lo.y; g[2] = lo.z; g[3] = lo.w; g[4] = hi.x; g[5] = hi.y; g[6] = hi.z; g[7] = hi.w;
