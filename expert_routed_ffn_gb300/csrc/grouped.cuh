@@ -64,7 +64,8 @@ constexpr long long kStageCycles = 4096, kTileCycles = 65536;
 // moe_operators_wait_limit replaces it.
 inline long long wait_cycles(long long stages_per_tile) {
     const long long limit = op_wait_limit();
-    return limit >= 0 ? limit : 4000000000ll + kStageCycles * stages_per_tile;
+    if (limit >= 0) return std::min(limit, 1ll << 62);  // roles add to it
+    return 4000000000ll + kStageCycles * stages_per_tile;
 }
 
 // Wait until the phase of parity `parity` of a barrier has completed; CLUSTER: a barrier that

@@ -82,3 +82,24 @@ def test_timeout_in_a_sum_of_several_segments(op, dtype):
         capi.check(lib.moe_operators_wait_limit(-1), "moe_operators_wait_limit")
     assert torch.equal(call(), want)
     assert capi.operators_status() == capi.MOE_OK
+
+
+def test_largest_bound():
+    """What the roles add to the bound does not overflow it."""
+    from expert_routed_ffn_gb300 import build
+    build.build()
+    lib = capi.load()
+    gen = torch.Generator(device="cuda").manual_seed(93)
+    counts = [0, 64, 33, 0, 0, 300] * 12
+    dY, X = (torch.randn(sum(counts), n, generator=gen, device="cuda").to(torch.bfloat16) for n in (1024, 2048))
+    offs = torch.tensor([0] + [sum(counts[:i + 1]) for i in range(len(counts))], dtype=torch.int32, device="cuda")
+    want = capi.grouped_wgrad(dY, X, offs)
+    assert capi.operators_status() == capi.MOE_OK
+    for limit in (2 ** 63 - 1, 2 ** 62):
+        capi.check(lib.moe_operators_wait_limit(limit), "moe_operators_wait_limit")
+        try:
+            got = capi.grouped_wgrad(dY, X, offs)
+            assert capi.operators_status() == capi.MOE_OK
+        finally:
+            capi.check(lib.moe_operators_wait_limit(-1), "moe_operators_wait_limit")
+        assert torch.equal(got, want)
