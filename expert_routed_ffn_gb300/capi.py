@@ -113,7 +113,10 @@ def load():
     L.moe_grouped_forward.argtypes = [P, P, P, I, I, I, I, I, P, P]
     L.moe_grouped_dgrad.argtypes = [P, P, P, I, I, I, I, I, P, P]
     L.moe_grouped_wgrad.argtypes = [P, P, P, I, I, I, I, I, I, P, P]
-    SZ = ctypes.c_size_t
+    SZ, F = ctypes.c_size_t, ctypes.c_float
+    L.moe_grouped_gated_forward.argtypes = [P, P, P, P, I, I, I, I, I, F, F, F, P, P, P, P]
+    L.moe_grouped_gated_backward.argtypes = [P, P, P, P, P, I, I, I, I, I, F, F, F, P, P, P]
+    L.moe_grouped_gated_dgrad.argtypes = [P, P, P, P, P, I, I, I, I, I, P, P]
     L.moe_mx_quantize.argtypes = [P, I, I, I, I, I, P, P, P]
     L.moe_mx_dequantize.argtypes = [P, P, I, I, I, I, I, P, P]
     L.moe_mx_grouped_forward.argtypes = [P, P, P, P, P, I, I, I, I, I, P, P]
@@ -122,7 +125,8 @@ def load():
     for name in ("moe_create", "moe_route", "moe_forward", "moe_forward_host", "moe_sync_status", "moe_dispatch_noalloc",
                  "moe_set_option", "moe_get_stats", "moe_inspect", "moe_get_stage_times", "moe_get_trace",
                  "moe_operators_status", "moe_operators_wait_limit", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad", "moe_mx_quantize",
-                 "moe_mx_dequantize", "moe_mx_grouped_forward", "moe_clip_workspace", "moe_clip_grad_norm"):
+                 "moe_mx_dequantize", "moe_mx_grouped_forward", "moe_clip_workspace", "moe_clip_grad_norm",
+                 "moe_grouped_gated_forward", "moe_grouped_gated_backward", "moe_grouped_gated_dgrad"):
         getattr(L, name).restype = I
     _lib = L
     return L
@@ -410,6 +414,107 @@ def grouped_wgrad(dY, X, offs, out=None, out_dtype=None, accumulate=False, strea
     finally:
         _leave(undo)
     check(status, "moe_grouped_wgrad")
+    return out
+
+
+def _act_code(act):
+    if act == "silu":
+        return MOE_ACT_SILU
+    _need(act == "swigluoai", f"act must be 'silu' or 'swigluoai', not {act!r}")
+    return MOE_ACT_SWIGLU_OAI
+
+
+def _outputs(given, names, shape, dtype, device):
+    """The tensors given, or new ones."""
+    if given is None:
+        return tuple(_torch.empty(shape, dtype=dtype, device=device) for _ in names)
+    given = tuple(given)
+    _need(len(given) == len(names), f"need the tensors {', '.join(names)}")
+    for t, name in zip(given, names):
+        _tensor(t, name, shape, dtype, device.index)
+    return given
+
+
+def grouped_gated_forward(X, Wg, Wu, offs, act="silu", alpha=1.702, limit=7.0, beta=1.0, out=None, save=None, stream=None):
+    """H = act(G, U), G[r] = Wg[e] X[r], U[r] = Wu[e] X[r] for the rows of expert e as in
+    grouped_forward; X [rows, K], Wg and Wu [E, I, K] bf16.  act: "silu", or "swigluoai" with
+    alpha, limit and beta.  Returns H [rows, I] bf16 (`out`, or a new tensor); with save=True, or
+    save=(G, U) to write into, (H, G, U) for the backward pass.  Rows outside
+    [offs[0], offs[E]) are left as they were."""
+    torch = _t()
+    _need(Wg.dim() == 3 and X.dim() == 2, "Wg must be [E, I, K] and X [rows, K]")
+    (E, I, K), rows, code = Wg.shape, X.shape[0], _act_code(act)
+    _fits(rows, E, I, K)
+    index, bf = X.get_device(), torch.bfloat16
+    _tensor(X, "X", (rows, K), bf, index)
+    _tensor(Wg, "Wg", (E, I, K), bf, index)
+    _tensor(Wu, "Wu", (E, I, K), bf, index)
+    _tensor(offs, "offs", (E + 1,), torch.int32, index)
+    keep = save is not None and save is not False
+    raw, undo = _enter(index, stream)
+    try:
+        H, = _outputs(None if out is None else (out,), ("out",), (rows, I), bf, X.device)
+        G, U = _outputs(None if save is True else save, ("G", "U"), (rows, I), bf, X.device) if keep else (None, None)
+        status = _lib.moe_grouped_gated_forward(
+            X.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), offs.data_ptr(), rows, E, I, K, code, alpha, limit, beta, H.data_ptr(),
+            G.data_ptr() if keep else None, U.data_ptr() if keep else None, raw)
+    finally:
+        _leave(undo)
+    check(status, "moe_grouped_gated_forward")
+    return (H, G, U) if keep else H
+
+
+def grouped_gated_backward(dY, Wd, G, U, offs, act="silu", alpha=1.702, limit=7.0, beta=1.0, out=None, stream=None):
+    """The gradients (dG, dU) [rows, I] bf16 of grouped_gated_forward's G and U, from dY [rows, K]
+    bf16, the gradient of grouped_forward(H, Wd, offs) with Wd [E, K, I]: dH = dY Wd stays in fp32.
+    out=(dG, dU): tensors to write into.  Rows outside [offs[0], offs[E]) are left as they were."""
+    torch = _t()
+    _need(Wd.dim() == 3 and dY.dim() == 2, "Wd must be [E, K, I] and dY [rows, K]")
+    (E, K, I), rows, code = Wd.shape, dY.shape[0], _act_code(act)
+    _fits(rows, E, I, K)
+    index, bf = dY.get_device(), torch.bfloat16
+    _tensor(dY, "dY", (rows, K), bf, index)
+    _tensor(Wd, "Wd", (E, K, I), bf, index)
+    _tensor(G, "G", (rows, I), bf, index)
+    _tensor(U, "U", (rows, I), bf, index)
+    _tensor(offs, "offs", (E + 1,), torch.int32, index)
+    raw, undo = _enter(index, stream)
+    try:
+        dG, dU = _outputs(out, ("dG", "dU"), (rows, I), bf, dY.device)
+        status = _lib.moe_grouped_gated_backward(
+            dY.data_ptr(), Wd.data_ptr(), G.data_ptr(), U.data_ptr(), offs.data_ptr(), rows, E, I, K, code, alpha, limit, beta,
+            dG.data_ptr(), dU.data_ptr(), raw)
+    finally:
+        _leave(undo)
+    check(status, "moe_grouped_gated_backward")
+    return dG, dU
+
+
+def grouped_gated_dgrad(dG, dU, Wg, Wu, offs, out=None, out_dtype=None, stream=None):
+    """The gradient of grouped_gated_forward by its X: dX[r] = Wg[e]^T dG[r] + Wu[e]^T dU[r], in out
+    (default: a new [rows, K] tensor of out_dtype, bf16 by default), whose rows outside
+    [offs[0], offs[E]) are left as they were."""
+    torch = _t()
+    _need(Wg.dim() == 3 and dG.dim() == 2, "Wg must be [E, I, K] and dG [rows, I]")
+    (E, I, K), rows = Wg.shape, dG.shape[0]
+    _fits(rows, E, I, K)
+    index, bf = dG.get_device(), torch.bfloat16
+    _tensor(dG, "dG", (rows, I), bf, index)
+    _tensor(dU, "dU", (rows, I), bf, index)
+    _tensor(Wg, "Wg", (E, I, K), bf, index)
+    _tensor(Wu, "Wu", (E, I, K), bf, index)
+    _tensor(offs, "offs", (E + 1,), torch.int32, index)
+    raw, undo = _enter(index, stream)
+    try:
+        if out is None:
+            out = torch.empty((rows, K), dtype=out_dtype or bf, device=dG.device)
+        else:
+            _tensor(out, "out", (rows, K), out_dtype or out.dtype, index)
+        status = _lib.moe_grouped_gated_dgrad(dG.data_ptr(), dU.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), offs.data_ptr(),
+                                              rows, E, I, K, _dtype_code(out.dtype), out.data_ptr(), raw)
+    finally:
+        _leave(undo)
+    check(status, "moe_grouped_gated_dgrad")
     return out
 
 

@@ -407,6 +407,27 @@ moe_status moe_grouped_dgrad(const void *dY, const void *W, const int32_t *offs,
 moe_status moe_grouped_wgrad(const void *dY, const void *X, const int32_t *offs, int rows, int E, int N, int K,
                              int out_dtype, int accumulate, void *dW, moe_stream_t stream);
 
+/* The gated block over rows grouped by expert, for training and serving; Wg and Wu are [E, I, K],
+ * Wd [E, K, I], X and dY [rows, K], everything else [rows, I]; all bf16 but dX (out_dtype).
+ *   forward:  G = X Wg^T, U = X Wu^T, H = act(G, U).  G and U are written (rounded) where both
+ *             are given, to be kept for the backward pass; H comes from the unrounded sums
+ *   backward: from dY, the gradient of what the down projection Wd made of H: dH = dY Wd (held in
+ *             fp32 only), dG = dH dact/dG, dU = dH dact/dU at the G and U given
+ *   dgrad:    dX = dG Wg + dU Wu, rounded once
+ * act (moe_act) with alpha, limit and beta as in moe_config (ignored for MOE_ACT_SILU; else limit > 0,
+ * alpha and beta finite).  The clamped activation passes gradients at the limit and none beyond
+ * it.  The weights' gradients are moe_grouped_wgrad(dG, X), (dU, X) and (dY, H).  Rows, offsets,
+ * sums and limits as in the products above, with I and K multiples of 8.  An output that overlaps another
+ * tensor is refused.  rows == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+moe_status moe_grouped_gated_forward(const void *X, const void *Wg, const void *Wu, const int32_t *offs, int rows, int E,
+                                     int I, int K, int act, float alpha, float limit, float beta, void *H, void *G,
+                                     void *U, moe_stream_t stream);
+moe_status moe_grouped_gated_backward(const void *dY, const void *Wd, const void *G, const void *U, const int32_t *offs,
+                                      int rows, int E, int I, int K, int act, float alpha, float limit, float beta,
+                                      void *dG, void *dU, moe_stream_t stream);
+moe_status moe_grouped_gated_dgrad(const void *dG, const void *dU, const void *Wg, const void *Wu, const int32_t *offs,
+                                   int rows, int E, int I, int K, int out_dtype, void *dX, moe_stream_t stream);
+
 /* Block-scaled quantisation of X [slices, rows, K] (dtype: moe_dtype) to MXFP8 or MXFP4
  * (moe_weight_format) in the layout of the block's weights: codes [slices, rows, K] or
  * [slices, rows, K / 2], scales [slices, K / 32, rows].  Per block of 32 values along K
