@@ -27,6 +27,7 @@ MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1
 MOE_ACT_SILU, MOE_ACT_SWIGLU_OAI = 0, 1
 MOE_DTYPE_BF16, MOE_DTYPE_F32 = 0, 1
 MOE_NORM_NONE, MOE_NORM_RMS, MOE_NORM_GEMMA = 0, 1, 2
+MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_CHANNEL = 0, 1, 2
 MOE_WEIGHTS_BF16, MOE_WEIGHTS_MXFP8, MOE_WEIGHTS_MXFP4 = 0, 1, 2
 WEIGHT_FORMATS = {"bf16": MOE_WEIGHTS_BF16, "mxfp8": MOE_WEIGHTS_MXFP8, "mxfp4": MOE_WEIGHTS_MXFP4}
 SCALE_KEYS = ("gate_scale", "up_scale", "down_scale", "sh_gate_scale", "sh_up_scale", "sh_down_scale")
@@ -117,6 +118,9 @@ def load():
     L.moe_grouped_gated_forward.argtypes = [P, P, P, P, I, I, I, I, I, F, F, F, P, P, P, P]
     L.moe_grouped_gated_backward.argtypes = [P, P, P, P, P, I, I, I, I, I, F, F, F, P, P, P]
     L.moe_grouped_gated_dgrad.argtypes = [P, P, P, P, P, I, I, I, I, I, P, P]
+    L.moe_sandwich_norm.argtypes = [P, P, P, P, P, I, F, F, I, I, I, I, I, P, P, P]
+    L.moe_sandwich_norm_workspace.argtypes = [I, I, ctypes.POINTER(SZ)]
+    L.moe_sandwich_norm_backward.argtypes = [P, P, P, P, P, P, P, I, F, F, I, I, I, I, I, P, P, P, P, P, P, SZ, P]
     L.moe_mx_quantize.argtypes = [P, I, I, I, I, I, P, P, P]
     L.moe_mx_dequantize.argtypes = [P, P, I, I, I, I, I, P, P]
     L.moe_mx_grouped_forward.argtypes = [P, P, P, P, P, I, I, I, I, I, P, P]
@@ -126,7 +130,8 @@ def load():
                  "moe_set_option", "moe_get_stats", "moe_inspect", "moe_get_stage_times", "moe_get_trace",
                  "moe_operators_status", "moe_operators_wait_limit", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad", "moe_mx_quantize",
                  "moe_mx_dequantize", "moe_mx_grouped_forward", "moe_clip_workspace", "moe_clip_grad_norm",
-                 "moe_grouped_gated_forward", "moe_grouped_gated_backward", "moe_grouped_gated_dgrad"):
+                 "moe_grouped_gated_forward", "moe_grouped_gated_backward", "moe_grouped_gated_dgrad",
+                 "moe_sandwich_norm", "moe_sandwich_norm_workspace", "moe_sandwich_norm_backward"):
         getattr(L, name).restype = I
     _lib = L
     return L
@@ -516,6 +521,109 @@ def grouped_gated_dgrad(dG, dU, Wg, Wu, offs, out=None, out_dtype=None, stream=N
         _leave(undo)
     check(status, "moe_grouped_gated_dgrad")
     return out
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _norm_arguments(X, F, pre_w, post_w, gate, kind):
+    """Checks what both directions take: X [T, H], F and the parameters.  Returns T, H, the device's
+    index, the kind's code and the gate's kind."""
+    torch = _torch
+    _need(X.dim() == 2, "X must be [T, H]")
+    T, H = X.shape
+    _fits(T, H)
+    index = X.get_device()
+    _tensor(X, "X", (T, H), X.dtype, index)
+    if F is not None:
+        _tensor(F, "F", (T, H), F.dtype, index)
+    for w, name in ((pre_w, "pre_w"), (post_w, "post_w")):
+        if w is not None:
+            _tensor(w, name, (H,), torch.float32, index)
+    _need(kind in ("rms", "gemma"), f"kind must be 'rms' or 'gemma', not {kind!r}")
+    gate_kind = MOE_GATE_NONE
+    if gate is not None:
+        gate_kind = MOE_GATE_TOKEN if gate.dim() == 2 else MOE_GATE_CHANNEL
+        _tensor(gate, "gate", (T, 1) if gate.dim() == 2 else (H,), torch.float32, index)
+    return T, H, index, MOE_NORM_GEMMA if kind == "gemma" else MOE_NORM_RMS, gate_kind
+
+
+def sandwich_norm(X, F=None, pre_w=None, post_w=None, gate=None, residual_scale=1.0, eps=1e-5, kind="rms", X_out=None,
+                  N_out=None, n_dtype=None, stream=None):
+    """X' = residual_scale X + gate * norm(F) post_w and N = norm(X') pre_w, the norms after one block and
+    before the next with the residual between them.  X [T, H] (bf16 or fp32) is the residual stream, F
+    [T, H] the block's result (of its own type, which N has too); pre_w and post_w [H] fp32, gate [H] or
+    [T, 1] fp32.  Returns (X', N): without post_w F is added as it is, without pre_w N is None,
+    without F X' is X itself and N = norm(X) pre_w (of n_dtype, by default X's).  kind "gemma": weights
+    are 1 + w.  X_out may be X, and N_out may be F."""
+    torch = _t()
+    T, H, index, code, gate_kind = _norm_arguments(X, F, pre_w, post_w, gate, kind)
+    of_n = F.dtype if F is not None else n_dtype or (X.dtype if N_out is None else N_out.dtype)
+    _need(F is None or n_dtype in (None, F.dtype), "N has F's type")
+    x_code, n_code = _dtype_code(X.dtype), _dtype_code(of_n)
+    _need(X_out is None or F is not None, "X_out needs F")
+    _need(N_out is None or pre_w is not None, "N_out needs pre_w")
+    raw, undo = _enter(index, stream)
+    try:
+        if F is not None:
+            if X_out is None:
+                X_out = torch.empty_like(X)
+            else:
+                _tensor(X_out, "X_out", (T, H), X.dtype, index)
+        if pre_w is not None:
+            if N_out is None:
+                N_out = torch.empty((T, H), dtype=of_n, device=X.device)
+            else:
+                _tensor(N_out, "N_out", (T, H), of_n, index)
+        status = _lib.moe_sandwich_norm(X.data_ptr(), _address(F), _address(pre_w), _address(post_w), _address(gate), gate_kind,
+                                        residual_scale, eps, code, T, H, x_code, n_code, _address(X_out), _address(N_out), raw)
+    finally:
+        _leave(undo)
+    check(status, "moe_sandwich_norm")
+    return (X if F is None else X_out), N_out
+
+
+def sandwich_norm_backward(dX, dN, X, F=None, pre_w=None, post_w=None, gate=None, residual_scale=1.0, eps=1e-5, kind="rms",
+                           dX_out=None, dF_out=None, stream=None):
+    """The gradients of sandwich_norm from those of X' and N (dX may be None for zeros, dN is None without
+    pre_w), X being the X' it returned: (of its X, of F, of pre_w, of post_w, of the gate), None where
+    there is no such tensor.  dX_out may be dX, and dF_out may be dN."""
+    torch = _t()
+    T, H, index, code, gate_kind = _norm_arguments(X, F, pre_w, post_w, gate, kind)
+    of_n = dN.dtype if F is None and dN is not None else X.dtype if F is None else F.dtype
+    x_code, n_code = _dtype_code(X.dtype), _dtype_code(of_n)
+    _need((dN is None) == (pre_w is None), "dN goes with pre_w")
+    _need(dX is not None or pre_w is not None, "dX is needed without pre_w")
+    _need(dF_out is None or F is not None, "dF_out needs F")
+    if dX is not None:
+        _tensor(dX, "dX", (T, H), X.dtype, index)
+    if dN is not None:
+        _tensor(dN, "dN", (T, H), of_n, index)
+    need = ctypes.c_size_t()
+    check(_lib.moe_sandwich_norm_workspace(T, H, ctypes.byref(need)), "moe_sandwich_norm_backward")
+    raw, undo = _enter(index, stream)
+    try:
+        device = X.device
+        if dX_out is None:
+            dX_out = torch.empty_like(X)
+        else:
+            _tensor(dX_out, "dX_out", (T, H), X.dtype, index)
+        if F is not None:
+            if dF_out is None:
+                dF_out = torch.empty_like(F)
+            else:
+                _tensor(dF_out, "dF_out", (T, H), of_n, index)
+        dpre, dpost, dgate = (None if w is None else torch.empty_like(w) for w in (pre_w, post_w, gate))
+        work = torch.empty(need.value, dtype=torch.uint8, device=device)
+        status = _lib.moe_sandwich_norm_backward(
+            _address(dX), _address(dN), X.data_ptr(), _address(F), _address(pre_w), _address(post_w), _address(gate), gate_kind,
+            residual_scale, eps, code, T, H, x_code, n_code, dX_out.data_ptr(), _address(dF_out), _address(dpre),
+            _address(dpost), _address(dgate), work.data_ptr(), need.value, raw)
+    finally:
+        _leave(undo)
+    check(status, "moe_sandwich_norm_backward")
+    return dX_out, dF_out, dpre, dpost, dgate
 
 
 def _mx_format(fmt):

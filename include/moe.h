@@ -428,6 +428,36 @@ moe_status moe_grouped_gated_backward(const void *dY, const void *Wd, const void
 moe_status moe_grouped_gated_dgrad(const void *dG, const void *dU, const void *Wg, const void *Wu, const int32_t *offs,
                                    int rows, int E, int I, int K, int out_dtype, void *dX, moe_stream_t stream);
 
+/* The norms around a block, fused with its gate and the residual (the RMSNorm sandwich of moe_config.mlp_norm,
+ * between any two blocks), and all their gradients.  The residual stream X [T, H] is of x_dtype, the
+ * block's result F and what the next block reads, N, of f_dtype (moe_dtype); weights, gates and
+ * their gradients are fp32:
+ *   X_out = residual_scale X + gate * norm(F) post_w,   N = norm(X_out) pre_w
+ *   norm(V) = V / sqrt(mean V^2 + eps) over a row; kind (moe_norm): MOE_NORM_RMS, or MOE_NORM_GEMMA with
+ *   1 + w in place of w; gate [T] or [H] (moe_gate), or NULL
+ * without post_w F is added as it is; without pre_w there is no N; without F (then no post_w, gate
+ * nor X_out) N = norm(X) pre_w.  N is of the unrounded X_out.
+ * backward: from dX_out (NULL: zeros, where there is pre_w) and dN, and X_out and F as they were
+ * stored: dX, dF, and dpre_w, dpost_w [H] and dgate (each may be NULL).  Sums over rows are fp32, in a
+ * fixed order.  Without F, dX is the whole gradient (no residual_scale).  X_out and dX_out may be NULL
+ * where nothing reads them (X_out without pre_w).
+ * In place: X_out may be X and N may be F, dX may be dX_out and dF may be dN; any other overlap of an
+ * output is refused.  H: a multiple of 8 up to 8192; eps >= 1e-30.  Rows of any magnitude are normed (sums of squares beyond fp32
+ * are taken again of scaled values); a row with an infinity or a NaN gives what the formulas
+ * give, in that row (and in the sums over rows).  T == 0: no-op, the gradients of weights are zeros.  `workspace` as in moe_clip_grad_norm.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_TOKEN = 1, MOE_GATE_CHANNEL = 2 } moe_gate;
+moe_status moe_sandwich_norm(const void *X, const void *F, const float *pre_w, const float *post_w, const float *gate,
+                             int gate_kind, float residual_scale, float eps, int kind, int T, int H, int x_dtype,
+                             int f_dtype, void *X_out, void *N, moe_stream_t stream);
+/* Bytes of workspace moe_sandwich_norm_backward needs. */
+moe_status moe_sandwich_norm_workspace(int T, int H, size_t *bytes);
+moe_status moe_sandwich_norm_backward(const void *dX_out, const void *dN, const void *X_out, const void *F,
+                                      const float *pre_w, const float *post_w, const float *gate, int gate_kind,
+                                      float residual_scale, float eps, int kind, int T, int H, int x_dtype, int f_dtype,
+                                      void *dX, void *dF, float *dpre_w, float *dpost_w, float *dgate, void *workspace,
+                                      size_t workspace_bytes, moe_stream_t stream);
+
 /* Block-scaled quantisation of X [slices, rows, K] (dtype: moe_dtype) to MXFP8 or MXFP4
  * (moe_weight_format) in the layout of the block's weights: codes [slices, rows, K] or
  * [slices, rows, K / 2], scales [slices, K / 32, rows].  Per block of 32 values along K

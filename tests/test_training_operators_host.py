@@ -71,3 +71,62 @@ def test_gated_outputs_overlap(lib):
     assert gated(lib, "forward", H=inside) == INVALID
     assert gated(lib, "dgrad", dX=inside) == INVALID
     assert gated(lib, "dgrad", out_dtype=2) == INVALID
+
+
+NORM = {"X": at(1), "F": at(2), "pre": at(3), "post": at(4), "gate": at(5), "gate_kind": 1, "alpha": 1.0, "eps": 1e-5, "kind": 1,
+        "T": 16, "H": 64, "x_dtype": 0, "f_dtype": 0, "X_out": at(6), "N": at(7)}
+NORM_BACKWARD = {"dX_out": at(1), "dN": at(2), "X_out": at(3), "F": at(4), "pre": at(5), "post": at(6), "gate": at(7), "gate_kind": 2,
+                 "alpha": 1.0, "eps": 1e-5, "kind": 2, "T": 16, "H": 64, "x_dtype": 1, "f_dtype": 0, "dX": at(8), "dF": at(9),
+                 "dpre": at(10), "dpost": at(11), "dgate": at(12), "work": at(13), "size": 1 << 20}
+
+
+def norm(lib, **change):
+    return lib.moe_sandwich_norm(*{**NORM, **change}.values(), None)
+
+
+def norm_backward(lib, **change):
+    return lib.moe_sandwich_norm_backward(*{**NORM_BACKWARD, **change}.values(), None)
+
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.mark.parametrize("call,base", [(norm, NORM), (norm_backward, NORM_BACKWARD)])
+def test_norm_refusals(lib, call, base):
+    for change, status in [({"T": -1}, INVALID), ({"H": 0}, INVALID), ({"H": 60}, UNSUPPORTED), ({"H": 8200}, UNSUPPORTED),
+                           ({"x_dtype": 2}, INVALID), ({"f_dtype": -1}, INVALID), ({"kind": 0}, INVALID), ({"kind": 3}, INVALID),
+                           ({"gate_kind": 3}, INVALID), ({"gate_kind": 0}, INVALID), ({"gate": None}, INVALID),
+                           ({"alpha": NAN}, INVALID), ({"alpha": INF}, INVALID), ({"eps": 0.0}, INVALID), ({"eps": NAN}, INVALID),
+                           ({"eps": INF}, INVALID)] + [({k: ODD}, INVALID) for k, v in base.items() if isinstance(v, ctypes.c_void_p)]:
+        assert call(lib, **change) == status, change
+        assert "moe_sandwich_norm" in lib.moe_last_error().decode()
+
+
+def test_norm_parts_refusals(lib):
+    for change in ({"X": None}, {"F": None}, {"X_out": None}, {"N": None}, {"pre": None},
+                   {"F": None, "X_out": None},  # post_w and the gate are F's
+                   {"F": None, "X_out": None, "post": None, "gate": None, "gate_kind": 0, "pre": None, "N": None}):
+        assert norm(lib, **change) == INVALID, change
+    for change in ({"dX": None}, {"F": None}, {"dF": None}, {"dN": None}, {"pre": None}, {"X_out": None}, {"work": None}, {"size": 16},
+                   {"pre": None, "dN": None},  # dpre_w of no weight
+                   {"post": None}, {"gate": None, "gate_kind": 0},
+                   {"pre": None, "dN": None, "dpre": None, "dX_out": None}):
+        assert norm_backward(lib, **change) == INVALID, change
+    assert norm(lib, T=0) == OK and norm(lib, T=0, X=None, F=None, X_out=None, N=None, gate=None, gate_kind=0, post=None) == OK
+    need = ctypes.c_size_t()
+    assert lib.moe_sandwich_norm_workspace(-1, 64, ctypes.byref(need)) == INVALID
+    assert lib.moe_sandwich_norm_workspace(4, 64, None) == INVALID
+    assert lib.moe_sandwich_norm_workspace(4, 12, ctypes.byref(need)) == UNSUPPORTED
+    assert lib.moe_sandwich_norm_workspace(4, 64, ctypes.byref(need)) == OK and need.value > 0
+
+
+def test_norm_outputs_overlap(lib):
+    in_place = {"X_out": "X", "N": "F", "dX": "dX_out", "dF": "dN"}
+    for call, base, outs in ((norm, NORM, ["X_out", "N"]), (norm_backward, NORM_BACKWARD, ["dX", "dF", "dpre", "dpost", "dgate", "work"])):
+        for out in outs:
+            for other, value in base.items():
+                if isinstance(value, ctypes.c_void_p) and other not in (out, in_place.get(out)):
+                    assert call(lib, **{out: value}) == INVALID, (out, other)
+            if out in in_place:  # in place, but shifted
+                shifted = ctypes.c_void_p(base[in_place[out]].value + 16)
+                assert call(lib, **{out: shifted}) == INVALID, out
