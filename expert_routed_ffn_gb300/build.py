@@ -23,7 +23,7 @@ LIB = os.path.join(BUILD, "libmoe.so")
 
 SOURCES = ["router.cu", "router_tc.cu", "stream.cu", "gemm_tc.cu", "gemm_sab.cu", "gemm_mxt.cu", "moe_capi.cu",
            "dispatch_static.cu", "op_capi.cu", "grouped.cu", "mx_quant.cu", "mx_grouped.cu",
-           "grad_clip.cu", "gated.cu", "norm.cu"]
+           "grad_clip.cu", "gated.cu", "norm.cu", "orthogonalize.cu"]
 HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "kernels.h"), os.path.join(CSRC, "routing.cuh"),
            os.path.join(CSRC, "op_host.h"), os.path.join(CSRC, "grouped.cuh"), os.path.join(CSRC, "gated.cuh"),
            os.path.join(CSRC, "grouped_kernel.cuh"), os.path.join(INCLUDE, "moe.h")]

@@ -121,6 +121,8 @@ def load():
     L.moe_sandwich_norm.argtypes = [P, P, P, P, P, I, F, F, I, I, I, I, I, P, P, P]
     L.moe_sandwich_norm_workspace.argtypes = [I, I, ctypes.POINTER(SZ)]
     L.moe_sandwich_norm_backward.argtypes = [P, P, P, P, P, P, P, I, F, F, I, I, I, I, I, P, P, P, P, P, P, SZ, P]
+    L.moe_orthogonalize_workspace.argtypes = [I, I, I, ctypes.POINTER(SZ)]
+    L.moe_orthogonalize.argtypes = [P, I, I, I, I, ctypes.POINTER(F), I, F, F, P, P, SZ, P]
     L.moe_mx_quantize.argtypes = [P, I, I, I, I, I, P, P, P]
     L.moe_mx_dequantize.argtypes = [P, P, I, I, I, I, I, P, P]
     L.moe_mx_grouped_forward.argtypes = [P, P, P, P, P, I, I, I, I, I, P, P]
@@ -131,7 +133,8 @@ def load():
                  "moe_operators_status", "moe_operators_wait_limit", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad", "moe_mx_quantize",
                  "moe_mx_dequantize", "moe_mx_grouped_forward", "moe_clip_workspace", "moe_clip_grad_norm",
                  "moe_grouped_gated_forward", "moe_grouped_gated_backward", "moe_grouped_gated_dgrad",
-                 "moe_sandwich_norm", "moe_sandwich_norm_workspace", "moe_sandwich_norm_backward"):
+                 "moe_sandwich_norm", "moe_sandwich_norm_workspace", "moe_sandwich_norm_backward",
+                 "moe_orthogonalize_workspace", "moe_orthogonalize"):
         getattr(L, name).restype = I
     _lib = L
     return L
@@ -777,3 +780,36 @@ def clip_grad_norm(grads, max_norm, out=None, stream=None):
         _leave(undo)
     check(status, "moe_clip_grad_norm")
     return norm
+
+
+def orthogonalize(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=1.0, out=None, stream=None):
+    """scale times the matrices of G ([N, K] or [E, N, K], bf16 or fp32) with their singular values moved
+    towards one by Newton-Schulz products: X = G / (|G| + eps), then `steps` times
+    X <- a X + (b A + c A^2) X with A = X X^T.  coefficients: (a, b, c), or one such triple for each step.  Returns
+    out (default: a new tensor), bf16 of G's shape; out may be G where G is bf16."""
+    torch = _t()
+    _need(G.dim() in (2, 3), "G must be [N, K] or [E, N, K]")
+    E, N, K = G.shape if G.dim() == 3 else (1, *G.shape)
+    _fits(E, N, K)
+    index, code = G.get_device(), _dtype_code(G.dtype)
+    _need(index >= 0 and G.is_contiguous(), "G must be a contiguous CUDA tensor")
+    triples = list(coefficients)
+    if triples and not hasattr(triples[0], "__len__"):
+        triples = [triples] * steps
+    _need(len(triples) == steps and all(len(c) == 3 for c in triples), "coefficients must be (a, b, c), or a triple for each step")
+    table = (ctypes.c_float * (3 * steps))(*[v for c in triples for v in c])
+    need = ctypes.c_size_t()
+    check(_lib.moe_orthogonalize_workspace(E, N, K, ctypes.byref(need)), "moe_orthogonalize")
+    raw, undo = _enter(index, stream)
+    try:
+        if out is None:
+            out = torch.empty(G.shape, dtype=torch.bfloat16, device=G.device)
+        else:
+            _tensor(out, "out", G.shape, torch.bfloat16, index)
+        work = torch.empty(need.value, dtype=torch.uint8, device=G.device)
+        status = _lib.moe_orthogonalize(G.data_ptr(), code, E, N, K, table, steps, eps, scale, out.data_ptr(), work.data_ptr(),
+                                        need.value, raw)
+    finally:
+        _leave(undo)
+    check(status, "moe_orthogonalize")
+    return out

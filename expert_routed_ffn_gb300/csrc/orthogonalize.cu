@@ -1,0 +1,808 @@
+// Newton-Schulz products that move the singular values of stacked matrices G [E, N, K] towards one
+// (the update of the Muon optimiser).  With m the smaller side, X0 = G / (|G|_F + eps) and for
+// each step's (a, b, c)
+//   A = X X^T,   B = a + b A + c A^2,   X <- B X          (N <= K; else A = X^T X, X <- X B)
+//
+// Three products a step, m^2 n + m^3 + 2 m^2 n FLOP (A and B are symmetric: tiles below their
+// diagonal are not computed but mirrored), all batched over the matrices.  Bound by the tensor
+// cores.  No operand is transposed in memory: whichever side is smaller, a tile is read with its
+// reduction index innermost or outermost, as in grouped.cu, whose tiles, pipeline of CTA pairs,
+// descriptors and bounded waits this kernel has.
+//
+// Precision.  Every value between the products is fp16: X, A and B are bounded (|X| <= 1.3 for the
+// usual coefficients; the host bounds the singular values step by step and picks power-of-two
+// scales that keep them inside fp16), so fp16's 11 bits cost nothing over bf16's 8 and are eight
+// times as accurate.  What rounding X still does: noise of 2^-12 of its largest directions enters
+// the small ones, which the polynomial multiplies by up to a = 3.4 a step.  Of the small directions'
+// change, B's part b A + c A^2 is nearly nothing and a X nearly all, so the steps that matter (all but the last
+// two) keep the rounding of X, hi + lo, and take it through a X alone: X <- (b A + c A^2) hi + a (hi + lo),
+// an epilogue's work; the tensor cores see hi only.  Where 16 directions are 300 times as large as
+// the rest, the result's error (2-norm, relative) falls from 2.0e-2 to 1.3e-3, below a
+// bf16 result's own rounding of 1.7e-3; bf16 throughout gives 0.16.
+// X0 is G times a power of two (exact for bf16 G), the rest of 1 / (|G| + eps) is a factor
+// s in (1/2, 1] of the first A and B.  Sums are fp32 in tensor memory, over at most 16384
+// products: the tensor core's truncation stays below 1e-4 (2^-13) of a sum of one sign.
+#include <algorithm>
+#include <cmath>
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "grouped.cuh"
+#include "kernels.h"
+#include "moe.h"
+#include "op_host.h"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxSide = 16384;
+constexpr int kBK = 64;                // reduction steps per stage: 128 bytes
+constexpr int kMaxStages = 12;
+constexpr int kParts = 2;              // epilogue warps per TMEM lane quadrant
+constexpr int kEpiWarps = kQuads * kParts;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kAccCols = 256;
+constexpr uint32_t kTmemCols = 2 * kAccCols;
+constexpr int kRow = kBK * 2;          // bytes of a K-major row, or of 64 columns in MN-major
+constexpr int kChunk = 64 * kRow;
+constexpr int kStageSpace = 229376;
+
+struct Header {
+    uint64_t bars[2 * kMaxStages + 5];
+    uint32_t tmem;
+    volatile int abort;
+};
+constexpr int kHeaderBytes = 1 << 10;
+constexpr int kSmemBytes = kHeaderBytes + kStageSpace;
+static_assert(sizeof(Header) <= kHeaderBytes && kSmemBytes <= 232448, "shared memory of one CTA");
+
+// One batched product: out[e] [R, C], summed over `red`; columns are the MMA's M.
+struct ProductArgs {
+    CUtensorMap map_a, map_b;
+    int E, R, C, red;
+    int cols, tile_rows, row_tiles, col_tiles, tiles;
+    int a_block, b_block, stages;
+    long long wait;
+    int *err;
+    // epilogue, see finish_symmetric and finish_x
+    const float2 *table;  // first step: s and the power of two, per matrix
+    const half *other;    // B: A; X: hi
+    const half *lo;
+    const void *g;        // first step of X: G itself
+    half *out, *out_lo;
+    bf16 *final;
+    int g_f32;
+    float k_acc, k_other, k_diag;
+};
+
+struct Place {
+    int e, row0, rows, col0;
+};
+
+// Walks tiles first, first + step, .. of all matrices, the column tile innermost.  SYM: of a row
+// tile only the column tiles that reach its first row or beyond.
+template <bool SYM>
+struct Walk {
+    const ProductArgs &p;
+    int tile, step, e = 0, r = 0, c;
+    __device__ __forceinline__ Walk(const ProductArgs &args, int first, int by) : p(args), tile(first), step(by), c(first) { settle(); }
+    __device__ __forceinline__ int skipped() const { return SYM ? r * p.tile_rows / p.cols : 0; }
+    __device__ __forceinline__ void settle() {
+        if (!SYM) {
+            const int per = p.row_tiles * p.col_tiles;
+            if (c >= per) {  // a matrix or more on
+                const int n = c / per;
+                e += n;
+                c -= n * per;
+            }
+        }
+        while (c >= p.col_tiles - skipped()) {
+            c -= p.col_tiles - skipped();
+            if (++r == p.row_tiles) {
+                r = 0;
+                ++e;
+            }
+        }
+    }
+    __device__ __forceinline__ bool more() const { return tile < p.tiles; }
+    __device__ __forceinline__ void next() {
+        tile += step;
+        c += step;
+        if (more()) settle();
+    }
+    __device__ __forceinline__ Place get() const {
+        const int row0 = r * p.tile_rows;
+        return {e, row0, min(p.tile_rows, p.R - row0), (c + skipped()) * p.cols};
+    }
+};
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack_half2(uint32_t v) { return __half22float2(*reinterpret_cast<const half2 *>(&v)); }
+
+// A tile of a symmetric result (A, or B from A) by one warp: the lane is column `col`, TMEM columns
+// are rows.  v = f (k_acc sum + k_other other + k_diag on the diagonal), f: s^2 for A, s for B.
+// Element (r, c) with c >= r is stored there and at (c, r); in a tile across the diagonal the
+// others are left to their mirror images, so the result is symmetric bit by bit.  `other` is read
+// in its mirror image too: a lane's 32 rows are 64 contiguous bytes there.
+__device__ __forceinline__ void finish_symmetric(const ProductArgs &p, const Place &t, uint32_t tcol, int col, int part, int lane) {
+    const size_t ld = p.C, base = (size_t)t.e * p.R * ld;
+    const bool ok = col < p.C;
+    float f = 1.0f;
+    if (p.table != nullptr) {
+        const float s = p.table[t.e].x;
+        f = p.other != nullptr ? s : s * s;
+    }
+    const int col_first = col - lane;
+    for (int c = 32 * part; c < t.rows; c += 32 * kParts) {
+        const int r0 = t.row0 + c, rows = min(32, t.rows - c);  // a multiple of 8, as all sizes are
+        if (col_first + 31 < r0) continue;                      // the chunk is below the diagonal
+        uint32_t v[32];
+        tmem_ld32(tcol + c, v);
+        uint4 a[4];
+        const size_t mirror = base + (size_t)col * ld + r0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = make_uint4(0, 0, 0, 0);
+            if (p.other != nullptr && ok && 8 * i < rows) a[i] = reinterpret_cast<const uint4 *>(p.other + mirror)[i];
+        }
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));  // not read before the wait
+        uint32_t h[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 o = unpack_half2((&a[i / 4].x)[i % 4]);
+            float x = fmaf(p.k_other, o.x, p.k_acc * __uint_as_float(v[2 * i]));
+            float y = fmaf(p.k_other, o.y, p.k_acc * __uint_as_float(v[2 * i + 1]));
+            if (r0 + 2 * i == col) x += p.k_diag;
+            if (r0 + 2 * i + 1 == col) y += p.k_diag;
+            h[i] = pack_half2(f * x, f * y);
+        }
+        if (col_first >= r0 + 32) {  // above the diagonal
+            if (ok) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (8 * i < rows)
+                        reinterpret_cast<uint4 *>(p.out + mirror)[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+            }
+            // both columns of a lane pair in one word, rows 2i (even lane) and 2i + 1
+            const int odd = lane & 1;
+            uint32_t *o = reinterpret_cast<uint32_t *>(p.out + base + (size_t)(r0 + odd) * ld + (col & ~1));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, h[i], 1);
+                if (ok && 2 * i < rows) o[i * ld] = __byte_perm(h[i], got, odd ? 0x3276 : 0x5410);
+            }
+        } else if (ok) {
+            half *down = p.out + base + (size_t)r0 * ld + col, *across = p.out + mirror;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                if (j >= rows || col < r0 + j) continue;
+                const half x = __ushort_as_half((unsigned short)(j & 1 ? h[j / 2] >> 16 : h[j / 2] & 0xffffu));
+                down[j * ld] = x;
+                across[j] = x;
+            }
+        }
+    }
+}
+
+// A tile of X by one warp: v = k_acc sum + k_other (hi + lo), or in the first step + k_other s 2^-k G;
+// stored as hi (and lo, in place of the old one), or as bf16 at the end.
+__device__ __forceinline__ void finish_x(const ProductArgs &p, const Place &t, uint32_t tcol, int col, int part, int lane) {
+    const int odd = lane & 1;
+    const bool ok = col < p.C;
+    const size_t ld = p.C;
+    float scale = p.k_other, shrink = 1.0f;
+    if (p.g != nullptr) {
+        scale *= p.table[t.e].x;
+        shrink = p.table[t.e].y;
+    }
+    for (int c = 32 * part; c < t.rows; c += 32 * kParts) {
+        const int left = ok ? t.rows - c - odd : 0;
+        const size_t at = ((size_t)t.e * p.R + t.row0 + c + odd) * ld + (col & ~1);
+        float2 old[16];
+        if (p.g != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                old[i] = make_float2(0.0f, 0.0f);
+                if (2 * i >= left) continue;
+                if (p.g_f32) {
+                    old[i] = *reinterpret_cast<const float2 *>(static_cast<const float *>(p.g) + at + 2 * i * ld);
+                } else {
+                    const uint32_t w = *reinterpret_cast<const uint32_t *>(static_cast<const bf16 *>(p.g) + at + 2 * i * ld);
+                    old[i] = make_float2(bf16_lo(w), bf16_hi(w));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) old[i] = make_float2(old[i].x * shrink, old[i].y * shrink);
+        } else if (p.lo != nullptr) {
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                hi[i] = 2 * i < left ? *reinterpret_cast<const uint32_t *>(p.other + at + 2 * i * ld) : 0u;
+                lo[i] = 2 * i < left ? *reinterpret_cast<const uint32_t *>(p.lo + at + 2 * i * ld) : 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float2 x = unpack_half2(hi[i]), y = unpack_half2(lo[i]);
+                old[i] = make_float2(x.x + y.x, x.y + y.y);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) old[i] = make_float2(0.0f, 0.0f);
+        }
+        uint32_t v[32];
+        tmem_ld32(tcol + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));  // not read before the wait
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t mine = odd ? v[2 * i + 1] : v[2 * i], give = odd ? v[2 * i] : v[2 * i + 1];
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
+            const float x = fmaf(scale, old[i].x, p.k_acc * __uint_as_float(odd ? got : mine));
+            const float y = fmaf(scale, old[i].y, p.k_acc * __uint_as_float(odd ? mine : got));
+            if (2 * i >= left) continue;
+            if (p.final != nullptr) {
+                *reinterpret_cast<uint32_t *>(p.final + at + 2 * i * ld) = pack_bf16x2(x, y);
+            } else {
+                const uint32_t h = pack_half2(x, y);
+                *reinterpret_cast<uint32_t *>(p.out + at + 2 * i * ld) = h;
+                if (p.out_lo != nullptr) {
+                    const float2 b = unpack_half2(h);
+                    *reinterpret_cast<uint32_t *>(p.out_lo + at + 2 * i * ld) = pack_half2(x - b.x, y - b.y);
+                }
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {  // as grouped_kernel.cuh
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(kChunk >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// A_MN, B_MN: the operand of the columns, of the rows, has its reduction index outermost.
+template <bool A_MN, bool B_MN, bool SYM>
+__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ ProductArgs p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Header &h = *reinterpret_cast<Header *>(smem);
+    const uint32_t base = smem_u32(smem) + kHeaderBytes;
+    const int a_block = p.a_block, b_block = p.b_block, stages = p.stages;
+    // all A blocks first: the MMA reads 128 columns of A where the box brought 64; the rest is
+    // whatever follows, and its results are not stored
+    const uint32_t sA = base, sB = base + (uint32_t)(stages * a_block);
+    const uint32_t bar0 = smem_u32(h.bars);
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
+    auto tfull_bar = [&](uint32_t a) { return bar0 + 8u * (2 * kMaxStages + a); };
+    auto tempty_bar = [&](uint32_t a) { return bar0 + 8u * (2 * kMaxStages + 2 + a); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * kMaxStages + 4);
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank();
+    const bool leader = rank == 0;
+    volatile int *abort_flag = &h.abort;
+    auto raise = [&]() {  // stops both CTAs' roles
+        atomicOr(p.err, ERR_TIMEOUT);
+        *abort_flag = 1;
+        st_cluster_s32(mapa_shared(smem_u32(const_cast<int *>(&h.abort)), (uint32_t)rank ^ 1u), 1);
+    };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (uint32_t a = 0; a < 2; ++a) {
+            mbar_init(tfull_bar(a), 1);
+            mbar_init(tempty_bar(a), 2 * kEpiWarps);  // both CTAs'
+        }
+        mbar_init(drain_bar, 1);
+        fence_mbar_init();
+        h.abort = 0;
+        tma_prefetch_desc(&p.map_a);
+        tma_prefetch_desc(&p.map_b);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(&h.tmem), kTmemCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before any copy or arrival crosses over
+    tc_fence_after();
+    const uint32_t tmem_base = h.tmem;
+    pdl_wait();  // the operands, by earlier kernels on the stream
+    pdl_trigger();
+    const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
+    const int half_cols = p.cols / 2, n = p.tile_rows;
+
+    if (warp == 0) {
+        const bool two_b = n / 2 > 64;
+        const uint32_t bytes = a_block + (B_MN ? (two_b ? 2 : 1) * kChunk : (n / 2) * kRow);
+        uint32_t ph = 1;
+        int s = 0;
+        bool ok = true;
+        for (Walk<SYM> walk(p, first, stride); ok && walk.more(); walk.next()) {
+            const Place t = walk.get();
+            const int col = t.col0 + rank * half_cols, row = t.row0 + rank * (n / 2);
+            for (int r = 0; r < p.red; r += kBK) {
+                if (!__all_sync(0xffffffffu, wait_bar(empty_bar(s), ph, p.wait, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t da = sA + s * a_block, db = sB + s * b_block, bar = mapa_shared(full_bar(s), 0);
+                if (elect_one()) {
+                    if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * bytes);
+                    if (A_MN) {
+                        tma_load_3d_pair(da, &p.map_a, bar, col, r, t.e);
+                        if (half_cols > 64) tma_load_3d_pair(da + kChunk, &p.map_a, bar, col + 64, r, t.e);
+                    } else {
+                        tma_load_3d_pair(da, &p.map_a, bar, r, col, t.e);
+                    }
+                    if (B_MN) {
+                        tma_load_3d_pair(db, &p.map_b, bar, row, r, t.e);
+                        if (two_b) tma_load_3d_pair(db + kChunk, &p.map_b, bar, row + 64, r, t.e);
+                    } else {
+                        tma_load_3d_pair(db, &p.map_b, bar, r, row, t.e);
+                    }
+                }
+                __syncwarp();
+                if (++s == stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        if (!ok && lane == 0) raise();
+    } else if (warp == 1) {
+        if (leader) {
+            constexpr uint32_t kStepA = A_MN ? (16 * kRow) >> 4 : 2;  // 16 reduction steps on,
+            constexpr uint32_t kStepB = B_MN ? (16 * kRow) >> 4 : 2;  // in units of 16 bytes
+            const uint64_t desc_a = A_MN ? smem_desc_mn(sA) : smem_desc_k128(sA);
+            const uint64_t desc_b = B_MN ? smem_desc_mn(sB) : smem_desc_k128(sB);
+            // fp16 operands (their format fields are 0), fp32 sums
+            const uint32_t idesc = (1u << 4) | (uint32_t)(n >> 3) << 17 | (256u >> 4) << 24 | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+            uint32_t ph = 0, acc = 0, free_ph = 1;
+            int s = 0;
+            bool ok = p.wait != 0, issued = false;  // a bound of 0: give up at once
+            for (int tile = first; ok && tile < p.tiles; tile += stride) {
+                const uint32_t d = tmem_base + acc * kAccCols;
+                if (!__all_sync(0xffffffffu, wait_bar<true>(tempty_bar(acc), free_ph, p.wait, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                for (int r = 0; r < p.red; r += kBK) {
+                    if (!__all_sync(0xffffffffu, wait_bar(full_bar(s), ph, p.wait, abort_flag))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t ad = desc_a + (uint32_t)(s * a_block >> 4), bd = desc_b + (uint32_t)(s * b_block >> 4);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < kBK / 16; ++k)
+                            tc_mma_bf16_pair(d, ad + k * kStepA, bd + k * kStepB, idesc, (r + k) != 0);
+                        tc_commit_pair(empty_bar(s), 3);  // frees the stage in both CTAs
+                        if (r + kBK >= p.red) tc_commit_pair(tfull_bar(acc), 3);
+                    }
+                    __syncwarp();
+                    issued = true;
+                    if (++s == stages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                acc ^= 1u;
+                if (acc == 0) free_ph ^= 1u;
+            }
+            if (!ok && lane == 0) {
+                raise();
+                if (issued) {
+                    tc_commit_pair(drain_bar, 1);
+                    wait_bar(drain_bar, 0, kDrainCycles, nullptr);
+                }
+            }
+        }
+    } else {
+        const int q = warp & 3;  // the TMEM lane quadrant this warp may read
+        const int part = (warp - 2) >> 2;
+        const bool mine = 32 * q < half_cols;
+        uint32_t acc = 0, ph = 0;
+        for (Walk<SYM> walk(p, first, stride); walk.more(); walk.next()) {
+            const Place t = walk.get();
+            const uint32_t tcol = tmem_base + ((uint32_t)(q * 32) << 16) + acc * kAccCols;
+            const int col = t.col0 + rank * half_cols + 32 * q + lane;
+            if (!__all_sync(0xffffffffu, wait_bar<true>(tfull_bar(acc), ph, p.wait, abort_flag))) {
+                if (lane == 0) raise();
+                break;
+            }
+            tc_fence_after();
+            if (mine) {
+                if (SYM)
+                    finish_symmetric(p, t, tcol, col, part, lane);
+                else
+                    finish_x(p, t, tcol, col, part, lane);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_bar(acc), 0));
+            acc ^= 1u;
+            if (acc == 0) ph ^= 1u;
+        }
+    }
+
+    leave_pair(abort_flag);
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------ |G|, X0
+
+constexpr int kNormThreads = 256;
+constexpr int kPerThread = 32;                       // values of a thread
+constexpr int kBlock = kNormThreads * kPerThread;    // values of a CTA: one matrix's, in turn
+
+// 8 values from p, as loaded
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, float (&o)[8]);
+template <>
+__device__ __forceinline__ void load8<float>(const float *p, float (&o)[8]) {
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+}
+template <>
+__device__ __forceinline__ void load8<bf16>(const bf16 *p, float (&o)[8]) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+    o[0] = bf16_lo(v.x), o[1] = bf16_hi(v.x), o[2] = bf16_lo(v.y), o[3] = bf16_hi(v.y);
+    o[4] = bf16_lo(v.z), o[5] = bf16_hi(v.z), o[6] = bf16_lo(v.w), o[7] = bf16_hi(v.w);
+}
+
+// Sum over the CTA, in thread 0 alone.
+__device__ __forceinline__ double cta_sum(double v, double *shared) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int w = 1; w < kNormThreads / 32; ++w) v += shared[w];
+    return v;
+}
+
+// Squares of a part of one matrix: a thread's 32 in fp32, the rest in fp64 (squares outside
+// [1e-30, 1e30] in sum are taken again in fp64).
+template <typename T>
+__global__ void __launch_bounds__(kNormThreads) square_kernel(const T *g, long long size, int parts, double *partial) {
+    __shared__ double shared[kNormThreads / 32];
+    const int e = blockIdx.x / parts, part = blockIdx.x - e * parts;
+    pdl_wait();
+    pdl_trigger();
+    const T *at = g + (size_t)e * size;
+    double sum = 0.0;
+    for (long long i = (long long)part * kBlock + 8 * threadIdx.x; i < size; i += (long long)parts * kBlock) {
+        float s = 0.0f, most = 0.0f, v[8];
+#pragma unroll
+        for (int j = 0; j < kPerThread / 8; ++j) {
+            const long long k = i + (long long)j * 8 * kNormThreads;
+            if (k >= size) break;
+            load8(at + k, v);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) s = fmaf(v[x], v[x], s), most = fmaxf(most, fabsf(v[x]));
+        }
+        if ((s > 1e-30f && s < 1e30f) || most == 0.0f) {  // (a NaN beside zeros is in s)
+            sum += s;
+        } else {
+            for (int j = 0; j < kPerThread / 8; ++j) {
+                const long long k = i + (long long)j * 8 * kNormThreads;
+                if (k >= size) break;
+                load8(at + k, v);
+                for (int x = 0; x < 8; ++x) sum += (double)v[x] * v[x];
+            }
+        }
+    }
+    sum = cta_sum(sum, shared);
+    if (threadIdx.x == 0) partial[blockIdx.x] = sum;
+}
+
+// table[e] = (s, 2^-k) with 2^k <= |G| + eps < 2^(k + 1), s = 2^k / (|G| + eps); X0 = up 2^-k G.
+// Each CTA adds up its matrix's sums.
+template <typename T>
+__global__ void __launch_bounds__(kNormThreads) scale_kernel(const T *g, long long size, int parts, const double *partial,
+                                                             float eps, float up, float2 *table, half *x) {
+    __shared__ double shared[kNormThreads / 32];
+    __shared__ float shrink_of;
+    const int e = blockIdx.x / parts, part = blockIdx.x - e * parts;
+    pdl_wait();
+    pdl_trigger();
+    double v = 0.0;
+    for (int i = threadIdx.x; i < parts; i += kNormThreads) v += partial[e * parts + i];
+    v = cta_sum(v, shared);
+    if (threadIdx.x == 0) {
+        const double norm = sqrt(v) + (double)eps;
+        float s = nanf(""), shrink = 1.0f;  // an infinity or a NaN: all of the result is NaN
+        if (norm < INFINITY) {
+            int k;
+            s = (float)(1.0 / (2.0 * frexp(norm, &k)));
+            shrink = (float)ldexp(1.0, 1 - k);
+        }
+        shrink_of = shrink;
+        if (part == 0) table[e] = make_float2(s, shrink);
+    }
+    __syncthreads();
+    const float shrink = shrink_of;
+    const T *at = g + (size_t)e * size;
+    half *to = x + (size_t)e * size;
+    for (long long i = (long long)part * kBlock + 8 * threadIdx.x; i < size; i += (long long)parts * kBlock) {
+#pragma unroll
+        for (int j = 0; j < kPerThread / 8; ++j) {
+            const long long k = i + (long long)j * 8 * kNormThreads;
+            if (k >= size) break;
+            float o[8];
+            load8(at + k, o);
+#pragma unroll
+            for (int x8 = 0; x8 < 8; ++x8) o[x8] = o[x8] * shrink * up;
+            *reinterpret_cast<uint4 *>(to + k) =
+                make_uint4(pack_half2(o[0], o[1]), pack_half2(o[2], o[3]), pack_half2(o[4], o[5]), pack_half2(o[6], o[7]));
+        }
+    }
+}
+
+// ---------------------------------------------------------------------- host
+
+OpDone g_attr[4];
+
+constexpr int kMaxSteps = 64;
+constexpr int kMaxParts = 64;  // CTAs of a matrix in the two kernels above
+
+int parts_of(long long size) { return (int)std::min<long long>(kMaxParts, (size + kBlock - 1) / kBlock); }
+
+struct Workspace {
+    size_t table, partial, x[2], lo, a, b, bytes;
+};
+Workspace lay_out(int E, int N, int K) {
+    const size_t n = (size_t)N * K, m = std::min(N, K), e = E;
+    auto room = [](size_t bytes) { return (bytes + 1023) / 1024 * 1024; };
+    Workspace w;
+    w.table = 0;
+    w.partial = w.table + room(e * sizeof(float2));
+    w.x[0] = w.partial + room(e * kMaxParts * sizeof(double));
+    w.x[1] = w.x[0] + room(2 * e * n);
+    w.lo = w.x[1] + room(2 * e * n);
+    w.a = w.lo + room(2 * e * n);
+    w.b = w.a + room(2 * e * m * m);
+    w.bytes = w.b + room(2 * e * m * m);
+    return w;
+}
+
+// Scales of one step's A and B, and of X: powers of two that keep what is stored below 60000.
+struct Scales {
+    float a, b;
+};
+double largest(double limit, double (*of)(double, const float *), const float *c) {
+    double most = 0.0;
+    for (int i = 0; i <= 4096; ++i) most = std::max(most, std::fabs(of(limit * i / 4096, c)));
+    return 1.01 * most;
+}
+float power_below(double bound, int most) {
+    return (float)std::ldexp(1.0, std::min(most, std::ilogb(60000.0 / std::max(bound, 1e-6))));
+}
+// Steps whose X keeps its rounding, and does not put a into B.
+bool keeps_lo(int step, int steps) { return step < steps - 2; }
+
+// false: the polynomials let a singular value grow beyond what fp16 holds
+bool choose_scales(const float *coef, int steps, Scales *scales, float *up) {
+    double x = 1.0, most = 1.0;
+    for (int i = 0; i < steps; ++i) {
+        const float *c = coef + 3 * i;
+        auto whole = [](double l, const float *k) { return k[0] + l * (k[1] + l * k[2]); };
+        auto rest = [](double l, const float *k) { return l * (k[1] + l * k[2]); };
+        auto step = [](double v, const float *k) { return v * (k[0] + v * v * (k[1] + v * v * k[2])); };
+        scales[i].a = power_below(1.01 * x * x, 14);
+        scales[i].b = power_below(keeps_lo(i, steps) ? largest(x * x, rest, c) : largest(x * x, whole, c), 14);
+        x = largest(x, step, c);
+        if (!(x < 1024.0)) return false;
+        if (i + 1 < steps) most = std::max(most, x);
+    }
+    *up = power_below(1.01 * most, 12);
+    return true;
+}
+
+// Tile sizes: 256 x 256, of fewer rows (down to 32) while the pairs outnumber the tiles; a matrix's
+// rows are dealt evenly to its tiles, in multiples of 32.
+long long count_tiles(const ProductArgs &g, bool sym) {
+    if (!sym) return (long long)g.E * g.row_tiles * g.col_tiles;
+    long long n = 0;
+    for (int r = 0; r < g.row_tiles; ++r) n += g.col_tiles - r * g.tile_rows / g.cols;
+    return n * g.E;
+}
+long long choose_tiles(ProductArgs &g, bool b_mn, bool sym, int sms) {
+    g.cols = g.C > 128 ? 256 : 128;
+    g.col_tiles = (g.C + g.cols - 1) / g.cols;
+    long long tiles = 0;
+    for (int rows = 256; rows >= 32; rows /= 2) {
+        const int parts = (g.R + rows - 1) / rows;
+        const int share = ((g.R + parts - 1) / parts + 31) / 32 * 32;  // the pair's MMA takes N in steps of 32
+        const ProductArgs before = g;
+        g.tile_rows = share;
+        g.row_tiles = (g.R + share - 1) / share;
+        const long long now = count_tiles(g, sym);
+        if (tiles > 0 && now > sms / 2) {
+            g = before;
+            break;
+        }
+        tiles = now;
+        if (2 * now > sms / 2) break;
+    }
+    g.a_block = g.cols / 2 * kRow;
+    g.b_block = b_mn ? (g.tile_rows / 2 + 63) / 64 * kChunk : g.tile_rows / 2 * kRow;
+    g.stages = std::min(kMaxStages, kStageSpace / (g.a_block + g.b_block));
+    return tiles;
+}
+
+// The operand [E, outer, inner] of fp16; `mn`: its reduction index is the outer one.
+CUresult operand_map(CUtensorMap *m, const half *p, int E, int outer, int inner, bool mn, int box) {
+    return op_encode(m, {CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p, {(uint64_t)inner, (uint64_t)outer, (uint64_t)E},
+                         {(uint64_t)inner * 2, (uint64_t)inner * outer * 2}, {64, mn ? (uint32_t)kBK : (uint32_t)box, 1},
+                         CU_TENSOR_MAP_SWIZZLE_128B});
+}
+
+struct Operand {
+    const half *p;
+    int outer, inner;
+};
+
+template <bool A_MN, bool B_MN, bool SYM>
+moe_status product(const char *name, ProductArgs &g, const Operand &a, const Operand &b, int which, int sms, cudaStream_t s) {
+    const long long tiles = choose_tiles(g, B_MN, SYM, sms);
+    if (tiles > (1ll << 30)) return op_fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^30 tiles", name);
+    g.tiles = (int)tiles;
+    g.wait = wait_cycles(g.red / kBK + 1);
+    CUresult cr = operand_map(&g.map_a, a.p, g.E, a.outer, a.inner, A_MN, g.cols / 2);
+    if (cr == CUDA_SUCCESS) cr = operand_map(&g.map_b, b.p, g.E, b.outer, b.inner, B_MN, g.tile_rows / 2);
+    if (cr != CUDA_SUCCESS) return op_fail(MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", name, (int)cr);
+    auto kernel = product_kernel<A_MN, B_MN, SYM>;
+    const cudaError_t ce = op_allow_smem(reinterpret_cast<const void *>(kernel), kSmemBytes, &g_attr[which]);
+    if (ce != cudaSuccess) return op_cuda(ce, name);
+    return op_cuda(launch_pdl_cluster(kernel, dim3(2u * (unsigned)std::min<long long>(sms / 2, tiles)), dim3(kThreads),
+                                      (size_t)kSmemBytes, s, dim3(2, 1, 1), g), name);
+}
+
+moe_status check_sizes(const char *name, int E, int N, int K) {
+    if (E < 0 || N < 1 || K < 1) return op_fail(MOE_ERR_INVALID_ARG, "%s: need E >= 0, N >= 1, K >= 1", name);
+    if (E > 65535 || N % 8 || K % 8 || N > kMaxSide || K > kMaxSide)
+        return op_fail(MOE_ERR_UNSUPPORTED, "%s: E up to 65535, N and K multiples of 8 up to %d (E %d, N %d, K %d)", name,
+                       kMaxSide, E, N, K);
+    return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" moe_status moe_orthogonalize_workspace(int E, int N, int K, size_t *bytes) {
+    using namespace moe;
+    const char *name = "moe_orthogonalize_workspace";
+    const moe_status st = check_sizes(name, E, N, K);
+    if (st != MOE_OK) return st;
+    if (bytes == nullptr) return op_fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", name);
+    *bytes = lay_out(E, N, K).bytes;
+    return MOE_OK;
+}
+
+extern "C" moe_status moe_orthogonalize(const void *G, int dtype, int E, int N, int K, const float *coefficients, int steps,
+                                        float eps, float scale, void *out, void *workspace, size_t workspace_bytes,
+                                        moe_stream_t stream) {
+    using namespace moe;
+    const char *name = "moe_orthogonalize";
+    moe_status st = check_sizes(name, E, N, K);
+    if (st != MOE_OK) return st;
+    if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F32) return op_fail(MOE_ERR_INVALID_ARG, "%s: unknown dtype %d", name, dtype);
+    if (steps < 1 || steps > kMaxSteps || coefficients == nullptr)
+        return op_fail(MOE_ERR_INVALID_ARG, "%s: need 1 to %d steps and their coefficients", name, kMaxSteps);
+    for (int i = 0; i < 3 * steps; ++i)
+        if (!(coefficients[i] - coefficients[i] == 0.0f)) return op_fail(MOE_ERR_INVALID_ARG, "%s: coefficients must be finite", name);
+    if (!(eps >= 1e-30f && eps < INFINITY) || !(scale - scale == 0.0f))
+        return op_fail(MOE_ERR_INVALID_ARG, "%s: need eps >= 1e-30 and a finite scale", name);
+    Scales scales[kMaxSteps];
+    float up;
+    if (!choose_scales(coefficients, steps, scales, &up))
+        return op_fail(MOE_ERR_UNSUPPORTED, "%s: these coefficients let singular values grow beyond 1024", name);
+    if (E == 0) return MOE_OK;
+    const Workspace w = lay_out(E, N, K);
+    if (!G || !out || !workspace || workspace_bytes < w.bytes)
+        return op_fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer, or less than %zu bytes of workspace", name, w.bytes);
+    if (!op_aligned16(G) || !op_aligned16(out) || !op_aligned16(workspace))
+        return op_fail(MOE_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", name);
+    const uint64_t n = (uint64_t)E * N * K, gb = n * (dtype == MOE_DTYPE_F32 ? 4 : 2);
+    const bool in_place = out == G && dtype == MOE_DTYPE_BF16;
+    if ((op_overlap(out, 2 * n, G, gb) && !in_place) || op_overlap(workspace, w.bytes, G, gb) || op_overlap(workspace, w.bytes, out, 2 * n))
+        return op_fail(MOE_ERR_INVALID_ARG, "%s: the output or the workspace overlaps another tensor", name);
+    const int sms = op_num_sms();
+    int *err = op_error_word();
+    if (sms < 2 || err == nullptr) return op_fail(MOE_ERR_CUDA, "%s: no usable current device", name);
+
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    float2 *table = reinterpret_cast<float2 *>(ws + w.table);
+    double *partial = reinterpret_cast<double *>(ws + w.partial);
+    half *x[2] = {reinterpret_cast<half *>(ws + w.x[0]), reinterpret_cast<half *>(ws + w.x[1])};
+    half *lo = reinterpret_cast<half *>(ws + w.lo), *A = reinterpret_cast<half *>(ws + w.a), *B = reinterpret_cast<half *>(ws + w.b);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const long long size = (long long)N * K;
+    const int parts = parts_of(size);
+    const dim3 grid((unsigned)(E * parts));
+    cudaError_t ce;
+    if (dtype == MOE_DTYPE_F32) {
+        const float *g = static_cast<const float *>(G);
+        ce = launch_pdl(square_kernel<float>, grid, dim3(kNormThreads), 0, s, g, size, parts, partial);
+        if (ce == cudaSuccess)
+            ce = launch_pdl(scale_kernel<float>, grid, dim3(kNormThreads), 0, s, g, size, parts, static_cast<const double *>(partial), eps, up, table, x[0]);
+    } else {
+        const bf16 *g = static_cast<const bf16 *>(G);
+        ce = launch_pdl(square_kernel<bf16>, grid, dim3(kNormThreads), 0, s, g, size, parts, partial);
+        if (ce == cudaSuccess)
+            ce = launch_pdl(scale_kernel<bf16>, grid, dim3(kNormThreads), 0, s, g, size, parts, static_cast<const double *>(partial), eps, up, table, x[0]);
+    }
+    if (ce != cudaSuccess) return op_cuda(ce, name);
+
+    const bool wide = N <= K;
+    const int m = std::min(N, K);
+    for (int i = 0; i < steps; ++i) {
+        const float *c = coefficients + 3 * i, sa = scales[i].a, sb = scales[i].b;
+        const bool keep = keeps_lo(i, steps);
+        const Operand X{x[i & 1], N, K}, sym_a{A, m, m}, sym_b{B, m, m};
+        ProductArgs g = {};  // A
+        g.E = E, g.R = g.C = m, g.red = wide ? K : N, g.err = err;
+        g.table = i == 0 ? table : nullptr;
+        g.out = A;
+        g.k_acc = sa / (up * up);
+        st = wide ? product<false, false, true>(name, g, X, X, 0, sms, s) : product<true, true, true>(name, g, X, X, 1, sms, s);
+        if (st != MOE_OK) return st;
+
+        g = {};  // B
+        g.E = E, g.R = g.C = g.red = m, g.err = err;
+        g.table = i == 0 ? table : nullptr;
+        g.other = A;
+        g.out = B;
+        g.k_acc = c[2] / sa / sa * sb;
+        g.k_other = c[1] / sa * sb;
+        g.k_diag = keep ? 0.0f : c[0] * sb;
+        st = product<false, false, true>(name, g, sym_a, sym_a, 0, sms, s);
+        if (st != MOE_OK) return st;
+
+        g = {};  // X
+        g.E = E, g.R = N, g.C = K, g.red = m, g.err = err;
+        const bool last = i + 1 == steps;
+        const float unit = last ? scale / up : 1.0f;  // of what is stored
+        g.k_acc = unit / sb;
+        if (keep) {
+            g.k_other = c[0] * unit;
+            if (i == 0) {
+                g.k_other *= up;
+                g.table = table;
+                g.g = G;
+                g.g_f32 = dtype == MOE_DTYPE_F32;
+            } else {
+                g.other = x[i & 1];
+                g.lo = lo;
+            }
+        }
+        g.out = x[(i + 1) & 1];
+        g.out_lo = !last && keeps_lo(i + 1, steps) ? lo : nullptr;
+        g.final = last ? static_cast<bf16 *>(out) : nullptr;
+        st = wide ? product<true, false, false>(name, g, X, sym_b, 2, sms, s) : product<false, false, false>(name, g, sym_b, X, 3, sms, s);
+        if (st != MOE_OK) return st;
+    }
+    return MOE_OK;
+}

@@ -484,6 +484,22 @@ moe_status moe_mx_grouped_forward(const void *Xc, const uint8_t *Xs, const void 
                                   const int32_t *offs, int rows, int E, int N, int K, int out_dtype, void *Y,
                                   moe_stream_t stream);
 
+/* Orthogonalising an update by Newton-Schulz products: for each matrix of G [E, N, K] (dtype:
+ * moe_dtype) X = G / (|G|_F + eps), then `steps` (up to 64) times, with its own (a, b, c) from the host array
+ * coefficients [steps][3],
+ *   X <- a X + (b A + c A^2) X,  A = X X^T
+ * and out = scale X [E, N, K] bf16, in place where G is bf16 and out == G.  The products run from the smaller side.
+ * X, A and the polynomial are held in fp16 with scales from bounds of the singular values, sums in
+ * fp32; the low half of X is carried through a X in all steps but the last two.  Coefficients that
+ * let singular values from [0, 1] grow beyond 1024 are refused.  A matrix with an infinity or a
+ * NaN gives NaN, and no other does.  N and K multiples of 8 up to 16384, E up to 65535 (0: no-op); eps >= 1e-30.
+ * `workspace` as in moe_clip_grad_norm.  Errors: INVALID_ARG, UNSUPPORTED, CUDA; a wait that
+ * runs out is reported by moe_operators_status. */
+moe_status moe_orthogonalize_workspace(int E, int N, int K, size_t *bytes);
+moe_status moe_orthogonalize(const void *G, int dtype, int E, int N, int K, const float *coefficients, int steps,
+                             float eps, float scale, void *out, void *workspace, size_t workspace_bytes,
+                             moe_stream_t stream);
+
 /* One gradient of moe_clip_grad_norm (device pointers, aligned to their type; 16-byte
  * alignment of both is faster). */
 typedef struct {

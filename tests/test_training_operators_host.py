@@ -130,3 +130,34 @@ def test_norm_outputs_overlap(lib):
             if out in in_place:  # in place, but shifted
                 shifted = ctypes.c_void_p(base[in_place[out]].value + 16)
                 assert call(lib, **{out: shifted}) == INVALID, out
+
+
+QUINTIC = (3.4445, -4.7750, 2.0315)
+ORTHO = {"G": at(1), "dtype": 1, "E": 2, "N": 64, "K": 128, "coefficients": QUINTIC * 5, "steps": 5, "eps": 1e-7, "scale": 1.0,
+         "out": at(2), "work": at(3), "size": 1 << 22}
+
+
+def ortho(lib, **change):
+    a = {**ORTHO, **change}
+    if a["coefficients"] is not None:
+        a["coefficients"] = (ctypes.c_float * len(a["coefficients"]))(*a["coefficients"])
+    return lib.moe_orthogonalize(*a.values(), None)
+
+
+def test_orthogonalize_refusals(lib):
+    for change, status in [({"G": None}, INVALID), ({"out": None}, INVALID), ({"work": None}, INVALID), ({"G": ODD}, INVALID),
+                           ({"out": ODD}, INVALID), ({"work": ODD}, INVALID), ({"dtype": 2}, INVALID), ({"E": -1}, INVALID),
+                           ({"N": 0}, INVALID), ({"K": -8}, INVALID), ({"N": 60}, UNSUPPORTED), ({"K": 16392}, UNSUPPORTED),
+                           ({"E": 65536}, UNSUPPORTED), ({"steps": 0}, INVALID), ({"steps": 65, "coefficients": QUINTIC * 65}, INVALID),
+                           ({"coefficients": None}, INVALID), ({"coefficients": QUINTIC * 4 + (NAN, 0.0, 0.0)}, INVALID),
+                           ({"coefficients": QUINTIC * 4 + (INF, 0.0, 0.0)}, INVALID), ({"coefficients": (40.0, 0.0, 0.0) * 5}, UNSUPPORTED),
+                           ({"eps": 0.0}, INVALID), ({"eps": NAN}, INVALID), ({"scale": NAN}, INVALID), ({"size": 1024}, INVALID),
+                           ({"out": at(1)}, INVALID), ({"work": at(1)}, INVALID), ({"work": at(2)}, INVALID),
+                           ({"out": ctypes.c_void_p((1 << 24) + 16), "dtype": 0}, INVALID)]:
+        assert ortho(lib, **change) == status, change
+        assert "moe_orthogonalize" in lib.moe_last_error().decode()
+    assert ortho(lib, E=0, G=None, out=None, work=None, size=0) == OK
+    need = ctypes.c_size_t()
+    assert lib.moe_orthogonalize_workspace(2, 64, 128, None) == INVALID
+    assert lib.moe_orthogonalize_workspace(2, 64, 100, ctypes.byref(need)) == UNSUPPORTED
+    assert lib.moe_orthogonalize_workspace(2, 64, 128, ctypes.byref(need)) == OK and need.value <= ORTHO["size"]
