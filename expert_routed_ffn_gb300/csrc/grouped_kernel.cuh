@@ -357,6 +357,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
         const int part = (warp - 2) >> 2;
         const bool mine = 32 * q < half_cols;
         Accumulators accs;
+        [[maybe_unused]] GatedBack back;
         auto release = [&](uint32_t a) {  // the MMA may write accumulator a
             tc_fence_before();
             __syncwarp();
@@ -367,6 +368,9 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
             const bool empty = t.r0 >= t.r1;
             const uint32_t a = accs.next, tmem_q = tmem_base + ((uint32_t)(q * 32) << 16);
             const int col = t.col0 + rank * half_cols + in_half;
+            if constexpr (OP == kGatedBack) {
+                if (t.last && mine && 32 * part < t.rows) back.fetch(h.gated, t, col, 32 * part, lane);
+            }
             if (!empty) {
                 if (!__all_sync(0xffffffffu, wait_bar<true>(tfull_bar(a), accs.ready(), p.o.wait + walk.slack, abort_flag))) {
                     if (lane == 0) raise();
@@ -385,7 +389,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
                     const int out_col = (t.col0 + rank * half_cols + 32 * q) / 2 + (lane & (kGranule - 1));
                     if (mine) store_gated<kParts>(tab.o, h.gated, t, tmem_q + from * kAccCols, out_col, part, lane);
                 } else if constexpr (OP == kGatedBack) {
-                    if (mine) store_gated_back<kParts>(h.gated, t, tmem_q + from * kAccCols, col, part, lane);
+                    if (mine) back.template store<kParts>(h.gated, t, tmem_q + from * kAccCols, col, part, lane);
                 } else {
                     if (mine) store_tile<kDense, ADD, kParts>(tab.o, t, tmem_q + from * kAccCols, empty, col, part, lane);
                 }

@@ -229,7 +229,9 @@ __global__ void __launch_bounds__(kThreads, 1) norm_forward_kernel(const Sandwic
 
 template <typename TX, typename TF, int V>
 __global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const SandwichArgs p) {
-    extern __shared__ float smem[];  // the effective weights and the channels' gate [3][H], later the teams' sums
+    // the effective weights and the channels' gate, later the teams' sums: three arrays of H values, the first
+    // four values of each group of 8 in one half, the other four in the other, so that a warp's loads have no bank conflicts
+    extern __shared__ float4 smem[];
     __shared__ float slots[kMaxTeams * 96];
     Team team = make_team(slots, p.team);
     const int me = threadIdx.x - team.id * p.team, H = p.H;
@@ -239,11 +241,24 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const Sandwi
     const bool channel = p.gate_kind == MOE_GATE_CHANNEL, token = p.gate_kind == MOE_GATE_TOKEN;
     pdl_wait();
     pdl_trigger();
-    for (int i = threadIdx.x; i < H; i += blockDim.x) {
-        smem[i] = has_pre ? p.pre[i] + p.one : 0.0f;
-        smem[H + i] = has_post ? p.post[i] + p.one : 1.0f;
-        smem[2 * H + i] = channel ? p.gate[i] : 1.0f;
+    const int groups = H / 8;
+    for (int i = threadIdx.x; i < 2 * groups; i += blockDim.x) {  // i: group of 4 values
+        const int to = (i & 1) * groups + i / 2;
+        auto four = [&](const float *w, float otherwise, float more) {
+            if (w == nullptr) return make_float4(otherwise, otherwise, otherwise, otherwise);
+            const float4 v = reinterpret_cast<const float4 *>(w)[i];
+            return make_float4(v.x + more, v.y + more, v.z + more, v.w + more);
+        };
+        smem[to] = four(p.pre, 0.0f, p.one);
+        smem[2 * groups + to] = four(p.post, 1.0f, p.one);
+        smem[4 * groups + to] = four(channel ? p.gate : nullptr, 1.0f, 0.0f);
     }
+    auto weights = [&](int which, int i, float (&w)[8]) {
+        const int g = me + i * p.team;
+        const float4 *at = smem + 2 * which * groups + (g < groups ? g : 0);  // (values beyond H are zeros)
+        const float4 a = at[0], b = at[groups];
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    };
     bool in[V];
     float d_pre[V][8], d_post[V][8], d_gate[V][8];
 #pragma unroll
@@ -284,9 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const Sandwi
             s[0] = s[1] = s[2] = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float *pre = smem + 8 * (me + i * p.team);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = in[i] ? pre[j] : 0.0f;
+                weights(0, i, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     s[0] = fmaf(x[i][j] * sx, x[i][j] * sx, s[0]);
@@ -308,9 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const Sandwi
         if (has_pre) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float *pre = smem + 8 * (me + i * p.team);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = in[i] ? pre[j] : 0.0f;
+                weights(0, i, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float xh = x[i][j] * rx;
@@ -331,15 +342,16 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const Sandwi
         float m[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float *post = smem + H + 8 * (me + i * p.team), *gates = post + H;
             float wg[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = in[i] ? post[j] : 0.0f, wg[j] = in[i] ? gates[j] : 0.0f;
+            weights(1, i, w);
+            if (channel) weights(2, i, wg);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float fh = f[i][j] * rf;
-                d_gate[i][j] = fmaf(t[i][j], fh * w[j], d_gate[i][j]);
-                t[i][j] *= wg[j];
+                if (channel) {
+                    d_gate[i][j] = fmaf(t[i][j], fh * w[j], d_gate[i][j]);
+                    t[i][j] *= wg[j];
+                }
                 m[0] = fmaf(t[i][j] * w[j], fh, m[0]);
                 t[i][j] *= g;
                 d_post[i][j] = fmaf(t[i][j], fh, d_post[i][j]);
@@ -354,10 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const Sandwi
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float *post = smem + H + 8 * (me + i * p.team);
             float o[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = in[i] ? post[j] : 0.0f;
+            weights(1, i, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[j] = rf * (has_post ? fmaf(-f[i][j], mean_f, t[i][j] * w[j]) : t[i][j]);
             if (in[i]) Raw<TF>::store(static_cast<TF *>(p.fo) + (size_t)row * H + 8 * (me + i * p.team), o);
@@ -372,19 +382,28 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const Sandwi
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 if (!in[i]) continue;
-                float *at = smem + 8 * (me + i * p.team);
+                auto add = [&](float4 *at, const float *d) {
+                    const float4 v = k ? *at : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    *at = make_float4(v.x + d[0], v.y + d[1], v.z + d[2], v.w + d[3]);
+                };
+                float4 *at = smem + me + i * p.team;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    at[j] = d_pre[i][j] + (k ? at[j] : 0.0f);
-                    at[H + j] = d_post[i][j] + (k ? at[H + j] : 0.0f);
-                    at[2 * H + j] = d_gate[i][j] + (k ? at[2 * H + j] : 0.0f);
+                for (int h = 0; h < 2; ++h) {
+                    add(at + h * groups, d_pre[i] + 4 * h);
+                    add(at + (2 + h) * groups, d_post[i] + 4 * h);
+                    if (channel) add(at + (4 + h) * groups, d_gate[i] + 4 * h);
                 }
             }
         }
         __syncthreads();
     }
-    float *mine = p.partial + (size_t)blockIdx.x * 3 * H;
-    for (int i = threadIdx.x; i < 3 * H; i += blockDim.x) mine[i] = smem[i];
+    float4 *mine = reinterpret_cast<float4 *>(p.partial + (size_t)blockIdx.x * 3 * H);
+    for (int i = threadIdx.x; i < 2 * groups; i += blockDim.x) {
+        const int from = (i & 1) * groups + i / 2;
+        mine[i] = smem[from];
+        mine[2 * groups + i] = smem[2 * groups + from];
+        if (channel) mine[4 * groups + i] = smem[4 * groups + from];
+    }
 }
 
 // The CTAs' sums, one column of one result per lane of a warp row.

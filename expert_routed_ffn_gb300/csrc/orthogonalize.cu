@@ -3,7 +3,7 @@
 // each step's (a, b, c)
 //   A = X X^T,   B = a + b A + c A^2,   X <- B X          (N <= K; else A = X^T X, X <- X B)
 //
-// Three products a step, m^2 n + m^3 + 2 m^2 n FLOP (A and B are symmetric: tiles below their
+// Three products a step, m^2 n + m^3 + 2 m^2 n FLOP (A and B are symmetric: tiles above their
 // diagonal are not computed but mirrored), all batched over the matrices.  Bound by the tensor
 // cores.  No operand is transposed in memory: whichever side is smaller, a tile is read with its
 // reduction index innermost or outermost, as in grouped.cu, whose tiles, pipeline of CTA pairs,
@@ -13,17 +13,18 @@
 // usual coefficients; the host bounds the singular values step by step and picks power-of-two
 // scales that keep them inside fp16), so fp16's 11 bits cost nothing over bf16's 8 and are eight
 // times as accurate.  What rounding X still does: noise of 2^-12 of its largest directions enters
-// the small ones, which the polynomial multiplies by up to a = 3.4 a step.  Of the small directions'
-// change, B's part b A + c A^2 is nearly nothing and a X nearly all, so the steps that matter (all but the last
-// two) keep the rounding of X, hi + lo, and take it through a X alone: X <- (b A + c A^2) hi + a (hi + lo),
-// an epilogue's work; the tensor cores see hi only.  Where 16 directions are 300 times as large as
-// the rest, the result's error (2-norm, relative) falls from 2.0e-2 to 1.3e-3, below a
+// the small ones, which the polynomial multiplies by up to a = 3.4 a step.  Of a small direction's
+// change nearly all is a X, and b A + c A^2 nearly nothing; so the steps that matter (all but the last two)
+// keep the rounding of X, hi + lo, and take lo through a X alone: X <- B hi + a lo, an
+// epilogue's work; the tensor cores see hi only.  Where 16 directions are 300 times as large as
+// the rest, the result's error (2-norm, relative) falls from 2.0e-2 to 1.5e-3, below a
 // bf16 result's own rounding of 1.7e-3; bf16 throughout gives 0.16.
-// X0 is G times a power of two (exact for bf16 G), the rest of 1 / (|G| + eps) is a factor
+// X0 is G times a power of two (exact for bf16 G: no lo), the rest of 1 / (|G| + eps) is a factor
 // s in (1/2, 1] of the first A and B.  Sums are fp32 in tensor memory, over at most 16384
 // products: the tensor core's truncation stays below 1e-4 (2^-13) of a sum of one sign.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -65,29 +66,31 @@ struct ProductArgs {
     int a_block, b_block, stages;
     long long wait;
     int *err;
-    // epilogue, see finish_symmetric and finish_x
-    const float2 *table;  // first step: s and the power of two, per matrix
-    const half *other;    // B: A; X: hi
-    const half *lo;
-    const void *g;        // first step of X: G itself
-    half *out, *out_lo;
-    bf16 *final;
-    int g_f32;
+    int col_shift;        // log2(cols)
+    // epilogue, see Symmetric and Update
+    const float *table;   // first step: s of each matrix, else NULL
+    const half *other;    // B: A; X: lo, or NULL
+    half *out, *out_lo;   // out_lo: X, or NULL
+    bf16 *final;          // X: the result, in place of out
     float k_acc, k_other, k_diag;
 };
 
 struct Place {
-    int e, row0, rows, col0;
+    int e, row0, rows, n, col0;  // matrix, first row, rows, the MMA's N, first column
 };
 
 // Walks tiles first, first + step, .. of all matrices, the column tile innermost.  SYM: of a row
-// tile only the column tiles that reach its first row or beyond.
+// tile only the column tiles that begin at its last row or before.  (The lower triangle: the last
+// row tile may be short, and then takes fewer of the MMA's N, where a short column tile takes
+// all of its M, so few tiles should be of the last columns.)
 template <bool SYM>
 struct Walk {
     const ProductArgs &p;
     int tile, step, e = 0, r = 0, c;
     __device__ __forceinline__ Walk(const ProductArgs &args, int first, int by) : p(args), tile(first), step(by), c(first) { settle(); }
-    __device__ __forceinline__ int skipped() const { return SYM ? r * p.tile_rows / p.cols : 0; }
+    __device__ __forceinline__ int reach() const {
+        return SYM ? ((min(p.R, (r + 1) * p.tile_rows) - 1) >> p.col_shift) + 1 : p.col_tiles;
+    }
     __device__ __forceinline__ void settle() {
         if (!SYM) {
             const int per = p.row_tiles * p.col_tiles;
@@ -97,8 +100,8 @@ struct Walk {
                 c -= n * per;
             }
         }
-        while (c >= p.col_tiles - skipped()) {
-            c -= p.col_tiles - skipped();
+        for (int here = reach(); c >= here; here = reach()) {
+            c -= here;
             if (++r == p.row_tiles) {
                 r = 0;
                 ++e;
@@ -112,8 +115,8 @@ struct Walk {
         if (more()) settle();
     }
     __device__ __forceinline__ Place get() const {
-        const int row0 = r * p.tile_rows;
-        return {e, row0, min(p.tile_rows, p.R - row0), (c + skipped()) * p.cols};
+        const int row0 = r * p.tile_rows, rows = min(p.tile_rows, p.R - row0);
+        return {e, row0, rows, (rows + 31) & ~31, c * p.cols};
     }
 };
 
@@ -123,32 +126,42 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 }
 __device__ __forceinline__ float2 unpack_half2(uint32_t v) { return __half22float2(*reinterpret_cast<const half2 *>(&v)); }
 
-// A tile of a symmetric result (A, or B from A) by one warp: the lane is column `col`, TMEM columns
-// are rows.  v = f (k_acc sum + k_other other + k_diag on the diagonal), f: s^2 for A, s for B.
-// Element (r, c) with c >= r is stored there and at (c, r); in a tile across the diagonal the
-// others are left to their mirror images, so the result is symmetric bit by bit.  `other` is read
-// in its mirror image too: a lane's 32 rows are 64 contiguous bytes there.
-__device__ __forceinline__ void finish_symmetric(const ProductArgs &p, const Place &t, uint32_t tcol, int col, int part, int lane) {
-    const size_t ld = p.C, base = (size_t)t.e * p.R * ld;
-    const bool ok = col < p.C;
-    float f = 1.0f;
-    if (p.table != nullptr) {
-        const float s = p.table[t.e].x;
-        f = p.other != nullptr ? s : s * s;
+// The epilogues, by one warp for its chunks of 32 columns (lanes) x 32 rows (TMEM columns).  What
+// a chunk reads from memory is asked for a chunk ahead (fetch), the first before the sums are there: with
+// the loads after it each chunk waited for them, and the products for the epilogue (five steps of
+// 32 x 1408 x 2048: 2459 us).
+
+// A symmetric result (A, or B from A): v = f (k_acc sum + k_other other + k_diag on the diagonal),
+// f: s^2 for A, s for B.  Element (r, c) with c <= r is stored there and at (c, r); in a chunk
+// across the diagonal the others are left to their mirror images, so the result is symmetric bit by
+// bit.  `other` is read in its mirror image too: a lane's 32 rows are 64 contiguous bytes there.
+struct Symmetric {
+    const ProductArgs &p;
+    int lane;
+    uint4 ahead[4];
+    __device__ __forceinline__ void fetch(const Place &t, int col, int c) {
+        const int rows = col < p.C && p.other != nullptr ? t.rows - c : 0;
+        const uint4 *o = reinterpret_cast<const uint4 *>(p.other + ((size_t)t.e * p.R + col) * p.C + t.row0 + c);
+        const bool above = col - lane > t.row0 + c + 31;  // not computed
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ahead[i] = 8 * i < rows && !above ? o[i] : make_uint4(0, 0, 0, 0);
     }
-    const int col_first = col - lane;
-    for (int c = 32 * part; c < t.rows; c += 32 * kParts) {
-        const int r0 = t.row0 + c, rows = min(32, t.rows - c);  // a multiple of 8, as all sizes are
-        if (col_first + 31 < r0) continue;                      // the chunk is below the diagonal
+    __device__ __forceinline__ void finish(const Place &t, uint32_t tcol, int col, int c, int next) {
+        const size_t ld = p.C, base = (size_t)t.e * p.R * ld;
+        const bool ok = col < p.C;
+        const int col_first = col - lane, r0 = t.row0 + c, rows = min(32, t.rows - c);  // a multiple of 8, as all sizes are
+        uint4 a[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = ahead[i];
+        if (next < t.rows) fetch(t, col, next);
+        if (col_first > r0 + 31) return;  // above the diagonal
+        float f = 1.0f;
+        if (p.table != nullptr) {
+            const float s = p.table[t.e];
+            f = p.other != nullptr ? s : s * s;
+        }
         uint32_t v[32];
         tmem_ld32(tcol + c, v);
-        uint4 a[4];
-        const size_t mirror = base + (size_t)col * ld + r0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = make_uint4(0, 0, 0, 0);
-            if (p.other != nullptr && ok && 8 * i < rows) a[i] = reinterpret_cast<const uint4 *>(p.other + mirror)[i];
-        }
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));  // not read before the wait
@@ -162,12 +175,13 @@ __device__ __forceinline__ void finish_symmetric(const ProductArgs &p, const Pla
             if (r0 + 2 * i + 1 == col) y += p.k_diag;
             h[i] = pack_half2(f * x, f * y);
         }
-        if (col_first >= r0 + 32) {  // above the diagonal
+        half *across = p.out + base + (size_t)col * ld + r0;
+        if (col_first + 31 < r0) {  // below the diagonal
             if (ok) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (8 * i < rows)
-                        reinterpret_cast<uint4 *>(p.out + mirror)[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+                        reinterpret_cast<uint4 *>(across)[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
             }
             // both columns of a lane pair in one word, rows 2i (even lane) and 2i + 1
             const int odd = lane & 1;
@@ -178,63 +192,41 @@ __device__ __forceinline__ void finish_symmetric(const ProductArgs &p, const Pla
                 if (ok && 2 * i < rows) o[i * ld] = __byte_perm(h[i], got, odd ? 0x3276 : 0x5410);
             }
         } else if (ok) {
-            half *down = p.out + base + (size_t)r0 * ld + col, *across = p.out + mirror;
+            half *down = p.out + base + (size_t)r0 * ld + col;
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-                if (j >= rows || col < r0 + j) continue;
+                if (j >= rows || col > r0 + j) continue;
                 const half x = __ushort_as_half((unsigned short)(j & 1 ? h[j / 2] >> 16 : h[j / 2] & 0xffffu));
                 down[j * ld] = x;
                 across[j] = x;
             }
         }
     }
-}
+};
 
-// A tile of X by one warp: v = k_acc sum + k_other (hi + lo), or in the first step + k_other s 2^-k G;
-// stored as hi (and lo, in place of the old one), or as bf16 at the end.
-__device__ __forceinline__ void finish_x(const ProductArgs &p, const Place &t, uint32_t tcol, int col, int part, int lane) {
-    const int odd = lane & 1;
-    const bool ok = col < p.C;
-    const size_t ld = p.C;
-    float scale = p.k_other, shrink = 1.0f;
-    if (p.g != nullptr) {
-        scale *= p.table[t.e].x;
-        shrink = p.table[t.e].y;
+// X: v = k_acc sum + f k_other lo, f: s in the first step; stored as hi (and lo, in place of the old one), or as bf16 at the
+// end.  Lane pairs exchange values so that each lane has both columns of every other row, one word.
+struct Update {
+    const ProductArgs &p;
+    int lane;
+    uint32_t ahead[16];
+    __device__ __forceinline__ size_t at(const Place &t, int col, int c) const {
+        return ((size_t)t.e * p.R + t.row0 + c + (lane & 1)) * p.C + (col & ~1);
     }
-    for (int c = 32 * part; c < t.rows; c += 32 * kParts) {
-        const int left = ok ? t.rows - c - odd : 0;
-        const size_t at = ((size_t)t.e * p.R + t.row0 + c + odd) * ld + (col & ~1);
-        float2 old[16];
-        if (p.g != nullptr) {
+    __device__ __forceinline__ void fetch(const Place &t, int col, int c) {
+        const int left = col < p.C && p.other != nullptr ? t.rows - c - (lane & 1) : 0;
+        const uint32_t *o = reinterpret_cast<const uint32_t *>(p.other + at(t, col, c));
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                old[i] = make_float2(0.0f, 0.0f);
-                if (2 * i >= left) continue;
-                if (p.g_f32) {
-                    old[i] = *reinterpret_cast<const float2 *>(static_cast<const float *>(p.g) + at + 2 * i * ld);
-                } else {
-                    const uint32_t w = *reinterpret_cast<const uint32_t *>(static_cast<const bf16 *>(p.g) + at + 2 * i * ld);
-                    old[i] = make_float2(bf16_lo(w), bf16_hi(w));
-                }
-            }
+        for (int i = 0; i < 16; ++i) ahead[i] = 2 * i < left ? o[(size_t)i * p.C] : 0u;
+    }
+    __device__ __forceinline__ void finish(const Place &t, uint32_t tcol, int col, int c, int next) {
+        const int odd = lane & 1, left = col < p.C ? t.rows - c - odd : 0;
+        const size_t ld = p.C, from = at(t, col, c);
+        const float scale = p.table != nullptr ? p.k_other * p.table[t.e] : p.k_other;
+        uint32_t lo[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) old[i] = make_float2(old[i].x * shrink, old[i].y * shrink);
-        } else if (p.lo != nullptr) {
-            uint32_t hi[16], lo[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                hi[i] = 2 * i < left ? *reinterpret_cast<const uint32_t *>(p.other + at + 2 * i * ld) : 0u;
-                lo[i] = 2 * i < left ? *reinterpret_cast<const uint32_t *>(p.lo + at + 2 * i * ld) : 0u;
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float2 x = unpack_half2(hi[i]), y = unpack_half2(lo[i]);
-                old[i] = make_float2(x.x + y.x, x.y + y.y);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) old[i] = make_float2(0.0f, 0.0f);
-        }
+        for (int i = 0; i < 16; ++i) lo[i] = ahead[i];
+        if (next < t.rows) fetch(t, col, next);
         uint32_t v[32];
         tmem_ld32(tcol + c, v);
         tmem_ld_wait();
@@ -244,22 +236,23 @@ __device__ __forceinline__ void finish_x(const ProductArgs &p, const Place &t, u
         for (int i = 0; i < 16; ++i) {
             const uint32_t mine = odd ? v[2 * i + 1] : v[2 * i], give = odd ? v[2 * i] : v[2 * i + 1];
             const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
-            const float x = fmaf(scale, old[i].x, p.k_acc * __uint_as_float(odd ? got : mine));
-            const float y = fmaf(scale, old[i].y, p.k_acc * __uint_as_float(odd ? mine : got));
+            const float2 old = unpack_half2(lo[i]);
+            const float x = fmaf(scale, old.x, p.k_acc * __uint_as_float(odd ? got : mine));
+            const float y = fmaf(scale, old.y, p.k_acc * __uint_as_float(odd ? mine : got));
             if (2 * i >= left) continue;
             if (p.final != nullptr) {
-                *reinterpret_cast<uint32_t *>(p.final + at + 2 * i * ld) = pack_bf16x2(x, y);
+                *reinterpret_cast<uint32_t *>(p.final + from + 2 * i * ld) = pack_bf16x2(x, y);
             } else {
                 const uint32_t h = pack_half2(x, y);
-                *reinterpret_cast<uint32_t *>(p.out + at + 2 * i * ld) = h;
+                *reinterpret_cast<uint32_t *>(p.out + from + 2 * i * ld) = h;
                 if (p.out_lo != nullptr) {
                     const float2 b = unpack_half2(h);
-                    *reinterpret_cast<uint32_t *>(p.out_lo + at + 2 * i * ld) = pack_half2(x - b.x, y - b.y);
+                    *reinterpret_cast<uint32_t *>(p.out_lo + from + 2 * i * ld) = pack_half2(x - b.x, y - b.y);
                 }
             }
         }
     }
-}
+};
 
 __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {  // as grouped_kernel.cuh
     uint64_t d = 0;
@@ -324,17 +317,18 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     pdl_wait();  // the operands, by earlier kernels on the stream
     pdl_trigger();
     const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
-    const int half_cols = p.cols / 2, n = p.tile_rows;
+    const int half_cols = p.cols / 2;
 
     if (warp == 0) {
-        const bool two_b = n / 2 > 64;
-        const uint32_t bytes = a_block + (B_MN ? (two_b ? 2 : 1) * kChunk : (n / 2) * kRow);
+        // a short tile is loaded as a whole one: what comes beyond its rows is not multiplied
+        const bool two_b = p.tile_rows / 2 > 64;
+        const uint32_t bytes = a_block + (B_MN ? (two_b ? 2 : 1) * kChunk : (p.tile_rows / 2) * kRow);
         uint32_t ph = 1;
         int s = 0;
         bool ok = true;
         for (Walk<SYM> walk(p, first, stride); ok && walk.more(); walk.next()) {
             const Place t = walk.get();
-            const int col = t.col0 + rank * half_cols, row = t.row0 + rank * (n / 2);
+            const int col = t.col0 + rank * half_cols, row = t.row0 + rank * (t.n / 2);
             for (int r = 0; r < p.red; r += kBK) {
                 if (!__all_sync(0xffffffffu, wait_bar(empty_bar(s), ph, p.wait, abort_flag))) {
                     ok = false;
@@ -371,11 +365,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const uint64_t desc_a = A_MN ? smem_desc_mn(sA) : smem_desc_k128(sA);
             const uint64_t desc_b = B_MN ? smem_desc_mn(sB) : smem_desc_k128(sB);
             // fp16 operands (their format fields are 0), fp32 sums
-            const uint32_t idesc = (1u << 4) | (uint32_t)(n >> 3) << 17 | (256u >> 4) << 24 | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+            constexpr uint32_t kDesc = (1u << 4) | (256u >> 4) << 24 | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
             uint32_t ph = 0, acc = 0, free_ph = 1;
             int s = 0;
             bool ok = p.wait != 0, issued = false;  // a bound of 0: give up at once
-            for (int tile = first; ok && tile < p.tiles; tile += stride) {
+            for (Walk<SYM> walk(p, first, stride); ok && walk.more(); walk.next()) {
+                const uint32_t idesc = kDesc | (uint32_t)(walk.get().n >> 3) << 17;
                 const uint32_t d = tmem_base + acc * kAccCols;
                 if (!__all_sync(0xffffffffu, wait_bar<true>(tempty_bar(acc), free_ph, p.wait, abort_flag))) {
                     ok = false;
@@ -419,21 +414,19 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const int part = (warp - 2) >> 2;
         const bool mine = 32 * q < half_cols;
         uint32_t acc = 0, ph = 0;
+        typename std::conditional<SYM, Symmetric, Update>::type epilogue{p, lane};
         for (Walk<SYM> walk(p, first, stride); walk.more(); walk.next()) {
             const Place t = walk.get();
             const uint32_t tcol = tmem_base + ((uint32_t)(q * 32) << 16) + acc * kAccCols;
             const int col = t.col0 + rank * half_cols + 32 * q + lane;
+            if (mine && 32 * part < t.rows) epilogue.fetch(t, col, 32 * part);
             if (!__all_sync(0xffffffffu, wait_bar<true>(tfull_bar(acc), ph, p.wait, abort_flag))) {
                 if (lane == 0) raise();
                 break;
             }
             tc_fence_after();
-            if (mine) {
-                if (SYM)
-                    finish_symmetric(p, t, tcol, col, part, lane);
-                else
-                    finish_x(p, t, tcol, col, part, lane);
-            }
+            if (mine)
+                for (int c = 32 * part; c < t.rows; c += 32 * kParts) epilogue.finish(t, tcol, col, c, c + 32 * kParts);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_bar(acc), 0));
@@ -517,14 +510,15 @@ __global__ void __launch_bounds__(kNormThreads) square_kernel(const T *g, long l
     if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
-// table[e] = (s, 2^-k) with 2^k <= |G| + eps < 2^(k + 1), s = 2^k / (|G| + eps); X0 = up 2^-k G.
-// Each CTA adds up its matrix's sums.
+// table[e] = s = 2^k / (|G| + eps) with 2^k <= |G| + eps < 2^(k + 1); X0 = up 2^-k G, as hi and, where lo
+// is not NULL, lo.  Each CTA adds up its matrix's sums.  The matrices come in reverse order, so
+// that what was read last is still in L2.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) scale_kernel(const T *g, long long size, int parts, const double *partial,
-                                                             float eps, float up, float2 *table, half *x) {
+                                                             float eps, float up, float *table, half *x, half *lo) {
     __shared__ double shared[kNormThreads / 32];
     __shared__ float shrink_of;
-    const int e = blockIdx.x / parts, part = blockIdx.x - e * parts;
+    const int block = gridDim.x - 1 - blockIdx.x, e = block / parts, part = block - e * parts;
     pdl_wait();
     pdl_trigger();
     double v = 0.0;
@@ -539,7 +533,7 @@ __global__ void __launch_bounds__(kNormThreads) scale_kernel(const T *g, long lo
             shrink = (float)ldexp(1.0, 1 - k);
         }
         shrink_of = shrink;
-        if (part == 0) table[e] = make_float2(s, shrink);
+        if (part == 0) table[e] = s;
     }
     __syncthreads();
     const float shrink = shrink_of;
@@ -554,8 +548,16 @@ __global__ void __launch_bounds__(kNormThreads) scale_kernel(const T *g, long lo
             load8(at + k, o);
 #pragma unroll
             for (int x8 = 0; x8 < 8; ++x8) o[x8] = o[x8] * shrink * up;
-            *reinterpret_cast<uint4 *>(to + k) =
-                make_uint4(pack_half2(o[0], o[1]), pack_half2(o[2], o[3]), pack_half2(o[4], o[5]), pack_half2(o[6], o[7]));
+            const uint4 hi = make_uint4(pack_half2(o[0], o[1]), pack_half2(o[2], o[3]), pack_half2(o[4], o[5]), pack_half2(o[6], o[7]));
+            *reinterpret_cast<uint4 *>(to + k) = hi;
+            if (lo == nullptr) continue;
+            uint32_t l[4];
+#pragma unroll
+            for (int i4 = 0; i4 < 4; ++i4) {
+                const float2 h = unpack_half2((&hi.x)[i4]);
+                l[i4] = pack_half2(o[2 * i4] - h.x, o[2 * i4 + 1] - h.y);
+            }
+            *reinterpret_cast<uint4 *>(lo + (size_t)e * size + k) = make_uint4(l[0], l[1], l[2], l[3]);
         }
     }
 }
@@ -577,7 +579,7 @@ Workspace lay_out(int E, int N, int K) {
     auto room = [](size_t bytes) { return (bytes + 1023) / 1024 * 1024; };
     Workspace w;
     w.table = 0;
-    w.partial = w.table + room(e * sizeof(float2));
+    w.partial = w.table + room(e * sizeof(float));
     w.x[0] = w.partial + room(e * kMaxParts * sizeof(double));
     w.x[1] = w.x[0] + room(2 * e * n);
     w.lo = w.x[1] + room(2 * e * n);
@@ -599,7 +601,7 @@ double largest(double limit, double (*of)(double, const float *), const float *c
 float power_below(double bound, int most) {
     return (float)std::ldexp(1.0, std::min(most, std::ilogb(60000.0 / std::max(bound, 1e-6))));
 }
-// Steps whose X keeps its rounding, and does not put a into B.
+// Steps whose X keeps its rounding.
 bool keeps_lo(int step, int steps) { return step < steps - 2; }
 
 // false: the polynomials let a singular value grow beyond what fp16 holds
@@ -608,10 +610,9 @@ bool choose_scales(const float *coef, int steps, Scales *scales, float *up) {
     for (int i = 0; i < steps; ++i) {
         const float *c = coef + 3 * i;
         auto whole = [](double l, const float *k) { return k[0] + l * (k[1] + l * k[2]); };
-        auto rest = [](double l, const float *k) { return l * (k[1] + l * k[2]); };
         auto step = [](double v, const float *k) { return v * (k[0] + v * v * (k[1] + v * v * k[2])); };
         scales[i].a = power_below(1.01 * x * x, 14);
-        scales[i].b = power_below(keeps_lo(i, steps) ? largest(x * x, rest, c) : largest(x * x, whole, c), 14);
+        scales[i].b = power_below(largest(x * x, whole, c), 14);
         x = largest(x, step, c);
         if (!(x < 1024.0)) return false;
         if (i + 1 < steps) most = std::max(most, x);
@@ -625,11 +626,12 @@ bool choose_scales(const float *coef, int steps, Scales *scales, float *up) {
 long long count_tiles(const ProductArgs &g, bool sym) {
     if (!sym) return (long long)g.E * g.row_tiles * g.col_tiles;
     long long n = 0;
-    for (int r = 0; r < g.row_tiles; ++r) n += g.col_tiles - r * g.tile_rows / g.cols;
+    for (int r = 0; r < g.row_tiles; ++r) n += (std::min(g.R, (r + 1) * g.tile_rows) - 1) / g.cols + 1;
     return n * g.E;
 }
 long long choose_tiles(ProductArgs &g, bool b_mn, bool sym, int sms) {
     g.cols = g.C > 128 ? 256 : 128;
+    g.col_shift = g.cols == 256 ? 8 : 7;
     g.col_tiles = (g.C + g.cols - 1) / g.cols;
     long long tiles = 0;
     for (int rows = 256; rows >= 32; rows /= 2) {
@@ -734,7 +736,7 @@ extern "C" moe_status moe_orthogonalize(const void *G, int dtype, int E, int N, 
     if (sms < 2 || err == nullptr) return op_fail(MOE_ERR_CUDA, "%s: no usable current device", name);
 
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    float2 *table = reinterpret_cast<float2 *>(ws + w.table);
+    float *table = reinterpret_cast<float *>(ws + w.table);
     double *partial = reinterpret_cast<double *>(ws + w.partial);
     half *x[2] = {reinterpret_cast<half *>(ws + w.x[0]), reinterpret_cast<half *>(ws + w.x[1])};
     half *lo = reinterpret_cast<half *>(ws + w.lo), *A = reinterpret_cast<half *>(ws + w.a), *B = reinterpret_cast<half *>(ws + w.b);
@@ -742,17 +744,19 @@ extern "C" moe_status moe_orthogonalize(const void *G, int dtype, int E, int N, 
     const long long size = (long long)N * K;
     const int parts = parts_of(size);
     const dim3 grid((unsigned)(E * parts));
+    // X0 of bf16 values is exact
+    half *lo0 = dtype == MOE_DTYPE_F32 && keeps_lo(0, steps) ? lo : nullptr;
     cudaError_t ce;
     if (dtype == MOE_DTYPE_F32) {
         const float *g = static_cast<const float *>(G);
         ce = launch_pdl(square_kernel<float>, grid, dim3(kNormThreads), 0, s, g, size, parts, partial);
         if (ce == cudaSuccess)
-            ce = launch_pdl(scale_kernel<float>, grid, dim3(kNormThreads), 0, s, g, size, parts, static_cast<const double *>(partial), eps, up, table, x[0]);
+            ce = launch_pdl(scale_kernel<float>, grid, dim3(kNormThreads), 0, s, g, size, parts, static_cast<const double *>(partial), eps, up, table, x[0], lo0);
     } else {
         const bf16 *g = static_cast<const bf16 *>(G);
         ce = launch_pdl(square_kernel<bf16>, grid, dim3(kNormThreads), 0, s, g, size, parts, partial);
         if (ce == cudaSuccess)
-            ce = launch_pdl(scale_kernel<bf16>, grid, dim3(kNormThreads), 0, s, g, size, parts, static_cast<const double *>(partial), eps, up, table, x[0]);
+            ce = launch_pdl(scale_kernel<bf16>, grid, dim3(kNormThreads), 0, s, g, size, parts, static_cast<const double *>(partial), eps, up, table, x[0], lo0);
     }
     if (ce != cudaSuccess) return op_cuda(ce, name);
 
@@ -760,7 +764,6 @@ extern "C" moe_status moe_orthogonalize(const void *G, int dtype, int E, int N, 
     const int m = std::min(N, K);
     for (int i = 0; i < steps; ++i) {
         const float *c = coefficients + 3 * i, sa = scales[i].a, sb = scales[i].b;
-        const bool keep = keeps_lo(i, steps);
         const Operand X{x[i & 1], N, K}, sym_a{A, m, m}, sym_b{B, m, m};
         ProductArgs g = {};  // A
         g.E = E, g.R = g.C = m, g.red = wide ? K : N, g.err = err;
@@ -777,7 +780,7 @@ extern "C" moe_status moe_orthogonalize(const void *G, int dtype, int E, int N, 
         g.out = B;
         g.k_acc = c[2] / sa / sa * sb;
         g.k_other = c[1] / sa * sb;
-        g.k_diag = keep ? 0.0f : c[0] * sb;
+        g.k_diag = c[0] * sb;
         st = product<false, false, true>(name, g, sym_a, sym_a, 0, sms, s);
         if (st != MOE_OK) return st;
 
@@ -786,18 +789,9 @@ extern "C" moe_status moe_orthogonalize(const void *G, int dtype, int E, int N, 
         const bool last = i + 1 == steps;
         const float unit = last ? scale / up : 1.0f;  // of what is stored
         g.k_acc = unit / sb;
-        if (keep) {
-            g.k_other = c[0] * unit;
-            if (i == 0) {
-                g.k_other *= up;
-                g.table = table;
-                g.g = G;
-                g.g_f32 = dtype == MOE_DTYPE_F32;
-            } else {
-                g.other = x[i & 1];
-                g.lo = lo;
-            }
-        }
+        g.other = i == 0 ? lo0 : keeps_lo(i, steps) ? lo : nullptr;
+        g.k_other = c[0];  // (the last step has no lo)
+        g.table = i == 0 ? table : nullptr;
         g.out = x[(i + 1) & 1];
         g.out_lo = !last && keeps_lo(i + 1, steps) ? lo : nullptr;
         g.final = last ? static_cast<bf16 *>(out) : nullptr;
