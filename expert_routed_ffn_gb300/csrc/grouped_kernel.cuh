@@ -25,10 +25,13 @@ constexpr int kBK = 64;                // reduction steps per stage: 128 bytes o
 constexpr int kMaxStages = 12;
 // Epilogue warps per TMEM lane quadrant.  One against two: a small product 11.7 / 11.0 us, a
 // small bf16 weight gradient 26.6 / 24.6 us, prefill the same.
-constexpr int kParts = 2;
-constexpr int kEpiWarps = kQuads * kParts;
+// Twice as many where the epilogue computes the activation or its gradients (gated.cuh).
 template <int OP>
-constexpr int kThreads = 64 + 32 * kEpiWarps + (OP == kWgrad ? 32 : 0);  // the wgrad's last warp zeroes tails
+constexpr int kParts = OP == kGated || OP == kGatedBack ? 4 : 2;
+template <int OP>
+constexpr int kEpiWarps = kQuads * kParts<OP>;
+template <int OP>
+constexpr int kThreads = 64 + 32 * kEpiWarps<OP> + (OP == kWgrad ? 32 : 0);  // the wgrad's last warp zeroes tails
 static_assert(kThreads<kForward> >= kMaxExperts, "load_table: a thread per expert");
 constexpr int kAccCols = 256;          // TMEM columns of one accumulator
 constexpr uint32_t kTmemCols = 2 * kAccCols;
@@ -135,7 +138,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
         }
         for (uint32_t a = 0; a < 2; ++a) {
             mbar_init(tfull_bar(a), 1);
-            mbar_init(tempty_bar(a), 2 * kEpiWarps);  // both CTAs'
+            mbar_init(tempty_bar(a), 2 * kEpiWarps<OP>);  // both CTAs'
         }
         mbar_init(drain_bar, 1);
         fence_mbar_init();
@@ -317,7 +320,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
                 }
             }
         }
-    } else if (kDense && warp == 2 + kEpiWarps) {
+    } else if (kDense && warp == 2 + kEpiWarps<OP>) {
         // wgrad: zero the rows past each tail's end, then hand the stage to the MMA
         uint32_t tail_ph = 0;
         int s = 0;
@@ -369,7 +372,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
             const uint32_t a = accs.next, tmem_q = tmem_base + ((uint32_t)(q * 32) << 16);
             const int col = t.col0 + rank * half_cols + in_half;
             if constexpr (OP == kGatedBack) {
-                if (t.last && mine && 32 * part < t.rows) back.fetch(h.gated, t, col, 32 * part, lane);
+                if (t.last && mine && kGatedRows * part < t.rows) back.fetch(h.gated, t, col, kGatedRows * part, lane);
             }
             if (!empty) {
                 if (!__all_sync(0xffffffffu, wait_bar<true>(tfull_bar(a), accs.ready(), p.o.wait + walk.slack, abort_flag))) {
@@ -381,17 +384,21 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
             uint32_t from = a;
             if (SEGMENTS && !(t.first && t.last)) {
                 from = a ^ 1u;
-                if (mine) add_segment<kDense, kParts>(tab.o, t, tmem_q + a * kAccCols, tmem_q + from * kAccCols, part);
+                if constexpr (OP == kGated || OP == kGatedBack) {
+                    if (mine) add_gated_segment<kParts<OP>>(t, tmem_q + a * kAccCols, tmem_q + from * kAccCols, part);
+                } else {
+                    if (mine) add_segment<kDense, kParts<OP>>(tab.o, t, tmem_q + a * kAccCols, tmem_q + from * kAccCols, part);
+                }
                 release(a);
             }
             if (!SEGMENTS || t.last) {
                 if constexpr (OP == kGated) {
                     const int out_col = (t.col0 + rank * half_cols + 32 * q) / 2 + (lane & (kGranule - 1));
-                    if (mine) store_gated<kParts>(tab.o, h.gated, t, tmem_q + from * kAccCols, out_col, part, lane);
+                    if (mine) store_gated<kParts<OP>>(h.gated, tab.o.out, t, tmem_q + from * kAccCols, out_col, part, lane);
                 } else if constexpr (OP == kGatedBack) {
-                    if (mine) back.template store<kParts>(h.gated, t, tmem_q + from * kAccCols, col, part, lane);
+                    if (mine) back.template store<kParts<OP>>(h.gated, t, tmem_q + from * kAccCols, col, part, lane);
                 } else {
-                    if (mine) store_tile<kDense, ADD, kParts>(tab.o, t, tmem_q + from * kAccCols, empty, col, part, lane);
+                    if (mine) store_tile<kDense, ADD, kParts<OP>>(tab.o, t, tmem_q + from * kAccCols, empty, col, part, lane);
                 }
                 if (!empty) release(from);
             }

@@ -40,7 +40,7 @@ namespace {
 constexpr int kMaxSide = 16384;
 constexpr int kBK = 64;                // reduction steps per stage: 128 bytes
 constexpr int kMaxStages = 12;
-constexpr int kParts = 2;              // epilogue warps per TMEM lane quadrant
+constexpr int kParts = 4;              // epilogue warps per TMEM lane quadrant
 constexpr int kEpiWarps = kQuads * kParts;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kAccCols = 256;
