@@ -67,6 +67,7 @@ struct ProductArgs {
     long long wait;
     int *err;
     int col_shift;        // log2(cols)
+    int ld;               // symmetric results: elements between rows, a multiple of 16
     // epilogue, see Symmetric and Update
     const float *table;   // first step: s of each matrix, else NULL
     const half *other;    // B: A; X: lo, or NULL
@@ -82,30 +83,38 @@ struct Place {
 // Walks tiles first, first + step, .. of all matrices, the column tile innermost.  SYM: of a row
 // tile only the column tiles that begin at its last row or before.  (The lower triangle: the last
 // row tile may be short, and then takes fewer of the MMA's N, where a short column tile takes
-// all of its M, so few tiles should be of the last columns.)
+// all of its M, so few tiles should be of the last columns.)  Where the last row tiles are short
+// they come after all the others, so that each CTA pair gets as many of them as any other.
 template <bool SYM>
 struct Walk {
     const ProductArgs &p;
     int tile, step, e = 0, r = 0, c;
-    __device__ __forceinline__ Walk(const ProductArgs &args, int first, int by) : p(args), tile(first), step(by), c(first) { settle(); }
+    int begin = 0, end;  // row tiles walked of each matrix
+    __device__ __forceinline__ Walk(const ProductArgs &args, int first, int by) : p(args), tile(first), step(by), c(first) {
+        end = p.row_tiles > 1 && p.row_tiles * p.tile_rows > p.R ? p.row_tiles - 1 : p.row_tiles;
+        settle();
+    }
     __device__ __forceinline__ int reach() const {
         return SYM ? ((min(p.R, (r + 1) * p.tile_rows) - 1) >> p.col_shift) + 1 : p.col_tiles;
     }
     __device__ __forceinline__ void settle() {
-        if (!SYM) {
-            const int per = p.row_tiles * p.col_tiles;
-            if (c >= per) {  // a matrix or more on
-                const int n = c / per;
+        for (;;) {
+            if (end - begin == 1 || !SYM) {  // as many tiles in each matrix: whole ones are skipped at once
+                const int per = (end - begin) * reach(), left = p.E - 1 - e;
+                const int n = min(c / per, left);
                 e += n;
                 c -= n * per;
             }
-        }
-        for (int here = reach(); c >= here; here = reach()) {
-            c -= here;
-            if (++r == p.row_tiles) {
-                r = 0;
-                ++e;
+            for (int here = reach(); c >= here; here = reach()) {
+                c -= here;
+                if (++r < end) continue;
+                r = begin;
+                if (++e == p.E) break;
             }
+            if (e < p.E) return;
+            e = 0;  // the last row tiles
+            r = begin = end;
+            end = p.row_tiles;
         }
     }
     __device__ __forceinline__ bool more() const { return tile < p.tiles; }
@@ -120,6 +129,24 @@ struct Walk {
     }
 };
 
+// 16 fp16 values at a 32-byte boundary
+struct Half16 {
+    uint32_t w[8];
+};
+__device__ __forceinline__ Half16 load_half16(const half *p) {
+    Half16 v;
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]), "=r"(v.w[7])
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void store_half16(half *p, const uint32_t *w) {
+    asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+                 "r"(w[5]), "r"(w[6]), "r"(w[7]), "l"(p)
+                 : "memory");
+}
+
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     const half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
@@ -132,29 +159,35 @@ __device__ __forceinline__ float2 unpack_half2(uint32_t v) { return __half22floa
 // 32 x 1408 x 2048: 2459 us).
 
 // A symmetric result (A, or B from A): v = f (k_acc sum + k_other other + k_diag on the diagonal),
-// f: s^2 for A, s for B.  Element (r, c) with c <= r is stored there and at (c, r); in a chunk
-// across the diagonal the others are left to their mirror images, so the result is symmetric bit by
-// bit.  `other` is read in its mirror image too: a lane's 32 rows are 64 contiguous bytes there.
+// f: s^2 for A, s for B.  Element (r, c) with c <= r is stored there and at (c, r), 32 bytes of a lane's
+// column at a time; `other` is read in its mirror image too.  A chunk on the diagonal holds its own
+// mirror image (the same products summed in the same order) and is stored once.
 struct Symmetric {
     const ProductArgs &p;
     int lane;
-    uint4 ahead[4];
+    Half16 ahead[2];
     __device__ __forceinline__ void fetch(const Place &t, int col, int c) {
-        const int rows = col < p.C && p.other != nullptr ? t.rows - c : 0;
-        const uint4 *o = reinterpret_cast<const uint4 *>(p.other + ((size_t)t.e * p.R + col) * p.C + t.row0 + c);
-        const bool above = col - lane > t.row0 + c + 31;  // not computed
+        const int rows = col < p.C && p.other != nullptr && col - lane <= t.row0 + c ? t.rows - c : 0;
+        const half *o = p.other + ((size_t)t.e * p.R + col) * p.ld + t.row0 + c;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ahead[i] = 8 * i < rows && !above ? o[i] : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < 2; ++i) {
+            if (16 * i < rows) {
+                ahead[i] = load_half16(o + 16 * i);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ahead[i].w[j] = 0u;
+            }
+        }
     }
     __device__ __forceinline__ void finish(const Place &t, uint32_t tcol, int col, int c, int next) {
-        const size_t ld = p.C, base = (size_t)t.e * p.R * ld;
+        const size_t ld = p.ld, base = (size_t)t.e * p.R * ld;
         const bool ok = col < p.C;
         const int col_first = col - lane, r0 = t.row0 + c, rows = min(32, t.rows - c);  // a multiple of 8, as all sizes are
-        uint4 a[4];
+        Half16 a[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = ahead[i];
+        for (int i = 0; i < 2; ++i) a[i] = ahead[i];
         if (next < t.rows) fetch(t, col, next);
-        if (col_first > r0 + 31) return;  // above the diagonal
+        if (col_first > r0) return;  // above the diagonal (both are multiples of 32)
         float f = 1.0f;
         if (p.table != nullptr) {
             const float s = p.table[t.e];
@@ -165,41 +198,30 @@ struct Symmetric {
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));  // not read before the wait
+        const int diagonal = col_first == r0 ? lane : -1;  // its row
         uint32_t h[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float2 o = unpack_half2((&a[i / 4].x)[i % 4]);
+            const float2 o = unpack_half2(a[i / 8].w[i % 8]);
             float x = fmaf(p.k_other, o.x, p.k_acc * __uint_as_float(v[2 * i]));
             float y = fmaf(p.k_other, o.y, p.k_acc * __uint_as_float(v[2 * i + 1]));
-            if (r0 + 2 * i == col) x += p.k_diag;
-            if (r0 + 2 * i + 1 == col) y += p.k_diag;
+            if (2 * i == diagonal) x += p.k_diag;
+            if (2 * i + 1 == diagonal) y += p.k_diag;
             h[i] = pack_half2(f * x, f * y);
         }
-        half *across = p.out + base + (size_t)col * ld + r0;
-        if (col_first + 31 < r0) {  // below the diagonal
-            if (ok) {
+        if (ok && col_first < r0) {  // (the last 16 values may reach into the rows' padding)
+            half *across = p.out + base + (size_t)col * ld + r0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (8 * i < rows)
-                        reinterpret_cast<uint4 *>(across)[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
-            }
-            // both columns of a lane pair in one word, rows 2i (even lane) and 2i + 1
-            const int odd = lane & 1;
-            uint32_t *o = reinterpret_cast<uint32_t *>(p.out + base + (size_t)(r0 + odd) * ld + (col & ~1));
+            for (int i = 0; i < 2; ++i)
+                if (16 * i < rows) store_half16(across + 16 * i, h + 8 * i);
+        }
+        // both columns of a lane pair in one word, rows 2i (even lane) and 2i + 1
+        const int odd = lane & 1;
+        uint32_t *o = reinterpret_cast<uint32_t *>(p.out + base + (size_t)(r0 + odd) * ld + (col & ~1));
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, h[i], 1);
-                if (ok && 2 * i < rows) o[i * ld] = __byte_perm(h[i], got, odd ? 0x3276 : 0x5410);
-            }
-        } else if (ok) {
-            half *down = p.out + base + (size_t)r0 * ld + col;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                if (j >= rows || col > r0 + j) continue;
-                const half x = __ushort_as_half((unsigned short)(j & 1 ? h[j / 2] >> 16 : h[j / 2] & 0xffffu));
-                down[j * ld] = x;
-                across[j] = x;
-            }
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, h[i], 1);
+            if (ok && 2 * i < rows) o[i * ld] = __byte_perm(h[i], got, odd ? 0x3276 : 0x5410);
         }
     }
 };
@@ -574,6 +596,7 @@ int parts_of(long long size) { return (int)std::min<long long>(kMaxParts, (size 
 struct Workspace {
     size_t table, partial, x[2], lo, a, b, bytes;
 };
+int padded(int m) { return (m + 15) / 16 * 16; }  // rows of A and B begin at 32-byte boundaries
 Workspace lay_out(int E, int N, int K) {
     const size_t n = (size_t)N * K, m = std::min(N, K), e = E;
     auto room = [](size_t bytes) { return (bytes + 1023) / 1024 * 1024; };
@@ -584,8 +607,8 @@ Workspace lay_out(int E, int N, int K) {
     w.x[1] = w.x[0] + room(2 * e * n);
     w.lo = w.x[1] + room(2 * e * n);
     w.a = w.lo + room(2 * e * n);
-    w.b = w.a + room(2 * e * m * m);
-    w.bytes = w.b + room(2 * e * m * m);
+    w.b = w.a + room(2 * e * m * padded((int)m));
+    w.bytes = w.b + room(2 * e * m * padded((int)m));
     return w;
 }
 
@@ -654,17 +677,16 @@ long long choose_tiles(ProductArgs &g, bool b_mn, bool sym, int sms) {
     return tiles;
 }
 
-// The operand [E, outer, inner] of fp16; `mn`: its reduction index is the outer one.
-CUresult operand_map(CUtensorMap *m, const half *p, int E, int outer, int inner, bool mn, int box) {
-    return op_encode(m, {CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p, {(uint64_t)inner, (uint64_t)outer, (uint64_t)E},
-                         {(uint64_t)inner * 2, (uint64_t)inner * outer * 2}, {64, mn ? (uint32_t)kBK : (uint32_t)box, 1},
-                         CU_TENSOR_MAP_SWIZZLE_128B});
-}
-
+// An operand [E, outer, inner] of fp16, ld elements from row to row; `mn`: its reduction index is the outer one.
 struct Operand {
     const half *p;
-    int outer, inner;
+    int outer, inner, ld;
 };
+CUresult operand_map(CUtensorMap *m, const Operand &o, int E, bool mn, int box) {
+    return op_encode(m, {CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, o.p, {(uint64_t)o.inner, (uint64_t)o.outer, (uint64_t)E},
+                         {(uint64_t)o.ld * 2, (uint64_t)o.ld * o.outer * 2}, {64, mn ? (uint32_t)kBK : (uint32_t)box, 1},
+                         CU_TENSOR_MAP_SWIZZLE_128B});
+}
 
 template <bool A_MN, bool B_MN, bool SYM>
 moe_status product(const char *name, ProductArgs &g, const Operand &a, const Operand &b, int which, int sms, cudaStream_t s) {
@@ -672,8 +694,8 @@ moe_status product(const char *name, ProductArgs &g, const Operand &a, const Ope
     if (tiles > (1ll << 30)) return op_fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^30 tiles", name);
     g.tiles = (int)tiles;
     g.wait = wait_cycles(g.red / kBK + 1);
-    CUresult cr = operand_map(&g.map_a, a.p, g.E, a.outer, a.inner, A_MN, g.cols / 2);
-    if (cr == CUDA_SUCCESS) cr = operand_map(&g.map_b, b.p, g.E, b.outer, b.inner, B_MN, g.tile_rows / 2);
+    CUresult cr = operand_map(&g.map_a, a, g.E, A_MN, g.cols / 2);
+    if (cr == CUDA_SUCCESS) cr = operand_map(&g.map_b, b, g.E, B_MN, g.tile_rows / 2);
     if (cr != CUDA_SUCCESS) return op_fail(MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", name, (int)cr);
     auto kernel = product_kernel<A_MN, B_MN, SYM>;
     const cudaError_t ce = op_allow_smem(reinterpret_cast<const void *>(kernel), kSmemBytes, &g_attr[which]);
@@ -761,12 +783,12 @@ extern "C" moe_status moe_orthogonalize(const void *G, int dtype, int E, int N, 
     if (ce != cudaSuccess) return op_cuda(ce, name);
 
     const bool wide = N <= K;
-    const int m = std::min(N, K);
+    const int m = std::min(N, K), ld = padded(m);
     for (int i = 0; i < steps; ++i) {
         const float *c = coefficients + 3 * i, sa = scales[i].a, sb = scales[i].b;
-        const Operand X{x[i & 1], N, K}, sym_a{A, m, m}, sym_b{B, m, m};
+        const Operand X{x[i & 1], N, K, K}, sym_a{A, m, m, ld}, sym_b{B, m, m, ld};
         ProductArgs g = {};  // A
-        g.E = E, g.R = g.C = m, g.red = wide ? K : N, g.err = err;
+        g.E = E, g.R = g.C = m, g.ld = ld, g.red = wide ? K : N, g.err = err;
         g.table = i == 0 ? table : nullptr;
         g.out = A;
         g.k_acc = sa / (up * up);
@@ -774,7 +796,7 @@ extern "C" moe_status moe_orthogonalize(const void *G, int dtype, int E, int N, 
         if (st != MOE_OK) return st;
 
         g = {};  // B
-        g.E = E, g.R = g.C = g.red = m, g.err = err;
+        g.E = E, g.R = g.C = g.red = m, g.ld = ld, g.err = err;
         g.table = i == 0 ? table : nullptr;
         g.other = A;
         g.out = B;
