@@ -27,9 +27,13 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512;
 constexpr int kMaxH = 8192;
-constexpr int kMaxTeams = kThreads / 32;
+constexpr int kForwardThreads = 512;
+// Threads of the backward kernel's CTAs (one per SM): as many as have registers for a thread's
+// sums (24) and the row's values.
+template <typename TX, typename TF>
+constexpr int kBackwardThreads = sizeof(TX) + sizeof(TF) == 4 ? 1024 : sizeof(TX) + sizeof(TF) == 6 ? 768 : 512;
+constexpr int kMaxTeams = 1024 / 32;
 constexpr int kMaxCtas = 256;  // of the backward kernel: partial sums of the weights' gradients
 constexpr float kDown = 0x1p-100f;
 
@@ -121,7 +125,7 @@ __device__ __forceinline__ float inverse_root(float sum, float inv_h, float eps)
 
 // V: groups of 8 values per thread, `team` threads apart.
 template <typename TX, typename TF, int V>
-__global__ void __launch_bounds__(kThreads, 1) norm_forward_kernel(const SandwichArgs p) {
+__global__ void __launch_bounds__(kForwardThreads, 1) norm_forward_kernel(const SandwichArgs p) {
     __shared__ float slots[kMaxTeams * 96];
     Team team = make_team(slots, p.team);
     const int me = threadIdx.x - team.id * p.team, H = p.H;
@@ -228,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_forward_kernel(const Sandwic
 }
 
 template <typename TX, typename TF, int V>
-__global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const SandwichArgs p) {
+__global__ void __launch_bounds__(kBackwardThreads<TX, TF>, 1) norm_backward_kernel(const SandwichArgs p) {
     // the effective weights and the channels' gate, later the teams' sums: three arrays of H values, the first
     // four values of each group of 8 in one half, the other four in the other, so that a warp's loads have no bank conflicts
     extern __shared__ float4 smem[];
@@ -269,42 +273,41 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const Sandwi
     }
     __syncthreads();
 
-    Raw<TX> xr[V], dxr[V];
-    Raw<TF> fr[V], dnr[V];
-    float gate = 1.0f;
-    auto fetch = [&](int row) {
+    int row = blockIdx.x * (blockDim.x / p.team) + team.id;
+    for (; row < p.T; row += stride) {
+        Raw<TX> xr[V], dxr[V];
+        Raw<TF> fr[V], dnr[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const size_t at = (size_t)row * H + 8 * (me + i * p.team);
-            const bool here = row < p.T && in[i];
             xr[i].zero(), dxr[i].zero(), fr[i].zero(), dnr[i].zero();
-            if (here && has_pre) xr[i].load(static_cast<const TX *>(p.x) + at), dnr[i].load(static_cast<const TF *>(p.dn) + at);
-            if (here && p.dx != nullptr) dxr[i].load(static_cast<const TX *>(p.dx) + at);
-            if (here && has_f) fr[i].load(static_cast<const TF *>(p.f) + at);
+            if (in[i] && has_pre) xr[i].load(static_cast<const TX *>(p.x) + at), dnr[i].load(static_cast<const TF *>(p.dn) + at);
+            if (in[i] && has_f) fr[i].load(static_cast<const TF *>(p.f) + at);
+            if (in[i] && p.dx != nullptr) dxr[i].load(static_cast<const TX *>(p.dx) + at);
         }
-        if (token && row < p.T) gate = p.gate[row];
-    };
-    int row = blockIdx.x * (blockDim.x / p.team) + team.id;
-    fetch(row);
-    for (; row < p.T; row += stride) {
-        float x[V][8], f[V][8], dn[V][8], t[V][8];
-        const float g = gate;
-#pragma unroll
-        for (int i = 0; i < V; ++i) xr[i].get(x[i]), fr[i].get(f[i]), dnr[i].get(dn[i]), dxr[i].get(t[i]);
-        fetch(row + stride < p.T ? row + stride : p.T);
-        float w[8];
+        const float g = token ? p.gate[row] : 1.0f;
+        float w[8], a[8], b[8];
         // the squares of X' and F, and dN w_pre X'
         float sx = 1.0f, sf = 1.0f, s[3];
         auto sums = [&]() {
             s[0] = s[1] = s[2] = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                weights(0, i, w);
+                if (has_pre) {
+                    weights(0, i, w);
+                    xr[i].get(a);
+                    dnr[i].get(b);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    s[0] = fmaf(x[i][j] * sx, x[i][j] * sx, s[0]);
-                    s[1] = fmaf(f[i][j] * sf, f[i][j] * sf, s[1]);
-                    s[2] = fmaf(dn[i][j] * w[j], x[i][j] * sx, s[2]);
+                    for (int j = 0; j < 8; ++j) {
+                        const float x = a[j] * sx;
+                        s[0] = fmaf(x, x, s[0]);
+                        s[2] = fmaf(b[j] * w[j], x, s[2]);
+                    }
+                }
+                if (has_post) {
+                    fr[i].get(a);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s[1] = fmaf(a[j] * sf, a[j] * sf, s[1]);
                 }
             }
             team.sum(s);
@@ -316,48 +319,45 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const Sandwi
             sums();
         }
         const float rxs = inverse_root(s[0], inv_h, p.eps * sx * sx), rx = rxs * sx, mean = rxs * s[2] * inv_h;
-        const float rfs = has_post ? inverse_root(s[1], inv_h, p.eps * sf * sf) : 1.0f;
-        const float rf = has_post ? rfs * sf : 1.0f;
-        if (has_pre) {
+        const float rf = has_post ? inverse_root(s[1], inv_h, p.eps * sf * sf) * sf : 1.0f;
+        float t[V][8], m[1] = {0.0f};
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < V; ++i) {
+            dxr[i].get(t[i]);
+            if (has_pre) {
                 weights(0, i, w);
+                xr[i].get(a);
+                dnr[i].get(b);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float xh = x[i][j] * rx;
-                    d_pre[i][j] = fmaf(dn[i][j], xh, d_pre[i][j]);
-                    t[i][j] = fmaf(rx, fmaf(-xh, mean, dn[i][j] * w[j]), t[i][j]);
+                    const float xh = a[j] * rx;
+                    d_pre[i][j] = fmaf(b[j], xh, d_pre[i][j]);
+                    t[i][j] = fmaf(rx, fmaf(-xh, mean, b[j] * w[j]), t[i][j]);
                 }
             }
-        }
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float o[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = has_f ? p.alpha * t[i][j] : t[i][j];
-            if (in[i]) Raw<TX>::store(static_cast<TX *>(p.xo) + (size_t)row * H + 8 * (me + i * p.team), o);
-        }
-        if (!has_f) continue;
-        // from here f is fh, and of T the channels' gate times T is kept
-        float m[1] = {0.0f};
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float wg[8];
+            for (int j = 0; j < 8; ++j) a[j] = has_f ? p.alpha * t[i][j] : t[i][j];
+            if (in[i]) Raw<TX>::store(static_cast<TX *>(p.xo) + (size_t)row * H + 8 * (me + i * p.team), a);
+            if (!has_f) continue;
+            fr[i].get(a);
             weights(1, i, w);
-            if (channel) weights(2, i, wg);
+            if (channel) {  // from here t is T times the gate
+                weights(2, i, b);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    d_gate[i][j] = fmaf(t[i][j], a[j] * rf * w[j], d_gate[i][j]);
+                    t[i][j] *= b[j];
+                }
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float fh = f[i][j] * rf;
-                if (channel) {
-                    d_gate[i][j] = fmaf(t[i][j], fh * w[j], d_gate[i][j]);
-                    t[i][j] *= wg[j];
-                }
+                const float fh = a[j] * rf;
                 m[0] = fmaf(t[i][j] * w[j], fh, m[0]);
                 t[i][j] *= g;
                 d_post[i][j] = fmaf(t[i][j], fh, d_post[i][j]);
-                f[i][j] = fh;
             }
         }
+        if (!has_f) continue;
         float mean_f = 0.0f;
         if (has_post || token) {
             team.sum(m);
@@ -366,11 +366,11 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const Sandwi
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            float o[8];
+            fr[i].get(a);
             weights(1, i, w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = rf * (has_post ? fmaf(-f[i][j], mean_f, t[i][j] * w[j]) : t[i][j]);
-            if (in[i]) Raw<TF>::store(static_cast<TF *>(p.fo) + (size_t)row * H + 8 * (me + i * p.team), o);
+            for (int j = 0; j < 8; ++j) a[j] = rf * (has_post ? fmaf(-a[j] * rf, mean_f, t[i][j] * w[j]) : t[i][j]);
+            if (in[i]) Raw<TF>::store(static_cast<TF *>(p.fo) + (size_t)row * H + 8 * (me + i * p.team), a);
         }
     }
 
@@ -431,13 +431,20 @@ __global__ void __launch_bounds__(32 * kSumRows) norm_sum_kernel(const float *pa
 
 OpDone g_attr[8];
 
-int groups_of(int H) { return H > 8 * kThreads ? 2 : 1; }
+int groups_of(int H, int threads) { return H > 8 * threads ? 2 : 1; }
+int backward_threads(int x_dtype, int f_dtype) {
+    if (x_dtype == MOE_DTYPE_F32 && f_dtype == MOE_DTYPE_F32) return kBackwardThreads<float, float>;
+    return x_dtype == f_dtype ? kBackwardThreads<bf16, bf16> : kBackwardThreads<float, bf16>;
+}
+
+// Teams of several warps have a named barrier each, of 15.
+int most_teams(int team) { return team > 32 ? 15 : kMaxTeams; }
 
 // Threads per team and teams per CTA: as many as fit, fewer where rows would leave SMs without one.
-void shape(int T, int H, int sms, int &team, int &teams) {
-    const int per = 8 * groups_of(H);
+void shape(int T, int H, int sms, int threads, int &team, int &teams) {
+    const int per = 8 * groups_of(H, threads);
     team = 32 * ((H + 32 * per - 1) / (32 * per));
-    teams = std::max(1, std::min(kThreads / team, (T + sms - 1) / sms));
+    teams = std::max(1, std::min(std::min(threads / team, most_teams(team)), (T + sms - 1) / sms));
 }
 
 struct Buffer {
@@ -532,9 +539,9 @@ extern "C" moe_status moe_sandwich_norm(const void *X, const void *F, const floa
     a.alpha = residual_scale, a.eps = eps, a.one = kind == MOE_NORM_GEMMA ? 1.0f : 0.0f;
     a.T = T, a.H = H, a.gate_kind = gate_kind;
     int teams;
-    shape(T, H, sms, a.team, teams);
+    shape(T, H, sms, kForwardThreads, a.team, teams);
     const unsigned grid = (unsigned)std::min<long long>(sms, ((long long)T + teams - 1) / teams);
-    return op_cuda(pick<Forward>(x_dtype, f_dtype, groups_of(H), [&](KernelFn k, int) {
+    return op_cuda(pick<Forward>(x_dtype, f_dtype, groups_of(H, kForwardThreads), [&](KernelFn k, int) {
                        return launch_pdl(k, dim3(grid), dim3(a.team * teams), 0, reinterpret_cast<cudaStream_t>(stream), a);
                    }), name);
 }
@@ -584,10 +591,11 @@ extern "C" moe_status moe_sandwich_norm_backward(const void *dX_out, const void 
         a.xo = dX, a.fo = dF, a.dgate = dgate, a.partial = static_cast<float *>(workspace);
         a.alpha = residual_scale, a.eps = eps, a.one = kind == MOE_NORM_GEMMA ? 1.0f : 0.0f;
         a.T = T, a.H = H, a.gate_kind = gate_kind;
+        const int threads = backward_threads(x_dtype, f_dtype);
         int teams;
-        shape(T, H, sms, a.team, teams);
+        shape(T, H, sms, threads, a.team, teams);
         grid = (int)std::min<long long>(std::min(sms, kMaxCtas), ((long long)T + teams - 1) / teams);
-        const cudaError_t e = pick<Backward>(x_dtype, f_dtype, groups_of(H), [&](KernelFn k, int which) {
+        const cudaError_t e = pick<Backward>(x_dtype, f_dtype, groups_of(H, threads), [&](KernelFn k, int which) {
             const cudaError_t ce = op_allow_smem(reinterpret_cast<const void *>(k), 3 * kMaxH * 4, &g_attr[which]);
             return ce != cudaSuccess ? ce : launch_pdl(k, dim3(grid), dim3(a.team * teams), 3ull * H * 4, s, a);
         });

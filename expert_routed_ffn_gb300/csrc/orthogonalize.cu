@@ -83,38 +83,32 @@ struct Place {
 // Walks tiles first, first + step, .. of all matrices, the column tile innermost.  SYM: of a row
 // tile only the column tiles that begin at its last row or before.  (The lower triangle: the last
 // row tile may be short, and then takes fewer of the MMA's N, where a short column tile takes
-// all of its M, so few tiles should be of the last columns.)  Where the last row tiles are short
-// they come after all the others, so that each CTA pair gets as many of them as any other.
+// all of its M, so few tiles should be of the last columns.)  The order is the matrices', for L2:
+// with all short row tiles last, which deals them evenly, five steps of 32 x 1408 x 2048 took
+// 2077 us for 1998.
 template <bool SYM>
 struct Walk {
     const ProductArgs &p;
     int tile, step, e = 0, r = 0, c;
-    int begin = 0, end;  // row tiles walked of each matrix
-    __device__ __forceinline__ Walk(const ProductArgs &args, int first, int by) : p(args), tile(first), step(by), c(first) {
-        end = p.row_tiles > 1 && p.row_tiles * p.tile_rows > p.R ? p.row_tiles - 1 : p.row_tiles;
-        settle();
-    }
+    __device__ __forceinline__ Walk(const ProductArgs &args, int first, int by) : p(args), tile(first), step(by), c(first) { settle(); }
     __device__ __forceinline__ int reach() const {
         return SYM ? ((min(p.R, (r + 1) * p.tile_rows) - 1) >> p.col_shift) + 1 : p.col_tiles;
     }
     __device__ __forceinline__ void settle() {
-        for (;;) {
-            if (end - begin == 1 || !SYM) {  // as many tiles in each matrix: whole ones are skipped at once
-                const int per = (end - begin) * reach(), left = p.E - 1 - e;
-                const int n = min(c / per, left);
+        if (!SYM) {
+            const int per = p.row_tiles * p.col_tiles;
+            if (c >= per) {  // a matrix or more on
+                const int n = c / per;
                 e += n;
                 c -= n * per;
             }
-            for (int here = reach(); c >= here; here = reach()) {
-                c -= here;
-                if (++r < end) continue;
-                r = begin;
-                if (++e == p.E) break;
+        }
+        for (int here = reach(); c >= here; here = reach()) {
+            c -= here;
+            if (++r == p.row_tiles) {
+                r = 0;
+                ++e;
             }
-            if (e < p.E) return;
-            e = 0;  // the last row tiles
-            r = begin = end;
-            end = p.row_tiles;
         }
     }
     __device__ __forceinline__ bool more() const { return tile < p.tiles; }
