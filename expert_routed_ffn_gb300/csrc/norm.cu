@@ -28,13 +28,14 @@ namespace moe {
 namespace {
 
 constexpr int kMaxH = 8192;
-constexpr int kForwardThreads = 512;
-// Threads of the backward kernel's CTAs (one per SM): as many as have registers for a thread's
-// sums (24) and the row's values.
+// Threads of a CTA (one per SM): as many as have registers for the values of a row, and backward
+// for a thread's sums.
 template <typename TX, typename TF>
-constexpr int kBackwardThreads = sizeof(TX) + sizeof(TF) == 4 ? 1024 : sizeof(TX) + sizeof(TF) == 6 ? 768 : 512;
+constexpr int kForwardThreads = sizeof(TX) + sizeof(TF) == 8 ? 768 : 1024;
+constexpr int kBackwardThreads = 512;
+constexpr int kBackwardSmem = 212 << 10;  // dynamic shared memory, most
 constexpr int kMaxTeams = 1024 / 32;
-constexpr int kMaxCtas = 256;  // of the backward kernel: partial sums of the weights' gradients
+constexpr int kMaxCtas = 256;
 constexpr float kDown = 0x1p-100f;
 
 struct SandwichArgs {
@@ -46,107 +47,198 @@ struct SandwichArgs {
     float *partial;       // backward: [grid][3][H]
     float alpha, eps, one;  // one: added to the weights
     int T, H, gate_kind, team;  // team: threads
+    int stages;                 // backward: rows in flight, 1 to 3, the present one among them
+    bool weights_in_smem;
 };
 
-// 8 consecutive values as loaded.
+// Two fp32 values in one 64-bit register, and arithmetic on both in one instruction: half the
+// instructions of a row, which bound the backward pass (105 us for 16384 x 2048 before).
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 make2(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ f2 both(float v) { return make2(v, v); }
+__device__ __forceinline__ float2 split(f2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float sum_of(f2 v) {
+    const float2 s = split(v);
+    return s.x + s.y;
+}
+
+// 8 consecutive values as loaded, and as pairs of fp32.
 template <typename T>
 struct Raw;
 template <>
 struct Raw<bf16> {
     uint4 v;
-    __device__ __forceinline__ void load(const bf16 *p) { v = *reinterpret_cast<const uint4 *>(p); }
-    __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float (&o)[8]) const {
-        o[0] = bf16_lo(v.x), o[1] = bf16_hi(v.x), o[2] = bf16_lo(v.y), o[3] = bf16_hi(v.y);
-        o[4] = bf16_lo(v.z), o[5] = bf16_hi(v.z), o[6] = bf16_lo(v.w), o[7] = bf16_hi(v.w);
+    __device__ __forceinline__ void load(const void *p, size_t at, bool in) {
+        v = in ? *reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(p) + at) : make_uint4(0, 0, 0, 0);
     }
-    static __device__ __forceinline__ void store(bf16 *p, const float (&o)[8]) {
-        *reinterpret_cast<uint4 *>(p) =
-            make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+    __device__ __forceinline__ f2 get(int i) const {
+        const uint32_t w = (&v.x)[i];
+        return make2(bf16_lo(w), bf16_hi(w));
+    }
+    static __device__ __forceinline__ void store(void *p, size_t at, const f2 (&o)[4]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 s = split(o[i]);
+            w[i] = pack_bf16x2(s.x, s.y);
+        }
+        *reinterpret_cast<uint4 *>(static_cast<bf16 *>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
 template <>
 struct Raw<float> {
     float4 a, b;
-    __device__ __forceinline__ void load(const float *p) {
-        a = reinterpret_cast<const float4 *>(p)[0];
-        b = reinterpret_cast<const float4 *>(p)[1];
+    __device__ __forceinline__ void load(const void *p, size_t at, bool in) {
+        const float4 *f = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
+        a = in ? f[0] : make_float4(0.f, 0.f, 0.f, 0.f);
+        b = in ? f[1] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void get(float (&o)[8]) const {
-        o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+    __device__ __forceinline__ f2 get(int i) const {
+        const float4 &h = i < 2 ? a : b;
+        return i % 2 ? make2(h.z, h.w) : make2(h.x, h.y);
     }
-    static __device__ __forceinline__ void store(float *p, const float (&o)[8]) {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(o[0], o[1], o[2], o[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(o[4], o[5], o[6], o[7]);
+    static __device__ __forceinline__ void store(void *p, size_t at, const f2 (&o)[4]) {
+        const float2 w = split(o[0]), x = split(o[1]), y = split(o[2]), z = split(o[3]);
+        float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
+        f[0] = make_float4(w.x, w.y, x.x, x.y);
+        f[1] = make_float4(y.x, y.y, z.x, z.y);
     }
 };
 
-// Sums over a team, in all its threads.  slots: [2][16][3] of the team; two sums in a row use
-// different halves, so one barrier each is enough: who writes a half again has passed the barrier
-// of the sum between, which everyone reaches after reading.
+// Sums over a team, in all its threads.  slots: [2][3][32], zeros where there is no warp; two sums
+// in a row use different halves, so one barrier each is enough: who writes a half again has passed
+// the barrier of the sum between, which everyone reaches after reading.
+constexpr int kSlots = 2 * 3 * 32;
 struct Team {
-    int threads, id, warps, warp;
+    int threads, id, warps, warp, lane;
     float *slots;
     int half;
-    template <int N>
-    __device__ __forceinline__ void sum(float (&v)[N]) {
+    __device__ __forceinline__ Team(float *all, int team_threads) {
+        threads = team_threads;
+        id = threadIdx.x / threads;
+        warps = threads / 32;
+        warp = (threadIdx.x - id * threads) / 32;
+        lane = threadIdx.x & 31;
+        slots = all + id * kSlots;
+        half = 0;
+    }
+    __device__ __forceinline__ void sync() const { asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory"); }
+    __device__ __forceinline__ float over_warps(const float *s) const {
+        f2 a = 0, b = 0;
+        for (int w = 0; w < warps; w += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(s + w);
+            a = add2(a, make2(v.x, v.y));
+            b = add2(b, make2(v.z, v.w));
+        }
+        return sum_of(add2(a, b));
+    }
+    __device__ __forceinline__ void sum(float &v) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         if (warps == 1) return;
-        float *s = slots + half * 48;
+        float *s = slots + half * 96;
         half ^= 1;
-        if ((threadIdx.x & 31) == 0)
+        if (lane == 0) s[warp] = v;
+        sync();
+        v = over_warps(s);
+    }
+    // Three at once: the first exchanges leave each quarter of the warp one of them to add up.
+    __device__ __forceinline__ void sum(float &x, float &y, float &z) {
+        const bool high = lane & 16, odd = lane & 8;
+        float a = (high ? z : x) + __shfl_xor_sync(0xffffffffu, high ? x : z, 16);
+        float b = (high ? 0.0f : y) + __shfl_xor_sync(0xffffffffu, high ? y : 0.0f, 16);
+        float v = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
 #pragma unroll
-            for (int i = 0; i < N; ++i) s[warp * 3 + i] = v[i];
-        asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = 0.0f;
-        for (int w = 0; w < warps; ++w)
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] += s[w * 3 + i];
+        for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (warps == 1) {
+            x = __shfl_sync(0xffffffffu, v, 0);
+            y = __shfl_sync(0xffffffffu, v, 8);
+            z = __shfl_sync(0xffffffffu, v, 16);
+            return;
+        }
+        float *s = slots + half * 96;
+        half ^= 1;
+        if ((lane & 7) == 0 && lane < 24) s[lane * 4 + warp] = v;
+        sync();
+        x = over_warps(s);
+        y = over_warps(s + 32);
+        z = over_warps(s + 64);
     }
 };
 
-__device__ __forceinline__ Team make_team(float *slots, int threads) {
-    Team t;
-    t.threads = threads;
-    t.id = threadIdx.x / threads;
-    t.warps = threads / 32;
-    t.warp = (threadIdx.x - t.id * threads) / 32;
-    t.slots = slots + t.id * 96;
-    t.half = 0;
-    return t;
-}
+// (good to 2.2 units of 2^-24, where the sum may be off by 24)
+__device__ __forceinline__ float inverse_root(float sum, float inv_h, float eps) { return rsqrtf(fmaf(sum, inv_h, eps)); }
 
-__device__ __forceinline__ float inverse_root(float sum, float inv_h, float eps) { return 1.0f / sqrtf(sum * inv_h + eps); }
+// Weights in shared memory: `count` arrays of H values, the first four values of each group of 8 in
+// one half of an array, the other four in the other, so that a warp's loads have no bank conflicts.
+struct Weights {
+    float4 *smem;
+    int groups;  // H / 8
+    template <typename Fn>
+    __device__ __forceinline__ void fill(int which, Fn four) const {  // four(i): values 4 i ..
+        for (int i = threadIdx.x; i < 2 * groups; i += blockDim.x) smem[2 * which * groups + (i & 1) * groups + i / 2] = four(i);
+    }
+    __device__ __forceinline__ void get(int which, int group, f2 (&w)[4]) const {
+        const float4 *at = smem + 2 * which * groups + group;
+        const float4 a = at[0], b = at[groups];
+        w[0] = make2(a.x, a.y), w[1] = make2(a.z, a.w), w[2] = make2(b.x, b.y), w[3] = make2(b.z, b.w);
+    }
+};
+__device__ __forceinline__ float4 four_of(const float *w, int i, float otherwise, float more) {
+    if (w == nullptr) return make_float4(otherwise, otherwise, otherwise, otherwise);
+    const float4 v = reinterpret_cast<const float4 *>(w)[i];
+    return make_float4(v.x + more, v.y + more, v.z + more, v.w + more);
+}
 
 // V: groups of 8 values per thread, `team` threads apart.
 template <typename TX, typename TF, int V>
-__global__ void __launch_bounds__(kForwardThreads, 1) norm_forward_kernel(const SandwichArgs p) {
-    __shared__ float slots[kMaxTeams * 96];
-    Team team = make_team(slots, p.team);
+__global__ void __launch_bounds__(kForwardThreads<TX, TF>, 1) norm_forward_kernel(const SandwichArgs p) {
+    extern __shared__ float4 smem[];
+    __shared__ __align__(16) float slots[kMaxTeams * kSlots];
+    Team team(slots, p.team);
     const int me = threadIdx.x - team.id * p.team, H = p.H;
     const int stride = gridDim.x * (blockDim.x / p.team);
     const float inv_h = 1.0f / H;
     const bool has_f = p.f != nullptr, has_pre = p.pre != nullptr, has_post = p.post != nullptr;
-    float pre[V][8], post[V][8];
-    bool in[V];
+    const bool channel = p.gate_kind == MOE_GATE_CHANNEL, token = p.gate_kind == MOE_GATE_TOKEN;
+    const Weights weights{smem, H / 8};
+    for (int i = threadIdx.x; i < kMaxTeams * kSlots; i += blockDim.x) slots[i] = 0.0f;
     pdl_wait();
     pdl_trigger();
+    weights.fill(0, [&](int i) { return four_of(p.pre, i, 0.0f, p.one); });
+    weights.fill(1, [&](int i) {  // the channels' gate is one more factor of the weight
+        const float4 w = four_of(p.post, i, 1.0f, p.one), g = four_of(channel ? p.gate : nullptr, i, 1.0f, 0.0f);
+        return make_float4(w.x * g.x, w.y * g.y, w.z * g.z, w.w * g.w);
+    });
+    int group[V];
+    bool in[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int at = 8 * (me + i * p.team);
-        in[i] = at < H;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            pre[i][j] = has_pre && in[i] ? p.pre[at + j] + p.one : 0.0f;
-            post[i][j] = !in[i] ? 0.0f : has_post ? p.post[at + j] + p.one : 1.0f;
-            // the channels' gate is one more factor of the weight
-            if (in[i] && p.gate_kind == MOE_GATE_CHANNEL) post[i][j] *= p.gate[at + j];
-        }
+        in[i] = 8 * (me + i * p.team) < H;
+        group[i] = in[i] ? me + i * p.team : 0;  // (the values beyond H are zeros)
     }
     Raw<TX> xr[V];
     Raw<TF> fr[V];
@@ -154,225 +246,299 @@ __global__ void __launch_bounds__(kForwardThreads, 1) norm_forward_kernel(const 
     auto fetch = [&](int row) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const size_t at = (size_t)row * H + 8 * (me + i * p.team);
-            if (row < p.T && in[i]) {
-                xr[i].load(static_cast<const TX *>(p.x) + at);
-                if (has_f) fr[i].load(static_cast<const TF *>(p.f) + at);
-            } else {
-                xr[i].zero();
-                fr[i].zero();
-            }
+            const size_t at = (size_t)row * H + 8 * group[i];
+            xr[i].load(p.x, at, in[i]);
+            if (has_f) fr[i].load(p.f, at, in[i]);
         }
-        if (p.gate_kind == MOE_GATE_TOKEN && row < p.T) gate = p.gate[row];
+        if (token) gate = p.gate[row];
     };
     int row = blockIdx.x * (blockDim.x / p.team) + team.id;
-    fetch(row);
+    if (row < p.T) fetch(row);
+    __syncthreads();
     for (; row < p.T; row += stride) {
-        float x[V][8], f[V][8];
-        const float g = gate;
+        f2 x[V][4], w[4];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            xr[i].get(x[i]);
-            if (has_f) fr[i].get(f[i]);
-        }
-        fetch(row + stride < p.T ? row + stride : p.T);
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[i][j] = xr[i].get(j);
         if (has_f) {
             float rf = 1.0f;
             if (has_post) {
-                float ss[1] = {0.0f};
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) ss[0] = fmaf(f[i][j], f[i][j], ss[0]);
-                team.sum(ss);
-                rf = inverse_root(ss[0], inv_h, p.eps);
-                if (!(ss[0] < INFINITY)) {
-                    ss[0] = 0.0f;
+                auto squares = [&](float scale) {
+                    f2 s = 0;
 #pragma unroll
                     for (int i = 0; i < V; ++i)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) ss[0] = fmaf(f[i][j] * kDown, f[i][j] * kDown, ss[0]);
-                    team.sum(ss);
-                    rf = inverse_root(ss[0], inv_h, p.eps * kDown * kDown) * kDown;
+                        for (int j = 0; j < 4; ++j) {
+                            f2 f = fr[i].get(j);
+                            if (scale != 1.0f) f = mul2(f, both(scale));
+                            s = fma2(f, f, s);
+                        }
+                    float total = sum_of(s);
+                    team.sum(total);
+                    return total;
+                };
+                float ss = squares(1.0f);
+                rf = inverse_root(ss, inv_h, p.eps);
+                if (!(ss < INFINITY)) {
+                    ss = squares(kDown);
+                    rf = inverse_root(ss, inv_h, p.eps * kDown * kDown) * kDown;
                 }
             }
-            rf *= g;
+            if (token) rf *= gate;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
+                weights.get(1, group[i], w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[i][j] = fmaf(p.alpha, x[i][j], f[i][j] * rf * post[i][j]);
-                if (in[i]) Raw<TX>::store(static_cast<TX *>(p.xo) + (size_t)row * H + 8 * (me + i * p.team), x[i]);
+                for (int j = 0; j < 4; ++j) {
+                    const f2 branch = mul2(mul2(fr[i].get(j), both(rf)), w[j]);
+                    x[i][j] = fma2(both(p.alpha), x[i][j], branch);
+                }
             }
         }
-        if (has_pre) {
-            float ss[1] = {0.0f};
+        const size_t base = (size_t)row * H;
+        if (row + stride < p.T) fetch(row + stride);
+        if (has_f) {
 #pragma unroll
             for (int i = 0; i < V; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) ss[0] = fmaf(x[i][j], x[i][j], ss[0]);
-            team.sum(ss);
-            float rx = inverse_root(ss[0], inv_h, p.eps);
-            if (!(ss[0] < INFINITY)) {
-                ss[0] = 0.0f;
+                if (in[i]) Raw<TX>::store(p.xo, base + 8 * group[i], x[i]);
+        }
+        if (has_pre) {
+            auto squares = [&](float scale) {
+                f2 s = 0;
 #pragma unroll
                 for (int i = 0; i < V; ++i)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) ss[0] = fmaf(x[i][j] * kDown, x[i][j] * kDown, ss[0]);
-                team.sum(ss);
-                rx = inverse_root(ss[0], inv_h, p.eps * kDown * kDown) * kDown;
+                    for (int j = 0; j < 4; ++j) {
+                        f2 v = in[i] ? x[i][j] : 0ull;
+                        if (scale != 1.0f) v = mul2(v, both(scale));
+                        s = fma2(v, v, s);
+                    }
+                float total = sum_of(s);
+                team.sum(total);
+                return total;
+            };
+            float ss = squares(1.0f);
+            float rx = inverse_root(ss, inv_h, p.eps);
+            if (!(ss < INFINITY)) {
+                ss = squares(kDown);
+                rx = inverse_root(ss, inv_h, p.eps * kDown * kDown) * kDown;
             }
 #pragma unroll
             for (int i = 0; i < V; ++i) {
+                weights.get(0, group[i], w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[i][j] = x[i][j] * rx * pre[i][j];
-                if (in[i]) Raw<TF>::store(static_cast<TF *>(p.fo) + (size_t)row * H + 8 * (me + i * p.team), x[i]);
+                for (int j = 0; j < 4; ++j) w[j] = mul2(mul2(x[i][j], both(rx)), w[j]);
+                if (in[i]) Raw<TF>::store(p.fo, base + 8 * group[i], w);
             }
         }
     }
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {  // zeros where not `in`
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
+// What a thread has in flight: its values of the next rows, in shared memory of its own, so that no
+// thread waits for another's copies.  A row's tensors are X', dN, F and dX' in pieces of 16 bytes.
 template <typename TX, typename TF, int V>
-__global__ void __launch_bounds__(kBackwardThreads<TX, TF>, 1) norm_backward_kernel(const SandwichArgs p) {
-    // the effective weights and the channels' gate, later the teams' sums: three arrays of H values, the first
-    // four values of each group of 8 in one half, the other four in the other, so that a warp's loads have no bank conflicts
+struct Ring {
+    static constexpr int kX = sizeof(TX) / 2, kF = sizeof(TF) / 2;  // pieces of 8 values
+    static constexpr int kPieces = 2 * V * (kX + kF);
+    static constexpr int kPieceStep = kBackwardThreads * 16;
+    uint32_t mine;  // the thread's first piece of stage 0
+    __device__ __forceinline__ uint32_t piece(int stage, int k) const { return mine + (stage * kPieces + k) * kPieceStep; }
+    template <typename T>
+    __device__ __forceinline__ void ask(int stage, int first, const void *p, size_t at, bool in) const {
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(p) + at);
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k) copy16(piece(stage, first + k), src + k, in);
+    }
+    __device__ __forceinline__ uint4 load(int stage, int k) const {
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(piece(stage, k)) : "memory");
+        return v;
+    }
+    template <typename T>
+    __device__ __forceinline__ void get(int stage, int first, f2 (&o)[4]) const {
+        if constexpr (sizeof(T) == 2) {
+            const uint4 v = load(stage, first);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = make2(bf16_lo((&v.x)[i]), bf16_hi((&v.x)[i]));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint4 v = load(stage, first + k);
+                o[2 * k] = make2(__uint_as_float(v.x), __uint_as_float(v.y));
+                o[2 * k + 1] = make2(__uint_as_float(v.z), __uint_as_float(v.w));
+            }
+        }
+    }
+    __device__ __forceinline__ void x(int s, int i, f2 (&o)[4]) const { get<TX>(s, i * kX, o); }
+    __device__ __forceinline__ void dn(int s, int i, f2 (&o)[4]) const { get<TF>(s, V * kX + i * kF, o); }
+    __device__ __forceinline__ void f(int s, int i, f2 (&o)[4]) const { get<TF>(s, V * (kX + kF) + i * kF, o); }
+    __device__ __forceinline__ void dx(int s, int i, f2 (&o)[4]) const { get<TX>(s, V * (kX + 2 * kF) + i * kX, o); }
+};
+
+// CHANNEL: the gate is one per channel.
+template <typename TX, typename TF, int V, bool CHANNEL>
+__global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_kernel(const SandwichArgs p) {
+    // the effective weights and the channels' gate (where they fit), and the rings; later the teams' sums
     extern __shared__ float4 smem[];
-    __shared__ float slots[kMaxTeams * 96];
-    Team team = make_team(slots, p.team);
+    __shared__ __align__(16) float slots[kBackwardThreads / 32 * kSlots];
+    Team team(slots, p.team);
     const int me = threadIdx.x - team.id * p.team, H = p.H;
     const int stride = gridDim.x * (blockDim.x / p.team);
     const float inv_h = 1.0f / H;
     const bool has_f = p.f != nullptr, has_pre = p.pre != nullptr, has_post = p.post != nullptr;
-    const bool channel = p.gate_kind == MOE_GATE_CHANNEL, token = p.gate_kind == MOE_GATE_TOKEN;
-    pdl_wait();
-    pdl_trigger();
-    const int groups = H / 8;
-    for (int i = threadIdx.x; i < 2 * groups; i += blockDim.x) {  // i: group of 4 values
-        const int to = (i & 1) * groups + i / 2;
-        auto four = [&](const float *w, float otherwise, float more) {
-            if (w == nullptr) return make_float4(otherwise, otherwise, otherwise, otherwise);
-            const float4 v = reinterpret_cast<const float4 *>(w)[i];
-            return make_float4(v.x + more, v.y + more, v.z + more, v.w + more);
-        };
-        smem[to] = four(p.pre, 0.0f, p.one);
-        smem[2 * groups + to] = four(p.post, 1.0f, p.one);
-        smem[4 * groups + to] = four(channel ? p.gate : nullptr, 1.0f, 0.0f);
-    }
-    auto weights = [&](int which, int i, float (&w)[8]) {
-        const int g = me + i * p.team;
-        const float4 *at = smem + 2 * which * groups + (g < groups ? g : 0);  // (values beyond H are zeros)
-        const float4 a = at[0], b = at[groups];
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-    };
+    const bool token = p.gate_kind == MOE_GATE_TOKEN;
+    const int groups = H / 8, stages = p.stages;
+    const Weights weights{smem, groups};
+    const Ring<TX, TF, V> ring{smem_u32(smem) + (p.weights_in_smem ? (CHANNEL ? 3u : 2u) * H * 4 : 0u) + threadIdx.x * 16u};
+    for (int i = threadIdx.x; i < kBackwardThreads / 32 * kSlots; i += blockDim.x) slots[i] = 0.0f;
+    int group[V];
     bool in[V];
-    float d_pre[V][8], d_post[V][8], d_gate[V][8];
+    f2 d_pre[V][4], d_post[V][4], d_gate[CHANNEL ? V : 1][4];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         in[i] = 8 * (me + i * p.team) < H;
+        group[i] = in[i] ? me + i * p.team : 0;  // (the values beyond H are zeros)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d_pre[i][j] = d_post[i][j] = d_gate[i][j] = 0.0f;
+        for (int j = 0; j < 4; ++j) {
+            d_pre[i][j] = d_post[i][j] = 0;
+            if (CHANNEL) d_gate[i][j] = 0;
+        }
+    }
+    auto ask = [&](int row, int stage) {
+        if (row < p.T) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const size_t at = (size_t)row * H + 8 * group[i];
+                constexpr int kX = Ring<TX, TF, V>::kX, kF = Ring<TX, TF, V>::kF;
+                ring.template ask<TX>(stage, i * kX, has_pre ? p.x : p.xo, at, in[i] && has_pre);
+                ring.template ask<TF>(stage, V * kX + i * kF, has_pre ? p.dn : p.xo, at, in[i] && has_pre);
+                ring.template ask<TF>(stage, V * (kX + kF) + i * kF, has_f ? p.f : p.xo, at, in[i] && has_f);
+                ring.template ask<TX>(stage, V * (kX + 2 * kF) + i * kX, p.dx != nullptr ? p.dx : p.xo, at, in[i] && p.dx != nullptr);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto weight = [&](int which, int i, f2 (&w)[4]) {
+        if (p.weights_in_smem) {
+            weights.get(which, group[i], w);
+        } else {
+            const float *from = which == 0 ? p.pre : which == 1 ? p.post : CHANNEL ? p.gate : nullptr;
+            const float otherwise = which == 0 ? 0.0f : 1.0f, more = which == 2 ? 0.0f : p.one;
+            const float4 a = four_of(from, 2 * group[i], otherwise, more), b = four_of(from, 2 * group[i] + 1, otherwise, more);
+            w[0] = make2(a.x, a.y), w[1] = make2(a.z, a.w), w[2] = make2(b.x, b.y), w[3] = make2(b.z, b.w);
+        }
+    };
+    pdl_wait();
+    pdl_trigger();
+    int row = blockIdx.x * (blockDim.x / p.team) + team.id, stage = 0;
+    for (int s = 0; s + 1 < stages; ++s) ask(row + s * stride, s);
+    if (p.weights_in_smem) {
+        weights.fill(0, [&](int i) { return four_of(p.pre, i, 0.0f, p.one); });
+        weights.fill(1, [&](int i) { return four_of(p.post, i, 1.0f, p.one); });
+        if (CHANNEL) weights.fill(2, [&](int i) { return four_of(p.gate, i, 1.0f, 0.0f); });
     }
     __syncthreads();
 
-    int row = blockIdx.x * (blockDim.x / p.team) + team.id;
-    for (; row < p.T; row += stride) {
-        Raw<TX> xr[V], dxr[V];
-        Raw<TF> fr[V], dnr[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const size_t at = (size_t)row * H + 8 * (me + i * p.team);
-            xr[i].zero(), dxr[i].zero(), fr[i].zero(), dnr[i].zero();
-            if (in[i] && has_pre) xr[i].load(static_cast<const TX *>(p.x) + at), dnr[i].load(static_cast<const TF *>(p.dn) + at);
-            if (in[i] && has_f) fr[i].load(static_cast<const TF *>(p.f) + at);
-            if (in[i] && p.dx != nullptr) dxr[i].load(static_cast<const TX *>(p.dx) + at);
-        }
-        const float g = token ? p.gate[row] : 1.0f;
-        float w[8], a[8], b[8];
-        // the squares of X' and F, and dN w_pre X'
-        float sx = 1.0f, sf = 1.0f, s[3];
-        auto sums = [&]() {
-            s[0] = s[1] = s[2] = 0.0f;
+    for (; row < p.T; row += stride, stage = stage + 1 == stages ? 0 : stage + 1) {
+        // the row that the stage freed by the last one is for, then wait for this one's
+        const int ahead = stages - 1, to = stage == 0 ? ahead : stage - 1;
+        ask(row + ahead * stride, to);
+        if (ahead == 0)
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        else if (ahead == 1)
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else
+            asm volatile("cp.async.wait_group 2;" ::: "memory");
+        const size_t base = (size_t)row * H;
+        // What is not there is zeros or ones, so that the values take no branches.
+        const float g = token ? p.gate[row] : 1.0f, alpha = has_f ? p.alpha : 1.0f;
+        f2 w[4], a[4], b[4];
+        // the squares of X' and F, and dN w_pre X'; of values scaled down where that is not enough
+        float sx = 1.0f, sf = 1.0f, s0, s1, s2;
+        auto sums = [&](bool scaled) {
+            f2 xx = 0, ff = 0, dx = 0;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                if (has_pre) {
-                    weights(0, i, w);
-                    xr[i].get(a);
-                    dnr[i].get(b);
+                weight(0, i, w);
+                ring.x(stage, i, a);
+                ring.dn(stage, i, b);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float x = a[j] * sx;
-                        s[0] = fmaf(x, x, s[0]);
-                        s[2] = fmaf(b[j] * w[j], x, s[2]);
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    if (scaled) a[j] = mul2(a[j], both(sx));
+                    xx = fma2(a[j], a[j], xx);
+                    dx = fma2(mul2(b[j], w[j]), a[j], dx);
                 }
-                if (has_post) {
-                    fr[i].get(a);
+                ring.f(stage, i, a);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) s[1] = fmaf(a[j] * sf, a[j] * sf, s[1]);
+                for (int j = 0; j < 4; ++j) {
+                    if (scaled) a[j] = mul2(a[j], both(sf));
+                    ff = fma2(a[j], a[j], ff);
                 }
             }
-            team.sum(s);
+            s0 = sum_of(xx), s1 = sum_of(ff), s2 = sum_of(dx);
+            team.sum(s0, s1, s2);
         };
-        sums();
-        if (!(s[0] < INFINITY) || !(s[1] < INFINITY)) {
-            if (!(s[0] < INFINITY)) sx = kDown;
-            if (!(s[1] < INFINITY)) sf = kDown;
-            sums();
+        sums(false);
+        if (!(s0 < INFINITY) || !(s1 < INFINITY)) {
+            if (!(s0 < INFINITY)) sx = kDown;
+            if (!(s1 < INFINITY)) sf = kDown;
+            sums(true);
         }
-        const float rxs = inverse_root(s[0], inv_h, p.eps * sx * sx), rx = rxs * sx, mean = rxs * s[2] * inv_h;
-        const float rf = has_post ? inverse_root(s[1], inv_h, p.eps * sf * sf) * sf : 1.0f;
-        float t[V][8], m[1] = {0.0f};
+        const float rxs = inverse_root(s0, inv_h, p.eps * sx * sx), rx = rxs * sx, mean = rxs * s2 * inv_h;
+        const float rf = has_post ? inverse_root(s1, inv_h, p.eps * sf * sf) * sf : 1.0f;
+        f2 t[V][4], m = 0;  // t: T, then T (times the channel's gate) times w_post
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            dxr[i].get(t[i]);
-            if (has_pre) {
-                weights(0, i, w);
-                xr[i].get(a);
-                dnr[i].get(b);
+            weight(0, i, w);
+            ring.x(stage, i, a);
+            ring.dn(stage, i, b);
+            ring.dx(stage, i, t[i]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float xh = a[j] * rx;
-                    d_pre[i][j] = fmaf(b[j], xh, d_pre[i][j]);
-                    t[i][j] = fmaf(rx, fmaf(-xh, mean, b[j] * w[j]), t[i][j]);
-                }
+            for (int j = 0; j < 4; ++j) {
+                const f2 xh = mul2(a[j], both(rx));
+                d_pre[i][j] = fma2(b[j], xh, d_pre[i][j]);
+                t[i][j] = fma2(both(rx), fma2(xh, both(-mean), mul2(b[j], w[j])), t[i][j]);
+                w[j] = mul2(both(alpha), t[i][j]);
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) a[j] = has_f ? p.alpha * t[i][j] : t[i][j];
-            if (in[i]) Raw<TX>::store(static_cast<TX *>(p.xo) + (size_t)row * H + 8 * (me + i * p.team), a);
+            if (in[i]) Raw<TX>::store(p.xo, base + 8 * group[i], w);
             if (!has_f) continue;
-            fr[i].get(a);
-            weights(1, i, w);
-            if (channel) {  // from here t is T times the gate
-                weights(2, i, b);
+            weight(1, i, w);
+            ring.f(stage, i, a);
+            if (CHANNEL) weight(2, i, b);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    d_gate[i][j] = fmaf(t[i][j], a[j] * rf * w[j], d_gate[i][j]);
-                    t[i][j] *= b[j];
+            for (int j = 0; j < 4; ++j) {
+                const f2 fh = mul2(a[j], both(rf));
+                if (CHANNEL) {
+                    d_gate[i][j] = fma2(mul2(t[i][j], fh), w[j], d_gate[i][j]);
+                    t[i][j] = mul2(t[i][j], b[j]);
+                    d_post[i][j] = fma2(t[i][j], fh, d_post[i][j]);
+                } else {
+                    d_post[i][j] = fma2(mul2(t[i][j], fh), both(g), d_post[i][j]);
                 }
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float fh = a[j] * rf;
-                m[0] = fmaf(t[i][j] * w[j], fh, m[0]);
-                t[i][j] *= g;
-                d_post[i][j] = fmaf(t[i][j], fh, d_post[i][j]);
+                t[i][j] = mul2(t[i][j], w[j]);
+                m = fma2(t[i][j], fh, m);
             }
         }
         if (!has_f) continue;
-        float mean_f = 0.0f;
-        if (has_post || token) {
-            team.sum(m);
-            if (token && me == 0 && p.dgate != nullptr) p.dgate[row] = m[0];
-            mean_f = has_post ? g * m[0] * inv_h : 0.0f;
-        }
+        float total = sum_of(m);
+        if (has_post || token) team.sum(total);
+        if (token && me == 0 && p.dgate != nullptr) p.dgate[row] = total;
+        // dF = g rf (T w_post - fh mean(T w_post fh)), or g T
+        const float out = g * rf, back = -total * inv_h * rf;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            fr[i].get(a);
-            weights(1, i, w);
+            if (has_post) ring.f(stage, i, a);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a[j] = rf * (has_post ? fmaf(-a[j] * rf, mean_f, t[i][j] * w[j]) : t[i][j]);
-            if (in[i]) Raw<TF>::store(static_cast<TF *>(p.fo) + (size_t)row * H + 8 * (me + i * p.team), a);
+            for (int j = 0; j < 4; ++j) w[j] = mul2(both(out), has_post ? fma2(a[j], both(back), t[i][j]) : t[i][j]);
+            if (in[i]) Raw<TF>::store(p.fo, base + 8 * group[i], w);
         }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 
     // the teams' sums one after the other, then this CTA's
     const int teams = blockDim.x / p.team;
@@ -382,16 +548,17 @@ __global__ void __launch_bounds__(kBackwardThreads<TX, TF>, 1) norm_backward_ker
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 if (!in[i]) continue;
-                auto add = [&](float4 *at, const float *d) {
+                auto add = [&](float4 *at, f2 lo, f2 hi) {
+                    const float2 a = split(lo), b = split(hi);
                     const float4 v = k ? *at : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    *at = make_float4(v.x + d[0], v.y + d[1], v.z + d[2], v.w + d[3]);
+                    *at = make_float4(v.x + a.x, v.y + a.y, v.z + b.x, v.w + b.y);
                 };
-                float4 *at = smem + me + i * p.team;
+                float4 *at = smem + group[i];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    add(at + h * groups, d_pre[i] + 4 * h);
-                    add(at + (2 + h) * groups, d_post[i] + 4 * h);
-                    if (channel) add(at + (4 + h) * groups, d_gate[i] + 4 * h);
+                    add(at + h * groups, d_pre[i][2 * h], d_pre[i][2 * h + 1]);
+                    add(at + (2 + h) * groups, d_post[i][2 * h], d_post[i][2 * h + 1]);
+                    if (CHANNEL) add(at + (4 + h) * groups, d_gate[i][2 * h], d_gate[i][2 * h + 1]);
                 }
             }
         }
@@ -402,7 +569,7 @@ __global__ void __launch_bounds__(kBackwardThreads<TX, TF>, 1) norm_backward_ker
         const int from = (i & 1) * groups + i / 2;
         mine[i] = smem[from];
         mine[2 * groups + i] = smem[2 * groups + from];
-        if (channel) mine[4 * groups + i] = smem[4 * groups + from];
+        if (CHANNEL) mine[4 * groups + i] = smem[4 * groups + from];
     }
 }
 
@@ -429,20 +596,13 @@ __global__ void __launch_bounds__(32 * kSumRows) norm_sum_kernel(const float *pa
     out[col] = v;
 }
 
-OpDone g_attr[8];
-
-int groups_of(int H, int threads) { return H > 8 * threads ? 2 : 1; }
-int backward_threads(int x_dtype, int f_dtype) {
-    if (x_dtype == MOE_DTYPE_F32 && f_dtype == MOE_DTYPE_F32) return kBackwardThreads<float, float>;
-    return x_dtype == f_dtype ? kBackwardThreads<bf16, bf16> : kBackwardThreads<float, bf16>;
-}
+OpDone g_attr[24];
 
 // Teams of several warps have a named barrier each, of 15.
 int most_teams(int team) { return team > 32 ? 15 : kMaxTeams; }
 
 // Threads per team and teams per CTA: as many as fit, fewer where rows would leave SMs without one.
-void shape(int T, int H, int sms, int threads, int &team, int &teams) {
-    const int per = 8 * groups_of(H, threads);
+void shape(int T, int H, int sms, int threads, int per, int &team, int &teams) {
     team = 32 * ((H + 32 * per - 1) / (32 * per));
     teams = std::max(1, std::min(std::min(threads / team, most_teams(team)), (T + sms - 1) / sms));
 }
@@ -485,30 +645,49 @@ bool aligned(std::initializer_list<const void *> all) {
     return std::all_of(all.begin(), all.end(), [](const void *p) { return op_aligned16(p); });
 }
 
-// fn(kernel) for the types and the groups per thread
-template <template <typename, typename, int> class Kernel, typename Fn>
-cudaError_t pick(int x_dtype, int f_dtype, int groups, Fn fn) {
-    const int which = (x_dtype == MOE_DTYPE_F32) * 4 + (f_dtype == MOE_DTYPE_F32) * 2 + (groups - 1);
-    switch (which) {
-    case 0: return fn(Kernel<bf16, bf16, 1>::get(), which);
-    case 1: return fn(Kernel<bf16, bf16, 2>::get(), which);
-    case 2: return fn(Kernel<bf16, float, 1>::get(), which);
-    case 3: return fn(Kernel<bf16, float, 2>::get(), which);
-    case 4: return fn(Kernel<float, bf16, 1>::get(), which);
-    case 5: return fn(Kernel<float, bf16, 2>::get(), which);
-    case 6: return fn(Kernel<float, float, 1>::get(), which);
-    default: return fn(Kernel<float, float, 2>::get(), which);
-    }
-}
 using KernelFn = void (*)(const SandwichArgs);
-template <typename TX, typename TF, int V>
-struct Forward {
-    static KernelFn get() { return norm_forward_kernel<TX, TF, V>; }
+struct Choice {
+    KernelFn kernel;
+    int threads, per, stage_bytes, which;  // per: values of a thread; stage_bytes: of a CTA's row in flight
 };
-template <typename TX, typename TF, int V>
-struct Backward {
-    static KernelFn get() { return norm_backward_kernel<TX, TF, V>; }
-};
+// Backward: 16 values per thread where rows are long enough for teams of several warps then: the
+// sums over a team cost each warp as much as 4 values per lane.
+template <typename TX, typename TF>
+Choice choose(bool backward, bool channel, int H, int which) {
+    if (!backward) {
+        constexpr int kThreads = kForwardThreads<TX, TF>;
+        if constexpr (8 * kThreads < kMaxH) {
+            if (H > 8 * kThreads) return {norm_forward_kernel<TX, TF, 2>, kThreads, 16, 0, which * 6 + 1};
+        }
+        return {norm_forward_kernel<TX, TF, 1>, kThreads, 8, 0, which * 6};
+    }
+    const bool two = H > 1024;
+    const int bytes = kBackwardThreads * (two ? 16 : 8) * 2 * (int)(sizeof(TX) + sizeof(TF));
+    if (two) return {channel ? norm_backward_kernel<TX, TF, 2, true> : norm_backward_kernel<TX, TF, 2, false>, kBackwardThreads, 16, bytes, which * 6 + 2 + channel};
+    return {channel ? norm_backward_kernel<TX, TF, 1, true> : norm_backward_kernel<TX, TF, 1, false>, kBackwardThreads, 8, bytes, which * 6 + 4 + channel};
+}
+Choice choose(int x_dtype, int f_dtype, bool backward, int gate_kind, int H) {
+    const bool channel = gate_kind == MOE_GATE_CHANNEL;
+    if (x_dtype == MOE_DTYPE_BF16)
+        return f_dtype == MOE_DTYPE_BF16 ? choose<bf16, bf16>(backward, channel, H, 0) : choose<bf16, float>(backward, channel, H, 1);
+    return f_dtype == MOE_DTYPE_BF16 ? choose<float, bf16>(backward, channel, H, 2) : choose<float, float>(backward, channel, H, 3);
+}
+
+moe_status launch(const char *name, bool backward, SandwichArgs &a, int x_dtype, int f_dtype, int sms, int &grid, cudaStream_t s) {
+    const Choice c = choose(x_dtype, f_dtype, backward, a.gate_kind, a.H);
+    int teams, smem = 2 * a.H * 4;
+    shape(a.T, a.H, sms, c.threads, c.per, a.team, teams);
+    grid = (int)std::min<long long>(std::min(sms, kMaxCtas), ((long long)a.T + teams - 1) / teams);
+    if (backward) {
+        const int weights = (a.gate_kind == MOE_GATE_CHANNEL ? 3 : 2) * a.H * 4;
+        a.weights_in_smem = weights + c.stage_bytes <= kBackwardSmem;
+        a.stages = std::min(3, (kBackwardSmem - (a.weights_in_smem ? weights : 0)) / c.stage_bytes);
+        smem = std::max(weights, (a.weights_in_smem ? weights : 0) + a.stages * c.stage_bytes);
+    }
+    const cudaError_t e = op_allow_smem(reinterpret_cast<const void *>(c.kernel), backward ? kBackwardSmem : 2 * kMaxH * 4, &g_attr[c.which]);
+    if (e != cudaSuccess) return op_cuda(e, name);
+    return op_cuda(launch_pdl(c.kernel, dim3(grid), dim3(a.team * teams), (size_t)smem, s, a), name);
+}
 
 size_t workspace_of(int T, int H) { return (size_t)std::max(1, std::min(T, kMaxCtas)) * 3 * H * sizeof(float); }
 
@@ -538,12 +717,8 @@ extern "C" moe_status moe_sandwich_norm(const void *X, const void *F, const floa
     a.x = X, a.f = F, a.pre = pre_w, a.post = post_w, a.gate = gate, a.xo = X_out, a.fo = N;
     a.alpha = residual_scale, a.eps = eps, a.one = kind == MOE_NORM_GEMMA ? 1.0f : 0.0f;
     a.T = T, a.H = H, a.gate_kind = gate_kind;
-    int teams;
-    shape(T, H, sms, kForwardThreads, a.team, teams);
-    const unsigned grid = (unsigned)std::min<long long>(sms, ((long long)T + teams - 1) / teams);
-    return op_cuda(pick<Forward>(x_dtype, f_dtype, groups_of(H, kForwardThreads), [&](KernelFn k, int) {
-                       return launch_pdl(k, dim3(grid), dim3(a.team * teams), 0, reinterpret_cast<cudaStream_t>(stream), a);
-                   }), name);
+    int grid;
+    return launch(name, false, a, x_dtype, f_dtype, sms, grid, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" moe_status moe_sandwich_norm_workspace(int T, int H, size_t *bytes) {
@@ -591,15 +766,8 @@ extern "C" moe_status moe_sandwich_norm_backward(const void *dX_out, const void 
         a.xo = dX, a.fo = dF, a.dgate = dgate, a.partial = static_cast<float *>(workspace);
         a.alpha = residual_scale, a.eps = eps, a.one = kind == MOE_NORM_GEMMA ? 1.0f : 0.0f;
         a.T = T, a.H = H, a.gate_kind = gate_kind;
-        const int threads = backward_threads(x_dtype, f_dtype);
-        int teams;
-        shape(T, H, sms, threads, a.team, teams);
-        grid = (int)std::min<long long>(std::min(sms, kMaxCtas), ((long long)T + teams - 1) / teams);
-        const cudaError_t e = pick<Backward>(x_dtype, f_dtype, groups_of(H, threads), [&](KernelFn k, int which) {
-            const cudaError_t ce = op_allow_smem(reinterpret_cast<const void *>(k), 3 * kMaxH * 4, &g_attr[which]);
-            return ce != cudaSuccess ? ce : launch_pdl(k, dim3(grid), dim3(a.team * teams), 3ull * H * 4, s, a);
-        });
-        if (e != cudaSuccess) return op_cuda(e, name);
+        st = launch(name, true, a, x_dtype, f_dtype, sms, grid, s);
+        if (st != MOE_OK) return st;
     }
     float *d_gate = gate_kind == MOE_GATE_CHANNEL ? dgate : nullptr;
     if (!dpre_w && !dpost_w && !d_gate) return MOE_OK;
