@@ -28,15 +28,13 @@ namespace moe {
 namespace {
 
 constexpr int kMaxH = 8192;
-// Threads of a CTA (one per SM): as many as have registers for the values of a row, and backward
-// for a thread's sums.
-template <typename TX, typename TF>
-constexpr int kForwardThreads = sizeof(TX) + sizeof(TF) == 8 ? 768 : 1024;
-constexpr int kBackwardThreads = 512;
-constexpr int kBackwardSmem = 212 << 10;  // dynamic shared memory, most
-constexpr int kMaxTeams = 1024 / 32;
+constexpr int kThreads = 512;      // of a CTA, one per SM
+constexpr int kMaxTeams = kThreads / 32;
+constexpr int kSmem = 212 << 10;   // dynamic shared memory, most
 constexpr int kMaxCtas = 256;
 constexpr float kDown = 0x1p-100f;
+constexpr int kMaxStages = 4;
+constexpr uint64_t kWaitNs = 2000000000ull;  // bound of the wait for a row
 
 struct SandwichArgs {
     const void *x, *f;
@@ -47,8 +45,9 @@ struct SandwichArgs {
     float *partial;       // backward: [grid][3][H]
     float alpha, eps, one;  // one: added to the weights
     int T, H, gate_kind, team;  // team: threads
-    int stages;                 // backward: rows in flight, 1 to 3, the present one among them
-    bool weights_in_smem;
+    int *err;
+    int stages;             // rows in flight, the present one among them
+    bool weights_in_smem;   // backward
 };
 
 // Two fp32 values in one 64-bit register, and arithmetic on both in one instruction: half the
@@ -85,48 +84,21 @@ __device__ __forceinline__ float sum_of(f2 v) {
     return s.x + s.y;
 }
 
-// 8 consecutive values as loaded, and as pairs of fp32.
-template <typename T>
-struct Raw;
-template <>
-struct Raw<bf16> {
-    uint4 v;
-    __device__ __forceinline__ void load(const void *p, size_t at, bool in) {
-        v = in ? *reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(p) + at) : make_uint4(0, 0, 0, 0);
-    }
-    __device__ __forceinline__ f2 get(int i) const {
-        const uint32_t w = (&v.x)[i];
-        return make2(bf16_lo(w), bf16_hi(w));
-    }
-    static __device__ __forceinline__ void store(void *p, size_t at, const f2 (&o)[4]) {
-        uint32_t w[4];
+// 8 consecutive values to memory.
+__device__ __forceinline__ void store8(bf16 *p, const f2 (&o)[4]) {
+    uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 s = split(o[i]);
-            w[i] = pack_bf16x2(s.x, s.y);
-        }
-        *reinterpret_cast<uint4 *>(static_cast<bf16 *>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 4; ++i) {
+        const float2 s = split(o[i]);
+        w[i] = pack_bf16x2(s.x, s.y);
     }
-};
-template <>
-struct Raw<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const void *p, size_t at, bool in) {
-        const float4 *f = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
-        a = in ? f[0] : make_float4(0.f, 0.f, 0.f, 0.f);
-        b = in ? f[1] : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    __device__ __forceinline__ f2 get(int i) const {
-        const float4 &h = i < 2 ? a : b;
-        return i % 2 ? make2(h.z, h.w) : make2(h.x, h.y);
-    }
-    static __device__ __forceinline__ void store(void *p, size_t at, const f2 (&o)[4]) {
-        const float2 w = split(o[0]), x = split(o[1]), y = split(o[2]), z = split(o[3]);
-        float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
-        f[0] = make_float4(w.x, w.y, x.x, x.y);
-        f[1] = make_float4(y.x, y.y, z.x, z.y);
-    }
-};
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(float *p, const f2 (&o)[4]) {
+    const float2 w = split(o[0]), x = split(o[1]), y = split(o[2]), z = split(o[3]);
+    reinterpret_cast<float4 *>(p)[0] = make_float4(w.x, w.y, x.x, x.y);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(y.x, y.y, z.x, z.y);
+}
 
 // Sums over a team, in all its threads.  slots: [2][3][32], zeros where there is no warp; two sums
 // in a row use different halves, so one barrier each is enough: who writes a half again has passed
@@ -145,7 +117,12 @@ struct Team {
         slots = all + id * kSlots;
         half = 0;
     }
-    __device__ __forceinline__ void sync() const { asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory"); }
+    __device__ __forceinline__ void sync() const {
+        if (warps == 1)
+            __syncwarp();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
+    }
     __device__ __forceinline__ float over_warps(const float *s) const {
         f2 a = 0, b = 0;
         for (int w = 0; w < warps; w += 4) {
@@ -158,7 +135,10 @@ struct Team {
     __device__ __forceinline__ void sum(float &v) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (warps == 1) return;
+        if (warps == 1) {
+            __syncwarp();  // as the barrier does, this orders what was read before
+            return;
+        }
         float *s = slots + half * 96;
         half ^= 1;
         if (lane == 0) s[warp] = v;
@@ -213,216 +193,236 @@ __device__ __forceinline__ float4 four_of(const float *w, int i, float otherwise
     return make_float4(v.x + more, v.y + more, v.z + more, v.w + more);
 }
 
+// A team's next rows, in shared memory: a row's tensors one after the other, by one bulk copy each
+// that a thread of the team starts, `stages` rows at most (the present one among them).  (Copies by
+// every thread for itself, 16 bytes at a time, took instructions, and half of each sector of fp32
+// rows twice: 8192 rows with an fp32 stream 46 us.)
+struct Ring {
+    uint32_t rows, bars;  // the team's: stage 0, and its barrier (8 bytes per stage)
+    uint32_t bytes;       // of a stage
+    int stages, stage;
+    uint32_t parity;      // of the present stage's barrier
+    __device__ __forceinline__ void init() const {
+        for (int s = 0; s < stages; ++s) mbar_init(bars + 8 * s, 1);
+    }
+    __device__ __forceinline__ void next() {
+        if (++stage == stages) {
+            stage = 0;
+            parity ^= 1u;
+        }
+    }
+    // Bounded: after it a row's values are whatever is there, the error is recorded, and no later
+    // wait of the CTA takes time.
+    __device__ __forceinline__ void wait(volatile int *abort, int *err) const {
+        if (mbar_wait(bars + 8 * stage, parity, kWaitNs, abort)) return;
+        *abort = 1;
+        atomicOr(err, ERR_TIMEOUT);
+    }
+    __device__ __forceinline__ uint32_t present() const { return rows + stage * bytes; }
+    // 8 values in shared memory
+    template <typename T>
+    static __device__ __forceinline__ void get(uint32_t at, f2 (&o)[4]) {
+        auto load = [&](uint32_t from) {
+            uint4 v;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from) : "memory");
+            return v;
+        };
+        if constexpr (sizeof(T) == 2) {
+            const uint4 v = load(at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = make2(bf16_lo((&v.x)[i]), bf16_hi((&v.x)[i]));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint4 v = load(at + 16 * k);
+                o[2 * k] = make2(__uint_as_float(v.x), __uint_as_float(v.y));
+                o[2 * k + 1] = make2(__uint_as_float(v.z), __uint_as_float(v.w));
+            }
+        }
+    }
+};
+
+// What both kernels set up.  `weight_arrays`: those in front of the rings in dynamic shared memory.
+struct Shared {
+    float slots[kMaxTeams * kSlots];
+    uint64_t bars[kMaxTeams * kMaxStages];
+    uint4 zeros[2];  // what lanes beyond H read
+    int abort;
+};
+__device__ __forceinline__ Ring make_ring(Shared &sh, const Team &team, uint32_t rings, uint32_t row_bytes, int stages) {
+    Ring r;
+    r.rows = rings + team.id * stages * row_bytes;
+    r.bars = smem_u32(sh.bars + team.id * kMaxStages);
+    r.bytes = row_bytes;
+    r.stages = stages;
+    r.stage = 0;
+    r.parity = 0;
+    for (int i = threadIdx.x; i < kMaxTeams * kSlots; i += blockDim.x) sh.slots[i] = 0.0f;
+    if (threadIdx.x == 0) {
+        sh.abort = 0;
+        sh.zeros[0] = sh.zeros[1] = make_uint4(0, 0, 0, 0);
+    }
+    if ((int)threadIdx.x == team.id * team.threads) {
+        r.init();
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    return r;
+}
+// The rows are waited for one by one, so that only after an abort a copy may be in flight: it is given a fixed time.
+__device__ __forceinline__ void leave(Shared &sh) {
+    __syncthreads();
+    if (*(volatile int *)&sh.abort) {
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000ull) __nanosleep(1000);
+    }
+}
+
 // V: groups of 8 values per thread, `team` threads apart.
 template <typename TX, typename TF, int V>
-__global__ void __launch_bounds__(kForwardThreads<TX, TF>, 1) norm_forward_kernel(const SandwichArgs p) {
-    extern __shared__ float4 smem[];
-    __shared__ __align__(16) float slots[kMaxTeams * kSlots];
-    Team team(slots, p.team);
+__global__ void __launch_bounds__(kThreads, 1) norm_forward_kernel(const SandwichArgs p) {
+    extern __shared__ float4 smem[];  // the effective weights, the rings
+    __shared__ __align__(16) Shared sh;
+    Team team(sh.slots, p.team);
     const int me = threadIdx.x - team.id * p.team, H = p.H;
     const int stride = gridDim.x * (blockDim.x / p.team);
     const float inv_h = 1.0f / H;
     const bool has_f = p.f != nullptr, has_pre = p.pre != nullptr, has_post = p.post != nullptr;
     const bool channel = p.gate_kind == MOE_GATE_CHANNEL, token = p.gate_kind == MOE_GATE_TOKEN;
     const Weights weights{smem, H / 8};
-    for (int i = threadIdx.x; i < kMaxTeams * kSlots; i += blockDim.x) slots[i] = 0.0f;
-    pdl_wait();
-    pdl_trigger();
-    weights.fill(0, [&](int i) { return four_of(p.pre, i, 0.0f, p.one); });
-    weights.fill(1, [&](int i) {  // the channels' gate is one more factor of the weight
-        const float4 w = four_of(p.post, i, 1.0f, p.one), g = four_of(channel ? p.gate : nullptr, i, 1.0f, 0.0f);
-        return make_float4(w.x * g.x, w.y * g.y, w.z * g.z, w.w * g.w);
-    });
+    const uint32_t x_bytes = H * sizeof(TX), f_bytes = H * sizeof(TF), row_bytes = x_bytes + f_bytes;
+    Ring ring = make_ring(sh, team, smem_u32(smem) + 2u * H * 4, row_bytes, p.stages);
+    auto ask = [&](int row, int s) {  // by the team's first thread
+        if (row >= p.T) return;
+        const uint32_t to = ring.rows + s * row_bytes, bar = ring.bars + 8 * s;
+        mbar_arrive_expect_tx(bar, has_f ? row_bytes : x_bytes);
+        bulk_g2s(to, static_cast<const TX *>(p.x) + (size_t)row * H, x_bytes, bar);
+        if (has_f) bulk_g2s(to + x_bytes, static_cast<const TF *>(p.f) + (size_t)row * H, f_bytes, bar);
+    };
+    const uint32_t zeros = smem_u32(sh.zeros);
     int group[V];
     bool in[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         in[i] = 8 * (me + i * p.team) < H;
-        group[i] = in[i] ? me + i * p.team : 0;  // (the values beyond H are zeros)
+        group[i] = in[i] ? me + i * p.team : 0;
     }
-    Raw<TX> xr[V];
-    Raw<TF> fr[V];
-    float gate = 1.0f;
-    auto fetch = [&](int row) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const size_t at = (size_t)row * H + 8 * group[i];
-            xr[i].load(p.x, at, in[i]);
-            if (has_f) fr[i].load(p.f, at, in[i]);
-        }
-        if (token) gate = p.gate[row];
-    };
+    pdl_wait();
+    pdl_trigger();
     int row = blockIdx.x * (blockDim.x / p.team) + team.id;
-    if (row < p.T) fetch(row);
+    if (me == 0)
+        for (int s = 0; s < p.stages; ++s) ask(row + s * stride, s);
+    weights.fill(0, [&](int i) { return four_of(p.pre, i, 0.0f, p.one); });
+    weights.fill(1, [&](int i) {  // the channels' gate is one more factor of the weight
+        const float4 w = four_of(p.post, i, 1.0f, p.one), g = four_of(channel ? p.gate : nullptr, i, 1.0f, 0.0f);
+        return make_float4(w.x * g.x, w.y * g.y, w.z * g.z, w.w * g.w);
+    });
+    float gate_next = token && row < p.T ? p.gate[row] : 1.0f;
     __syncthreads();
-    for (; row < p.T; row += stride) {
-        f2 x[V][4], w[4];
+    for (; row < p.T; row += stride, ring.next()) {
+        const float gate = gate_next;
+        if (token && row + stride < p.T) gate_next = p.gate[row + stride];
+        ring.wait(&sh.abort, p.err);
+        const size_t base = (size_t)row * H;
+        f2 x[V][4], f[V][4], w[4];
+        auto squares = [&](const f2 (&v)[V][4], float scale) {  // (zeros beyond H, unless the row has no norm)
+            f2 s = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+            for (int i = 0; i < V; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[i][j] = xr[i].get(j);
-        if (has_f) {
-            float rf = 1.0f;
-            if (has_post) {
-                auto squares = [&](float scale) {
-                    f2 s = 0;
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            f2 f = fr[i].get(j);
-                            if (scale != 1.0f) f = mul2(f, both(scale));
-                            s = fma2(f, f, s);
-                        }
-                    float total = sum_of(s);
-                    team.sum(total);
-                    return total;
-                };
-                float ss = squares(1.0f);
-                rf = inverse_root(ss, inv_h, p.eps);
-                if (!(ss < INFINITY)) {
-                    ss = squares(kDown);
-                    rf = inverse_root(ss, inv_h, p.eps * kDown * kDown) * kDown;
+                for (int j = 0; j < 4; ++j) {
+                    const f2 a = scale != 1.0f ? mul2(v[i][j], both(scale)) : v[i][j];
+                    s = fma2(a, a, s);
                 }
+            float total = sum_of(s);
+            team.sum(total);
+            return total;
+        };
+        auto norm = [&](const f2 (&v)[V][4]) {
+            float ss = squares(v, 1.0f);
+            if (ss < INFINITY) return inverse_root(ss, inv_h, p.eps);
+            ss = squares(v, kDown);
+            return inverse_root(ss, inv_h, p.eps * kDown * kDown) * kDown;
+        };
+#pragma unroll
+        for (int i = 0; i < V; ++i) Ring::get<TX>(in[i] ? ring.present() + 8 * sizeof(TX) * group[i] : zeros, x[i]);
+        if (has_f) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) Ring::get<TF>(in[i] ? ring.present() + x_bytes + 8 * sizeof(TF) * group[i] : zeros, f[i]);
+        }
+        if (has_f) {
+            float rf = gate;
+            if (has_post) {
+                rf *= norm(f);
+                if (me == 0) ask(row + p.stages * stride, ring.stage);  // the team has read the row
             }
-            if (token) rf *= gate;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 weights.get(1, group[i], w);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const f2 branch = mul2(mul2(fr[i].get(j), both(rf)), w[j]);
-                    x[i][j] = fma2(both(p.alpha), x[i][j], branch);
-                }
+                for (int j = 0; j < 4; ++j) x[i][j] = fma2(both(p.alpha), x[i][j], mul2(mul2(f[i][j], both(rf)), w[j]));
+                if (in[i]) store8(static_cast<TX *>(p.xo) + base + 8 * group[i], x[i]);
             }
         }
-        const size_t base = (size_t)row * H;
-        if (row + stride < p.T) fetch(row + stride);
-        if (has_f) {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (in[i]) Raw<TX>::store(p.xo, base + 8 * group[i], x[i]);
-        }
+        if (!has_post && !has_pre) team.sync();
         if (has_pre) {
-            auto squares = [&](float scale) {
-                f2 s = 0;
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        f2 v = in[i] ? x[i][j] : 0ull;
-                        if (scale != 1.0f) v = mul2(v, both(scale));
-                        s = fma2(v, v, s);
-                    }
-                float total = sum_of(s);
-                team.sum(total);
-                return total;
-            };
-            float ss = squares(1.0f);
-            float rx = inverse_root(ss, inv_h, p.eps);
-            if (!(ss < INFINITY)) {
-                ss = squares(kDown);
-                rx = inverse_root(ss, inv_h, p.eps * kDown * kDown) * kDown;
-            }
+            const float rx = norm(x);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 weights.get(0, group[i], w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) w[j] = mul2(mul2(x[i][j], both(rx)), w[j]);
-                if (in[i]) Raw<TF>::store(p.fo, base + 8 * group[i], w);
+                if (in[i]) store8(static_cast<TF *>(p.fo) + base + 8 * group[i], w);
             }
         }
+        if (!has_post && me == 0) ask(row + p.stages * stride, ring.stage);
     }
+    leave(sh);
 }
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {  // zeros where not `in`
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-
-// What a thread has in flight: its values of the next rows, in shared memory of its own, so that no
-// thread waits for another's copies.  A row's tensors are X', dN, F and dX' in pieces of 16 bytes.
-template <typename TX, typename TF, int V>
-struct Ring {
-    static constexpr int kX = sizeof(TX) / 2, kF = sizeof(TF) / 2;  // pieces of 8 values
-    static constexpr int kPieces = 2 * V * (kX + kF);
-    static constexpr int kPieceStep = kBackwardThreads * 16;
-    uint32_t mine;  // the thread's first piece of stage 0
-    __device__ __forceinline__ uint32_t piece(int stage, int k) const { return mine + (stage * kPieces + k) * kPieceStep; }
-    template <typename T>
-    __device__ __forceinline__ void ask(int stage, int first, const void *p, size_t at, bool in) const {
-        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(p) + at);
-#pragma unroll
-        for (int k = 0; k < (int)sizeof(T) / 2; ++k) copy16(piece(stage, first + k), src + k, in);
-    }
-    __device__ __forceinline__ uint4 load(int stage, int k) const {
-        uint4 v;
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(piece(stage, k)) : "memory");
-        return v;
-    }
-    template <typename T>
-    __device__ __forceinline__ void get(int stage, int first, f2 (&o)[4]) const {
-        if constexpr (sizeof(T) == 2) {
-            const uint4 v = load(stage, first);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = make2(bf16_lo((&v.x)[i]), bf16_hi((&v.x)[i]));
-        } else {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint4 v = load(stage, first + k);
-                o[2 * k] = make2(__uint_as_float(v.x), __uint_as_float(v.y));
-                o[2 * k + 1] = make2(__uint_as_float(v.z), __uint_as_float(v.w));
-            }
-        }
-    }
-    __device__ __forceinline__ void x(int s, int i, f2 (&o)[4]) const { get<TX>(s, i * kX, o); }
-    __device__ __forceinline__ void dn(int s, int i, f2 (&o)[4]) const { get<TF>(s, V * kX + i * kF, o); }
-    __device__ __forceinline__ void f(int s, int i, f2 (&o)[4]) const { get<TF>(s, V * (kX + kF) + i * kF, o); }
-    __device__ __forceinline__ void dx(int s, int i, f2 (&o)[4]) const { get<TX>(s, V * (kX + 2 * kF) + i * kX, o); }
-};
 
 // CHANNEL: the gate is one per channel.
 template <typename TX, typename TF, int V, bool CHANNEL>
-__global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_kernel(const SandwichArgs p) {
+__global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const SandwichArgs p) {
     // the effective weights and the channels' gate (where they fit), and the rings; later the teams' sums
     extern __shared__ float4 smem[];
-    __shared__ __align__(16) float slots[kBackwardThreads / 32 * kSlots];
-    Team team(slots, p.team);
+    __shared__ __align__(16) Shared sh;
+    Team team(sh.slots, p.team);
     const int me = threadIdx.x - team.id * p.team, H = p.H;
     const int stride = gridDim.x * (blockDim.x / p.team);
     const float inv_h = 1.0f / H;
     const bool has_f = p.f != nullptr, has_pre = p.pre != nullptr, has_post = p.post != nullptr;
     const bool token = p.gate_kind == MOE_GATE_TOKEN;
-    const int groups = H / 8, stages = p.stages;
+    const int groups = H / 8;
     const Weights weights{smem, groups};
-    const Ring<TX, TF, V> ring{smem_u32(smem) + (p.weights_in_smem ? (CHANNEL ? 3u : 2u) * H * 4 : 0u) + threadIdx.x * 16u};
-    for (int i = threadIdx.x; i < kBackwardThreads / 32 * kSlots; i += blockDim.x) slots[i] = 0.0f;
+    // X', dN, F, dX'
+    const uint32_t x_bytes = H * sizeof(TX), f_bytes = H * sizeof(TF), row_bytes = 2 * (x_bytes + f_bytes);
+    const uint32_t of_dn = x_bytes, of_f = x_bytes + f_bytes, of_dx = x_bytes + 2 * f_bytes;
+    Ring ring = make_ring(sh, team, smem_u32(smem) + (p.weights_in_smem ? (CHANNEL ? 3u : 2u) * H * 4 : 0u), row_bytes, p.stages);
+    auto ask = [&](int row, int s) {  // by the team's first thread
+        if (row >= p.T) return;
+        const uint32_t to = ring.rows + s * row_bytes, bar = ring.bars + 8 * s;
+        const size_t at = (size_t)row * H;
+        mbar_arrive_expect_tx(bar, (has_pre ? x_bytes + f_bytes : 0) + (has_f ? f_bytes : 0) + (p.dx != nullptr ? x_bytes : 0));
+        if (has_pre) {
+            bulk_g2s(to, static_cast<const TX *>(p.x) + at, x_bytes, bar);
+            bulk_g2s(to + of_dn, static_cast<const TF *>(p.dn) + at, f_bytes, bar);
+        }
+        if (has_f) bulk_g2s(to + of_f, static_cast<const TF *>(p.f) + at, f_bytes, bar);
+        if (p.dx != nullptr) bulk_g2s(to + of_dx, static_cast<const TX *>(p.dx) + at, x_bytes, bar);
+    };
+    const uint32_t zeros = smem_u32(sh.zeros);
     int group[V];
     bool in[V];
     f2 d_pre[V][4], d_post[V][4], d_gate[CHANNEL ? V : 1][4];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         in[i] = 8 * (me + i * p.team) < H;
-        group[i] = in[i] ? me + i * p.team : 0;  // (the values beyond H are zeros)
+        group[i] = in[i] ? me + i * p.team : 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             d_pre[i][j] = d_post[i][j] = 0;
             if (CHANNEL) d_gate[i][j] = 0;
         }
     }
-    auto ask = [&](int row, int stage) {
-        if (row < p.T) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const size_t at = (size_t)row * H + 8 * group[i];
-                constexpr int kX = Ring<TX, TF, V>::kX, kF = Ring<TX, TF, V>::kF;
-                ring.template ask<TX>(stage, i * kX, has_pre ? p.x : p.xo, at, in[i] && has_pre);
-                ring.template ask<TF>(stage, V * kX + i * kF, has_pre ? p.dn : p.xo, at, in[i] && has_pre);
-                ring.template ask<TF>(stage, V * (kX + kF) + i * kF, has_f ? p.f : p.xo, at, in[i] && has_f);
-                ring.template ask<TX>(stage, V * (kX + 2 * kF) + i * kX, p.dx != nullptr ? p.dx : p.xo, at, in[i] && p.dx != nullptr);
-            }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
     auto weight = [&](int which, int i, f2 (&w)[4]) {
         if (p.weights_in_smem) {
             weights.get(which, group[i], w);
@@ -435,29 +435,41 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_kernel(cons
     };
     pdl_wait();
     pdl_trigger();
-    int row = blockIdx.x * (blockDim.x / p.team) + team.id, stage = 0;
-    for (int s = 0; s + 1 < stages; ++s) ask(row + s * stride, s);
+    int row = blockIdx.x * (blockDim.x / p.team) + team.id;
+    // tensors that the call does not have are zeros in every stage
+    if (!has_pre || !has_f || p.dx == nullptr) {
+        for (uint32_t s = 0; s < p.stages * row_bytes; s += row_bytes)
+            for (uint32_t i = 16 * me; i < row_bytes; i += 16 * p.team) {
+                const bool here = i < of_f ? has_pre : i < of_dx ? has_f : p.dx != nullptr;
+                if (!here) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(ring.rows + s + i), "r"(0u) : "memory");
+            }
+    }
+    if (me == 0)
+        for (int s = 0; s < p.stages; ++s) ask(row + s * stride, s);
     if (p.weights_in_smem) {
         weights.fill(0, [&](int i) { return four_of(p.pre, i, 0.0f, p.one); });
         weights.fill(1, [&](int i) { return four_of(p.post, i, 1.0f, p.one); });
         if (CHANNEL) weights.fill(2, [&](int i) { return four_of(p.gate, i, 1.0f, 0.0f); });
     }
+    float gate_next = token && row < p.T ? p.gate[row] : 1.0f;
     __syncthreads();
 
-    for (; row < p.T; row += stride, stage = stage + 1 == stages ? 0 : stage + 1) {
-        // the row that the stage freed by the last one is for, then wait for this one's
-        const int ahead = stages - 1, to = stage == 0 ? ahead : stage - 1;
-        ask(row + ahead * stride, to);
-        if (ahead == 0)
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-        else if (ahead == 1)
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-        else
-            asm volatile("cp.async.wait_group 2;" ::: "memory");
-        const size_t base = (size_t)row * H;
+    for (; row < p.T; row += stride, ring.next()) {
         // What is not there is zeros or ones, so that the values take no branches.
-        const float g = token ? p.gate[row] : 1.0f, alpha = has_f ? p.alpha : 1.0f;
-        f2 w[4], a[4], b[4];
+        const float g = gate_next, alpha = has_f ? p.alpha : 1.0f;
+        if (token && row + stride < p.T) gate_next = p.gate[row + stride];
+        ring.wait(&sh.abort, p.err);
+        const size_t base = (size_t)row * H;
+        f2 x[V][4], dn[V][4], f[V][4], w[4];
+        uint32_t at_x[V], at_f[V];  // a thread's values of the first tensor of either type in this stage
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            at_x[i] = ring.present() + 8 * sizeof(TX) * group[i];
+            at_f[i] = ring.present() + of_dn + 8 * sizeof(TF) * group[i];
+            Ring::get<TX>(in[i] ? at_x[i] : zeros, x[i]);
+            Ring::get<TF>(in[i] ? at_f[i] : zeros, dn[i]);
+            Ring::get<TF>(in[i] ? at_f[i] + f_bytes : zeros, f[i]);
+        }
         // the squares of X' and F, and dN w_pre X'; of values scaled down where that is not enough
         float sx = 1.0f, sf = 1.0f, s0, s1, s2;
         auto sums = [&](bool scaled) {
@@ -465,19 +477,12 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_kernel(cons
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 weight(0, i, w);
-                ring.x(stage, i, a);
-                ring.dn(stage, i, b);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (scaled) a[j] = mul2(a[j], both(sx));
-                    xx = fma2(a[j], a[j], xx);
-                    dx = fma2(mul2(b[j], w[j]), a[j], dx);
-                }
-                ring.f(stage, i, a);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (scaled) a[j] = mul2(a[j], both(sf));
-                    ff = fma2(a[j], a[j], ff);
+                    const f2 a = scaled ? mul2(x[i][j], both(sx)) : x[i][j], b = scaled ? mul2(f[i][j], both(sf)) : f[i][j];
+                    xx = fma2(a, a, xx);
+                    ff = fma2(b, b, ff);
+                    dx = fma2(mul2(dn[i][j], w[j]), a, dx);
                 }
             }
             s0 = sum_of(xx), s1 = sum_of(ff), s2 = sum_of(dx);
@@ -488,57 +493,61 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_kernel(cons
             if (!(s0 < INFINITY)) sx = kDown;
             if (!(s1 < INFINITY)) sf = kDown;
             sums(true);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[i][j] = mul2(f[i][j], both(sf));  // scaled from here, for the sum below
         }
         const float rxs = inverse_root(s0, inv_h, p.eps * sx * sx), rx = rxs * sx, mean = rxs * s2 * inv_h;
-        const float rf = has_post ? inverse_root(s1, inv_h, p.eps * sf * sf) * sf : 1.0f;
-        f2 t[V][4], m = 0;  // t: T, then T (times the channel's gate) times w_post
+        const float rf = has_post ? inverse_root(s1, inv_h, p.eps * sf * sf) : 1.0f / sf;  // of f as it is now
+        f2 t[V][4], m = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             weight(0, i, w);
-            ring.x(stage, i, a);
-            ring.dn(stage, i, b);
-            ring.dx(stage, i, t[i]);
+            Ring::get<TX>(in[i] ? at_x[i] + of_dx : zeros, t[i]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const f2 xh = mul2(a[j], both(rx));
-                d_pre[i][j] = fma2(b[j], xh, d_pre[i][j]);
-                t[i][j] = fma2(both(rx), fma2(xh, both(-mean), mul2(b[j], w[j])), t[i][j]);
+                const f2 xh = mul2(x[i][j], both(rx));
+                d_pre[i][j] = fma2(dn[i][j], xh, d_pre[i][j]);
+                t[i][j] = fma2(both(rx), fma2(xh, both(-mean), mul2(dn[i][j], w[j])), t[i][j]);
                 w[j] = mul2(both(alpha), t[i][j]);
             }
-            if (in[i]) Raw<TX>::store(p.xo, base + 8 * group[i], w);
+            if (in[i]) store8(static_cast<TX *>(p.xo) + base + 8 * group[i], w);
             if (!has_f) continue;
+            // t: from T to T (times the channel's gate) times w_post
             weight(1, i, w);
-            ring.f(stage, i, a);
-            if (CHANNEL) weight(2, i, b);
+            f2 gates[4];
+            if (CHANNEL) weight(2, i, gates);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const f2 fh = mul2(a[j], both(rf));
+                const f2 fh = mul2(f[i][j], both(rf * g));
                 if (CHANNEL) {
-                    d_gate[i][j] = fma2(mul2(t[i][j], fh), w[j], d_gate[i][j]);
-                    t[i][j] = mul2(t[i][j], b[j]);
-                    d_post[i][j] = fma2(t[i][j], fh, d_post[i][j]);
-                } else {
-                    d_post[i][j] = fma2(mul2(t[i][j], fh), both(g), d_post[i][j]);
+                    d_gate[i][j] = fma2(mul2(t[i][j], w[j]), fh, d_gate[i][j]);
+                    t[i][j] = mul2(t[i][j], gates[j]);
                 }
+                d_post[i][j] = fma2(t[i][j], fh, d_post[i][j]);
                 t[i][j] = mul2(t[i][j], w[j]);
-                m = fma2(t[i][j], fh, m);
+                m = fma2(t[i][j], f[i][j], m);
             }
         }
+        float total = sum_of(m) * rf;
+        if (has_f && (has_post || token))
+            team.sum(total);
+        else
+            team.sync();
+        if (me == 0) ask(row + p.stages * stride, ring.stage);  // the team has read the row
         if (!has_f) continue;
-        float total = sum_of(m);
-        if (has_post || token) team.sum(total);
         if (token && me == 0 && p.dgate != nullptr) p.dgate[row] = total;
         // dF = g rf (T w_post - fh mean(T w_post fh)), or g T
-        const float out = g * rf, back = -total * inv_h * rf;
+        const float out = has_post ? g * (rf * sf) : g, back = has_post ? -total * inv_h * rf : 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (has_post) ring.f(stage, i, a);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = mul2(both(out), has_post ? fma2(a[j], both(back), t[i][j]) : t[i][j]);
-            if (in[i]) Raw<TF>::store(p.fo, base + 8 * group[i], w);
+            for (int j = 0; j < 4; ++j) w[j] = mul2(both(out), has_post ? fma2(f[i][j], both(back), t[i][j]) : t[i][j]);
+            if (in[i]) store8(static_cast<TF *>(p.fo) + base + 8 * group[i], w);
         }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    leave(sh);
 
     // the teams' sums one after the other, then this CTA's
     const int teams = blockDim.x / p.team;
@@ -574,7 +583,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_kernel(cons
 }
 
 // The CTAs' sums, one column of one result per lane of a warp row.
-constexpr int kSumRows = 8;
+constexpr int kSumRows = 32;
 __global__ void __launch_bounds__(32 * kSumRows) norm_sum_kernel(const float *partial, int parts, int H, float *d_pre,
                                                                  float *d_post, float *d_gate) {
     __shared__ float s[kSumRows][33];
@@ -602,9 +611,9 @@ OpDone g_attr[24];
 int most_teams(int team) { return team > 32 ? 15 : kMaxTeams; }
 
 // Threads per team and teams per CTA: as many as fit, fewer where rows would leave SMs without one.
-void shape(int T, int H, int sms, int threads, int per, int &team, int &teams) {
+void shape(int T, int H, int sms, int per, int &team, int &teams) {
     team = 32 * ((H + 32 * per - 1) / (32 * per));
-    teams = std::max(1, std::min(std::min(threads / team, most_teams(team)), (T + sms - 1) / sms));
+    teams = std::max(1, std::min(std::min(kThreads / team, most_teams(team)), (T + sms - 1) / sms));
 }
 
 struct Buffer {
@@ -648,43 +657,39 @@ bool aligned(std::initializer_list<const void *> all) {
 using KernelFn = void (*)(const SandwichArgs);
 struct Choice {
     KernelFn kernel;
-    int threads, per, stage_bytes, which;  // per: values of a thread; stage_bytes: of a CTA's row in flight
+    int which;
 };
-// Backward: 16 values per thread where rows are long enough for teams of several warps then: the
-// sums over a team cost each warp as much as 4 values per lane.
-template <typename TX, typename TF>
-Choice choose(bool backward, bool channel, int H, int which) {
-    if (!backward) {
-        constexpr int kThreads = kForwardThreads<TX, TF>;
-        if constexpr (8 * kThreads < kMaxH) {
-            if (H > 8 * kThreads) return {norm_forward_kernel<TX, TF, 2>, kThreads, 16, 0, which * 6 + 1};
-        }
-        return {norm_forward_kernel<TX, TF, 1>, kThreads, 8, 0, which * 6};
-    }
-    const bool two = H > 1024;
-    const int bytes = kBackwardThreads * (two ? 16 : 8) * 2 * (int)(sizeof(TX) + sizeof(TF));
-    if (two) return {channel ? norm_backward_kernel<TX, TF, 2, true> : norm_backward_kernel<TX, TF, 2, false>, kBackwardThreads, 16, bytes, which * 6 + 2 + channel};
-    return {channel ? norm_backward_kernel<TX, TF, 1, true> : norm_backward_kernel<TX, TF, 1, false>, kBackwardThreads, 8, bytes, which * 6 + 4 + channel};
+template <typename TX, typename TF, int V>
+Choice choose(bool backward, bool channel, int which) {
+    if (!backward) return {norm_forward_kernel<TX, TF, V>, which};
+    return channel ? Choice{norm_backward_kernel<TX, TF, V, true>, which + 1} : Choice{norm_backward_kernel<TX, TF, V, false>, which + 2};
 }
-Choice choose(int x_dtype, int f_dtype, bool backward, int gate_kind, int H) {
-    const bool channel = gate_kind == MOE_GATE_CHANNEL;
+template <int V>
+Choice choose(int x_dtype, int f_dtype, bool backward, bool channel) {
+    const int which = 12 * (V - 1);
     if (x_dtype == MOE_DTYPE_BF16)
-        return f_dtype == MOE_DTYPE_BF16 ? choose<bf16, bf16>(backward, channel, H, 0) : choose<bf16, float>(backward, channel, H, 1);
-    return f_dtype == MOE_DTYPE_BF16 ? choose<float, bf16>(backward, channel, H, 2) : choose<float, float>(backward, channel, H, 3);
+        return f_dtype == MOE_DTYPE_BF16 ? choose<bf16, bf16, V>(backward, channel, which) : choose<bf16, float, V>(backward, channel, which + 3);
+    return f_dtype == MOE_DTYPE_BF16 ? choose<float, bf16, V>(backward, channel, which + 6) : choose<float, float, V>(backward, channel, which + 9);
 }
 
 moe_status launch(const char *name, bool backward, SandwichArgs &a, int x_dtype, int f_dtype, int sms, int &grid, cudaStream_t s) {
-    const Choice c = choose(x_dtype, f_dtype, backward, a.gate_kind, a.H);
-    int teams, smem = 2 * a.H * 4;
-    shape(a.T, a.H, sms, c.threads, c.per, a.team, teams);
+    const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
+    // 16 values per thread where a row has them for a warp: the sums over a team cost a warp as much
+    // as 4 values per lane
+    const bool two = a.H > 256;
+    const Choice c = two ? choose<2>(x_dtype, f_dtype, backward, channel) : choose<1>(x_dtype, f_dtype, backward, channel);
+    int teams;
+    shape(a.T, a.H, sms, two ? 16 : 8, a.team, teams);
     grid = (int)std::min<long long>(std::min(sms, kMaxCtas), ((long long)a.T + teams - 1) / teams);
-    if (backward) {
-        const int weights = (a.gate_kind == MOE_GATE_CHANNEL ? 3 : 2) * a.H * 4;
-        a.weights_in_smem = weights + c.stage_bytes <= kBackwardSmem;
-        a.stages = std::min(3, (kBackwardSmem - (a.weights_in_smem ? weights : 0)) / c.stage_bytes);
-        smem = std::max(weights, (a.weights_in_smem ? weights : 0) + a.stages * c.stage_bytes);
-    }
-    const cudaError_t e = op_allow_smem(reinterpret_cast<const void *>(c.kernel), backward ? kBackwardSmem : 2 * kMaxH * 4, &g_attr[c.which]);
+    // X and F, backward also their gradients, of a row of each team
+    const int stage = teams * a.H * ((x_dtype == MOE_DTYPE_F32 ? 4 : 2) + (f_dtype == MOE_DTYPE_F32 ? 4 : 2)) * (backward ? 2 : 1);
+    const int weights = (backward && channel ? 3 : 2) * a.H * 4;
+    a.weights_in_smem = weights + stage <= kSmem;
+    a.stages = std::min(kMaxStages, (kSmem - (a.weights_in_smem ? weights : 0)) / stage);
+    a.err = op_error_word();
+    if (a.err == nullptr) return op_fail(MOE_ERR_CUDA, "%s: no usable current device", name);
+    const int smem = std::max(weights, (a.weights_in_smem ? weights : 0) + a.stages * stage);
+    const cudaError_t e = op_allow_smem(reinterpret_cast<const void *>(c.kernel), kSmem, &g_attr[c.which]);
     if (e != cudaSuccess) return op_cuda(e, name);
     return op_cuda(launch_pdl(c.kernel, dim3(grid), dim3(a.team * teams), (size_t)smem, s, a), name);
 }

@@ -170,13 +170,13 @@ def test_norm_before_the_first_block(x_type, n_type, with_stream):
     assert back[1] is None and back[3] is None and back[4] is None
 
 
-@pytest.mark.parametrize("factor", [1e30, 1e-25, 1e18])
+@pytest.mark.parametrize("factor", [1e37, 1e30, 1e-25, 1e18])
 def test_magnitudes(factor):
     """Squares beyond fp32 and below it; the gradients of F fall with 1 / |F|."""
     s = _inputs(64, 520, F32, F32, "channel", "rms")
     s["F"] = s["F"] * factor
     _both(s)
-    s["X"] = s["X"] * factor
+    s["X"] = s["X"] * min(factor, 1e34)  # its largest values are 200 times the others
     s["dX"] = s["dX"] / max(factor, 1.0)
     _both(s, eps=1e-30 if factor < 1 else 1e-5)
 
