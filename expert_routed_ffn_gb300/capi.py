@@ -576,7 +576,7 @@ def sandwich_norm(X, F=None, pre_w=None, post_w=None, gate=None, residual_scale=
                 _tensor(X_out, "X_out", (T, H), X.dtype, index)
         if pre_w is not None:
             if N_out is None:
-                N_out = torch.empty((T, H), dtype=of_n, device=X.device)
+                N_out = torch.empty_like(F) if F is not None else torch.empty((T, H), dtype=of_n, device=X.device)
             else:
                 _tensor(N_out, "N_out", (T, H), of_n, index)
         status = _lib.moe_sandwich_norm(X.data_ptr(), _address(F), _address(pre_w), _address(post_w), _address(gate), gate_kind,
@@ -607,7 +607,6 @@ def sandwich_norm_backward(dX, dN, X, F=None, pre_w=None, post_w=None, gate=None
     check(_lib.moe_sandwich_norm_workspace(T, H, ctypes.byref(need)), "moe_sandwich_norm_backward")
     raw, undo = _enter(index, stream)
     try:
-        device = X.device
         if dX_out is None:
             dX_out = torch.empty_like(X)
         else:
@@ -617,8 +616,10 @@ def sandwich_norm_backward(dX, dN, X, F=None, pre_w=None, post_w=None, gate=None
                 dF_out = torch.empty_like(F)
             else:
                 _tensor(dF_out, "dF_out", (T, H), of_n, index)
-        dpre, dpost, dgate = (None if w is None else torch.empty_like(w) for w in (pre_w, post_w, gate))
-        work = torch.empty(need.value, dtype=torch.uint8, device=device)
+        dpre = None if pre_w is None else torch.empty_like(pre_w)
+        dpost = None if post_w is None else torch.empty_like(post_w)
+        dgate = None if gate is None else torch.empty_like(gate)
+        work = torch.empty(need.value, dtype=torch.uint8, device=X.device)
         status = _lib.moe_sandwich_norm_backward(
             _address(dX), _address(dN), X.data_ptr(), _address(F), _address(pre_w), _address(post_w), _address(gate), gate_kind,
             residual_scale, eps, code, T, H, x_code, n_code, dX_out.data_ptr(), _address(dF_out), _address(dpre),
