@@ -610,9 +610,12 @@ Workspace lay_out(int E, int N, int K) {
 struct Scales {
     float a, b;
 };
+// Samples of a polynomial of degree 5: between two of them it rises by at most 100 / kSamples^2 of
+// its largest value (its second derivative is at most 800 / limit^2 of that, by Markov's inequality)
+constexpr int kSamples = 128;
 double largest(double limit, double (*of)(double, const float *), const float *c) {
     double most = 0.0;
-    for (int i = 0; i <= 4096; ++i) most = std::max(most, std::fabs(of(limit * i / 4096, c)));
+    for (int i = 0; i <= kSamples; ++i) most = std::max(most, std::fabs(of(limit * i / kSamples, c)));
     return 1.01 * most;
 }
 float power_below(double bound, int most) {
