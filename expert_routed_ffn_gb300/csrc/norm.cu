@@ -646,7 +646,8 @@ moe_status check(const char *op, int T, int H, int x_dtype, int f_dtype, int kin
     if (T > 0 && !has_f && (post != nullptr || gate_kind != MOE_GATE_NONE))
         return op_fail(MOE_ERR_INVALID_ARG, "%s: post_w and the gate belong to a block's result F", op);
     if (T > 0 && !has_f && pre == nullptr) return op_fail(MOE_ERR_INVALID_ARG, "%s: neither F nor pre_w: nothing to do", op);
-    if (H % 8 || H > kMaxH) return op_fail(MOE_ERR_UNSUPPORTED, "%s: H %d: need a multiple of 8 up to %d", op, H, kMaxH);
+    if (H % 8 || H > kMaxH || T > (1 << 30))
+        return op_fail(MOE_ERR_UNSUPPORTED, "%s: T up to 2^30, H a multiple of 8 up to %d (T %d, H %d)", op, kMaxH, T, H);
     return MOE_OK;
 }
 

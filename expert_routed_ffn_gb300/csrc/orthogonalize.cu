@@ -688,8 +688,7 @@ CUresult operand_map(CUtensorMap *m, const Operand &o, int E, bool mn, int box) 
 template <bool A_MN, bool B_MN, bool SYM>
 moe_status product(const char *name, ProductArgs &g, const Operand &a, const Operand &b, int which, int sms, cudaStream_t s) {
     const long long tiles = choose_tiles(g, B_MN, SYM, sms);
-    if (tiles > (1ll << 30)) return op_fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^30 tiles", name);
-    g.tiles = (int)tiles;
+    g.tiles = (int)tiles;  // at most 65535 * 64^2
     g.wait = wait_cycles(g.red / kBK + 1);
     CUresult cr = operand_map(&g.map_a, a, g.E, A_MN, g.cols / 2);
     if (cr == CUDA_SUCCESS) cr = operand_map(&g.map_b, b, g.E, B_MN, g.tile_rows / 2);

@@ -442,7 +442,7 @@ moe_status moe_grouped_gated_dgrad(const void *dG, const void *dU, const void *W
  * fixed order.  Without F, dX is the whole gradient (no residual_scale).  X_out and dX_out may be NULL
  * where nothing reads them (X_out without pre_w).
  * In place: X_out may be X and N may be F, dX may be dX_out and dF may be dN; any other overlap of an
- * output is refused.  H: a multiple of 8 up to 8192; eps >= 1e-30.  Rows of any magnitude are normed (sums of squares beyond fp32
+ * output is refused.  H: a multiple of 8 up to 8192, T up to 2^30; eps >= 1e-30.  Rows of any magnitude are normed (sums of squares beyond fp32
  * are taken again of scaled values); a row with an infinity or a NaN gives what the formulas
  * give, in that row (and in the sums over rows).  T == 0: no-op, the gradients of weights are zeros.  `workspace` as in moe_clip_grad_norm.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */

@@ -68,7 +68,8 @@ def _near(got, ref, units):
 
 
 SIZES = [(1, 8, 8), (1, 64, 64), (3, 8, 200), (3, 200, 8), (2, 136, 264), (2, 264, 136), (1, 256, 1024), (1, 1024, 256), (5, 328, 328),
-         (2, 520, 1032), (40, 256, 128), (1, 1408, 2048), (3, 2048, 1408), (130, 64, 72), (1, 4096, 264), (1, 264, 4096)]
+         (2, 520, 1032), (40, 256, 128), (1, 1408, 2048), (3, 2048, 1408), (130, 64, 72), (1, 4096, 264), (1, 264, 4096), (1, 64, 16384),
+         (1, 16384, 64)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
