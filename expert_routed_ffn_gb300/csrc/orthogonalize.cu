@@ -685,19 +685,27 @@ CUresult operand_map(CUtensorMap *m, const Operand &o, int E, bool mn, int box) 
                          CU_TENSOR_MAP_SWIZZLE_128B});
 }
 
+// A product's kernel and arguments but what changes from step to step.
+struct Product {
+    ProductArgs g;
+    void (*kernel)(const ProductArgs);
+    int grid;
+};
 template <bool A_MN, bool B_MN, bool SYM>
-moe_status product(const char *name, ProductArgs &g, const Operand &a, const Operand &b, int which, int sms, cudaStream_t s) {
+moe_status plan(const char *name, Product &p, const Operand &a, const Operand &b, int which, int sms) {
+    ProductArgs &g = p.g;
     const long long tiles = choose_tiles(g, B_MN, SYM, sms);
     g.tiles = (int)tiles;  // at most 65535 * 64^2
     g.wait = wait_cycles(g.red / kBK + 1);
+    p.grid = 2 * (int)std::min<long long>(sms / 2, tiles);
+    p.kernel = product_kernel<A_MN, B_MN, SYM>;
     CUresult cr = operand_map(&g.map_a, a, g.E, A_MN, g.cols / 2);
     if (cr == CUDA_SUCCESS) cr = operand_map(&g.map_b, b, g.E, B_MN, g.tile_rows / 2);
     if (cr != CUDA_SUCCESS) return op_fail(MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", name, (int)cr);
-    auto kernel = product_kernel<A_MN, B_MN, SYM>;
-    const cudaError_t ce = op_allow_smem(reinterpret_cast<const void *>(kernel), kSmemBytes, &g_attr[which]);
-    if (ce != cudaSuccess) return op_cuda(ce, name);
-    return op_cuda(launch_pdl_cluster(kernel, dim3(2u * (unsigned)std::min<long long>(sms / 2, tiles)), dim3(kThreads),
-                                      (size_t)kSmemBytes, s, dim3(2, 1, 1), g), name);
+    return op_cuda(op_allow_smem(reinterpret_cast<const void *>(p.kernel), kSmemBytes, &g_attr[which]), name);
+}
+cudaError_t launch(const Product &p, cudaStream_t s) {
+    return launch_pdl_cluster(p.kernel, dim3(p.grid), dim3(kThreads), (size_t)kSmemBytes, s, dim3(2, 1, 1), p.g);
 }
 
 moe_status check_sizes(const char *name, int E, int N, int K) {
@@ -759,6 +767,25 @@ extern "C" moe_status moe_orthogonalize(const void *G, int dtype, int E, int N, 
     half *x[2] = {reinterpret_cast<half *>(ws + w.x[0]), reinterpret_cast<half *>(ws + w.x[1])};
     half *lo = reinterpret_cast<half *>(ws + w.lo), *A = reinterpret_cast<half *>(ws + w.a), *B = reinterpret_cast<half *>(ws + w.b);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    // the products, by the buffer that X is in, before anything is launched
+    const bool wide = N <= K;
+    const int m = std::min(N, K), ld = padded(m);
+    Product gram[2] = {}, poly = {}, update[2] = {};
+    const Operand sym_a{A, m, m, ld}, sym_b{B, m, m, ld};
+    poly.g.E = E, poly.g.R = poly.g.C = poly.g.red = m, poly.g.ld = ld, poly.g.err = err;
+    poly.g.other = A, poly.g.out = B;
+    st = plan<false, false, true>(name, poly, sym_a, sym_a, 0, sms);
+    for (int i = 0; i < 2 && st == MOE_OK; ++i) {
+        const Operand X{x[i], N, K, K};
+        ProductArgs &a = gram[i].g, &u = update[i].g;
+        a.E = E, a.R = a.C = m, a.ld = ld, a.red = wide ? K : N, a.err = err, a.out = A;
+        u.E = E, u.R = N, u.C = K, u.red = m, u.err = err, u.out = x[i ^ 1];
+        st = wide ? plan<false, false, true>(name, gram[i], X, X, 0, sms) : plan<true, true, true>(name, gram[i], X, X, 1, sms);
+        if (st != MOE_OK) break;
+        st = wide ? plan<true, false, false>(name, update[i], X, sym_b, 2, sms) : plan<false, false, false>(name, update[i], sym_b, X, 3, sms);
+    }
+    if (st != MOE_OK) return st;
+
     const long long size = (long long)N * K;
     const int parts = parts_of(size);
     const dim3 grid((unsigned)(E * parts));
@@ -778,43 +805,25 @@ extern "C" moe_status moe_orthogonalize(const void *G, int dtype, int E, int N, 
     }
     if (ce != cudaSuccess) return op_cuda(ce, name);
 
-    const bool wide = N <= K;
-    const int m = std::min(N, K), ld = padded(m);
     for (int i = 0; i < steps; ++i) {
         const float *c = coefficients + 3 * i, sa = scales[i].a, sb = scales[i].b;
-        const Operand X{x[i & 1], N, K, K}, sym_a{A, m, m, ld}, sym_b{B, m, m, ld};
-        ProductArgs g = {};  // A
-        g.E = E, g.R = g.C = m, g.ld = ld, g.red = wide ? K : N, g.err = err;
-        g.table = i == 0 ? table : nullptr;
-        g.out = A;
-        g.k_acc = sa / (up * up);
-        st = wide ? product<false, false, true>(name, g, X, X, 0, sms, s) : product<true, true, true>(name, g, X, X, 1, sms, s);
-        if (st != MOE_OK) return st;
-
-        g = {};  // B
-        g.E = E, g.R = g.C = g.red = m, g.ld = ld, g.err = err;
-        g.table = i == 0 ? table : nullptr;
-        g.other = A;
-        g.out = B;
-        g.k_acc = c[2] / sa / sa * sb;
-        g.k_other = c[1] / sa * sb;
-        g.k_diag = c[0] * sb;
-        st = product<false, false, true>(name, g, sym_a, sym_a, 0, sms, s);
-        if (st != MOE_OK) return st;
-
-        g = {};  // X
-        g.E = E, g.R = N, g.C = K, g.red = m, g.err = err;
+        ProductArgs &a = gram[i & 1].g, &b = poly.g, &u = update[i & 1].g;
+        a.table = b.table = u.table = i == 0 ? table : nullptr;
+        a.k_acc = sa / (up * up);
+        b.k_acc = c[2] / sa / sa * sb;
+        b.k_other = c[1] / sa * sb;
+        b.k_diag = c[0] * sb;
         const bool last = i + 1 == steps;
         const float unit = last ? scale / up : 1.0f;  // of what is stored
-        g.k_acc = unit / sb;
-        g.other = i == 0 ? lo0 : keeps_lo(i, steps) ? lo : nullptr;
-        g.k_other = c[0];  // (the last step has no lo)
-        g.table = i == 0 ? table : nullptr;
-        g.out = x[(i + 1) & 1];
-        g.out_lo = !last && keeps_lo(i + 1, steps) ? lo : nullptr;
-        g.final = last ? static_cast<bf16 *>(out) : nullptr;
-        st = wide ? product<true, false, false>(name, g, X, sym_b, 2, sms, s) : product<false, false, false>(name, g, sym_b, X, 3, sms, s);
-        if (st != MOE_OK) return st;
+        u.k_acc = unit / sb;
+        u.other = i == 0 ? lo0 : keeps_lo(i, steps) ? lo : nullptr;
+        u.k_other = c[0];  // (the last step has no lo)
+        u.out_lo = !last && keeps_lo(i + 1, steps) ? lo : nullptr;
+        u.final = last ? static_cast<bf16 *>(out) : nullptr;
+        ce = launch(gram[i & 1], s);
+        if (ce == cudaSuccess) ce = launch(poly, s);
+        if (ce == cudaSuccess) ce = launch(update[i & 1], s);
+        if (ce != cudaSuccess) return op_cuda(ce, name);
     }
     return MOE_OK;
 }
