@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import re
 import struct
@@ -530,26 +531,36 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
+@functools.lru_cache(maxsize=1024)
+def _norm_workspace(T, H):
+    need = ctypes.c_size_t()
+    check(_lib.moe_sandwich_norm_workspace(T, H, ctypes.byref(need)), "moe_sandwich_norm_backward")
+    return need.value
+
+
 def _norm_arguments(X, F, pre_w, post_w, gate, kind):
-    """Checks what both directions take: X [T, H], F and the parameters.  Returns T, H, the device's
-    index, the kind's code and the gate's kind."""
-    torch = _torch
-    _need(X.dim() == 2, "X must be [T, H]")
-    T, H = X.shape
+    """Checks what both directions take: X [T, H], F and the parameters.  Returns X's shape, the
+    device's index, the kind's code and the gate's kind."""
+    f32, shape = _torch.float32, X.shape
+    if len(shape) != 2:
+        raise ValueError("X must be [T, H]")
+    T, H = shape
     _fits(T, H)
     index = X.get_device()
-    _tensor(X, "X", (T, H), X.dtype, index)
+    _tensor(X, "X", shape, X.dtype, index)
     if F is not None:
-        _tensor(F, "F", (T, H), F.dtype, index)
-    for w, name in ((pre_w, "pre_w"), (post_w, "post_w")):
-        if w is not None:
-            _tensor(w, name, (H,), torch.float32, index)
-    _need(kind in ("rms", "gemma"), f"kind must be 'rms' or 'gemma', not {kind!r}")
+        _tensor(F, "F", shape, F.dtype, index)
+    if pre_w is not None:
+        _tensor(pre_w, "pre_w", (H,), f32, index)
+    if post_w is not None:
+        _tensor(post_w, "post_w", (H,), f32, index)
+    if kind != "rms" and kind != "gemma":
+        raise ValueError(f"kind must be 'rms' or 'gemma', not {kind!r}")
     gate_kind = MOE_GATE_NONE
     if gate is not None:
         gate_kind = MOE_GATE_TOKEN if gate.dim() == 2 else MOE_GATE_CHANNEL
-        _tensor(gate, "gate", (T, 1) if gate.dim() == 2 else (H,), torch.float32, index)
-    return T, H, index, MOE_NORM_GEMMA if kind == "gemma" else MOE_NORM_RMS, gate_kind
+        _tensor(gate, "gate", (T, 1) if gate_kind == MOE_GATE_TOKEN else (H,), f32, index)
+    return shape, index, MOE_NORM_GEMMA if kind == "gemma" else MOE_NORM_RMS, gate_kind
 
 
 def sandwich_norm(X, F=None, pre_w=None, post_w=None, gate=None, residual_scale=1.0, eps=1e-5, kind="rms", X_out=None,
@@ -561,26 +572,27 @@ def sandwich_norm(X, F=None, pre_w=None, post_w=None, gate=None, residual_scale=
     without F X' is X itself and N = norm(X) pre_w (of n_dtype, by default X's).  kind "gemma": weights
     are 1 + w.  X_out may be X, and N_out may be F."""
     torch = _t()
-    T, H, index, code, gate_kind = _norm_arguments(X, F, pre_w, post_w, gate, kind)
+    shape, index, code, gate_kind = _norm_arguments(X, F, pre_w, post_w, gate, kind)
     of_n = F.dtype if F is not None else n_dtype or (X.dtype if N_out is None else N_out.dtype)
-    _need(F is None or n_dtype in (None, F.dtype), "N has F's type")
+    if n_dtype is not None and n_dtype is not of_n:
+        raise ValueError("N has F's type")
     x_code, n_code = _dtype_code(X.dtype), _dtype_code(of_n)
-    _need(X_out is None or F is not None, "X_out needs F")
-    _need(N_out is None or pre_w is not None, "N_out needs pre_w")
+    if X_out is not None and F is None or N_out is not None and pre_w is None:
+        raise ValueError("X_out needs F, and N_out needs pre_w")
     raw, undo = _enter(index, stream)
     try:
         if F is not None:
             if X_out is None:
                 X_out = torch.empty_like(X)
             else:
-                _tensor(X_out, "X_out", (T, H), X.dtype, index)
+                _tensor(X_out, "X_out", shape, X.dtype, index)
         if pre_w is not None:
             if N_out is None:
-                N_out = torch.empty_like(F) if F is not None else torch.empty((T, H), dtype=of_n, device=X.device)
+                N_out = torch.empty_like(F) if F is not None else torch.empty(shape, dtype=of_n, device=X.device)
             else:
-                _tensor(N_out, "N_out", (T, H), of_n, index)
+                _tensor(N_out, "N_out", shape, of_n, index)
         status = _lib.moe_sandwich_norm(X.data_ptr(), _address(F), _address(pre_w), _address(post_w), _address(gate), gate_kind,
-                                        residual_scale, eps, code, T, H, x_code, n_code, _address(X_out), _address(N_out), raw)
+                                        residual_scale, eps, code, *shape, x_code, n_code, _address(X_out), _address(N_out), raw)
     finally:
         _leave(undo)
     check(status, "moe_sandwich_norm")
@@ -593,37 +605,35 @@ def sandwich_norm_backward(dX, dN, X, F=None, pre_w=None, post_w=None, gate=None
     pre_w), X being the X' it returned: (of its X, of F, of pre_w, of post_w, of the gate), None where
     there is no such tensor.  dX_out may be dX, and dF_out may be dN."""
     torch = _t()
-    T, H, index, code, gate_kind = _norm_arguments(X, F, pre_w, post_w, gate, kind)
-    of_n = dN.dtype if F is None and dN is not None else X.dtype if F is None else F.dtype
+    shape, index, code, gate_kind = _norm_arguments(X, F, pre_w, post_w, gate, kind)
+    of_n = F.dtype if F is not None else X.dtype if dN is None else dN.dtype
     x_code, n_code = _dtype_code(X.dtype), _dtype_code(of_n)
-    _need((dN is None) == (pre_w is None), "dN goes with pre_w")
-    _need(dX is not None or pre_w is not None, "dX is needed without pre_w")
-    _need(dF_out is None or F is not None, "dF_out needs F")
+    if (dN is None) != (pre_w is None) or dX is None and pre_w is None or dF_out is not None and F is None:
+        raise ValueError("dN goes with pre_w, dX is needed without it, and dF_out needs F")
     if dX is not None:
-        _tensor(dX, "dX", (T, H), X.dtype, index)
+        _tensor(dX, "dX", shape, X.dtype, index)
     if dN is not None:
-        _tensor(dN, "dN", (T, H), of_n, index)
-    need = ctypes.c_size_t()
-    check(_lib.moe_sandwich_norm_workspace(T, H, ctypes.byref(need)), "moe_sandwich_norm_backward")
+        _tensor(dN, "dN", shape, of_n, index)
+    need = _norm_workspace(*shape)
     raw, undo = _enter(index, stream)
     try:
         if dX_out is None:
             dX_out = torch.empty_like(X)
         else:
-            _tensor(dX_out, "dX_out", (T, H), X.dtype, index)
+            _tensor(dX_out, "dX_out", shape, X.dtype, index)
         if F is not None:
             if dF_out is None:
                 dF_out = torch.empty_like(F)
             else:
-                _tensor(dF_out, "dF_out", (T, H), of_n, index)
+                _tensor(dF_out, "dF_out", shape, of_n, index)
         dpre = None if pre_w is None else torch.empty_like(pre_w)
         dpost = None if post_w is None else torch.empty_like(post_w)
         dgate = None if gate is None else torch.empty_like(gate)
-        work = torch.empty(need.value, dtype=torch.uint8, device=X.device)
+        work = torch.empty(need, dtype=torch.uint8, device=X.device)
         status = _lib.moe_sandwich_norm_backward(
             _address(dX), _address(dN), X.data_ptr(), _address(F), _address(pre_w), _address(post_w), _address(gate), gate_kind,
-            residual_scale, eps, code, T, H, x_code, n_code, dX_out.data_ptr(), _address(dF_out), _address(dpre),
-            _address(dpost), _address(dgate), work.data_ptr(), need.value, raw)
+            residual_scale, eps, code, *shape, x_code, n_code, dX_out.data_ptr(), _address(dF_out), _address(dpre),
+            _address(dpost), _address(dgate), work.data_ptr(), need, raw)
     finally:
         _leave(undo)
     check(status, "moe_sandwich_norm_backward")

@@ -14,6 +14,17 @@
 //   dgrad: one sum over both projections' columns, so dX is written once and rounded once.  Each
 //     half of the sum is padded to whole steps of 64, whose copies bring zeros in both operands.
 // The weights' gradients are moe_grouped_wgrad's of dG, dU with X and of dY with H.
+//
+// Measured on GB300, calls one after the other on the same tensors (64 experts, I 1408, K 2048):
+//   forward, 24576 rows, G and U kept   201 us (without them 186), 1.41 PFLOP/s, 5.1 TB/s: the tensor pipe is
+//              busy 72% of the cycles and HBM 65% at 1.7 GHz (power); with all rows in one expert, whose
+//              weights stay in L2, 153 and 145 us, 1.95 PFLOP/s
+//   backward, 24576 rows   130 us, 5.6 TB/s, tensor pipe 62%: 553 MB of dY, G, U, dG and dU beside 369 MB of
+//              weights.  With two epilogue warps per lane quadrant it waited for the gradients' arithmetic
+//              (180 us), with loads of G and U after the sums for those
+//   dgrad, 24576 rows, fp32   203 us, 5.4 TB/s, tensor pipe 71%; bf16 197
+//   forward, one token's six experts   12.8 us (14.9 with changing inputs), 69 MB of weights
+//   dgrad, 2000 rows, 128 experts, 256 x 1024   25.5 us with changing inputs, 5.5 TB/s
 #include <algorithm>
 
 #include "grouped_kernel.cuh"

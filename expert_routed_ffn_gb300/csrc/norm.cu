@@ -7,16 +7,27 @@
 //   dF = rf (T g w_post - fh mean(T g w_post fh))        (T g without a post-norm)
 //   dw_pre = sum over rows of dN xh,  dw_post = of T g fh,  dg = T P summed over what shares a gate
 //
-// Bound by HBM: each tensor is read or written once.  A row belongs to a team of warps, 8 values of
-// it to a thread (16 beyond 4096), so that its norms are sums over the team and its values stay in
-// registers from the load to the store; the next row of a team is loaded while this one is
-// computed.  The backward pass needs two sums over the team per row: X' and F's norms and
-// mean(dN w_pre xh) come in the first one (the last up to a factor rx, known afterwards).  The
-// weights' gradients are summed per thread over the rows of its team, then over the teams of a CTA
-// in shared memory, then by a second kernel over the CTAs (one per SM, so that these partial sums
-// are few): always in the same order, in fp32.
+// Bound by HBM: each tensor is read or written once.  A row belongs to a team of warps, 16 values of
+// it to a thread (8 where it has no more for a warp), so that its norms are sums over the team and its
+// values stay in registers from the load to the store; the next row of a team comes to shared
+// memory by bulk copies meanwhile.  The backward pass needs two sums over the team per row: X' and
+// F's norms and mean(dN w_pre xh) come in the first one (the last up to a factor rx, known
+// afterwards).  The weights' gradients are summed per thread over the rows of its team, then over the
+// teams of a CTA in shared memory, then by a second kernel over the CTAs (one per SM, so that these
+// partial sums are few): always in the same order, in fp32.
 //
 // A sum of squares beyond fp32 is taken again of values scaled by 2^-100.
+//
+// Measured on GB300 (captured into a graph, one call after the other on the same tensors):
+//   forward, 8192 x 2048, fp32 stream, bf16 block   39 us, 5.1 TB/s; 65536 rows 247 us, 6.5 TB/s; bf16
+//                              throughout 28.6 and 163 us.  A call has 8 us beside the copying: launch,
+//                              weights, a team's first rows and last stores
+//   backward, 16384 x 2048, bf16   86 us, 4.7 TB/s: half of an SM's issue slots are taken, 46
+//                              instructions per value of a warp's lane, and 16 warps wait for one
+//                              another twice a row.  (With 8 values per thread and weights read across
+//                              banks it took 203 us, without bank conflicts 109, with 768 threads of fewer
+//                              registers 103.)
+//   one row of 2048            6.2 us
 #include <algorithm>
 
 #include "common.cuh"
@@ -33,7 +44,7 @@ constexpr int kMaxTeams = kThreads / 32;
 constexpr int kSmem = 212 << 10;   // dynamic shared memory, most
 constexpr int kMaxCtas = 256;
 constexpr float kDown = 0x1p-100f;
-constexpr int kMaxStages = 2;  // (with 3 and 4, 8192 rows of 2048 with an fp32 stream took 41 and 43 us for 39)
+constexpr int kMaxStages = 2;  // rows (8192 x 2048 with an fp32 stream: 39 us, with 3 41, with 4 43)
 constexpr uint64_t kWaitNs = 2000000000ull;  // bound of the wait for a row
 
 struct SandwichArgs {
@@ -50,8 +61,8 @@ struct SandwichArgs {
     bool weights_in_smem;   // backward
 };
 
-// Two fp32 values in one 64-bit register, and arithmetic on both in one instruction: half the
-// instructions of a row, which bound the backward pass (105 us for 16384 x 2048 before).
+// Two fp32 values in one 64-bit register, and arithmetic on both in one instruction (16384 x 2048
+// backward: 86 us, with one value each 92).
 typedef unsigned long long f2;
 __device__ __forceinline__ f2 make2(float lo, float hi) {
     f2 r;
@@ -195,8 +206,8 @@ __device__ __forceinline__ float4 four_of(const float *w, int i, float otherwise
 
 // A team's next rows, in shared memory: a row's tensors one after the other, by one bulk copy each
 // that a thread of the team starts, `stages` rows at most (the present one among them).  (Copies by
-// every thread for itself, 16 bytes at a time, took instructions, and half of each sector of fp32
-// rows twice: 8192 rows with an fp32 stream 46 us.)
+// every thread for itself, 16 bytes at a time, took half of each sector of fp32 rows twice: 8192 rows
+// with an fp32 stream 48 us for 39; backward, 16384 x 8192 in fp32, 965 us for 745.)
 struct Ring {
     uint32_t rows, bars;  // the team's: stage 0, and its barrier (8 bytes per stage)
     uint32_t bytes;       // of a stage

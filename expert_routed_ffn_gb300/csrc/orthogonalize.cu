@@ -17,11 +17,20 @@
 // change nearly all is a X, and b A + c A^2 nearly nothing; so the steps that matter (all but the last two)
 // keep the rounding of X, hi + lo, and take lo through a X alone: X <- B hi + a lo, an
 // epilogue's work; the tensor cores see hi only.  Where 16 directions are 300 times as large as
-// the rest, the result's error (2-norm, relative) falls from 2.0e-2 to 1.5e-3, below a
-// bf16 result's own rounding of 1.7e-3; bf16 throughout gives 0.16.
+// the rest, the result's error (2-norm, relative) is 2.2e-3, of which its rounding to bf16 is 1.7e-3;
+// with hi alone it would be 2.0e-2, with bf16 throughout 0.16.  Gaussian matrices and singular values
+// falling as 1 / j: 2.1e-3 and 1.8e-3.
 // X0 is G times a power of two (exact for bf16 G: no lo), the rest of 1 / (|G| + eps) is a factor
 // s in (1/2, 1] of the first A and B.  Sums are fp32 in tensor memory, over at most 16384
 // products: the tensor core's truncation stays below 1e-4 (2^-13) of a sum of one sign.
+//
+// Measured on GB300, 32 x 1408 x 2048 in fp32, five steps, one call after the other: 2.0 ms, 1.2
+// PFLOP/s of the products counted above; |G| 57 us and X0 with its lo 113 us (6.6 and 6.1 TB/s), then per
+// step A 104, B 76 to 80 and X 187 us (with lo) or 160.  The tensor pipe is busy 70 to 78% of the cycles
+// and the clock falls to 1.5 to 1.7 GHz of 2.07 (power): 5.5 tiles of 256 to a side make 18 tiles' work of the 15.1 below
+// the diagonal, a tile's epilogue shares shared memory's bandwidth with the MMAs' operands, and a
+// launch's first and last tiles leave SMs idle.  256 x 1024: 76 us in 17 launches, each
+// bound by its latency (64 x 64: 51 us).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -148,9 +157,8 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 __device__ __forceinline__ float2 unpack_half2(uint32_t v) { return __half22float2(*reinterpret_cast<const half2 *>(&v)); }
 
 // The epilogues, by one warp for its chunks of 32 columns (lanes) x 32 rows (TMEM columns).  What
-// a chunk reads from memory is asked for a chunk ahead (fetch), the first before the sums are there: with
-// the loads after it each chunk waited for them, and the products for the epilogue (five steps of
-// 32 x 1408 x 2048: 2459 us).
+// a chunk reads from memory is asked for a chunk ahead (fetch), the first before the sums are there; with
+// four warps per lane quadrant (two: five steps of 32 x 1408 x 2048 took 2277 us for 2178).
 
 // A symmetric result (A, or B from A): v = f (k_acc sum + k_other other + k_diag on the diagonal),
 // f: s^2 for A, s for B.  Element (r, c) with c <= r is stored there and at (c, r), 32 bytes of a lane's
