@@ -29,8 +29,8 @@
 // step A 104, B 76 to 80 and X 187 us (with lo) or 160.  The tensor pipe is busy 70 to 78% of the cycles
 // and the clock falls to 1.5 to 1.7 GHz of 2.07 (power): 5.5 tiles of 256 to a side make 18 tiles' work of the 15.1 below
 // the diagonal, a tile's epilogue shares shared memory's bandwidth with the MMAs' operands, and a
-// launch's first and last tiles leave SMs idle.  256 x 1024: 76 us in 17 launches, each
-// bound by its latency (64 x 64: 51 us).
+// launch's first and last tiles leave SMs idle.  256 x 1024: 74 us in 17 launches, each
+// bound by its latency (64 x 64: 49 us); 8 x 512 x 512 116, 1024 x 1024 101.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -49,14 +49,21 @@ namespace {
 constexpr int kMaxSide = 16384;
 constexpr int kBK = 64;                // reduction steps per stage: 128 bytes
 constexpr int kMaxStages = 12;
-constexpr int kParts = 4;              // epilogue warps per TMEM lane quadrant
-constexpr int kEpiWarps = kQuads * kParts;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kAccCols = 256;
-constexpr uint32_t kTmemCols = 2 * kAccCols;
+// SMALL: half of an SM's shared memory, tensor memory and registers, so that while one product ends
+// the next one's CTAs are there, with their barriers and tensor memory, and wait for it.  For
+// products whose tiles are one wave of up to 128 rows (1024 x 1024 101 us for 109, 256 x 1024 74 for 76).
+template <bool SMALL>
+constexpr int kParts = SMALL ? 2 : 4;  // epilogue warps per TMEM lane quadrant
+template <bool SMALL>
+constexpr int kEpiWarps = kQuads * kParts<SMALL>;
+template <bool SMALL>
+constexpr int kThreads = 64 + 32 * kEpiWarps<SMALL>;
+template <bool SMALL>
+constexpr int kAccCols = SMALL ? 128 : 256;
 constexpr int kRow = kBK * 2;          // bytes of a K-major row, or of 64 columns in MN-major
 constexpr int kChunk = 64 * kRow;
-constexpr int kStageSpace = 229376;
+template <bool SMALL>
+constexpr int kStageSpace = SMALL ? 110592 : 229376;
 
 struct Header {
     uint64_t bars[2 * kMaxStages + 5];
@@ -64,8 +71,10 @@ struct Header {
     volatile int abort;
 };
 constexpr int kHeaderBytes = 1 << 10;
-constexpr int kSmemBytes = kHeaderBytes + kStageSpace;
-static_assert(sizeof(Header) <= kHeaderBytes && kSmemBytes <= 232448, "shared memory of one CTA");
+template <bool SMALL>
+constexpr int kSmemBytes = kHeaderBytes + kStageSpace<SMALL>;
+static_assert(sizeof(Header) <= kHeaderBytes && kSmemBytes<false> <= 232448, "shared memory of one CTA");
+static_assert(2 * (kSmemBytes<true> + 1024) <= 233472, "shared memory of two on an SM");
 
 // One batched product: out[e] [R, C], summed over `red`; columns are the MMA's M.
 struct ProductArgs {
@@ -289,8 +298,8 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {  // as groupe
 }
 
 // A_MN, B_MN: the operand of the columns, of the rows, has its reduction index outermost.
-template <bool A_MN, bool B_MN, bool SYM>
-__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ ProductArgs p) {
+template <bool A_MN, bool B_MN, bool SYM, bool SMALL>
+__global__ void __launch_bounds__(kThreads<SMALL>, SMALL ? 2 : 1) product_kernel(const __grid_constant__ ProductArgs p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     Header &h = *reinterpret_cast<Header *>(smem);
     const uint32_t base = smem_u32(smem) + kHeaderBytes;
@@ -321,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
         for (uint32_t a = 0; a < 2; ++a) {
             mbar_init(tfull_bar(a), 1);
-            mbar_init(tempty_bar(a), 2 * kEpiWarps);  // both CTAs'
+            mbar_init(tempty_bar(a), 2 * kEpiWarps<SMALL>);  // both CTAs'
         }
         mbar_init(drain_bar, 1);
         fence_mbar_init();
@@ -330,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         tma_prefetch_desc(&p.map_b);
     }
     if (warp == 1) {
-        tmem_alloc_pair(smem_u32(&h.tmem), kTmemCols);
+        tmem_alloc_pair(smem_u32(&h.tmem), 2 * kAccCols<SMALL>);
         tmem_relinquish_pair();
     }
     tc_fence_before();
@@ -395,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             bool ok = p.wait != 0, issued = false;  // a bound of 0: give up at once
             for (Walk<SYM> walk(p, first, stride); ok && walk.more(); walk.next()) {
                 const uint32_t idesc = kDesc | (uint32_t)(walk.get().n >> 3) << 17;
-                const uint32_t d = tmem_base + acc * kAccCols;
+                const uint32_t d = tmem_base + acc * kAccCols<SMALL>;
                 if (!__all_sync(0xffffffffu, wait_bar<true>(tempty_bar(acc), free_ph, p.wait, abort_flag))) {
                     ok = false;
                     break;
@@ -441,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         typename std::conditional<SYM, Symmetric, Update>::type epilogue{p, lane};
         for (Walk<SYM> walk(p, first, stride); walk.more(); walk.next()) {
             const Place t = walk.get();
-            const uint32_t tcol = tmem_base + ((uint32_t)(q * 32) << 16) + acc * kAccCols;
+            const uint32_t tcol = tmem_base + ((uint32_t)(q * 32) << 16) + acc * kAccCols<SMALL>;
             const int col = t.col0 + rank * half_cols + 32 * q + lane;
             if (mine && 32 * part < t.rows) epilogue.fetch(t, col, 32 * part);
             if (!__all_sync(0xffffffffu, wait_bar<true>(tfull_bar(acc), ph, p.wait, abort_flag))) {
@@ -450,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             }
             tc_fence_after();
             if (mine)
-                for (int c = 32 * part; c < t.rows; c += 32 * kParts) epilogue.finish(t, tcol, col, c, c + 32 * kParts);
+                for (int c = 32 * part; c < t.rows; c += 32 * kParts<SMALL>) epilogue.finish(t, tcol, col, c, c + 32 * kParts<SMALL>);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_bar(acc), 0));
@@ -463,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc_pair(tmem_base, kTmemCols);
+        tmem_dealloc_pair(tmem_base, 2 * kAccCols<SMALL>);
     }
 }
 
@@ -588,7 +597,7 @@ __global__ void __launch_bounds__(kNormThreads) scale_kernel(const T *g, long lo
 
 // ---------------------------------------------------------------------- host
 
-OpDone g_attr[4];
+OpDone g_attr[8];
 
 constexpr int kMaxSteps = 64;
 constexpr int kMaxParts = 64;  // CTAs of a matrix in the two kernels above
@@ -678,7 +687,6 @@ long long choose_tiles(ProductArgs &g, bool b_mn, bool sym, int sms) {
     }
     g.a_block = g.cols / 2 * kRow;
     g.b_block = b_mn ? (g.tile_rows / 2 + 63) / 64 * kChunk : g.tile_rows / 2 * kRow;
-    g.stages = std::min(kMaxStages, kStageSpace / (g.a_block + g.b_block));
     return tiles;
 }
 
@@ -697,7 +705,7 @@ CUresult operand_map(CUtensorMap *m, const Operand &o, int E, bool mn, int box) 
 struct Product {
     ProductArgs g;
     void (*kernel)(const ProductArgs);
-    int grid;
+    int grid, threads, smem;
 };
 template <bool A_MN, bool B_MN, bool SYM>
 moe_status plan(const char *name, Product &p, const Operand &a, const Operand &b, int which, int sms) {
@@ -706,14 +714,18 @@ moe_status plan(const char *name, Product &p, const Operand &a, const Operand &b
     g.tiles = (int)tiles;  // at most 65535 * 64^2
     g.wait = wait_cycles(g.red / kBK + 1);
     p.grid = 2 * (int)std::min<long long>(sms / 2, tiles);
-    p.kernel = product_kernel<A_MN, B_MN, SYM>;
+    const bool small = tiles <= sms / 2 && g.tile_rows <= 128;
+    p.kernel = small ? product_kernel<A_MN, B_MN, SYM, true> : product_kernel<A_MN, B_MN, SYM, false>;
+    p.threads = small ? kThreads<true> : kThreads<false>;
+    p.smem = small ? kSmemBytes<true> : kSmemBytes<false>;
+    g.stages = std::min(kMaxStages, (p.smem - kHeaderBytes) / (g.a_block + g.b_block));
     CUresult cr = operand_map(&g.map_a, a, g.E, A_MN, g.cols / 2);
     if (cr == CUDA_SUCCESS) cr = operand_map(&g.map_b, b, g.E, B_MN, g.tile_rows / 2);
     if (cr != CUDA_SUCCESS) return op_fail(MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", name, (int)cr);
-    return op_cuda(op_allow_smem(reinterpret_cast<const void *>(p.kernel), kSmemBytes, &g_attr[which]), name);
+    return op_cuda(op_allow_smem(reinterpret_cast<const void *>(p.kernel), p.smem, &g_attr[2 * which + small]), name);
 }
 cudaError_t launch(const Product &p, cudaStream_t s) {
-    return launch_pdl_cluster(p.kernel, dim3(p.grid), dim3(kThreads), (size_t)kSmemBytes, s, dim3(2, 1, 1), p.g);
+    return launch_pdl_cluster(p.kernel, dim3(p.grid), dim3(p.threads), (size_t)p.smem, s, dim3(2, 1, 1), p.g);
 }
 
 moe_status check_sizes(const char *name, int E, int N, int K) {
