@@ -39,9 +39,11 @@ namespace moe {
 namespace {
 
 constexpr int kMaxH = 8192;
-constexpr int kThreads = 512;      // of a CTA, one per SM
-constexpr int kMaxTeams = kThreads / 32;
-constexpr int kSmem = 212 << 10;   // dynamic shared memory, most
+// Threads of a CTA, one per SM: as many as have the registers (backward with 640: 16384 x 2048 111 us
+// for 86, spills; forward with 512: 8192 x 4104 96 us for 76, one team where there could be two).
+constexpr int kForwardThreads = 768, kBackwardThreads = 512;
+constexpr int kMaxTeams = kForwardThreads / 32;
+constexpr int kSmem = 206 << 10;   // dynamic shared memory, most
 constexpr int kMaxCtas = 256;
 constexpr float kDown = 0x1p-100f;
 constexpr int kMaxStages = 2;  // rows (8192 x 2048 with an fp32 stream: 39 us, with 3 41, with 4 43)
@@ -290,7 +292,7 @@ __device__ __forceinline__ void leave(Shared &sh) {
 
 // V: groups of 8 values per thread, `team` threads apart.
 template <typename TX, typename TF, int V>
-__global__ void __launch_bounds__(kThreads, 1) norm_forward_kernel(const SandwichArgs p) {
+__global__ void __launch_bounds__(kForwardThreads, 1) norm_forward_kernel(const SandwichArgs p) {
     extern __shared__ float4 smem[];  // the effective weights, the rings
     __shared__ __align__(16) Shared sh;
     Team team(sh.slots, p.team);
@@ -392,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_forward_kernel(const Sandwic
 
 // CHANNEL: the gate is one per channel.
 template <typename TX, typename TF, int V, bool CHANNEL>
-__global__ void __launch_bounds__(kThreads, 1) norm_backward_kernel(const SandwichArgs p) {
+__global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_kernel(const SandwichArgs p) {
     // the effective weights and the channels' gate (where they fit), and the rings; later the teams' sums
     extern __shared__ float4 smem[];
     __shared__ __align__(16) Shared sh;
@@ -622,9 +624,9 @@ OpDone g_attr[24];
 int most_teams(int team) { return team > 32 ? 15 : kMaxTeams; }
 
 // Threads per team and teams per CTA: as many as fit, fewer where rows would leave SMs without one.
-void shape(int T, int H, int sms, int per, int &team, int &teams) {
+void shape(int T, int H, int sms, int per, int threads, int &team, int &teams) {
     team = 32 * ((H + 32 * per - 1) / (32 * per));
-    teams = std::max(1, std::min(std::min(kThreads / team, most_teams(team)), (T + sms - 1) / sms));
+    teams = std::max(1, std::min(std::min(threads / team, most_teams(team)), (T + sms - 1) / sms));
 }
 
 struct Buffer {
@@ -691,7 +693,7 @@ moe_status launch(const char *name, bool backward, SandwichArgs &a, int x_dtype,
     const bool two = a.H > 256;
     const Choice c = two ? choose<2>(x_dtype, f_dtype, backward, channel) : choose<1>(x_dtype, f_dtype, backward, channel);
     int teams;
-    shape(a.T, a.H, sms, two ? 16 : 8, a.team, teams);
+    shape(a.T, a.H, sms, two ? 16 : 8, backward ? kBackwardThreads : kForwardThreads, a.team, teams);
     grid = (int)std::min<long long>(std::min(sms, kMaxCtas), ((long long)a.T + teams - 1) / teams);
     // X and F, backward also their gradients, of a row of each team
     const int stage = teams * a.H * ((x_dtype == MOE_DTYPE_F32 ? 4 : 2) + (f_dtype == MOE_DTYPE_F32 ? 4 : 2)) * (backward ? 2 : 1);
