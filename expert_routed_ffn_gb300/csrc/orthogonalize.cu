@@ -600,9 +600,9 @@ __global__ void __launch_bounds__(kNormThreads) scale_kernel(const T *g, long lo
 OpDone g_attr[8];
 
 constexpr int kMaxSteps = 64;
-constexpr int kMaxParts = 64;  // CTAs of a matrix in the two kernels above
-
-int parts_of(long long size) { return (int)std::min<long long>(kMaxParts, (size + kBlock - 1) / kBlock); }
+// CTAs of a matrix in the two kernels above: about 2048 in all, each with a block of values at least
+// (with at most 64 a matrix, 2048 x 2048 in fp32 took 18 and 23 us)
+int parts_of(int E, long long size) { return (int)std::min<long long>(std::max(1, 2048 / std::max(1, E)), (size + kBlock - 1) / kBlock); }
 
 struct Workspace {
     size_t table, partial, x[2], lo, a, b, bytes;
@@ -614,7 +614,7 @@ Workspace lay_out(int E, int N, int K) {
     Workspace w;
     w.table = 0;
     w.partial = w.table + room(e * sizeof(float));
-    w.x[0] = w.partial + room(e * kMaxParts * sizeof(double));
+    w.x[0] = w.partial + room(e * parts_of(E, (long long)n) * sizeof(double));
     w.x[1] = w.x[0] + room(2 * e * n);
     w.lo = w.x[1] + room(2 * e * n);
     w.a = w.lo + room(2 * e * n);
@@ -658,8 +658,12 @@ bool choose_scales(const float *coef, int steps, Scales *scales, float *up) {
     return true;
 }
 
-// Tile sizes: 256 x 256, of fewer rows (down to 32) while the pairs outnumber the tiles; a matrix's
-// rows are dealt evenly to its tiles, in multiples of 32.
+// Tile sizes: 256 columns (128 where there are no more) and 32 to 256 rows, dealt evenly to a
+// matrix's tiles in multiples of 32 (the pair's MMA takes N in steps of 32); what takes the least
+// time by: waves of tiles times a tile's stages, each 150 + 0.6 ns for each row (the copies of 128
+// columns and half of the rows to an SM at 110 bytes a ns, or as long for the MMAs), 600 ns to fill
+// the pipeline, and at the end an epilogue.  (256 rows, halved while the pairs outnumber the tiles: 4096
+// x 4096 1012 us for 882, 2 x 1408 x 2048 270 for 241, 4 x 1024 x 1024 188 for 175.)
 long long count_tiles(const ProductArgs &g, bool sym) {
     if (!sym) return (long long)g.E * g.row_tiles * g.col_tiles;
     long long n = 0;
@@ -670,21 +674,23 @@ long long choose_tiles(ProductArgs &g, bool b_mn, bool sym, int sms) {
     g.cols = g.C > 128 ? 256 : 128;
     g.col_shift = g.cols == 256 ? 8 : 7;
     g.col_tiles = (g.C + g.cols - 1) / g.cols;
+    const long long pairs = sms / 2;
     long long tiles = 0;
-    for (int rows = 256; rows >= 32; rows /= 2) {
+    double least = 0.0;
+    int best = 0;
+    for (int rows = 256; rows >= 32; rows -= 32) {
         const int parts = (g.R + rows - 1) / rows;
-        const int share = ((g.R + parts - 1) / parts + 31) / 32 * 32;  // the pair's MMA takes N in steps of 32
-        const ProductArgs before = g;
+        const int share = ((g.R + parts - 1) / parts + 31) / 32 * 32;
+        if (share != rows && rows < 256) continue;  // the same as a size before
         g.tile_rows = share;
         g.row_tiles = (g.R + share - 1) / share;
-        const long long now = count_tiles(g, sym);
-        if (tiles > 0 && now > sms / 2) {
-            g = before;
-            break;
-        }
-        tiles = now;
-        if (2 * now > sms / 2) break;
+        const long long waves = (count_tiles(g, sym) + pairs - 1) / pairs;
+        const double cost = waves * ((g.red + kBK - 1) / kBK * (150 + 0.6 * share) + 600) + 8.0 * share;
+        if (best == 0 || cost < least) best = share, least = cost;
     }
+    g.tile_rows = best;
+    g.row_tiles = (g.R + best - 1) / best;
+    tiles = count_tiles(g, sym);
     g.a_block = g.cols / 2 * kRow;
     g.b_block = b_mn ? (g.tile_rows / 2 + 63) / 64 * kChunk : g.tile_rows / 2 * kRow;
     return tiles;
@@ -807,7 +813,7 @@ extern "C" moe_status moe_orthogonalize(const void *G, int dtype, int E, int N, 
     if (st != MOE_OK) return st;
 
     const long long size = (long long)N * K;
-    const int parts = parts_of(size);
+    const int parts = parts_of(E, size);
     const dim3 grid((unsigned)(E * parts));
     // X0 of bf16 values is exact
     half *lo0 = dtype == MOE_DTYPE_F32 && keeps_lo(0, steps) ? lo : nullptr;
