@@ -91,6 +91,9 @@ moe_status start(const char *name, GroupedArgs &g, int op, const Sizes &z, const
     o.m_dense = 1;
     o.red = red;
     o.f32 = f32;
+    // fp32 results: the products' segments of 256 instructions, 3.0e-6 off (2-norm) over 2 x 1408 columns.  With
+    // 64 they would be 9e-7 off and take 220 us for 208 (24576 rows, 64 experts), with 32 4.6e-7 and 237:
+    // the operands are bf16, whose own roundings are 2^-9
     o.segment = segment_of(f32, 16);
     o.wait = wait_cycles(red / kBK + 1);
     const int sms = op_num_sms();
