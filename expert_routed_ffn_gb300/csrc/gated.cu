@@ -33,7 +33,12 @@
 namespace moe {
 namespace {
 
-OpDone g_attr[9];
+OpDone g_attr[12];
+
+// Products that one accumulator sums for fp32 results: 32 instructions, 4.6e-7 off (2-norm) over 2 x 1408
+// columns where a sum in fp32 is 3e-7 off, and at 24576 rows of 64 experts 209 us.  With 256, as the
+// single products' have, 3.0e-6 and 206; 64 9.3e-7 and 207; 16 2.4e-7 and 217.  A multiple of a stage's 128.
+constexpr int kExactSegment = 32 * 16;
 
 struct Sizes {
     int rows, E, I, K;
@@ -91,16 +96,13 @@ moe_status start(const char *name, GroupedArgs &g, int op, const Sizes &z, const
     o.m_dense = 1;
     o.red = red;
     o.f32 = f32;
-    // fp32 results: the products' segments of 256 instructions, 3.0e-6 off (2-norm) over 2 x 1408 columns.  With
-    // 64 they would be 9e-7 off and take 220 us for 208 (24576 rows, 64 experts), with 32 4.6e-7 and 237:
-    // the operands are bf16, whose own roundings are 2^-9
-    o.segment = segment_of(f32, 16);
+    o.segment = f32 ? kExactSegment : segment_of(false, 16);
     o.wait = wait_cycles(red / kBK + 1);
     const int sms = op_num_sms();
     o.err = op_error_word();
     if (sms < 2 || o.err == nullptr) return op_fail(MOE_ERR_CUDA, "%s: no usable current device", name);
     segments = red > o.segment;
-    blocks = choose_tiles(g, op, segments, sms);
+    blocks = choose_tiles(g, op, segments && op != kDgradTwo, sms);
     tiles = ((long long)z.rows / o.tile_rows + std::min(z.E, z.rows)) * o.col_tiles;
     if (tiles > (1ll << 30)) return op_fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^30 output tiles", name);
     return MOE_OK;
@@ -125,11 +127,14 @@ moe_status go(const char *name, const typename ArgsOf<OP>::type &g, CUresult cr,
     if (cr != CUDA_SUCCESS) return op_fail(MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", name, (int)cr);
     const dim3 grid(2u * (unsigned)std::min<long long>(op_num_sms() / 2, tiles));
     auto launch = [&](auto kernel, int which) -> cudaError_t {
-        const cudaError_t ce = op_allow_smem(reinterpret_cast<const void *>(kernel), kSmemBytes, &g_attr[3 * (OP - kGated) + which]);
+        const cudaError_t ce = op_allow_smem(reinterpret_cast<const void *>(kernel), kSmemBytes, &g_attr[4 * (OP - kGated) + which]);
         return ce != cudaSuccess ? ce
                                  : launch_pdl_cluster(kernel, grid, dim3((unsigned)kThreads<OP>), (size_t)kSmemBytes,
                                                       reinterpret_cast<cudaStream_t>(stream), dim3(2, 1, 1), g);
     };
+    if constexpr (OP == kDgradTwo) {
+        if (segments && blocks == 2) return op_cuda(launch(grouped_kernel<OP, 2, false, true>, 3), name);
+    }
     return op_cuda(segments      ? launch(grouped_kernel<OP, 1, false, true>, 0)
                    : blocks == 1 ? launch(grouped_kernel<OP, 1, false, false>, 1)
                                  : launch(grouped_kernel<OP, 2, false, false>, 2),

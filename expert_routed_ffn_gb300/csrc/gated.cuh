@@ -107,6 +107,37 @@ __device__ __forceinline__ void add_gated_segment(const Tile &t, uint32_t acc, u
     tmem_st_wait();
 }
 
+// The running sums of a tile's segments, to nearest, in the registers of the warps that store them: a warp
+// has its 32-row chunks of store_tile.  Segments so take the two accumulators in turn, and the MMA goes
+// on with one while the other is added here; with the sums in tensor memory (add_segment) it waits for
+// each segment's addition (32 instructions a segment, 24576 rows of 64 experts: 237 for 209 us).  The roles that
+// feed the tensor core walk tiles, not segments: finding the tile again took 0.6 us a segment.
+// The last segment's sums end in its accumulator, where store_tile reads them.
+template <int PARTS>
+struct RegisterSums {
+    static constexpr int kPieces = 2 * (256 / 32 / PARTS);  // of 16 rows
+    float sum[kPieces][16];
+    __device__ __forceinline__ void add(const Tile &t, uint32_t acc, int part, bool last) {
+#pragma unroll
+        for (int g = 0; g < kPieces; ++g) {
+            const int c = 32 * (part + PARTS * (g / 2)) + 16 * (g % 2);
+            if (c < t.rows) {
+                uint32_t v[16];
+                tmem_ld16(acc + c, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    asm volatile("" : "+r"(v[i]));  // not read before the wait
+                    sum[g][i] += __uint_as_float(v[i]);
+                    v[i] = __float_as_uint(sum[g][i]);
+                }
+                if (last) tmem_st16(acc + c, v);
+            }
+        }
+        if (last) tmem_st_wait();
+    }
+};
+
 // Forward.  The MMA's columns alternate 16 of the gate's and the same 16 of the up projection's, so
 // that lanes l and l + 16 of a warp hold both values of a column: lane l takes the first half of a
 // chunk's rows, lane l + 16 the second, exchanged by shuffles.  (With 64 columns of each in the

@@ -103,6 +103,8 @@ __device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
 template <int OP, int BLOCKS, bool ADD, bool SEGMENTS>
 __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_constant__ typename ArgsOf<OP>::type p) {
     constexpr bool kDense = OP == kWgrad;
+    constexpr bool kRegisters = SEGMENTS && OP == kDgradTwo;  // a tile's segments: RegisterSums
+    constexpr bool kWalkSegments = SEGMENTS && !kRegisters;
     extern __shared__ __align__(1024) uint8_t smem[];
     Header &h = *reinterpret_cast<Header *>(smem);
     const TileTable &tab = h.table;
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
         uint32_t ph = 1;
         int s = 0;
         bool ok = true;
-        for (TileWalk<kDense, SEGMENTS> walk(tab, first, stride); ok && walk.more(); walk.next()) {
+        for (TileWalk<kDense, kWalkSegments> walk(tab, first, stride); ok && walk.more(); walk.next()) {
             const Tile t = walk.get();
             const int col = t.col0 + rank * half_cols, row = t.row0 + rank * (t.n / 2);
             const bool two_b = t.n / 2 > 64;  // MN-major B: two chunks of 64 columns
@@ -253,15 +255,21 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
             uint32_t ph = 0, zeroed_ph = 0;
             int s = 0;
             bool ok = p.o.wait != 0, issued = false;  // a bound of 0: give up at once
-            TileWalk<kDense, SEGMENTS> walk(tab, first, stride);
+            TileWalk<kDense, kWalkSegments> walk(tab, first, stride);
             Tile next;
+            [[maybe_unused]] int at = 0;  // kRegisters: the first of the segment's reduction steps
             auto advance = [&]() {
                 walk.next();
                 if (walk.more()) next = walk.get();
             };
             if (walk.more()) next = walk.get();
             while (ok && walk.more()) {
-                const Tile t = next;
+                Tile t = next;
+                if (kRegisters) {
+                    t.r0 = at;
+                    t.r1 = min(t.r1, at + tab.o.segment);
+                    at = t.r1 == tab.o.red ? 0 : t.r1;
+                }
                 if (t.r0 >= t.r1) {  // an expert without rows: the epilogue writes its zeros
                     advance();
                     continue;
@@ -304,7 +312,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
                     __syncwarp();
                     issued = true;
                     // the next tile's place, while this one's products run
-                    if (r == t.r0) advance();
+                    if (r == t.r0 && (!kRegisters || at == 0)) advance();
                     if (++s == stages) {
                         s = 0;
                         ph ^= 1u;
@@ -328,7 +336,7 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
         // all their stages do: the bound grows with them, by as much a stage as in wait_cycles.
         long long passed = 0;
         const int chunks_a = half_cols / 64;
-        for (TileWalk<kDense, SEGMENTS> walk(tab, first, stride); walk.more(); walk.next()) {
+        for (TileWalk<kDense, kWalkSegments> walk(tab, first, stride); walk.more(); walk.next()) {
             const Tile t = walk.get();
             const int whole = (t.r1 - t.r0) / (BLOCKS * kBK), rest = t.r1 - t.r0 - whole * (BLOCKS * kBK);
             const int tile_stages = whole + (rest + kBK - 1) / kBK;
@@ -366,10 +374,11 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
             __syncwarp();
             if (lane == 0) mbar_arrive_pair(mapa_shared(tempty_bar(a), 0));
         };
-        for (TileWalk<kDense, SEGMENTS> walk(tab, first, stride); walk.more(); walk.next()) {
+        for (TileWalk<kDense, kWalkSegments> walk(tab, first, stride); walk.more(); walk.next()) {
             const Tile t = walk.get();
             const bool empty = t.r0 >= t.r1;
-            const uint32_t a = accs.next, tmem_q = tmem_base + ((uint32_t)(q * 32) << 16);
+            uint32_t a = accs.next;
+            const uint32_t tmem_q = tmem_base + ((uint32_t)(q * 32) << 16);
             const int col = t.col0 + rank * half_cols + in_half;
             if constexpr (OP == kGatedBack) {
                 if (t.last && mine && kGatedRows * part < t.rows) back.fetch(h.gated, t, col, kGatedRows * part, lane);
@@ -382,7 +391,25 @@ __global__ void __launch_bounds__(kThreads<OP>, 1) grouped_kernel(const __grid_c
                 tc_fence_after();
             }
             uint32_t from = a;
-            if (SEGMENTS && !(t.first && t.last)) {
+            if constexpr (kRegisters) {
+                RegisterSums<kParts<OP>> sums = {};
+                bool ok = true;
+                for (int at = tab.o.segment; at < tab.o.red; at += tab.o.segment) {
+                    if (mine) sums.add(t, tmem_q + a * kAccCols, part, false);
+                    release(a);
+                    accs.done(t);
+                    a = accs.next;
+                    ok = __all_sync(0xffffffffu, wait_bar<true>(tfull_bar(a), accs.ready(), p.o.wait, abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                if (!ok) {
+                    if (lane == 0) raise();
+                    break;
+                }
+                if (mine) sums.add(t, tmem_q + a * kAccCols, part, true);
+                from = a;
+            } else if (SEGMENTS && !(t.first && t.last)) {
                 from = a ^ 1u;
                 if constexpr (OP == kGated || OP == kGatedBack) {
                     if (mine) add_gated_segment<kParts<OP>>(t, tmem_q + a * kAccCols, tmem_q + from * kAccCols, part);

@@ -413,7 +413,8 @@ moe_status moe_grouped_wgrad(const void *dY, const void *X, const int32_t *offs,
  *             are given, to be kept for the backward pass; H comes from the unrounded sums
  *   backward: from dY, the gradient of what the down projection Wd made of H: dH = dY Wd (held in
  *             fp32 only), dG = dH dact/dG, dU = dH dact/dU at the G and U given
- *   dgrad:    dX = dG Wg + dU Wu, rounded once
+ *   dgrad:    dX = dG Wg + dU Wu, rounded once; fp32 results are summed by the tensor core over
+ *             512 products at most (an error of 2^-18 of the products' magnitudes), to nearest from there
  * act (moe_act) with alpha, limit and beta as in moe_config (ignored for MOE_ACT_SILU; else limit > 0,
  * alpha and beta finite).  The clamped activation passes gradients at the limit and none beyond
  * it.  The weights' gradients are moe_grouped_wgrad(dG, X), (dU, X) and (dY, H).  Rows, offsets,

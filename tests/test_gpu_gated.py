@@ -170,6 +170,22 @@ def test_dgrad(name, dtype):
     assert again.dtype == dtype and torch.equal(again[own], out[own])
 
 
+@pytest.mark.parametrize("I", [256, 264, 512, 768, 1400, 8200])
+@pytest.mark.parametrize("counts", [[1, 0, 37, 64], [300, 1, 513]])
+def test_dgrad_fp32_sums_are_exact_ones(counts, I):
+    # Operands of one sign, where truncation shows most.  A segment's 32 additions lose up to 2^-23 of
+    # its sum each, the sums of segments 2^-24 of the whole each: 2^-18 + segments 2^-24.
+    K, rows = 328, sum(counts)
+    gen = torch.Generator(device="cuda").manual_seed(29)
+    dG, dU = _bf16(gen, rows, I).abs(), _bf16(gen, rows, I).abs()
+    Wg, Wu = _bf16(gen, len(counts), I, K).abs(), _bf16(gen, len(counts), I, K).abs()
+    offs = _offs(counts)
+    out = capi.grouped_gated_dgrad(dG, dU, Wg, Wu, offs, out_dtype=torch.float32)
+    ref = _product(dG, Wg, offs, False)[0] + _product(dU, Wu, offs, False)[0]
+    segments = -(-2 * (I + 63) // 512)
+    _near(out, ref, (2.0 ** -18 + segments * 2.0 ** -24) * ref, _own(rows, offs))
+
+
 @pytest.mark.parametrize("act", ["silu", "swigluoai"])
 def test_gradients_against_differences(act):
     """The backward chain against central differences of the fp64 block, in random directions.
