@@ -110,8 +110,8 @@ __device__ __forceinline__ void add_gated_segment(const Tile &t, uint32_t acc, u
 // The running sums of a tile's segments, to nearest, in the registers of the warps that store them: a warp
 // has its 32-row chunks of store_tile.  Segments so take the two accumulators in turn, and the MMA goes
 // on with one while the other is added here; with the sums in tensor memory (add_segment) it waits for
-// each segment's addition (32 instructions a segment, 24576 rows of 64 experts: 237 for 209 us).  The roles that
-// feed the tensor core walk tiles, not segments: finding the tile again took 0.6 us a segment.
+// each segment's addition (32 instructions a segment, 24576 rows of 64 experts: 237 for 209 us).  All
+// roles walk tiles and count the segments inside (walking segments, as the other long sums do, 218).
 // The last segment's sums end in its accumulator, where store_tile reads them.
 template <int PARTS>
 struct RegisterSums {
