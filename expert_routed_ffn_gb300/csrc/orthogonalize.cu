@@ -604,13 +604,16 @@ constexpr int kMaxSteps = 64;
 // (with at most 64 a matrix, 2048 x 2048 in fp32 took 18 and 23 us)
 int parts_of(int E, long long size) { return (int)std::min<long long>(std::max(1, 2048 / std::max(1, E)), (size + kBlock - 1) / kBlock); }
 
+// Offsets from the workspace rounded up to kRoom bytes: the rows of A and B are read and written 32
+// bytes at a time, and callers' workspaces are only sure to begin at 16.
+constexpr size_t kRoom = 1024;
 struct Workspace {
     size_t table, partial, x[2], lo, a, b, bytes;
 };
 int padded(int m) { return (m + 15) / 16 * 16; }  // rows of A and B begin at 32-byte boundaries
 Workspace lay_out(int E, int N, int K) {
     const size_t n = (size_t)N * K, m = std::min(N, K), e = E;
-    auto room = [](size_t bytes) { return (bytes + 1023) / 1024 * 1024; };
+    auto room = [](size_t bytes) { return (bytes + kRoom - 1) / kRoom * kRoom; };
     Workspace w;
     w.table = 0;
     w.partial = w.table + room(e * sizeof(float));
@@ -619,7 +622,7 @@ Workspace lay_out(int E, int N, int K) {
     w.lo = w.x[1] + room(2 * e * n);
     w.a = w.lo + room(2 * e * n);
     w.b = w.a + room(2 * e * m * padded((int)m));
-    w.bytes = w.b + room(2 * e * m * padded((int)m));
+    w.bytes = w.b + room(2 * e * m * padded((int)m)) + kRoom - 16;  // and what rounding up may take
     return w;
 }
 
@@ -787,7 +790,7 @@ extern "C" moe_status moe_orthogonalize(const void *G, int dtype, int E, int N, 
     int *err = op_error_word();
     if (sms < 2 || err == nullptr) return op_fail(MOE_ERR_CUDA, "%s: no usable current device", name);
 
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    uint8_t *ws = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(workspace) + kRoom - 1) / kRoom * kRoom);
     float *table = reinterpret_cast<float *>(ws + w.table);
     double *partial = reinterpret_cast<double *>(ws + w.partial);
     half *x[2] = {reinterpret_cast<half *>(ws + w.x[0]), reinterpret_cast<half *>(ws + w.x[1])};

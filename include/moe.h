@@ -495,8 +495,9 @@ moe_status moe_mx_grouped_forward(const void *Xc, const uint8_t *Xs, const void 
  * fp32; the low half of X is carried through a X in all steps but the last two.  Coefficients that
  * let singular values from [0, 1] grow beyond 1024 are refused.  A matrix with an infinity or a
  * NaN gives NaN, and no other does.  N and K multiples of 8 up to 16384, E up to 65535 (0: no-op); eps >= 1e-30.
- * `workspace` as in moe_clip_grad_norm.  Errors: INVALID_ARG, UNSUPPORTED, CUDA; a wait that
- * runs out is reported by moe_operators_status. */
+ * `workspace` as in moe_clip_grad_norm (16-byte aligned; the size has room for the call to round its
+ * beginning up).  Errors: INVALID_ARG, UNSUPPORTED, CUDA; a wait that runs out is reported by
+ * moe_operators_status. */
 moe_status moe_orthogonalize_workspace(int E, int N, int K, size_t *bytes);
 moe_status moe_orthogonalize(const void *G, int dtype, int E, int N, int K, const float *coefficients, int steps,
                              float eps, float scale, void *out, void *workspace, size_t workspace_bytes,
