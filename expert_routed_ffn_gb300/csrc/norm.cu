@@ -32,6 +32,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "grouped.cuh"
 #include "kernels.h"
 #include "moe.h"
 #include "op_host.h"
@@ -48,7 +49,6 @@ constexpr int kSmem = 206 << 10;   // dynamic shared memory, most
 constexpr int kMaxCtas = 256;      // a partial sum of the weights' gradients each
 constexpr float kDown = 0x1p-100f;
 constexpr int kMaxStages = 2;  // rows (8192 x 2048 with an fp32 stream: 39 us, with 3 41, with 4 43)
-constexpr uint64_t kWaitNs = 2000000000ull;  // bound of the wait for a row
 
 struct SandwichArgs {
     const void *x, *f;
@@ -60,6 +60,7 @@ struct SandwichArgs {
     float alpha, eps, one;  // one: added to the weights
     int T, H, gate_kind, team;  // team: threads
     int *err;
+    uint64_t wait_ns;       // bound of the wait for a row
     int stages;             // rows in flight, the present one among them
     bool weights_in_smem;   // backward
 };
@@ -225,12 +226,14 @@ struct Ring {
             parity ^= 1u;
         }
     }
-    // Bounded: after it a row's values are whatever is there, the error is recorded, and no later
-    // wait of the CTA takes time.
-    __device__ __forceinline__ void wait(volatile int *abort, int *err) const {
-        if (mbar_wait(bars + 8 * stage, parity, kWaitNs, abort)) return;
-        *abort = 1;
-        atomicOr(err, ERR_TIMEOUT);
+    // False: the row is not there within the bound (0: give up at once).  Lanes may differ (one answer for
+    // a warp cost the gradients up to 5%).
+    __device__ __forceinline__ bool wait(uint64_t limit_ns, volatile int *abort) const {
+        return limit_ns != 0 && mbar_wait(bars + 8 * stage, parity, limit_ns, abort);
+    }
+    // After such a wait for `row`: wait for the copies in flight, again with a bound.
+    __device__ __forceinline__ void drain(int row, int stride, int T) {
+        for (int s = 0; s < stages && row < T; ++s, row += stride, next()) wait_bar(bars + 8 * stage, parity, kDrainCycles, nullptr);
     }
     __device__ __forceinline__ uint32_t present() const { return rows + stage * bytes; }
     // 8 values in shared memory
@@ -261,8 +264,21 @@ struct Shared {
     float slots[kMaxTeams * kSlots];
     uint64_t bars[kMaxTeams * kMaxStages];
     uint4 zeros[2];  // what lanes beyond H read
-    int abort;
+    int abort;       // a wait of the CTA ran out: no later one takes time
+    int lost[kMaxTeams];  // the row that a team did not get, see lost_row
 };
+// A thread's wait for `row` ran out.  It goes on with whatever is there up to the team's next sum, which it
+// makes a NaN: where a sum is not finite all of the team's threads look here and leave, so nobody asks
+// for another row.  A row is given by its number, so that a thread that is a row ahead is not taken for it.
+__device__ __forceinline__ void lose_row(Shared &sh, const Team &team, int row, int *err) {
+    *(volatile int *)&sh.lost[team.id] = row;
+    *(volatile int *)&sh.abort = 1;
+    atomicOr(err, ERR_TIMEOUT);
+}
+__device__ __forceinline__ bool lost_row(const Shared &sh, const Team &team, int row) {
+    __syncwarp();  // (a team of one warp has passed no other barrier)
+    return *(const volatile int *)&sh.lost[team.id] == row;
+}
 __device__ __forceinline__ Ring make_ring(Shared &sh, const Team &team, uint32_t rings, uint32_t row_bytes, int stages) {
     Ring r;
     r.rows = rings + team.id * stages * row_bytes;
@@ -272,6 +288,7 @@ __device__ __forceinline__ Ring make_ring(Shared &sh, const Team &team, uint32_t
     r.stage = 0;
     r.parity = 0;
     for (int i = threadIdx.x; i < kMaxTeams * kSlots; i += blockDim.x) sh.slots[i] = 0.0f;
+    if (threadIdx.x < kMaxTeams) sh.lost[threadIdx.x] = -1;
     if (threadIdx.x == 0) {
         sh.abort = 0;
         sh.zeros[0] = sh.zeros[1] = make_uint4(0, 0, 0, 0);
@@ -281,14 +298,6 @@ __device__ __forceinline__ Ring make_ring(Shared &sh, const Team &team, uint32_t
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     return r;
-}
-// The rows are waited for one by one, so that only after an abort a copy may be in flight: it is given a fixed time.
-__device__ __forceinline__ void leave(Shared &sh) {
-    __syncthreads();
-    if (*(volatile int *)&sh.abort) {
-        const uint64_t t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < 1000000ull) __nanosleep(1000);
-    }
 }
 
 // V: groups of 8 values per thread, `team` threads apart.
@@ -335,7 +344,8 @@ __global__ void __launch_bounds__(kForwardThreads, 1) norm_forward_kernel(const 
     for (; row < p.T; row += stride, ring.next()) {
         const float gate = gate_next;
         if (token && row + stride < p.T) gate_next = p.gate[row + stride];
-        ring.wait(&sh.abort, p.err);
+        const bool got = ring.wait(p.wait_ns, &sh.abort);
+        if (!got) lose_row(sh, team, row, p.err);
         const size_t base = (size_t)row * H;
         f2 x[V][4], f[V][4], w[4];
         auto squares = [&](const f2 (&v)[V][4], float scale) {  // (values beyond H are zeros)
@@ -347,13 +357,15 @@ __global__ void __launch_bounds__(kForwardThreads, 1) norm_forward_kernel(const 
                     const f2 a = scale != 1.0f ? mul2(v[i][j], both(scale)) : v[i][j];
                     s = fma2(a, a, s);
                 }
-            float total = sum_of(s);
+            float total = got ? sum_of(s) : NAN;
             team.sum(total);
             return total;
         };
+        bool lost = false;
         auto norm = [&](const f2 (&v)[V][4]) {
             float ss = squares(v, 1.0f);
             if (ss < INFINITY) return inverse_root(ss, inv_h, p.eps);
+            lost = lost_row(sh, team, row);
             ss = squares(v, kDown);
             return inverse_root(ss, inv_h, p.eps * kDown * kDown) * kDown;
         };
@@ -367,6 +379,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) norm_forward_kernel(const 
             float rf = gate;
             if (has_post) {
                 rf *= norm(f);
+                if (lost) break;
                 if (me == 0) ask(row + p.stages * stride, ring.stage);  // the team has read the row
             }
 #pragma unroll
@@ -377,7 +390,10 @@ __global__ void __launch_bounds__(kForwardThreads, 1) norm_forward_kernel(const 
                 if (in[i]) store8(static_cast<TX *>(p.xo) + base + 8 * group[i], x[i]);
             }
         }
-        if (!has_post && !has_pre) team.sync();
+        if (!has_post && !has_pre) {
+            team.sync();
+            lost = lost_row(sh, team, row);
+        }
         if (has_pre) {
             const float rx = norm(x);
 #pragma unroll
@@ -388,9 +404,12 @@ __global__ void __launch_bounds__(kForwardThreads, 1) norm_forward_kernel(const 
                 if (in[i]) store8(static_cast<TF *>(p.fo) + base + 8 * group[i], w);
             }
         }
-        if (!has_post && me == 0) ask(row + p.stages * stride, ring.stage);
+        if (!has_post) {
+            if (lost) break;
+            if (me == 0) ask(row + p.stages * stride, ring.stage);
+        }
     }
-    leave(sh);
+    if (row < p.T) ring.drain(row, stride, p.T);
 }
 
 // CHANNEL: the gate is one per channel.
@@ -472,7 +491,8 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_kernel(cons
         // What is not there is zeros or ones, so that the values take no branches.
         const float g = gate_next, alpha = has_f ? p.alpha : 1.0f;
         if (token && row + stride < p.T) gate_next = p.gate[row + stride];
-        ring.wait(&sh.abort, p.err);
+        const bool got = ring.wait(p.wait_ns, &sh.abort);
+        if (!got) lose_row(sh, team, row, p.err);
         const size_t base = (size_t)row * H;
         f2 x[V][4], dn[V][4], f[V][4], w[4];
         uint32_t at_x[V], at_f[V];  // a thread's values of the first tensor of either type in this stage
@@ -499,11 +519,12 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_kernel(cons
                     dx = fma2(mul2(dn[i][j], w[j]), a, dx);
                 }
             }
-            s0 = sum_of(xx), s1 = sum_of(ff), s2 = sum_of(dx);
+            s0 = got ? sum_of(xx) : NAN, s1 = sum_of(ff), s2 = sum_of(dx);
             team.sum(s0, s1, s2);
         };
         sums(false);
         if (!(s0 < INFINITY) || !(s1 < INFINITY)) {
+            if (lost_row(sh, team, row)) break;
             if (!(s0 < INFINITY)) sx = kDown;
             if (!(s1 < INFINITY)) sf = kDown;
             sums(true);
@@ -561,11 +582,12 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_kernel(cons
             if (in[i]) store8(static_cast<TF *>(p.fo) + base + 8 * group[i], w);
         }
     }
-    leave(sh);
+    if (row < p.T) ring.drain(row, stride, p.T);
 
     // the teams' sums one after the other, then this CTA's
     const int teams = blockDim.x / p.team;
     __syncthreads();
+    if (*(volatile int *)&sh.abort) return;  // (a copy that did not end may still write to shared memory)
     for (int k = 0; k < teams; ++k) {
         if (team.id == k) {
 #pragma unroll
@@ -702,6 +724,7 @@ moe_status launch(const char *name, bool backward, SandwichArgs &a, int x_dtype,
     a.weights_in_smem = weights + stage <= kSmem;
     a.stages = std::min(kMaxStages, (kSmem - (a.weights_in_smem ? weights : 0)) / stage);
     a.err = op_error_word();
+    a.wait_ns = ((uint64_t)wait_cycles(0) + 1) / 2;  // of cycles at 2 GHz; 0 for 0 alone
     if (a.err == nullptr) return op_fail(MOE_ERR_CUDA, "%s: no usable current device", name);
     const int smem = std::max(weights, (a.weights_in_smem ? weights : 0) + a.stages * stage);
     const cudaError_t e = op_allow_smem(reinterpret_cast<const void *>(c.kernel), kSmem, &g_attr[c.which]);

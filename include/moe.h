@@ -379,9 +379,9 @@ moe_status moe_dispatch_noalloc(const int32_t *topk_idx, int T, int k, int E, in
  * next call.  Not during a stream capture. */
 moe_status moe_operators_status(void);
 
-/* Bound of the device-side waits of the products (grouped, gated, of orthogonalised updates) launched
- * from now on, in SM clock cycles, for the whole process: -1 (the start) is about 2 s and more for very long sums; 0
- * makes the products give up at their first wait for data, which exercises the timeout path.
+/* Bound of the device-side waits of the products (grouped, gated, of orthogonalised updates) and of the
+ * norms' rows launched from now on, in SM clock cycles, for the whole process: -1 (the start) is about 2 s
+ * and more for very long sums; 0 makes them give up at their first wait for data, which exercises the timeout path.
  * Weight gradients add what the tiles passed so far may take.  Errors: INVALID_ARG. */
 moe_status moe_operators_wait_limit(long long cycles);
 
@@ -446,8 +446,8 @@ moe_status moe_grouped_gated_dgrad(const void *dG, const void *dU, const void *W
  * output is refused.  H: a multiple of 8 up to 8192, T up to 2^30; eps >= 1e-30.  Rows of any magnitude are normed (sums of squares beyond fp32
  * are taken again of scaled values); a row with an infinity or a NaN gives what the formulas
  * give, in that row (and in the sums over rows).  T == 0: no-op, the gradients of weights are zeros.  `workspace` as in moe_clip_grad_norm.
- * Errors: INVALID_ARG, UNSUPPORTED, CUDA; a wait for a row (2 s) that runs out is reported by
- * moe_operators_status. */
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA; a wait for a row that runs out is reported by
+ * moe_operators_status, and the call's results are unspecified. */
 typedef enum { MOE_GATE_NONE = 0, MOE_GATE_TOKEN = 1, MOE_GATE_CHANNEL = 2 } moe_gate;
 moe_status moe_sandwich_norm(const void *X, const void *F, const float *pre_w, const float *post_w, const float *gate,
                              int gate_kind, float residual_scale, float eps, int kind, int T, int H, int x_dtype,

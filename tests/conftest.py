@@ -26,6 +26,15 @@ def pytest_collection_modifyitems(config, items):
             item.add_marker(skip)
 
 
+@pytest.fixture(autouse=True)
+def _operators_recorded_nothing(request):
+    """The norms' tests compare results; what their kernels record (a wait that ran out) fails them too."""
+    yield
+    if request.module.__name__.endswith("test_gpu_sandwich_norm"):
+        from expert_routed_ffn_gb300 import capi
+        assert capi.operators_status() == capi.MOE_OK
+
+
 def pytest_sessionfinish(session, exitstatus):
     """Write the output-parity errors the GPU tests measured to
     $MOE_PARITY_DIR/parity_summary.json (nothing when the variable is unset)."""
