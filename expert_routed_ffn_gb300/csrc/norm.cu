@@ -13,8 +13,10 @@
 // memory by bulk copies meanwhile.  The backward pass needs two sums over the team per row: X' and
 // F's norms and mean(dN w_pre xh) come in the first one (the last up to a factor rx, known
 // afterwards).  The weights' gradients are summed per thread over the rows of its team, then over the
-// teams of a CTA in shared memory, then by a second kernel over the CTAs (one per SM, so that these
-// partial sums are few): always in the same order, in fp32.
+// teams of a CTA in shared memory, then by a second kernel over the CTAs: always in the same order, in fp32.
+// There is one CTA per SM, so that these partial sums are few, and a multiple of that where a team would have
+// more than 1024 rows; the second kernel keeps what its additions round off.  So the error is that of
+// 1075 additions at most, 2^-13.9 of the sum of magnitudes, however many rows there are.
 //
 // A sum of squares beyond fp32 is taken again of values scaled by 2^-100.
 //
@@ -46,7 +48,8 @@ constexpr int kMaxH = 8192;
 constexpr int kForwardThreads = 768, kBackwardThreads = 512;
 constexpr int kMaxTeams = kForwardThreads / 32;
 constexpr int kSmem = 206 << 10;   // dynamic shared memory, most
-constexpr int kMaxCtas = 256;      // a partial sum of the weights' gradients each
+constexpr int kMaxCtas = 256;      // at one per SM; backward: a partial sum of the weights' gradients each
+constexpr int kMaxTeamRows = 1024; // backward: rows of a team, whose gradients are one fp32 sum
 constexpr float kDown = 0x1p-100f;
 constexpr int kMaxStages = 2;  // rows (8192 x 2048 with an fp32 stream: 39 us, with 3 41, with 4 43)
 
@@ -618,7 +621,9 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_kernel(cons
     }
 }
 
-// The CTAs' sums, one column of one result per lane of a warp row.
+// The CTAs' sums, one column of one result per lane of a warp row.  A thread's additions, 5 with one CTA per
+// SM and any number beyond, with their rounding errors (a + b = s + e exactly; in fp64 a call took 3 to 6 us
+// longer).
 constexpr int kSumRows = 32;
 __global__ void __launch_bounds__(32 * kSumRows) norm_sum_kernel(const float *partial, int parts, int H, float *d_pre,
                                                                  float *d_post, float *d_gate) {
@@ -629,10 +634,14 @@ __global__ void __launch_bounds__(32 * kSumRows) norm_sum_kernel(const float *pa
     pdl_wait();
     pdl_trigger();
     if (out == nullptr) return;
-    float v = 0.0f;
+    float v = 0.0f, lost = 0.0f;
     if (col < H)
-        for (int i = r; i < parts; i += kSumRows) v += partial[((size_t)i * 3 + which) * H + col];
-    s[r][lane] = v;
+        for (int i = r; i < parts; i += kSumRows) {
+            const float b = partial[((size_t)i * 3 + which) * H + col], sum = __fadd_rn(v, b), of_b = __fsub_rn(sum, v);
+            lost = __fadd_rn(lost, __fadd_rn(__fsub_rn(v, __fsub_rn(sum, of_b)), __fsub_rn(b, of_b)));
+            v = sum;
+        }
+    s[r][lane] = fabsf(v) < INFINITY ? v + lost : v;  // (beside an infinity, `lost` is a NaN)
     __syncthreads();
     if (r != 0 || col >= H) return;
     v = 0.0f;
@@ -646,10 +655,18 @@ OpDone g_attr[24];
 // Teams of several warps have a named barrier each, of 15.
 int most_teams(int team) { return team > 32 ? 15 : kMaxTeams; }
 
-// Threads per team and teams per CTA: as many as fit, fewer where rows would leave SMs without one.
-void shape(int T, int H, int sms, int per, int threads, int &team, int &teams) {
-    team = 32 * ((H + 32 * per - 1) / (32 * per));
-    teams = std::max(1, std::min(std::min(threads / team, most_teams(team)), (T + sms - 1) / sms));
+// 16 values per thread where a row has them for a warp: the sums over a team cost a warp as much as 4
+// values per lane.
+bool two_groups(int H) { return H > 256; }
+// Threads per team and teams per CTA: as many as fit (shape: fewer where rows would leave SMs without one).
+int team_threads(int H) {
+    const int per = 32 * (two_groups(H) ? 16 : 8);
+    return 32 * ((H + per - 1) / per);
+}
+int full_teams(int H, int threads) { return std::min(threads / team_threads(H), most_teams(team_threads(H))); }
+void shape(int T, int H, int sms, int threads, int &team, int &teams) {
+    team = team_threads(H);
+    teams = std::max(1, std::min(full_teams(H, threads), (T + sms - 1) / sms));
 }
 
 struct Buffer {
@@ -711,13 +728,14 @@ Choice choose(int x_dtype, int f_dtype, bool backward, bool channel) {
 
 moe_status launch(const char *name, bool backward, SandwichArgs &a, int x_dtype, int f_dtype, int sms, int &grid, cudaStream_t s) {
     const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
-    // 16 values per thread where a row has them for a warp: the sums over a team cost a warp as much
-    // as 4 values per lane
-    const bool two = a.H > 256;
-    const Choice c = two ? choose<2>(x_dtype, f_dtype, backward, channel) : choose<1>(x_dtype, f_dtype, backward, channel);
+    const Choice c = two_groups(a.H) ? choose<2>(x_dtype, f_dtype, backward, channel) : choose<1>(x_dtype, f_dtype, backward, channel);
     int teams;
-    shape(a.T, a.H, sms, two ? 16 : 8, backward ? kBackwardThreads : kForwardThreads, a.team, teams);
+    shape(a.T, a.H, sms, backward ? kBackwardThreads : kForwardThreads, a.team, teams);
     grid = (int)std::min<long long>(std::min(sms, kMaxCtas), ((long long)a.T + teams - 1) / teams);
+    if (backward) {  // times the waves that bring a team's rows to kMaxTeamRows
+        const long long wave = (long long)grid * teams * kMaxTeamRows;
+        grid *= (int)((a.T + wave - 1) / wave);
+    }
     // X and F, backward also their gradients, of a row of each team
     const int stage = teams * a.H * ((x_dtype == MOE_DTYPE_F32 ? 4 : 2) + (f_dtype == MOE_DTYPE_F32 ? 4 : 2)) * (backward ? 2 : 1);
     const int weights = (backward && channel ? 3 : 2) * a.H * 4;
@@ -732,7 +750,12 @@ moe_status launch(const char *name, bool backward, SandwichArgs &a, int x_dtype,
     return op_cuda(launch_pdl(c.kernel, dim3(grid), dim3(a.team * teams), (size_t)smem, s, a), name);
 }
 
-size_t workspace_of(int T, int H) { return (size_t)std::max(1, std::min(T, kMaxCtas)) * 3 * H * sizeof(float); }
+// A partial sum of each CTA, whatever the device: up to kMaxCtas, or what is needed for T rows rounded up to
+// a multiple of as many.  (More than one wave is of full teams.)
+size_t workspace_of(int T, int H) {
+    const int ctas = std::min(T, kMaxCtas + T / (kMaxTeamRows * full_teams(H, kBackwardThreads)));
+    return (size_t)std::max(1, ctas) * 3 * H * sizeof(float);
+}
 
 }  // namespace
 }  // namespace moe

@@ -440,8 +440,8 @@ moe_status moe_grouped_gated_dgrad(const void *dG, const void *dU, const void *W
  * nor X_out) N = norm(X) pre_w.  N is of the unrounded X_out.
  * backward: from dX_out (NULL: zeros, where there is pre_w) and dN, and X_out and F as they were
  * stored: dX, dF, and dpre_w, dpost_w [H] and dgate (each may be NULL).  Sums over rows are fp32, in a
- * fixed order.  Without F, dX is the whole gradient (no residual_scale).  X_out and dX_out may be NULL
- * where nothing reads them (X_out without pre_w).
+ * fixed order, and as exact as 1075 additions, however many rows there are.  Without F, dX is the whole
+ * gradient (no residual_scale).  X_out and dX_out may be NULL where nothing reads them (X_out without pre_w).
  * In place: X_out may be X and N may be F, dX may be dX_out and dF may be dN; any other overlap of an
  * output is refused.  H: a multiple of 8 up to 8192, T up to 2^30; eps >= 1e-30.  Rows of any magnitude are normed (sums of squares beyond fp32
  * are taken again of scaled values); a row with an infinity or a NaN gives what the formulas
