@@ -365,12 +365,19 @@ __global__ void __launch_bounds__(kForwardThreads, 1) norm_forward_kernel(const 
             return total;
         };
         bool lost = false;
-        auto norm = [&](const f2 (&v)[V][4]) {
+        // the factor that norms v; of values whose squares are beyond fp32 it may be under fp32's normal
+        // range, so those are normed here and the factor is 1
+        auto norm = [&](f2 (&v)[V][4]) {
             float ss = squares(v, 1.0f);
             if (ss < INFINITY) return inverse_root(ss, inv_h, p.eps);
             lost = lost_row(sh, team, row);
             ss = squares(v, kDown);
-            return inverse_root(ss, inv_h, p.eps * kDown * kDown) * kDown;
+            const float r = inverse_root(ss, inv_h, p.eps * kDown * kDown);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[i][j] = mul2(mul2(v[i][j], both(r)), both(kDown));
+            return 1.0f;
         };
 #pragma unroll
         for (int i = 0; i < V; ++i) Ring::get<TX>(in[i] ? ring.present() + 8 * sizeof(TX) * group[i] : zeros, x[i]);
@@ -577,11 +584,15 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_kernel(cons
         if (!has_f) continue;
         if (token && me == 0 && p.dgate != nullptr) p.dgate[row] = total;
         // dF = g rf (T w_post - fh mean(T w_post fh)), or g T
-        const float out = has_post ? g * (rf * sf) : g, back = has_post ? -total * inv_h * rf : 0.0f;
+        const float out = has_post ? g * rf : g, back = has_post ? -total * inv_h * rf : 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[j] = mul2(both(out), has_post ? fma2(f[i][j], both(back), t[i][j]) : t[i][j]);
+            if (has_post && sf != 1.0f) {  // (g rf sf may be under fp32's normal range)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = mul2(w[j], both(sf));
+            }
             if (in[i]) store8(static_cast<TF *>(p.fo) + base + 8 * group[i], w);
         }
     }
