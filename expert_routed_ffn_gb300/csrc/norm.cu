@@ -63,7 +63,7 @@ struct SandwichArgs {
     float alpha, eps, one;  // one: added to the weights
     int T, H, gate_kind, team;  // team: threads
     int *err;
-    uint64_t wait_ns;       // bound of the wait for a row
+    uint32_t wait_us;       // bound of the wait for a row
     int stages;             // rows in flight, the present one among them
     bool weights_in_smem;   // backward
 };
@@ -231,12 +231,8 @@ struct Ring {
     }
     // False: the row is not there within the bound (0: give up at once).  Lanes may differ (one answer for
     // a warp cost the gradients up to 5%).
-    __device__ __forceinline__ bool wait(uint64_t limit_ns, volatile int *abort) const {
-        return limit_ns != 0 && mbar_wait(bars + 8 * stage, parity, limit_ns, abort);
-    }
-    // After such a wait for `row`: wait for the copies in flight, again with a bound.
-    __device__ __forceinline__ void drain(int row, int stride, int T) {
-        for (int s = 0; s < stages && row < T; ++s, row += stride, next()) wait_bar(bars + 8 * stage, parity, kDrainCycles, nullptr);
+    __device__ __forceinline__ bool wait(uint32_t limit_us) const {
+        return limit_us != 0 && mbar_wait(bars + 8 * stage, parity, 1000ull * limit_us, nullptr);
     }
     __device__ __forceinline__ uint32_t present() const { return rows + stage * bytes; }
     // 8 values in shared memory
@@ -267,20 +263,24 @@ struct Shared {
     float slots[kMaxTeams * kSlots];
     uint64_t bars[kMaxTeams * kMaxStages];
     uint4 zeros[2];  // what lanes beyond H read
-    int abort;       // a wait of the CTA ran out: no later one takes time
-    int lost[kMaxTeams];  // the row that a team did not get, see lost_row
+    int abort;       // a wait of the CTA ran out
+    // The row that a team did not get.  A thread whose wait ran out writes it here and goes on with whatever is
+    // there up to the team's next sum, which it makes a NaN: where a sum is not finite all of the team's
+    // threads look here and leave, so nobody asks for another row.  A row is given by its number, so that a
+    // thread that is a row ahead is not taken for it.
+    int lost[kMaxTeams];
 };
-// A thread's wait for `row` ran out.  It goes on with whatever is there up to the team's next sum, which it
-// makes a NaN: where a sum is not finite all of the team's threads look here and leave, so nobody asks
-// for another row.  A row is given by its number, so that a thread that is a row ahead is not taken for it.
-__device__ __forceinline__ void lose_row(Shared &sh, const Team &team, int row, int *err) {
-    *(volatile int *)&sh.lost[team.id] = row;
-    *(volatile int *)&sh.abort = 1;
-    atomicOr(err, ERR_TIMEOUT);
-}
 __device__ __forceinline__ bool lost_row(const Shared &sh, const Team &team, int row) {
     __syncwarp();  // (a team of one warp has passed no other barrier)
     return *(const volatile int *)&sh.lost[team.id] == row;
+}
+// A team's end.  Where it did not get `row`: record it, and wait for the copies in flight, again with a bound.
+__device__ __forceinline__ void end_team(Shared &sh, Ring &ring, int row, int stride, int T, int *err) {
+    if (row >= T) return;
+    *(volatile int *)&sh.abort = 1;
+    atomicOr(err, ERR_TIMEOUT);
+    for (int s = 0; s < ring.stages && row < T; ++s, row += stride, ring.next())
+        wait_bar(ring.bars + 8 * ring.stage, ring.parity, kDrainCycles, nullptr);
 }
 __device__ __forceinline__ Ring make_ring(Shared &sh, const Team &team, uint32_t rings, uint32_t row_bytes, int stages) {
     Ring r;
@@ -347,8 +347,8 @@ __global__ void __launch_bounds__(kForwardThreads, 1) norm_forward_kernel(const 
     for (; row < p.T; row += stride, ring.next()) {
         const float gate = gate_next;
         if (token && row + stride < p.T) gate_next = p.gate[row + stride];
-        const bool got = ring.wait(p.wait_ns, &sh.abort);
-        if (!got) lose_row(sh, team, row, p.err);
+        const bool got = ring.wait(p.wait_us);
+        if (!got) *(volatile int *)&sh.lost[team.id] = row;
         const size_t base = (size_t)row * H;
         f2 x[V][4], f[V][4], w[4];
         auto squares = [&](const f2 (&v)[V][4], float scale) {  // (values beyond H are zeros)
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) norm_forward_kernel(const 
             if (me == 0) ask(row + p.stages * stride, ring.stage);
         }
     }
-    if (row < p.T) ring.drain(row, stride, p.T);
+    end_team(sh, ring, row, stride, p.T, p.err);
 }
 
 // CHANNEL: the gate is one per channel.
@@ -501,8 +501,8 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_kernel(cons
         // What is not there is zeros or ones, so that the values take no branches.
         const float g = gate_next, alpha = has_f ? p.alpha : 1.0f;
         if (token && row + stride < p.T) gate_next = p.gate[row + stride];
-        const bool got = ring.wait(p.wait_ns, &sh.abort);
-        if (!got) lose_row(sh, team, row, p.err);
+        const bool got = ring.wait(p.wait_us);
+        if (!got) *(volatile int *)&sh.lost[team.id] = row;
         const size_t base = (size_t)row * H;
         f2 x[V][4], dn[V][4], f[V][4], w[4];
         uint32_t at_x[V], at_f[V];  // a thread's values of the first tensor of either type in this stage
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_kernel(cons
             if (in[i]) store8(static_cast<TF *>(p.fo) + base + 8 * group[i], w);
         }
     }
-    if (row < p.T) ring.drain(row, stride, p.T);
+    end_team(sh, ring, row, stride, p.T, p.err);
 
     // the teams' sums one after the other, then this CTA's
     const int teams = blockDim.x / p.team;
@@ -753,7 +753,7 @@ moe_status launch(const char *name, bool backward, SandwichArgs &a, int x_dtype,
     a.weights_in_smem = weights + stage <= kSmem;
     a.stages = std::min(kMaxStages, (kSmem - (a.weights_in_smem ? weights : 0)) / stage);
     a.err = op_error_word();
-    a.wait_ns = ((uint64_t)wait_cycles(0) + 1) / 2;  // of cycles at 2 GHz; 0 for 0 alone
+    a.wait_us = (uint32_t)std::min<uint64_t>(~0u, ((uint64_t)wait_cycles(0) + 1999) / 2000);  // of cycles at 2 GHz; 0 for 0 alone
     if (a.err == nullptr) return op_fail(MOE_ERR_CUDA, "%s: no usable current device", name);
     const int smem = std::max(weights, (a.weights_in_smem ? weights : 0) + a.stages * stage);
     const cudaError_t e = op_allow_smem(reinterpret_cast<const void *>(c.kernel), kSmem, &g_attr[c.which]);
