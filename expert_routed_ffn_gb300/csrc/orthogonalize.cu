@@ -90,7 +90,8 @@ struct ProductArgs {
     const float *table;   // first step: s of each matrix, else NULL
     const half *other;    // B: A; X: lo, or NULL
     half *out, *out_lo;   // out_lo: X, or NULL
-    bf16 *final;          // X: the result, in place of out
+    bf16 *final;          // X: the result, `scale` times, in place of out
+    float scale;
     float k_acc, k_other, k_diag;
 };
 
@@ -274,7 +275,7 @@ struct Update {
             const float y = fmaf(scale, old.y, p.k_acc * __uint_as_float(odd ? mine : got));
             if (2 * i >= left) continue;
             if (p.final != nullptr) {
-                *reinterpret_cast<uint32_t *>(p.final + from + 2 * i * ld) = pack_bf16x2(x, y);
+                *reinterpret_cast<uint32_t *>(p.final + from + 2 * i * ld) = pack_bf16x2(p.scale * x, p.scale * y);
             } else {
                 const uint32_t h = pack_half2(x, y);
                 *reinterpret_cast<uint32_t *>(p.out + from + 2 * i * ld) = h;
@@ -843,8 +844,8 @@ extern "C" moe_status moe_orthogonalize(const void *G, int dtype, int E, int N, 
         b.k_other = c[1] / sa * sb;
         b.k_diag = c[0] * sb;
         const bool last = i + 1 == steps;
-        const float unit = last ? scale / up : 1.0f;  // of what is stored
-        u.k_acc = unit / sb;
+        u.k_acc = 1.0f / sb / (last ? up : 1.0f);  // a power of two; `scale`, of any size, comes after it
+        u.scale = scale;
         u.other = i == 0 ? lo0 : keeps_lo(i, steps) ? lo : nullptr;
         u.k_other = c[0];  // (the last step has no lo)
         u.out_lo = !last && keeps_lo(i + 1, steps) ? lo : nullptr;
