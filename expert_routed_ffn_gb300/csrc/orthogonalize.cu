@@ -645,7 +645,9 @@ float power_below(double bound, int most) {
 // Steps whose X keeps its rounding.
 bool keeps_lo(int step, int steps) { return step < steps - 2; }
 
-// false: the polynomials let a singular value grow beyond what fp16 holds
+// Largest singular values and polynomials that fp16 holds beside others: X's scale is one for all steps.
+constexpr double kMostValue = 1024.0, kLeastValue = 1.0 / 1024.0;
+// false: the polynomials let the singular values grow beyond that, or all of them shrink
 bool choose_scales(const float *coef, int steps, Scales *scales, float *up) {
     double x = 1.0, most = 1.0;
     for (int i = 0; i < steps; ++i) {
@@ -653,10 +655,13 @@ bool choose_scales(const float *coef, int steps, Scales *scales, float *up) {
         auto whole = [](double l, const float *k) { return k[0] + l * (k[1] + l * k[2]); };
         auto step = [](double v, const float *k) { return v * (k[0] + v * v * (k[1] + v * v * k[2])); };
         scales[i].a = power_below(1.01 * x * x, 14);
-        scales[i].b = power_below(largest(x * x, whole, c), 14);
+        const double b = largest(x * x, whole, c);
+        scales[i].b = power_below(b, 14);
         x = largest(x, step, c);
-        if (!(x < 1024.0)) return false;
-        if (i + 1 < steps) most = std::max(most, x);
+        if (!(x < kMostValue && b > kLeastValue)) return false;
+        if (i + 1 == steps) break;
+        if (!(x > kLeastValue)) return false;
+        most = std::max(most, x);
     }
     *up = power_below(1.01 * most, 12);
     return true;
@@ -776,7 +781,7 @@ extern "C" moe_status moe_orthogonalize(const void *G, int dtype, int E, int N, 
     Scales scales[kMaxSteps];
     float up;
     if (!choose_scales(coefficients, steps, scales, &up))
-        return op_fail(MOE_ERR_UNSUPPORTED, "%s: these coefficients let singular values grow beyond 1024", name);
+        return op_fail(MOE_ERR_UNSUPPORTED, "%s: these coefficients let singular values grow beyond 1024, or all of them shrink below 1 / 1024", name);
     if (E == 0) return MOE_OK;
     const Workspace w = lay_out(E, N, K);
     if (!G || !out || !workspace || workspace_bytes < w.bytes)
