@@ -570,7 +570,7 @@ def sandwich_norm(X, F=None, pre_w=None, post_w=None, gate=None, residual_scale=
     [T, H] the block's result (of its own type, which N has too); pre_w and post_w [H] fp32, gate [H] or
     [T, 1] fp32.  Returns (X', N): without post_w F is added as it is, without pre_w N is None,
     without F X' is X itself and N = norm(X) pre_w (of n_dtype, by default X's).  kind "gemma": weights
-    are 1 + w.  X_out may be X, and N_out may be F."""
+    are 1 + w.  X_out may be X, and N_out may be F.  A gate begins at 16 bytes as every tensor does (gate[1:] does not)."""
     torch = _t()
     shape, index, code, gate_kind = _norm_arguments(X, F, pre_w, post_w, gate, kind)
     of_n = F.dtype if F is not None else n_dtype or (X.dtype if N_out is None else N_out.dtype)

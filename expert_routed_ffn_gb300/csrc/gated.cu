@@ -15,14 +15,20 @@
 //     half of the sum is padded to whole steps of 64, whose copies bring zeros in both operands.
 // The weights' gradients are moe_grouped_wgrad's of dG, dU with X and of dY with H.
 //
-// Measured on GB300, calls one after the other on the same tensors (64 experts, I 1408, K 2048):
-//   forward, 24576 rows, G and U kept   201 us (without them 186), 1.41 PFLOP/s, 5.1 TB/s: the tensor pipe is
-//              busy 72% of the cycles and HBM 65% at 1.7 GHz (power); with all rows in one expert, whose
-//              weights stay in L2, 153 and 145 us, 1.95 PFLOP/s
-//   backward, 24576 rows   130 us, 5.6 TB/s, tensor pipe 62%: 553 MB of dY, G, U, dG and dU beside 369 MB of
+// Measured on GB300, 30 calls in a row after a pause, at 1.7 GHz (in brackets: called for seconds, when power
+// brings the clock to 1.33 to 1.4 GHz; the same or other tensors from call to call make no difference); 64
+// experts, I 1408, K 2048:
+//   forward, 24576 rows, G and U kept   201 us (243), without them 186 (227): 1.41 PFLOP/s, 5.1 TB/s, the
+//              tensor pipe busy 72% of the cycles and HBM 65%; with all rows in one expert, whose weights
+//              stay in L2, 153 (185) and 145 us, 1.95 PFLOP/s
+//   backward, 24576 rows   130 us (148), 5.6 TB/s, tensor pipe 62%: 553 MB of dY, G, U, dG and dU beside 369 MB of
 //              weights.  With two epilogue warps per lane quadrant it waited for the gradients' arithmetic
 //              (180 us), with loads of G and U after the sums for those
-//   dgrad, 24576 rows, fp32   203 us, 5.4 TB/s, tensor pipe 71%; bf16 197
+//   dgrad, 24576 rows, fp32   209 us (239), 5.2 TB/s, tensor pipe 71%
+// What bounds forward and dgrad: experts of 384 rows (tiles of 192) take as many cycles as experts of 448
+// (322 and 321 us x GHz; of 512 341, 89% of the MMAs' rate), so a stage of few rows takes as long as its
+// operands need into shared memory, 16 KB of weights and 12 KB of rows, and not as long as its MMAs.
+//
 //   forward, one token's six experts   12.8 us (14.9 with changing inputs), 69 MB of weights
 //   dgrad, 2000 rows, 128 experts, 256 x 1024   25.5 us with changing inputs, 5.5 TB/s
 #include <algorithm>

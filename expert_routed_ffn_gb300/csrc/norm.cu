@@ -24,12 +24,13 @@
 //   forward, 8192 x 2048, fp32 stream, bf16 block   39 us, 5.1 TB/s; 65536 rows 247 us, 6.5 TB/s; bf16
 //                              throughout 28.6 and 163 us.  A call has 8 us beside the copying: launch,
 //                              weights, a team's first rows and last stores
-//   backward, 16384 x 2048, bf16   86 us, 4.7 TB/s: half of an SM's issue slots are taken, 46
+//   backward, 16384 x 2048, bf16   85 us, 4.7 TB/s (a gate per channel: 106, registers spill): half of an SM's issue slots are taken, 46
 //                              instructions per value of a warp's lane, and 16 warps wait for one
 //                              another twice a row.  (With 8 values per thread and weights read across
 //                              banks it took 203 us, without bank conflicts 109, with 768 threads of fewer
 //                              registers 103.)  Rows beyond 4096 leave a CTA to one team, whose steps
-//                              then wait for one another: 20000 x 6144 340 us, 4.3 TB/s, x 4104 333
+//                              then wait for one another: 20000 x 6144 340 us, 4.3 TB/s, x 4104 330
+//   without a block, 16384 x 2048, bf16   25 us (partly from L2), backward 66
 //   one row of 2048            6.2 us
 #include <algorithm>
 

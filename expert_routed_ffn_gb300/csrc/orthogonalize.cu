@@ -22,10 +22,12 @@
 // falling as 1 / j: 2.1e-3 and 1.8e-3 (five steps; six of a Gaussian 224 x 96 in fp32: 2.4e-3).
 // X0 is G times a power of two (exact for bf16 G: no lo), the rest of 1 / (|G| + eps) is a factor
 // s in (1/2, 1] of the first A and B.  Sums are fp32 in tensor memory, over at most 16384
-// products: the tensor core's truncation stays below 1e-4 (2^-13) of a sum of one sign.
+// products: the tensor core's truncation stays below 2^-13 (1.2e-4) of a sum of one sign.  Further steps of these
+// coefficients, which move singular values about in [0.7, 1.2] for good, raise the error (3.1e-3 for 8, 7e-3 for 20,
+// up to 3e-2 for 64); coefficients that converge keep it below 2e-3.
 //
-// Measured on GB300, 32 x 1408 x 2048 in fp32, five steps, one call after the other: 2.0 ms, 1.2
-// PFLOP/s of the products counted above; |G| 57 us and X0 with its lo 113 us (6.6 and 6.1 TB/s), then per
+// Measured on GB300, 32 x 1408 x 2048 in fp32, five steps: 1.93 ms after a pause, 1.24 PFLOP/s of the products
+// counted above, and 2.26 ms when called for seconds (power: 1.37 GHz); |G| 57 us and X0 with its lo 113 us (6.6 and 6.1 TB/s), then per
 // step A 104, B 76 to 80 and X 187 us (with lo) or 160.  The tensor pipe is busy 70 to 78% of the cycles
 // and the clock falls to 1.5 to 1.7 GHz of 2.07 (power): 5.5 tiles of 256 to a side make 18 tiles' work of the 15.1 below
 // the diagonal, a tile's epilogue shares shared memory's bandwidth with the MMAs' operands, and a
@@ -672,7 +674,7 @@ bool choose_scales(const float *coef, int steps, Scales *scales, float *up) {
 // time by: waves of tiles times a tile's stages, each 150 + 0.6 ns for each row (the copies of 128
 // columns and half of the rows to an SM at 110 bytes a ns, or as long for the MMAs), 600 ns to fill
 // the pipeline, and at the end an epilogue.  (256 rows, halved while the pairs outnumber the tiles: 4096
-// x 4096 1012 us for 882, 2 x 1408 x 2048 270 for 241, 4 x 1024 x 1024 188 for 175.)
+// x 4096 1012 us for 874, 2 x 1408 x 2048 270 for 241, 4 x 1024 x 1024 188 for 175.)
 long long count_tiles(const ProductArgs &g, bool sym) {
     if (!sym) return (long long)g.E * g.row_tiles * g.col_tiles;
     long long n = 0;
