@@ -23,7 +23,7 @@
 // X0 is G times a power of two (exact for bf16 G: no lo), the rest of 1 / (|G| + eps) is a factor
 // s in (1/2, 1] of the first A and B.  Sums are fp32 in tensor memory, over at most 16384
 // products: the tensor core's truncation stays below 2^-13 (1.2e-4) of a sum of one sign.  Further steps of these
-// coefficients, which move singular values about in [0.7, 1.2] for good, raise the error (3.1e-3 for 8, 7e-3 for 20,
+// coefficients, which move singular values about in [0.7, 1.2] for good, raise the error (3.4e-3 for 8, 7e-3 for 20,
 // up to 3e-2 for 64); coefficients that converge keep it below 2e-3.
 //
 // Measured on GB300, 32 x 1408 x 2048 in fp32, five steps: 1.93 ms after a pause, 1.24 PFLOP/s of the products

@@ -495,10 +495,12 @@ moe_status moe_mx_grouped_forward(const void *Xc, const uint8_t *Xs, const void 
  * fp32; the low half of X is carried through a X in all steps but the last two.  The result's error, where
  * its rounding to bf16 alone is 1.7e-3 (2-norm, relative): up to 2e-3 for any number of steps of
  * coefficients that converge; 2.3e-3 after five steps of (3.4445, -4.7750, 2.0315), under which singular
- * values never settle, and with them the error grows: 3.1e-3 after 8, 7e-3 after 20, 3e-2 after 64.  Coefficients that
- * let singular values from [0, 1] grow beyond 1024, or all of them shrink below 1 / 1024 before the last
+ * values never settle, and with them the error grows: 2.6e-3 after 6, 3.4e-3 after 8, 7e-3 after 20, 3e-2 after
+ * 64 (up to twice that with fewer than 64 rows or columns, over which less is averaged).  Coefficients that let
+ * singular values from [0, 1] grow beyond 1024, or all of them shrink below 1 / 1024 before the last
  * step, are refused, and so is a step of which |a + b s^2 + c s^4| stays below 1 / 1024 (`scale` may be
- * any finite number).  A matrix with an infinity or a NaN gives NaN, and no other does.  N and K multiples of 8 up to 16384, E up to 65535 (0: no-op); eps >= 1e-30.
+ * any finite number).  A matrix with an infinity or a NaN gives NaN, and no other does.  N and K multiples of 8
+ * up to 16384, E up to 65535 (0: no-op); eps >= 1e-30.
  * `workspace` as in moe_clip_grad_norm (16-byte aligned; the size has room for the call to round its
  * beginning up).  Errors: INVALID_ARG, UNSUPPORTED, CUDA; a wait that runs out is reported by
  * moe_operators_status. */

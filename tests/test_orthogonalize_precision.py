@@ -93,9 +93,9 @@ def test_the_bound_tells_a_lost_low_half(N, K, dtype, mistake):
 
 
 def test_errors_that_the_header_states():
-    """What include/moe.h says of the quintic's steps, and of an iteration that converges."""
+    """What include/moe.h says of the quintic's steps (8: of smaller matrices too), and of an iteration that converges."""
     for G in (_few(264, 352, F32), _falling(264, 352, F32), _falling(264, 352, BF, seed=3)):
-        for steps, stated in ((5, 2.3e-3), (8, 3.1e-3), (20, 7e-3), (64, 3e-2)):
+        for steps, stated in ((5, 2.3e-3), (6, 2.6e-3), (8, 3.1e-3), (20, 7e-3), (64, 3e-2)):
             assert _error(_chain(G, [QUINTIC] * steps), _chain(G, [QUINTIC] * steps, rounded=False)) <= stated
             assert _error(_chain(G, [CUBIC] * steps), _chain(G, [CUBIC] * steps, rounded=False)) <= 2e-3
 
